@@ -2,8 +2,9 @@
 
 C = alpha * A * B + beta * C for row-major FP32 operands ("GEMM 优化之路",
 problem statement), and the same product with bfloat16 or float16 A and B and
-FP32 C (the gsyq.cn guide, section 5.1).  Every step runs in the HIP library ``libsgemm.so``; this
-module only marshals arguments.  PyTorch provides device memory and streams.
+FP32 C (the gsyq.cn guide, section 5.1).  Beside the products stand microscaled
+4-bit operands (quantisation, and products of them).  Every step runs in the
+HIP library ``libsgemm.so``; this module only marshals arguments.  PyTorch provides device memory and streams.
 There is no fallback: if the library is missing, loading fails loudly.
 """
 from __future__ import annotations
@@ -39,10 +40,14 @@ SGEMM_MODE_ALIGNED = 0
 SGEMM_MODE_EDGE = 1
 SGEMM_MODE_GUARDED = 2
 
+SGEMM_DTYPE_F32 = 0
 SGEMM_DTYPE_BF16 = 1
 SGEMM_DTYPE_F16 = 2
 SGEMM_DTYPE_FP8_E4M3 = 3
 SGEMM_DTYPE_FP8_E5M2 = 4
+
+SGEMM_MX_BLOCK = 32  # values of a microscaled row that share a scale
+SGEMM_MX_MAX_K = 1 << 27
 
 SGEMM_SCHEDULE_TILES = 0
 SGEMM_SCHEDULE_STREAM_K = 1
@@ -60,6 +65,8 @@ EXPORTED = [
     "sgemm_lowp_select_kernel", "sgemm_set_lowp_kernel", "sgemm_diag_mfma_chain_lowp",
     "sgemm_diag_run_clocked", "sgemm_diag_wall_clock_khz", "sgemm_run_ex_noalloc",
     "sgemm_lowp_kernel_schedule", "sgemm_lowp_plan_handle",
+    "sgemm_mx_quantize", "sgemm_mx_dequantize", "sgemm_run_mx", "sgemm_validate_mx",
+    "sgemm_run_mx_quant",
 ]
 
 
@@ -113,6 +120,14 @@ def _bind(lib):
     lib.sgemm_lowp_plan_handle.argtypes = [p, i, i, i, i, i, i, p, i, p, i, p, i, ip, ip]
     lib.sgemm_diag_run_clocked.argtypes = [p, i, i, i, i, i, f, p, i, p, i, f, p, i, p, i, p]
     lib.sgemm_diag_wall_clock_khz.argtypes = [ip]
+    lib.sgemm_mx_quantize.argtypes = [p, i, i, i, i, p, i, p, i, p, i, p]
+    lib.sgemm_mx_dequantize.argtypes = [p, i, i, i, p, i, p, i, p, i, p]
+    lib.sgemm_run_mx.argtypes = [p, i, i, i, f, p, i, p, i, p, i, p, i, f, i, p, i, p]
+    lib.sgemm_validate_mx.argtypes = [i, i, i, p, i, p, i, p, i, p, i, i, p, i]
+    lib.sgemm_run_mx_quant.argtypes = [p, i, i, i, i, f, p, i, p, i, p, i, f, i, p, i, p]
+    for name in ("sgemm_mx_quantize", "sgemm_mx_dequantize", "sgemm_run_mx",
+                 "sgemm_validate_mx", "sgemm_run_mx_quant"):
+        getattr(lib, name).restype = i
     for name in ("sgemm_lowp_kernel_schedule", "sgemm_lowp_plan_handle",
                  "sgemm_diag_run_clocked", "sgemm_diag_wall_clock_khz", "sgemm_run_ex_noalloc",
                  "sgemm_run_lowp", "sgemm_diag_mfma_chain_lowp", "sgemm_validate_lowp", "sgemm_lowp_num_kernels",
@@ -239,6 +254,39 @@ def sgemm_lowp_select_kernel(dtype, transa, transb, M, N, K, A, lda, B, ldb, C,
 
 def sgemm_set_lowp_kernel(h, kernel_id: int) -> int:
     return _check(library().sgemm_set_lowp_kernel(h, kernel_id), "sgemm_set_lowp_kernel")
+
+
+def sgemm_mx_quantize(h, dtype, trans, R, K, X, ldx, codes, ldc, scales, lds,
+                      stream=0) -> int:
+    """Microscaled 4-bit rows of X; X, codes and scales are device addresses."""
+    return _check(library().sgemm_mx_quantize(h, dtype, trans, R, K, X, ldx, codes, ldc,
+                                              scales, lds, stream), "sgemm_mx_quantize")
+
+
+def sgemm_mx_dequantize(h, dtype, R, K, codes, ldc, scales, lds, Y, ldy, stream=0) -> int:
+    """The values of microscaled rows as a tensor of type ``dtype``."""
+    return _check(library().sgemm_mx_dequantize(h, dtype, R, K, codes, ldc, scales, lds, Y,
+                                                ldy, stream), "sgemm_mx_dequantize")
+
+
+def sgemm_run_mx(h, M, N, K, alpha, A, lda, SA, ldsa, B, ldb, SB, ldsb, beta, dtype, C, ldc,
+                 stream=0) -> int:
+    """The product of two microscaled operands (codes A, B and scales SA, SB)."""
+    return _check(library().sgemm_run_mx(h, M, N, K, alpha, A, lda, SA, ldsa, B, ldb, SB,
+                                         ldsb, beta, dtype, C, ldc, stream), "sgemm_run_mx")
+
+
+def sgemm_validate_mx(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, dtype, C, ldc) -> int:
+    return library().sgemm_validate_mx(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, dtype, C,
+                                       ldc)
+
+
+def sgemm_run_mx_quant(h, xtype, M, N, K, alpha, X, ldx, B, ldb, SB, ldsb, beta, dtype, C,
+                       ldc, stream=0) -> int:
+    """sgemm_run_mx with A quantised in the call from the M x K tensor X."""
+    return _check(library().sgemm_run_mx_quant(h, xtype, M, N, K, alpha, X, ldx, B, ldb, SB,
+                                               ldsb, beta, dtype, C, ldc, stream),
+                  "sgemm_run_mx_quant")
 
 
 def sgemm_destroy(h) -> int:
@@ -426,6 +474,60 @@ def mfma_chain_tflops(workgroups=1024, iterations=4096, reps=3, dtype=None):
 
 # ---- torch-tensor convenience ------------------------------------------------
 
+TENSOR_DTYPES = {torch.float32: SGEMM_DTYPE_F32, torch.bfloat16: SGEMM_DTYPE_BF16,
+                 torch.float16: SGEMM_DTYPE_F16}
+
+
+class Mx4:
+    """Microscaled 4-bit rows: ``codes``, a uint8 matrix of 16 bytes a block of
+    32 values, and ``scales``, a uint8 matrix of one byte a block (the
+    exponent plus 127).  Rows may be strided, bytes of a row not."""
+
+    __slots__ = ("codes", "scales")
+
+    def __init__(self, codes, scales):
+        for name, t in (("codes", codes), ("scales", scales)):
+            if t.dtype != torch.uint8 or t.dim() != 2:
+                raise TypeError(f"{name} must be a 2-D uint8 tensor")
+            if t.numel() and t.stride(1) != 1:
+                raise ValueError(f"{name} must be row-major (unit column stride)")
+        if codes.shape[0] != scales.shape[0] or codes.shape[1] != 16 * scales.shape[1]:
+            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} "
+                             "disagree: 16 code bytes and a scale byte a block")
+        self.codes, self.scales = codes, scales
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def K(self) -> int:
+        """Values a row holds, whole blocks."""
+        return SGEMM_MX_BLOCK * self.scales.shape[1]
+
+    @staticmethod
+    def empty(rows: int, K: int, device="cuda") -> "Mx4":
+        nb = -(-K // SGEMM_MX_BLOCK)
+        return Mx4(torch.empty(rows, 16 * nb, dtype=torch.uint8, device=device),
+                   torch.empty(rows, nb, dtype=torch.uint8, device=device))
+
+    def _args(self):
+        c, s = self.codes, self.scales
+        return c.data_ptr(), max(c.stride(0), 1), s.data_ptr(), max(s.stride(0), 1)
+
+
+def _matrix(name, t):
+    """A 2-D row-major float32, bfloat16 or float16 tensor: its library type
+    and leading dimension."""
+    if t.dtype not in TENSOR_DTYPES or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D float32, bfloat16 or float16 tensor")
+    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be row-major (unit column stride)")
+    if t.shape[0] > 1 and 0 < t.numel() and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)}, {t.shape[1]} columns)")
+    return TENSOR_DTYPES[t.dtype], max(t.stride(0), t.shape[1], 1)
+
+
 class Handle:
     """Owns one sgemm handle; usable as a context manager.
 
@@ -437,6 +539,7 @@ class Handle:
     def __init__(self, variant: int = SGEMM_VARIANT_AUTO, kernel: int = -1,
                  workspace: bool = True):
         self.h = sgemm_create()
+        self.device = torch.device("cuda", torch.cuda.current_device())
         self.workspace = None
         self._stamps = None
         if variant != SGEMM_VARIANT_AUTO:
@@ -573,6 +676,74 @@ class Handle:
                               int(bool(transb)), M, N, K, float(alpha), A.data_ptr(),
                               lda, B.data_ptr(), ldb, float(beta), C.data_ptr(), ldc,
                               stream)
+
+    # -- microscaled 4-bit operands --
+
+    def _on(self, stream, **tensors):
+        """The stream's address, after checking that every tensor lies on the
+        handle's device."""
+        for name, t in tensors.items():
+            if t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, the handle on {self.device}")
+        if stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
+
+    def mx4_quantize(self, X, trans=False, out=None, stream=None):
+        """Microscaled 4-bit rows of X (R x K, or stored K x R when ``trans``;
+        float32, bfloat16 or float16): an ``Mx4`` of R rows, ``out`` if given
+        (else allocated on ``stream``).  K need not be whole blocks; the last
+        one is filled with zeros."""
+        dtype, ldx = _matrix("X", X)
+        R, K = X.shape[::-1] if trans else X.shape
+        if out is None:
+            if stream is None:
+                out = Mx4.empty(R, K, X.device)
+            else:
+                s = stream if isinstance(stream, torch.cuda.Stream) else \
+                    torch.cuda.ExternalStream(stream, self.device)
+                with torch.cuda.stream(s):
+                    out = Mx4.empty(R, K, X.device)
+        elif out.rows != R or out.K != SGEMM_MX_BLOCK * -(-K // SGEMM_MX_BLOCK):
+            raise ValueError(f"out holds {out.rows} rows of {out.K} values, X gives {R} of {K}")
+        codes, ldc, scales, lds = out._args()
+        sgemm_mx_quantize(self.h, dtype, int(bool(trans)), R, K, X.data_ptr(), ldx, codes, ldc,
+                          scales, lds, self._on(stream, X=X, codes=out.codes, scales=out.scales))
+        return out
+
+    def mx4_dequantize(self, Q, out, stream=None):
+        """The values of ``Q`` into ``out`` (float32, bfloat16 or float16; its
+        columns are at most Q.K, the rest is left out).  Returns ``out``."""
+        dtype, ldy = _matrix("out", out)
+        if out.shape[0] != Q.rows or out.shape[1] > Q.K:
+            raise ValueError(f"out is {tuple(out.shape)}, Q holds {Q.rows} rows of {Q.K} values")
+        codes, ldc, scales, lds = Q._args()
+        sgemm_mx_dequantize(self.h, dtype, *out.shape, codes, ldc, scales, lds, out.data_ptr(),
+                            ldy, self._on(stream, codes=Q.codes, scales=Q.scales, out=out))
+        return out
+
+    def gemm_mx4(self, A, B, C, alpha=1.0, beta=0.0, stream=None):
+        """C = alpha * A @ B^T + beta * C with B an ``Mx4`` of N rows and A an
+        ``Mx4`` of M rows, or an M x K float32, bfloat16 or float16 tensor
+        that the call quantises (``mx4_quantize``; over 16 rows through the
+        handle's workspace).  C is M x N, float32, bfloat16 or float16."""
+        dtype, ldc = _matrix("C", C)
+        M, N = C.shape
+        quantised = isinstance(A, Mx4)
+        rows, K = (A.rows, A.K) if quantised else A.shape
+        if rows != M or B.rows != N or SGEMM_MX_BLOCK * -(-K // SGEMM_MX_BLOCK) != B.K:
+            raise ValueError(f"A {rows} x {K} and B {B.rows} x {B.K} do not give "
+                             f"{M} x {N}")
+        b, ldb, sb, ldsb = B._args()
+        if quantised:
+            a, lda, sa, ldsa = A._args()
+            s = self._on(stream, A=A.codes, A_scales=A.scales, B=B.codes, B_scales=B.scales, C=C)
+            return sgemm_run_mx(self.h, M, N, K, alpha, a, lda, sa, ldsa, b, ldb, sb, ldsb,
+                                beta, dtype, C.data_ptr(), ldc, s)
+        xtype, lda = _matrix("A", A)
+        s = self._on(stream, A=A, B=B.codes, B_scales=B.scales, C=C)
+        return sgemm_run_mx_quant(self.h, xtype, M, N, K, alpha, A.data_ptr(), lda, b, ldb, sb,
+                                  ldsb, beta, dtype, C.data_ptr(), ldc, s)
 
 
 def _span(rows, cols, ld):

@@ -1,0 +1,212 @@
+// C ABI of the microscaled 4-bit operators: argument checks, the choice of a
+// kernel and the launches.  Declarations and contracts are in
+// include/sgemm.h.
+#include "sgemm.h"
+
+#include <hip/hip_runtime.h>
+#include <limits.h>
+
+#include "handle.hpp"
+#include "mx_quant.hpp"
+#include "mx_small.hpp"
+
+using namespace sgemm;
+
+namespace {
+
+int blocks_of(int K) { return K / MX_BLOCK + (K % MX_BLOCK != 0); }
+int at_least_one(int n) { return n > 1 ? n : 1; }
+long long up_div(long long a, long long b) { return (a + b - 1) / b; }
+
+ByteRange code_range(const void* p, int rows, int K, int ld) {
+  return byte_range(p, rows, 16LL * blocks_of(K), ld, 1);
+}
+ByteRange scale_range(const void* p, int rows, int K, int ld) {
+  return byte_range(p, rows, blocks_of(K), ld, 1);
+}
+
+// Strides of a quantised operand of K values a row.
+bool mx_strides_ok(int K, int ldc, int lds) {
+  const int nb = blocks_of(K);
+  return ldc >= at_least_one(16 * nb) && lds >= at_least_one(nb);
+}
+
+// Column and row counts that the kernels' 32-bit indexes hold.
+bool mx_sizes_ok(int R, int K) { return R >= 0 && K >= 0 && K <= SGEMM_MX_MAX_K; }
+
+typedef void (*quant_fn)(MxQuantArgs);
+typedef void (*quant_t_fn)(MxQuantArgs, int);
+typedef void (*dequant_fn)(MxDequantArgs);
+const quant_fn kQuant[3] = {mx_quantize_kernel<SGEMM_DTYPE_F32>, mx_quantize_kernel<SGEMM_DTYPE_BF16>,
+                            mx_quantize_kernel<SGEMM_DTYPE_F16>};
+const quant_t_fn kQuantT[3] = {mx_quantize_t_kernel<SGEMM_DTYPE_F32>,
+                               mx_quantize_t_kernel<SGEMM_DTYPE_BF16>,
+                               mx_quantize_t_kernel<SGEMM_DTYPE_F16>};
+const dequant_fn kDequant[3] = {mx_dequantize_kernel<SGEMM_DTYPE_F32>,
+                                mx_dequantize_kernel<SGEMM_DTYPE_BF16>,
+                                mx_dequantize_kernel<SGEMM_DTYPE_F16>};
+typedef void (*small_fn)(MxArgs);
+const small_fn kSmall[4] = {mx_small_kernel<-1>, mx_small_kernel<SGEMM_DTYPE_F32>,
+                            mx_small_kernel<SGEMM_DTYPE_BF16>, mx_small_kernel<SGEMM_DTYPE_F16>};
+
+int launch_quantize(int dtype, int trans, const MxQuantArgs& g, hipStream_t stream) {
+  const long long nb = blocks_of(g.K);
+  if (trans) {
+    const long long kgroups = up_div(nb, MXT_BLOCKS);
+    const long long wgs = up_div(g.R, MXT_ROWS) * kgroups;
+    if (wgs > INT_MAX) return SGEMM_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL(kQuantT[dtype], dim3((unsigned)wgs), dim3(MX_THREADS), 0, stream, g,
+                       (int)kgroups);
+  } else {
+    const long long wgs = up_div(4 * nb * g.R, MX_THREADS * MX_UNROLL);
+    if (wgs > INT_MAX) return SGEMM_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL(kQuant[dtype], dim3((unsigned)wgs), dim3(MX_THREADS), 0, stream, g);
+  }
+  return launched();
+}
+
+// The product, A in codes (xdt < 0) or in activations.
+int launch_small(int xdt, const MxArgs& g, hipStream_t stream) {
+  const long long tm = up_div(g.M, MXS_TILE), tn = up_div(g.N, MXS_TILE);
+  if (tm > 65535) return SGEMM_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL(kSmall[xdt + 1], dim3((unsigned)tn, (unsigned)tm), dim3(MXS_THREADS), 0,
+                     stream, g);
+  return launched();
+}
+
+int launch_product(const sgemm_handle_s*, const MxArgs& g, hipStream_t stream) {
+  return launch_small(-1, g, stream);
+}
+
+// Checks shared by both product entries but for A's own.
+int validate_product(int M, int N, int K, const void* A, const void* B, int ldb, const void* SB,
+                     int ldsb, int dtype, const void* C, int ldc) {
+  const unsigned esz = tensor_elem_bytes(dtype);
+  if (esz == 0) return SGEMM_ERR_VALUE;
+  if (N < 0 || !mx_sizes_ok(M, K)) return SGEMM_ERR_SIZE;
+  if (!mx_strides_ok(K, ldb, ldsb) || ldc < at_least_one(N)) return SGEMM_ERR_LD;
+  if (M == 0 || N == 0) return SGEMM_OK;
+  if (C == nullptr || (K > 0 && (A == nullptr || B == nullptr || SB == nullptr)))
+    return SGEMM_ERR_NULL;
+  if (!elem_aligned(C, esz)) return SGEMM_ERR_VALUE;
+  const ByteRange c = byte_range(C, M, N, ldc, esz);
+  if (K > 0 && (ranges_meet(c, code_range(B, N, K, ldb)) || ranges_meet(c, scale_range(SB, N, K, ldsb))))
+    return SGEMM_ERR_ALIAS;
+  return SGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sgemm_mx_quantize(sgemm_handle_t h, int dtype, int trans, int R, int K, const void* X,
+                      int ldx, void* codes, int ldc, void* scales, int lds,
+                      hipStream_t stream) {
+  if (h == nullptr) return SGEMM_ERR_HANDLE;
+  const unsigned esz = tensor_elem_bytes(dtype);
+  if (esz == 0 || (trans != SGEMM_OP_N && trans != SGEMM_OP_T)) return SGEMM_ERR_VALUE;
+  if (!mx_sizes_ok(R, K)) return SGEMM_ERR_SIZE;
+  if (ldx < at_least_one(trans ? R : K) || !mx_strides_ok(K, ldc, lds)) return SGEMM_ERR_LD;
+  if (R == 0 || K == 0) return SGEMM_OK;
+  if (X == nullptr || codes == nullptr || scales == nullptr) return SGEMM_ERR_NULL;
+  if (!elem_aligned(X, esz)) return SGEMM_ERR_VALUE;
+  const ByteRange x = byte_range(X, trans ? K : R, trans ? R : K, ldx, esz);
+  const ByteRange c = code_range(codes, R, K, ldc), s = scale_range(scales, R, K, lds);
+  if (ranges_meet(x, c) || ranges_meet(x, s) || ranges_meet(c, s)) return SGEMM_ERR_ALIAS;
+  const int st = check_device(h);
+  if (st != SGEMM_OK) return st;
+  const MxQuantArgs g = {R, K, X, ldx, static_cast<uint8_t*>(codes), ldc,
+                         static_cast<uint8_t*>(scales), lds};
+  return launch_quantize(dtype, trans, g, stream);
+}
+
+int sgemm_mx_dequantize(sgemm_handle_t h, int dtype, int R, int K, const void* codes, int ldc,
+                        const void* scales, int lds, void* Y, int ldy, hipStream_t stream) {
+  if (h == nullptr) return SGEMM_ERR_HANDLE;
+  const unsigned esz = tensor_elem_bytes(dtype);
+  if (esz == 0) return SGEMM_ERR_VALUE;
+  if (!mx_sizes_ok(R, K)) return SGEMM_ERR_SIZE;
+  if (ldy < at_least_one(K) || !mx_strides_ok(K, ldc, lds)) return SGEMM_ERR_LD;
+  if (R == 0 || K == 0) return SGEMM_OK;
+  if (codes == nullptr || scales == nullptr || Y == nullptr) return SGEMM_ERR_NULL;
+  if (!elem_aligned(Y, esz)) return SGEMM_ERR_VALUE;
+  const ByteRange y = byte_range(Y, R, K, ldy, esz);
+  if (ranges_meet(y, code_range(codes, R, K, ldc)) || ranges_meet(y, scale_range(scales, R, K, lds)))
+    return SGEMM_ERR_ALIAS;
+  const int st = check_device(h);
+  if (st != SGEMM_OK) return st;
+  const MxDequantArgs g = {R, K, static_cast<const uint8_t*>(codes), ldc,
+                           static_cast<const uint8_t*>(scales), lds, Y, ldy};
+  const long long wgs = up_div(up_div(K, 8) * R, MX_THREADS * MX_UNROLL);
+  if (wgs > INT_MAX) return SGEMM_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL(kDequant[dtype], dim3((unsigned)wgs), dim3(MX_THREADS), 0, stream, g);
+  return launched();
+}
+
+int sgemm_validate_mx(int M, int N, int K, const void* A, int lda, const void* SA, int ldsa,
+                      const void* B, int ldb, const void* SB, int ldsb, int dtype,
+                      const void* C, int ldc) {
+  const int st = validate_product(M, N, K, A, B, ldb, SB, ldsb, dtype, C, ldc);
+  if (st != SGEMM_OK) return st;
+  if (K % MX_BLOCK != 0) return SGEMM_ERR_SIZE;
+  if (!mx_strides_ok(K, lda, ldsa)) return SGEMM_ERR_LD;
+  if (M == 0 || N == 0 || K == 0) return SGEMM_OK;
+  if (SA == nullptr) return SGEMM_ERR_NULL;
+  const ByteRange c = byte_range(C, M, N, ldc, tensor_elem_bytes(dtype));
+  if (ranges_meet(c, code_range(A, M, K, lda)) || ranges_meet(c, scale_range(SA, M, K, ldsa)))
+    return SGEMM_ERR_ALIAS;
+  return SGEMM_OK;
+}
+
+int sgemm_run_mx(sgemm_handle_t h, int M, int N, int K, float alpha, const void* A, int lda,
+                 const void* SA, int ldsa, const void* B, int ldb, const void* SB, int ldsb,
+                 float beta, int dtype, void* C, int ldc, hipStream_t stream) {
+  if (h == nullptr) return SGEMM_ERR_HANDLE;
+  int st = sgemm_validate_mx(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, dtype, C, ldc);
+  if (st != SGEMM_OK) return st;
+  if (M == 0 || N == 0) return SGEMM_OK;
+  st = check_device(h);
+  if (st != SGEMM_OK) return st;
+  const MxArgs g = {M, N, K, alpha, beta, A, lda, static_cast<const uint8_t*>(SA), ldsa,
+                    static_cast<const uint8_t*>(B), ldb, static_cast<const uint8_t*>(SB), ldsb,
+                    dtype, C, ldc};
+  return launch_product(h, g, stream);
+}
+
+int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K, float alpha,
+                       const void* X, int ldx, const void* B, int ldb, const void* SB, int ldsb,
+                       float beta, int dtype, void* C, int ldc, hipStream_t stream) {
+  if (h == nullptr) return SGEMM_ERR_HANDLE;
+  const unsigned xsz = tensor_elem_bytes(xtype);
+  if (xsz == 0) return SGEMM_ERR_VALUE;
+  int st = validate_product(M, N, K, X, B, ldb, SB, ldsb, dtype, C, ldc);
+  if (st != SGEMM_OK) return st;
+  if (ldx < at_least_one(K)) return SGEMM_ERR_LD;
+  if (M == 0 || N == 0) return SGEMM_OK;
+  if (K > 0 && !elem_aligned(X, xsz)) return SGEMM_ERR_VALUE;
+  if (ranges_meet(byte_range(C, M, N, ldc, tensor_elem_bytes(dtype)), byte_range(X, M, K, ldx, xsz)))
+    return SGEMM_ERR_ALIAS;
+  st = check_device(h);
+  if (st != SGEMM_OK) return st;
+  MxArgs g = {M, N, K, alpha, beta, X, ldx, nullptr, 0, static_cast<const uint8_t*>(B), ldb,
+              static_cast<const uint8_t*>(SB), ldsb, dtype, C, ldc};
+  if (M <= MXS_TILE) return launch_small(xtype, g, stream);
+  // A's codes and then its scales in the handle's workspace
+  const size_t nb = (size_t)blocks_of(K), rows = (size_t)M;
+  if (h->workspace_bytes < 17 * nb * rows || 16 * nb > INT_MAX) return SGEMM_ERR_SCRATCH;
+  uint8_t* codes = static_cast<uint8_t*>(h->workspace);
+  uint8_t* scales = codes + 16 * nb * rows;
+  const MxQuantArgs q = {M, K, X, ldx, codes, (int)(16 * nb), scales, (int)nb};
+  if (K > 0) {
+    st = launch_quantize(xtype, SGEMM_OP_N, q, stream);
+    if (st != SGEMM_OK) return st;
+  }
+  g.K = (int)(MX_BLOCK * nb);
+  g.A = codes;
+  g.lda = q.ldc;
+  g.SA = scales;
+  g.ldsa = q.lds;
+  return launch_product(h, g, stream);
+}
+
+}  // extern "C"

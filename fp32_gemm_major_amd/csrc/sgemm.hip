@@ -19,6 +19,7 @@
 #include <new>
 
 #include "diag.hpp"
+#include "handle.hpp"
 #include "lowp_gemm.hpp"
 #include "lowp_gemv.hpp"
 #include "mfma_sgemm.hpp"
@@ -28,16 +29,6 @@
 #include "valu_sgemm.hpp"
 
 using namespace sgemm;
-
-struct sgemm_handle_s {
-  int device;
-  int cus;
-  int variant;       // SGEMM_VARIANT_*
-  int forced_kernel; // -1 = automatic
-  void* workspace;   // caller's device memory for partial sums, or null
-  size_t workspace_bytes;
-  int forced_lowp;   // low-precision product kernel, -1 = automatic
-};
 
 namespace {
 
@@ -1158,7 +1149,7 @@ const char* sgemm_status_string(int status) {
     case SGEMM_ERR_ALIAS: return "C overlaps A or B";
     case SGEMM_ERR_UNSUPPORTED: return "forced kernel cannot run these arguments";
     case SGEMM_ERR_SCRATCH:
-      return "the forced kernel needs more scratch than the library's fixed buffer holds";
+      return "more scratch needed than the fixed buffer or the handle's workspace holds";
     default: return "unknown status";
   }
 }

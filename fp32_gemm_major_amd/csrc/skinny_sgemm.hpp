@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(SKINNY_THREADS)
 // products: 3.9 us with 256-thread workgroups and 8 loads at a time).
 constexpr int SKINNY_REDUCE_THREADS = 64;
 
-__global__ void __launch_bounds__(SKINNY_REDUCE_THREADS)
+static __global__ void __launch_bounds__(SKINNY_REDUCE_THREADS)
     skinny_reduce_kernel(GemmArgs g, int splits, const float* __restrict__ ws) {
   const int M = g.M, N = g.N;
   const int stride = skinny_ws_stride(N);

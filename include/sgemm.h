@@ -74,7 +74,9 @@ enum sgemm_status {
   SGEMM_ERR_ALIAS = -8,  /* the C window overlaps the A or B window */
   SGEMM_ERR_UNSUPPORTED = -9, /* forced kernel cannot run these arguments */
   SGEMM_ERR_SCRATCH = -10  /* sgemm_run_ex_noalloc: forced kernel needs more
-                              than SGEMM_SCRATCH_BYTES of scratch */
+                              than SGEMM_SCRATCH_BYTES of scratch; 4-bit and
+                              loss entries: the handle's workspace is smaller
+                              than the call needs */
 };
 
 /* Operand storage for sgemm_run_ex: as stated (N) or transposed (T). */
@@ -362,6 +364,7 @@ int sgemm_diag_wall_clock_khz(int* khz);
  * workspace, when set, also serves the split-K kernels of products with few
  * rows (sgemm_lowp_kernel_schedule). */
 enum sgemm_dtype {
+  SGEMM_DTYPE_F32 = 0, /* tensors of the 4-bit and loss entries only */
   SGEMM_DTYPE_BF16 = 1,
   SGEMM_DTYPE_F16 = 2,
   SGEMM_DTYPE_FP8_E4M3 = 3, /* OCP 8-bit: 4 exponent bits, bias 7, no inf */
@@ -445,6 +448,65 @@ int sgemm_diag_mfma_chain_lowp(int dtype, int workgroups, int iterations,
  * storage cannot take the arguments makes sgemm_run_lowp return
  * SGEMM_ERR_UNSUPPORTED. */
 int sgemm_set_lowp_kernel(sgemm_handle_t h, int kernel_id);
+
+/* ---- microscaled 4-bit operands --------------------------------------------
+ *
+ * A microscaled row holds K values in blocks of 32 along K: 16 code bytes a
+ * block (value 2i in the low half of byte i, 2i+1 in the high half; E2M1: a
+ * sign and one of 0, 1/2, 1, 3/2, 2, 3, 4, 6) and one scale byte s, worth
+ * 2^(s-127).  Codes and scales are two byte matrices, both row-major over the
+ * rows, with strides in bytes of at least 16*ceil(K/32) and ceil(K/32); any
+ * byte alignment.  s = 255 makes every value of its block NaN.
+ *
+ * Ownership, streams, errors and threading as for sgemm_run.  K is at most
+ * SGEMM_MX_MAX_K (SGEMM_ERR_SIZE).  Tensors of activations and results have
+ * dtype SGEMM_DTYPE_F32, _BF16 or _F16 (SGEMM_ERR_VALUE for another, and for
+ * a tensor not aligned to its element). */
+#define SGEMM_MX_MAX_K (1 << 27)
+
+/* Quantise X into codes and scales, whole blocks: positions from K to the end
+ * of the last block hold zero codes.  X is R x K (trans SGEMM_OP_N) or stored
+ * K x R (SGEMM_OP_T), stride ldx in elements.  A block with largest magnitude
+ * a gets s - 127 = floor(log2 a) - 2, at least -127 (also for a = 0), and the
+ * elements x / 2^(s-127) rounded to the nearest code, ties to the even code,
+ * magnitudes over 6 to 6.  A block holding an infinity or a NaN gets s = 255
+ * and zero codes.  SGEMM_ERR_ALIAS if X, codes and scales overlap. */
+int sgemm_mx_quantize(sgemm_handle_t h, int dtype, int trans, int R, int K,
+                      const void* X, int ldx, void* codes, int ldc,
+                      void* scales, int lds, hipStream_t stream);
+
+/* The values of the first K positions of R microscaled rows, as a tensor of
+ * type dtype and stride ldy.  In the type that was quantised (and in
+ * SGEMM_DTYPE_F32) every value is exact. */
+int sgemm_mx_dequantize(sgemm_handle_t h, int dtype, int R, int K,
+                        const void* codes, int ldc, const void* scales,
+                        int lds, void* Y, int ldy, hipStream_t stream);
+
+/* C(m,n) = alpha * sum_k A(m,k)*B(n,k) + beta*C(m,n): A is M and B is N
+ * microscaled rows of K values, K a multiple of 32 (SGEMM_ERR_SIZE; the
+ * quantiser's whole blocks make it one), C of type dtype.  beta == 0 and
+ * K == 0 as in sgemm_run.  Products and sums are formed in the matrix units
+ * with FP32 accuracy: |C - exact| <= 4*max(K,1)*2^-24*(|alpha|*sum_k|a*b| +
+ * |beta*c|), plus one rounding to dtype.  The same inputs give the same bits.
+ * sgemm_validate_mx makes the argument checks alone, without a device. */
+int sgemm_run_mx(sgemm_handle_t h, int M, int N, int K, float alpha,
+                 const void* A, int lda, const void* SA, int ldsa,
+                 const void* B, int ldb, const void* SB, int ldsb, float beta,
+                 int dtype, void* C, int ldc, hipStream_t stream);
+int sgemm_validate_mx(int M, int N, int K, const void* A, int lda,
+                      const void* SA, int ldsa, const void* B, int ldb,
+                      const void* SB, int ldsb, int dtype, const void* C,
+                      int ldc);
+
+/* The same with A given as an M x K tensor X of type xtype (any K; stride ldx
+ * in elements) and quantised as sgemm_mx_quantize does: a linear layer with
+ * 4-bit weights.  The result is that of the two calls.  Up to 16 rows are
+ * quantised on the way into the product; more need 17*ceil(K/32)*M bytes of
+ * the handle's workspace (SGEMM_ERR_SCRATCH). */
+int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K,
+                       float alpha, const void* X, int ldx, const void* B,
+                       int ldb, const void* SB, int ldsb, float beta,
+                       int dtype, void* C, int ldc, hipStream_t stream);
 
 /* ---- handle options ----------------------------------------------------- */
 

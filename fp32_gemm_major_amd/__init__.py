@@ -3,7 +3,8 @@
 C = alpha * A * B + beta * C for row-major FP32 operands ("GEMM 优化之路",
 problem statement), and the same product with bfloat16 or float16 A and B and
 FP32 C (the gsyq.cn guide, section 5.1).  Beside the products stand microscaled
-4-bit operands (quantisation, and products of them).  Every step runs in the
+4-bit operands (quantisation, and products of them) and the softmax cross
+entropy of an output layer with its gradients.  Every step runs in the
 HIP library ``libsgemm.so``; this module only marshals arguments.  PyTorch provides device memory and streams.
 There is no fallback: if the library is missing, loading fails loudly.
 """
@@ -67,6 +68,8 @@ EXPORTED = [
     "sgemm_lowp_kernel_schedule", "sgemm_lowp_plan_handle",
     "sgemm_mx_quantize", "sgemm_mx_dequantize", "sgemm_run_mx", "sgemm_validate_mx",
     "sgemm_run_mx_quant",
+    "sgemm_ce_workspace_size", "sgemm_ce_forward", "sgemm_ce_backward", "sgemm_validate_ce",
+    "sgemm_validate_ce_backward",
 ]
 
 
@@ -125,7 +128,14 @@ def _bind(lib):
     lib.sgemm_run_mx.argtypes = [p, i, i, i, f, p, i, p, i, p, i, p, i, f, i, p, i, p]
     lib.sgemm_validate_mx.argtypes = [i, i, i, p, i, p, i, p, i, p, i, i, p, i]
     lib.sgemm_run_mx_quant.argtypes = [p, i, i, i, i, f, p, i, p, i, p, i, f, i, p, i, p]
-    for name in ("sgemm_mx_quantize", "sgemm_mx_dequantize", "sgemm_run_mx",
+    q, sp = ctypes.c_longlong, ctypes.POINTER(ctypes.c_size_t)
+    lib.sgemm_ce_workspace_size.argtypes = [p, i, i, i, i, i, sp, sp]
+    lib.sgemm_ce_forward.argtypes = [p, i, i, i, i, f, p, i, p, i, p, q, p, p, p]
+    lib.sgemm_ce_backward.argtypes = [p, i, i, i, i, f, p, i, p, i, p, q, p, p, p, p, i, p, i, p]
+    lib.sgemm_validate_ce.argtypes = [i, i, i, i, p, i, p, i, p, p, p]
+    lib.sgemm_validate_ce_backward.argtypes = [i, i, i, i, p, i, p, i, p, p, p, p, p, i, p, i]
+    for name in ("sgemm_ce_workspace_size", "sgemm_ce_forward", "sgemm_ce_backward",
+                 "sgemm_validate_ce", "sgemm_validate_ce_backward", "sgemm_mx_quantize", "sgemm_mx_dequantize", "sgemm_run_mx",
                  "sgemm_validate_mx", "sgemm_run_mx_quant"):
         getattr(lib, name).restype = i
     for name in ("sgemm_lowp_kernel_schedule", "sgemm_lowp_plan_handle",
@@ -287,6 +297,40 @@ def sgemm_run_mx_quant(h, xtype, M, N, K, alpha, X, ldx, B, ldb, SB, ldsb, beta,
     return _check(library().sgemm_run_mx_quant(h, xtype, M, N, K, alpha, X, ldx, B, ldb, SB,
                                                ldsb, beta, dtype, C, ldc, stream),
                   "sgemm_run_mx_quant")
+
+
+def sgemm_ce_workspace_size(h, dtype, T, V, D, backward):
+    """(least, full) bytes of workspace of a loss call (``backward``: of its
+    gradients)."""
+    least, full = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(library().sgemm_ce_workspace_size(h, dtype, T, V, D, backward, ctypes.byref(least),
+                                             ctypes.byref(full)), "sgemm_ce_workspace_size")
+    return least.value, full.value
+
+
+def sgemm_ce_forward(h, dtype, T, V, D, alpha, X, ldx, W, ldw, labels, ignore, loss, lse,
+                     stream=0) -> int:
+    """Softmax cross entropy of alpha*X*W^T; all pointers are device addresses."""
+    return _check(library().sgemm_ce_forward(h, dtype, T, V, D, alpha, X, ldx, W, ldw, labels,
+                                             ignore, loss, lse, stream), "sgemm_ce_forward")
+
+
+def sgemm_ce_backward(h, dtype, T, V, D, alpha, X, ldx, W, ldw, labels, ignore, lse, dloss,
+                      dlse, dX, lddx, dW, lddw, stream=0) -> int:
+    """Its gradients; dlse, dX and dW may be None."""
+    return _check(library().sgemm_ce_backward(h, dtype, T, V, D, alpha, X, ldx, W, ldw, labels,
+                                              ignore, lse, dloss, dlse, dX, lddx, dW, lddw,
+                                              stream), "sgemm_ce_backward")
+
+
+def sgemm_validate_ce(dtype, T, V, D, X, ldx, W, ldw, labels, loss, lse) -> int:
+    return library().sgemm_validate_ce(dtype, T, V, D, X, ldx, W, ldw, labels, loss, lse)
+
+
+def sgemm_validate_ce_backward(dtype, T, V, D, X, ldx, W, ldw, labels, lse, dloss, dlse, dX,
+                               lddx, dW, lddw) -> int:
+    return library().sgemm_validate_ce_backward(dtype, T, V, D, X, ldx, W, ldw, labels, lse,
+                                                dloss, dlse, dX, lddx, dW, lddw)
 
 
 def sgemm_destroy(h) -> int:
@@ -744,6 +788,73 @@ class Handle:
         s = self._on(stream, A=A, B=B.codes, B_scales=B.scales, C=C)
         return sgemm_run_mx_quant(self.h, xtype, M, N, K, alpha, A.data_ptr(), lda, b, ldb, sb,
                                   ldsb, beta, dtype, C.data_ptr(), ldc, s)
+
+    # -- softmax cross entropy of an output layer --
+
+    def ce_workspace_size(self, X, W, backward=False, least=False) -> int:
+        """Bytes of workspace (``set_workspace``) that ``ce_forward`` (or
+        ``ce_backward``) on these tensors makes use of; ``least``: the fewest
+        it runs with."""
+        dtype, T, V, D, _, _ = _ce_shapes(X, W)
+        return sgemm_ce_workspace_size(self.h, dtype, T, V, D, int(bool(backward)))[
+            0 if least else 1]
+
+    def ce_forward(self, X, W, labels, loss, lse, alpha=1.0, ignore_index=-100, stream=None):
+        """loss[t] = lse[t] - z[t, labels[t]] and lse[t] = log sum_v exp z[t, v]
+        of z = alpha * X @ W^T, with X T x D and W V x D of one type (float32,
+        bfloat16 or float16), ``labels`` T int64 and ``loss``, ``lse`` T
+        float32.  Rows labelled ``ignore_index`` are left out (0, 0).  z is
+        never kept; the handle's workspace holds a piece of it."""
+        dtype, T, V, D, ldx, ldw = _ce_shapes(X, W)
+        _vectors(T, torch.int64, labels=labels)
+        _vectors(T, torch.float32, loss=loss, lse=lse)
+        s = self._on(stream, X=X, W=W, labels=labels, loss=loss, lse=lse)
+        return sgemm_ce_forward(self.h, dtype, T, V, D, alpha, X.data_ptr(), ldx, W.data_ptr(),
+                                ldw, labels.data_ptr(), ignore_index, loss.data_ptr(),
+                                lse.data_ptr(), s)
+
+    def ce_backward(self, X, W, labels, lse, dloss, dX=None, dW=None, dlse=None, alpha=1.0,
+                    ignore_index=-100, stream=None):
+        """The gradients dX (T x D) and dW (V x D), of X's type, from those of
+        every row's loss (``dloss``, T float32) and, if given, of its lse
+        (``dlse``); ``lse`` is ``ce_forward``'s.  Either may be None."""
+        dtype, T, V, D, ldx, ldw = _ce_shapes(X, W)
+        _vectors(T, torch.int64, labels=labels)
+        _vectors(T, torch.float32, lse=lse, dloss=dloss, **({} if dlse is None else {"dlse": dlse}))
+        outs, args = {}, []
+        for name, t, rows in (("dX", dX, T), ("dW", dW, V)):
+            if t is None:
+                args += [None, 0]
+                continue
+            kind, ld = _matrix(name, t)
+            if kind != dtype or tuple(t.shape) != (rows, D):
+                raise ValueError(f"{name} must be {rows} x {D} of X's type")
+            outs[name] = t
+            args += [t.data_ptr(), ld]
+        if dlse is not None:
+            outs["dlse"] = dlse
+        s = self._on(stream, X=X, W=W, labels=labels, lse=lse, dloss=dloss, **outs)
+        return sgemm_ce_backward(self.h, dtype, T, V, D, alpha, X.data_ptr(), ldx, W.data_ptr(),
+                                 ldw, labels.data_ptr(), ignore_index, lse.data_ptr(),
+                                 dloss.data_ptr(), None if dlse is None else dlse.data_ptr(),
+                                 *args, s)
+
+
+def _ce_shapes(X, W):
+    """Type, sizes and leading dimensions of a loss call's X and W."""
+    (dtype, ldx), (other, ldw) = _matrix("X", X), _matrix("W", W)
+    if dtype != other or X.shape[1] != W.shape[1]:
+        raise ValueError(f"X ({X.dtype}, {tuple(X.shape)}) and W ({W.dtype}, {tuple(W.shape)}) "
+                         "must have one type and as many columns")
+    return dtype, X.shape[0], W.shape[0], X.shape[1], ldx, ldw
+
+
+def _vectors(n, dtype, **tensors):
+    for name, t in tensors.items():
+        if t.dtype != dtype or t.dim() != 1:
+            raise TypeError(f"{name} must be a 1-D {dtype} tensor")
+        if t.shape[0] != n or not t.is_contiguous():
+            raise ValueError(f"{name} must be {n} contiguous elements")
 
 
 def _span(rows, cols, ld):

@@ -20,7 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libsgemm.so")
-SOURCES = [os.path.join(CSRC, name) for name in ("sgemm.hip", "mx.hip")]
+SOURCES = [os.path.join(CSRC, name) for name in ("sgemm.hip", "mx.hip", "ce.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

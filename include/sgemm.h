@@ -508,6 +508,69 @@ int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K,
                        int ldb, const void* SB, int ldsb, float beta,
                        int dtype, void* C, int ldc, hipStream_t stream);
 
+/* ---- softmax cross entropy of an output layer --------------------------------
+ *
+ *     z = alpha * X * W^T,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,label(t)
+ *
+ * for X of T x D, W of V x D (one row a word of the vocabulary), both of type
+ * dtype (SGEMM_DTYPE_F32, _BF16 or _F16) with row strides in elements, and
+ * one label a row.  z is formed in pieces of the vocabulary and never kept;
+ * products, maxima, sums and results are FP32.
+ *
+ * Rows whose label equals `ignore` are left out: loss and lse are 0 there,
+ * their row of dX is 0, and nothing of them (X, dloss, dlse may be NaN) meets
+ * dW.  A label outside [0, V) other than `ignore` makes its row's loss and
+ * gradients NaN (and so dW).  Infinities and NaNs in X and W spread as the
+ * formulas make them.
+ *
+ * Both calls divide the handle's workspace (sgemm_set_workspace) among the
+ * pieces; with less than the size's `least` bytes they return
+ * SGEMM_ERR_SCRATCH, and with less than `full` they take smaller pieces and
+ * more launches.  Ownership, streams, errors and threading as for sgemm_run
+ * with a workspace.  T == 0: nothing is read (backward: dW is set to 0).
+ * SGEMM_ERR_SIZE for T < 0, V < 1 or D < 1; SGEMM_ERR_LD for a stride below D;
+ * SGEMM_ERR_VALUE for another dtype or a tensor not aligned to its element;
+ * SGEMM_ERR_ALIAS where an output overlaps another argument. */
+
+/* Workspace of a forward (backward == 0) or a backward call: the least that
+ * it runs with and what it makes use of; either pointer may be NULL. */
+int sgemm_ce_workspace_size(sgemm_handle_t h, int dtype, int T, int V, int D,
+                            int backward, size_t* least, size_t* full);
+
+/* loss and lse of every row (T floats each). */
+int sgemm_ce_forward(sgemm_handle_t h, int dtype, int T, int V, int D,
+                     float alpha, const void* X, int ldx, const void* W,
+                     int ldw, const long long* labels, long long ignore,
+                     float* loss, float* lse, hipStream_t stream);
+
+/* Gradients: with dloss (and dlse, or NULL for 0) those of the rows' loss and
+ * lse,
+ *
+ *     dz_tv = (dloss_t + dlse_t) * exp(z_tv - lse_t) - dloss_t * [v == label(t)]
+ *     dX = alpha * dz * W,   dW = alpha * dz^T * X
+ *
+ * are overwritten (either may be NULL), of type dtype.  lse is a forward
+ * call's.  dz is rounded to dtype between the two products (binary16: after a
+ * power-of-two scale a row), their sums are FP32 and the results are rounded
+ * once. */
+int sgemm_ce_backward(sgemm_handle_t h, int dtype, int T, int V, int D,
+                      float alpha, const void* X, int ldx, const void* W,
+                      int ldw, const long long* labels, long long ignore,
+                      const float* lse, const float* dloss, const float* dlse,
+                      void* dX, int lddx, void* dW, int lddw,
+                      hipStream_t stream);
+
+/* The argument checks of the two, without a device. */
+int sgemm_validate_ce(int dtype, int T, int V, int D, const void* X, int ldx,
+                      const void* W, int ldw, const long long* labels,
+                      const float* loss, const float* lse);
+int sgemm_validate_ce_backward(int dtype, int T, int V, int D, const void* X,
+                               int ldx, const void* W, int ldw,
+                               const long long* labels, const float* lse,
+                               const float* dloss, const float* dlse,
+                               const void* dX, int lddx, const void* dW,
+                               int lddw);
+
 /* ---- handle options ----------------------------------------------------- */
 
 /* Choose the kernel family used by sgemm_run on this handle. */

@@ -1,0 +1,114 @@
+"""The output layer's loss without a GPU: the plain implementation against
+differences and closed forms, and every refusal of the C entries and the
+binding."""
+import numpy as np
+import pytest
+
+import fp32_gemm_major_amd as sg
+from tests import ce_reference as ref
+
+X, W, Y, LOSS, LSE = 0x10000000, 0x20000000, 0x30000000, 0x31000000, 0x32000000  # never touched
+DL, DE, DX, DW = 0x33000000, 0x34000000, 0x40000000, 0x50000000
+F32, BF16, F16 = sg.SGEMM_DTYPE_F32, sg.SGEMM_DTYPE_BF16, sg.SGEMM_DTYPE_F16
+
+
+def test_reference_closed_forms():
+    # equal logits: log V; one logit far above: its label costs nothing
+    _, loss, lse = ref.forward(np.zeros((2, 3)), np.ones((7, 3)), np.array([0, 6]))
+    assert np.allclose(loss, np.log(7)) and np.allclose(lse, np.log(7))
+    w = np.zeros((4, 1))
+    w[2] = 100.0
+    _, loss, lse = ref.forward(np.ones((2, 1)), w, np.array([2, 1]))
+    assert np.allclose(loss, [0, 100]) and np.allclose(lse, 100)
+
+
+def test_reference_gradients_by_differences():
+    rng = np.random.default_rng(0)
+    T, V, D, alpha = 5, 11, 4, 0.7
+    x, w = rng.standard_normal((T, D)), rng.standard_normal((V, D))
+    labels = np.array([3, ref.IGNORE, 0, 10, 3])
+    a, b = rng.standard_normal(T), rng.standard_normal(T)
+
+    def total(x, w):
+        _, loss, lse = ref.forward(x, w, labels, alpha)
+        return (a * loss + b * lse).sum()
+
+    z, _, lse = ref.forward(x, w, labels, alpha)
+    dx, dw = ref.gradients(x, w, labels, ref.dlogits(z, labels, lse, a, b), alpha)
+    h = 1e-6
+    for g, t in ((dx, x), (dw, w)):
+        for i in np.ndindex(t.shape):
+            keep = t[i]
+            t[i] = keep + h
+            up = total(x, w)
+            t[i] = keep - h
+            down = total(x, w)
+            t[i] = keep
+            assert abs((up - down) / (2 * h) - g[i]) < 1e-7
+
+
+def fwd(**kw):
+    a = dict(dtype=F32, T=4, V=9, D=6, X=X, ldx=6, W=W, ldw=6, labels=Y, loss=LOSS, lse=LSE)
+    a.update(kw)
+    return sg.sgemm_validate_ce(*a.values())
+
+
+def bwd(**kw):
+    a = dict(dtype=F32, T=4, V=9, D=6, X=X, ldx=6, W=W, ldw=6, labels=Y, lse=LSE, dloss=DL, dlse=DE,
+             dX=DX, lddx=6, dW=DW, lddw=6)
+    a.update(kw)
+    return sg.sgemm_validate_ce_backward(*a.values())
+
+
+def test_validate():
+    for v in (fwd, bwd):
+        assert v() == sg.SGEMM_OK
+        assert v(dtype=BF16) == sg.SGEMM_OK and v(dtype=F16) == sg.SGEMM_OK
+        for bad in (-1, 3, 4):
+            assert v(dtype=bad) == sg.SGEMM_ERR_VALUE
+        assert v(T=-1) == sg.SGEMM_ERR_SIZE and v(V=0) == sg.SGEMM_ERR_SIZE
+        assert v(D=0) == sg.SGEMM_ERR_SIZE and v(V=-3) == sg.SGEMM_ERR_SIZE
+        assert v(ldx=5) == sg.SGEMM_ERR_LD and v(ldw=5) == sg.SGEMM_ERR_LD
+        for name in ("X", "W", "labels", "lse"):
+            assert v(**{name: None}) == sg.SGEMM_ERR_NULL, name
+        assert v(T=0, X=None, labels=None) == sg.SGEMM_OK
+        assert v(X=X + 2) == sg.SGEMM_ERR_VALUE and v(W=W + 1, dtype=BF16) == sg.SGEMM_ERR_VALUE
+        assert v(X=X + 2, dtype=BF16) == sg.SGEMM_OK
+    assert fwd(loss=None) == sg.SGEMM_ERR_NULL
+    assert fwd(loss=LSE + 12) == sg.SGEMM_ERR_ALIAS and fwd(loss=LSE + 16) == sg.SGEMM_OK
+    for a in (X, W, Y):
+        assert fwd(loss=a) == sg.SGEMM_ERR_ALIAS and fwd(lse=a + 4) == sg.SGEMM_ERR_ALIAS
+    assert bwd(dloss=None) == sg.SGEMM_ERR_NULL
+    assert bwd(dlse=None) == sg.SGEMM_OK
+    assert bwd(dX=None, lddx=0) == sg.SGEMM_OK and bwd(dW=None, lddw=0) == sg.SGEMM_OK
+    assert bwd(lddx=5) == sg.SGEMM_ERR_LD and bwd(lddw=5) == sg.SGEMM_ERR_LD
+    assert bwd(dX=DX + 2) == sg.SGEMM_ERR_VALUE
+    for a in (X, W, Y, LSE, DL, DE, DW):
+        assert bwd(dX=a) == sg.SGEMM_ERR_ALIAS, hex(a)
+    for a in (X, W, Y, LSE, DL, DE):
+        assert bwd(dW=a) == sg.SGEMM_ERR_ALIAS, hex(a)
+
+
+def test_null_handle():
+    lib = sg.library()
+    assert lib.sgemm_ce_workspace_size(None, F32, 1, 1, 1, 0, None, None) == sg.SGEMM_ERR_HANDLE
+    assert lib.sgemm_ce_forward(None, F32, 1, 1, 1, 1.0, X, 1, W, 1, Y, -100, LOSS, LSE,
+                                None) == sg.SGEMM_ERR_HANDLE
+    assert lib.sgemm_ce_backward(None, F32, 1, 1, 1, 1.0, X, 1, W, 1, Y, -100, LSE, DL, None, DX, 1,
+                                 DW, 1, None) == sg.SGEMM_ERR_HANDLE
+
+
+def test_binding_checks():
+    torch = pytest.importorskip("torch")
+    x, w = torch.zeros(3, 8), torch.zeros(5, 8)
+    assert sg._ce_shapes(x, w) == (F32, 3, 5, 8, 8, 8)
+    with pytest.raises(ValueError):
+        sg._ce_shapes(x, w.bfloat16())
+    with pytest.raises(ValueError):
+        sg._ce_shapes(x, torch.zeros(5, 7))
+    with pytest.raises(TypeError):
+        sg._vectors(3, torch.int64, labels=torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        sg._vectors(3, torch.int64, labels=torch.zeros(4, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        sg._vectors(3, torch.float32, loss=torch.zeros(6)[::2])

@@ -7,6 +7,7 @@
 #include <limits.h>
 
 #include "handle.hpp"
+#include "mx_gemm.hpp"
 #include "mx_quant.hpp"
 #include "mx_small.hpp"
 
@@ -74,7 +75,45 @@ int launch_small(int xdt, const MxArgs& g, hipStream_t stream) {
   return launched();
 }
 
-int launch_product(const sgemm_handle_s*, const MxArgs& g, hipStream_t stream) {
+typedef void (*tile_fn)(MxArgs, int, int, int);
+struct MxTileDesc {
+  int b;  // rows and columns of the tile
+  int threads;
+  tile_fn kernel[3];  // by type of C
+};
+template <class T>
+constexpr MxTileDesc tile_desc() {
+  return MxTileDesc{T::BM, T::THREADS,
+                    {mx_gemm_kernel<T, SGEMM_DTYPE_F32>, mx_gemm_kernel<T, SGEMM_DTYPE_BF16>,
+                     mx_gemm_kernel<T, SGEMM_DTYPE_F16>}};
+}
+const MxTileDesc kTiles[3] = {tile_desc<X256x256>(), tile_desc<X128x128>(), tile_desc<X64x64>()};
+
+// The tile kernels' direct loads address a tile's rows by 32-bit offsets.
+bool tile_fits(const MxTileDesc& t, const MxArgs& g) {
+  const long long far = 1LL << 32, r = t.b - 1;
+  return r * g.lda + 128 < far && r * g.ldb + 128 < far && r * g.ldsa + 8 < far &&
+         r * g.ldsb + 8 < far && up_div(g.M, t.b) * up_div(g.N, t.b) <= INT_MAX;
+}
+
+int launch_tile(const MxTileDesc& t, const MxArgs& g, hipStream_t stream) {
+  const int tm = (int)up_div(g.M, t.b), tn = (int)up_div(g.N, t.b);
+  hipLaunchKernelGGL(t.kernel[g.cdt], dim3((unsigned)(tm * tn)), dim3(t.threads), 0, stream, g, tm,
+                     tn, band_rows(tm, tm * tn));
+  return launched();
+}
+
+// At most 16 rows: the kernel that reads B once from memory.  Else the
+// largest tile that gives every CU one, or the 256-square one where 128-square
+// tiles would take three rounds or more.
+int launch_product(const sgemm_handle_s* h, const MxArgs& g, hipStream_t stream) {
+  if (g.M > MXS_TILE && g.K > 0) {
+    const long long t256 = up_div(g.M, 256) * up_div(g.N, 256);
+    const long long t128 = up_div(g.M, 128) * up_div(g.N, 128);
+    const int at = t256 >= h->cus || t128 > 2LL * h->cus ? 0 : t128 >= h->cus ? 1 : 2;
+    for (int i = at; i < 3; ++i)
+      if (tile_fits(kTiles[i], g)) return launch_tile(kTiles[i], g, stream);
+  }
   return launch_small(-1, g, stream);
 }
 

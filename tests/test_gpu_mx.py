@@ -148,7 +148,11 @@ def check(got, a, b, K, alpha, beta, c, dt, what=""):
 
 PRODUCTS = [(1, 1, 32), (1, 16, 64), (1, 4096, 4096), (2, 17, 96), (4, 100, 512), (16, 333, 4096),
             (17, 40, 544), (33, 65, 32), (64, 64, 256), (100, 128, 1056), (128, 256, 800),
-            (200, 300, 160), (256, 512, 512), (257, 511, 288), (1000, 1500, 800)]
+            (200, 300, 160), (256, 512, 512), (257, 511, 288), (1000, 1500, 800),
+            # enough tiles for the 128-square and the 256-square ones, K of less
+            # than a step, of whole steps (odd and even counts) and ragged
+            (2050, 2100, 64), (2050, 2100, 256), (2048, 2176, 1024), (2050, 2100, 1312),
+            (2900, 3050, 96), (2900, 3050, 256), (2816, 3328, 512), (2900, 3050, 1568)]
 
 
 @pytest.mark.parametrize("M,N,K", PRODUCTS)

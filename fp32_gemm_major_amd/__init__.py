@@ -518,6 +518,11 @@ def mfma_chain_tflops(workgroups=1024, iterations=4096, reps=3, dtype=None):
 
 # ---- torch-tensor convenience ------------------------------------------------
 
+def _current_stream(index: int) -> int:
+    """Address of torch's current stream on a device."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 TENSOR_DTYPES = {torch.float32: SGEMM_DTYPE_F32, torch.bfloat16: SGEMM_DTYPE_BF16,
                  torch.float16: SGEMM_DTYPE_F16}
 
@@ -525,51 +530,54 @@ TENSOR_DTYPES = {torch.float32: SGEMM_DTYPE_F32, torch.bfloat16: SGEMM_DTYPE_BF1
 class Mx4:
     """Microscaled 4-bit rows: ``codes``, a uint8 matrix of 16 bytes a block of
     32 values, and ``scales``, a uint8 matrix of one byte a block (the
-    exponent plus 127).  Rows may be strided, bytes of a row not."""
+    exponent plus 127).  Rows may be strided, bytes of a row not.  ``rows``
+    and ``K`` (values a row holds, whole blocks) are its sizes."""
 
-    __slots__ = ("codes", "scales")
+    __slots__ = ("codes", "scales", "rows", "K", "_ldc", "_lds")
 
     def __init__(self, codes, scales):
         for name, t in (("codes", codes), ("scales", scales)):
             if t.dtype != torch.uint8 or t.dim() != 2:
                 raise TypeError(f"{name} must be a 2-D uint8 tensor")
-            if t.numel() and t.stride(1) != 1:
-                raise ValueError(f"{name} must be row-major (unit column stride)")
-        if codes.shape[0] != scales.shape[0] or codes.shape[1] != 16 * scales.shape[1]:
+        (rows, width), (rows_s, nb) = codes.shape, scales.shape
+        if rows != rows_s or width != 16 * nb:
             raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} "
                              "disagree: 16 code bytes and a scale byte a block")
-        self.codes, self.scales = codes, scales
-
-    @property
-    def rows(self) -> int:
-        return self.codes.shape[0]
-
-    @property
-    def K(self) -> int:
-        """Values a row holds, whole blocks."""
-        return SGEMM_MX_BLOCK * self.scales.shape[1]
+        self.codes, self.scales, self.rows, self.K = codes, scales, rows, SGEMM_MX_BLOCK * nb
+        self._ldc, self._lds = _row_stride("codes", codes), _row_stride("scales", scales)
 
     @staticmethod
     def empty(rows: int, K: int, device="cuda") -> "Mx4":
         nb = -(-K // SGEMM_MX_BLOCK)
-        return Mx4(torch.empty(rows, 16 * nb, dtype=torch.uint8, device=device),
-                   torch.empty(rows, nb, dtype=torch.uint8, device=device))
+        q = object.__new__(Mx4)
+        q.codes = torch.empty((rows, 16 * nb), dtype=torch.uint8, device=device)
+        q.scales = torch.empty((rows, nb), dtype=torch.uint8, device=device)
+        q.rows, q.K, q._ldc, q._lds = rows, SGEMM_MX_BLOCK * nb, max(16 * nb, 1), max(nb, 1)
+        return q
 
-    def _args(self):
-        c, s = self.codes, self.scales
-        return c.data_ptr(), max(c.stride(0), 1), s.data_ptr(), max(s.stride(0), 1)
+
+def _row_stride(name, t) -> int:
+    """Leading dimension of a 2-D row-major tensor (its rows may be strided,
+    but must not overlap)."""
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    if rows == 0 or cols == 0:
+        return max(ld, cols, 1)
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must be row-major (unit column stride)")
+    if ld < cols:
+        if rows > 1:
+            raise ValueError(f"{name}: rows overlap (stride {ld}, {cols} columns)")
+        return cols
+    return ld
 
 
 def _matrix(name, t):
     """A 2-D row-major float32, bfloat16 or float16 tensor: its library type
     and leading dimension."""
-    if t.dtype not in TENSOR_DTYPES or t.dim() != 2:
+    dtype = TENSOR_DTYPES.get(t.dtype)
+    if dtype is None or t.dim() != 2:
         raise TypeError(f"{name} must be a 2-D float32, bfloat16 or float16 tensor")
-    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must be row-major (unit column stride)")
-    if t.shape[0] > 1 and 0 < t.numel() and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)}, {t.shape[1]} columns)")
-    return TENSOR_DTYPES[t.dtype], max(t.stride(0), t.shape[1], 1)
+    return dtype, _row_stride(name, t)
 
 
 class Handle:
@@ -726,11 +734,12 @@ class Handle:
     def _on(self, stream, **tensors):
         """The stream's address, after checking that every tensor lies on the
         handle's device."""
+        index = self.device.index
         for name, t in tensors.items():
-            if t.device != self.device:
+            if t.get_device() != index:
                 raise ValueError(f"{name} is on {t.device}, the handle on {self.device}")
         if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return _current_stream(index)
         return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
     def mx4_quantize(self, X, trans=False, out=None, stream=None):
@@ -739,31 +748,34 @@ class Handle:
         (else allocated on ``stream``).  K need not be whole blocks; the last
         one is filled with zeros."""
         dtype, ldx = _matrix("X", X)
-        R, K = X.shape[::-1] if trans else X.shape
+        R, K = X.shape
+        if trans:
+            R, K = K, R
         if out is None:
             if stream is None:
-                out = Mx4.empty(R, K, X.device)
+                out = Mx4.empty(R, K, self.device)
             else:
                 s = stream if isinstance(stream, torch.cuda.Stream) else \
                     torch.cuda.ExternalStream(stream, self.device)
                 with torch.cuda.stream(s):
-                    out = Mx4.empty(R, K, X.device)
+                    out = Mx4.empty(R, K, self.device)
         elif out.rows != R or out.K != SGEMM_MX_BLOCK * -(-K // SGEMM_MX_BLOCK):
             raise ValueError(f"out holds {out.rows} rows of {out.K} values, X gives {R} of {K}")
-        codes, ldc, scales, lds = out._args()
-        sgemm_mx_quantize(self.h, dtype, int(bool(trans)), R, K, X.data_ptr(), ldx, codes, ldc,
-                          scales, lds, self._on(stream, X=X, codes=out.codes, scales=out.scales))
+        s = self._on(stream, X=X, codes=out.codes, scales=out.scales)
+        sgemm_mx_quantize(self.h, dtype, 1 if trans else 0, R, K, X.data_ptr(), ldx,
+                          out.codes.data_ptr(), out._ldc, out.scales.data_ptr(), out._lds, s)
         return out
 
     def mx4_dequantize(self, Q, out, stream=None):
         """The values of ``Q`` into ``out`` (float32, bfloat16 or float16; its
         columns are at most Q.K, the rest is left out).  Returns ``out``."""
         dtype, ldy = _matrix("out", out)
-        if out.shape[0] != Q.rows or out.shape[1] > Q.K:
+        R, K = out.shape
+        if R != Q.rows or K > Q.K:
             raise ValueError(f"out is {tuple(out.shape)}, Q holds {Q.rows} rows of {Q.K} values")
-        codes, ldc, scales, lds = Q._args()
-        sgemm_mx_dequantize(self.h, dtype, *out.shape, codes, ldc, scales, lds, out.data_ptr(),
-                            ldy, self._on(stream, codes=Q.codes, scales=Q.scales, out=out))
+        s = self._on(stream, codes=Q.codes, scales=Q.scales, out=out)
+        sgemm_mx_dequantize(self.h, dtype, R, K, Q.codes.data_ptr(), Q._ldc,
+                            Q.scales.data_ptr(), Q._lds, out.data_ptr(), ldy, s)
         return out
 
     def gemm_mx4(self, A, B, C, alpha=1.0, beta=0.0, stream=None):
@@ -778,16 +790,16 @@ class Handle:
         if rows != M or B.rows != N or SGEMM_MX_BLOCK * -(-K // SGEMM_MX_BLOCK) != B.K:
             raise ValueError(f"A {rows} x {K} and B {B.rows} x {B.K} do not give "
                              f"{M} x {N}")
-        b, ldb, sb, ldsb = B._args()
         if quantised:
-            a, lda, sa, ldsa = A._args()
             s = self._on(stream, A=A.codes, A_scales=A.scales, B=B.codes, B_scales=B.scales, C=C)
-            return sgemm_run_mx(self.h, M, N, K, alpha, a, lda, sa, ldsa, b, ldb, sb, ldsb,
-                                beta, dtype, C.data_ptr(), ldc, s)
+            return sgemm_run_mx(self.h, M, N, K, alpha, A.codes.data_ptr(), A._ldc,
+                                A.scales.data_ptr(), A._lds, B.codes.data_ptr(), B._ldc,
+                                B.scales.data_ptr(), B._lds, beta, dtype, C.data_ptr(), ldc, s)
         xtype, lda = _matrix("A", A)
         s = self._on(stream, A=A, B=B.codes, B_scales=B.scales, C=C)
-        return sgemm_run_mx_quant(self.h, xtype, M, N, K, alpha, A.data_ptr(), lda, b, ldb, sb,
-                                  ldsb, beta, dtype, C.data_ptr(), ldc, s)
+        return sgemm_run_mx_quant(self.h, xtype, M, N, K, alpha, A.data_ptr(), lda,
+                                  B.codes.data_ptr(), B._ldc, B.scales.data_ptr(), B._lds, beta,
+                                  dtype, C.data_ptr(), ldc, s)
 
     # -- softmax cross entropy of an output layer --
 

@@ -7,7 +7,9 @@
 #include <limits.h>
 
 #include "ce.hpp"
+#include "ce_gemm.hpp"
 #include "handle.hpp"
+#include "tile_map.hpp"
 
 using namespace sgemm;
 
@@ -46,6 +48,66 @@ constexpr int kPieceStep = 256;               // columns by which pieces grow
 struct CeLayout {
   size_t fixed, per_col;
 };
+
+// ---- calls on packed rows (16-bit X and W) ------------------------------------
+
+constexpr int kPadRows = CE_ROW_PAD, kPadCols = 256;  // whole tiles
+constexpr int kStep = 64;                             // k per step of the products
+constexpr int kSplitCols = 1024;                      // least columns of a split of dX's sums
+
+long long padded_rows(const CeProblem& a) { return round_up(a.T > 1 ? a.T : 1, kPadRows); }
+long long padded_cols(const CeProblem& a) { return round_up(a.D, kPadCols); }
+
+// Whether sizes allow packed rows: whole 16-byte units a row.
+bool packable(const CeProblem& a) {
+  return tensor_elem_bytes(a.dtype) == 2 && a.D % 8 == 0 && a.D <= INT_MAX / 4 - kPadCols &&
+         a.T <= INT_MAX - kPadRows;
+}
+// Whether a call takes them: W's rows inside the direct loads' 32-bit offsets
+// and near enough for the copy of its last rows to have their stride.  Few
+// rows of a forward pass go through the products with few rows instead.
+constexpr int kFewRows = 16;
+bool packed(const CeProblem& a, int backward) {
+  return packable(a) && a.ldw <= 2LL * a.D && (backward || a.T > kFewRows);
+}
+
+CeLayout packed_layout(const CeProblem& a, int backward) {
+  const size_t T = (size_t)a.T, Tp = (size_t)padded_rows(a), Dp = (size_t)padded_cols(a);
+  CeLayout l = {16 * 256, 0};
+  if (!backward) {
+    l.fixed += 4 * T + 20 * Tp + 2 * Tp * Dp;
+    l.per_col = Tp / 8;  // eight bytes a row for 64 columns or more
+  } else {
+    l.fixed += 4 * T + 24 * Tp + (a.dtype == SGEMM_DTYPE_F16 ? 4 : 2) * Tp * Dp +
+               2 * kStep * 2 * (size_t)a.D + 4 * T * a.D;
+    l.per_col = 2 * Tp;
+  }
+  return l;
+}
+
+// Columns of a piece, in whole tiles, that `bytes` hold beside the rest (0:
+// not even the least).
+long long packed_columns(const CeProblem& a, const CeLayout& l, size_t bytes) {
+  if (bytes < l.fixed + l.per_col * kPadCols) return 0;
+  long long cols = (long long)((bytes - l.fixed) / l.per_col);
+  const long long most = (long long)(kPieceBytes / l.per_col);
+  if (cols > most) cols = most;
+  cols = cols < kPadCols ? kPadCols : cols / kPadCols * kPadCols;
+  const long long all = round_up(a.V, kPadCols);
+  return cols < all ? cols : all;
+}
+
+// Slabs of dX's sums: where its tiles are fewer than the CUs, the vocabulary
+// is split over workgroups.
+int dx_slabs(const CeProblem& a, int cus, int bm, int bn) {
+  const long long tiles = up_div(a.T, bm) * up_div(a.D, bn);
+  long long s = up_div(cus, tiles), most = a.V / kSplitCols;
+  if (s > most) s = most;
+  if (s > 64) s = 64;
+  return s < 1 ? 1 : (int)s;
+}
+// Tiles of dX's product: 256 square unless one extent fits half of one.
+bool dx_big(const CeProblem& a) { return a.T > 128 && a.D > 128; }
 
 CeLayout layout_of(const CeProblem& a, int backward) {
   const unsigned esz = tensor_elem_bytes(a.dtype);
@@ -138,8 +200,286 @@ int zero(int rows, int D, void* out, int ldo, hipStream_t s) {
   return launched();
 }
 
+// The workspace of a call: what both ways need, so that it depends on the
+// sizes alone.
+struct CeSizes {
+  size_t least, full;
+};
+CeSizes sizes_of(const CeProblem& a, int backward, int cus) {
+  CeLayout l = layout_of(a, backward);
+  const int small = a.V < kPieceStep ? a.V : kPieceStep;
+  const int big = piece_columns(a, l, (size_t)1 << 62);
+  CeSizes z = {l.fixed + l.per_col * (size_t)(small + 8),
+               l.fixed + l.per_col * (size_t)(big + 8) + kProductBytes};
+  if (packable(a)) {
+    l = packed_layout(a, backward);
+    size_t least = l.fixed + l.per_col * kPadCols;
+    if (least > z.least) z.least = least;
+    const int slabs = !backward    ? 1
+                      : dx_big(a) ? dx_slabs(a, cus, 256, 256)
+                                  : dx_slabs(a, cus, 128, 128);
+    const size_t more = 4 * (size_t)a.T * a.D * (slabs - 1);
+    const size_t piece = l.per_col * (size_t)packed_columns(a, l, (size_t)1 << 62);
+    // (spare room is shared between slabs and the piece)
+    const size_t full = l.fixed + l.per_col * kPadCols + (2 * more > more + piece ? 2 * more : more + piece);
+    if (full > z.full) z.full = full;
+  }
+  return z;
+}
+
+// ---- launches on packed rows -----------------------------------------------------
+
+// The arguments of one piece's product.
+struct CePiece {
+  CeGemm gemm;
+  int tiles_m, tiles_n;
+};
+
+template <class T>
+CePiece piece_of(const CeProblem& a, int M, int N, int K, float c, const void* A, int lda,
+                 const void* B, int ldb, const int* count) {
+  CePiece p = {};
+  p.gemm.g.M = M;
+  p.gemm.g.N = N;
+  p.gemm.g.K = K;
+  p.gemm.g.alpha = a.alpha;
+  p.gemm.g.A = A;
+  p.gemm.g.lda = lda;
+  p.gemm.g.B = B;
+  p.gemm.g.ldb = ldb;
+  p.gemm.c = c;
+  p.gemm.count = count;
+  p.tiles_m = (int)up_div(M, T::BM);
+  p.tiles_n = (int)up_div(N, T::BN);
+  return p;
+}
+
+bool grid_fits(const CePiece& p, int splits = 1) {
+  return (long long)p.tiles_m * p.tiles_n * splits <= INT_MAX;
+}
+
+template <class T, int DT, int MODE>
+int launch_logits(const CePiece& p, const int* label, int v0, CeRow* part, int rows,
+                  float* zlabel, hipStream_t s) {
+  if (!grid_fits(p)) return SGEMM_ERR_UNSUPPORTED;
+  const int n = p.tiles_m * p.tiles_n;
+  hipLaunchKernelGGL((ce_logits_kernel<T, DT, MODE>), dim3(n), dim3(T::THREADS), 0, s, p.gemm,
+                     p.tiles_m, p.tiles_n, band_rows(p.tiles_m, n), label, v0, part, rows, zlabel);
+  return launched();
+}
+
+template <class T, int DT, int MODE>
+int launch_dz(const CePiece& p, const CeRowInfo* info, int v0, uint16_t* dz, int lddz,
+              hipStream_t s) {
+  if (!grid_fits(p)) return SGEMM_ERR_UNSUPPORTED;
+  const int n = p.tiles_m * p.tiles_n;
+  hipLaunchKernelGGL((ce_dz_gemm_kernel<T, DT, MODE>), dim3(n), dim3(T::THREADS), 0, s, p.gemm,
+                     p.tiles_m, p.tiles_n, band_rows(p.tiles_m, n), info, v0, dz, lddz);
+  return launched();
+}
+
+template <class T, int DT, int MODE>
+int launch_dx(const CePiece& p, int splits, int kps, const void* w_tail, float* sums, size_t slab,
+              hipStream_t s) {
+  if (!grid_fits(p, splits)) return SGEMM_ERR_UNSUPPORTED;
+  const int n = p.tiles_m * p.tiles_n;
+  hipLaunchKernelGGL((ce_dx_kernel<T, DT, MODE>), dim3(n * splits), dim3(T::THREADS), 0, s, p.gemm,
+                     p.tiles_m, p.tiles_n, band_rows(p.tiles_m, n), kps, w_tail, sums, slab);
+  return launched();
+}
+
+template <class T, int DT>
+int launch_dw(const CePiece& p, const float* factor, void* out, int ldo, hipStream_t s) {
+  if (!grid_fits(p)) return SGEMM_ERR_UNSUPPORTED;
+  const int n = p.tiles_m * p.tiles_n;
+  hipLaunchKernelGGL((ce_dw_kernel<T, DT>), dim3(n), dim3(T::THREADS), 0, s, p.gemm, p.tiles_m,
+                     p.tiles_n, band_rows(p.tiles_m, n), factor, out, ldo);
+  return launched();
+}
+
+// 256-square tiles where they give every CU one, else 128-square ones; rows
+// that fit half a tile take the smaller.
+bool big_tiles(long long rows, long long cols, int cus) {
+  return rows > 128 && up_div(rows, 256) * up_div(cols, 256) >= cus;
+}
+
+template <class T, int DT>
+int logits_piece(const CeProblem& a, int n, const void* xp, int dp, const void* w,
+                 const int* count, const int* label, int v0, CeRow* part, int rows, float* zlabel,
+                 hipStream_t s) {
+  const CePiece p = piece_of<T>(a, a.T, n, a.D, a.alpha * CE_LOG2E, xp, dp, w, a.ldw, count);
+  return n % T::BN == 0 && a.D % kStep == 0
+             ? launch_logits<T, DT, MODE_ALIGNED>(p, label, v0, part, rows, zlabel, s)
+             : launch_logits<T, DT, MODE_PADDED>(p, label, v0, part, rows, zlabel, s);
+}
+
+template <int DT>
+int packed_forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
+                   float* loss, float* lse, hipStream_t s) {
+  const int Tp = (int)padded_rows(a), dp = (int)padded_cols(a);
+  const long long cols = packed_columns(a, packed_layout(a, 0), h->workspace_bytes);
+  if (cols == 0) return SGEMM_ERR_SCRATCH;
+  Carver c = {static_cast<char*>(h->workspace)};
+  int* count = c.take<int>(4);
+  int* pos = c.take<int>(4 * (size_t)a.T);
+  int* order = c.take<int>(4 * (size_t)Tp);
+  int* label = c.take<int>(4 * (size_t)Tp);
+  float* zlabel = c.take<float>(4 * (size_t)Tp);
+  CeRow* state = c.take<CeRow>(sizeof(CeRow) * (size_t)Tp);
+  void* xp = c.take<char>(2 * (size_t)Tp * dp);
+  CeRow* part = c.take<CeRow>(0);
+  hipLaunchKernelGGL(ce_pack_kernel, dim3(1), dim3(CE_PACK_THREADS), 0, s, a.T, Tp, labels, pos,
+                     order, label, count, loss, lse);
+  int st = launched();
+  if (st != SGEMM_OK) return st;
+  const unsigned g = grid_of((unsigned long long)(a.T + CE_ROW_PAD) * (unsigned)(dp / 8));
+  if (g == 0) return SGEMM_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL(ce_gather_kernel<DT>, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D, a.X, a.ldx,
+                     pos, count, static_cast<const float*>(nullptr), xp,
+                     static_cast<void*>(nullptr), dp);
+  st = launched();
+  if (st != SGEMM_OK) return st;
+  for (long long v0 = 0; v0 < a.V; v0 += cols) {
+    const int n = (int)(a.V - v0 < cols ? a.V - v0 : cols);
+    const void* w = rows_from(a.W, (size_t)v0, a.ldw, 2);
+    const bool big = big_tiles(a.T, n, h->cus);
+    st = big ? logits_piece<L256x256, DT>(a, n, xp, dp, w, count, label, (int)v0, part, Tp, zlabel, s)
+             : logits_piece<L128x128, DT>(a, n, xp, dp, w, count, label, (int)v0, part, Tp, zlabel, s);
+    if (st != SGEMM_OK) return st;
+    const int chunks = (int)up_div(n, big ? L256x256::WN : L128x128::WN);
+    hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)up_div(a.T, CE_JOIN_ROWS)),
+                       dim3(CE_JOIN_ROWS * CE_JOIN_LANES), 0, s, part, chunks, Tp, count, order,
+                       label, state, zlabel, v0 == 0, v0 + n == a.V, loss, lse);
+    st = launched();
+    if (st != SGEMM_OK) return st;
+  }
+  return SGEMM_OK;
+}
+
+template <class T, int DT>
+int dz_piece(const CeProblem& a, int n, const void* xp, int dp, const void* w, const int* count,
+             const CeRowInfo* info, int v0, uint16_t* dz, int lddz, hipStream_t s) {
+  const CePiece p = piece_of<T>(a, a.T, n, a.D, a.alpha * CE_LOG2E, xp, dp, w, a.ldw, count);
+  return n % T::BN == 0 && a.D % kStep == 0
+             ? launch_dz<T, DT, MODE_ALIGNED>(p, info, v0, dz, lddz, s)
+             : launch_dz<T, DT, MODE_PADDED>(p, info, v0, dz, lddz, s);
+}
+
+template <class T, int DT>
+int dx_piece(const CeProblem& a, int n, const uint16_t* dz, int lddz, const void* w,
+             const int* count, int splits, int kps, const void* w_tail, float* sums, size_t slab,
+             float beta, hipStream_t s) {
+  CePiece p = piece_of<T>(a, a.T, a.D, n, 0.0f, dz, lddz, w, a.ldw, count);
+  p.gemm.g.beta = beta;
+  p.gemm.g.ldc = a.D;
+  return a.D % T::BN == 0 && n % kStep == 0
+             ? launch_dx<T, DT, MODE_ALIGNED>(p, splits, kps, nullptr, sums, slab, s)
+             : launch_dx<T, DT, MODE_PADDED>(p, splits, kps, n % kStep != 0 ? w_tail : nullptr, sums,
+                                             slab, s);
+}
+
+template <int DT>
+int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
+                    const float* lse, const float* dloss, const float* dlse, void* dX, int lddx,
+                    void* dW, int lddw, hipStream_t s) {
+  constexpr bool SCALED = DT == SGEMM_DTYPE_F16;
+  const int Tp = (int)padded_rows(a), dp = (int)padded_cols(a);
+  CeLayout l = packed_layout(a, 1);
+  const size_t slab = (size_t)a.T * a.D;
+  const size_t least = l.fixed + l.per_col * kPadCols;
+  if (h->workspace_bytes < least) return SGEMM_ERR_SCRATCH;
+  // half of what is left over the least may go to slabs of dX's sums
+  const bool bigx = dx_big(a);
+  int slabs = bigx ? dx_slabs(a, h->cus, 256, 256) : dx_slabs(a, h->cus, 128, 128);
+  const size_t spare = (h->workspace_bytes - least) / 2 / (4 * slab);
+  if (slabs > 1 && (size_t)(slabs - 1) > spare) slabs = 1 + (int)spare;
+  l.fixed += 4 * slab * (slabs - 1);
+  const long long cols = packed_columns(a, l, h->workspace_bytes);
+  if (cols == 0) return SGEMM_ERR_SCRATCH;
+  const int lddz = (int)cols;
+
+  Carver c = {static_cast<char*>(h->workspace)};
+  int* count = c.take<int>(4);
+  float* dw_factor = c.take<float>(4);
+  int* pos = c.take<int>(4 * (size_t)a.T);
+  CeRowInfo* info = c.take<CeRowInfo>(sizeof(CeRowInfo) * (size_t)Tp);
+  float* x_factor = c.take<float>(4 * (size_t)Tp);
+  float* out_factor = c.take<float>(4 * (size_t)Tp);
+  void* xp = c.take<char>(2 * (size_t)Tp * dp);
+  // (bfloat16 rows need no scaling: one copy serves both products)
+  void* xs = SCALED ? c.take<char>(2 * (size_t)Tp * dp) : xp;
+  void* w_tail = c.take<char>(2 * (size_t)kStep * a.ldw);
+  float* sums = c.take<float>(4 * slab * slabs);
+  uint16_t* dz = c.take<uint16_t>(0);
+
+  hipLaunchKernelGGL(ce_pack_factors_kernel<SCALED>, dim3(1), dim3(CE_PACK_THREADS), 0, s, a.T, Tp,
+                     a.alpha, labels, lse, dloss, dlse, pos, info, x_factor, out_factor, dw_factor,
+                     count);
+  int st = launched();
+  if (st != SGEMM_OK) return st;
+  unsigned g = grid_of((unsigned long long)(a.T + CE_ROW_PAD) * (unsigned)(dp / 8));
+  if (g == 0) return SGEMM_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL(ce_gather_kernel<DT>, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D, a.X, a.ldx,
+                     pos, count, x_factor, xp, SCALED ? xs : nullptr, dp);
+  st = launched();
+  if (st != SGEMM_OK) return st;
+  if (dX != nullptr && a.V % kStep != 0) {
+    const int rows = a.V % kStep;
+    hipLaunchKernelGGL(ce_tail_kernel<DT>, dim3(grid_of((unsigned long long)kStep * (a.D / 8))),
+                       dim3(CE_THREADS), 0, s, rows, a.D,
+                       rows_from(a.W, (size_t)(a.V - rows), a.ldw, 2), w_tail, a.ldw);
+    st = launched();
+    if (st != SGEMM_OK) return st;
+  }
+  for (long long v0 = 0; v0 < a.V; v0 += cols) {
+    const int n = (int)(a.V - v0 < cols ? a.V - v0 : cols);
+    const void* w = rows_from(a.W, (size_t)v0, a.ldw, 2);
+    st = big_tiles(a.T, n, h->cus)
+             ? dz_piece<L256x256, DT>(a, n, xp, dp, w, count, info, (int)v0, dz, lddz, s)
+             : dz_piece<L128x128, DT>(a, n, xp, dp, w, count, info, (int)v0, dz, lddz, s);
+    if (st != SGEMM_OK) return st;
+    if (dX != nullptr) {
+      // the first piece sets every slab, so a later one uses no more
+      int splits = slabs;
+      if (splits > 1 && splits > n / kSplitCols) splits = n / kSplitCols > 1 ? n / kSplitCols : 1;
+      const int kps = (int)round_up(up_div(n, splits), kStep);
+      splits = (int)up_div(n, kps);
+      if (v0 == 0) slabs = splits;
+      const float beta = v0 == 0 ? 0.0f : 1.0f;
+      st = bigx ? dx_piece<L256x256, DT>(a, n, dz, lddz, w, count, splits, kps, w_tail, sums, slab,
+                                         beta, s)
+                : dx_piece<L128x128, DT>(a, n, dz, lddz, w, count, splits, kps, w_tail, sums, slab,
+                                         beta, s);
+      if (st != SGEMM_OK) return st;
+    }
+    if (dW != nullptr) {
+      void* out = rows_from(dW, (size_t)v0, lddw, 2);
+      st = big_tiles(n, a.D, h->cus)
+               ? launch_dw<L256x256, DT>(
+                     piece_of<L256x256>(a, n, a.D, Tp, 0.0f, dz, lddz, xs, dp, count), dw_factor,
+                     out, lddw, s)
+               : launch_dw<L128x128, DT>(
+                     piece_of<L128x128>(a, n, a.D, Tp, 0.0f, dz, lddz, xs, dp, count), dw_factor,
+                     out, lddw, s);
+      if (st != SGEMM_OK) return st;
+    }
+  }
+  if (dX == nullptr) return SGEMM_OK;
+  g = grid_of((unsigned long long)a.T * (unsigned)(a.D / 8));
+  if (g == 0) return SGEMM_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL(ce_dx_rows_kernel<DT>, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D, pos, sums,
+                     a.D, slab, slabs, out_factor, dX, lddx);
+  return launched();
+}
+
+// ---- calls over the library's products (32-bit X and W, odd sizes) -----------------
+
 int forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels, float* loss,
             float* lse, hipStream_t s) {
+  if (packed(a, 0))
+    return a.dtype == SGEMM_DTYPE_BF16
+               ? packed_forward<SGEMM_DTYPE_BF16>(h, a, labels, loss, lse, s)
+               : packed_forward<SGEMM_DTYPE_F16>(h, a, labels, loss, lse, s);
   const CeLayout l = layout_of(a, 0);
   const int cols = piece_columns(a, l, h->workspace_bytes);
   if (cols == 0) return SGEMM_ERR_SCRATCH;
@@ -170,6 +510,9 @@ int backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels
              void* dW, int lddw, hipStream_t s) {
   constexpr bool WIDE = DT == SGEMM_DTYPE_F32;  // 32-bit gradients are their own sums
   constexpr unsigned esz = WIDE ? 4 : 2;
+  if constexpr (!WIDE)
+    if (packed(a, 1))
+      return packed_backward<DT>(h, a, labels, lse, dloss, dlse, dX, lddx, dW, lddw, s);
   const CeLayout l = layout_of(a, 1);
   const int cols = piece_columns(a, l, h->workspace_bytes);
   if (cols == 0) return SGEMM_ERR_SCRATCH;
@@ -257,11 +600,9 @@ int sgemm_ce_workspace_size(sgemm_handle_t h, int dtype, int T, int V, int D, in
   const CeProblem a = {dtype, T, V, D, 1.0f, nullptr, D, nullptr, D};
   if (tensor_elem_bytes(dtype) == 0) return SGEMM_ERR_VALUE;
   if (T < 0 || V < 1 || D < 1 || D > INT_MAX - 8 || V > INT_MAX - 8) return SGEMM_ERR_SIZE;
-  const CeLayout l = layout_of(a, backward);
-  const int small = V < kPieceStep ? V : kPieceStep;
-  const int big = piece_columns(a, l, (size_t)1 << 62);
-  if (least != nullptr) *least = l.fixed + l.per_col * (size_t)(small + 8);
-  if (full != nullptr) *full = l.fixed + l.per_col * (size_t)(big + 8) + kProductBytes;
+  const CeSizes z = sizes_of(a, backward, h->cus);
+  if (least != nullptr) *least = z.least;
+  if (full != nullptr) *full = z.full;
   return SGEMM_OK;
 }
 
@@ -288,6 +629,7 @@ int sgemm_ce_forward(sgemm_handle_t h, int dtype, int T, int V, int D, float alp
   if (st != SGEMM_OK) return st;
   const CeProblem a = {dtype, T, V, D, alpha, X, ldx, W, ldw};
   const CeLabels y = {labels, ignore, V};
+  if (h->workspace_bytes < sizes_of(a, 0, h->cus).least) return SGEMM_ERR_SCRATCH;
   return forward(h, a, y, loss, lse, stream);
 }
 
@@ -323,6 +665,7 @@ int sgemm_ce_backward(sgemm_handle_t h, int dtype, int T, int V, int D, float al
   if (st != SGEMM_OK) return st;
   const CeProblem a = {dtype, T, V, D, alpha, X, ldx, W, ldw};
   const CeLabels y = {labels, ignore, V};
+  if (T > 0 && h->workspace_bytes < sizes_of(a, 1, h->cus).least) return SGEMM_ERR_SCRATCH;
   switch (dtype) {
     case SGEMM_DTYPE_F32:
       if (T == 0) return zero<SGEMM_DTYPE_F32>(V, D, dW, lddw, stream);

@@ -272,4 +272,269 @@ __global__ void __launch_bounds__(CE_THREADS) ce_zero_kernel(int rows, int D, vo
   store8<DT>(static_cast<E*>(out) + (size_t)r * ldo + c, D - (int)c, v);
 }
 
+// ---- packed rows (16-bit X and W) ------------------------------------------------
+
+// What a packed row's product epilogues need: the factors of dz, lse * log2(e)
+// and the label (CE_IGNORED for padding rows, whose factors are 0).
+struct CeRowInfo {
+  float p, q, lse2;
+  int label;
+};
+
+// Packs the rows that count (label other than `ignore`), in order: pos[t] is
+// row t's packed row or -1, order its reverse, `label` the packed rows' labels
+// (CE_IGNORED from *count to `padded`).  One workgroup; a step of the loop
+// takes a row a lane.
+constexpr int CE_PACK_THREADS = 1024;
+constexpr int CE_PACK_WAVES = CE_PACK_THREADS / 64;
+
+// The packed place of this lane's row, and the total so far in `base`.
+__device__ __forceinline__ int ce_place(bool counts, int& base, int* wave_sum) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const unsigned long long mask = __ballot(counts);
+  const int before = __popcll(mask & ((1ull << lane) - 1ull));
+  __syncthreads();  // (the last step's sums have been read)
+  if (lane == 0) wave_sum[wave] = __popcll(mask);
+  __syncthreads();
+  int at = base + before;
+#pragma unroll
+  for (int w = 0; w < CE_PACK_WAVES; ++w) {
+    const int n = wave_sum[w];
+    if (w < wave) at += n;
+    base += n;
+  }
+  return counts ? at : -1;
+}
+
+// Forward: loss and lse of the rows left out are set to 0 here.
+static __global__ void __launch_bounds__(CE_PACK_THREADS)
+    ce_pack_kernel(int T, int padded, CeLabels labels, int* __restrict__ pos,
+                   int* __restrict__ order, int* __restrict__ label, int* __restrict__ count,
+                   float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ int wave_sum[CE_PACK_WAVES];
+  int base = 0;
+  for (int t0 = 0; t0 < T; t0 += CE_PACK_THREADS) {
+    const int t = t0 + threadIdx.x;
+    const int y = t < T ? ce_label(labels, t) : CE_IGNORED;
+    const int at = ce_place(y != CE_IGNORED, base, wave_sum);
+    if (t < T) {
+      pos[t] = at;
+      if (at >= 0) {
+        order[at] = t;
+        label[at] = y;
+      } else {
+        loss[t] = 0.0f;
+        lse[t] = 0.0f;
+      }
+    }
+  }
+  for (int r = base + threadIdx.x; r < padded; r += CE_PACK_THREADS) label[r] = CE_IGNORED;
+  if (threadIdx.x == 0) *count = base;
+}
+
+// Backward: the packed rows' factors (see ce_factors_kernel for SCALED) as
+// info, the factors of X's rows and of dX's.
+template <bool SCALED>
+__global__ void __launch_bounds__(CE_PACK_THREADS)
+    ce_pack_factors_kernel(int T, int padded, float alpha, CeLabels labels,
+                           const float* __restrict__ lse, const float* __restrict__ dloss,
+                           const float* __restrict__ dlse, int* __restrict__ pos,
+                           CeRowInfo* __restrict__ info, float* __restrict__ x_factor,
+                           float* __restrict__ out_factor, float* __restrict__ dw_factor,
+                           int* __restrict__ count) {
+  __shared__ int wave_sum[CE_PACK_WAVES];
+  __shared__ int top[CE_PACK_WAVES];
+  constexpr int NONE = -1000;
+  auto grads = [&](int t, int y, float& p, float& q) {
+    q = y == CE_IGNORED ? 0.0f : y == CE_BAD ? NAN : dloss[t];
+    p = y == CE_IGNORED ? 0.0f : dlse != nullptr ? q + dlse[t] : q;
+  };
+  auto exponent = [&](float p, float q) {
+    const float r = fmaxf(fabsf(p), fabsf(q));
+    return r > 0.0f && r < INFINITY ? ilogbf(r) : NONE;
+  };
+  int kmax = NONE;
+  if (SCALED) {
+    for (int t = threadIdx.x; t < T; t += CE_PACK_THREADS) {
+      float p, q;
+      grads(t, ce_label(labels, t), p, q);
+      kmax = max(kmax, exponent(p, q));
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) kmax = max(kmax, __shfl_xor(kmax, d));
+    if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = kmax;
+    __syncthreads();
+    for (int w = 0; w < CE_PACK_WAVES; ++w) kmax = max(kmax, top[w]);
+    if (kmax == NONE) kmax = 13;
+  }
+  int base = 0;
+  for (int t0 = 0; t0 < T; t0 += CE_PACK_THREADS) {
+    const int t = t0 + threadIdx.x;
+    const int y = t < T ? ce_label(labels, t) : CE_IGNORED;
+    CeRowInfo f = {0.0f, 0.0f, 0.0f, y};
+    if (t < T) grads(t, y, f.p, f.q);
+    // a row whose gradients are both 0 adds nothing to dX or dW either
+    const int at = ce_place(!(f.p == 0.0f && f.q == 0.0f), base, wave_sum);
+    if (t < T) pos[t] = at;
+    if (at >= 0) {
+      float x = 1.0f, out = alpha;
+      if (SCALED) {
+        const int k = exponent(f.p, f.q);
+        if (k != NONE) {
+          f.p = ldexpf(f.p, 13 - k);
+          f.q = ldexpf(f.q, 13 - k);
+          x = ldexpf(1.0f, k - kmax);
+          out = ldexpf(alpha, k - 13);
+        }
+      }
+      f.lse2 = lse[t] * CE_LOG2E;
+      info[at] = f;
+      x_factor[at] = x;
+      out_factor[at] = out;
+    }
+  }
+  for (int r = base + threadIdx.x; r < padded; r += CE_PACK_THREADS)
+    info[r] = CeRowInfo{0.0f, 0.0f, 0.0f, CE_IGNORED};
+  if (threadIdx.x == 0) {
+    *count = base;
+    *dw_factor = SCALED ? ldexpf(alpha, kmax - 13) : alpha;
+  }
+}
+
+// Row t of X to packed row pos[t] (times x_factor where given, to `scaled`;
+// as it is to `plain`; either may be null), zeros in the columns from D to the
+// stride; and zero rows from *count to the end of its tile of CE_ROW_PAD rows.
+// Blocks of T + CE_ROW_PAD rows.
+constexpr int CE_ROW_PAD = 256;
+template <int DT>
+__global__ void __launch_bounds__(CE_THREADS)
+    ce_gather_kernel(int T, int D, const void* X, int ldx, const int* __restrict__ pos,
+                     const int* __restrict__ count, const float* __restrict__ x_factor,
+                     void* plain, void* scaled, int ld) {
+  typedef typename TensorElem<DT>::type E;
+  const unsigned units = (unsigned)ld / 8u;
+  const unsigned long long at = (unsigned long long)blockIdx.x * CE_THREADS + threadIdx.x;
+  const long long t = (long long)(at / units);
+  const int c = 8 * (int)(at % units);
+  float v[8];
+  long long r;
+  if (t < T) {
+    r = pos[t];
+    if (r < 0) return;
+    load8<DT>(static_cast<const E*>(X) + (size_t)t * ldx + c, D - c, v);
+  } else {
+    const int n = *count, end = ((n > 1 ? n : 1) + CE_ROW_PAD - 1) / CE_ROW_PAD * CE_ROW_PAD;
+    r = n + (t - T);
+    if (r >= end) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  }
+  if (plain != nullptr) store8<DT>(static_cast<E*>(plain) + (size_t)r * ld + c, 8, v);
+  if (scaled != nullptr) {
+    const float f = t < T ? x_factor[r] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= f;
+    store8<DT>(static_cast<E*>(scaled) + (size_t)r * ld + c, 8, v);
+  }
+}
+
+// The last `rows` (under 64) rows of W as 64 rows, the others zeros: the last
+// K step of dX's product, in W's stride.
+template <int DT>
+__global__ void __launch_bounds__(CE_THREADS)
+    ce_tail_kernel(int rows, int D, const void* W, void* copy, int ld) {
+  typedef typename TensorElem<DT>::type E;
+  const unsigned units = (unsigned)D / 8u;
+  const unsigned at = blockIdx.x * CE_THREADS + threadIdx.x;
+  const unsigned r = at / units, c = 8u * (at % units);
+  if (r >= 64u) return;
+  float v[8];
+  load8<DT>(static_cast<const E*>(W) + (r < (unsigned)rows ? (size_t)r * ld + c : (size_t)0),
+            r < (unsigned)rows ? 8 : 0, v);
+  store8<DT>(static_cast<E*>(copy) + (size_t)r * ld + c, 8, v);
+}
+
+// As ce_join, with m in units of log2.
+__device__ __forceinline__ CeRow ce_join2(CeRow a, CeRow b) {
+  const float m = fmaxf(a.m, b.m);
+  if (m == -INFINITY) return CeRow{m, a.l + b.l};
+  return CeRow{m, a.l * __builtin_amdgcn_exp2f(a.m - m) + b.l * __builtin_amdgcn_exp2f(b.m - m)};
+}
+
+// Joins a piece's parts (part[chunk][row], rows of the stride `padded`) into
+// the packed rows' state; the last piece writes the rows' loss and lse.  A
+// workgroup takes 32 rows, 32 lanes a row stride over its chunks.
+constexpr int CE_JOIN_ROWS = 32, CE_JOIN_LANES = 32;
+static __global__ void __launch_bounds__(CE_JOIN_ROWS * CE_JOIN_LANES)
+    ce_join_kernel(const CeRow* __restrict__ part, int chunks, int padded,
+                   const int* __restrict__ count, const int* __restrict__ order,
+                   const int* __restrict__ label, CeRow* __restrict__ state,
+                   const float* __restrict__ zlabel, int first, int last, float* __restrict__ loss,
+                   float* __restrict__ lse) {
+  __shared__ CeRow sh[CE_JOIN_LANES * CE_JOIN_ROWS];
+  const int n = *count;
+  const int row0 = blockIdx.x * CE_JOIN_ROWS;
+  if (row0 >= n) return;
+  const int lr = threadIdx.x % CE_JOIN_ROWS, lane = threadIdx.x / CE_JOIN_ROWS;
+  const int row = row0 + lr;
+  CeRow r = {-INFINITY, 0.0f};
+  int k = lane;
+  for (; k + 3 * CE_JOIN_LANES < chunks; k += 4 * CE_JOIN_LANES) {
+    CeRow x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = part[(size_t)(k + i * CE_JOIN_LANES) * padded + row];
+    r = ce_join2(r, ce_join2(ce_join2(x[0], x[1]), ce_join2(x[2], x[3])));
+  }
+  for (; k < chunks; k += CE_JOIN_LANES) r = ce_join2(r, part[(size_t)k * padded + row]);
+  sh[threadIdx.x] = r;
+  __syncthreads();
+  for (int d = CE_JOIN_LANES / 2; d > 0; d >>= 1) {
+    if (lane < d) sh[threadIdx.x] = ce_join2(sh[threadIdx.x], sh[threadIdx.x + d * CE_JOIN_ROWS]);
+    __syncthreads();
+  }
+  if (lane != 0 || row >= n) return;
+  r = sh[threadIdx.x];
+  if (!first) r = ce_join2(state[row], r);
+  if (!last) {
+    state[row] = r;
+    return;
+  }
+  const int t = order[row], y = label[row];
+  const float e = (r.m + log2f(r.l)) * 0.693147180559945309417f;
+  lse[t] = e;
+  loss[t] = y == CE_BAD ? NAN : e - zlabel[row];
+}
+
+// dX's rows: the slabs' sums of the row's packed row in slab order, times its
+// factor; zeros for rows that have none.  Eight columns a lane.
+template <int DT>
+__global__ void __launch_bounds__(CE_THREADS)
+    ce_dx_rows_kernel(int T, int D, const int* __restrict__ pos, const float* __restrict__ sums,
+                      int lds, size_t slab, int slabs, const float* __restrict__ out_factor,
+                      void* dX, int lddx) {
+  typedef typename TensorElem<DT>::type E;
+  const unsigned units = (unsigned)D / 8u;
+  const unsigned long long at = (unsigned long long)blockIdx.x * CE_THREADS + threadIdx.x;
+  const long long t = (long long)(at / units);
+  const int c = 8 * (int)(at % units);
+  if (t >= T) return;
+  const int r = pos[t];
+  float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (r >= 0) {
+    const float* p = sums + (size_t)r * lds + c;
+    for (int s = 0; s < slabs; ++s, p += slab) {
+      const v4u a = *reinterpret_cast<const v4u*>(p), b = *reinterpret_cast<const v4u*>(p + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] += __uint_as_float(a[i]);
+        v[4 + i] += __uint_as_float(b[i]);
+      }
+    }
+    const float f = out_factor[r];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= f;
+  }
+  store8<DT>(static_cast<E*>(dX) + (size_t)t * lddx + c, 8, v);
+}
+
 }  // namespace sgemm

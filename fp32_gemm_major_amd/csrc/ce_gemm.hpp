@@ -1,0 +1,277 @@
+// The products of the output layer's loss for 16-bit X and W, each with the
+// work around it folded in (see ce.hpp for the formulas):
+//
+//   ce_logits_kernel   z = X W^T, a tile's rows reduced at once to (max, sum
+//                      of exp); z itself never leaves the registers
+//   ce_dz_gemm_kernel  z again, turned into dz in the registers and stored in
+//                      16 bits for the two products that follow
+//   ce_dx_kernel       dz W, split over the vocabulary where rows and columns
+//                      alone do not fill the device, sums kept in 32 bits
+//   ce_dw_kernel       dz^T X, stored in 16 bits
+//
+// All run the 16-bit products' schedule (lowp_gemm.hpp, padded and aligned
+// modes) on operands laid out for it: the rows of X that count, packed
+// together and padded with zeros to whole tiles (`count` rows; left-out rows
+// cost nothing), and dz in pieces of whole tiles of columns.  Only the device
+// knows `count`; tiles past it end at once, and dW's sums run over no more
+// rows than that.
+//
+// In a result block, register 4q + e of lane (li, lh) is row li, column
+// 8q + 4lh + e.
+#pragma once
+
+#include "ce.hpp"
+#include "lowp_gemm.hpp"
+
+namespace sgemm {
+
+struct CeGemm {
+  LpArgs g;          // A: packed rows, B: W's piece; M, N, K of the product
+  float c;           // alpha * log2(e) (logits), or alpha
+  const int* count;  // rows that count
+};
+
+// Rows of A a kernel works on: those that count, one tile at least.
+template <class T>
+__device__ __forceinline__ bool ce_tile_idle(const int* count, int m0) {
+  const int n = *count;
+  return m0 >= (n > 1 ? n : 1);
+}
+
+// ---- logits to (max, sum) ------------------------------------------------------
+
+// part[chunk][row]: chunk = the wave's columns (T::WN of them), rows padded.
+template <class T, int DT, int MODE>
+__global__ void __launch_bounds__(T::THREADS, T::OCC)
+    ce_logits_kernel(CeGemm a, int tiles_m, int tiles_n, int band, const int* __restrict__ label,
+                     int v0, CeRow* __restrict__ part, int rows, float* __restrict__ zlabel) {
+  __shared__ __attribute__((aligned(1024))) char lds[T::LDS_ALIGNED];
+  int tm, tn;
+  tile_coords(blockIdx.x, gridDim.x, tiles_m, tiles_n, band, tm, tn);
+  const int m0 = tm * T::BM, n0 = tn * T::BN;
+  if (ce_tile_idle<T>(a.count, m0)) return;
+  f32x16 acc[T::FM][T::FN];
+  zero_acc<T>(acc);
+  lp_tile_accumulate<T, DT, MODE, false, true>(a.g, lds, m0, n0, acc);
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // the loop's look-ahead loads
+  const WaveCoords<T> w;
+  const int col0 = n0 + w.wn * T::WN;  // the wave's first column
+  const int have = a.g.N - col0;
+  if (have <= 0) return;
+  const float c = a.c, alpha = a.g.alpha;
+#pragma unroll
+  for (int i = 0; i < T::FM; ++i) {
+    const int row = m0 + w.wm * T::WM + 32 * i + w.li;
+    const int y = label[row] - v0 - col0;
+    // the label's logit, in the one tile that holds it
+    if (__any(y >= 0 && y < T::WN && y < have)) {
+      float z = 0.0f;
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (y == 32 * j + 8 * (k / 4) + 4 * w.lh + k % 4) z = acc[i][j][k];
+      if (y >= 0 && y < T::WN && y < have && ((y >> 2) & 1) == w.lh) zlabel[row] = alpha * z;
+    }
+    // t = z * log2(e): m = max t, l = sum 2^(t - m).  The difference is one
+    // fused multiply-add, so only m's own rounding enters lse.
+    float m = -INFINITY, l = 0.0f;
+    if (have >= T::WN) {
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) m = fmaxf(m, c * acc[i][j][k]);
+      m = fmaxf(m, __shfl_xor(m, 32));
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          l += __builtin_amdgcn_exp2f(fmaf(c, acc[i][j][k], -m));
+    } else {
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (32 * j + 8 * (k / 4) + 4 * w.lh + k % 4 < have) m = fmaxf(m, c * acc[i][j][k]);
+      m = fmaxf(m, __shfl_xor(m, 32));
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (32 * j + 8 * (k / 4) + 4 * w.lh + k % 4 < have)
+            l += __builtin_amdgcn_exp2f(fmaf(c, acc[i][j][k], -m));
+    }
+    l += __shfl_xor(l, 32);
+    if (w.lh == 0) part[(size_t)(col0 / T::WN) * rows + row] = CeRow{m, l};
+  }
+}
+
+// ---- logits to dz ------------------------------------------------------------------
+
+// dz (16-bit, rows of lddz elements) is written for whole tiles: zeros in
+// columns past N and in rows that count for nothing.
+template <class T, int DT, int MODE>
+__global__ void __launch_bounds__(T::THREADS, T::OCC)
+    ce_dz_gemm_kernel(CeGemm a, int tiles_m, int tiles_n, int band,
+                      const CeRowInfo* __restrict__ info, int v0, uint16_t* __restrict__ dz,
+                      int lddz) {
+  constexpr int ODT = DT == LP_BF16 ? SGEMM_DTYPE_BF16 : SGEMM_DTYPE_F16;
+  constexpr int LD = T::WN + 4, LPR = T::WN / 8, RPI = 64 / LPR, NI = 32 / RPI;
+  static_assert(T::WAVES * 32 * LD * 4 <= T::LDS_BYTES, "staging area");
+  __shared__ __attribute__((aligned(1024))) char lds[T::LDS_ALIGNED];
+  int tm, tn;
+  tile_coords(blockIdx.x, gridDim.x, tiles_m, tiles_n, band, tm, tn);
+  const int m0 = tm * T::BM, n0 = tn * T::BN;
+  if (ce_tile_idle<T>(a.count, m0)) return;
+  f32x16 acc[T::FM][T::FN];
+  zero_acc<T>(acc);
+  lp_tile_accumulate<T, DT, MODE, false, true>(a.g, lds, m0, n0, acc);
+  const WaveCoords<T> w;
+  const int col0 = n0 + w.wn * T::WN;
+  const int have = a.g.N - col0;
+  const float c = a.c;
+  float* reg = reinterpret_cast<float*>(lds) + w.wave * 32 * LD;
+  const int rr = w.lane / LPR, cc = 8 * (w.lane % LPR);
+  __syncthreads();  // every wave is done reading the stages
+#pragma unroll
+  for (int i = 0; i < T::FM; ++i) {
+    const int row = m0 + w.wm * T::WM + 32 * i;
+    const CeRowInfo f = info[row + w.li];
+    const bool counts = !(f.p == 0.0f && f.q == 0.0f);
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float p = f.p * __builtin_amdgcn_exp2f(fmaf(c, acc[i][j][k], -f.lse2));
+        acc[i][j][k] = counts ? p : 0.0f;
+      }
+    const int y = f.label - v0 - col0;
+    if (__any(y >= 0 && y < T::WN)) {
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (y == 32 * j + 8 * (k / 4) + 4 * w.lh + k % 4) acc[i][j][k] -= f.q;
+    }
+    if (have < T::WN) {
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (32 * j + 8 * (k / 4) + 4 * w.lh + k % 4 >= have) acc[i][j][k] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4*>(reg + w.li * LD + 32 * j + 8 * q + 4 * w.lh) =
+            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                  acc[i][j][4 * q + 3]};
+    __builtin_amdgcn_wave_barrier();  // (a wave's LDS operations complete in order)
+    uint16_t* out = dz + (size_t)(row + rr) * lddz + col0 + cc;
+    const float* src = reg + rr * LD + cc;
+#pragma unroll
+    for (int t = 0; t < NI; ++t, out += (size_t)RPI * lddz, src += RPI * LD) {
+      v4u o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        o[e] = (unsigned)elem_bits<ODT>(src[2 * e]) | ((unsigned)elem_bits<ODT>(src[2 * e + 1]) << 16);
+      *reinterpret_cast<v4u*>(out) = o;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_wave_barrier();
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // the loop's look-ahead loads
+}
+
+// ---- the gradients' products -----------------------------------------------------
+
+// sums[s][row][d] (+)= dz W over the piece's columns [s * kps, ...): workgroup
+// b takes tile b % tiles of split b / tiles.
+template <class T, int DT, int MODE>
+__global__ void __launch_bounds__(T::THREADS, T::OCC)
+    ce_dx_kernel(CeGemm a, int tiles_m, int tiles_n, int band, int kps,
+                 const void* __restrict__ w_tail, float* __restrict__ sums, size_t slab) {
+  __shared__ __attribute__((aligned(1024))) char lds[T::LDS_ALIGNED];
+  const int tiles = tiles_m * tiles_n;
+  const int split = blockIdx.x / tiles, tile = blockIdx.x - split * tiles;
+  int tm, tn;
+  tile_coords(tile, tiles, tiles_m, tiles_n, band, tm, tn);
+  const int m0 = tm * T::BM, n0 = tn * T::BN;
+  if (ce_tile_idle<T>(a.count, m0)) return;
+  LpArgs g = a.g;
+  const int k0 = split * kps;
+  g.K = a.g.K - k0 < kps ? a.g.K - k0 : kps;
+  g.A = static_cast<const uint16_t*>(a.g.A) + k0;
+  g.B = static_cast<const uint16_t*>(a.g.B) + (size_t)k0 * a.g.ldb;
+  g.C = sums + split * slab;
+  f32x16 acc[T::FM][T::FN];
+  zero_acc<T>(acc);
+  lp_tile_accumulate<T, DT, MODE, false, false>(g, lds, m0, n0, acc,
+                                                k0 + g.K == a.g.K ? w_tail : nullptr);
+  GemmArgs e = {};
+  e.M = g.M;
+  e.N = g.N;
+  e.K = g.K;
+  e.alpha = 1.0f;
+  e.beta = g.beta;
+  e.C = g.C;
+  e.ldc = g.ldc;
+  lp_store_tile_lds<T>(e, m0, n0, acc, lds);
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+}
+
+// dW's rows [0, N of W's piece) = factor * dz^T X: the sums run over the rows
+// that count, to whole K steps (the rows between hold zeros).
+template <class T, int DT>
+__global__ void __launch_bounds__(T::THREADS, T::OCC)
+    ce_dw_kernel(CeGemm a, int tiles_m, int tiles_n, int band, const float* __restrict__ factor,
+                 void* __restrict__ out, int ldo) {
+  constexpr int ODT = DT == LP_BF16 ? SGEMM_DTYPE_BF16 : SGEMM_DTYPE_F16;
+  constexpr int LD = T::WN + 4, LPR = T::WN / 8, RPI = 64 / LPR, NI = 32 / RPI;
+  __shared__ __attribute__((aligned(1024))) char lds[T::LDS_ALIGNED];
+  int tm, tn;
+  tile_coords(blockIdx.x, gridDim.x, tiles_m, tiles_n, band, tm, tn);
+  const int m0 = tm * T::BM, n0 = tn * T::BN;
+  LpArgs g = a.g;
+  const int n = *a.count;
+  g.K = ((n > 1 ? n : 1) + 63) & ~63;
+  f32x16 acc[T::FM][T::FN];
+  zero_acc<T>(acc);
+  lp_tile_accumulate<T, DT, MODE_ALIGNED, true, false>(g, lds, m0, n0, acc);
+  const WaveCoords<T> w;
+  float* reg = reinterpret_cast<float*>(lds) + w.wave * 32 * LD;
+  const int rr = w.lane / LPR, cc = 8 * (w.lane % LPR);
+  const int col = n0 + w.wn * T::WN + cc, have = g.N - col;
+  const float f = *factor;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < T::FM; ++i) {
+    const int row0 = m0 + w.wm * T::WM + 32 * i + rr;
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4*>(reg + w.li * LD + 32 * j + 8 * q + 4 * w.lh) =
+            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                  acc[i][j][4 * q + 3]};
+    __builtin_amdgcn_wave_barrier();
+    const float* src = reg + rr * LD + cc;
+    uint16_t* p = static_cast<uint16_t*>(out) + (size_t)row0 * ldo + col;
+    // (D is a multiple of eight: a lane's run lies inside or outside)
+#pragma unroll
+    for (int t = 0; t < NI; ++t, p += (size_t)RPI * ldo, src += RPI * LD) {
+      v4u o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        o[e] = (unsigned)elem_bits<ODT>(f * src[2 * e]) |
+               ((unsigned)elem_bits<ODT>(f * src[2 * e + 1]) << 16);
+      if (have > 0 && row0 + t * RPI < g.M) *reinterpret_cast<v4u_any*>(p) = o;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_wave_barrier();
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+}
+
+}  // namespace sgemm

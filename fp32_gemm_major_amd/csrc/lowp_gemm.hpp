@@ -55,6 +55,13 @@
 //   pair-swapped, so one LDS write of 16 lanes covers all 16 bank groups (only
 //   the v_perm byte selector differs).  The edge kernels' register step uses
 //   the same loads.  Their stores are masked.
+// * Padded kernels (the output layer's loss; not in the product table) run
+//   the aligned schedule on an A whose rows and k are padded with zeros to
+//   whole tiles and steps, against a B of any sizes: rows and pieces past N
+//   are clamped as in edge kernels, a K-contiguous B's units past K move back
+//   to the row's last one (K a multiple of a unit), and an outer-contiguous
+//   B's last, partial step is read from a copy whose missing rows are zeros.
+//   What is read in place of a missing k meets A's zeros.
 // * Global loads of both kinds, direct-to-LDS ones included, take any byte
 //   address on gfx950 (checked with in-bounds probes at 1- and 2-byte
 //   offsets): no kernel needs aligned leading dimensions or base pointers.
@@ -264,17 +271,23 @@ __device__ __forceinline__ u32x4 lp_load_unit(const E* p, int n) {
   return out;
 }
 
+// Padded kernels' mode, beside MODE_ALIGNED, MODE_EDGE and MODE_GUARDED.
+constexpr int MODE_PADDED = 3;
+
 // Accumulate the output tile at (m0, n0) over all of K into acc (zeroed by
-// the caller).  TA: A stored K x M; TB: B stored N x K.
+// the caller).  TA: A stored K x M; TB: B stored N x K.  b_tail (padded mode,
+// outer-contiguous B): the last, partial K step's rows, in B's stride.
 template <class T, int DT, int MODE, bool TA, bool TB>
 __device__ __forceinline__ void lp_tile_accumulate(const LpArgs& g, char* lds,
                                                    int m0, int n0,
-                                                   f32x16 (&acc)[T::FM][T::FN]) {
+                                                   f32x16 (&acc)[T::FM][T::FN],
+                                                   const void* b_tail = nullptr) {
   typedef LpFmt<DT> F;
   typedef typename F::E E;
   constexpr int ESZ = F::ESZ, UE = F::UE, BKE = F::BKE, FU = F::FU, QG = F::QG;
   constexpr bool GUARD = MODE == MODE_GUARDED;
   constexpr bool EDGE = MODE == MODE_EDGE;
+  constexpr bool PAD = MODE == MODE_PADDED;
   constexpr bool A_KC = !TA;  // A stored K-contiguous
   constexpr bool B_KC = TB;   // B stored K-contiguous
   const int M = g.M, N = g.N, K = g.K;
@@ -343,17 +356,25 @@ __device__ __forceinline__ void lp_tile_accumulate(const LpArgs& g, char* lds,
     for (int v = 0; v < T::B_VEC; ++v) {
       if (B_KC) {
         int r = b_r[v];
-        if (EDGE && n0 + r >= N) r = N - 1 - n0;
+        if ((EDGE || PAD) && n0 + r >= N) r = N - 1 - n0;
         b_voff[v] = ESZ * ((unsigned)r * (unsigned)ldb + UE * (unsigned)b_c[v]);
       } else {
         const int u = (v * T::WAVES + wave) * 64 + lane;
         constexpr int UPR = T::BN * ESZ / 16;  // units per row of k
         const int k = u / UPR, c = (u % UPR) ^ lp_oc_unit_swz<ESZ, T::BN>(k);
         int o = UE * c;
-        if (EDGE && n0 + o >= N) o = N - UE > n0 ? N - UE - n0 : 0;
+        if ((EDGE || PAD) && n0 + o >= N) o = N - UE > n0 ? N - UE - n0 : 0;
         b_voff[v] = ESZ * ((unsigned)k * (unsigned)ldb + (unsigned)o);
       }
     }
+  }
+  // Padded mode, K-contiguous B: how far a lane's unit of the last step lies
+  // past the row's last one, in bytes.  (The unit is the same in all the
+  // lane's loads.)
+  unsigned b_back = 0;
+  if (PAD && B_KC) {
+    const int past = b_c[0] - ((K - 1) % BKE) / UE;
+    b_back = past > 0 ? 16u * (unsigned)past : 0u;
   }
   // Tile origins and the advance per K step of the direct loads.
   const E* a_dbase = A_KC ? A + (size_t)m0 * lda : A + m0;
@@ -460,7 +481,10 @@ __device__ __forceinline__ void lp_tile_accumulate(const LpArgs& g, char* lds,
             live ? lds_u + (unsigned)a_off(st) + 1024u * (unsigned)(d * T::WAVES + wave_u)
                  : lds_dummy);
     else
-      dma16(reinterpret_cast<const float*>(b_dbase + (size_t)kt * b_dstep), b_voff[d - ND_A],
+      dma16(reinterpret_cast<const float*>(PAD && !B_KC && b_tail != nullptr && kt == nk - 1
+                                               ? static_cast<const E*>(b_tail) + n0
+                                               : b_dbase + (size_t)kt * b_dstep),
+            b_voff[d - ND_A] - (PAD && B_KC && kt == nk - 1 ? b_back : 0u),
             live ? lds_u + (unsigned)b_off(st) +
                        1024u * (unsigned)((d - ND_A) * T::WAVES + wave_u)
                  : lds_dummy);

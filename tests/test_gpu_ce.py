@@ -125,7 +125,9 @@ class Problem:
 
 
 SIZES = [(1, 1, 1), (1, 5, 3), (2, 300, 7), (3, 100, 16), (16, 257, 64), (17, 1000, 33), (64, 512, 128),
-         (65, 2050, 100), (130, 5000, 257), (256, 1024, 256), (300, 777, 512), (513, 4099, 130)]
+         (65, 2050, 100), (130, 5000, 257), (256, 1024, 256), (300, 777, 512), (513, 4099, 130),
+         # packed rows: 128- and 256-square tiles, ragged and whole in every extent
+         (20, 4096, 72), (129, 2048, 320), (257, 6401, 392), (300, 33001, 264), (260, 65536, 64)]
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))
@@ -233,6 +235,38 @@ def test_no_rows(handle):
         handle.ce_forward(X, W, Y, f, f.clone())
         handle.ce_backward(X, W, Y, f, f, torch.empty_like(X), dW)
         assert (dW == 0).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("count", [0, 1, 127, 128, 255, 256, 257, 384, 512, 600])
+def test_rows_that_count_at_tile_edges(handle, count, dt):
+    p = Problem(600, 1300, 72, dt, seed=6, ignored=0.0)
+    p.labels[np.random.default_rng(count).permutation(600)[count:]] = ref.IGNORE
+    p.Y.copy_(torch.from_numpy(p.labels))
+    p.X[p.Y == ref.IGNORE] = float("nan")
+    p.forward(handle)
+    p.check_forward()
+    p.backward(handle)
+    p.check_backward()
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("T", [6, 200])
+def test_no_read_past_the_operands(handle, T, dt):
+    """X and W end where their buffers do not: NaNs stand behind the last
+    element of W's and X's rows and after the last row."""
+    V, D = 333, 40
+    p = Problem(T, V, D, dt, seed=7)
+    for name, rows in (("X", T), ("W", V)):
+        t = getattr(p, name)
+        buf = torch.full((rows * (D + 8) + 4096,), float("nan"), dtype=t.dtype, device="cuda")
+        view = buf[:rows * (D + 8)].view(rows, D + 8)[:, :D]
+        view.copy_(t)
+        setattr(p, name, view)
+    p.forward(handle)
+    p.check_forward()
+    p.backward(handle)
+    p.check_backward()
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))

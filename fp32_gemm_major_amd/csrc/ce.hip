@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <limits.h>
 
+#include <algorithm>
+
 #include "ce.hpp"
 #include "ce_gemm.hpp"
 #include "handle.hpp"
@@ -53,7 +55,6 @@ struct CeLayout {
 
 constexpr int kPadRows = CE_ROW_PAD, kPadCols = 256;  // whole tiles
 constexpr int kStep = 64;                             // k per step of the products
-constexpr int kSplitCols = 1024;                      // least columns of a split of dX's sums
 
 long long padded_rows(const CeProblem& a) { return round_up(a.T > 1 ? a.T : 1, kPadRows); }
 long long padded_cols(const CeProblem& a) { return round_up(a.D, kPadCols); }
@@ -98,13 +99,13 @@ long long packed_columns(const CeProblem& a, const CeLayout& l, size_t bytes) {
 }
 
 // Slabs of dX's sums: where its tiles are fewer than the CUs, the vocabulary
-// is split over workgroups.
-int dx_slabs(const CeProblem& a, int cus, int bm, int bn) {
-  const long long tiles = up_div(a.T, bm) * up_div(a.D, bn);
-  long long s = up_div(cus, tiles), most = a.V / kSplitCols;
-  if (s > most) s = most;
-  if (s > 64) s = 64;
-  return s < 1 ? 1 : (int)s;
+// is split over workgroups (ce_split).  Rows that are left out make fewer
+// tiles and more splits, up to twice as many as for all rows.
+int dx_slabs(const CeProblem& a, int cus, int b) {
+  const long long tiles = up_div(a.T, b) * up_div(a.D, b);
+  if (tiles > cus) return 1;
+  const int s = ce_split((int)tiles, cus, a.V, 64).splits;
+  return s < 32 ? 2 * s : 64;
 }
 // Tiles of dX's product: 256 square unless one extent fits half of one.
 bool dx_big(const CeProblem& a) { return a.T > 128 && a.D > 128; }
@@ -215,9 +216,7 @@ CeSizes sizes_of(const CeProblem& a, int backward, int cus) {
     l = packed_layout(a, backward);
     size_t least = l.fixed + l.per_col * kPadCols;
     if (least > z.least) z.least = least;
-    const int slabs = !backward    ? 1
-                      : dx_big(a) ? dx_slabs(a, cus, 256, 256)
-                                  : dx_slabs(a, cus, 128, 128);
+    const int slabs = backward ? dx_slabs(a, cus, dx_big(a) ? 256 : 128) : 1;
     const size_t more = 4 * (size_t)a.T * a.D * (slabs - 1);
     const size_t piece = l.per_col * (size_t)packed_columns(a, l, (size_t)1 << 62);
     // (spare room is shared between slabs and the piece)
@@ -254,8 +253,8 @@ CePiece piece_of(const CeProblem& a, int M, int N, int K, float c, const void* A
   return p;
 }
 
-bool grid_fits(const CePiece& p, int splits = 1) {
-  return (long long)p.tiles_m * p.tiles_n * splits <= INT_MAX;
+bool grid_fits(const CePiece& p) {
+  return (long long)p.tiles_m * p.tiles_n <= INT_MAX;
 }
 
 template <class T, int DT, int MODE>
@@ -264,7 +263,7 @@ int launch_logits(const CePiece& p, const int* label, int v0, CeRow* part, int r
   if (!grid_fits(p)) return SGEMM_ERR_UNSUPPORTED;
   const int n = p.tiles_m * p.tiles_n;
   hipLaunchKernelGGL((ce_logits_kernel<T, DT, MODE>), dim3(n), dim3(T::THREADS), 0, s, p.gemm,
-                     p.tiles_m, p.tiles_n, band_rows(p.tiles_m, n), label, v0, part, rows, zlabel);
+                     p.tiles_n, label, v0, part, rows, zlabel);
   return launched();
 }
 
@@ -274,17 +273,19 @@ int launch_dz(const CePiece& p, const CeRowInfo* info, int v0, uint16_t* dz, int
   if (!grid_fits(p)) return SGEMM_ERR_UNSUPPORTED;
   const int n = p.tiles_m * p.tiles_n;
   hipLaunchKernelGGL((ce_dz_gemm_kernel<T, DT, MODE>), dim3(n), dim3(T::THREADS), 0, s, p.gemm,
-                     p.tiles_m, p.tiles_n, band_rows(p.tiles_m, n), info, v0, dz, lddz);
+                     p.tiles_n, info, v0, dz, lddz);
   return launched();
 }
 
 template <class T, int DT, int MODE>
-int launch_dx(const CePiece& p, int splits, int kps, const void* w_tail, float* sums, size_t slab,
-              hipStream_t s) {
-  if (!grid_fits(p, splits)) return SGEMM_ERR_UNSUPPORTED;
-  const int n = p.tiles_m * p.tiles_n;
-  hipLaunchKernelGGL((ce_dx_kernel<T, DT, MODE>), dim3(n * splits), dim3(T::THREADS), 0, s, p.gemm,
-                     p.tiles_m, p.tiles_n, band_rows(p.tiles_m, n), kps, w_tail, sums, slab);
+int launch_dx(const CePiece& p, int cus, int slabs, int n_first, const void* w_tail, float* sums,
+              size_t slab, hipStream_t s) {
+  // (for fewer rows than T the splits grow, the workgroups stay below cus or
+  // one a tile)
+  const int n = std::max(p.tiles_m * p.tiles_n, cus);
+  if (!grid_fits(p)) return SGEMM_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL((ce_dx_kernel<T, DT, MODE>), dim3(n), dim3(T::THREADS), 0, s, p.gemm,
+                     p.tiles_n, cus, slabs, n_first, w_tail, sums, slab);
   return launched();
 }
 
@@ -367,15 +368,15 @@ int dz_piece(const CeProblem& a, int n, const void* xp, int dp, const void* w, c
 
 template <class T, int DT>
 int dx_piece(const CeProblem& a, int n, const uint16_t* dz, int lddz, const void* w,
-             const int* count, int splits, int kps, const void* w_tail, float* sums, size_t slab,
-             float beta, hipStream_t s) {
+             const int* count, int cus, int slabs, int n_first, const void* w_tail, float* sums,
+             size_t slab, float beta, hipStream_t s) {
   CePiece p = piece_of<T>(a, a.T, a.D, n, 0.0f, dz, lddz, w, a.ldw, count);
   p.gemm.g.beta = beta;
   p.gemm.g.ldc = a.D;
   return a.D % T::BN == 0 && n % kStep == 0
-             ? launch_dx<T, DT, MODE_ALIGNED>(p, splits, kps, nullptr, sums, slab, s)
-             : launch_dx<T, DT, MODE_PADDED>(p, splits, kps, n % kStep != 0 ? w_tail : nullptr, sums,
-                                             slab, s);
+             ? launch_dx<T, DT, MODE_ALIGNED>(p, cus, slabs, n_first, nullptr, sums, slab, s)
+             : launch_dx<T, DT, MODE_PADDED>(p, cus, slabs, n_first,
+                                             n % kStep != 0 ? w_tail : nullptr, sums, slab, s);
 }
 
 template <int DT>
@@ -390,13 +391,13 @@ int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels&
   if (h->workspace_bytes < least) return SGEMM_ERR_SCRATCH;
   // half of what is left over the least may go to slabs of dX's sums
   const bool bigx = dx_big(a);
-  int slabs = bigx ? dx_slabs(a, h->cus, 256, 256) : dx_slabs(a, h->cus, 128, 128);
+  int slabs = dx_slabs(a, h->cus, bigx ? 256 : 128);
   const size_t spare = (h->workspace_bytes - least) / 2 / (4 * slab);
   if (slabs > 1 && (size_t)(slabs - 1) > spare) slabs = 1 + (int)spare;
   l.fixed += 4 * slab * (slabs - 1);
   const long long cols = packed_columns(a, l, h->workspace_bytes);
   if (cols == 0) return SGEMM_ERR_SCRATCH;
-  const int lddz = (int)cols;
+  const int lddz = (int)cols, n_first = (int)(a.V < cols ? a.V : cols);
 
   Carver c = {static_cast<char*>(h->workspace)};
   int* count = c.take<int>(4);
@@ -439,17 +440,11 @@ int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels&
              : dz_piece<L128x128, DT>(a, n, xp, dp, w, count, info, (int)v0, dz, lddz, s);
     if (st != SGEMM_OK) return st;
     if (dX != nullptr) {
-      // the first piece sets every slab, so a later one uses no more
-      int splits = slabs;
-      if (splits > 1 && splits > n / kSplitCols) splits = n / kSplitCols > 1 ? n / kSplitCols : 1;
-      const int kps = (int)round_up(up_div(n, splits), kStep);
-      splits = (int)up_div(n, kps);
-      if (v0 == 0) slabs = splits;
       const float beta = v0 == 0 ? 0.0f : 1.0f;
-      st = bigx ? dx_piece<L256x256, DT>(a, n, dz, lddz, w, count, splits, kps, w_tail, sums, slab,
-                                         beta, s)
-                : dx_piece<L128x128, DT>(a, n, dz, lddz, w, count, splits, kps, w_tail, sums, slab,
-                                         beta, s);
+      st = bigx ? dx_piece<L256x256, DT>(a, n, dz, lddz, w, count, h->cus, slabs, n_first, w_tail,
+                                         sums, slab, beta, s)
+                : dx_piece<L128x128, DT>(a, n, dz, lddz, w, count, h->cus, slabs, n_first, w_tail,
+                                         sums, slab, beta, s);
       if (st != SGEMM_OK) return st;
     }
     if (dW != nullptr) {
@@ -467,8 +462,14 @@ int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels&
   if (dX == nullptr) return SGEMM_OK;
   g = grid_of((unsigned long long)a.T * (unsigned)(a.D / 8));
   if (g == 0) return SGEMM_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL(ce_dx_rows_kernel<DT>, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D, pos, sums,
-                     a.D, slab, slabs, out_factor, dX, lddx);
+  if (bigx)
+    hipLaunchKernelGGL((ce_dx_rows_kernel<L256x256, DT>), dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D,
+                       count, pos, sums, slab, (int)up_div(a.D, 256), h->cus, slabs, n_first,
+                       out_factor, dX, lddx);
+  else
+    hipLaunchKernelGGL((ce_dx_rows_kernel<L128x128, DT>), dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D,
+                       count, pos, sums, slab, (int)up_div(a.D, 128), h->cus, slabs, n_first,
+                       out_factor, dX, lddx);
   return launched();
 }
 

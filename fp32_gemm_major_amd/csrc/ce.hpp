@@ -505,36 +505,4 @@ static __global__ void __launch_bounds__(CE_JOIN_ROWS * CE_JOIN_LANES)
   loss[t] = y == CE_BAD ? NAN : e - zlabel[row];
 }
 
-// dX's rows: the slabs' sums of the row's packed row in slab order, times its
-// factor; zeros for rows that have none.  Eight columns a lane.
-template <int DT>
-__global__ void __launch_bounds__(CE_THREADS)
-    ce_dx_rows_kernel(int T, int D, const int* __restrict__ pos, const float* __restrict__ sums,
-                      int lds, size_t slab, int slabs, const float* __restrict__ out_factor,
-                      void* dX, int lddx) {
-  typedef typename TensorElem<DT>::type E;
-  const unsigned units = (unsigned)D / 8u;
-  const unsigned long long at = (unsigned long long)blockIdx.x * CE_THREADS + threadIdx.x;
-  const long long t = (long long)(at / units);
-  const int c = 8 * (int)(at % units);
-  if (t >= T) return;
-  const int r = pos[t];
-  float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  if (r >= 0) {
-    const float* p = sums + (size_t)r * lds + c;
-    for (int s = 0; s < slabs; ++s, p += slab) {
-      const v4u a = *reinterpret_cast<const v4u*>(p), b = *reinterpret_cast<const v4u*>(p + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] += __uint_as_float(a[i]);
-        v[4 + i] += __uint_as_float(b[i]);
-      }
-    }
-    const float f = out_factor[r];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= f;
-  }
-  store8<DT>(static_cast<E*>(dX) + (size_t)t * lddx + c, 8, v);
-}
-
 }  // namespace sgemm

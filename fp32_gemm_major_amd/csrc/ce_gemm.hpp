@@ -13,8 +13,10 @@
 // modes) on operands laid out for it: the rows of X that count, packed
 // together and padded with zeros to whole tiles (`count` rows; left-out rows
 // cost nothing), and dz in pieces of whole tiles of columns.  Only the device
-// knows `count`; tiles past it end at once, and dW's sums run over no more
-// rows than that.
+// knows `count`: a grid is launched for all rows, its first workgroups divide
+// the tiles that hold rows among them and the others end at once (spread
+// among the working ones they cost half a round of the device: 777 rows of
+// which 389 count took 105 us for 50001 words of 1024 columns, 512 rows 65).
 //
 // In a result block, register 4q + e of lane (li, lh) is row li, column
 // 8q + 4lh + e.
@@ -31,11 +33,33 @@ struct CeGemm {
   const int* count;  // rows that count
 };
 
-// Rows of A a kernel works on: those that count, one tile at least.
+// Rows of tiles that hold rows that count, one at least.
 template <class T>
-__device__ __forceinline__ bool ce_tile_idle(const int* count, int m0) {
+__device__ __forceinline__ int ce_tile_rows(const int* count) {
   const int n = *count;
-  return m0 >= (n > 1 ? n : 1);
+  return ((n > 1 ? n : 1) + T::BM - 1) / T::BM;
+}
+
+// The tile of workgroup wg (of those for tiles_m x tiles_n); false past them.
+__device__ __forceinline__ bool ce_tile(int wg, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int nwg = tiles_m * tiles_n;
+  if (wg >= nwg) return false;
+  tile_coords(wg, nwg, tiles_m, tiles_n, band_rows(tiles_m, nwg), tm, tn);
+  return true;
+}
+
+// How dX's sums over n columns are split: a workgroup a CU if the columns give
+// each split enough, in whole K steps; never more than `most`.
+struct CeSplit {
+  int splits, kps;
+};
+__host__ __device__ inline CeSplit ce_split(int tiles, int cus, int n, int most) {
+  int s = cus / tiles;
+  if (s > most) s = most;
+  if (s > n / 1024) s = n / 1024;
+  if (s < 1) s = 1;
+  const int kps = ((n + s - 1) / s + 63) & ~63;
+  return CeSplit{(n + kps - 1) / kps, kps};
 }
 
 // ---- logits to (max, sum) ------------------------------------------------------
@@ -43,13 +67,12 @@ __device__ __forceinline__ bool ce_tile_idle(const int* count, int m0) {
 // part[chunk][row]: chunk = the wave's columns (T::WN of them), rows padded.
 template <class T, int DT, int MODE>
 __global__ void __launch_bounds__(T::THREADS, T::OCC)
-    ce_logits_kernel(CeGemm a, int tiles_m, int tiles_n, int band, const int* __restrict__ label,
+    ce_logits_kernel(CeGemm a, int tiles_n, const int* __restrict__ label,
                      int v0, CeRow* __restrict__ part, int rows, float* __restrict__ zlabel) {
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS_ALIGNED];
   int tm, tn;
-  tile_coords(blockIdx.x, gridDim.x, tiles_m, tiles_n, band, tm, tn);
+  if (!ce_tile(blockIdx.x, ce_tile_rows<T>(a.count), tiles_n, tm, tn)) return;
   const int m0 = tm * T::BM, n0 = tn * T::BN;
-  if (ce_tile_idle<T>(a.count, m0)) return;
   f32x16 acc[T::FM][T::FN];
   zero_acc<T>(acc);
   lp_tile_accumulate<T, DT, MODE, false, true>(a.g, lds, m0, n0, acc);
@@ -112,7 +135,7 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
 // columns past N and in rows that count for nothing.
 template <class T, int DT, int MODE>
 __global__ void __launch_bounds__(T::THREADS, T::OCC)
-    ce_dz_gemm_kernel(CeGemm a, int tiles_m, int tiles_n, int band,
+    ce_dz_gemm_kernel(CeGemm a, int tiles_n,
                       const CeRowInfo* __restrict__ info, int v0, uint16_t* __restrict__ dz,
                       int lddz) {
   constexpr int ODT = DT == LP_BF16 ? SGEMM_DTYPE_BF16 : SGEMM_DTYPE_F16;
@@ -120,9 +143,8 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
   static_assert(T::WAVES * 32 * LD * 4 <= T::LDS_BYTES, "staging area");
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS_ALIGNED];
   int tm, tn;
-  tile_coords(blockIdx.x, gridDim.x, tiles_m, tiles_n, band, tm, tn);
+  if (!ce_tile(blockIdx.x, ce_tile_rows<T>(a.count), tiles_n, tm, tn)) return;
   const int m0 = tm * T::BM, n0 = tn * T::BN;
-  if (ce_tile_idle<T>(a.count, m0)) return;
   f32x16 acc[T::FM][T::FN];
   zero_acc<T>(acc);
   lp_tile_accumulate<T, DT, MODE, false, true>(a.g, lds, m0, n0, acc);
@@ -187,18 +209,22 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
 // ---- the gradients' products -----------------------------------------------------
 
 // sums[s][row][d] (+)= dz W over the piece's columns [s * kps, ...): workgroup
-// b takes tile b % tiles of split b / tiles.
+// b takes tile b % tiles of split b / tiles.  The first piece (of n_first
+// columns, none has more) sets the slabs that later ones add to.
 template <class T, int DT, int MODE>
 __global__ void __launch_bounds__(T::THREADS, T::OCC)
-    ce_dx_kernel(CeGemm a, int tiles_m, int tiles_n, int band, int kps,
+    ce_dx_kernel(CeGemm a, int tiles_n, int cus, int slabs, int n_first,
                  const void* __restrict__ w_tail, float* __restrict__ sums, size_t slab) {
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS_ALIGNED];
-  const int tiles = tiles_m * tiles_n;
+  const int tiles_m = ce_tile_rows<T>(a.count), tiles = tiles_m * tiles_n;
+  const CeSplit all = ce_split(tiles, cus, n_first, slabs);
+  const CeSplit sp = ce_split(tiles, cus, a.g.K, all.splits);
+  const int kps = sp.kps;
   const int split = blockIdx.x / tiles, tile = blockIdx.x - split * tiles;
+  if (split >= sp.splits) return;
   int tm, tn;
-  tile_coords(tile, tiles, tiles_m, tiles_n, band, tm, tn);
+  if (!ce_tile(tile, tiles_m, tiles_n, tm, tn)) return;
   const int m0 = tm * T::BM, n0 = tn * T::BN;
-  if (ce_tile_idle<T>(a.count, m0)) return;
   LpArgs g = a.g;
   const int k0 = split * kps;
   g.K = a.g.K - k0 < kps ? a.g.K - k0 : kps;
@@ -272,6 +298,39 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
     __builtin_amdgcn_wave_barrier();
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);
+}
+
+// dX's rows: the slabs' sums of the row's packed row in slab order, times its
+// factor; zeros for rows that have none.  Eight columns a lane.
+template <class Tile, int DT>
+__global__ void __launch_bounds__(CE_THREADS)
+    ce_dx_rows_kernel(int T, int D, const int* __restrict__ count, const int* __restrict__ pos,
+                      const float* __restrict__ sums, size_t slab, int tiles_n, int cus, int most,
+                      int n_first, const float* __restrict__ out_factor, void* dX, int lddx) {
+  const int slabs = ce_split(ce_tile_rows<Tile>(count) * tiles_n, cus, n_first, most).splits;
+  typedef typename TensorElem<DT>::type E;
+  const unsigned units = (unsigned)D / 8u;
+  const unsigned long long at = (unsigned long long)blockIdx.x * CE_THREADS + threadIdx.x;
+  const long long t = (long long)(at / units);
+  const int c = 8 * (int)(at % units);
+  if (t >= T) return;
+  const int r = pos[t];
+  float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (r >= 0) {
+    const float* p = sums + (size_t)r * D + c;
+    for (int s = 0; s < slabs; ++s, p += slab) {
+      const v4u a = *reinterpret_cast<const v4u*>(p), b = *reinterpret_cast<const v4u*>(p + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] += __uint_as_float(a[i]);
+        v[4 + i] += __uint_as_float(b[i]);
+      }
+    }
+    const float f = out_factor[r];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= f;
+  }
+  store8<DT>(static_cast<E*>(dX) + (size_t)t * lddx + c, 8, v);
 }
 
 }  // namespace sgemm

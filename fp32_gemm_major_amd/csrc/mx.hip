@@ -47,8 +47,17 @@ const dequant_fn kDequant[3] = {mx_dequantize_kernel<SGEMM_DTYPE_F32>,
                                 mx_dequantize_kernel<SGEMM_DTYPE_BF16>,
                                 mx_dequantize_kernel<SGEMM_DTYPE_F16>};
 typedef void (*small_fn)(MxArgs);
-const small_fn kSmall[4] = {mx_small_kernel<-1>, mx_small_kernel<SGEMM_DTYPE_F32>,
-                            mx_small_kernel<SGEMM_DTYPE_BF16>, mx_small_kernel<SGEMM_DTYPE_F16>};
+// [A's kind: codes, activations by type, activations of few rows by type]
+// [one or four tiles of columns a workgroup]
+#define MX_SMALL(XDT, FEW) {mx_small_kernel<XDT, FEW, 1>, mx_small_kernel<XDT, FEW, 4>}
+const small_fn kSmall[7][2] = {MX_SMALL(-1, false),
+                               MX_SMALL(SGEMM_DTYPE_F32, false),
+                               MX_SMALL(SGEMM_DTYPE_BF16, false),
+                               MX_SMALL(SGEMM_DTYPE_F16, false),
+                               MX_SMALL(SGEMM_DTYPE_F32, true),
+                               MX_SMALL(SGEMM_DTYPE_BF16, true),
+                               MX_SMALL(SGEMM_DTYPE_F16, true)};
+#undef MX_SMALL
 
 int launch_quantize(int dtype, int trans, const MxQuantArgs& g, hipStream_t stream) {
   const long long nb = blocks_of(g.K);
@@ -66,13 +75,24 @@ int launch_quantize(int dtype, int trans, const MxQuantArgs& g, hipStream_t stre
   return launched();
 }
 
-// The product, A in codes (xdt < 0) or in activations.
-int launch_small(int xdt, const MxArgs& g, hipStream_t stream) {
-  const long long tm = up_div(g.M, MXS_TILE), tn = up_div(g.N, MXS_TILE);
+// The product straight from memory, A in codes (xdt < 0) or in activations,
+// one or four tiles of 16 columns a workgroup.
+int launch_small(int xdt, int tiles, const MxArgs& g, hipStream_t stream) {
+  const long long tm = up_div(g.M, MXS_TILE), tn = up_div(g.N, MXS_TILE * tiles);
   if (tm > 65535) return SGEMM_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL(kSmall[xdt + 1], dim3((unsigned)tn, (unsigned)tm), dim3(MXS_THREADS), 0,
+  const int kind = xdt < 0 ? 0 : g.M <= MXS_FEW ? 4 + xdt : 1 + xdt;
+  hipLaunchKernelGGL(kSmall[kind][tiles == 4], dim3((unsigned)tn, (unsigned)tm), dim3(MXS_THREADS), 0,
                      stream, g);
   return launched();
+}
+
+// Tiles of columns a workgroup of up to 16 rows takes.  Four, once that still
+// leaves half the CUs one: they share A's loads (16 x 11008 x 4096: 10.5 ->
+// 9.2 us, 16 x 32000 x 4096: 23.6 -> 18.8) and its quantisation (1 x 11008 x
+// 4096: 12.2 -> 9.6).  With codes and a short K the loads of one tile already
+// overlap enough (16 x 65536 x 1024: 16.4 us, with four 18.0).
+int row_tiles(int xdt, const MxArgs& g, int cus) {
+  return 2 * up_div(g.N, 4 * MXS_TILE) >= cus && (xdt >= 0 || g.K >= 2048) ? 4 : 1;
 }
 
 typedef void (*tile_fn)(MxArgs, int, int, int);
@@ -103,18 +123,29 @@ int launch_tile(const MxTileDesc& t, const MxArgs& g, hipStream_t stream) {
   return launched();
 }
 
-// At most 16 rows: the kernel that reads B once from memory.  Else the
-// largest tile that gives every CU one, or the 256-square one where 128-square
-// tiles would take three rounds or more.
+// The kernel for a product of codes (measured on 256 CUs):
+//
+// * up to 16 rows: straight from memory, which reads B once;
+// * more, while its 16 x 16 tiles are at most two a CU: the same (17 x 4096 x
+//   11008 in 13.0 us against 17.2 in 64-square tiles, 128 x 1500 x 800 in 3.7
+//   against 4.5); also up to 64 rows of a long K where 64-square tiles reach
+//   a quarter of the CUs, four column tiles a workgroup (64 x 4096 x 11008:
+//   17.1 against 26.0);
+// * 256-square tiles where they give every CU one, or 128-square ones would
+//   start a second round (512 x 11008 x 4096: 33.7 against 36.7 us);
+// * 128-square ones where they give three CUs in five one (256 x 11008 x 4096:
+//   20.1 us against 28.3 in 64-square ones);
+// * else 64-square ones.
 int launch_product(const sgemm_handle_s* h, const MxArgs& g, hipStream_t stream) {
-  if (g.M > MXS_TILE && g.K > 0) {
-    const long long t256 = up_div(g.M, 256) * up_div(g.N, 256);
-    const long long t128 = up_div(g.M, 128) * up_div(g.N, 128);
-    const int at = t256 >= h->cus || t128 > 2LL * h->cus ? 0 : t128 >= h->cus ? 1 : 2;
-    for (int i = at; i < 3; ++i)
-      if (tile_fits(kTiles[i], g)) return launch_tile(kTiles[i], g, stream);
-  }
-  return launch_small(-1, g, stream);
+  const long long cus = h->cus;
+  if (g.M <= MXS_TILE || g.K == 0) return launch_small(-1, row_tiles(-1, g, h->cus), g, stream);
+  auto tiles = [&](int b) { return up_div(g.M, b) * up_div(g.N, b); };
+  if (tiles(MXS_TILE) <= 2 * cus) return launch_small(-1, 1, g, stream);
+  if (g.M <= 64 && g.K >= 8192 && 4 * tiles(64) <= cus) return launch_small(-1, 4, g, stream);
+  const int at = tiles(256) >= cus || 4 * tiles(128) > 5 * cus ? 0 : 5 * tiles(128) >= 3 * cus ? 1 : 2;
+  for (int i = at; i < 3; ++i)
+    if (tile_fits(kTiles[i], g)) return launch_tile(kTiles[i], g, stream);
+  return launch_small(-1, 1, g, stream);  // (strides past the tiles' offsets)
 }
 
 // Checks shared by both product entries but for A's own.
@@ -229,10 +260,16 @@ int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K, float a
   if (st != SGEMM_OK) return st;
   MxArgs g = {M, N, K, alpha, beta, X, ldx, nullptr, 0, static_cast<const uint8_t*>(B), ldb,
               static_cast<const uint8_t*>(SB), ldsb, dtype, C, ldc};
-  if (M <= MXS_TILE) return launch_small(xtype, g, stream);
-  // A's codes and then its scales in the handle's workspace
+  // A's codes and then its scales in the handle's workspace.  The kernel that
+  // quantises for itself takes up to 16 rows, but with more than four the
+  // quantisation, repeated by every workgroup, costs more than a launch (16 x
+  // 11008 x 4096: 18.0 us in one launch, 10.8 in two), unless there is no
+  // workspace.
   const size_t nb = (size_t)blocks_of(K), rows = (size_t)M;
-  if (h->workspace_bytes < 17 * nb * rows || 16 * nb > INT_MAX) return SGEMM_ERR_SCRATCH;
+  const bool room = h->workspace_bytes >= 17 * nb * rows;
+  if (M <= MXS_FEW || (M <= MXS_TILE && !room))
+    return launch_small(xtype, row_tiles(xtype, g, h->cus), g, stream);
+  if (!room) return SGEMM_ERR_SCRATCH;
   uint8_t* codes = static_cast<uint8_t*>(h->workspace);
   uint8_t* scales = codes + 16 * nb * rows;
   const MxQuantArgs q = {M, K, X, ldx, codes, (int)(16 * nb), scales, (int)nb};

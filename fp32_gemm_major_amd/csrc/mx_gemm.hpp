@@ -17,9 +17,12 @@
 //   instruction's byte select picks group q's.
 // * The step's scale bytes come by direct loads too, a dword a lane: two lanes
 //   a row, 32 rows a wave instruction.
-// * A step in which K ends (K is whole blocks, not whole steps) goes through
-//   registers, with zero codes and zero scales past the end: a scale byte
-//   there might say NaN.
+// * A step in which K ends (K is whole blocks, not whole steps) is loaded like
+//   the others, but nothing is read from outside a row: units past the end
+//   read the row's last one, and the scale dwords are the row's last eight
+//   bytes, which a shift brings into place with zeros past the end (a scale
+//   byte there might say NaN).  A's units past the end are zeroed as they come
+//   out of LDS.  K of less than a step goes through registers instead.
 // * Rows past M and N read the last valid row; what they give is not stored.
 //
 // C leaves through LDS as whole runs of a row, in 32, 16 bits a value.
@@ -124,21 +127,29 @@ __device__ __forceinline__ void mx_tile_accumulate(const MxArgs& g, char* lds, i
     for (int v = 0; v < T::S_VEC; ++v) s_voff[v] = 0u, s_base[v] = A;
   }
   const int steps = max(kd, 1);
+  // The partial step, loaded as step `steps` when there is one: its blocks,
+  // and how far a lane's unit lies past the row's last one (a lane's unit is
+  // the same in all its loads).
+  const int rest = kd > 0 ? nb - 8 * kd : 0;
+  const int loads = rest > 0 ? steps + 1 : steps;
+  const int unit_c = (lane & 7) ^ ((((wave * 64 + lane) >> 3) >> 1) & 7);
+  const unsigned back = rest > 0 ? 16u * (unsigned)max(unit_c - (rest - 1), 0) : 0u;
 
   constexpr int ND = T::A_VEC + T::B_VEC + T::S_VEC;
   const unsigned lds_u = (unsigned)(uintptr_t)(lds_void_t*)lds;
   const unsigned dummy = lds_u + (unsigned)T::LDS_BYTES;
   auto load_one = [&](int kt, int st, int d, bool live) {
+    const bool part = kt == steps;
     if (d < T::S_VEC) {
-      dma4(s_base[d] + (size_t)kt * 8, s_voff[d],
+      dma4(s_base[d] + (part ? (size_t)(nb - 8) : (size_t)kt * 8), s_voff[d],
            live ? lds_u + (unsigned)s_at(st) + 256u * (unsigned)(d * T::WAVES + wave_u) : dummy);
     } else if (d < T::S_VEC + T::A_VEC) {
       const int v = d - T::S_VEC;
-      dma16(reinterpret_cast<const float*>(A + (size_t)kt * 128), a_voff[v],
+      dma16(reinterpret_cast<const float*>(A + (size_t)kt * 128), a_voff[v] - (part ? back : 0u),
             live ? lds_u + (unsigned)a_at(st) + 1024u * (unsigned)(v * T::WAVES + wave_u) : dummy);
     } else {
       const int v = d - T::S_VEC - T::A_VEC;
-      dma16(reinterpret_cast<const float*>(B + (size_t)kt * 128), b_voff[v],
+      dma16(reinterpret_cast<const float*>(B + (size_t)kt * 128), b_voff[v] - (part ? back : 0u),
             live ? lds_u + (unsigned)b_at(st) + 1024u * (unsigned)(v * T::WAVES + wave_u) : dummy);
     }
   };
@@ -202,8 +213,8 @@ __device__ __forceinline__ void mx_tile_accumulate(const MxArgs& g, char* lds, i
   constexpr int AHEAD = (S - 2) * ND;
   constexpr int WAIT_AHEAD = 0x0F70 | (AHEAD & 15) | ((AHEAD >> 4) << 14);
   auto step = [&](int kt, auto st_c) {
-    const bool live = kt + S < steps;
-    const int kl = live ? kt + S : steps - 1;
+    const bool live = kt + S < loads;
+    const int kl = live ? kt + S : loads - 1;
     lp_static_for<H>([&](auto q_c) { group(kl, live, st_c, q_c); });
     wait_lds();
     __builtin_amdgcn_s_waitcnt(WAIT_AHEAD);
@@ -219,7 +230,8 @@ __device__ __forceinline__ void mx_tile_accumulate(const MxArgs& g, char* lds, i
   lp_static_for<S>([&](auto i) {
     constexpr int st = decltype(i)::value;
 #pragma unroll
-    for (int o = 0; o < ND; ++o) load_one(st < kd ? st : steps - 1, st, o, st < kd);
+    for (int o = 0; o < ND; ++o)
+      load_one(st < loads ? st : loads - 1, st, o, kd > 0 && st < loads);
   });
   if (kd == 0) {
 #pragma unroll 1
@@ -243,14 +255,44 @@ __device__ __forceinline__ void mx_tile_accumulate(const MxArgs& g, char* lds, i
   lp_static_for<S - 1>([&](auto i) {
     if (kt + decltype(i)::value < steps) step(kt + decltype(i)::value, i);
   });
-  if (8 * kd < nb) {
-    // The blocks of the last, partial step, into stage 0 once every wave is
-    // done with it and the look-ahead loads have landed.  (The lane's index is
-    // hidden from the compiler, which would otherwise keep this part's
-    // addresses in registers through the loop.)
+  if (rest > 0) {
+    // the partial step's loads have had whole steps to land
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    wait_lds();
+    __syncthreads();
+    const int st = steps % S;
+    const int shift = 8 * (8 - rest);
+    auto scale = [&](int row) {
+      const uint2 d = *reinterpret_cast<const uint2*>(lds + s_at(st) + 8 * row);
+      const unsigned long long v = (((unsigned long long)d.y << 32) | d.x) >> shift;
+      return lh ? (unsigned)(v >> 32) : (unsigned)v;
+    };
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) sc[0].a[i] = scale(wm * T::WM + 32 * i + li);
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) sc[0].b[j] = scale(T::BM + wn * T::WN + 32 * j + li);
+    lp_static_for<QG>([&](auto q_c) {
+      constexpr int q = decltype(q_c)::value;
+#pragma unroll
+      for (int r = 0; r < NF; ++r) read_one(st, q, r, fr[0]);
+#pragma unroll
+      for (int i = 0; i < T::FM; ++i)
+        if (4 * lh + q >= rest) fr[0].a[i] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int m = 0; m < SL; ++m) {
+        const int i = m / T::FN, j = m % T::FN;
+        acc[i][j] = mx_mfma<q>(fr[0].b[j], sc[0].b[j], fr[0].a[i], sc[0].a[i], acc[i][j]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
+  if (kd == 0) {
+    // K of less than a step, into stage 0 once every wave is done with it and
+    // the loop's loads have landed.  (The lane's index is hidden from the
+    // compiler, which would otherwise keep this part's addresses in registers
+    // through the loop.)
     int t = tid;
     asm volatile("" : "+v"(t));
-    const int have = nb - 8 * kd;
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
     wait_lds();
     __syncthreads();
@@ -259,10 +301,10 @@ __device__ __forceinline__ void mx_tile_accumulate(const MxArgs& g, char* lds, i
       const bool of_a = u < T::BM * 8;
       const int r = (of_a ? u : u - T::BM * 8) >> 3, c = (u & 7) ^ ((r >> 1) & 7);
       u32x4 x = {0u, 0u, 0u, 0u};
-      if (c < have) {
+      if (c < nb) {
         const uint8_t* p = of_a ? A + (size_t)min(r, a_last) * g.lda
                                 : B + (size_t)min(r, b_last) * g.ldb;
-        const v4u w = *reinterpret_cast<const v4u_any*>(p + 16 * (size_t)(8 * kd + c));
+        const v4u w = *reinterpret_cast<const v4u_any*>(p + 16 * (size_t)c);
         x = u32x4{w[0], w[1], w[2], w[3]};
       }
       *reinterpret_cast<u32x4*>(lds + 16 * u) = x;  // (A's tile, then B's)
@@ -271,9 +313,9 @@ __device__ __forceinline__ void mx_tile_accumulate(const MxArgs& g, char* lds, i
     for (int i = t; i < (T::BM + T::BN) * 8; i += T::THREADS) {
       const int c = i & 7, r = i >> 3;
       uint8_t b = 0;
-      if (c < have)
-        b = r < T::BM ? SA[(size_t)min(r, a_last) * g.ldsa + 8 * (size_t)kd + c]
-                      : SB[(size_t)min(r - T::BM, b_last) * g.ldsb + 8 * (size_t)kd + c];
+      if (c < nb)
+        b = r < T::BM ? SA[(size_t)min(r, a_last) * g.ldsa + c]
+                      : SB[(size_t)min(r - T::BM, b_last) * g.ldsb + c];
       lds[s_at(0) + i] = (char)b;
     }
     wait_lds();
@@ -294,13 +336,25 @@ __device__ __forceinline__ void mx_tile_accumulate(const MxArgs& g, char* lds, i
   }
 }
 
-// One run of EPL values of a row of C.
+// Up to EPL values of a row of C, those before the last column.
 template <int CDT, int EPL>
 __device__ __forceinline__ void mx_store_run(const MxArgs& g, const float* src, int row, int col) {
   typedef typename TensorElem<CDT>::type E;
   const int have = g.N - col;
   if (row >= g.M || have <= 0) return;
   E* p = static_cast<E*>(g.C) + (size_t)row * g.ldc + col;
+  if (have >= EPL && g.beta == 0.0f) {
+    v4u o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if constexpr (EPL == 4)
+        o[e] = __float_as_uint(g.alpha * src[e]);
+      else
+        o[e] = (unsigned)elem_bits<CDT>(g.alpha * src[2 * e]) |
+               ((unsigned)elem_bits<CDT>(g.alpha * src[2 * e + 1]) << 16);
+    *reinterpret_cast<v4u_any*>(p) = o;
+    return;
+  }
 #pragma unroll 1
   for (int e = 0; e < (have < EPL ? have : EPL); ++e) {
     float o = g.alpha * src[e];

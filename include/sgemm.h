@@ -500,9 +500,9 @@ int sgemm_validate_mx(int M, int N, int K, const void* A, int lda,
 
 /* The same with A given as an M x K tensor X of type xtype (any K; stride ldx
  * in elements) and quantised as sgemm_mx_quantize does: a linear layer with
- * 4-bit weights.  The result is that of the two calls.  Up to 16 rows are
- * quantised on the way into the product; more need 17*ceil(K/32)*M bytes of
- * the handle's workspace (SGEMM_ERR_SCRATCH). */
+ * 4-bit weights.  The result is that of the two calls.  Four rows or fewer are
+ * quantised on the way into the product; more use 17*ceil(K/32)*M bytes of
+ * the handle's workspace, which over 16 rows need (SGEMM_ERR_SCRATCH). */
 int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K,
                        float alpha, const void* X, int ldx, const void* B,
                        int ldb, const void* SB, int ldsb, float beta,

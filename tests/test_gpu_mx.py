@@ -176,7 +176,8 @@ def test_product(handle, M, N, K, dt, alpha, beta):
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))
-@pytest.mark.parametrize("M,N,K", [(1, 100, 33), (1, 4096, 4096), (7, 64, 777), (16, 50, 1024),
+@pytest.mark.parametrize("M,N,K", [(1, 100, 33), (1, 4096, 4096), (2, 40, 1), (3, 70, 5000),
+                                   (4, 33, 8192), (5, 90, 512), (7, 64, 777), (16, 50, 1024),
                                    (17, 64, 100), (40, 200, 4090), (300, 260, 520)])
 def test_product_of_activations(handle, M, N, K, dt):
     x = torch.from_numpy(values(M, K, M + K, spread=2)).to(DTYPES[dt])
@@ -269,7 +270,11 @@ def test_refusals(handle):
         with pytest.raises(sg.SgemmError) as e:
             bare.gemm_mx4(X, B, C)
         assert e.value.status == sg.SGEMM_ERR_SCRATCH
-        bare.gemm_mx4(X[:16], B, C[:16])  # up to 16 rows need none
+        for m in (3, 5, 16):  # up to 16 rows need none
+            want = torch.empty(m, 5, device="cuda")
+            handle.gemm_mx4(X[:m], B, want)
+            bare.gemm_mx4(X[:m], B, C[:m])
+            assert torch.equal(C[:m], want)
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 256, 1024), (40, 100, 800)])

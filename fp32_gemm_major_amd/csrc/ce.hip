@@ -44,6 +44,7 @@ struct Carver {
 
 constexpr size_t kProductBytes = 64u << 20;   // for the products' partial sums
 constexpr size_t kPieceBytes = 256u << 20;    // logits of a piece, when there is room
+constexpr size_t kPackedBytes = (size_t)1 << 30; // of a piece on packed rows
 constexpr int kPieceStep = 256;               // columns by which pieces grow
 
 // What a pass keeps besides a piece, and a piece's columns.
@@ -59,30 +60,44 @@ constexpr int kStep = 64;                             // k per step of the produ
 long long padded_rows(const CeProblem& a) { return round_up(a.T > 1 ? a.T : 1, kPadRows); }
 long long padded_cols(const CeProblem& a) { return round_up(a.D, kPadCols); }
 
-// Whether sizes allow packed rows: whole 16-byte units a row.
+// Elements of a packed row's copy in one plane, planes a row (32-bit X and W
+// are split into three), and the row stride of dX's sums.
+int plane_count(const CeProblem& a) { return a.dtype == SGEMM_DTYPE_F32 ? 3 : 1; }
+long long sum_cols(const CeProblem& a) { return round_up(a.D, 8); }
+
+// Whether sizes allow packed rows: 16-bit rows of whole 16-byte units (32-bit
+// ones are copied).
 bool packable(const CeProblem& a) {
-  return tensor_elem_bytes(a.dtype) == 2 && a.D % 8 == 0 && a.D <= INT_MAX / 4 - kPadCols &&
+  return (a.dtype == SGEMM_DTYPE_F32 || a.D % 8 == 0) && a.D <= (1 << 21) &&
          a.T <= INT_MAX - kPadRows;
 }
-// Whether a call takes them: W's rows inside the direct loads' 32-bit offsets
-// and near enough for the copy of its last rows to have their stride.  Few
-// rows of a forward pass go through the products with few rows instead.
-constexpr int kFewRows = 16;
+// Whether a call takes them.  16-bit: W's rows inside the direct loads' 32-bit
+// offsets and near enough for the copy of its last rows to have their stride;
+// few rows of a forward pass go through the products with few rows instead.
+// 32-bit: more rows, for the copies of W and the whole tiles to pay (1024
+// columns, 32000 words, forward and backward: 256 rows in 655 us, 564 over the
+// library's products; 512 rows 905 against 1029; 2048 rows 2.76 ms against
+// 3.88).
+constexpr int kFewRows = 16, kFewRows32 = 511;
 bool packed(const CeProblem& a, int backward) {
-  return packable(a) && a.ldw <= 2LL * a.D && (backward || a.T > kFewRows);
+  if (!packable(a)) return false;
+  if (a.dtype == SGEMM_DTYPE_F32) return a.T > kFewRows32;
+  return a.ldw <= 2LL * a.D && (backward || a.T > kFewRows);
 }
 
 CeLayout packed_layout(const CeProblem& a, int backward) {
   const size_t T = (size_t)a.T, Tp = (size_t)padded_rows(a), Dp = (size_t)padded_cols(a);
+  const size_t planes = (size_t)plane_count(a);
   CeLayout l = {16 * 256, 0};
   if (!backward) {
-    l.fixed += 4 * T + 20 * Tp + 2 * Tp * Dp;
+    l.fixed += 4 * T + 20 * Tp + 2 * planes * Tp * Dp;
     l.per_col = Tp / 8;  // eight bytes a row for 64 columns or more
   } else {
-    l.fixed += 4 * T + 24 * Tp + (a.dtype == SGEMM_DTYPE_F16 ? 4 : 2) * Tp * Dp +
-               2 * kStep * 2 * (size_t)a.D + 4 * T * a.D;
-    l.per_col = 2 * Tp;
+    l.fixed += 4 * T + 24 * Tp + (a.dtype == SGEMM_DTYPE_F16 ? 4 : 2) * planes * Tp * Dp +
+               2 * kStep * 2 * (size_t)a.D + 4 * T * (size_t)sum_cols(a);
+    l.per_col = 2 * planes * Tp;
   }
+  if (planes > 1) l.per_col += 2 * planes * Dp;  // W's piece in planes
   return l;
 }
 
@@ -91,11 +106,11 @@ CeLayout packed_layout(const CeProblem& a, int backward) {
 long long packed_columns(const CeProblem& a, const CeLayout& l, size_t bytes) {
   if (bytes < l.fixed + l.per_col * kPadCols) return 0;
   long long cols = (long long)((bytes - l.fixed) / l.per_col);
-  const long long most = (long long)(kPieceBytes / l.per_col);
+  const long long most = (long long)(kPackedBytes / l.per_col);
   if (cols > most) cols = most;
   cols = cols < kPadCols ? kPadCols : cols / kPadCols * kPadCols;
-  const long long all = round_up(a.V, kPadCols);
-  return cols < all ? cols : all;
+  // as many pieces as that takes, of about one size
+  return round_up(up_div(a.V, up_div(a.V, cols)), kPadCols);
 }
 
 // Slabs of dX's sums: where its tiles are fewer than the CUs, the vocabulary
@@ -104,7 +119,7 @@ long long packed_columns(const CeProblem& a, const CeLayout& l, size_t bytes) {
 int dx_slabs(const CeProblem& a, int cus, int b) {
   const long long tiles = up_div(a.T, b) * up_div(a.D, b);
   if (tiles > cus) return 1;
-  const int s = ce_split((int)tiles, cus, a.V, 64).splits;
+  const int s = ce_split((int)tiles, cus, a.V, 64, plane_count(a) > 1).splits;
   return s < 32 ? 2 * s : 64;
 }
 // Tiles of dX's product: 256 square unless one extent fits half of one.
@@ -217,7 +232,7 @@ CeSizes sizes_of(const CeProblem& a, int backward, int cus) {
     size_t least = l.fixed + l.per_col * kPadCols;
     if (least > z.least) z.least = least;
     const int slabs = backward ? dx_slabs(a, cus, dx_big(a) ? 256 : 128) : 1;
-    const size_t more = 4 * (size_t)a.T * a.D * (slabs - 1);
+    const size_t more = 4 * (size_t)a.T * (size_t)sum_cols(a) * (slabs - 1);
     const size_t piece = l.per_col * (size_t)packed_columns(a, l, (size_t)1 << 62);
     // (spare room is shared between slabs and the piece)
     const size_t full = l.fixed + l.per_col * kPadCols + (2 * more > more + piece ? 2 * more : more + piece);
@@ -236,8 +251,9 @@ struct CePiece {
 
 template <class T>
 CePiece piece_of(const CeProblem& a, int M, int N, int K, float c, const void* A, int lda,
-                 const void* B, int ldb, const int* count) {
+                 const void* B, int ldb, const int* count, LpPlanes planes = LpPlanes{0, 0}) {
   CePiece p = {};
+  p.gemm.planes = planes;
   p.gemm.g.M = M;
   p.gemm.g.N = N;
   p.gemm.g.K = K;
@@ -268,12 +284,12 @@ int launch_logits(const CePiece& p, const int* label, int v0, CeRow* part, int r
 }
 
 template <class T, int DT, int MODE>
-int launch_dz(const CePiece& p, const CeRowInfo* info, int v0, uint16_t* dz, int lddz,
+int launch_dz(const CePiece& p, const CeRowInfo* info, int v0, uint16_t* dz, int lddz, int plane,
               hipStream_t s) {
   if (!grid_fits(p)) return SGEMM_ERR_UNSUPPORTED;
   const int n = p.tiles_m * p.tiles_n;
   hipLaunchKernelGGL((ce_dz_gemm_kernel<T, DT, MODE>), dim3(n), dim3(T::THREADS), 0, s, p.gemm,
-                     p.tiles_n, info, v0, dz, lddz);
+                     p.tiles_n, info, v0, dz, lddz, plane);
   return launched();
 }
 
@@ -289,35 +305,98 @@ int launch_dx(const CePiece& p, int cus, int slabs, int n_first, const void* w_t
   return launched();
 }
 
-template <class T, int DT>
+template <class T, int DT, int MODE>
 int launch_dw(const CePiece& p, const float* factor, void* out, int ldo, hipStream_t s) {
   if (!grid_fits(p)) return SGEMM_ERR_UNSUPPORTED;
   const int n = p.tiles_m * p.tiles_n;
-  hipLaunchKernelGGL((ce_dw_kernel<T, DT>), dim3(n), dim3(T::THREADS), 0, s, p.gemm, p.tiles_m,
+  hipLaunchKernelGGL((ce_dw_kernel<T, DT, MODE>), dim3(n), dim3(T::THREADS), 0, s, p.gemm, p.tiles_m,
                      p.tiles_n, band_rows(p.tiles_m, n), factor, out, ldo);
   return launched();
 }
 
-// 256-square tiles where they give every CU one, else 128-square ones; rows
-// that fit half a tile take the smaller.
+// 256-square tiles where they give three CUs in five one, else 128-square ones
+// (which ask the caches for twice the bytes per product); rows that fit half a
+// tile take the smaller.
 bool big_tiles(long long rows, long long cols, int cus) {
-  return rows > 128 && up_div(rows, 256) * up_div(cols, 256) >= cus;
+  return rows > 128 && 5 * up_div(rows, 256) * up_div(cols, 256) >= 3LL * cus;
+}
+
+// The operands of a packed pass: X's packed rows and a piece of W, as the
+// products read them.  16-bit W stays where it is; 32-bit W's piece is copied
+// into planes.
+struct CeOperands {
+  const void* x;  // X's packed rows, stride ldx
+  int ldx;
+  const void* w;  // the piece of W, stride ldw
+  int ldw;
+  int plane;      // between planes of a row of either (32-bit)
+  const int* count;
+};
+
+constexpr int product_type(int dtype) {  // of the matrix instructions
+  return dtype == SGEMM_DTYPE_F16 ? SGEMM_DTYPE_F16 : SGEMM_DTYPE_BF16;
 }
 
 template <class T, int DT>
-int logits_piece(const CeProblem& a, int n, const void* xp, int dp, const void* w,
-                 const int* count, const int* label, int v0, CeRow* part, int rows, float* zlabel,
-                 hipStream_t s) {
-  const CePiece p = piece_of<T>(a, a.T, n, a.D, a.alpha * CE_LOG2E, xp, dp, w, a.ldw, count);
-  return n % T::BN == 0 && a.D % kStep == 0
-             ? launch_logits<T, DT, MODE_ALIGNED>(p, label, v0, part, rows, zlabel, s)
-             : launch_logits<T, DT, MODE_PADDED>(p, label, v0, part, rows, zlabel, s);
+int logits_piece(const CeProblem& a, int n, const CeOperands& o, const int* label, int v0,
+                 CeRow* part, int rows, float* zlabel, hipStream_t s) {
+  constexpr int MT = product_type(DT);
+  const CePiece p = piece_of<T>(a, a.T, n, a.D, a.alpha * CE_LOG2E, o.x, o.ldx, o.w, o.ldw, o.count,
+                                LpPlanes{o.plane, o.plane});
+  if constexpr (DT == SGEMM_DTYPE_F32)
+    return launch_logits<T, MT, MODE_PLANES>(p, label, v0, part, rows, zlabel, s);
+  else
+    return n % T::BN == 0 && a.D % kStep == 0
+               ? launch_logits<T, MT, MODE_ALIGNED>(p, label, v0, part, rows, zlabel, s)
+               : launch_logits<T, MT, MODE_PADDED>(p, label, v0, part, rows, zlabel, s);
+}
+
+// X's packed rows (for 32-bit X in planes), their stride in *ldx.
+template <int DT>
+int pack_rows(const CeProblem& a, const int* pos, const int* count, const float* x_factor,
+              void* plain, void* scaled, int dp, int* ldx, hipStream_t s) {
+  const unsigned g = grid_of((unsigned long long)(a.T + CE_ROW_PAD) * (unsigned)(dp / 8));
+  if (g == 0) return SGEMM_ERR_UNSUPPORTED;
+  if constexpr (DT == SGEMM_DTYPE_F32) {
+    *ldx = 3 * dp;
+    hipLaunchKernelGGL(ce_planes_kernel, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.T + CE_ROW_PAD, a.D,
+                       static_cast<const float*>(a.X), a.ldx, pos, count,
+                       static_cast<uint16_t*>(plain), dp);
+  } else {
+    *ldx = dp;
+    hipLaunchKernelGGL(ce_gather_kernel<DT>, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D, a.X, a.ldx,
+                       pos, count, x_factor, plain, scaled, dp);
+  }
+  return launched();
+}
+
+// The piece of W from row v0 on, n rows: in place, or in planes at `copy`.
+template <int DT>
+int piece_of_w(const CeProblem& a, long long v0, int n, void* copy, int dp, CeOperands* o,
+               hipStream_t s) {
+  const void* w = rows_from(a.W, (size_t)v0, a.ldw, tensor_elem_bytes(DT));
+  o->w = w;
+  o->ldw = a.ldw;
+  o->plane = 0;
+  if constexpr (DT == SGEMM_DTYPE_F32) {
+    const int rows = (int)round_up(n, kPadCols);  // zeros after the last: they meet dz's zeros
+    const unsigned g = grid_of((unsigned long long)rows * (unsigned)(dp / 8));
+    if (g == 0) return SGEMM_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL(ce_planes_kernel, dim3(g), dim3(CE_THREADS), 0, s, n, rows, a.D,
+                       static_cast<const float*>(w), a.ldw, static_cast<const int*>(nullptr),
+                       static_cast<const int*>(nullptr), static_cast<uint16_t*>(copy), dp);
+    o->w = copy;
+    o->ldw = 3 * dp;
+    o->plane = dp;
+    return launched();
+  }
+  return SGEMM_OK;
 }
 
 template <int DT>
 int packed_forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
                    float* loss, float* lse, hipStream_t s) {
-  const int Tp = (int)padded_rows(a), dp = (int)padded_cols(a);
+  const int Tp = (int)padded_rows(a), dp = (int)padded_cols(a), planes = plane_count(a);
   const long long cols = packed_columns(a, packed_layout(a, 0), h->workspace_bytes);
   if (cols == 0) return SGEMM_ERR_SCRATCH;
   Carver c = {static_cast<char*>(h->workspace)};
@@ -327,25 +406,23 @@ int packed_forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& 
   int* label = c.take<int>(4 * (size_t)Tp);
   float* zlabel = c.take<float>(4 * (size_t)Tp);
   CeRow* state = c.take<CeRow>(sizeof(CeRow) * (size_t)Tp);
-  void* xp = c.take<char>(2 * (size_t)Tp * dp);
+  void* xp = c.take<char>(2 * (size_t)planes * Tp * dp);
+  void* wp = c.take<char>(planes > 1 ? 2 * (size_t)planes * cols * dp : 0);
   CeRow* part = c.take<CeRow>(0);
   hipLaunchKernelGGL(ce_pack_kernel, dim3(1), dim3(CE_PACK_THREADS), 0, s, a.T, Tp, labels, pos,
                      order, label, count, loss, lse);
   int st = launched();
   if (st != SGEMM_OK) return st;
-  const unsigned g = grid_of((unsigned long long)(a.T + CE_ROW_PAD) * (unsigned)(dp / 8));
-  if (g == 0) return SGEMM_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL(ce_gather_kernel<DT>, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D, a.X, a.ldx,
-                     pos, count, static_cast<const float*>(nullptr), xp,
-                     static_cast<void*>(nullptr), dp);
-  st = launched();
+  CeOperands o = {xp, 0, nullptr, 0, 0, count};
+  st = pack_rows<DT>(a, pos, count, nullptr, xp, nullptr, dp, &o.ldx, s);
   if (st != SGEMM_OK) return st;
   for (long long v0 = 0; v0 < a.V; v0 += cols) {
     const int n = (int)(a.V - v0 < cols ? a.V - v0 : cols);
-    const void* w = rows_from(a.W, (size_t)v0, a.ldw, 2);
+    st = piece_of_w<DT>(a, v0, n, wp, dp, &o, s);
+    if (st != SGEMM_OK) return st;
     const bool big = big_tiles(a.T, n, h->cus);
-    st = big ? logits_piece<L256x256, DT>(a, n, xp, dp, w, count, label, (int)v0, part, Tp, zlabel, s)
-             : logits_piece<L128x128, DT>(a, n, xp, dp, w, count, label, (int)v0, part, Tp, zlabel, s);
+    st = big ? logits_piece<L256x256, DT>(a, n, o, label, (int)v0, part, Tp, zlabel, s)
+             : logits_piece<L128x128, DT>(a, n, o, label, (int)v0, part, Tp, zlabel, s);
     if (st != SGEMM_OK) return st;
     const int chunks = (int)up_div(n, big ? L256x256::WN : L128x128::WN);
     hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)up_div(a.T, CE_JOIN_ROWS)),
@@ -357,26 +434,60 @@ int packed_forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& 
   return SGEMM_OK;
 }
 
+// dz of a piece: rows of lddz elements a plane.
+struct CeDz {
+  uint16_t* dz;
+  int lddz;
+};
+
 template <class T, int DT>
-int dz_piece(const CeProblem& a, int n, const void* xp, int dp, const void* w, const int* count,
-             const CeRowInfo* info, int v0, uint16_t* dz, int lddz, hipStream_t s) {
-  const CePiece p = piece_of<T>(a, a.T, n, a.D, a.alpha * CE_LOG2E, xp, dp, w, a.ldw, count);
-  return n % T::BN == 0 && a.D % kStep == 0
-             ? launch_dz<T, DT, MODE_ALIGNED>(p, info, v0, dz, lddz, s)
-             : launch_dz<T, DT, MODE_PADDED>(p, info, v0, dz, lddz, s);
+int dz_piece(const CeProblem& a, int n, const CeOperands& o, const CeRowInfo* info, int v0,
+             const CeDz& d, hipStream_t s) {
+  constexpr int MT = product_type(DT);
+  const CePiece p = piece_of<T>(a, a.T, n, a.D, a.alpha * CE_LOG2E, o.x, o.ldx, o.w, o.ldw, o.count,
+                                LpPlanes{o.plane, o.plane});
+  if constexpr (DT == SGEMM_DTYPE_F32)
+    return launch_dz<T, MT, MODE_PLANES>(p, info, v0, d.dz, 3 * d.lddz, d.lddz, s);
+  else
+    return n % T::BN == 0 && a.D % kStep == 0
+               ? launch_dz<T, MT, MODE_ALIGNED>(p, info, v0, d.dz, d.lddz, 0, s)
+               : launch_dz<T, MT, MODE_PADDED>(p, info, v0, d.dz, d.lddz, 0, s);
+}
+
+// dX's sums: `slabs` of `slab` elements, rows of lds.
+struct CeSums {
+  float* sums;
+  int lds;
+  size_t slab;
+  int slabs, n_first;
+};
+
+template <class T, int DT>
+int dx_piece(const CeProblem& a, int n, const CeOperands& o, const CeDz& d, int cus,
+             const void* w_tail, const CeSums& x, float beta, hipStream_t s) {
+  constexpr int MT = product_type(DT);
+  constexpr bool WIDE = DT == SGEMM_DTYPE_F32;
+  CePiece p = piece_of<T>(a, a.T, a.D, n, 0.0f, d.dz, WIDE ? 3 * d.lddz : d.lddz, o.w, o.ldw,
+                          o.count, LpPlanes{d.lddz, o.plane});
+  p.gemm.g.beta = beta;
+  p.gemm.g.ldc = x.lds;
+  if constexpr (WIDE)
+    return launch_dx<T, MT, MODE_PLANES>(p, cus, x.slabs, x.n_first, nullptr, x.sums, x.slab, s);
+  else
+    return a.D % T::BN == 0 && n % kStep == 0
+               ? launch_dx<T, MT, MODE_ALIGNED>(p, cus, x.slabs, x.n_first, nullptr, x.sums, x.slab, s)
+               : launch_dx<T, MT, MODE_PADDED>(p, cus, x.slabs, x.n_first,
+                                               n % kStep != 0 ? w_tail : nullptr, x.sums, x.slab, s);
 }
 
 template <class T, int DT>
-int dx_piece(const CeProblem& a, int n, const uint16_t* dz, int lddz, const void* w,
-             const int* count, int cus, int slabs, int n_first, const void* w_tail, float* sums,
-             size_t slab, float beta, hipStream_t s) {
-  CePiece p = piece_of<T>(a, a.T, a.D, n, 0.0f, dz, lddz, w, a.ldw, count);
-  p.gemm.g.beta = beta;
-  p.gemm.g.ldc = a.D;
-  return a.D % T::BN == 0 && n % kStep == 0
-             ? launch_dx<T, DT, MODE_ALIGNED>(p, cus, slabs, n_first, nullptr, sums, slab, s)
-             : launch_dx<T, DT, MODE_PADDED>(p, cus, slabs, n_first,
-                                             n % kStep != 0 ? w_tail : nullptr, sums, slab, s);
+int dw_piece(const CeProblem& a, int n, const CeDz& d, const void* xs, int ldxs, int dp,
+             const int* count, const float* factor, void* out, int ldo, hipStream_t s) {
+  constexpr int MT = product_type(DT);
+  constexpr bool WIDE = DT == SGEMM_DTYPE_F32;
+  const CePiece p = piece_of<T>(a, n, a.D, (int)padded_rows(a), 0.0f, d.dz,
+                                WIDE ? 3 * d.lddz : d.lddz, xs, ldxs, count, LpPlanes{d.lddz, dp});
+  return launch_dw<T, MT, WIDE ? MODE_PLANES : MODE_ALIGNED>(p, factor, out, ldo, s);
 }
 
 template <int DT>
@@ -384,20 +495,23 @@ int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels&
                     const float* lse, const float* dloss, const float* dlse, void* dX, int lddx,
                     void* dW, int lddw, hipStream_t s) {
   constexpr bool SCALED = DT == SGEMM_DTYPE_F16;
-  const int Tp = (int)padded_rows(a), dp = (int)padded_cols(a);
+  const unsigned esz = tensor_elem_bytes(DT);
+  const int Tp = (int)padded_rows(a), dp = (int)padded_cols(a), planes = plane_count(a);
   CeLayout l = packed_layout(a, 1);
-  const size_t slab = (size_t)a.T * a.D;
+  CeSums x = {};
+  x.lds = (int)sum_cols(a);
+  x.slab = (size_t)a.T * x.lds;
   const size_t least = l.fixed + l.per_col * kPadCols;
   if (h->workspace_bytes < least) return SGEMM_ERR_SCRATCH;
   // half of what is left over the least may go to slabs of dX's sums
   const bool bigx = dx_big(a);
-  int slabs = dx_slabs(a, h->cus, bigx ? 256 : 128);
-  const size_t spare = (h->workspace_bytes - least) / 2 / (4 * slab);
-  if (slabs > 1 && (size_t)(slabs - 1) > spare) slabs = 1 + (int)spare;
-  l.fixed += 4 * slab * (slabs - 1);
+  x.slabs = dx_slabs(a, h->cus, bigx ? 256 : 128);
+  const size_t spare = (h->workspace_bytes - least) / 2 / (4 * x.slab);
+  if (x.slabs > 1 && (size_t)(x.slabs - 1) > spare) x.slabs = 1 + (int)spare;
+  l.fixed += 4 * x.slab * (x.slabs - 1);
   const long long cols = packed_columns(a, l, h->workspace_bytes);
   if (cols == 0) return SGEMM_ERR_SCRATCH;
-  const int lddz = (int)cols, n_first = (int)(a.V < cols ? a.V : cols);
+  x.n_first = (int)(a.V < cols ? a.V : cols);
 
   Carver c = {static_cast<char*>(h->workspace)};
   int* count = c.take<int>(4);
@@ -406,81 +520,76 @@ int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels&
   CeRowInfo* info = c.take<CeRowInfo>(sizeof(CeRowInfo) * (size_t)Tp);
   float* x_factor = c.take<float>(4 * (size_t)Tp);
   float* out_factor = c.take<float>(4 * (size_t)Tp);
-  void* xp = c.take<char>(2 * (size_t)Tp * dp);
-  // (bfloat16 rows need no scaling: one copy serves both products)
+  void* xp = c.take<char>(2 * (size_t)planes * Tp * dp);
+  // (only binary16 rows are scaled: else one copy serves both products)
   void* xs = SCALED ? c.take<char>(2 * (size_t)Tp * dp) : xp;
-  void* w_tail = c.take<char>(2 * (size_t)kStep * a.ldw);
-  float* sums = c.take<float>(4 * slab * slabs);
-  uint16_t* dz = c.take<uint16_t>(0);
+  void* w_tail = c.take<char>(planes > 1 ? 0 : 2 * (size_t)kStep * a.ldw);
+  x.sums = c.take<float>(4 * x.slab * x.slabs);
+  void* wp = c.take<char>(planes > 1 ? 2 * (size_t)planes * cols * dp : 0);
+  const CeDz d = {c.take<uint16_t>(0), (int)cols};
 
   hipLaunchKernelGGL(ce_pack_factors_kernel<SCALED>, dim3(1), dim3(CE_PACK_THREADS), 0, s, a.T, Tp,
                      a.alpha, labels, lse, dloss, dlse, pos, info, x_factor, out_factor, dw_factor,
                      count);
   int st = launched();
   if (st != SGEMM_OK) return st;
-  unsigned g = grid_of((unsigned long long)(a.T + CE_ROW_PAD) * (unsigned)(dp / 8));
-  if (g == 0) return SGEMM_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL(ce_gather_kernel<DT>, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D, a.X, a.ldx,
-                     pos, count, x_factor, xp, SCALED ? xs : nullptr, dp);
-  st = launched();
+  CeOperands o = {xp, 0, nullptr, 0, 0, count};
+  st = pack_rows<DT>(a, pos, count, x_factor, xp, SCALED ? xs : nullptr, dp, &o.ldx, s);
   if (st != SGEMM_OK) return st;
-  if (dX != nullptr && a.V % kStep != 0) {
-    const int rows = a.V % kStep;
-    hipLaunchKernelGGL(ce_tail_kernel<DT>, dim3(grid_of((unsigned long long)kStep * (a.D / 8))),
-                       dim3(CE_THREADS), 0, s, rows, a.D,
-                       rows_from(a.W, (size_t)(a.V - rows), a.ldw, 2), w_tail, a.ldw);
-    st = launched();
-    if (st != SGEMM_OK) return st;
+  if constexpr (DT != SGEMM_DTYPE_F32) {
+    if (dX != nullptr && a.V % kStep != 0) {
+      const int rows = a.V % kStep;
+      hipLaunchKernelGGL(ce_tail_kernel<DT>, dim3(grid_of((unsigned long long)kStep * (a.D / 8))),
+                         dim3(CE_THREADS), 0, s, rows, a.D,
+                         rows_from(a.W, (size_t)(a.V - rows), a.ldw, esz), w_tail, a.ldw);
+      st = launched();
+      if (st != SGEMM_OK) return st;
+    }
   }
   for (long long v0 = 0; v0 < a.V; v0 += cols) {
     const int n = (int)(a.V - v0 < cols ? a.V - v0 : cols);
-    const void* w = rows_from(a.W, (size_t)v0, a.ldw, 2);
-    st = big_tiles(a.T, n, h->cus)
-             ? dz_piece<L256x256, DT>(a, n, xp, dp, w, count, info, (int)v0, dz, lddz, s)
-             : dz_piece<L128x128, DT>(a, n, xp, dp, w, count, info, (int)v0, dz, lddz, s);
+    st = piece_of_w<DT>(a, v0, n, wp, dp, &o, s);
+    if (st != SGEMM_OK) return st;
+    st = big_tiles(a.T, n, h->cus) ? dz_piece<L256x256, DT>(a, n, o, info, (int)v0, d, s)
+                                   : dz_piece<L128x128, DT>(a, n, o, info, (int)v0, d, s);
     if (st != SGEMM_OK) return st;
     if (dX != nullptr) {
       const float beta = v0 == 0 ? 0.0f : 1.0f;
-      st = bigx ? dx_piece<L256x256, DT>(a, n, dz, lddz, w, count, h->cus, slabs, n_first, w_tail,
-                                         sums, slab, beta, s)
-                : dx_piece<L128x128, DT>(a, n, dz, lddz, w, count, h->cus, slabs, n_first, w_tail,
-                                         sums, slab, beta, s);
+      st = bigx ? dx_piece<L256x256, DT>(a, n, o, d, h->cus, w_tail, x, beta, s)
+                : dx_piece<L128x128, DT>(a, n, o, d, h->cus, w_tail, x, beta, s);
       if (st != SGEMM_OK) return st;
     }
     if (dW != nullptr) {
-      void* out = rows_from(dW, (size_t)v0, lddw, 2);
+      void* out = rows_from(dW, (size_t)v0, lddw, esz);
       st = big_tiles(n, a.D, h->cus)
-               ? launch_dw<L256x256, DT>(
-                     piece_of<L256x256>(a, n, a.D, Tp, 0.0f, dz, lddz, xs, dp, count), dw_factor,
-                     out, lddw, s)
-               : launch_dw<L128x128, DT>(
-                     piece_of<L128x128>(a, n, a.D, Tp, 0.0f, dz, lddz, xs, dp, count), dw_factor,
-                     out, lddw, s);
+               ? dw_piece<L256x256, DT>(a, n, d, xs, o.ldx, dp, count, dw_factor, out, lddw, s)
+               : dw_piece<L128x128, DT>(a, n, d, xs, o.ldx, dp, count, dw_factor, out, lddw, s);
       if (st != SGEMM_OK) return st;
     }
   }
   if (dX == nullptr) return SGEMM_OK;
-  g = grid_of((unsigned long long)a.T * (unsigned)(a.D / 8));
+  const unsigned g = grid_of((unsigned long long)a.T * (unsigned)up_div(a.D, 8));
   if (g == 0) return SGEMM_ERR_UNSUPPORTED;
   if (bigx)
     hipLaunchKernelGGL((ce_dx_rows_kernel<L256x256, DT>), dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D,
-                       count, pos, sums, slab, (int)up_div(a.D, 256), h->cus, slabs, n_first,
-                       out_factor, dX, lddx);
+                       count, pos, x.sums, x.lds, x.slab, (int)up_div(a.D, 256), h->cus, x.slabs,
+                       x.n_first, out_factor, dX, lddx);
   else
     hipLaunchKernelGGL((ce_dx_rows_kernel<L128x128, DT>), dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D,
-                       count, pos, sums, slab, (int)up_div(a.D, 128), h->cus, slabs, n_first,
-                       out_factor, dX, lddx);
+                       count, pos, x.sums, x.lds, x.slab, (int)up_div(a.D, 128), h->cus, x.slabs,
+                       x.n_first, out_factor, dX, lddx);
   return launched();
 }
 
-// ---- calls over the library's products (32-bit X and W, odd sizes) -----------------
+// ---- calls over the library's products (few rows, odd sizes) ------------------------
 
 int forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels, float* loss,
             float* lse, hipStream_t s) {
-  if (packed(a, 0))
-    return a.dtype == SGEMM_DTYPE_BF16
-               ? packed_forward<SGEMM_DTYPE_BF16>(h, a, labels, loss, lse, s)
-               : packed_forward<SGEMM_DTYPE_F16>(h, a, labels, loss, lse, s);
+  if (packed(a, 0)) switch (a.dtype) {
+      case SGEMM_DTYPE_F32: return packed_forward<SGEMM_DTYPE_F32>(h, a, labels, loss, lse, s);
+      case SGEMM_DTYPE_BF16: return packed_forward<SGEMM_DTYPE_BF16>(h, a, labels, loss, lse, s);
+      default: return packed_forward<SGEMM_DTYPE_F16>(h, a, labels, loss, lse, s);
+    }
   const CeLayout l = layout_of(a, 0);
   const int cols = piece_columns(a, l, h->workspace_bytes);
   if (cols == 0) return SGEMM_ERR_SCRATCH;
@@ -511,9 +620,8 @@ int backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels
              void* dW, int lddw, hipStream_t s) {
   constexpr bool WIDE = DT == SGEMM_DTYPE_F32;  // 32-bit gradients are their own sums
   constexpr unsigned esz = WIDE ? 4 : 2;
-  if constexpr (!WIDE)
-    if (packed(a, 1))
-      return packed_backward<DT>(h, a, labels, lse, dloss, dlse, dX, lddx, dW, lddw, s);
+  if (packed(a, 1))
+    return packed_backward<DT>(h, a, labels, lse, dloss, dlse, dX, lddx, dW, lddw, s);
   const CeLayout l = layout_of(a, 1);
   const int cols = piece_columns(a, l, h->workspace_bytes);
   if (cols == 0) return SGEMM_ERR_SCRATCH;

@@ -1,5 +1,6 @@
-// The products of the output layer's loss for 16-bit X and W, each with the
-// work around it folded in (see ce.hpp for the formulas):
+// The products of the output layer's loss, each with the work around it folded
+// in (see ce.hpp for the formulas), for 16-bit X and W and for 32-bit ones
+// split into three bfloat16 planes (MODE_PLANES):
 //
 //   ce_logits_kernel   z = X W^T, a tile's rows reduced at once to (max, sum
 //                      of exp); z itself never leaves the registers
@@ -29,9 +30,21 @@ namespace sgemm {
 
 struct CeGemm {
   LpArgs g;          // A: packed rows, B: W's piece; M, N, K of the product
-  float c;           // alpha * log2(e) (logits), or alpha
+  float c;           // alpha * log2(e) (logits)
   const int* count;  // rows that count
+  LpPlanes planes;   // split operands: A's and B's plane strides
 };
+
+// x = h + m + l in three bfloat16 planes (bit patterns).  Values that would
+// round past the largest bfloat16 are truncated; infinities and NaNs are all h.
+__device__ __forceinline__ void ce_split3(float x, uint16_t (&p)[3]) {
+  p[0] = elem_bits<SGEMM_DTYPE_BF16>(x);
+  const bool finite = (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u;
+  if ((p[0] & 0x7f80u) == 0x7f80u && finite) p[0] = (uint16_t)(__float_as_uint(x) >> 16);
+  const float r = x - elem_value<SGEMM_DTYPE_BF16>(p[0]);
+  p[1] = finite ? elem_bits<SGEMM_DTYPE_BF16>(r) : (uint16_t)0;
+  p[2] = finite ? elem_bits<SGEMM_DTYPE_BF16>(r - elem_value<SGEMM_DTYPE_BF16>(p[1])) : (uint16_t)0;
+}
 
 // Rows of tiles that hold rows that count, one at least.
 template <class T>
@@ -53,10 +66,11 @@ __device__ __forceinline__ bool ce_tile(int wg, int tiles_m, int tiles_n, int& t
 struct CeSplit {
   int splits, kps;
 };
-__host__ __device__ inline CeSplit ce_split(int tiles, int cus, int n, int most) {
+__host__ __device__ inline CeSplit ce_split(int tiles, int cus, int n, int most, bool planes) {
+  const int least = planes ? 256 : 512;  // columns: 24 and 8 K steps
   int s = cus / tiles;
   if (s > most) s = most;
-  if (s > n / 1024) s = n / 1024;
+  if (s > n / least) s = n / least;
   if (s < 1) s = 1;
   const int kps = ((n + s - 1) / s + 63) & ~63;
   return CeSplit{(n + kps - 1) / kps, kps};
@@ -75,7 +89,7 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
   const int m0 = tm * T::BM, n0 = tn * T::BN;
   f32x16 acc[T::FM][T::FN];
   zero_acc<T>(acc);
-  lp_tile_accumulate<T, DT, MODE, false, true>(a.g, lds, m0, n0, acc);
+  lp_tile_accumulate<T, DT, MODE, false, true>(a.g, lds, m0, n0, acc, nullptr, a.planes);
   __builtin_amdgcn_s_waitcnt(0x0F70);  // the loop's look-ahead loads
   const WaveCoords<T> w;
   const int col0 = n0 + w.wn * T::WN;  // the wave's first column
@@ -131,13 +145,14 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
 
 // ---- logits to dz ------------------------------------------------------------------
 
-// dz (16-bit, rows of lddz elements) is written for whole tiles: zeros in
-// columns past N and in rows that count for nothing.
+// dz (rows of lddz elements) is written for whole tiles: zeros in columns past
+// N and in rows that count for nothing.  16-bit dz is rounded once; 32-bit dz
+// leaves in its three planes, `plane` elements apart.
 template <class T, int DT, int MODE>
 __global__ void __launch_bounds__(T::THREADS, T::OCC)
     ce_dz_gemm_kernel(CeGemm a, int tiles_n,
                       const CeRowInfo* __restrict__ info, int v0, uint16_t* __restrict__ dz,
-                      int lddz) {
+                      int lddz, int plane) {
   constexpr int ODT = DT == LP_BF16 ? SGEMM_DTYPE_BF16 : SGEMM_DTYPE_F16;
   constexpr int LD = T::WN + 4, LPR = T::WN / 8, RPI = 64 / LPR, NI = 32 / RPI;
   static_assert(T::WAVES * 32 * LD * 4 <= T::LDS_BYTES, "staging area");
@@ -147,7 +162,7 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
   const int m0 = tm * T::BM, n0 = tn * T::BN;
   f32x16 acc[T::FM][T::FN];
   zero_acc<T>(acc);
-  lp_tile_accumulate<T, DT, MODE, false, true>(a.g, lds, m0, n0, acc);
+  lp_tile_accumulate<T, DT, MODE, false, true>(a.g, lds, m0, n0, acc, nullptr, a.planes);
   const WaveCoords<T> w;
   const int col0 = n0 + w.wn * T::WN;
   const int have = a.g.N - col0;
@@ -194,11 +209,26 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
     const float* src = reg + rr * LD + cc;
 #pragma unroll
     for (int t = 0; t < NI; ++t, out += (size_t)RPI * lddz, src += RPI * LD) {
-      v4u o;
+      if constexpr (MODE == MODE_PLANES) {
+        v4u o[3];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        o[e] = (unsigned)elem_bits<ODT>(src[2 * e]) | ((unsigned)elem_bits<ODT>(src[2 * e + 1]) << 16);
-      *reinterpret_cast<v4u*>(out) = o;
+        for (int e = 0; e < 4; ++e) {
+          uint16_t lo[3], hi[3];
+          ce_split3(src[2 * e], lo);
+          ce_split3(src[2 * e + 1], hi);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) o[k][e] = (unsigned)lo[k] | ((unsigned)hi[k] << 16);
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<v4u*>(out + (size_t)k * plane) = o[k];
+      } else {
+        v4u o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[e] = (unsigned)elem_bits<ODT>(src[2 * e]) |
+                 ((unsigned)elem_bits<ODT>(src[2 * e + 1]) << 16);
+        *reinterpret_cast<v4u*>(out) = o;
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_wave_barrier();
@@ -217,8 +247,8 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
                  const void* __restrict__ w_tail, float* __restrict__ sums, size_t slab) {
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS_ALIGNED];
   const int tiles_m = ce_tile_rows<T>(a.count), tiles = tiles_m * tiles_n;
-  const CeSplit all = ce_split(tiles, cus, n_first, slabs);
-  const CeSplit sp = ce_split(tiles, cus, a.g.K, all.splits);
+  const CeSplit all = ce_split(tiles, cus, n_first, slabs, MODE == MODE_PLANES);
+  const CeSplit sp = ce_split(tiles, cus, a.g.K, all.splits, MODE == MODE_PLANES);
   const int kps = sp.kps;
   const int split = blockIdx.x / tiles, tile = blockIdx.x - split * tiles;
   if (split >= sp.splits) return;
@@ -234,7 +264,7 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
   f32x16 acc[T::FM][T::FN];
   zero_acc<T>(acc);
   lp_tile_accumulate<T, DT, MODE, false, false>(g, lds, m0, n0, acc,
-                                                k0 + g.K == a.g.K ? w_tail : nullptr);
+                                                k0 + g.K == a.g.K ? w_tail : nullptr, a.planes);
   GemmArgs e = {};
   e.M = g.M;
   e.N = g.N;
@@ -248,13 +278,18 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
 }
 
 // dW's rows [0, N of W's piece) = factor * dz^T X: the sums run over the rows
-// that count, to whole K steps (the rows between hold zeros).
-template <class T, int DT>
+// that count, to whole K steps (the rows between hold zeros).  Split operands
+// give 32-bit gradients, others 16-bit ones.
+template <class T, int DT, int MODE>
 __global__ void __launch_bounds__(T::THREADS, T::OCC)
     ce_dw_kernel(CeGemm a, int tiles_m, int tiles_n, int band, const float* __restrict__ factor,
                  void* __restrict__ out, int ldo) {
-  constexpr int ODT = DT == LP_BF16 ? SGEMM_DTYPE_BF16 : SGEMM_DTYPE_F16;
-  constexpr int LD = T::WN + 4, LPR = T::WN / 8, RPI = 64 / LPR, NI = 32 / RPI;
+  constexpr int ODT = MODE == MODE_PLANES ? SGEMM_DTYPE_F32
+                      : DT == LP_BF16     ? SGEMM_DTYPE_BF16
+                                          : SGEMM_DTYPE_F16;
+  typedef typename TensorElem<ODT>::type E;
+  constexpr int EPL = MODE == MODE_PLANES ? 4 : 8;  // values a lane
+  constexpr int LD = T::WN + 4, LPR = T::WN / EPL, RPI = 64 / LPR, NI = 32 / RPI;
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS_ALIGNED];
   int tm, tn;
   tile_coords(blockIdx.x, gridDim.x, tiles_m, tiles_n, band, tm, tn);
@@ -264,10 +299,10 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
   g.K = ((n > 1 ? n : 1) + 63) & ~63;
   f32x16 acc[T::FM][T::FN];
   zero_acc<T>(acc);
-  lp_tile_accumulate<T, DT, MODE_ALIGNED, true, false>(g, lds, m0, n0, acc);
+  lp_tile_accumulate<T, DT, MODE, true, false>(g, lds, m0, n0, acc, nullptr, a.planes);
   const WaveCoords<T> w;
   float* reg = reinterpret_cast<float*>(lds) + w.wave * 32 * LD;
-  const int rr = w.lane / LPR, cc = 8 * (w.lane % LPR);
+  const int rr = w.lane / LPR, cc = EPL * (w.lane % LPR);
   const int col = n0 + w.wn * T::WN + cc, have = g.N - col;
   const float f = *factor;
   __syncthreads();
@@ -283,16 +318,24 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
                   acc[i][j][4 * q + 3]};
     __builtin_amdgcn_wave_barrier();
     const float* src = reg + rr * LD + cc;
-    uint16_t* p = static_cast<uint16_t*>(out) + (size_t)row0 * ldo + col;
-    // (D is a multiple of eight: a lane's run lies inside or outside)
+    E* p = static_cast<E*>(out) + (size_t)row0 * ldo + col;
 #pragma unroll
     for (int t = 0; t < NI; ++t, p += (size_t)RPI * ldo, src += RPI * LD) {
-      v4u o;
+      if (have <= 0 || row0 + t * RPI >= g.M) continue;
+      if (have >= EPL) {
+        v4u o;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        o[e] = (unsigned)elem_bits<ODT>(f * src[2 * e]) |
-               ((unsigned)elem_bits<ODT>(f * src[2 * e + 1]) << 16);
-      if (have > 0 && row0 + t * RPI < g.M) *reinterpret_cast<v4u_any*>(p) = o;
+        for (int e = 0; e < 4; ++e)
+          if constexpr (EPL == 4)
+            o[e] = __float_as_uint(f * src[e]);
+          else
+            o[e] = (unsigned)elem_bits<ODT>(f * src[2 * e]) |
+                   ((unsigned)elem_bits<ODT>(f * src[2 * e + 1]) << 16);
+        *reinterpret_cast<v4u_any*>(p) = o;
+      } else {
+#pragma unroll 1
+        for (int e = 0; e < have; ++e) p[e] = elem_bits<ODT>(f * src[e]);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_wave_barrier();
@@ -300,16 +343,60 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
   __builtin_amdgcn_s_waitcnt(0x0F70);
 }
 
+// Rows of 32-bit values to bfloat16 planes: rows [0, n) of `in` (or, with pos,
+// row t to row pos[t], none where it is negative) to `out`, rows of 3 * ld
+// elements, plane k at k * ld; zeros in the columns from D to ld and in the
+// rows after the last one up to `padded` (with pos: from *count to the end of
+// its CE_ROW_PAD rows).  Eight columns a lane.
+static __global__ void __launch_bounds__(CE_THREADS)
+    ce_planes_kernel(int n, int padded, int D, const float* __restrict__ in, int ldin,
+                     const int* __restrict__ pos, const int* __restrict__ count,
+                     uint16_t* __restrict__ out, int ld) {
+  const unsigned units = (unsigned)ld / 8u;
+  const unsigned long long at = (unsigned long long)blockIdx.x * CE_THREADS + threadIdx.x;
+  const long long t = (long long)(at / units);
+  const int c = 8 * (int)(at % units);
+  if (t >= padded) return;
+  long long r = t;
+  if (pos != nullptr) {
+    if (t < n) {
+      r = pos[t];
+      if (r < 0) return;
+    } else {
+      const int k = *count, end = ((k > 1 ? k : 1) + CE_ROW_PAD - 1) / CE_ROW_PAD * CE_ROW_PAD;
+      r = k + (t - n);
+      if (r >= end) return;
+    }
+  }
+  float v[8];
+  load8<SGEMM_DTYPE_F32>(reinterpret_cast<const uint32_t*>(in) + (t < n ? (size_t)t * ldin + c : (size_t)0),
+                         t < n ? D - c : 0, v);
+  v4u o[3];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint16_t lo[3], hi[3];
+    ce_split3(v[2 * e], lo);
+    ce_split3(v[2 * e + 1], hi);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) o[k][e] = (unsigned)lo[k] | ((unsigned)hi[k] << 16);
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    *reinterpret_cast<v4u*>(out + (size_t)r * 3 * ld + (size_t)k * ld + c) = o[k];
+}
+
 // dX's rows: the slabs' sums of the row's packed row in slab order, times its
 // factor; zeros for rows that have none.  Eight columns a lane.
 template <class Tile, int DT>
 __global__ void __launch_bounds__(CE_THREADS)
     ce_dx_rows_kernel(int T, int D, const int* __restrict__ count, const int* __restrict__ pos,
-                      const float* __restrict__ sums, size_t slab, int tiles_n, int cus, int most,
-                      int n_first, const float* __restrict__ out_factor, void* dX, int lddx) {
-  const int slabs = ce_split(ce_tile_rows<Tile>(count) * tiles_n, cus, n_first, most).splits;
+                      const float* __restrict__ sums, int lds, size_t slab, int tiles_n, int cus,
+                      int most, int n_first, const float* __restrict__ out_factor, void* dX, int lddx) {
+  const int slabs = ce_split(ce_tile_rows<Tile>(count) * tiles_n, cus, n_first, most,
+                             DT == SGEMM_DTYPE_F32)
+                        .splits;
   typedef typename TensorElem<DT>::type E;
-  const unsigned units = (unsigned)D / 8u;
+  const unsigned units = ((unsigned)D + 7u) / 8u;
   const unsigned long long at = (unsigned long long)blockIdx.x * CE_THREADS + threadIdx.x;
   const long long t = (long long)(at / units);
   const int c = 8 * (int)(at % units);
@@ -317,7 +404,7 @@ __global__ void __launch_bounds__(CE_THREADS)
   const int r = pos[t];
   float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   if (r >= 0) {
-    const float* p = sums + (size_t)r * D + c;
+    const float* p = sums + (size_t)r * lds + c;  // (rows of whole units)
     for (int s = 0; s < slabs; ++s, p += slab) {
       const v4u a = *reinterpret_cast<const v4u*>(p), b = *reinterpret_cast<const v4u*>(p + 4);
 #pragma unroll
@@ -330,7 +417,7 @@ __global__ void __launch_bounds__(CE_THREADS)
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= f;
   }
-  store8<DT>(static_cast<E*>(dX) + (size_t)t * lddx + c, 8, v);
+  store8<DT>(static_cast<E*>(dX) + (size_t)t * lddx + c, D - c, v);
 }
 
 }  // namespace sgemm

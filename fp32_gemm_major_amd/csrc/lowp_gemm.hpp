@@ -271,8 +271,32 @@ __device__ __forceinline__ u32x4 lp_load_unit(const E* p, int n) {
   return out;
 }
 
-// Padded kernels' mode, beside MODE_ALIGNED, MODE_EDGE and MODE_GUARDED.
-constexpr int MODE_PADDED = 3;
+// Padded kernels' mode, beside MODE_ALIGNED, MODE_EDGE and MODE_GUARDED, and
+// the mode of products of 32-bit operands split into three bfloat16 planes.
+//
+// x = h + m + l, each what is left rounded to eight bits (exactly x: 24 bits).
+// A product of two such numbers is the sum of nine plane products, of which
+// six are formed, smallest first: hl, lh, mm, hm, mh, hh.  The three left out
+// are below 2^-24 of the product each, a bit or more below a 32-bit rounding,
+// and the sums carry fewer roundings than the 32-bit matrix instruction's (one
+// for 16 products instead of one for two).  Six 16-bit products run at about
+// 200 TFLOP/s of 32-bit work, against 150 on the 32-bit matrix cores.
+//
+// The planes of a row of either operand stand beside one another, LpPlanes
+// elements apart; operands are padded as for aligned kernels and g.K is the k
+// of one plane.
+constexpr int MODE_PADDED = 3, MODE_PLANES = 4;
+struct LpPlanes {
+  int a, b;
+};
+constexpr int LP_PLANE_PRODUCTS = 6;
+// The planes (0: h, 1: m, 2: l) of A and of B in product i.
+__device__ __forceinline__ int lp_plane_a(int i) {
+  return i == 1 ? 2 : i == 2 || i == 4 ? 1 : 0;
+}
+__device__ __forceinline__ int lp_plane_b(int i) {
+  return i == 0 ? 2 : i == 2 || i == 3 ? 1 : 0;
+}
 
 // Accumulate the output tile at (m0, n0) over all of K into acc (zeroed by
 // the caller).  TA: A stored K x M; TB: B stored N x K.  b_tail (padded mode,
@@ -281,13 +305,14 @@ template <class T, int DT, int MODE, bool TA, bool TB>
 __device__ __forceinline__ void lp_tile_accumulate(const LpArgs& g, char* lds,
                                                    int m0, int n0,
                                                    f32x16 (&acc)[T::FM][T::FN],
-                                                   const void* b_tail = nullptr) {
+                                                   const void* b_tail = nullptr,
+                                                   LpPlanes planes = LpPlanes{0, 0}) {
   typedef LpFmt<DT> F;
   typedef typename F::E E;
   constexpr int ESZ = F::ESZ, UE = F::UE, BKE = F::BKE, FU = F::FU, QG = F::QG;
   constexpr bool GUARD = MODE == MODE_GUARDED;
   constexpr bool EDGE = MODE == MODE_EDGE;
-  constexpr bool PAD = MODE == MODE_PADDED;
+  constexpr bool PAD = MODE == MODE_PADDED, PLANES = MODE == MODE_PLANES;
   constexpr bool A_KC = !TA;  // A stored K-contiguous
   constexpr bool B_KC = TB;   // B stored K-contiguous
   const int M = g.M, N = g.N, K = g.K;
@@ -301,7 +326,8 @@ __device__ __forceinline__ void lp_tile_accumulate(const LpArgs& g, char* lds,
   const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
   const int li = lane & 31, lh = lane >> 5;
   const int kb = lane & 7, ob = lane >> 3;  // transposing loader block
-  const int nk = (K + BKE - 1) / BKE;
+  const int nk1 = (K + BKE - 1) / BKE;  // K steps of one plane
+  const int nk = PLANES ? LP_PLANE_PRODUCTS * nk1 : nk1;
 
   // LDS: the A tiles of all stages, then the B tiles.
   auto a_off = [](int st) { return st * T::A_BYTES; };
@@ -475,15 +501,33 @@ __device__ __forceinline__ void lp_tile_accumulate(const LpArgs& g, char* lds,
   // them to a scratch KB past the stages that nothing reads, so the stages
   // are free for the epilogue once the loop's last barrier has passed.
   const unsigned lds_dummy = lds_u + (unsigned)T::LDS_BYTES;
+  // Step kt's place in A and B (split operands: inside plane product i).  The
+  // division leaves a value that the compiler no longer knows to be uniform.
+  auto uniform = [](const E* p) {
+    const unsigned long long x = reinterpret_cast<unsigned long long>(p);
+    const unsigned lo = __builtin_amdgcn_readfirstlane((unsigned)x);
+    const unsigned hi = __builtin_amdgcn_readfirstlane((unsigned)(x >> 32));
+    return reinterpret_cast<const E*>(((unsigned long long)hi << 32) | lo);
+  };
+  auto a_step = [&](int kt) {
+    if constexpr (!PLANES) return a_dbase + (size_t)kt * a_dstep;
+    const int i = kt / nk1;
+    return uniform(a_dbase + (size_t)lp_plane_a(i) * planes.a + (size_t)(kt - i * nk1) * a_dstep);
+  };
+  auto b_step = [&](int kt) {
+    if constexpr (!PLANES) return b_dbase + (size_t)kt * b_dstep;
+    const int i = kt / nk1;
+    return uniform(b_dbase + (size_t)lp_plane_b(i) * planes.b + (size_t)(kt - i * nk1) * b_dstep);
+  };
   auto direct_one = [&](int kt, int st, int d, bool live) {
     if (d < ND_A)
-      dma16(reinterpret_cast<const float*>(a_dbase + (size_t)kt * a_dstep), a_voff[d],
+      dma16(reinterpret_cast<const float*>(a_step(kt)), a_voff[d],
             live ? lds_u + (unsigned)a_off(st) + 1024u * (unsigned)(d * T::WAVES + wave_u)
                  : lds_dummy);
     else
       dma16(reinterpret_cast<const float*>(PAD && !B_KC && b_tail != nullptr && kt == nk - 1
                                                ? static_cast<const E*>(b_tail) + n0
-                                               : b_dbase + (size_t)kt * b_dstep),
+                                               : b_step(kt)),
             b_voff[d - ND_A] - (PAD && B_KC && kt == nk - 1 ? b_back : 0u),
             live ? lds_u + (unsigned)b_off(st) +
                        1024u * (unsigned)((d - ND_A) * T::WAVES + wave_u)

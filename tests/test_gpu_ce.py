@@ -127,7 +127,8 @@ class Problem:
 SIZES = [(1, 1, 1), (1, 5, 3), (2, 300, 7), (3, 100, 16), (16, 257, 64), (17, 1000, 33), (64, 512, 128),
          (65, 2050, 100), (130, 5000, 257), (256, 1024, 256), (300, 777, 512), (513, 4099, 130),
          # packed rows: 128- and 256-square tiles, ragged and whole in every extent
-         (20, 4096, 72), (129, 2048, 320), (257, 6401, 392), (300, 33001, 264), (260, 65536, 64)]
+         (20, 4096, 72), (129, 2048, 320), (257, 6401, 392), (300, 33001, 264), (260, 65536, 64),
+         (520, 9001, 100), (600, 700, 1030)]
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))
@@ -237,7 +238,7 @@ def test_no_rows(handle):
         assert (dW == 0).all()
 
 
-@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("dt", list(DTYPES))
 @pytest.mark.parametrize("count", [0, 1, 127, 128, 255, 256, 257, 384, 512, 600])
 def test_rows_that_count_at_tile_edges(handle, count, dt):
     p = Problem(600, 1300, 72, dt, seed=6, ignored=0.0)
@@ -344,6 +345,23 @@ def test_random_inputs(handle, T, V, D, dt):
     ez = 4 * D * U * (np.abs(x) @ np.abs(w).T).max(1) + (V / 64 + 32) * U + 2.0 ** -14
     assert np.all(np.abs(lse.double().cpu().numpy() - want_lse) <= ez + 4 * U * np.abs(want_lse))
     assert np.all(np.abs(loss.double().cpu().numpy() - want) <= 2 * ez)
+
+
+@pytest.mark.parametrize("T", [1, 40, 520])
+@pytest.mark.parametrize("D", [1, 2, 4])
+def test_32_bit_logits_keep_24_bits(handle, T, D):
+    """One word: lse is the logit itself.  Operands with all 24 bits set: a
+    product of 16 bits or 21 would miss the library's 32-bit bound, 4 D u
+    sum|x w|, to which the logarithm's scale and back add 4 u |z|."""
+    rng = np.random.default_rng([T, D])
+    x, w = (1 + (rng.integers(0, 1 << 11, s) * 4096 + 2047) * 2.0 ** -23 for s in ((T, D), (1, D)))
+    X, W = (torch.from_numpy(v).float().cuda() for v in (x, w))
+    assert np.array_equal(X.double().cpu().numpy(), x)
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    handle.ce_forward(X, W, torch.zeros(T, dtype=torch.int64, device="cuda"), loss, lse)
+    z = (x @ w.T)[:, 0]
+    assert np.all(np.abs(lse.double().cpu().numpy() - z) <= (4 * D + 4) * U * z)
+    assert np.all(np.abs(loss.double().cpu().numpy()) <= (4 * D + 8) * U * z)
 
 
 def test_gradients_by_differences(handle):

@@ -44,7 +44,8 @@ struct Carver {
 
 constexpr size_t kProductBytes = 64u << 20;   // for the products' partial sums
 constexpr size_t kPieceBytes = 256u << 20;    // logits of a piece, when there is room
-constexpr size_t kPackedBytes = (size_t)1 << 30; // of a piece on packed rows
+constexpr size_t kPackedBytes = (size_t)1 << 30;  // of a piece on packed rows
+constexpr size_t kDzBytes = 256u << 20;       // of its dz: what the last-level cache holds
 constexpr int kPieceStep = 256;               // columns by which pieces grow
 
 // What a pass keeps besides a piece, and a piece's columns.
@@ -52,61 +53,70 @@ struct CeLayout {
   size_t fixed, per_col;
 };
 
-// ---- calls on packed rows (16-bit X and W) ------------------------------------
+// ---- calls on packed rows ------------------------------------------------------
 
 constexpr int kPadRows = CE_ROW_PAD, kPadCols = 256;  // whole tiles
 constexpr int kStep = 64;                             // k per step of the products
 
 long long padded_rows(const CeProblem& a) { return round_up(a.T > 1 ? a.T : 1, kPadRows); }
 long long padded_cols(const CeProblem& a) { return round_up(a.D, kPadCols); }
-
-// Elements of a packed row's copy in one plane, planes a row (32-bit X and W
-// are split into three), and the row stride of dX's sums.
+// Planes of a row's copy (32-bit X and W are split into three), and the row
+// stride of dX's sums.
 int plane_count(const CeProblem& a) { return a.dtype == SGEMM_DTYPE_F32 ? 3 : 1; }
 long long sum_cols(const CeProblem& a) { return round_up(a.D, 8); }
 
-// Whether sizes allow packed rows: 16-bit rows of whole 16-byte units (32-bit
-// ones are copied).
-bool packable(const CeProblem& a) {
-  return (a.dtype == SGEMM_DTYPE_F32 || a.D % 8 == 0) && a.D <= (1 << 21) &&
-         a.T <= INT_MAX - kPadRows;
-}
-// Whether a call takes them.  16-bit: W's rows inside the direct loads' 32-bit
-// offsets and near enough for the copy of its last rows to have their stride;
-// few rows of a forward pass go through the products with few rows instead.
-// 32-bit: more rows, for the copies of W and the whole tiles to pay (1024
-// columns, 32000 words, forward and backward: 256 rows in 655 us, 564 over the
-// library's products; 512 rows 905 against 1029; 2048 rows 2.76 ms against
-// 3.88).
+// Whether a call runs on packed rows.  16-bit: every backward pass; few rows
+// of a forward pass go through the products with few rows instead.  32-bit:
+// from rows on for which the copies of W and the whole tiles pay (1024 columns,
+// 32000 words, forward and backward: 256 rows in 655 us, 564 over the library's
+// products; 512 rows 905 against 1029; 2048 rows 2.76 ms against 3.88).
 constexpr int kFewRows = 16, kFewRows32 = 511;
 bool packed(const CeProblem& a, int backward) {
-  if (!packable(a)) return false;
-  if (a.dtype == SGEMM_DTYPE_F32) return a.T > kFewRows32;
-  return a.ldw <= 2LL * a.D && (backward || a.T > kFewRows);
+  return a.dtype == SGEMM_DTYPE_F32 ? a.T > kFewRows32 : backward || a.T > kFewRows;
 }
+// Whether W's pieces are copied: 32-bit ones into planes, 16-bit ones whose
+// rows are no whole 16-byte units, or too far apart for the copy of W's last
+// rows to have their stride.
+bool copies_w(const CeProblem& a) {
+  return a.dtype == SGEMM_DTYPE_F32 || a.D % 8 != 0 || a.ldw > 2LL * a.D;
+}
+// Whether a backward pass keeps dz's rounding residues (ce_dz_gemm_kernel), and
+// the rows its products take then.  Above, 128 rows or more that count bring the
+// error of dz's rounding to within a few percent of its mean, that of the
+// gradients' own rounding.
+constexpr int kResidueRows = 256;
+bool residues(const CeProblem& a) {
+  return a.dtype != SGEMM_DTYPE_F32 && a.T <= kResidueRows;
+}
+int product_rows(const CeProblem& a) { return residues(a) ? 2 * (int)round_up(a.T, kStep) : a.T; }
+long long padded_product_rows(const CeProblem& a) { return round_up(product_rows(a), kPadRows); }
 
 CeLayout packed_layout(const CeProblem& a, int backward) {
   const size_t T = (size_t)a.T, Tp = (size_t)padded_rows(a), Dp = (size_t)padded_cols(a);
-  const size_t planes = (size_t)plane_count(a);
+  const size_t planes = (size_t)plane_count(a), Rp = (size_t)padded_product_rows(a);
   CeLayout l = {16 * 256, 0};
   if (!backward) {
     l.fixed += 4 * T + 20 * Tp + 2 * planes * Tp * Dp;
     l.per_col = Tp / 8;  // eight bytes a row for 64 columns or more
   } else {
-    l.fixed += 4 * T + 24 * Tp + (a.dtype == SGEMM_DTYPE_F16 ? 4 : 2) * planes * Tp * Dp +
-               2 * kStep * 2 * (size_t)a.D + 4 * T * (size_t)sum_cols(a);
-    l.per_col = 2 * planes * Tp;
+    l.fixed += 4 * T + 24 * Tp + (a.dtype == SGEMM_DTYPE_F16 ? 4 : 2) * planes * Rp * Dp +
+               2 * kStep * 2 * (size_t)a.D + 4 * (size_t)product_rows(a) * (size_t)sum_cols(a);
+    l.per_col = 2 * planes * Rp;
   }
-  if (planes > 1) l.per_col += 2 * planes * Dp;  // W's piece in planes
+  if (copies_w(a)) l.per_col += 2 * planes * Dp;
   return l;
 }
 
 // Columns of a piece, in whole tiles, that `bytes` hold beside the rest (0:
 // not even the least).
-long long packed_columns(const CeProblem& a, const CeLayout& l, size_t bytes) {
+long long packed_columns(const CeProblem& a, int backward, const CeLayout& l, size_t bytes) {
   if (bytes < l.fixed + l.per_col * kPadCols) return 0;
   long long cols = (long long)((bytes - l.fixed) / l.per_col);
-  const long long most = (long long)(kPackedBytes / l.per_col);
+  long long most = (long long)(kPackedBytes / l.per_col);
+  if (backward) {
+    const size_t dz = 2 * (size_t)plane_count(a) * (size_t)padded_product_rows(a);
+    most = std::min(most, (long long)(kDzBytes / dz));
+  }
   if (cols > most) cols = most;
   cols = cols < kPadCols ? kPadCols : cols / kPadCols * kPadCols;
   // as many pieces as that takes, of about one size
@@ -117,26 +127,19 @@ long long packed_columns(const CeProblem& a, const CeLayout& l, size_t bytes) {
 // is split over workgroups (ce_split).  Rows that are left out make fewer
 // tiles and more splits, up to twice as many as for all rows.
 int dx_slabs(const CeProblem& a, int cus, int b) {
-  const long long tiles = up_div(a.T, b) * up_div(a.D, b);
+  const long long tiles = up_div(product_rows(a), b) * up_div(a.D, b);
   if (tiles > cus) return 1;
   const int s = ce_split((int)tiles, cus, a.V, 64, plane_count(a) > 1).splits;
   return s < 32 ? 2 * s : 64;
 }
 // Tiles of dX's product: 256 square unless one extent fits half of one.
-bool dx_big(const CeProblem& a) { return a.T > 128 && a.D > 128; }
+bool dx_big(const CeProblem& a) { return product_rows(a) > 128 && a.D > 128; }
 
+// Calls over the library's products (backward: 32-bit only).
 CeLayout layout_of(const CeProblem& a, int backward) {
-  const unsigned esz = tensor_elem_bytes(a.dtype);
-  const size_t T = (size_t)a.T, dpad = (size_t)round_up(a.D, 8);
-  CeLayout l = {0, 0};
-  if (!backward) {
-    l.fixed = 12 * T;
-    l.per_col = 4 * T;
-  } else {
-    l.fixed = 16 * T + 256 + dpad * T * esz + (esz == 2 ? 4 * dpad * T : 0);
-    l.per_col = 4 * T + (esz == 2 ? 2 * T + 4 * dpad : 0);
-  }
-  l.fixed += 16 * 256;  // boundaries, and the columns a row is padded by
+  const size_t T = (size_t)a.T;
+  CeLayout l = {16 * 256 + 12 * T, 4 * T};  // (boundaries, and padding of rows)
+  if (backward) l.fixed += 4 * T * (size_t)round_up(a.D, 8);
   return l;
 }
 
@@ -185,7 +188,8 @@ void* rows_from(void* p, size_t row, int ld, unsigned esz) {
 int validate(const CeProblem& a, const long long* labels) {
   const unsigned esz = tensor_elem_bytes(a.dtype);
   if (esz == 0) return SGEMM_ERR_VALUE;
-  if (a.T < 0 || a.V < 1 || a.D < 1 || a.D > INT_MAX - 8 || a.V > INT_MAX - 8)
+  if (a.T < 0 || a.V < 1 || a.D < 1 || a.D > SGEMM_CE_MAX_D || a.V > INT_MAX - 256 ||
+      a.T > INT_MAX - 1024)
     return SGEMM_ERR_SIZE;
   if (a.ldx < a.D || a.ldw < a.D) return SGEMM_ERR_LD;
   if (a.T == 0) return SGEMM_OK;
@@ -216,29 +220,28 @@ int zero(int rows, int D, void* out, int ldo, hipStream_t s) {
   return launched();
 }
 
-// The workspace of a call: what both ways need, so that it depends on the
-// sizes alone.
+// The workspace of a call, as its sizes alone give it: a W whose rows are far
+// apart is copied besides, in pieces as the workspace allows.
 struct CeSizes {
   size_t least, full;
 };
-CeSizes sizes_of(const CeProblem& a, int backward, int cus) {
-  CeLayout l = layout_of(a, backward);
-  const int small = a.V < kPieceStep ? a.V : kPieceStep;
-  const int big = piece_columns(a, l, (size_t)1 << 62);
-  CeSizes z = {l.fixed + l.per_col * (size_t)(small + 8),
-               l.fixed + l.per_col * (size_t)(big + 8) + kProductBytes};
-  if (packable(a)) {
-    l = packed_layout(a, backward);
-    size_t least = l.fixed + l.per_col * kPadCols;
-    if (least > z.least) z.least = least;
-    const int slabs = backward ? dx_slabs(a, cus, dx_big(a) ? 256 : 128) : 1;
-    const size_t more = 4 * (size_t)a.T * (size_t)sum_cols(a) * (slabs - 1);
-    const size_t piece = l.per_col * (size_t)packed_columns(a, l, (size_t)1 << 62);
-    // (spare room is shared between slabs and the piece)
-    const size_t full = l.fixed + l.per_col * kPadCols + (2 * more > more + piece ? 2 * more : more + piece);
-    if (full > z.full) z.full = full;
+CeSizes sizes_of(CeProblem a, int backward, int cus) {
+  a.ldw = a.D;
+  if (!packed(a, backward)) {
+    const CeLayout l = layout_of(a, backward);
+    const int small = a.V < kPieceStep ? a.V : kPieceStep;
+    const int big = piece_columns(a, l, (size_t)1 << 62);
+    return CeSizes{l.fixed + l.per_col * (size_t)(small + 8),
+                   l.fixed + l.per_col * (size_t)(big + 8) + kProductBytes};
   }
-  return z;
+  const CeLayout l = packed_layout(a, backward);
+  size_t base = l.fixed + l.per_col * kPadCols;
+  if (!copies_w(a)) base += 2 * kPadCols * (size_t)padded_cols(a);
+  const int slabs = backward ? dx_slabs(a, cus, dx_big(a) ? 256 : 128) : 1;
+  const size_t more = 4 * (size_t)product_rows(a) * (size_t)sum_cols(a) * (slabs - 1);
+  const size_t piece = l.per_col * (size_t)packed_columns(a, backward, l, (size_t)1 << 62);
+  // (spare room is shared between slabs and the piece)
+  return CeSizes{base, base + (2 * more > more + piece ? 2 * more : more + piece)};
 }
 
 // ---- launches on packed rows -----------------------------------------------------
@@ -285,11 +288,11 @@ int launch_logits(const CePiece& p, const int* label, int v0, CeRow* part, int r
 
 template <class T, int DT, int MODE>
 int launch_dz(const CePiece& p, const CeRowInfo* info, int v0, uint16_t* dz, int lddz, int plane,
-              hipStream_t s) {
+              int residue_rows, hipStream_t s) {
   if (!grid_fits(p)) return SGEMM_ERR_UNSUPPORTED;
   const int n = p.tiles_m * p.tiles_n;
   hipLaunchKernelGGL((ce_dz_gemm_kernel<T, DT, MODE>), dim3(n), dim3(T::THREADS), 0, s, p.gemm,
-                     p.tiles_n, info, v0, dz, lddz, plane);
+                     p.tiles_n, info, v0, dz, lddz, plane, residue_rows);
   return launched();
 }
 
@@ -346,31 +349,34 @@ int logits_piece(const CeProblem& a, int n, const CeOperands& o, const int* labe
   if constexpr (DT == SGEMM_DTYPE_F32)
     return launch_logits<T, MT, MODE_PLANES>(p, label, v0, part, rows, zlabel, s);
   else
-    return n % T::BN == 0 && a.D % kStep == 0
+    return copies_w(a) || (n % T::BN == 0 && a.D % kStep == 0)
                ? launch_logits<T, MT, MODE_ALIGNED>(p, label, v0, part, rows, zlabel, s)
                : launch_logits<T, MT, MODE_PADDED>(p, label, v0, part, rows, zlabel, s);
 }
 
-// X's packed rows (for 32-bit X in planes), their stride in *ldx.
+// X's packed rows (for 32-bit X in planes), their stride in *ldx; with
+// residue_rows each also at its residue's row.
 template <int DT>
-int pack_rows(const CeProblem& a, const int* pos, const int* count, const float* x_factor,
-              void* plain, void* scaled, int dp, int* ldx, hipStream_t s) {
-  const unsigned g = grid_of((unsigned long long)(a.T + CE_ROW_PAD) * (unsigned)(dp / 8));
+int pack_rows(const CeProblem& a, const int* pos, const int* count, bool residue_rows,
+              const float* x_factor, void* plain, void* scaled, int dp, int* ldx, hipStream_t s) {
+  const int tail = residue_rows ? (int)padded_product_rows(a) : CE_ROW_PAD;
+  const unsigned g = grid_of((unsigned long long)(a.T + tail) * (unsigned)(dp / 8));
   if (g == 0) return SGEMM_ERR_UNSUPPORTED;
   if constexpr (DT == SGEMM_DTYPE_F32) {
     *ldx = 3 * dp;
-    hipLaunchKernelGGL(ce_planes_kernel, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.T + CE_ROW_PAD, a.D,
+    hipLaunchKernelGGL(ce_planes_kernel, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.T + tail, a.D,
                        static_cast<const float*>(a.X), a.ldx, pos, count,
                        static_cast<uint16_t*>(plain), dp);
   } else {
     *ldx = dp;
-    hipLaunchKernelGGL(ce_gather_kernel<DT>, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D, a.X, a.ldx,
-                       pos, count, x_factor, plain, scaled, dp);
+    hipLaunchKernelGGL(ce_gather_kernel<DT>, dim3(g), dim3(CE_THREADS), 0, s, a.T, tail, a.D, a.X,
+                       a.ldx, pos, count, (int)residue_rows, x_factor, plain, scaled, dp);
   }
   return launched();
 }
 
-// The piece of W from row v0 on, n rows: in place, or in planes at `copy`.
+// The piece of W from row v0 on, n rows: in place, or copied to whole tiles
+// (zeros after the last row: they meet dz's zeros).
 template <int DT>
 int piece_of_w(const CeProblem& a, long long v0, int n, void* copy, int dp, CeOperands* o,
                hipStream_t s) {
@@ -378,26 +384,31 @@ int piece_of_w(const CeProblem& a, long long v0, int n, void* copy, int dp, CeOp
   o->w = w;
   o->ldw = a.ldw;
   o->plane = 0;
+  if (!copies_w(a)) return SGEMM_OK;
+  const int rows = (int)round_up(n, kPadCols);
+  const unsigned g = grid_of((unsigned long long)rows * (unsigned)(dp / 8));
+  if (g == 0) return SGEMM_ERR_UNSUPPORTED;
+  o->w = copy;
   if constexpr (DT == SGEMM_DTYPE_F32) {
-    const int rows = (int)round_up(n, kPadCols);  // zeros after the last: they meet dz's zeros
-    const unsigned g = grid_of((unsigned long long)rows * (unsigned)(dp / 8));
-    if (g == 0) return SGEMM_ERR_UNSUPPORTED;
     hipLaunchKernelGGL(ce_planes_kernel, dim3(g), dim3(CE_THREADS), 0, s, n, rows, a.D,
                        static_cast<const float*>(w), a.ldw, static_cast<const int*>(nullptr),
                        static_cast<const int*>(nullptr), static_cast<uint16_t*>(copy), dp);
-    o->w = copy;
     o->ldw = 3 * dp;
     o->plane = dp;
-    return launched();
+  } else {
+    hipLaunchKernelGGL(ce_gather_kernel<DT>, dim3(g), dim3(CE_THREADS), 0, s, n, rows - n, a.D, w,
+                       a.ldw, static_cast<const int*>(nullptr), static_cast<const int*>(nullptr), 0,
+                       static_cast<const float*>(nullptr), copy, static_cast<void*>(nullptr), dp);
+    o->ldw = dp;
   }
-  return SGEMM_OK;
+  return launched();
 }
 
 template <int DT>
 int packed_forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
                    float* loss, float* lse, hipStream_t s) {
   const int Tp = (int)padded_rows(a), dp = (int)padded_cols(a), planes = plane_count(a);
-  const long long cols = packed_columns(a, packed_layout(a, 0), h->workspace_bytes);
+  const long long cols = packed_columns(a, 0, packed_layout(a, 0), h->workspace_bytes);
   if (cols == 0) return SGEMM_ERR_SCRATCH;
   Carver c = {static_cast<char*>(h->workspace)};
   int* count = c.take<int>(4);
@@ -407,14 +418,14 @@ int packed_forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& 
   float* zlabel = c.take<float>(4 * (size_t)Tp);
   CeRow* state = c.take<CeRow>(sizeof(CeRow) * (size_t)Tp);
   void* xp = c.take<char>(2 * (size_t)planes * Tp * dp);
-  void* wp = c.take<char>(planes > 1 ? 2 * (size_t)planes * cols * dp : 0);
+  void* wp = c.take<char>(copies_w(a) ? 2 * (size_t)planes * cols * dp : 0);
   CeRow* part = c.take<CeRow>(0);
   hipLaunchKernelGGL(ce_pack_kernel, dim3(1), dim3(CE_PACK_THREADS), 0, s, a.T, Tp, labels, pos,
                      order, label, count, loss, lse);
   int st = launched();
   if (st != SGEMM_OK) return st;
   CeOperands o = {xp, 0, nullptr, 0, 0, count};
-  st = pack_rows<DT>(a, pos, count, nullptr, xp, nullptr, dp, &o.ldx, s);
+  st = pack_rows<DT>(a, pos, count, false, nullptr, xp, nullptr, dp, &o.ldx, s);
   if (st != SGEMM_OK) return st;
   for (long long v0 = 0; v0 < a.V; v0 += cols) {
     const int n = (int)(a.V - v0 < cols ? a.V - v0 : cols);
@@ -447,11 +458,11 @@ int dz_piece(const CeProblem& a, int n, const CeOperands& o, const CeRowInfo* in
   const CePiece p = piece_of<T>(a, a.T, n, a.D, a.alpha * CE_LOG2E, o.x, o.ldx, o.w, o.ldw, o.count,
                                 LpPlanes{o.plane, o.plane});
   if constexpr (DT == SGEMM_DTYPE_F32)
-    return launch_dz<T, MT, MODE_PLANES>(p, info, v0, d.dz, 3 * d.lddz, d.lddz, s);
+    return launch_dz<T, MT, MODE_PLANES>(p, info, v0, d.dz, 3 * d.lddz, d.lddz, 0, s);
   else
-    return n % T::BN == 0 && a.D % kStep == 0
-               ? launch_dz<T, MT, MODE_ALIGNED>(p, info, v0, d.dz, d.lddz, 0, s)
-               : launch_dz<T, MT, MODE_PADDED>(p, info, v0, d.dz, d.lddz, 0, s);
+    return copies_w(a) || (n % T::BN == 0 && a.D % kStep == 0)
+               ? launch_dz<T, MT, MODE_ALIGNED>(p, info, v0, d.dz, d.lddz, 0, residues(a), s)
+               : launch_dz<T, MT, MODE_PADDED>(p, info, v0, d.dz, d.lddz, 0, residues(a), s);
 }
 
 // dX's sums: `slabs` of `slab` elements, rows of lds.
@@ -467,14 +478,14 @@ int dx_piece(const CeProblem& a, int n, const CeOperands& o, const CeDz& d, int 
              const void* w_tail, const CeSums& x, float beta, hipStream_t s) {
   constexpr int MT = product_type(DT);
   constexpr bool WIDE = DT == SGEMM_DTYPE_F32;
-  CePiece p = piece_of<T>(a, a.T, a.D, n, 0.0f, d.dz, WIDE ? 3 * d.lddz : d.lddz, o.w, o.ldw,
-                          o.count, LpPlanes{d.lddz, o.plane});
+  CePiece p = piece_of<T>(a, product_rows(a), a.D, n, 0.0f, d.dz, WIDE ? 3 * d.lddz : d.lddz, o.w,
+                          o.ldw, o.count + 1, LpPlanes{d.lddz, o.plane});
   p.gemm.g.beta = beta;
   p.gemm.g.ldc = x.lds;
   if constexpr (WIDE)
     return launch_dx<T, MT, MODE_PLANES>(p, cus, x.slabs, x.n_first, nullptr, x.sums, x.slab, s);
   else
-    return a.D % T::BN == 0 && n % kStep == 0
+    return copies_w(a) || (a.D % T::BN == 0 && n % kStep == 0)
                ? launch_dx<T, MT, MODE_ALIGNED>(p, cus, x.slabs, x.n_first, nullptr, x.sums, x.slab, s)
                : launch_dx<T, MT, MODE_PADDED>(p, cus, x.slabs, x.n_first,
                                                n % kStep != 0 ? w_tail : nullptr, x.sums, x.slab, s);
@@ -485,8 +496,8 @@ int dw_piece(const CeProblem& a, int n, const CeDz& d, const void* xs, int ldxs,
              const int* count, const float* factor, void* out, int ldo, hipStream_t s) {
   constexpr int MT = product_type(DT);
   constexpr bool WIDE = DT == SGEMM_DTYPE_F32;
-  const CePiece p = piece_of<T>(a, n, a.D, (int)padded_rows(a), 0.0f, d.dz,
-                                WIDE ? 3 * d.lddz : d.lddz, xs, ldxs, count, LpPlanes{d.lddz, dp});
+  const CePiece p = piece_of<T>(a, n, a.D, product_rows(a), 0.0f, d.dz, WIDE ? 3 * d.lddz : d.lddz,
+                                xs, ldxs, count + 1, LpPlanes{d.lddz, dp});
   return launch_dw<T, MT, WIDE ? MODE_PLANES : MODE_ALIGNED>(p, factor, out, ldo, s);
 }
 
@@ -494,13 +505,14 @@ template <int DT>
 int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
                     const float* lse, const float* dloss, const float* dlse, void* dX, int lddx,
                     void* dW, int lddw, hipStream_t s) {
-  constexpr bool SCALED = DT == SGEMM_DTYPE_F16;
+  constexpr bool UNIT = DT != SGEMM_DTYPE_F32, SCALED = DT == SGEMM_DTYPE_F16;
   const unsigned esz = tensor_elem_bytes(DT);
   const int Tp = (int)padded_rows(a), dp = (int)padded_cols(a), planes = plane_count(a);
+  const size_t Rp = (size_t)padded_product_rows(a);
   CeLayout l = packed_layout(a, 1);
   CeSums x = {};
   x.lds = (int)sum_cols(a);
-  x.slab = (size_t)a.T * x.lds;
+  x.slab = (size_t)product_rows(a) * x.lds;
   const size_t least = l.fixed + l.per_col * kPadCols;
   if (h->workspace_bytes < least) return SGEMM_ERR_SCRATCH;
   // half of what is left over the least may go to slabs of dX's sums
@@ -509,7 +521,7 @@ int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels&
   const size_t spare = (h->workspace_bytes - least) / 2 / (4 * x.slab);
   if (x.slabs > 1 && (size_t)(x.slabs - 1) > spare) x.slabs = 1 + (int)spare;
   l.fixed += 4 * x.slab * (x.slabs - 1);
-  const long long cols = packed_columns(a, l, h->workspace_bytes);
+  const long long cols = packed_columns(a, 1, l, h->workspace_bytes);
   if (cols == 0) return SGEMM_ERR_SCRATCH;
   x.n_first = (int)(a.V < cols ? a.V : cols);
 
@@ -520,24 +532,25 @@ int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels&
   CeRowInfo* info = c.take<CeRowInfo>(sizeof(CeRowInfo) * (size_t)Tp);
   float* x_factor = c.take<float>(4 * (size_t)Tp);
   float* out_factor = c.take<float>(4 * (size_t)Tp);
-  void* xp = c.take<char>(2 * (size_t)planes * Tp * dp);
+  void* xp = c.take<char>(2 * (size_t)planes * Rp * dp);
   // (only binary16 rows are scaled: else one copy serves both products)
-  void* xs = SCALED ? c.take<char>(2 * (size_t)Tp * dp) : xp;
-  void* w_tail = c.take<char>(planes > 1 ? 0 : 2 * (size_t)kStep * a.ldw);
+  void* xs = SCALED ? c.take<char>(2 * Rp * dp) : xp;
+  const bool tail = dX != nullptr && !copies_w(a) && a.V % kStep != 0;
+  void* w_tail = c.take<char>(tail ? 2 * (size_t)kStep * a.ldw : 0);
   x.sums = c.take<float>(4 * x.slab * x.slabs);
-  void* wp = c.take<char>(planes > 1 ? 2 * (size_t)planes * cols * dp : 0);
+  void* wp = c.take<char>(copies_w(a) ? 2 * (size_t)planes * cols * dp : 0);
   const CeDz d = {c.take<uint16_t>(0), (int)cols};
 
-  hipLaunchKernelGGL(ce_pack_factors_kernel<SCALED>, dim3(1), dim3(CE_PACK_THREADS), 0, s, a.T, Tp,
-                     a.alpha, labels, lse, dloss, dlse, pos, info, x_factor, out_factor, dw_factor,
-                     count);
+  hipLaunchKernelGGL((ce_pack_factors_kernel<UNIT, SCALED>), dim3(1), dim3(CE_PACK_THREADS), 0, s,
+                     a.T, Tp, a.alpha, labels, lse, dloss, dlse, (int)residues(a), pos, info,
+                     x_factor, out_factor, dw_factor, count);
   int st = launched();
   if (st != SGEMM_OK) return st;
   CeOperands o = {xp, 0, nullptr, 0, 0, count};
-  st = pack_rows<DT>(a, pos, count, x_factor, xp, SCALED ? xs : nullptr, dp, &o.ldx, s);
+  st = pack_rows<DT>(a, pos, count, residues(a), x_factor, xp, SCALED ? xs : nullptr, dp, &o.ldx, s);
   if (st != SGEMM_OK) return st;
   if constexpr (DT != SGEMM_DTYPE_F32) {
-    if (dX != nullptr && a.V % kStep != 0) {
+    if (tail) {
       const int rows = a.V % kStep;
       hipLaunchKernelGGL(ce_tail_kernel<DT>, dim3(grid_of((unsigned long long)kStep * (a.D / 8))),
                          dim3(CE_THREADS), 0, s, rows, a.D,
@@ -573,11 +586,11 @@ int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels&
   if (bigx)
     hipLaunchKernelGGL((ce_dx_rows_kernel<L256x256, DT>), dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D,
                        count, pos, x.sums, x.lds, x.slab, (int)up_div(a.D, 256), h->cus, x.slabs,
-                       x.n_first, out_factor, dX, lddx);
+                       x.n_first, (int)residues(a), out_factor, dX, lddx);
   else
     hipLaunchKernelGGL((ce_dx_rows_kernel<L128x128, DT>), dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D,
                        count, pos, x.sums, x.lds, x.slab, (int)up_div(a.D, 128), h->cus, x.slabs,
-                       x.n_first, out_factor, dX, lddx);
+                       x.n_first, (int)residues(a), out_factor, dX, lddx);
   return launched();
 }
 
@@ -614,89 +627,65 @@ int forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
   return SGEMM_OK;
 }
 
-template <int DT>
-int backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
-             const float* lse, const float* dloss, const float* dlse, void* dX, int lddx,
-             void* dW, int lddw, hipStream_t s) {
-  constexpr bool WIDE = DT == SGEMM_DTYPE_F32;  // 32-bit gradients are their own sums
-  constexpr unsigned esz = WIDE ? 4 : 2;
-  if (packed(a, 1))
-    return packed_backward<DT>(h, a, labels, lse, dloss, dlse, dX, lddx, dW, lddw, s);
+// 32-bit, few rows: z in place becomes dz, and the gradients are their own
+// sums.
+int backward32(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
+               const float* lse, const float* dloss, const float* dlse, float* dX, int lddx,
+               float* dW, int lddw, hipStream_t s) {
+  constexpr int DT = SGEMM_DTYPE_F32;
   const CeLayout l = layout_of(a, 1);
   const int cols = piece_columns(a, l, h->workspace_bytes);
   if (cols == 0) return SGEMM_ERR_SCRATCH;
   const int ldz = (int)round_up(cols, 8), dpad = (int)round_up(a.D, 8);
   const size_t T = (size_t)a.T;
   Carver c = {static_cast<char*>(h->workspace)};
-  CeFactors* factors = c.take<CeFactors>(sizeof(CeFactors) * T);
-  float* dw_factor = c.take<float>(4);
-  void* xs = c.take<char>(T * dpad * esz);
-  float* sum_x = WIDE ? static_cast<float*>(dX) : c.take<float>(4 * T * dpad);
-  const int ld_sum_x = WIDE ? lddx : dpad;
+  float* xs = c.take<float>(4 * T * dpad);
   float* z = c.take<float>(4 * T * ldz);
-  void* dz = WIDE ? static_cast<void*>(z) : c.take<char>(2 * T * ldz);
-  float* sum_w = WIDE ? nullptr : c.take<float>(4 * (size_t)cols * dpad);
   const size_t left = h->workspace_bytes - c.used;
   sgemm_handle_s ph = product_handle(h, c.base + c.used, left < kProductBytes ? left : kProductBytes);
-
-  hipLaunchKernelGGL(ce_factors_kernel<DT == SGEMM_DTYPE_F16>, dim3(1), dim3(CE_FACTOR_THREADS), 0,
-                     s, a.T, a.alpha, labels, dloss, dlse, factors, dw_factor);
-  int st = launched();
-  if (st != SGEMM_OK) return st;
+  int st;
   if (dW != nullptr) {
     const unsigned g = grid_of(T * (unsigned long long)(dpad / 8));
     if (g == 0) return SGEMM_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL(ce_rows_kernel<DT>, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D, a.X, a.ldx,
-                       factors, xs, dpad);
+    hipLaunchKernelGGL(ce_rows_kernel, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D,
+                       static_cast<const float*>(a.X), a.ldx, labels, dloss, dlse, xs, dpad);
     st = launched();
     if (st != SGEMM_OK) return st;
   }
-  const float scale = WIDE ? a.alpha : 1.0f;
   for (int v0 = 0; v0 < a.V; v0 += cols) {
     const int n = a.V - v0 < cols ? a.V - v0 : cols;
-    const void* w = rows_from(a.W, v0, a.ldw, esz);
+    const void* w = rows_from(a.W, v0, a.ldw, 4);
     st = product(&ph, DT, SGEMM_OP_N, SGEMM_OP_T, a.T, n, a.D, a.alpha, a.X, a.ldx, w, a.ldw, 0.0f,
                  z, ldz, s);
     if (st != SGEMM_OK) return st;
-    // (a grid's second extent holds 65535 rows at most)
-    for (int t0 = 0; t0 < a.T; t0 += 65535) {
-      const int rows = a.T - t0 < 65535 ? a.T - t0 : 65535;
-      CeLabels part = labels;
-      part.label += t0;
-      hipLaunchKernelGGL(ce_dz_kernel<DT>, dim3((unsigned)up_div(n, 8 * CE_THREADS), rows),
-                         dim3(CE_THREADS), 0, s, z + (size_t)t0 * ldz, ldz, n, v0, part, lse + t0,
-                         factors + t0, rows_from(dz, t0, ldz, esz), ldz);
-      st = launched();
-      if (st != SGEMM_OK) return st;
-    }
+    hipLaunchKernelGGL(ce_dz_kernel, dim3((unsigned)up_div(n, 8 * CE_THREADS), a.T),
+                       dim3(CE_THREADS), 0, s, z, ldz, n, v0, labels, lse, dloss, dlse);
+    st = launched();
+    if (st != SGEMM_OK) return st;
     if (dX != nullptr) {
-      st = product(&ph, DT, SGEMM_OP_N, SGEMM_OP_N, a.T, a.D, n, scale, dz, ldz, w, a.ldw,
-                   v0 == 0 ? 0.0f : 1.0f, sum_x, ld_sum_x, s);
+      st = product(&ph, DT, SGEMM_OP_N, SGEMM_OP_N, a.T, a.D, n, a.alpha, z, ldz, w, a.ldw,
+                   v0 == 0 ? 0.0f : 1.0f, dX, lddx, s);
       if (st != SGEMM_OK) return st;
     }
     if (dW != nullptr) {
-      void* out = rows_from(dW, v0, lddw, esz);
-      st = product(&ph, DT, SGEMM_OP_T, SGEMM_OP_N, n, a.D, a.T, scale, dz, ldz, xs, dpad, 0.0f,
-                   WIDE ? static_cast<float*>(out) : sum_w, WIDE ? lddw : dpad, s);
+      st = product(&ph, DT, SGEMM_OP_T, SGEMM_OP_N, n, a.D, a.T, a.alpha, z, ldz, xs, dpad, 0.0f,
+                   dW + (size_t)v0 * lddw, lddw, s);
       if (st != SGEMM_OK) return st;
-      if (!WIDE) {
-        const unsigned g = grid_of((unsigned long long)n * (dpad / 8));
-        if (g == 0) return SGEMM_ERR_UNSUPPORTED;
-        hipLaunchKernelGGL(ce_grad_kernel<DT>, dim3(g), dim3(CE_THREADS), 0, s, n, a.D, sum_w, dpad,
-                           static_cast<const CeFactors*>(nullptr), dw_factor, out, lddw);
-        st = launched();
-        if (st != SGEMM_OK) return st;
-      }
     }
   }
-  if (dX != nullptr && !WIDE) {
-    const unsigned g = grid_of(T * (unsigned long long)(dpad / 8));
-    if (g == 0) return SGEMM_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL(ce_grad_kernel<DT>, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D, sum_x, dpad,
-                       factors, static_cast<const float*>(nullptr), dX, lddx);
-    st = launched();
-  }
-  return st;
+  return SGEMM_OK;
+}
+
+template <int DT>
+int backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
+             const float* lse, const float* dloss, const float* dlse, void* dX, int lddx,
+             void* dW, int lddw, hipStream_t s) {
+  if (a.T == 0) return zero<DT>(a.V, a.D, dW, lddw, s);
+  if (h->workspace_bytes < sizes_of(a, 1, h->cus).least) return SGEMM_ERR_SCRATCH;
+  if (packed(a, 1))
+    return packed_backward<DT>(h, a, labels, lse, dloss, dlse, dX, lddx, dW, lddw, s);
+  return backward32(h, a, labels, lse, dloss, dlse, static_cast<float*>(dX), lddx,
+                    static_cast<float*>(dW), lddw, s);
 }
 
 }  // namespace
@@ -708,7 +697,8 @@ int sgemm_ce_workspace_size(sgemm_handle_t h, int dtype, int T, int V, int D, in
   if (h == nullptr) return SGEMM_ERR_HANDLE;
   const CeProblem a = {dtype, T, V, D, 1.0f, nullptr, D, nullptr, D};
   if (tensor_elem_bytes(dtype) == 0) return SGEMM_ERR_VALUE;
-  if (T < 0 || V < 1 || D < 1 || D > INT_MAX - 8 || V > INT_MAX - 8) return SGEMM_ERR_SIZE;
+  if (T < 0 || T > INT_MAX - 1024 || V < 1 || V > INT_MAX - 256 || D < 1 || D > SGEMM_CE_MAX_D)
+    return SGEMM_ERR_SIZE;
   const CeSizes z = sizes_of(a, backward, h->cus);
   if (least != nullptr) *least = z.least;
   if (full != nullptr) *full = z.full;
@@ -774,16 +764,12 @@ int sgemm_ce_backward(sgemm_handle_t h, int dtype, int T, int V, int D, float al
   if (st != SGEMM_OK) return st;
   const CeProblem a = {dtype, T, V, D, alpha, X, ldx, W, ldw};
   const CeLabels y = {labels, ignore, V};
-  if (T > 0 && h->workspace_bytes < sizes_of(a, 1, h->cus).least) return SGEMM_ERR_SCRATCH;
   switch (dtype) {
     case SGEMM_DTYPE_F32:
-      if (T == 0) return zero<SGEMM_DTYPE_F32>(V, D, dW, lddw, stream);
       return backward<SGEMM_DTYPE_F32>(h, a, y, lse, dloss, dlse, dX, lddx, dW, lddw, stream);
     case SGEMM_DTYPE_BF16:
-      if (T == 0) return zero<SGEMM_DTYPE_BF16>(V, D, dW, lddw, stream);
       return backward<SGEMM_DTYPE_BF16>(h, a, y, lse, dloss, dlse, dX, lddx, dW, lddw, stream);
     default:
-      if (T == 0) return zero<SGEMM_DTYPE_F16>(V, D, dW, lddw, stream);
       return backward<SGEMM_DTYPE_F16>(h, a, y, lse, dloss, dlse, dX, lddx, dW, lddw, stream);
   }
 }

@@ -123,140 +123,65 @@ static __global__ void __launch_bounds__(CE_THREADS)
   }
 }
 
-// ---- backward ---------------------------------------------------------------------
+// ---- backward over the library's products (32-bit X and W, few rows) ----------------
 
-// A row's factors: dz = p * exp(z - lse) - q [v = label]; `x` scales the row
-// of X in dW's product and `out` the row of dX.  (See ce_factors_kernel.)
+// A row's factors: dz = p * exp(z - lse) - q [v = label]; both 0 for a row
+// that counts for nothing.
 struct CeFactors {
-  float p, q, x, out;
+  float p, q;
 };
-
-// The rows' factors, one workgroup for all rows.  32-bit and bfloat16: p =
-// dloss + dlse, q = dloss, x = 1, out = alpha, and dW's factor is alpha.
-// binary16 (SCALED) holds dz between its limits by a power of two a row:
-// with 2^k <= max(|p|, |q|) < 2^(k+1), p and q are scaled by 2^(13-k) (so
-// |dz| < 2^15, and a probability keeps all its bits down to 2^-27), dX's rows
-// by 2^(k-13) in 32 bits, and X's rows by 2^(k-kmax), exactly but for values
-// that the largest row's outweigh by 2^24.  Rows that count for nothing get
-// zeros.
-constexpr int CE_FACTOR_THREADS = 1024;
-template <bool SCALED>
-__global__ void __launch_bounds__(CE_FACTOR_THREADS)
-    ce_factors_kernel(int T, float alpha, CeLabels labels, const float* __restrict__ dloss,
-                      const float* __restrict__ dlse, CeFactors* __restrict__ factors,
-                      float* __restrict__ dw_factor) {
-  __shared__ int top[CE_FACTOR_THREADS / 64];
-  constexpr int NONE = -1000;
-  auto grads = [&](int t, float& p, float& q) {
-    const int y = ce_label(labels, t);
-    q = y == CE_IGNORED ? 0.0f : y == CE_BAD ? NAN : dloss[t];
-    p = y == CE_IGNORED ? 0.0f : dlse != nullptr ? q + dlse[t] : q;
-  };
-  auto exponent = [&](float p, float q) {
-    const float r = fmaxf(fabsf(p), fabsf(q));
-    return r > 0.0f && r < INFINITY ? ilogbf(r) : NONE;
-  };
-  int kmax = NONE;
-  if (SCALED) {
-    for (int t = threadIdx.x; t < T; t += CE_FACTOR_THREADS) {
-      float p, q;
-      grads(t, p, q);
-      kmax = max(kmax, exponent(p, q));
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) kmax = max(kmax, __shfl_xor(kmax, d));
-    if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = kmax;
-    __syncthreads();
-    for (int w = 0; w < CE_FACTOR_THREADS / 64; ++w) kmax = max(kmax, top[w]);
-    if (kmax == NONE) kmax = 13;
-  }
-  for (int t = threadIdx.x; t < T; t += CE_FACTOR_THREADS) {
-    CeFactors f;
-    grads(t, f.p, f.q);
-    const bool counts = !(f.p == 0.0f && f.q == 0.0f);
-    f.x = counts ? 1.0f : 0.0f;
-    f.out = alpha;
-    if (SCALED) {
-      const int k = exponent(f.p, f.q);
-      if (k != NONE) {
-        f.p = ldexpf(f.p, 13 - k);
-        f.q = ldexpf(f.q, 13 - k);
-        f.x = ldexpf(1.0f, k - kmax);
-        f.out = ldexpf(alpha, k - 13);
-      }
-    }
-    factors[t] = f;
-  }
-  if (threadIdx.x == 0) *dw_factor = SCALED ? ldexpf(alpha, kmax - 13) : alpha;
+__device__ __forceinline__ CeFactors ce_row_factors(int t, int label, const float* dloss,
+                                                    const float* dlse) {
+  CeFactors f = {0.0f, 0.0f};
+  if (label == CE_IGNORED) return f;
+  f.q = label == CE_BAD ? NAN : dloss[t];
+  f.p = dlse != nullptr ? f.q + dlse[t] : f.q;
+  return f;
+}
+__device__ __forceinline__ bool ce_counts(const CeFactors& f) {
+  return !(f.p == 0.0f && f.q == 0.0f);
 }
 
-// X's rows scaled by their factor, rows of zeros where it is 0 (so nothing of
-// a row that is left out, not even a NaN, meets dW's sums).  Eight columns a
-// lane; the copy's stride is a multiple of eight.
-template <int DT>
-__global__ void __launch_bounds__(CE_THREADS)
-    ce_rows_kernel(int T, int D, const void* X, int ldx, const CeFactors* __restrict__ factors,
-                   void* copy, int ldcopy) {
-  typedef typename TensorElem<DT>::type E;
+// X's rows, zeros where a row counts for nothing (so nothing of it, not even a
+// NaN, meets dW's sums).  Eight columns a lane; the copy's stride is a multiple
+// of eight.
+static __global__ void __launch_bounds__(CE_THREADS)
+    ce_rows_kernel(int T, int D, const float* __restrict__ X, int ldx, CeLabels labels,
+                   const float* __restrict__ dloss, const float* __restrict__ dlse,
+                   float* __restrict__ copy, int ldcopy) {
   const unsigned units = (unsigned)ldcopy / 8u;
   const unsigned long long at = (unsigned long long)blockIdx.x * CE_THREADS + threadIdx.x;
   const unsigned long long t = at / units;
-  const unsigned c = 8u * (unsigned)(at % units);
+  const int c = 8 * (int)(at % units);
   if (t >= (unsigned long long)T) return;
-  const float f = factors[t].x;
+  const bool counts = ce_counts(ce_row_factors((int)t, ce_label(labels, (int)t), dloss, dlse));
   float v[8];
-  load8<DT>(static_cast<const E*>(X) + (size_t)t * ldx + c, f != 0.0f ? D - (int)c : 0, v);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= f;
-  store8<DT>(static_cast<E*>(copy) + (size_t)t * ldcopy + c, 8, v);
+  load8<SGEMM_DTYPE_F32>(reinterpret_cast<const uint32_t*>(X) + (size_t)t * ldx + c,
+                         counts ? D - c : 0, v);
+  store8<SGEMM_DTYPE_F32>(reinterpret_cast<uint32_t*>(copy) + (size_t)t * ldcopy + c, 8, v);
 }
 
-// dz of a piece of z, columns [v0, v0 + n): rounded once to the type of X and
-// W, whose products follow (an error of half a step of each p, against sums
-// whose terms carry that step already in W and X).  32-bit dz may overwrite z.
-template <int DT>
-__global__ void __launch_bounds__(CE_THREADS)
-    ce_dz_kernel(const float* z, int ldz, int n, int v0, CeLabels labels,
-                 const float* __restrict__ lse, const CeFactors* __restrict__ factors, void* dz,
-                 int lddz) {
-  typedef typename TensorElem<DT>::type E;
+// z of a piece, columns [v0, v0 + n), turned into dz in place.
+static __global__ void __launch_bounds__(CE_THREADS)
+    ce_dz_kernel(float* __restrict__ z, int ldz, int n, int v0, CeLabels labels,
+                 const float* __restrict__ lse, const float* __restrict__ dloss,
+                 const float* __restrict__ dlse) {
   const int t = blockIdx.y;
   const int c = 8 * (blockIdx.x * CE_THREADS + threadIdx.x);
   if (c >= n) return;
-  const CeFactors f = factors[t];
-  const int y = ce_label(labels, t) - v0;
+  const int label = ce_label(labels, t);
+  const CeFactors f = ce_row_factors(t, label, dloss, dlse);
+  const bool counts = ce_counts(f);
   const float e = lse[t];
+  uint32_t* row = reinterpret_cast<uint32_t*>(z) + (size_t)t * ldz + c;
   float v[8];
-  load8<SGEMM_DTYPE_F32>(reinterpret_cast<const uint32_t*>(z) + (size_t)t * ldz + c, n - c, v);
-  const bool counts = !(f.p == 0.0f && f.q == 0.0f);
+  load8<SGEMM_DTYPE_F32>(row, n - c, v);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     v[i] = counts ? f.p * ce_exp(v[i] - e) : 0.0f;
-    if (c + i == y) v[i] -= f.q;
+    if (c + i == label - v0) v[i] -= f.q;
   }
-  store8<DT>(static_cast<E*>(dz) + (size_t)t * lddz + c, n - c, v);
-}
-
-// 32-bit sums to a gradient of type DT, times the row's factor (dX) or one
-// factor for all (dW).
-template <int DT>
-__global__ void __launch_bounds__(CE_THREADS)
-    ce_grad_kernel(int rows, int D, const float* __restrict__ sums, int lds,
-                   const CeFactors* __restrict__ factors, const float* __restrict__ factor,
-                   void* out, int ldo) {
-  typedef typename TensorElem<DT>::type E;
-  const unsigned units = ((unsigned)D + 7u) / 8u;
-  const unsigned long long at = (unsigned long long)blockIdx.x * CE_THREADS + threadIdx.x;
-  const unsigned long long r = at / units;
-  const unsigned c = 8u * (unsigned)(at % units);
-  if (r >= (unsigned long long)rows) return;
-  const float f = factors != nullptr ? factors[r].out : *factor;
-  float v[8];
-  const int n = D - (int)c;
-  load8<SGEMM_DTYPE_F32>(reinterpret_cast<const uint32_t*>(sums) + (size_t)r * lds + c, n, v);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= f;
-  store8<DT>(static_cast<E*>(out) + (size_t)r * ldo + c, n, v);
+  store8<SGEMM_DTYPE_F32>(row, n - c, v);
 }
 
 // Zeros (rows x D) in any type: a gradient with no rows to come from.
@@ -272,7 +197,7 @@ __global__ void __launch_bounds__(CE_THREADS) ce_zero_kernel(int rows, int D, vo
   store8<DT>(static_cast<E*>(out) + (size_t)r * ldo + c, D - (int)c, v);
 }
 
-// ---- packed rows (16-bit X and W) ------------------------------------------------
+// ---- packed rows ------------------------------------------------
 
 // What a packed row's product epilogues need: the factors of dz, lse * log2(e)
 // and the label (CE_IGNORED for padding rows, whose factors are 0).
@@ -332,109 +257,148 @@ static __global__ void __launch_bounds__(CE_PACK_THREADS)
   if (threadIdx.x == 0) *count = base;
 }
 
-// Backward: the packed rows' factors (see ce_factors_kernel for SCALED) as
-// info, the factors of X's rows and of dX's.
-template <bool SCALED>
+// Rows that dz's rounding residues stand in, after the packed rows' whole K
+// steps: a residue row r stands at ce_residue_row(count) + r.
+__host__ __device__ inline int ce_residue_row(int count) {
+  return ((count > 1 ? count : 1) + 63) & ~63;
+}
+
+// Backward: the packed rows' factors as info, the factors of X's rows in dW's
+// product (x), of dX's rows (out) and of dW.
+//
+// 32-bit: the factors as they are, out = alpha, dW's alpha.
+//
+// 16-bit (UNIT): dz is rounded to 16 bits, and where every row's dloss is one
+// value -- a mean's -- its rounding would be one error common to all labels'
+// terms, up to half a step of the gradient.  So dz is divided by the largest
+// |dloss| (u), which makes that value 1, and alpha * u is applied to the 32-bit
+// sums.
+//
+// binary16 (SCALED) also holds dz between its limits by a power of two a row:
+// with 2^k <= max(|p|, |q|) / u < 2^(k+1), the row is scaled by 2^(13-k) (so
+// |dz| < 2^15, and a probability keeps all its bits down to 2^-27), its row of
+// dX by 2^(k-13) in 32 bits, and its row of X in dW's product by 2^(k-kmax),
+// exactly but for values that the largest row's outweigh by 2^24.
+//
+// count[0]: the rows that count; count[1]: the rows of dX's and dW's products,
+// with the residues' (see ce_dz_gemm_kernel) if any.
+template <bool UNIT, bool SCALED>
 __global__ void __launch_bounds__(CE_PACK_THREADS)
     ce_pack_factors_kernel(int T, int padded, float alpha, CeLabels labels,
                            const float* __restrict__ lse, const float* __restrict__ dloss,
-                           const float* __restrict__ dlse, int* __restrict__ pos,
+                           const float* __restrict__ dlse, int residues, int* __restrict__ pos,
                            CeRowInfo* __restrict__ info, float* __restrict__ x_factor,
                            float* __restrict__ out_factor, float* __restrict__ dw_factor,
                            int* __restrict__ count) {
   __shared__ int wave_sum[CE_PACK_WAVES];
-  __shared__ int top[CE_PACK_WAVES];
-  constexpr int NONE = -1000;
-  auto grads = [&](int t, int y, float& p, float& q) {
-    q = y == CE_IGNORED ? 0.0f : y == CE_BAD ? NAN : dloss[t];
-    p = y == CE_IGNORED ? 0.0f : dlse != nullptr ? q + dlse[t] : q;
-  };
-  auto exponent = [&](float p, float q) {
-    const float r = fmaxf(fabsf(p), fabsf(q));
-    return r > 0.0f && r < INFINITY ? ilogbf(r) : NONE;
-  };
-  int kmax = NONE;
-  if (SCALED) {
+  __shared__ float top_q[CE_PACK_WAVES], top_r[CE_PACK_WAVES];
+  // the largest finite |q| and max(|p|, |q|)
+  float q_max = 0.0f, r_max = 0.0f;
+  if (UNIT) {
     for (int t = threadIdx.x; t < T; t += CE_PACK_THREADS) {
-      float p, q;
-      grads(t, ce_label(labels, t), p, q);
-      kmax = max(kmax, exponent(p, q));
+      const CeFactors f = ce_row_factors(t, ce_label(labels, t), dloss, dlse);
+      const float q = fabsf(f.q), r = fmaxf(fabsf(f.p), q);
+      if (q < INFINITY) q_max = fmaxf(q_max, q);
+      if (r < INFINITY) r_max = fmaxf(r_max, r);
     }
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) kmax = max(kmax, __shfl_xor(kmax, d));
-    if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = kmax;
+    for (int d = 32; d > 0; d >>= 1) {
+      q_max = fmaxf(q_max, __shfl_xor(q_max, d));
+      r_max = fmaxf(r_max, __shfl_xor(r_max, d));
+    }
+    if ((threadIdx.x & 63) == 0) {
+      top_q[threadIdx.x >> 6] = q_max;
+      top_r[threadIdx.x >> 6] = r_max;
+    }
     __syncthreads();
-    for (int w = 0; w < CE_PACK_WAVES; ++w) kmax = max(kmax, top[w]);
-    if (kmax == NONE) kmax = 13;
+    for (int w = 0; w < CE_PACK_WAVES; ++w) {
+      q_max = fmaxf(q_max, top_q[w]);
+      r_max = fmaxf(r_max, top_r[w]);
+    }
   }
+  const float unit = !UNIT ? 1.0f : q_max > 0.0f ? q_max : r_max > 0.0f ? r_max : 1.0f;
+  auto exponent = [](float r) { return r > 0.0f && r < INFINITY ? ilogbf(r) : 13; };
+  const int kmax = SCALED ? exponent(r_max / unit) : 13;
+  const float scale = alpha * unit;
   int base = 0;
   for (int t0 = 0; t0 < T; t0 += CE_PACK_THREADS) {
     const int t = t0 + threadIdx.x;
     const int y = t < T ? ce_label(labels, t) : CE_IGNORED;
-    CeRowInfo f = {0.0f, 0.0f, 0.0f, y};
-    if (t < T) grads(t, y, f.p, f.q);
+    CeFactors f = {0.0f, 0.0f};
+    if (t < T) f = ce_row_factors(t, y, dloss, dlse);
     // a row whose gradients are both 0 adds nothing to dX or dW either
-    const int at = ce_place(!(f.p == 0.0f && f.q == 0.0f), base, wave_sum);
+    const int at = ce_place(ce_counts(f), base, wave_sum);
     if (t < T) pos[t] = at;
     if (at >= 0) {
-      float x = 1.0f, out = alpha;
-      if (SCALED) {
-        const int k = exponent(f.p, f.q);
-        if (k != NONE) {
-          f.p = ldexpf(f.p, 13 - k);
-          f.q = ldexpf(f.q, 13 - k);
-          x = ldexpf(1.0f, k - kmax);
-          out = ldexpf(alpha, k - 13);
-        }
-      }
-      f.lse2 = lse[t] * CE_LOG2E;
-      info[at] = f;
-      x_factor[at] = x;
-      out_factor[at] = out;
+      if (UNIT) f.p /= unit, f.q /= unit;
+      const int k = SCALED ? exponent(fmaxf(fabsf(f.p), fabsf(f.q))) : 13;
+      info[at] = CeRowInfo{ldexpf(f.p, 13 - k), ldexpf(f.q, 13 - k), lse[t] * CE_LOG2E, y};
+      x_factor[at] = ldexpf(1.0f, k - kmax);
+      out_factor[at] = ldexpf(scale, k - 13);
     }
   }
   for (int r = base + threadIdx.x; r < padded; r += CE_PACK_THREADS)
     info[r] = CeRowInfo{0.0f, 0.0f, 0.0f, CE_IGNORED};
   if (threadIdx.x == 0) {
-    *count = base;
-    *dw_factor = SCALED ? ldexpf(alpha, kmax - 13) : alpha;
+    count[0] = base;
+    count[1] = residues ? ce_residue_row(base) + base : base;
+    *dw_factor = ldexpf(scale, kmax - 13);
   }
 }
 
-// Row t of X to packed row pos[t] (times x_factor where given, to `scaled`;
-// as it is to `plain`; either may be null), zeros in the columns from D to the
-// stride; and zero rows from *count to the end of its tile of CE_ROW_PAD rows.
-// Blocks of T + CE_ROW_PAD rows.
+// 16-bit rows of X to their packed rows (row t to pos[t], none where that is
+// negative; without pos, rows as they are) in a copy of stride ld, zeros in the
+// columns from D on and in the rows that follow: of a whole tile with pos
+// (CE_ROW_PAD), else up to `rows`.  With x_factor a second copy, `scaled`, is
+// times the row's factor.  With `residues` each packed row also stands at its
+// residue's row.  Eight columns a lane; T + tail rows of lanes.
 constexpr int CE_ROW_PAD = 256;
 template <int DT>
 __global__ void __launch_bounds__(CE_THREADS)
-    ce_gather_kernel(int T, int D, const void* X, int ldx, const int* __restrict__ pos,
-                     const int* __restrict__ count, const float* __restrict__ x_factor,
-                     void* plain, void* scaled, int ld) {
+    ce_gather_kernel(int T, int tail, int D, const void* X, int ldx, const int* __restrict__ pos,
+                     const int* __restrict__ count, int residues,
+                     const float* __restrict__ x_factor, void* plain, void* scaled, int ld) {
   typedef typename TensorElem<DT>::type E;
   const unsigned units = (unsigned)ld / 8u;
   const unsigned long long at = (unsigned long long)blockIdx.x * CE_THREADS + threadIdx.x;
   const long long t = (long long)(at / units);
   const int c = 8 * (int)(at % units);
+  if (t >= (long long)T + tail) return;
   float v[8];
-  long long r;
+  long long r = t, again = -1;  // where the row goes, and once more
   if (t < T) {
-    r = pos[t];
-    if (r < 0) return;
+    if (pos != nullptr) {
+      r = pos[t];
+      if (r < 0) return;
+      if (residues) again = ce_residue_row(*count) + r;
+    }
     load8<DT>(static_cast<const E*>(X) + (size_t)t * ldx + c, D - c, v);
   } else {
-    const int n = *count, end = ((n > 1 ? n : 1) + CE_ROW_PAD - 1) / CE_ROW_PAD * CE_ROW_PAD;
-    r = n + (t - T);
-    if (r >= end) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    if (pos != nullptr) {
+      const int n = *count;
+      if (residues) {  // every row of `tail` that no packed row takes
+        const int second = ce_residue_row(n);
+        r = t - T;
+        if (r < n || (r >= second && r < second + n)) return;
+      } else {
+        r = n + (t - T);
+        if (r >= ((n > 1 ? n : 1) + CE_ROW_PAD - 1) / CE_ROW_PAD * CE_ROW_PAD) return;
+      }
+    }
   }
-  if (plain != nullptr) store8<DT>(static_cast<E*>(plain) + (size_t)r * ld + c, 8, v);
-  if (scaled != nullptr) {
-    const float f = t < T ? x_factor[r] : 0.0f;
+  const float f = scaled != nullptr && t < T ? x_factor[r] : 0.0f;
+  for (int k = 0; k < 2; ++k) {
+    if (plain != nullptr) store8<DT>(static_cast<E*>(plain) + (size_t)r * ld + c, 8, v);
+    if (scaled != nullptr) {
+      float w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= f;
-    store8<DT>(static_cast<E*>(scaled) + (size_t)r * ld + c, 8, v);
+      for (int i = 0; i < 8; ++i) w[i] = v[i] * f;
+      store8<DT>(static_cast<E*>(scaled) + (size_t)r * ld + c, 8, w);
+    }
+    if (again < 0) return;
+    r = again;
   }
 }
 

@@ -4,8 +4,8 @@
 //
 //   ce_logits_kernel   z = X W^T, a tile's rows reduced at once to (max, sum
 //                      of exp); z itself never leaves the registers
-//   ce_dz_gemm_kernel  z again, turned into dz in the registers and stored in
-//                      16 bits for the two products that follow
+//   ce_dz_gemm_kernel  z again, turned into dz in the registers and stored
+//                      for the two products that follow
 //   ce_dx_kernel       dz W, split over the vocabulary where rows and columns
 //                      alone do not fill the device, sums kept in 32 bits
 //   ce_dw_kernel       dz^T X, stored in 16 bits
@@ -146,13 +146,17 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
 // ---- logits to dz ------------------------------------------------------------------
 
 // dz (rows of lddz elements) is written for whole tiles: zeros in columns past
-// N and in rows that count for nothing.  16-bit dz is rounded once; 32-bit dz
-// leaves in its three planes, `plane` elements apart.
+// N and in rows that count for nothing.  32-bit dz leaves in its three planes,
+// `plane` elements apart.  16-bit dz is rounded once.  Over many rows those
+// roundings average out below the gradients' own; with few rows (`residues`)
+// one label's term can be most of a gradient, and what the rounding leaves is
+// stored as rows of its own (ce_residue_row), which the gradients' products
+// take like others: they cost those little, bound by W and dW as they are.
 template <class T, int DT, int MODE>
 __global__ void __launch_bounds__(T::THREADS, T::OCC)
     ce_dz_gemm_kernel(CeGemm a, int tiles_n,
                       const CeRowInfo* __restrict__ info, int v0, uint16_t* __restrict__ dz,
-                      int lddz, int plane) {
+                      int lddz, int plane, int residues) {
   constexpr int ODT = DT == LP_BF16 ? SGEMM_DTYPE_BF16 : SGEMM_DTYPE_F16;
   constexpr int LD = T::WN + 4, LPR = T::WN / 8, RPI = 64 / LPR, NI = 32 / RPI;
   static_assert(T::WAVES * 32 * LD * 4 <= T::LDS_BYTES, "staging area");
@@ -169,6 +173,7 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
   const float c = a.c;
   float* reg = reinterpret_cast<float*>(lds) + w.wave * 32 * LD;
   const int rr = w.lane / LPR, cc = 8 * (w.lane % LPR);
+  const int second = residues ? ce_residue_row(*a.count) : 0;
   __syncthreads();  // every wave is done reading the stages
 #pragma unroll
   for (int i = 0; i < T::FM; ++i) {
@@ -227,7 +232,19 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
         for (int e = 0; e < 4; ++e)
           o[e] = (unsigned)elem_bits<ODT>(src[2 * e]) |
                  ((unsigned)elem_bits<ODT>(src[2 * e + 1]) << 16);
-        *reinterpret_cast<v4u*>(out) = o;
+        if (!residues) {
+          *reinterpret_cast<v4u*>(out) = o;
+        } else if (row + rr + t * RPI < second) {
+          *reinterpret_cast<v4u*>(out) = o;
+          v4u l;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            l[e] = (unsigned)elem_bits<ODT>(src[2 * e] - elem_value<ODT>((uint16_t)o[e])) |
+                   ((unsigned)elem_bits<ODT>(src[2 * e + 1] -
+                                             elem_value<ODT>((uint16_t)(o[e] >> 16)))
+                    << 16);
+          *reinterpret_cast<v4u*>(out + (size_t)second * lddz) = l;
+        }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -385,14 +402,16 @@ static __global__ void __launch_bounds__(CE_THREADS)
     *reinterpret_cast<v4u*>(out + (size_t)r * 3 * ld + (size_t)k * ld + c) = o[k];
 }
 
-// dX's rows: the slabs' sums of the row's packed row in slab order, times its
-// factor; zeros for rows that have none.  Eight columns a lane.
+// dX's rows: the slabs' sums of the row's packed row (and its residue's, count:
+// see ce_pack_factors_kernel) in slab order, times its factor; zeros for rows
+// that have none.  Eight columns a lane.
 template <class Tile, int DT>
 __global__ void __launch_bounds__(CE_THREADS)
     ce_dx_rows_kernel(int T, int D, const int* __restrict__ count, const int* __restrict__ pos,
                       const float* __restrict__ sums, int lds, size_t slab, int tiles_n, int cus,
-                      int most, int n_first, const float* __restrict__ out_factor, void* dX, int lddx) {
-  const int slabs = ce_split(ce_tile_rows<Tile>(count) * tiles_n, cus, n_first, most,
+                      int most, int n_first, int residues, const float* __restrict__ out_factor,
+                      void* dX, int lddx) {
+  const int slabs = ce_split(ce_tile_rows<Tile>(count + 1) * tiles_n, cus, n_first, most,
                              DT == SGEMM_DTYPE_F32)
                         .splits;
   typedef typename TensorElem<DT>::type E;
@@ -405,14 +424,17 @@ __global__ void __launch_bounds__(CE_THREADS)
   float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   if (r >= 0) {
     const float* p = sums + (size_t)r * lds + c;  // (rows of whole units)
-    for (int s = 0; s < slabs; ++s, p += slab) {
-      const v4u a = *reinterpret_cast<const v4u*>(p), b = *reinterpret_cast<const v4u*>(p + 4);
+    const size_t second = residues ? (size_t)ce_residue_row(*count) * lds : 0;
+    for (int s = 0; s < slabs; ++s, p += slab)
+      for (int k = 0; k <= residues; ++k) {
+        const float* x = p + k * second;
+        const v4u a = *reinterpret_cast<const v4u*>(x), b = *reinterpret_cast<const v4u*>(x + 4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] += __uint_as_float(a[i]);
-        v[4 + i] += __uint_as_float(b[i]);
+        for (int i = 0; i < 4; ++i) {
+          v[i] += __uint_as_float(a[i]);
+          v[4 + i] += __uint_as_float(b[i]);
+        }
       }
-    }
     const float f = out_factor[r];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= f;

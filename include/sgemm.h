@@ -528,9 +528,11 @@ int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K,
  * SGEMM_ERR_SCRATCH, and with less than `full` they take smaller pieces and
  * more launches.  Ownership, streams, errors and threading as for sgemm_run
  * with a workspace.  T == 0: nothing is read (backward: dW is set to 0).
- * SGEMM_ERR_SIZE for T < 0, V < 1 or D < 1; SGEMM_ERR_LD for a stride below D;
+ * SGEMM_ERR_SIZE for T < 0, V < 1, D < 1 or D over SGEMM_CE_MAX_D; SGEMM_ERR_LD for a stride below D;
  * SGEMM_ERR_VALUE for another dtype or a tensor not aligned to its element;
  * SGEMM_ERR_ALIAS where an output overlaps another argument. */
+
+#define SGEMM_CE_MAX_D (1 << 21)
 
 /* Workspace of a forward (backward == 0) or a backward call: the least that
  * it runs with and what it makes use of; either pointer may be NULL. */

@@ -11,7 +11,9 @@ logits are exact in any order of summation.  What is left, with u = 2^-24:
   exponential's error of its own: (V/64 + 32) u + 32 * 2^-20 relative at the
   most; with those lse is off by E = (V/64 + 32) u + 2^-14, plus |lse| 4u from
   the logarithm's result and the addition of the maximum;
-* dz: relative E + 2^-19 of p, then half a step of its type;
+* dz: relative E + 2^-19 of p, then half a step of its type (up to 256 rows of
+  16-bit operands keep what that leaves, rounded in turn: half a step of half a
+  step);
 * a gradient: that error of every dz against |W| or |X|, 4 n u of the sum of
   magnitudes of n products, and half a step of the type of the result.
   (binary16: dz and X may also lose half a step of the subnormal numbers.)"""
@@ -99,7 +101,7 @@ class Problem:
             np.where(keep[:, None], z - lse[:, None], -np.inf))
         rel = 2 * self.sum_error() + 2.0 ** -18
         ez = rel * p + 4 * U * np.abs(dz)
-        ez += half * (np.abs(dz) + ez)
+        ez += (half if self.T > 256 else half * half) * (np.abs(dz) + ez)
         ax, aw = np.abs(np.where(keep[:, None], self.x, 0.0)), np.abs(self.w)
         low_x = low_w = 0.0
         if self.dt == "f16":
@@ -268,6 +270,45 @@ def test_no_read_past_the_operands(handle, T, dt):
     p.check_forward()
     p.backward(handle)
     p.check_backward()
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("T,V,D,pad", [(4, 300, 40, 100), (70, 1300, 72, 600), (300, 777, 64, 65),
+                                       (530, 1000, 41, 300)])
+def test_rows_far_apart(handle, T, V, D, pad, dt):
+    p = Problem(T, V, D, dt, seed=8, pad=pad)
+    p.forward(handle)
+    p.check_forward()
+    p.backward(handle)
+    p.check_backward()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("T,V", [(1, 50), (1, 5000), (3, 700), (33, 2000), (256, 3000), (900, 6000)])
+def test_gradients_lose_no_more_than_their_rounding(handle, T, V, dt):
+    """Error in the 2-norm against 64 bits: that of rounding the exact
+    gradients, or, past 256 rows, sqrt(2) of it and a tenth (dz's rounding is
+    another of the same size)."""
+    D = 96
+    rng = np.random.default_rng([T, V])
+    tt = DTYPES[dt]
+    W = torch.from_numpy(rng.standard_normal((V, D)) * 2 / D ** 0.5).to(tt).cuda()
+    labels = rng.integers(0, V, T)
+    w = W.double().cpu().numpy()
+    X = torch.from_numpy(rng.standard_normal((T, D)) + 2 * rng.random((T, 1)) * w[labels]).to(tt).cuda()
+    Y = torch.from_numpy(labels).cuda()
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    dl = torch.full((T,), (1024.0 if dt == "f16" else 1.0) / (T + 0.37), device="cuda")
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    handle.ce_forward(X, W, Y, loss, lse)
+    handle.ce_backward(X, W, Y, lse, dl, dX, dW)
+    x = X.double().cpu().numpy()
+    z, _, e = ref.forward(x, w, labels)
+    want = ref.gradients(x, w, labels, ref.dlogits(z, labels, e, dl.double().cpu().numpy()))
+    for got, g in zip((dX, dW), want):
+        own = np.linalg.norm(torch.from_numpy(g).to(tt).double().numpy() - g)
+        off = np.linalg.norm(got.double().cpu().numpy() - g)
+        assert off <= (1.02 if T <= 256 else 1.1 * 2 ** 0.5) * own, (off, own)
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))

@@ -438,7 +438,7 @@ int packed_forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& 
     const int chunks = (int)up_div(n, big ? L256x256::WN : L128x128::WN);
     hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)up_div(a.T, CE_JOIN_ROWS)),
                        dim3(CE_JOIN_ROWS * CE_JOIN_LANES), 0, s, part, chunks, Tp, count, order,
-                       label, state, zlabel, v0 == 0, v0 + n == a.V, loss, lse);
+                       label, state, a.alpha * CE_LOG2E, zlabel, v0 == 0, v0 + n == a.V, loss, lse);
     st = launched();
     if (st != SGEMM_OK) return st;
   }
@@ -614,13 +614,17 @@ int forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
   float* z = c.take<float>(4 * (size_t)a.T * ldz);
   const size_t left = h->workspace_bytes - c.used;
   sgemm_handle_s ph = product_handle(h, c.base + c.used, left < kProductBytes ? left : kProductBytes);
+  const auto stats = a.dtype == SGEMM_DTYPE_F32    ? ce_stats_kernel<SGEMM_DTYPE_F32>
+                     : a.dtype == SGEMM_DTYPE_BF16 ? ce_stats_kernel<SGEMM_DTYPE_BF16>
+                                                   : ce_stats_kernel<SGEMM_DTYPE_F16>;
+  const CeInputs in = {a.X, a.ldx, a.W, a.ldw, a.D, a.alpha};
   for (int v0 = 0; v0 < a.V; v0 += cols) {
     const int n = a.V - v0 < cols ? a.V - v0 : cols;
     const int st = product(&ph, a.dtype, SGEMM_OP_N, SGEMM_OP_T, a.T, n, a.D, a.alpha, a.X, a.ldx,
                            rows_from(a.W, v0, a.ldw, esz), a.ldw, 0.0f, z, ldz, s);
     if (st != SGEMM_OK) return st;
-    hipLaunchKernelGGL(ce_stats_kernel, dim3(a.T), dim3(CE_THREADS), 0, s, z, ldz, n, v0, labels,
-                       state, zlabel, v0 == 0, n == a.V - v0, loss, lse);
+    hipLaunchKernelGGL(stats, dim3(a.T), dim3(CE_THREADS), 0, s, z, ldz, n, v0, labels, in, state,
+                       zlabel, v0 == 0, n == a.V - v0, loss, lse);
     const int e = launched();
     if (e != SGEMM_OK) return e;
   }

@@ -63,25 +63,36 @@ __device__ __forceinline__ int ce_label(const CeLabels& s, int t) {
   return y >= 0 && y < s.V ? (int)y : CE_BAD;
 }
 
-// The last step of a forward pass for row t.
-__device__ __forceinline__ void ce_write_loss(int label, CeRow r, float zlabel, int t,
-                                              float* loss, float* lse) {
-  const float e = r.m + logf(r.l);
-  lse[t] = label == CE_IGNORED ? 0.0f : e;
-  loss[t] = label == CE_IGNORED ? 0.0f : label == CE_BAD ? NAN : e - zlabel;
-}
-
 constexpr int CE_THREADS = 256;
 constexpr int CE_WAVES = CE_THREADS / 64;
+
+// X and W as a forward pass over the library's products reads them again.
+struct CeInputs {
+  const void* X;
+  int ldx;
+  const void* W;
+  int ldw, D;
+  float alpha;
+};
 
 // Joins columns [v0, v0 + n) of a piece of z (T rows of stride ldz, 16-byte
 // aligned) into the rows' state, one workgroup a row; the last piece writes
 // loss and lse.
-static __global__ void __launch_bounds__(CE_THREADS)
+//
+// With few rows an error of z, though only a unit or two in its last place,
+// is not averaged out by others: where the label is nearly certain, the
+// loss's relative error is z's absolute one.  So the label's logit is formed
+// once more, in 64 bits, and takes the place of the product's in the sum; what
+// is left are the errors of many words' logits, which average out.  The loss is
+// (m - z_label) + log(l), not lse - z_label: its terms are about its own size.
+template <int DT>
+__global__ void __launch_bounds__(CE_THREADS)
     ce_stats_kernel(const float* __restrict__ z, int ldz, int n, int v0, CeLabels labels,
-                    CeRow* __restrict__ state, float* __restrict__ zlabel, int first, int last,
-                    float* __restrict__ loss, float* __restrict__ lse) {
+                    CeInputs in, CeRow* __restrict__ state, float* __restrict__ zlabel, int first,
+                    int last, float* __restrict__ loss, float* __restrict__ lse) {
+  typedef typename TensorElem<DT>::type E;
   __shared__ CeRow part[CE_WAVES];
+  __shared__ double dot[CE_WAVES];
   const int t = blockIdx.x;
   const float* row = z + (size_t)t * ldz;
   CeRow r = {-INFINITY, 0.0f};
@@ -106,21 +117,52 @@ static __global__ void __launch_bounds__(CE_THREADS)
       if (i < have) r.l += ce_exp(v[i] - r.m);
   }
   r = ce_wave_join(r);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = r;
+  const int y = ce_label(labels, t);
+  double d = 0.0;
+  if (last && y >= 0) {
+    const E* x = static_cast<const E*>(in.X) + (size_t)t * in.ldx;
+    const E* w = static_cast<const E*>(in.W) + (size_t)y * in.ldw;
+    for (int c = 8 * threadIdx.x; c < in.D; c += 8 * CE_THREADS) {
+      float a[8], b[8];
+      load8<DT>(x + c, in.D - c, a);
+      load8<DT>(w + c, in.D - c, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d += (double)a[i] * (double)b[i];
+    }
+#pragma unroll
+    for (int k = 32; k > 0; k >>= 1) d += __shfl_xor(d, k);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    part[threadIdx.x >> 6] = r;
+    dot[threadIdx.x >> 6] = d;
+  }
   __syncthreads();
   if (threadIdx.x != 0) return;
 #pragma unroll
   for (int w = 1; w < CE_WAVES; ++w) r = ce_join(r, part[w]);
   if (!first) r = ce_join(state[t], r);
-  const int y = ce_label(labels, t);
   float zl = first ? 0.0f : zlabel[t];
   if (y >= v0 && y - v0 < n) zl = row[y - v0];
-  if (last) {
-    ce_write_loss(y, r, zl, t, loss, lse);
-  } else {
+  if (!last) {
     state[t] = r;
     zlabel[t] = zl;
+    return;
   }
+  if (y == CE_IGNORED) {
+    lse[t] = 0.0f;
+    loss[t] = 0.0f;
+    return;
+  }
+  double over = 0.0;  // m - z_label
+  if (y >= 0) {
+#pragma unroll
+    for (int w = 1; w < CE_WAVES; ++w) d += dot[w];
+    over = (double)r.m - (double)in.alpha * d;
+    r.l += ce_exp(-(float)over) - ce_exp(zl - r.m);
+  }
+  const float log_l = logf(r.l);
+  lse[t] = r.m + log_l;
+  loss[t] = y == CE_BAD ? NAN : (float)over + log_l;
 }
 
 // ---- backward over the library's products (32-bit X and W, few rows) ----------------
@@ -426,13 +468,14 @@ __device__ __forceinline__ CeRow ce_join2(CeRow a, CeRow b) {
 }
 
 // Joins a piece's parts (part[chunk][row], rows of the stride `padded`) into
-// the packed rows' state; the last piece writes the rows' loss and lse.  A
+// the packed rows' state (m in units of log2, c = alpha * log2(e), zlabel the
+// labels' x w); the last piece writes the rows' loss and lse.  A
 // workgroup takes 32 rows, 32 lanes a row stride over its chunks.
 constexpr int CE_JOIN_ROWS = 32, CE_JOIN_LANES = 32;
 static __global__ void __launch_bounds__(CE_JOIN_ROWS * CE_JOIN_LANES)
     ce_join_kernel(const CeRow* __restrict__ part, int chunks, int padded,
                    const int* __restrict__ count, const int* __restrict__ order,
-                   const int* __restrict__ label, CeRow* __restrict__ state,
+                   const int* __restrict__ label, CeRow* __restrict__ state, float c,
                    const float* __restrict__ zlabel, int first, int last, float* __restrict__ loss,
                    float* __restrict__ lse) {
   __shared__ CeRow sh[CE_JOIN_LANES * CE_JOIN_ROWS];
@@ -464,9 +507,12 @@ static __global__ void __launch_bounds__(CE_JOIN_ROWS * CE_JOIN_LANES)
     return;
   }
   const int t = order[row], y = label[row];
-  const float e = (r.m + log2f(r.l)) * 0.693147180559945309417f;
-  lse[t] = e;
-  loss[t] = y == CE_BAD ? NAN : e - zlabel[row];
+  constexpr float LN2 = 0.693147180559945309417f;
+  const float l = log2f(r.l);
+  lse[t] = (r.m + l) * LN2;
+  // (m - c * x w is exact but for one rounding: the terms are about the loss's
+  // own size, so a label that is nearly certain keeps its small loss's bits)
+  loss[t] = y == CE_BAD ? NAN : (fmaf(-c, zlabel[row], r.m) + l) * LN2;
 }
 
 }  // namespace sgemm

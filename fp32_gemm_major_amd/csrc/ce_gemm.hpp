@@ -95,12 +95,12 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
   const int col0 = n0 + w.wn * T::WN;  // the wave's first column
   const int have = a.g.N - col0;
   if (have <= 0) return;
-  const float c = a.c, alpha = a.g.alpha;
+  const float c = a.c;
 #pragma unroll
   for (int i = 0; i < T::FM; ++i) {
     const int row = m0 + w.wm * T::WM + 32 * i + w.li;
     const int y = label[row] - v0 - col0;
-    // the label's logit, in the one tile that holds it
+    // the label's x w, in the one tile that holds it
     if (__any(y >= 0 && y < T::WN && y < have)) {
       float z = 0.0f;
 #pragma unroll
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
 #pragma unroll
         for (int k = 0; k < 16; ++k)
           if (y == 32 * j + 8 * (k / 4) + 4 * w.lh + k % 4) z = acc[i][j][k];
-      if (y >= 0 && y < T::WN && y < have && ((y >> 2) & 1) == w.lh) zlabel[row] = alpha * z;
+      if (y >= 0 && y < T::WN && y < have && ((y >> 2) & 1) == w.lh) zlabel[row] = z;
     }
     // t = z * log2(e): m = max t, l = sum 2^(t - m).  The difference is one
     // fused multiply-add, so only m's own rounding enters lse.

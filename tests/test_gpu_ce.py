@@ -388,6 +388,30 @@ def test_random_inputs(handle, T, V, D, dt):
     assert np.all(np.abs(loss.double().cpu().numpy() - want) <= 2 * ez)
 
 
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("T", [1, 10, 100, 520])
+def test_small_losses_keep_their_bits(handle, T, dt):
+    """Labels that are nearly certain, logits of about 25 that are exact in any
+    order: the loss log(1 + s) is off by s's own errors (2^-16 relative here:
+    few words, |z - m| < 50), by the rounding of the sum 1 + s -- V additions of
+    at most u each, in whatever order -- by the exponential of the largest term
+    (v_exp_f32: one unit in the last place, 2 u), and by the logarithm and the
+    steps that join the parts (at most 6 u), not by lse's own rounding."""
+    V, D = 40, 64
+    rng = np.random.default_rng(T)
+    w = rng.integers(-1, 2, (V, D)).astype(float)
+    labels = rng.integers(0, V, T)
+    x = w[labels] * rng.choice([1.0, 1.5, 2.0], (T, 1)) / 4
+    tt = DTYPES[dt]
+    X, W = torch.from_numpy(x).to(tt).cuda(), torch.from_numpy(w).to(tt).cuda()
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    handle.ce_forward(X, W, torch.from_numpy(labels).cuda(), loss, lse)
+    _, want, _ = ref.forward(x, w, labels)
+    assert want.max() < 0.1
+    got = loss.double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= 2.0 ** -15 * want + (V + 8) * U), np.abs(got - want).max()
+
+
 @pytest.mark.parametrize("T", [1, 40, 520])
 @pytest.mark.parametrize("D", [1, 2, 4])
 def test_32_bit_logits_keep_24_bits(handle, T, D):

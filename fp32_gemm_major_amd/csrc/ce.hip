@@ -81,10 +81,11 @@ bool copies_w(const CeProblem& a) {
   return a.dtype == SGEMM_DTYPE_F32 || a.D % 8 != 0 || a.ldw > 2LL * a.D;
 }
 // Whether a backward pass keeps dz's rounding residues (ce_dz_gemm_kernel), and
-// the rows its products take then.  Above, 128 rows or more that count bring the
-// error of dz's rounding to within a few percent of its mean, that of the
-// gradients' own rounding.
-constexpr int kResidueRows = 256;
+// the rows its products take then.  With more rows one label's term is no
+// longer most of a gradient, and dz's rounding adds about a seventh to the
+// error of the gradients' own (4096 rows: 1.9e-3 against 1.7e-3 in bfloat16),
+// while twice the rows would cost a quarter of the time (256 rows).
+constexpr int kResidueRows = 128;
 bool residues(const CeProblem& a) {
   return a.dtype != SGEMM_DTYPE_F32 && a.T <= kResidueRows;
 }
@@ -324,6 +325,11 @@ bool big_tiles(long long rows, long long cols, int cus) {
   return rows > 128 && 5 * up_div(rows, 256) * up_div(cols, 256) >= 3LL * cus;
 }
 
+// K steps up to which the two-stage 128-square tile is the faster small one
+// (128 rows of 1000 columns: forward 34 us against 39, of 4096: 71 against 60).
+constexpr int kFewSteps = 32;
+bool few_steps(long long k) { return k <= (long long)kFewSteps * kStep; }
+
 // The operands of a packed pass: X's packed rows and a piece of W, as the
 // products read them.  16-bit W stays where it is; 32-bit W's piece is copied
 // into planes.
@@ -432,8 +438,9 @@ int packed_forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& 
     st = piece_of_w<DT>(a, v0, n, wp, dp, &o, s);
     if (st != SGEMM_OK) return st;
     const bool big = big_tiles(a.T, n, h->cus);
-    st = big ? logits_piece<L256x256, DT>(a, n, o, label, (int)v0, part, Tp, zlabel, s)
-             : logits_piece<L128x128, DT>(a, n, o, label, (int)v0, part, Tp, zlabel, s);
+    st = big              ? logits_piece<L256x256, DT>(a, n, o, label, (int)v0, part, Tp, zlabel, s)
+         : few_steps(a.D) ? logits_piece<L128x128s, DT>(a, n, o, label, (int)v0, part, Tp, zlabel, s)
+                          : logits_piece<L128x128, DT>(a, n, o, label, (int)v0, part, Tp, zlabel, s);
     if (st != SGEMM_OK) return st;
     const int chunks = (int)up_div(n, big ? L256x256::WN : L128x128::WN);
     hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)up_div(a.T, CE_JOIN_ROWS)),
@@ -564,6 +571,7 @@ int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels&
     st = piece_of_w<DT>(a, v0, n, wp, dp, &o, s);
     if (st != SGEMM_OK) return st;
     st = big_tiles(a.T, n, h->cus) ? dz_piece<L256x256, DT>(a, n, o, info, (int)v0, d, s)
+         : few_steps(a.D)          ? dz_piece<L128x128s, DT>(a, n, o, info, (int)v0, d, s)
                                    : dz_piece<L128x128, DT>(a, n, o, info, (int)v0, d, s);
     if (st != SGEMM_OK) return st;
     if (dX != nullptr) {
@@ -574,8 +582,15 @@ int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels&
     }
     if (dW != nullptr) {
       void* out = rows_from(dW, (size_t)v0, lddw, esz);
-      st = big_tiles(n, a.D, h->cus)
+      // Up to 512 rows writing dW takes longer than its sums, and two small
+      // tiles a CU overlap better -- as long as the last-level cache takes the
+      // writes, in rows of 256 bytes (512 rows: 50001 x 1000 in 79 us against 86,
+      // 65536 x 4096 in 484 against 373).
+      const bool small = product_rows(a) <= 512 && 2 * (size_t)n * a.D <= kDzBytes;
+      st = !small && big_tiles(n, a.D, h->cus)
                ? dw_piece<L256x256, DT>(a, n, d, xs, o.ldx, dp, count, dw_factor, out, lddw, s)
+           : few_steps(product_rows(a))
+               ? dw_piece<L128x128s, DT>(a, n, d, xs, o.ldx, dp, count, dw_factor, out, lddw, s)
                : dw_piece<L128x128, DT>(a, n, d, xs, o.ldx, dp, count, dw_factor, out, lddw, s);
       if (st != SGEMM_OK) return st;
     }
@@ -623,7 +638,7 @@ int forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
     const int st = product(&ph, a.dtype, SGEMM_OP_N, SGEMM_OP_T, a.T, n, a.D, a.alpha, a.X, a.ldx,
                            rows_from(a.W, v0, a.ldw, esz), a.ldw, 0.0f, z, ldz, s);
     if (st != SGEMM_OK) return st;
-    hipLaunchKernelGGL(stats, dim3(a.T), dim3(CE_THREADS), 0, s, z, ldz, n, v0, labels, in, state,
+    hipLaunchKernelGGL(stats, dim3(a.T), dim3(CE_STATS_THREADS), 0, s, z, ldz, n, v0, labels, in, state,
                        zlabel, v0 == 0, n == a.V - v0, loss, lse);
     const int e = launched();
     if (e != SGEMM_OK) return e;

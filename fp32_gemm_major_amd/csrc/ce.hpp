@@ -64,7 +64,6 @@ __device__ __forceinline__ int ce_label(const CeLabels& s, int t) {
 }
 
 constexpr int CE_THREADS = 256;
-constexpr int CE_WAVES = CE_THREADS / 64;
 
 // X and W as a forward pass over the library's products reads them again.
 struct CeInputs {
@@ -77,7 +76,9 @@ struct CeInputs {
 
 // Joins columns [v0, v0 + n) of a piece of z (T rows of stride ldz, 16-byte
 // aligned) into the rows' state, one workgroup a row; the last piece writes
-// loss and lse.
+// loss and lse.  With one row the kernel is bound by its loads' latency: 1024
+// lanes with four loads in flight each take 32000 columns in 7.4 us, 256 with one
+// took 16.5.
 //
 // With few rows an error of z, though only a unit or two in its last place,
 // is not averaged out by others: where the label is nearly certain, the
@@ -85,28 +86,21 @@ struct CeInputs {
 // once more, in 64 bits, and takes the place of the product's in the sum; what
 // is left are the errors of many words' logits, which average out.  The loss is
 // (m - z_label) + log(l), not lse - z_label: its terms are about its own size.
+constexpr int CE_STATS_THREADS = 1024, CE_STATS_WAVES = CE_STATS_THREADS / 64;
 template <int DT>
-__global__ void __launch_bounds__(CE_THREADS)
+__global__ void __launch_bounds__(CE_STATS_THREADS)
     ce_stats_kernel(const float* __restrict__ z, int ldz, int n, int v0, CeLabels labels,
                     CeInputs in, CeRow* __restrict__ state, float* __restrict__ zlabel, int first,
                     int last, float* __restrict__ loss, float* __restrict__ lse) {
   typedef typename TensorElem<DT>::type E;
-  __shared__ CeRow part[CE_WAVES];
-  __shared__ double dot[CE_WAVES];
+  constexpr int BATCH = 4, STEP = 4 * CE_STATS_THREADS;
+  __shared__ CeRow part[CE_STATS_WAVES];
+  __shared__ double dot[CE_STATS_WAVES];
   const int t = blockIdx.x;
   const float* row = z + (size_t)t * ldz;
   CeRow r = {-INFINITY, 0.0f};
-  for (int c = 4 * threadIdx.x; c < n; c += 4 * CE_THREADS) {
-    float v[4];
-    const int have = n - c < 4 ? n - c : 4;
-    if (have == 4) {
-      const v4u x = *reinterpret_cast<const v4u*>(row + c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(x[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = i < have ? row[c + i] : -INFINITY;
-    }
+  // four values at c, those that are there
+  auto take = [&](const float (&v)[4], int have) {
     const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
     if (top > r.m) {
       r.l *= ce_exp(r.m - top);
@@ -115,6 +109,25 @@ __global__ void __launch_bounds__(CE_THREADS)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (i < have) r.l += ce_exp(v[i] - r.m);
+  };
+  int c = 4 * threadIdx.x;
+  for (; c + (BATCH - 1) * STEP + 4 <= n; c += BATCH * STEP) {
+    v4u x[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) x[k] = *reinterpret_cast<const v4u*>(row + c + k * STEP);
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const float v[4] = {__uint_as_float(x[k][0]), __uint_as_float(x[k][1]),
+                          __uint_as_float(x[k][2]), __uint_as_float(x[k][3])};
+      take(v, 4);
+    }
+  }
+  for (; c < n; c += STEP) {
+    const int have = n - c < 4 ? n - c : 4;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < have ? row[c + i] : -INFINITY;
+    take(v, have);
   }
   r = ce_wave_join(r);
   const int y = ce_label(labels, t);
@@ -122,10 +135,10 @@ __global__ void __launch_bounds__(CE_THREADS)
   if (last && y >= 0) {
     const E* x = static_cast<const E*>(in.X) + (size_t)t * in.ldx;
     const E* w = static_cast<const E*>(in.W) + (size_t)y * in.ldw;
-    for (int c = 8 * threadIdx.x; c < in.D; c += 8 * CE_THREADS) {
+    for (int k = 8 * threadIdx.x; k < in.D; k += 8 * CE_STATS_THREADS) {
       float a[8], b[8];
-      load8<DT>(x + c, in.D - c, a);
-      load8<DT>(w + c, in.D - c, b);
+      load8<DT>(x + k, in.D - k, a);
+      load8<DT>(w + k, in.D - k, b);
 #pragma unroll
       for (int i = 0; i < 8; ++i) d += (double)a[i] * (double)b[i];
     }
@@ -139,7 +152,7 @@ __global__ void __launch_bounds__(CE_THREADS)
   __syncthreads();
   if (threadIdx.x != 0) return;
 #pragma unroll
-  for (int w = 1; w < CE_WAVES; ++w) r = ce_join(r, part[w]);
+  for (int w = 1; w < CE_STATS_WAVES; ++w) r = ce_join(r, part[w]);
   if (!first) r = ce_join(state[t], r);
   float zl = first ? 0.0f : zlabel[t];
   if (y >= v0 && y - v0 < n) zl = row[y - v0];
@@ -156,7 +169,7 @@ __global__ void __launch_bounds__(CE_THREADS)
   double over = 0.0;  // m - z_label
   if (y >= 0) {
 #pragma unroll
-    for (int w = 1; w < CE_WAVES; ++w) d += dot[w];
+    for (int w = 1; w < CE_STATS_WAVES; ++w) d += dot[w];
     over = (double)r.m - (double)in.alpha * d;
     r.l += ce_exp(-(float)over) - ce_exp(zl - r.m);
   }

@@ -43,16 +43,21 @@ __host__ __device__ inline void band_walk(int lin, int tiles_m, int tiles_n,
   tn = in / rows;
 }
 
+// Bijection of [0, nwg) that gives each XCD (wg % kXcds) one contiguous run.
+__host__ __device__ inline int xcd_run(int wg, int nwg) {
+  const int q = nwg / kXcds, r = nwg % kXcds;
+  const int xcd = wg % kXcds, idx = wg / kXcds;
+  // XCD x owns ids [start(x), start(x) + count(x)), count = q + (x < r).
+  const int start = xcd < r ? xcd * (q + 1) : r * (q + 1) + (xcd - r) * q;
+  return start + idx;
+}
+
 // Bijection from workgroup id `wg` in [0, nwg) to tile (tm, tn), with
 // nwg == tiles_m * tiles_n and band >= 1.
 __host__ __device__ inline void tile_coords(int wg, int nwg, int tiles_m,
                                             int tiles_n, int band, int& tm,
                                             int& tn) {
-  const int q = nwg / kXcds, r = nwg % kXcds;
-  const int xcd = wg % kXcds, idx = wg / kXcds;
-  // XCD x owns ids [start(x), start(x) + count(x)), count = q + (x < r).
-  const int start = xcd < r ? xcd * (q + 1) : r * (q + 1) + (xcd - r) * q;
-  band_walk(start + idx, tiles_m, tiles_n, band, tm, tn);
+  band_walk(xcd_run(wg, nwg), tiles_m, tiles_n, band, tm, tn);
 }
 
 // Workgroup position in a persistent grid of G (the stream-K kernels):

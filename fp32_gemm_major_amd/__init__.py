@@ -49,6 +49,8 @@ SGEMM_DTYPE_FP8_E5M2 = 4
 
 SGEMM_MX_BLOCK = 32  # values of a microscaled row that share a scale
 SGEMM_MX_MAX_K = 1 << 27
+SGEMM_MX_MAX_ROWS = 0x7fffff00
+SGEMM_CE_MAX_D = 1 << 21
 
 SGEMM_SCHEDULE_TILES = 0
 SGEMM_SCHEDULE_STREAM_K = 1

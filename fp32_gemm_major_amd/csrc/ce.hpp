@@ -371,7 +371,8 @@ __global__ void __launch_bounds__(CE_PACK_THREADS)
       r_max = fmaxf(r_max, top_r[w]);
     }
   }
-  const float unit = !UNIT ? 1.0f : q_max > 0.0f ? q_max : r_max > 0.0f ? r_max : 1.0f;
+  // (a q far below the p's would take them out of range)
+  const float unit = !UNIT ? 1.0f : q_max > 0x1p-16f * r_max ? q_max : r_max > 0.0f ? r_max : 1.0f;
   auto exponent = [](float r) { return r > 0.0f && r < INFINITY ? ilogbf(r) : 13; };
   const int kmax = SCALED ? exponent(r_max / unit) : 13;
   const float scale = alpha * unit;

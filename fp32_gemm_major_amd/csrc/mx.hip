@@ -32,8 +32,11 @@ bool mx_strides_ok(int K, int ldc, int lds) {
   return ldc >= at_least_one(16 * nb) && lds >= at_least_one(nb);
 }
 
-// Column and row counts that the kernels' 32-bit indexes hold.
-bool mx_sizes_ok(int R, int K) { return R >= 0 && K >= 0 && K <= SGEMM_MX_MAX_K; }
+// Column and row counts that the kernels' 32-bit indexes hold (a tile past the
+// last row or column included).
+bool mx_sizes_ok(int R, int K) {
+  return R >= 0 && R <= SGEMM_MX_MAX_ROWS && K >= 0 && K <= SGEMM_MX_MAX_K;
+}
 
 typedef void (*quant_fn)(MxQuantArgs);
 typedef void (*quant_t_fn)(MxQuantArgs, int);
@@ -78,12 +81,25 @@ int launch_quantize(int dtype, int trans, const MxQuantArgs& g, hipStream_t stre
 // The product straight from memory, A in codes (xdt < 0) or in activations,
 // one or four tiles of 16 columns a workgroup.
 int launch_small(int xdt, int tiles, const MxArgs& g, hipStream_t stream) {
-  const long long tm = up_div(g.M, MXS_TILE), tn = up_div(g.N, MXS_TILE * tiles);
-  if (tm > 65535) return SGEMM_ERR_UNSUPPORTED;
+  constexpr int kRows = 65535 * MXS_TILE;  // a grid's second extent
   const int kind = xdt < 0 ? 0 : g.M <= MXS_FEW ? 4 + xdt : 1 + xdt;
-  hipLaunchKernelGGL(kSmall[kind][tiles == 4], dim3((unsigned)tn, (unsigned)tm), dim3(MXS_THREADS), 0,
-                     stream, g);
-  return launched();
+  const unsigned tn = (unsigned)up_div(g.N, MXS_TILE * tiles);
+  for (long long m0 = 0; m0 < g.M; m0 += kRows) {
+    MxArgs p = g;
+    p.M = (int)(g.M - m0 < kRows ? g.M - m0 : kRows);
+    if (m0 > 0) {  // (activations come with 16 rows at most)
+      if (g.K > 0) {
+        p.A = static_cast<const uint8_t*>(g.A) + (size_t)m0 * g.lda;
+        p.SA = g.SA + (size_t)m0 * g.ldsa;
+      }
+      p.C = static_cast<char*>(g.C) + (size_t)m0 * g.ldc * tensor_elem_bytes(g.cdt);
+    }
+    hipLaunchKernelGGL(kSmall[kind][tiles == 4], dim3(tn, (unsigned)up_div(p.M, MXS_TILE)),
+                       dim3(MXS_THREADS), 0, stream, p);
+    const int st = launched();
+    if (st != SGEMM_OK) return st;
+  }
+  return SGEMM_OK;
 }
 
 // Tiles of columns a workgroup of up to 16 rows takes.  Four, once that still
@@ -153,7 +169,7 @@ int validate_product(int M, int N, int K, const void* A, const void* B, int ldb,
                      int ldsb, int dtype, const void* C, int ldc) {
   const unsigned esz = tensor_elem_bytes(dtype);
   if (esz == 0) return SGEMM_ERR_VALUE;
-  if (N < 0 || !mx_sizes_ok(M, K)) return SGEMM_ERR_SIZE;
+  if (!mx_sizes_ok(M, K) || !mx_sizes_ok(N, K)) return SGEMM_ERR_SIZE;
   if (!mx_strides_ok(K, ldb, ldsb) || ldc < at_least_one(N)) return SGEMM_ERR_LD;
   if (M == 0 || N == 0) return SGEMM_OK;
   if (C == nullptr || (K > 0 && (A == nullptr || B == nullptr || SB == nullptr)))

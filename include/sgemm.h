@@ -458,11 +458,13 @@ int sgemm_set_lowp_kernel(sgemm_handle_t h, int kernel_id);
  * rows, with strides in bytes of at least 16*ceil(K/32) and ceil(K/32); any
  * byte alignment.  s = 255 makes every value of its block NaN.
  *
- * Ownership, streams, errors and threading as for sgemm_run.  K is at most
- * SGEMM_MX_MAX_K (SGEMM_ERR_SIZE).  Tensors of activations and results have
+ * Ownership, streams, errors and threading as for sgemm_run (with a workspace:
+ * sgemm_run_mx_quant).  K is at most SGEMM_MX_MAX_K, rows and columns at most
+ * SGEMM_MX_MAX_ROWS (SGEMM_ERR_SIZE).  Tensors of activations and results have
  * dtype SGEMM_DTYPE_F32, _BF16 or _F16 (SGEMM_ERR_VALUE for another, and for
  * a tensor not aligned to its element). */
 #define SGEMM_MX_MAX_K (1 << 27)
+#define SGEMM_MX_MAX_ROWS 0x7fffff00
 
 /* Quantise X into codes and scales, whole blocks: positions from K to the end
  * of the last block hold zero codes.  X is R x K (trans SGEMM_OP_N) or stored

@@ -68,6 +68,9 @@ def test_validate():
             assert v(dtype=bad) == sg.SGEMM_ERR_VALUE
         assert v(T=-1) == sg.SGEMM_ERR_SIZE and v(V=0) == sg.SGEMM_ERR_SIZE
         assert v(D=0) == sg.SGEMM_ERR_SIZE and v(V=-3) == sg.SGEMM_ERR_SIZE
+        big = sg.SGEMM_CE_MAX_D + 1
+        assert v(D=big, ldx=big, ldw=big) == sg.SGEMM_ERR_SIZE
+        assert v(T=2 ** 31 - 1) == sg.SGEMM_ERR_SIZE and v(V=2 ** 31 - 1) == sg.SGEMM_ERR_SIZE
         assert v(ldx=5) == sg.SGEMM_ERR_LD and v(ldw=5) == sg.SGEMM_ERR_LD
         for name in ("X", "W", "labels", "lse"):
             assert v(**{name: None}) == sg.SGEMM_ERR_NULL, name

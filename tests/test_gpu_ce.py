@@ -184,6 +184,18 @@ def test_uneven_upstream_gradients(handle, T, dt):
     p.check_backward()
 
 
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("T", [5, 200])
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -60, 2.0 ** -14])
+def test_gradients_of_lse_beside_small_ones_of_loss(handle, size, T, dt):
+    p = Problem(T, 500, 40, dt, seed=9, ignored=0.1)
+    p.dloss = (p.dloss * size).astype(np.float32).astype(float)
+    p.dl.copy_(torch.from_numpy(p.dloss))
+    p.forward(handle)
+    p.backward(handle)
+    p.check_backward()
+
+
 @pytest.mark.parametrize("scale", [2.0 ** -30, 2.0 ** -14, 2.0 ** 10])
 def test_half_gradients_keep_their_range(handle, scale):
     """binary16 dz neither vanishes nor overflows, whatever dloss' size: the

@@ -250,6 +250,21 @@ def test_empty_and_k_zero(handle):
     handle.mx4_dequantize(q, torch.empty(0, 64, device="cuda"))
 
 
+@pytest.mark.parametrize("K", [0, 32])
+def test_more_rows_than_a_grid_extent_holds(handle, K):
+    M = 65535 * 16 + 40
+    A, B = sg.Mx4.empty(M, K), operand(2, 32, 3) if K else sg.Mx4.empty(2, 0)
+    rng = np.random.default_rng(0)
+    if K:
+        A.codes.copy_(torch.from_numpy(rng.integers(0, 256, (M, 16), dtype=np.uint8)))
+        A.scales.fill_(127)
+    C = torch.ones(M, 2, device="cuda")
+    handle.gemm_mx4(A, B, C, beta=0.5)
+    a, b = (ref.dequantize(*as_numpy(q)) for q in (A, B))
+    want, mag = ref.product(1.0, a, b, 0.5, np.ones((M, 2)))
+    assert np.all(np.abs(C.double().cpu().numpy() - want) <= 4 * max(K, 1) * 2.0 ** -24 * mag)
+
+
 def test_refusals(handle):
     A, B = operand(20, 64, 1), operand(5, 64, 2)
     C = torch.empty(20, 5, device="cuda")

@@ -42,6 +42,8 @@ def test_validate_product():
         assert good(**{name: -32}) == sg.SGEMM_ERR_SIZE
     assert good(K=63) == sg.SGEMM_ERR_SIZE
     assert good(K=sg.SGEMM_MX_MAX_K + 32, lda=1 << 30, ldb=1 << 30) == sg.SGEMM_ERR_SIZE
+    for name in ("M", "N"):
+        assert good(**{name: sg.SGEMM_MX_MAX_ROWS + 1}, ldc=2 ** 31 - 1) == sg.SGEMM_ERR_SIZE
     for name, short in (("lda", 31), ("ldsa", 1), ("ldb", 31), ("ldsb", 1), ("ldc", 4)):
         assert good(**{name: short}) == sg.SGEMM_ERR_LD, name
     for name in ("A", "SA", "B", "SB", "C"):

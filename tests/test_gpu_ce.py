@@ -510,6 +510,43 @@ def test_same_bits_every_call_and_in_graphs(dt, T):
             assert all(torch.equal(a, b) for a, b in zip(outs, want))
 
 
+@pytest.mark.parametrize("T", [5, 40, 300])
+def test_past_32_bit_offsets(T):
+    """W and dW of 2.2e9 elements (the reference's sums in 64 bits on the GPU,
+    by pieces)."""
+    V, D = 540000, 4096
+    W = torch.empty(V, D, dtype=torch.bfloat16, device="cuda").normal_(std=0.03)
+    X = torch.empty(T, D, dtype=torch.bfloat16, device="cuda").normal_()
+    Y = torch.randint(0, V, (T,), device="cuda")
+    Y[0], Y[1], Y[2] = V - 1, 524288, ref.IGNORE
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    dl = torch.full((T,), 0.5, device="cuda")
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    with sg.Handle(workspace=False) as h:
+        h.set_workspace(h.ce_workspace_size(X, W, backward=True))
+        h.ce_forward(X, W, Y, loss, lse)
+        h.ce_backward(X, W, Y, lse, dl, dX, dW)
+    x = X.double()
+    z = torch.cat([x @ w.double().t() for w in W.split(60000)], 1)
+    want = torch.logsumexp(z, 1)
+    keep = Y != ref.IGNORE
+    # 4 D u sum|x w| of about 0.03 * 4096 * 0.64, and the sum's bound
+    tol = 4 * D * U * 80 + (V / 64 + 32) * U + 2.0 ** -14
+    assert ((lse.double() - want).abs()[keep] < tol).all() and lse[2] == 0 and loss[2] == 0
+    assert ((loss.double() - (want - z.gather(1, Y.clamp(min=0)[:, None])[:, 0])).abs()[keep] < 2 * tol).all()
+    dz = torch.exp(z - want[:, None])
+    dz[torch.arange(T), Y.clamp(min=0)] -= 1
+    dz *= 0.5 * keep[:, None]
+    half = 2.0 ** -8
+    at = torch.cat([Y[keep], torch.tensor([0, 1, 524287, 524289, V - 2], device="cuda")])
+    for got, w, size in ((dW[at], dz[:, at].t() @ x, dz[:, at].abs().t() @ x.abs()),
+                         (dX, sum(a @ b.double() for a, b in zip(dz.split(60000, 1), W.split(60000))),
+                          sum(a.abs() @ b.double().abs() for a, b in zip(dz.split(60000, 1),
+                                                                         W.split(60000))))):
+        bound = half * w.abs() + (half + 2 * tol) * 1.01 * size
+        assert ((got.double() - w).abs() <= bound).all()
+
+
 def test_refusals(handle):
     p = Problem(6, 40, 16, "bf16")
     with pytest.raises(ValueError):

@@ -250,6 +250,39 @@ def test_empty_and_k_zero(handle):
     handle.mx4_dequantize(q, torch.empty(0, 64, device="cuda"))
 
 
+@pytest.mark.parametrize("M", [3, 40])
+def test_operand_past_32_bit_offsets(handle, M):
+    N, K = 70000, 131072  # 4.6 GB of codes
+    B = sg.Mx4.empty(N, K)
+    B.codes.random_(0, 256)
+    B.scales.fill_(120)
+    A = operand(M, K, 6)
+    C = torch.empty(M, N, device="cuda")
+    handle.gemm_mx4(A, B, C)
+    at = torch.tensor([0, 1, 65535, 65536, N - 2, N - 1])
+    a = ref.dequantize(*as_numpy(A))
+    b = ref.dequantize(B.codes[at.cuda()].cpu().numpy(), B.scales[at.cuda()].cpu().numpy())
+    check(C[:, at.cuda()].cpu().numpy(), a, b, K, 1.0, 0.0, None, "f32")
+
+
+def test_calls_on_two_handles_overlap():
+    """Calls that use a workspace, on two streams at once: each handle its own."""
+    B = operand(512, 1024, 8)
+    X = [torch.from_numpy(values(60, 1024, 30 + k, spread=2)).bfloat16().cuda() for k in range(2)]
+    with sg.Handle() as one, sg.Handle() as two:
+        want = [torch.empty(60, 512, device="cuda") for _ in range(2)]
+        for k in range(2):
+            one.gemm_mx4(X[k], B, want[k])
+        got = [torch.empty_like(w) for w in want]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        torch.cuda.synchronize()
+        for _ in range(50):
+            for h, s, x, c in zip((one, two), streams, X, got):
+                h.gemm_mx4(x, B, c, stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("K", [0, 32])
 def test_more_rows_than_a_grid_extent_holds(handle, K):
     M = 65535 * 16 + 40

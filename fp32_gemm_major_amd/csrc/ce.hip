@@ -69,10 +69,21 @@ long long sum_cols(const CeProblem& a) { return round_up(a.D, 8); }
 // of a forward pass go through the products with few rows instead.  32-bit:
 // from rows on for which the copies of W and the whole tiles pay (1024 columns,
 // 32000 words, forward and backward: 256 rows in 655 us, 564 over the library's
-// products; 512 rows 905 against 1029; 2048 rows 2.76 ms against 3.88).
+// products; 512 rows 905 against 1029; 2048 rows 2.76 ms against 3.88), and
+// while the logits, and in a backward pass dW, have tiles enough for the card:
+// unlike the library's products, these split no sum of theirs over workgroups.
+// In tiles of 128 square: 1000 rows, 1000 columns, 4000 words (256 of z) forward
+// 86 us against 82, 8000 words (504) 117 against 139; backward, 4000 rows of
+// 1000 columns, 1000 words (256 of z, 64 of dW) 331 us against 220, 4000 words
+// (1024, 256) 581 against 746; 16000 rows, 200 columns, 4000 words (4000, 64)
+// 1796 against 823.  2000 rows, 220 words, 3839 columns: 175 and 348 us against
+// 61 and 140.
 constexpr int kFewRows = 16, kFewRows32 = 511;
+constexpr long long kTiles32 = 512, kGradientTiles32 = 256;
 bool packed(const CeProblem& a, int backward) {
-  return a.dtype == SGEMM_DTYPE_F32 ? a.T > kFewRows32 : backward || a.T > kFewRows;
+  if (a.dtype != SGEMM_DTYPE_F32) return backward || a.T > kFewRows;
+  return a.T > kFewRows32 && up_div(a.T, 128) * up_div(a.V, 128) >= kTiles32 &&
+         (!backward || up_div(a.V, 128) * up_div(a.D, 128) >= kGradientTiles32);
 }
 // Whether W's pieces are copied: 32-bit ones into planes, 16-bit ones whose
 // rows are no whole 16-byte units, or too far apart for the copy of W's last

@@ -143,8 +143,48 @@ def test_loss_and_gradients(handle, T, V, D, dt):
     p.check_backward()
 
 
+# 32-bit operands in planes: tiles enough of z, and of dW but for the last two
+# (forward in planes, backward over the library's products).
+WIDE = [(520, 16500, 300), (1100, 8200, 600), (4200, 2100, 2000), (513, 13057, 257), (520, 16500, 16),
+        (4097, 2048, 130)]
+
+
+@pytest.mark.parametrize("T,V,D", WIDE)
+def test_32_bit_loss_and_gradients_in_planes(T, V, D):
+    p = Problem(T, V, D, "f32", pad=0 if T % 2 else 3)
+    with sg.Handle(workspace=False) as h:
+        h.set_workspace(max(h.ce_workspace_size(p.X, p.W, backward=b) for b in (False, True)))
+        p.forward(h)
+        p.check_forward()
+        p.backward(h)
+        p.check_backward()
+
+
+@pytest.mark.parametrize("count", [0, 1, 127, 128, 129, 256, 257, 512, 600])
+def test_32_bit_rows_that_count_at_tile_edges(handle, count):
+    p = Problem(600, 13200, 264, "f32", seed=6, ignored=0.0)
+    p.labels[np.random.default_rng(count).permutation(600)[count:]] = ref.IGNORE
+    p.Y.copy_(torch.from_numpy(p.labels))
+    p.X[p.Y == ref.IGNORE] = float("nan")
+    p.forward(handle)
+    p.check_forward()
+    p.backward(handle)
+    p.check_backward()
+
+
+@pytest.mark.parametrize("T,V,D", [(2100, 220, 1900), (700, 900, 500), (9000, 130, 70), (9000, 130, 1)])
 @pytest.mark.parametrize("dt", list(DTYPES))
-@pytest.mark.parametrize("T,V,D", [(5, 2050, 64), (130, 3000, 96), (300, 1111, 40)])
+def test_many_rows_few_words(handle, T, V, D, dt):
+    p = Problem(T, V, D, dt, seed=9)
+    p.forward(handle)
+    p.check_forward()
+    p.backward(handle)
+    p.check_backward()
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("T,V,D", [(5, 2050, 64), (130, 3000, 96), (300, 1111, 40),
+                                   (550, 14000, 300)])
 def test_least_workspace_takes_small_pieces(T, V, D, dt):
     p = Problem(T, V, D, dt, seed=1)
     with sg.Handle(workspace=False) as h:
@@ -286,7 +326,7 @@ def test_no_read_past_the_operands(handle, T, dt):
 
 @pytest.mark.parametrize("dt", list(DTYPES))
 @pytest.mark.parametrize("T,V,D,pad", [(4, 300, 40, 100), (70, 1300, 72, 600), (300, 777, 64, 65),
-                                       (530, 1000, 41, 300)])
+                                       (530, 1000, 41, 300), (530, 14000, 290, 300)])
 def test_rows_far_apart(handle, T, V, D, pad, dt):
     p = Problem(T, V, D, dt, seed=8, pad=pad)
     p.forward(handle)
@@ -402,8 +442,8 @@ def test_random_inputs(handle, T, V, D, dt):
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))
-@pytest.mark.parametrize("T", [1, 10, 100, 520])
-def test_small_losses_keep_their_bits(handle, T, dt):
+@pytest.mark.parametrize("T", [1, 10, 100, 520, 65536])
+def test_small_losses_keep_their_bits(T, dt):
     """Labels that are nearly certain, logits of about 25 that are exact in any
     order: the loss log(1 + s) is off by s's own errors (2^-16 relative here:
     few words, |z - m| < 50), by the rounding of the sum 1 + s -- V additions of
@@ -418,16 +458,18 @@ def test_small_losses_keep_their_bits(handle, T, dt):
     tt = DTYPES[dt]
     X, W = torch.from_numpy(x).to(tt).cuda(), torch.from_numpy(w).to(tt).cuda()
     loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
-    handle.ce_forward(X, W, torch.from_numpy(labels).cuda(), loss, lse)
+    with sg.Handle(workspace=False) as h:
+        h.set_workspace(h.ce_workspace_size(X, W))
+        h.ce_forward(X, W, torch.from_numpy(labels).cuda(), loss, lse)
     _, want, _ = ref.forward(x, w, labels)
     assert want.max() < 0.1
     got = loss.double().cpu().numpy()
     assert np.all(np.abs(got - want) <= 2.0 ** -15 * want + (V + 8) * U), np.abs(got - want).max()
 
 
-@pytest.mark.parametrize("T", [1, 40, 520])
+@pytest.mark.parametrize("T", [1, 40, 520, 65536])
 @pytest.mark.parametrize("D", [1, 2, 4])
-def test_32_bit_logits_keep_24_bits(handle, T, D):
+def test_32_bit_logits_keep_24_bits(T, D):
     """One word: lse is the logit itself.  Operands with all 24 bits set: a
     product of 16 bits or 21 would miss the library's 32-bit bound, 4 D u
     sum|x w|, to which the logarithm's scale and back add 4 u |z|."""
@@ -436,7 +478,9 @@ def test_32_bit_logits_keep_24_bits(handle, T, D):
     X, W = (torch.from_numpy(v).float().cuda() for v in (x, w))
     assert np.array_equal(X.double().cpu().numpy(), x)
     loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
-    handle.ce_forward(X, W, torch.zeros(T, dtype=torch.int64, device="cuda"), loss, lse)
+    with sg.Handle(workspace=False) as h:
+        h.set_workspace(h.ce_workspace_size(X, W))
+        h.ce_forward(X, W, torch.zeros(T, dtype=torch.int64, device="cuda"), loss, lse)
     z = (x @ w.T)[:, 0]
     assert np.all(np.abs(lse.double().cpu().numpy() - z) <= (4 * D + 4) * U * z)
     assert np.all(np.abs(loss.double().cpu().numpy()) <= (4 * D + 8) * U * z)
@@ -470,11 +514,11 @@ def test_gradients_by_differences(handle):
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))
-@pytest.mark.parametrize("T", [1, 40, 300])
-def test_same_bits_every_call_and_in_graphs(dt, T):
+@pytest.mark.parametrize("T,V,D", [(1, 1500, 64), (40, 1500, 64), (300, 1500, 64), (600, 13200, 264)])
+def test_same_bits_every_call_and_in_graphs(dt, T, V, D):
     """Two eager calls, and a captured one replayed with eager work of other
     sizes between on the same workspace: the same bits."""
-    p = Problem(T, 1500, 64, dt)
+    p = Problem(T, V, D, dt)
     with sg.Handle(workspace=False) as h, sg.Handle(workspace=False) as other:
         size = h.ce_workspace_size(p.X, p.W, backward=True)
         for each in (h, other):

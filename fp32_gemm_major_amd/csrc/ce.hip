@@ -9,6 +9,7 @@
 #include <algorithm>
 
 #include "ce.hpp"
+#include "ce_few.hpp"
 #include "ce_gemm.hpp"
 #include "handle.hpp"
 #include "tile_map.hpp"
@@ -65,8 +66,22 @@ long long padded_cols(const CeProblem& a) { return round_up(a.D, kPadCols); }
 int plane_count(const CeProblem& a) { return a.dtype == SGEMM_DTYPE_F32 ? 3 : 1; }
 long long sum_cols(const CeProblem& a) { return round_up(a.D, 8); }
 
-// Whether a call runs on packed rows.  16-bit: every backward pass; few rows
-// of a forward pass go through the products with few rows instead.  32-bit:
+// Whether a backward pass is one for few rows (ce_few_kernel).  Its products are
+// the vector units', and rows of 16-bit W whose four-element groups stand at odd
+// places cost it twice the loads; what it saves are packing, copies and launches.
+// Microseconds here and on the other path: bfloat16, 4 rows, 80000 x 801 126 and
+// 211, one row of 118231 x 2303 825 and 708; 16 rows, 50000 x 128 44 and 57,
+// 20000 x 800 77 and 68; 32-bit, 16 rows, 131072 x 64 74 and 83, 20000 x 800 80
+// and 65.
+constexpr long long kFewElements8 = 1 << 27, kFewElements16 = 1 << 23;
+bool few(const CeProblem& a) {
+  const long long elements = (long long)a.V * a.D;
+  if (a.T <= 8) return a.dtype == SGEMM_DTYPE_F32 || a.D % 4 == 0 || elements <= kFewElements8;
+  return a.T <= CE_FEW_ROWS && elements <= kFewElements16;
+}
+
+// Whether a call runs on packed rows.  16-bit: all but few rows, which go through
+// the products with few rows instead (and ce_few_kernel).  32-bit:
 // from rows on for which the copies of W and the whole tiles pay (1024 columns,
 // 32000 words, forward and backward: 256 rows in 655 us, 564 over the library's
 // products; 512 rows 905 against 1029; 2048 rows 2.76 ms against 3.88), and
@@ -78,10 +93,10 @@ long long sum_cols(const CeProblem& a) { return round_up(a.D, 8); }
 // (1024, 256) 581 against 746; 16000 rows, 200 columns, 4000 words (4000, 64)
 // 1796 against 823.  2000 rows, 220 words, 3839 columns: 175 and 348 us against
 // 61 and 140.
-constexpr int kFewRows = 16, kFewRows32 = 511;
+constexpr int kFewRows = CE_FEW_ROWS, kFewRows32 = 511;
 constexpr long long kTiles32 = 512, kGradientTiles32 = 256;
 bool packed(const CeProblem& a, int backward) {
-  if (a.dtype != SGEMM_DTYPE_F32) return backward || a.T > kFewRows;
+  if (a.dtype != SGEMM_DTYPE_F32) return backward ? !few(a) : a.T > kFewRows;
   return a.T > kFewRows32 && up_div(a.T, 128) * up_div(a.V, 128) >= kTiles32 &&
          (!backward || up_div(a.V, 128) * up_div(a.D, 128) >= kGradientTiles32);
 }
@@ -147,12 +162,18 @@ int dx_slabs(const CeProblem& a, int cus, int b) {
 // Tiles of dX's product: 256 square unless one extent fits half of one.
 bool dx_big(const CeProblem& a) { return product_rows(a) > 128 && a.D > 128; }
 
-// Calls over the library's products (backward: 32-bit only).
+// Calls over the library's products (backward: few rows, or 32-bit).
 CeLayout layout_of(const CeProblem& a, int backward) {
   const size_t T = (size_t)a.T;
   CeLayout l = {16 * 256 + 12 * T, 4 * T};  // (boundaries, and padding of rows)
-  if (backward) l.fixed += 4 * T * (size_t)round_up(a.D, 8);
+  if (backward) l.fixed += 4 * T * (size_t)round_up(a.D, 8);  // X's rows, or a slab of dX's sums
   return l;
+}
+// Slabs of dX's sums with few rows: four workgroups a CU, each with a chunk of
+// the vocabulary at least.
+int few_slabs(const CeProblem& a, int cus) {
+  const long long want = up_div(4LL * cus, up_div(a.D, CE_FEW_COLS));
+  return (int)std::min(want, up_div(a.V, std::max(CE_FEW_STEP, 8 * a.T)));
 }
 
 // Columns of a piece that `bytes` of workspace hold (0: not even the least).
@@ -242,9 +263,11 @@ CeSizes sizes_of(CeProblem a, int backward, int cus) {
   if (!packed(a, backward)) {
     const CeLayout l = layout_of(a, backward);
     const int small = a.V < kPieceStep ? a.V : kPieceStep;
-    const int big = piece_columns(a, l, (size_t)1 << 62);
-    return CeSizes{l.fixed + l.per_col * (size_t)(small + 8),
-                   l.fixed + l.per_col * (size_t)(big + 8) + kProductBytes};
+    const size_t piece = l.per_col * (size_t)(piece_columns(a, l, (size_t)1 << 62) + 8);
+    const size_t least = l.fixed + l.per_col * (size_t)(small + 8);
+    const size_t more = backward && few(a) ? 4 * (size_t)a.T * (size_t)sum_cols(a) * (few_slabs(a, cus) - 1) : 0;
+    // (spare room is shared between slabs and the piece)
+    return CeSizes{least, std::max(least + 2 * more, l.fixed + more + piece + kProductBytes)};
   }
   const CeLayout l = packed_layout(a, backward);
   size_t base = l.fixed + l.per_col * kPadCols;
@@ -644,7 +667,8 @@ int forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
                      : a.dtype == SGEMM_DTYPE_BF16 ? ce_stats_kernel<SGEMM_DTYPE_BF16>
                                                    : ce_stats_kernel<SGEMM_DTYPE_F16>;
   const CeInputs in = {a.X, a.ldx, a.W, a.ldw, a.D, a.alpha};
-  for (int v0 = 0; v0 < a.V; v0 += cols) {
+  for (long long at = 0; at < a.V; at += cols) {
+    const int v0 = (int)at;
     const int n = a.V - v0 < cols ? a.V - v0 : cols;
     const int st = product(&ph, a.dtype, SGEMM_OP_N, SGEMM_OP_T, a.T, n, a.D, a.alpha, a.X, a.ldx,
                            rows_from(a.W, v0, a.ldw, esz), a.ldw, 0.0f, z, ldz, s);
@@ -657,7 +681,87 @@ int forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
   return SGEMM_OK;
 }
 
-// 32-bit, few rows: z in place becomes dz, and the gradients are their own
+template <int DT, int TB>
+int launch_few(CeFew f, int slabs, const CeLabels& labels, const float* lse,
+               const float* dloss, const float* dlse, bool dx, bool dw, hipStream_t s) {
+  const long long run = round_up(up_div(f.n, slabs), CE_FEW_STEP);
+  f.chunk = (int)std::min<long long>(run, ce_few_chunk(TB));
+  int log_lanes = 0;
+  while (log_lanes < 6 && 4 << log_lanes < f.D) ++log_lanes;
+  // (with sixteen rows both gradients' registers would leave two waves a SIMD)
+  constexpr bool TOGETHER = TB <= 8;
+  const dim3 g((unsigned)up_div(f.D, CE_FEW_COLS), (unsigned)slabs);
+  if constexpr (TOGETHER)
+    if (dx && dw)
+      hipLaunchKernelGGL((ce_few_kernel<DT, TB, CE_FEW_DX | CE_FEW_DW>), g, dim3(CE_THREADS), 0, s, f,
+                         labels, lse, dloss, dlse, log_lanes);
+  if (dx && !(TOGETHER && dw))
+    hipLaunchKernelGGL((ce_few_kernel<DT, TB, CE_FEW_DX>), g, dim3(CE_THREADS), 0, s, f, labels, lse,
+                       dloss, dlse, log_lanes);
+  if (dw && !(TOGETHER && dx))
+    hipLaunchKernelGGL((ce_few_kernel<DT, TB, CE_FEW_DW>), g, dim3(CE_THREADS), 0, s, f, labels, lse,
+                       dloss, dlse, log_lanes);
+  return launched();
+}
+
+// Few rows: a product for a piece's logits, then both gradients in one pass.
+template <int DT>
+int few_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
+                 const float* lse, const float* dloss, const float* dlse, void* dX, int lddx,
+                 void* dW, int lddw, hipStream_t s) {
+  const unsigned esz = tensor_elem_bytes(DT);
+  CeLayout l = layout_of(a, 1);
+  const size_t least = sizes_of(a, 1, h->cus).least;
+  if (h->workspace_bytes < least) return SGEMM_ERR_SCRATCH;
+  CeFew f = {};
+  f.lds = (int)sum_cols(a);
+  f.slab = (size_t)a.T * f.lds;
+  // half of what is left over the least may go to slabs of dX's sums
+  int slabs = few_slabs(a, h->cus);
+  const size_t spare = (h->workspace_bytes - least) / 2 / (4 * f.slab);
+  if ((size_t)(slabs - 1) > spare) slabs = 1 + (int)spare;
+  l.fixed += 4 * f.slab * (slabs - 1);
+  const int cols = piece_columns(a, l, h->workspace_bytes);
+  if (cols == 0) return SGEMM_ERR_SCRATCH;
+  Carver c = {static_cast<char*>(h->workspace)};
+  f.ldz = (int)round_up(cols, 8);
+  float* z = c.take<float>(4 * (size_t)a.T * f.ldz);
+  f.sums = c.take<float>(4 * f.slab * slabs);
+  const size_t left = h->workspace_bytes - c.used;
+  sgemm_handle_s ph = product_handle(h, c.base + c.used, left < kProductBytes ? left : kProductBytes);
+  f.z = z;
+  f.T = a.T;
+  f.D = a.D;
+  f.alpha = a.alpha;
+  f.X = a.X;
+  f.ldx = a.ldx;
+  f.ldw = a.ldw;
+  f.lddw = lddw;
+  int st;
+  for (long long at = 0; at < a.V; at += cols) {
+    const int v0 = (int)at;
+    f.v0 = v0;
+    f.n = a.V - v0 < cols ? a.V - v0 : cols;
+    f.W = rows_from(a.W, v0, a.ldw, esz);
+    f.dW = dW != nullptr ? rows_from(dW, v0, lddw, esz) : nullptr;
+    f.first = v0 == 0;
+    st = product(&ph, DT, SGEMM_OP_N, SGEMM_OP_T, a.T, f.n, a.D, a.alpha, a.X, a.ldx, f.W, a.ldw,
+                 0.0f, z, f.ldz, s);
+    if (st != SGEMM_OK) return st;
+    const bool dx = dX != nullptr, dw = dW != nullptr;
+    st = a.T <= 4   ? launch_few<DT, 4>(f, slabs, labels, lse, dloss, dlse, dx, dw, s)
+         : a.T <= 8 ? launch_few<DT, 8>(f, slabs, labels, lse, dloss, dlse, dx, dw, s)
+                    : launch_few<DT, 16>(f, slabs, labels, lse, dloss, dlse, dx, dw, s);
+    if (st != SGEMM_OK) return st;
+  }
+  if (dX == nullptr) return SGEMM_OK;
+  hipLaunchKernelGGL(ce_few_rows_kernel<DT>, dim3((unsigned)up_div(a.D, 64), a.T),
+                     dim3(64 * CE_FEW_SUM_WAVES), 0, s, a.D, f.sums, f.lds, f.slab, slabs, a.alpha,
+                     labels, dloss, dlse, dX, lddx);
+  return launched();
+}
+
+// 32-bit, other sizes: z in place becomes dz, and the gradients are their own
 // sums.
 int backward32(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels,
                const float* lse, const float* dloss, const float* dlse, float* dX, int lddx,
@@ -682,7 +786,8 @@ int backward32(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labe
     st = launched();
     if (st != SGEMM_OK) return st;
   }
-  for (int v0 = 0; v0 < a.V; v0 += cols) {
+  for (long long at = 0; at < a.V; at += cols) {
+    const int v0 = (int)at;
     const int n = a.V - v0 < cols ? a.V - v0 : cols;
     const void* w = rows_from(a.W, v0, a.ldw, 4);
     st = product(&ph, DT, SGEMM_OP_N, SGEMM_OP_T, a.T, n, a.D, a.alpha, a.X, a.ldx, w, a.ldw, 0.0f,
@@ -712,6 +817,7 @@ int backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labels
              void* dW, int lddw, hipStream_t s) {
   if (a.T == 0) return zero<DT>(a.V, a.D, dW, lddw, s);
   if (h->workspace_bytes < sizes_of(a, 1, h->cus).least) return SGEMM_ERR_SCRATCH;
+  if (few(a)) return few_backward<DT>(h, a, labels, lse, dloss, dlse, dX, lddx, dW, lddw, s);
   if (packed(a, 1))
     return packed_backward<DT>(h, a, labels, lse, dloss, dlse, dX, lddx, dW, lddw, s);
   return backward32(h, a, labels, lse, dloss, dlse, static_cast<float*>(dX), lddx,

@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(CE_STATS_THREADS)
   loss[t] = y == CE_BAD ? NAN : (float)over + log_l;
 }
 
-// ---- backward over the library's products (32-bit X and W, few rows) ----------------
+// ---- backward over the library's products (32-bit X and W) --------------------------
 
 // A row's factors: dz = p * exp(z - lse) - q [v = label]; both 0 for a row
 // that counts for nothing.

@@ -143,6 +143,25 @@ def test_loss_and_gradients(handle, T, V, D, dt):
     p.check_backward()
 
 
+FEW = [(4, 1, 1), (1, 131, 1030), (8, 700, 260), (9, 64, 257), (16, 5000, 515), (7, 40000, 4),
+       (2, 20000, 300), (13, 63, 2), (8, 65, 9), (5, 12000, 96), (15, 129, 2050)]
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("T,V,D", FEW)
+def test_few_rows(handle, T, V, D, dt):
+    p = Problem(T, V, D, dt, seed=10, uneven=T % 2 == 1, pad=T % 4)
+    p.forward(handle)
+    p.check_forward()
+    p.backward(handle)
+    p.check_backward()
+    both = [t.clone() for t in (p.dX, p.dW)]
+    p.dX.zero_(), p.dW.zero_()
+    p.backward(handle, dW=None)
+    p.backward(handle, dX=None)
+    assert all(torch.equal(a, b) for a, b in zip(both, (p.dX, p.dW)))
+
+
 # 32-bit operands in planes: tiles enough of z, and of dW but for the last two
 # (forward in planes, backward over the library's products).
 WIDE = [(520, 16500, 300), (1100, 8200, 600), (4200, 2100, 2000), (513, 13057, 257), (520, 16500, 16),
@@ -183,7 +202,7 @@ def test_many_rows_few_words(handle, T, V, D, dt):
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))
-@pytest.mark.parametrize("T,V,D", [(5, 2050, 64), (130, 3000, 96), (300, 1111, 40),
+@pytest.mark.parametrize("T,V,D", [(5, 2050, 64), (16, 9000, 70), (8, 3000, 2), (130, 3000, 96), (300, 1111, 40),
                                    (550, 14000, 300)])
 def test_least_workspace_takes_small_pieces(T, V, D, dt):
     p = Problem(T, V, D, dt, seed=1)

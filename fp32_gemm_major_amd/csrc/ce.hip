@@ -617,9 +617,9 @@ int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels&
     if (dW != nullptr) {
       void* out = rows_from(dW, (size_t)v0, lddw, esz);
       // Up to 512 rows writing dW takes longer than its sums, and two small
-      // tiles a CU overlap better -- as long as the last-level cache takes the
-      // writes, in rows of 256 bytes (512 rows: 50001 x 1000 in 79 us against 86,
-      // 65536 x 4096 in 484 against 373).
+      // tiles a CU overlap better, as long as the last-level cache takes the
+      // writes (dz and dW, 128 rows: 50176 x 1024 in 77 us against 88, 65536 x
+      // 4096 in 392 against 358).
       const bool small = product_rows(a) <= 512 && 2 * (size_t)n * a.D <= kDzBytes;
       st = !small && big_tiles(n, a.D, h->cus)
                ? dw_piece<L256x256, DT>(a, n, d, xs, o.ldx, dp, count, dw_factor, out, lddw, s)
@@ -630,16 +630,17 @@ int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels&
     }
   }
   if (dX == nullptr) return SGEMM_OK;
-  const unsigned g = grid_of((unsigned long long)a.T * (unsigned)up_div(a.D, 8));
+  const int parts = x.slabs << (int)residues(a), lanes = parts >= 16 ? 8 : 1;
+  const unsigned g = grid_of((unsigned long long)a.T * (unsigned)up_div(a.D, 8) * lanes);
   if (g == 0) return SGEMM_ERR_UNSUPPORTED;
   if (bigx)
     hipLaunchKernelGGL((ce_dx_rows_kernel<L256x256, DT>), dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D,
                        count, pos, x.sums, x.lds, x.slab, (int)up_div(a.D, 256), h->cus, x.slabs,
-                       x.n_first, (int)residues(a), out_factor, dX, lddx);
+                       x.n_first, (int)residues(a), lanes, out_factor, dX, lddx);
   else
     hipLaunchKernelGGL((ce_dx_rows_kernel<L128x128, DT>), dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D,
                        count, pos, x.sums, x.lds, x.slab, (int)up_div(a.D, 128), h->cus, x.slabs,
-                       x.n_first, (int)residues(a), out_factor, dX, lddx);
+                       x.n_first, (int)residues(a), lanes, out_factor, dX, lddx);
   return launched();
 }
 

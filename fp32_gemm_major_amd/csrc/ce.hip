@@ -691,7 +691,9 @@ int launch_few(CeFew f, int slabs, const CeLabels& labels, const float* lse,
   while (log_lanes < 6 && 4 << log_lanes < f.D) ++log_lanes;
   // (with sixteen rows both gradients' registers would leave two waves a SIMD)
   constexpr bool TOGETHER = TB <= 8;
-  const dim3 g((unsigned)up_div(f.D, CE_FEW_COLS), (unsigned)slabs);
+  f.blocks = (int)up_div(f.D, CE_FEW_COLS);
+  f.splits = slabs;
+  const dim3 g((unsigned)(f.blocks * slabs));  // (at most 8192 of one, 1024 of the other)
   if constexpr (TOGETHER)
     if (dx && dw)
       hipLaunchKernelGGL((ce_few_kernel<DT, TB, CE_FEW_DX | CE_FEW_DW>), g, dim3(CE_THREADS), 0, s, f,

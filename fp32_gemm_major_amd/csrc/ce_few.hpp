@@ -10,12 +10,13 @@
 //
 // With the product before it, against packed rows (16-bit) and the library's
 // products (32-bit): bfloat16, 8 rows, 32000 words, 4096 columns 156 us, 235;
-// one row 131 (262 MB read twice and written once: 4.8 TB/s without dz's 15 us),
-// 235; 4 rows, 118231 x 2304 411, 506 (4.0 TB/s); 3 rows, 8829 x 513 24, 53.
-// 32-bit, 2 rows, 3259 x 37 17, 87; 4 rows, 112049 x 2884 899, 996.
+// one row 135 (262 MB read twice and written once), 235; 4 rows, 118231 x 2304
+// 387, 506; 3 rows, 8829 x 513 22, 53.  32-bit, 2 rows, 3259 x 37 16, 87; 4 rows,
+// 112049 x 2884 889, 996.
 #pragma once
 
 #include "ce.hpp"
+#include "tile_map.hpp"
 
 namespace sgemm {
 
@@ -73,7 +74,8 @@ __device__ __forceinline__ void values4(const Raw4<DT>& r, float (&v)[4]) {
   }
 }
 
-// (Not kept in the caches: dW, 118231 x 2304 bfloat16, 168 -> 137 us.)
+// (Not kept in the caches: dW, 118231 x 2304 bfloat16, 168 -> 137 us.  Kept where
+// rows are not whole lines: both gradients, 112049 x 2884 in 32 bits, 887 -> 927.)
 template <int DT>
 __device__ __forceinline__ void store4(typename TensorElem<DT>::type* p, int n,
                                        const float (&v)[4]) {
@@ -114,11 +116,13 @@ struct CeFew {
   float* sums;  // dX's, a slab of T rows of lds each split
   int lds, first;
   size_t slab;
+  int blocks, splits;  // of columns and of the piece's rows
 };
 
 // A workgroup takes 256 columns (a lane four of one row; where D is less, the
 // 1 << log_lanes lanes that a row needs, and several rows a wave) and a run of
-// the piece's rows: split blockIdx.y of gridDim.y.  dX's terms stay in
+// the piece's rows; the blocks of columns of a run share an XCD's L2, where the
+// lines that two of them write meet (118231 x 2304 bfloat16: 406 -> 387 us).  dX's terms stay in
 // registers over the run, X's in registers throughout; the parts of a run's
 // rows that its waves hold are joined in a fixed order and added to the split's
 // slab.
@@ -137,6 +141,8 @@ __global__ void __launch_bounds__(CE_THREADS)
   __shared__ int row_label[TB];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int at = xcd_run(blockIdx.x, a.blocks * a.splits);
+  const int split = at / a.blocks, block = at - split * a.blocks;
   if (tid < TB) {
     CeFactors f = {0.0f, 0.0f};
     int y = CE_IGNORED;
@@ -154,7 +160,7 @@ __global__ void __launch_bounds__(CE_THREADS)
   __syncthreads();
 
   const int lanes = 1 << log_lanes;
-  const int c = CE_FEW_COLS * blockIdx.x + 4 * (lane & (lanes - 1));
+  const int c = CE_FEW_COLS * block + 4 * (lane & (lanes - 1));
   const int have = a.D - c;                             // columns from c on
   const int group = (wave << (6 - log_lanes)) + (lane >> log_lanes);
   const int groups = CE_THREADS >> log_lanes;
@@ -171,8 +177,8 @@ __global__ void __launch_bounds__(CE_THREADS)
   }
 
   const int chunks = (a.n + a.chunk - 1) / a.chunk;
-  const int from = (int)((long long)chunks * blockIdx.y / gridDim.y);
-  const int to = (int)((long long)chunks * (blockIdx.y + 1) / gridDim.y);
+  const int from = (int)((long long)chunks * split / a.splits);
+  const int to = (int)((long long)chunks * (split + 1) / a.splits);
   for (int k = from; k < to; ++k) {
     const int r0 = k * a.chunk;
     const int rows = a.n - r0 < a.chunk ? a.n - r0 : a.chunk;
@@ -262,7 +268,7 @@ __global__ void __launch_bounds__(CE_THREADS)
         sum[3] += d.w;
       }
       // (lds is a multiple of four)
-      float4* s = reinterpret_cast<float4*>(a.sums + blockIdx.y * a.slab + (size_t)t * a.lds + c);
+      float4* s = reinterpret_cast<float4*>(a.sums + split * a.slab + (size_t)t * a.lds + c);
       if (!a.first) {
         const float4 d = *s;
         sum[0] += d.x;

@@ -530,7 +530,8 @@ int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K,
  * SGEMM_ERR_SCRATCH, and with less than `full` they take smaller pieces and
  * more launches.  Ownership, streams, errors and threading as for sgemm_run
  * with a workspace.  T == 0: nothing is read (backward: dW is set to 0).
- * SGEMM_ERR_SIZE for T < 0, V < 1, D < 1 or D over SGEMM_CE_MAX_D; SGEMM_ERR_LD for a stride below D;
+ * SGEMM_ERR_SIZE for T < 0, V < 1, D < 1 or D over SGEMM_CE_MAX_D;
+ * SGEMM_ERR_LD for a stride below D;
  * SGEMM_ERR_VALUE for another dtype or a tensor not aligned to its element;
  * SGEMM_ERR_ALIAS where an output overlaps another argument. */
 
@@ -555,8 +556,8 @@ int sgemm_ce_forward(sgemm_handle_t h, int dtype, int T, int V, int D,
  *
  * are overwritten (either may be NULL), of type dtype.  lse is a forward
  * call's.  dz is rounded to dtype between the two products (binary16: after a
- * power-of-two scale a row), their sums are FP32 and the results are rounded
- * once. */
+ * power-of-two scale a row; with up to 128 rows what the rounding leaves is
+ * kept too), their sums are FP32 and the results are rounded once. */
 int sgemm_ce_backward(sgemm_handle_t h, int dtype, int T, int V, int D,
                       float alpha, const void* X, int ldx, const void* W,
                       int ldw, const long long* labels, long long ignore,

@@ -259,6 +259,7 @@ struct CeSizes {
   size_t least, full;
 };
 CeSizes sizes_of(CeProblem a, int backward, int cus) {
+  if (a.T == 0) return CeSizes{0, 0};  // (dW is set to 0, if asked for)
   a.ldw = a.D;
   if (!packed(a, backward)) {
     const CeLayout l = layout_of(a, backward);

@@ -538,7 +538,8 @@ int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K,
 #define SGEMM_CE_MAX_D (1 << 21)
 
 /* Workspace of a forward (backward == 0) or a backward call: the least that
- * it runs with and what it makes use of; either pointer may be NULL. */
+ * it runs with and what it makes use of (both 0 for T == 0); either pointer
+ * may be NULL. */
 int sgemm_ce_workspace_size(sgemm_handle_t h, int dtype, int T, int V, int D,
                             int backward, size_t* least, size_t* full);
 

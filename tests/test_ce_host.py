@@ -1,6 +1,8 @@
 """The output layer's loss without a GPU: the plain implementation against
 differences and closed forms, and every refusal of the C entries and the
 binding."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -115,3 +117,32 @@ def test_binding_checks():
         sg._vectors(3, torch.int64, labels=torch.zeros(4, dtype=torch.int64))
     with pytest.raises(ValueError):
         sg._vectors(3, torch.float32, loss=torch.zeros(6)[::2])
+
+
+class HostHandle(ctypes.Structure):
+    """A handle as the library lays it out, for entries that launch nothing."""
+    _fields_ = [("device", ctypes.c_int), ("cus", ctypes.c_int), ("variant", ctypes.c_int),
+                ("forced_kernel", ctypes.c_int), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t), ("forced_lowp", ctypes.c_int)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("backward", [0, 1])
+def test_workspace_size(dtype, backward):
+    """An empty batch needs no workspace; other sizes grow with the rows."""
+    h = HostHandle(cus=256, forced_kernel=-1, forced_lowp=-1)
+    at = ctypes.addressof(h)
+    for V, D in ((1, 1), (32000, 4096), (300, 7)):
+        assert sg.sgemm_ce_workspace_size(at, dtype, 0, V, D, backward) == (0, 0)
+        last = (0, 0)
+        for T in (1, 16, 17, 511, 512, 5000):
+            size = sg.sgemm_ce_workspace_size(at, dtype, T, V, D, backward)
+            assert 0 < size[0] <= size[1]
+            if T in (16, 511, 5000):  # (with the row before it on one path)
+                assert size[0] > last[0]
+            last = size
+    for bad in (dict(T=-1), dict(V=0), dict(D=0)):
+        a = dict(T=0, V=1, D=1) | bad
+        with pytest.raises(sg.SgemmError) as e:
+            sg.sgemm_ce_workspace_size(at, dtype, a["T"], a["V"], a["D"], backward)
+        assert e.value.status == sg.SGEMM_ERR_SIZE

@@ -312,6 +312,20 @@ def test_no_rows(handle):
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))
+def test_no_rows_need_no_workspace(dt):
+    tt = DTYPES[dt]
+    X, W = torch.empty(0, 24, dtype=tt, device="cuda"), torch.ones(30, 24, dtype=tt, device="cuda")
+    Y, f = torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
+    dW = torch.full_like(W, 3.0)
+    with sg.Handle(workspace=False) as h:
+        h.set_workspace(h.ce_workspace_size(X, W))
+        h.ce_forward(X, W, Y, f, f.clone())
+        h.set_workspace(h.ce_workspace_size(X, W, backward=True))
+        h.ce_backward(X, W, Y, f, f, torch.empty_like(X), dW)
+    assert (dW == 0).all()
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
 @pytest.mark.parametrize("count", [0, 1, 127, 128, 255, 256, 257, 384, 512, 600])
 def test_rows_that_count_at_tile_edges(handle, count, dt):
     p = Problem(600, 1300, 72, dt, seed=6, ignored=0.0)

@@ -28,15 +28,20 @@ __device__ __forceinline__ float ce_exp(float x) {
   return __builtin_amdgcn_exp2f(x * CE_LOG2E);
 }
 
-// What is known of a row so far: sum l of exp(z - m), the label's logit.
+// What is known of a row so far: sum l of exp(z - m).  m is always finite --
+// the largest z, between the lowest and the largest 32-bit number -- so that
+// z - m is a NaN only where z is: a logit of -inf adds 0, whatever the others
+// are, and one of +inf makes l infinite.  A part with no values (or only -inf)
+// has l = 0.
+constexpr float CE_MOST = 3.402823466e38f;
 struct CeRow {
   float m, l;
 };
+__device__ __forceinline__ CeRow ce_no_values() { return CeRow{-CE_MOST, 0.0f}; }
 
-// Two parts of a row joined.  (A part with no values has m = -inf, l = 0.)
+// Two parts of a row joined.
 __device__ __forceinline__ CeRow ce_join(CeRow a, CeRow b) {
   const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return CeRow{m, a.l + b.l};
   return CeRow{m, a.l * ce_exp(a.m - m) + b.l * ce_exp(b.m - m)};
 }
 
@@ -98,10 +103,10 @@ __global__ void __launch_bounds__(CE_STATS_THREADS)
   __shared__ double dot[CE_STATS_WAVES];
   const int t = blockIdx.x;
   const float* row = z + (size_t)t * ldz;
-  CeRow r = {-INFINITY, 0.0f};
+  CeRow r = ce_no_values();
   // four values at c, those that are there
   auto take = [&](const float (&v)[4], int have) {
-    const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+    const float top = fminf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), CE_MOST);
     if (top > r.m) {
       r.l *= ce_exp(r.m - top);
       r.m = top;
@@ -170,8 +175,15 @@ __global__ void __launch_bounds__(CE_STATS_THREADS)
   if (y >= 0) {
 #pragma unroll
     for (int w = 1; w < CE_STATS_WAVES; ++w) d += dot[w];
-    over = (double)r.m - (double)in.alpha * d;
-    r.l += ce_exp(-(float)over) - ce_exp(zl - r.m);
+    // (infinite logits, and ones so large that their rounding alone would move
+    // the sum, stay as the product gives them)
+    const double exact = (double)in.alpha * d;
+    if (fabs((double)zl - exact) <= 0.5) {
+      over = (double)r.m - exact;
+      r.l += ce_exp(-(float)over) - ce_exp(zl - r.m);
+    } else {
+      over = (double)r.m - (double)zl;
+    }
   }
   const float log_l = logf(r.l);
   lse[t] = r.m + log_l;

@@ -1,0 +1,151 @@
+"""Words that a mask takes out of the output layer's loss, and other infinite
+logits, on the GPU against the plain 64-bit implementation (ce_reference).
+
+A mask is a column of W that meets a constant column of X: -inf (or, with a
+negative alpha, +inf) or the type's lowest value where a word is out, else 0.
+Such a word adds nothing to lse, so the reference takes -1e4 in its place,
+whose exponential is 0 in 64 bits, and the bounds are those of the other loss
+tests.  (dX's column of the mask is the sum of 0 * -inf: NaN.)"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+import fp32_gemm_major_amd as sg  # noqa: E402
+from tests import ce_reference as ref  # noqa: E402
+from tests.test_gpu_ce import DTYPES, U, Problem  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def handle():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    h = sg.Handle()
+    yield h
+    h.close()
+
+
+def masked(T, V, D, dt, words, value, column=0, alpha=0.5, seed=0, pad=0):
+    """A problem whose `words` are out, labels elsewhere; value: "inf" or "lowest"."""
+    p = Problem(T, V, D, dt, seed=seed, ignored=0.1, alpha=alpha, pad=pad)
+    out = np.zeros(V, bool)
+    out[words] = True
+    left = np.flatnonzero(~out)
+    hit = (p.labels != ref.IGNORE) & out[np.maximum(p.labels, 0)]
+    p.labels[hit] = left[p.labels[hit] % len(left)]
+    p.Y.copy_(torch.from_numpy(p.labels))
+    p.x[:, column], p.w[:, column] = 1.0, 0.0
+    sign = -1.0 if alpha > 0 else 1.0
+    p.w[out, column] = sign * 1e4
+    size = float("inf") if value == "inf" else torch.finfo(DTYPES[dt]).max
+    p.X[:, column] = 1.0
+    p.W[:, column] = 0.0
+    p.W[torch.from_numpy(out).cuda(), column] = sign * size
+    p.column, p.infinite = column, value == "inf"
+    return p
+
+
+def check(p, handle):
+    p.forward(handle)
+    p.check_forward()
+    p.backward(handle)
+    if p.infinite:
+        kept = p.Y != ref.IGNORE
+        assert torch.isnan(p.dX[kept, p.column]).all()
+        p.dX[kept, p.column] = 0.0
+    if p.alpha < 0:  # the same problem with -X and -alpha (check_backward's bounds grow with alpha)
+        p.alpha, p.x = -p.alpha, -p.x
+        p.dX.neg_()
+    p.check_backward()
+
+
+def runs(V):
+    """Sets of words: aligned runs of every reduction's width, ragged ones,
+    a vocabulary's padding, every word but one."""
+    return {"4": np.arange(8, 12), "64": np.arange(64, 128), "128": np.arange(128, 256),
+            "ragged": np.arange(3, 301), "half": np.arange(0, V, 2), "end": np.arange(V - 270, V),
+            "but one": np.delete(np.arange(V), V // 3)}
+
+
+# Over the library's products (up to 16 rows; 32-bit up to 511 rows or few
+# tiles): statistics a row.
+@pytest.mark.parametrize("value", ["inf", "lowest"])
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("words", ["4", "64", "128", "ragged", "half", "end", "but one"])
+@pytest.mark.parametrize("T", [1, 7, 16])
+def test_masked_words_few_rows(handle, T, words, dt, value):
+    V = 18000 if words == "128" else 1300
+    check(masked(T, V, 48, dt, runs(V)[words], value), handle)
+
+
+@pytest.mark.parametrize("value", ["lowest"])
+@pytest.mark.parametrize("words", ["4", "ragged", "but one"])
+def test_masked_words_32_bit_library_products(handle, words, value):
+    check(masked(90, 1300, 48, "f32", runs(1300)[words], value), handle)
+
+
+def test_negative_scale_few_rows(handle):
+    for dt in DTYPES:
+        check(masked(7, 1300, 48, dt, np.arange(3, 301), "inf", alpha=-0.5), handle)
+        check(masked(7, 1300, 48, dt, np.arange(3, 301), "lowest", alpha=-0.5), handle)
+
+
+PATHS = [(5, 900, 40, "bf16"), (5, 900, 40, "f16"), (5, 900, 40, "f32"), (90, 900, 40, "f32")]
+
+
+@pytest.mark.parametrize("T,V,D,dt", PATHS)
+def test_no_word_left(handle, T, V, D, dt):
+    """Every word at the type's lowest value: lse is it (as far as 32 bits hold
+    it), the loss the logarithm of V where the others' part of the logits is
+    lost beside it, and every gradient finite but where the sums leave the type;
+    at -inf: lse is -inf, the loss NaN."""
+    p = masked(T, V, D, dt, np.arange(V - 1), "lowest", seed=2)
+    low = torch.finfo(DTYPES[dt]).min
+    p.w[:, 0] = low
+    p.W[:, 0] = low
+    p.forward(handle)
+    keep = p.labels != ref.IGNORE
+    if dt == "f16":
+        p.check_forward()
+    else:
+        for one in (1.0, 1.0 - 5 * 2.0 ** -7):  # (x w itself is in range)
+            p.X[:, 0] = one
+            p.forward(handle)
+            got = p.lse.double().cpu().numpy()[keep]
+            assert np.all(np.abs(got - 0.5 * one * low) <= 4 * U * abs(low)), got[:4]
+            got = p.loss.double().cpu().numpy()[keep]
+            assert np.all(np.abs(got - np.log(V)) <= p.sum_error() + 8 * U * np.log(V)), got[:4]
+    p.backward(handle)
+    assert not torch.isnan(p.dW[:, 1:]).any()
+    p.W[:, 0] = float("-inf")
+    p.forward(handle)
+    assert (p.lse.cpu().numpy()[keep] == -np.inf).all()
+    assert torch.isnan(p.loss).cpu().numpy()[keep].all()
+    assert (p.loss.cpu().numpy()[~keep] == 0).all() and (p.lse.cpu().numpy()[~keep] == 0).all()
+
+
+@pytest.mark.parametrize("T,V,D,dt", PATHS)
+def test_infinite_and_nan_logits(handle, T, V, D, dt):
+    """One word at +inf: lse is +inf, and the loss but for rows labelled with
+    that word (inf - inf).  A label at -inf costs +inf.  One word at NaN:
+    everything is."""
+    p = masked(T, V, D, dt, [V // 2], "inf", seed=3)
+    p.labels[:] = np.arange(T) % 5
+    p.labels[1] = V // 2
+    p.labels[3] = ref.IGNORE
+    p.Y.copy_(torch.from_numpy(p.labels))
+    keep = p.labels != ref.IGNORE
+    p.forward(handle)
+    lse, loss = p.lse.cpu().numpy(), p.loss.cpu().numpy()
+    assert np.isfinite(lse[keep]).all() and loss[1] == np.inf
+    assert np.isfinite(np.delete(loss, 1)).all()
+    p.W[V // 2, 0] = float("inf")
+    p.forward(handle)
+    lse, loss = p.lse.cpu().numpy(), p.loss.cpu().numpy()
+    assert (lse[keep] == np.inf).all() and np.isnan(loss[1]) and loss[3] == 0
+    assert (np.delete(loss, [1, 3]) == np.inf).all()
+    p.W[V // 2, 0] = float("nan")
+    p.forward(handle)
+    assert np.isnan(p.lse.cpu().numpy()[keep]).all() and np.isnan(p.loss.cpu().numpy()[keep]).all()

@@ -289,7 +289,7 @@ struct CePiece {
 };
 
 template <class T>
-CePiece piece_of(const CeProblem& a, int M, int N, int K, float c, const void* A, int lda,
+CePiece piece_of(const CeProblem& a, int M, int N, int K, const void* A, int lda,
                  const void* B, int ldb, const int* count, LpPlanes planes = LpPlanes{0, 0}) {
   CePiece p = {};
   p.gemm.planes = planes;
@@ -301,7 +301,7 @@ CePiece piece_of(const CeProblem& a, int M, int N, int K, float c, const void* A
   p.gemm.g.lda = lda;
   p.gemm.g.B = B;
   p.gemm.g.ldb = ldb;
-  p.gemm.c = c;
+  p.gemm.scale = ce_scale(a.alpha);
   p.gemm.count = count;
   p.tiles_m = (int)up_div(M, T::BM);
   p.tiles_n = (int)up_div(N, T::BN);
@@ -385,7 +385,7 @@ template <class T, int DT>
 int logits_piece(const CeProblem& a, int n, const CeOperands& o, const int* label, int v0,
                  CeRow* part, int rows, float* zlabel, hipStream_t s) {
   constexpr int MT = product_type(DT);
-  const CePiece p = piece_of<T>(a, a.T, n, a.D, a.alpha * CE_LOG2E, o.x, o.ldx, o.w, o.ldw, o.count,
+  const CePiece p = piece_of<T>(a, a.T, n, a.D, o.x, o.ldx, o.w, o.ldw, o.count,
                                 LpPlanes{o.plane, o.plane});
   if constexpr (DT == SGEMM_DTYPE_F32)
     return launch_logits<T, MT, MODE_PLANES>(p, label, v0, part, rows, zlabel, s);
@@ -480,7 +480,7 @@ int packed_forward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& 
     const int chunks = (int)up_div(n, big ? L256x256::WN : L128x128::WN);
     hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)up_div(a.T, CE_JOIN_ROWS)),
                        dim3(CE_JOIN_ROWS * CE_JOIN_LANES), 0, s, part, chunks, Tp, count, order,
-                       label, state, a.alpha * CE_LOG2E, zlabel, v0 == 0, v0 + n == a.V, loss, lse);
+                       label, state, ce_scale(a.alpha), zlabel, v0 == 0, v0 + n == a.V, loss, lse);
     st = launched();
     if (st != SGEMM_OK) return st;
   }
@@ -497,7 +497,7 @@ template <class T, int DT>
 int dz_piece(const CeProblem& a, int n, const CeOperands& o, const CeRowInfo* info, int v0,
              const CeDz& d, hipStream_t s) {
   constexpr int MT = product_type(DT);
-  const CePiece p = piece_of<T>(a, a.T, n, a.D, a.alpha * CE_LOG2E, o.x, o.ldx, o.w, o.ldw, o.count,
+  const CePiece p = piece_of<T>(a, a.T, n, a.D, o.x, o.ldx, o.w, o.ldw, o.count,
                                 LpPlanes{o.plane, o.plane});
   if constexpr (DT == SGEMM_DTYPE_F32)
     return launch_dz<T, MT, MODE_PLANES>(p, info, v0, d.dz, 3 * d.lddz, d.lddz, 0, s);
@@ -520,7 +520,7 @@ int dx_piece(const CeProblem& a, int n, const CeOperands& o, const CeDz& d, int 
              const void* w_tail, const CeSums& x, float beta, hipStream_t s) {
   constexpr int MT = product_type(DT);
   constexpr bool WIDE = DT == SGEMM_DTYPE_F32;
-  CePiece p = piece_of<T>(a, product_rows(a), a.D, n, 0.0f, d.dz, WIDE ? 3 * d.lddz : d.lddz, o.w,
+  CePiece p = piece_of<T>(a, product_rows(a), a.D, n, d.dz, WIDE ? 3 * d.lddz : d.lddz, o.w,
                           o.ldw, o.count + 1, LpPlanes{d.lddz, o.plane});
   p.gemm.g.beta = beta;
   p.gemm.g.ldc = x.lds;
@@ -538,7 +538,7 @@ int dw_piece(const CeProblem& a, int n, const CeDz& d, const void* xs, int ldxs,
              const int* count, const float* factor, void* out, int ldo, hipStream_t s) {
   constexpr int MT = product_type(DT);
   constexpr bool WIDE = DT == SGEMM_DTYPE_F32;
-  const CePiece p = piece_of<T>(a, n, a.D, product_rows(a), 0.0f, d.dz, WIDE ? 3 * d.lddz : d.lddz,
+  const CePiece p = piece_of<T>(a, n, a.D, product_rows(a), d.dz, WIDE ? 3 * d.lddz : d.lddz,
                                 xs, ldxs, count + 1, LpPlanes{d.lddz, dp});
   return launch_dw<T, MT, WIDE ? MODE_PLANES : MODE_ALIGNED>(p, factor, out, ldo, s);
 }

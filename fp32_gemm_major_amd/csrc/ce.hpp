@@ -486,22 +486,33 @@ __global__ void __launch_bounds__(CE_THREADS)
   store8<DT>(static_cast<E*>(copy) + (size_t)r * ld + c, 8, v);
 }
 
-// As ce_join, with m in units of log2.
-__device__ __forceinline__ CeRow ce_join2(CeRow a, CeRow b) {
+// As ce_join, with m a value of x w in alpha's direction (CeScale).
+__device__ __forceinline__ CeRow ce_join2(CeRow a, CeRow b, float c) {
   const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return CeRow{m, a.l + b.l};
-  return CeRow{m, a.l * __builtin_amdgcn_exp2f(a.m - m) + b.l * __builtin_amdgcn_exp2f(b.m - m)};
+  return CeRow{m, a.l * __builtin_amdgcn_exp2f((a.m - m) * c) +
+                      b.l * __builtin_amdgcn_exp2f((b.m - m) * c)};
+}
+
+// Packed rows' parts hold the largest of sign * x w, not of the logit: its
+// product with |alpha| (or with log2(e)) may leave 32 bits where x w does not
+// -- a mask's lowest value -- and its rounding would be lse's.
+struct CeScale {
+  float sign, size, c;  // alpha's; c = size * log2(e)
+};
+__host__ __device__ inline CeScale ce_scale(float alpha) {
+  const float size = fabsf(alpha);
+  return CeScale{alpha < 0.0f ? -1.0f : 1.0f, size, size * CE_LOG2E};
 }
 
 // Joins a piece's parts (part[chunk][row], rows of the stride `padded`) into
-// the packed rows' state (m in units of log2, c = alpha * log2(e), zlabel the
-// labels' x w); the last piece writes the rows' loss and lse.  A
-// workgroup takes 32 rows, 32 lanes a row stride over its chunks.
+// the packed rows' state (zlabel: the labels' x w); the last piece writes the
+// rows' loss and lse.  A workgroup takes 32 rows, 32 lanes a row stride over
+// its chunks.
 constexpr int CE_JOIN_ROWS = 32, CE_JOIN_LANES = 32;
 static __global__ void __launch_bounds__(CE_JOIN_ROWS * CE_JOIN_LANES)
     ce_join_kernel(const CeRow* __restrict__ part, int chunks, int padded,
                    const int* __restrict__ count, const int* __restrict__ order,
-                   const int* __restrict__ label, CeRow* __restrict__ state, float c,
+                   const int* __restrict__ label, CeRow* __restrict__ state, CeScale a,
                    const float* __restrict__ zlabel, int first, int last, float* __restrict__ loss,
                    float* __restrict__ lse) {
   __shared__ CeRow sh[CE_JOIN_LANES * CE_JOIN_ROWS];
@@ -510,35 +521,36 @@ static __global__ void __launch_bounds__(CE_JOIN_ROWS * CE_JOIN_LANES)
   if (row0 >= n) return;
   const int lr = threadIdx.x % CE_JOIN_ROWS, lane = threadIdx.x / CE_JOIN_ROWS;
   const int row = row0 + lr;
-  CeRow r = {-INFINITY, 0.0f};
+  CeRow r = ce_no_values();
   int k = lane;
   for (; k + 3 * CE_JOIN_LANES < chunks; k += 4 * CE_JOIN_LANES) {
     CeRow x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = part[(size_t)(k + i * CE_JOIN_LANES) * padded + row];
-    r = ce_join2(r, ce_join2(ce_join2(x[0], x[1]), ce_join2(x[2], x[3])));
+    r = ce_join2(r, ce_join2(ce_join2(x[0], x[1], a.c), ce_join2(x[2], x[3], a.c), a.c), a.c);
   }
-  for (; k < chunks; k += CE_JOIN_LANES) r = ce_join2(r, part[(size_t)k * padded + row]);
+  for (; k < chunks; k += CE_JOIN_LANES) r = ce_join2(r, part[(size_t)k * padded + row], a.c);
   sh[threadIdx.x] = r;
   __syncthreads();
   for (int d = CE_JOIN_LANES / 2; d > 0; d >>= 1) {
-    if (lane < d) sh[threadIdx.x] = ce_join2(sh[threadIdx.x], sh[threadIdx.x + d * CE_JOIN_ROWS]);
+    if (lane < d)
+      sh[threadIdx.x] = ce_join2(sh[threadIdx.x], sh[threadIdx.x + d * CE_JOIN_ROWS], a.c);
     __syncthreads();
   }
   if (lane != 0 || row >= n) return;
   r = sh[threadIdx.x];
-  if (!first) r = ce_join2(state[row], r);
+  if (!first) r = ce_join2(state[row], r, a.c);
   if (!last) {
     state[row] = r;
     return;
   }
   const int t = order[row], y = label[row];
   constexpr float LN2 = 0.693147180559945309417f;
-  const float l = log2f(r.l);
-  lse[t] = (r.m + l) * LN2;
-  // (m - c * x w is exact but for one rounding: the terms are about the loss's
-  // own size, so a label that is nearly certain keeps its small loss's bits)
-  loss[t] = y == CE_BAD ? NAN : (fmaf(-c, zlabel[row], r.m) + l) * LN2;
+  const float l = log2f(r.l) * LN2;
+  lse[t] = fmaf(a.size, r.m, l);
+  // (m - x w is 0 where the label is the largest, so a label that is nearly
+  // certain keeps its small loss's bits)
+  loss[t] = y == CE_BAD ? NAN : fmaf(a.size, fmaf(-a.sign, zlabel[row], r.m), l);
 }
 
 }  // namespace sgemm

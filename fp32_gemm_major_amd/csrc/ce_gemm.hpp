@@ -36,7 +36,7 @@ typedef LpTile<128, 128, 64, 64, 2, 2> L128x128s;
 
 struct CeGemm {
   LpArgs g;          // A: packed rows, B: W's piece; M, N, K of the product
-  float c;           // alpha * log2(e) (logits)
+  CeScale scale;     // alpha's (logits)
   const int* count;  // rows that count
   LpPlanes planes;   // split operands: A's and B's plane strides
 };
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
   const int col0 = n0 + w.wn * T::WN;  // the wave's first column
   const int have = a.g.N - col0;
   if (have <= 0) return;
-  const float c = a.c;
+  const float sign = a.scale.sign, c = a.scale.c;
 #pragma unroll
   for (int i = 0; i < T::FM; ++i) {
     const int row = m0 + w.wm * T::WM + 32 * i + w.li;
@@ -116,33 +116,32 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
           if (y == 32 * j + 8 * (k / 4) + 4 * w.lh + k % 4) z = acc[i][j][k];
       if (y >= 0 && y < T::WN && y < have && ((y >> 2) & 1) == w.lh) zlabel[row] = z;
     }
-    // t = z * log2(e): m = max t, l = sum 2^(t - m).  The difference is one
-    // fused multiply-add, so only m's own rounding enters lse.
-    float m = -INFINITY, l = 0.0f;
+    // m = max(sign * x w), kept finite (see CeRow), l = sum 2^(c (sign * x w - m))
+    float m = -CE_MOST, l = 0.0f;
     if (have >= T::WN) {
 #pragma unroll
       for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) m = fmaxf(m, c * acc[i][j][k]);
-      m = fmaxf(m, __shfl_xor(m, 32));
+        for (int k = 0; k < 16; ++k) m = fmaxf(m, sign * acc[i][j][k]);
+      m = fminf(fmaxf(m, __shfl_xor(m, 32)), CE_MOST);
 #pragma unroll
       for (int j = 0; j < T::FN; ++j)
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          l += __builtin_amdgcn_exp2f(fmaf(c, acc[i][j][k], -m));
+          l += __builtin_amdgcn_exp2f(c * fmaf(sign, acc[i][j][k], -m));
     } else {
 #pragma unroll
       for (int j = 0; j < T::FN; ++j)
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          if (32 * j + 8 * (k / 4) + 4 * w.lh + k % 4 < have) m = fmaxf(m, c * acc[i][j][k]);
-      m = fmaxf(m, __shfl_xor(m, 32));
+          if (32 * j + 8 * (k / 4) + 4 * w.lh + k % 4 < have) m = fmaxf(m, sign * acc[i][j][k]);
+      m = fminf(fmaxf(m, __shfl_xor(m, 32)), CE_MOST);
 #pragma unroll
       for (int j = 0; j < T::FN; ++j)
 #pragma unroll
         for (int k = 0; k < 16; ++k)
           if (32 * j + 8 * (k / 4) + 4 * w.lh + k % 4 < have)
-            l += __builtin_amdgcn_exp2f(fmaf(c, acc[i][j][k], -m));
+            l += __builtin_amdgcn_exp2f(c * fmaf(sign, acc[i][j][k], -m));
     }
     l += __shfl_xor(l, 32);
     if (w.lh == 0) part[(size_t)(col0 / T::WN) * rows + row] = CeRow{m, l};
@@ -176,7 +175,7 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
   const WaveCoords<T> w;
   const int col0 = n0 + w.wn * T::WN;
   const int have = a.g.N - col0;
-  const float c = a.c;
+  const float c = a.scale.sign * a.scale.c;
   float* reg = reinterpret_cast<float*>(lds) + w.wave * 32 * LD;
   const int rr = w.lane / LPR, cc = 8 * (w.lane % LPR);
   const int second = residues ? ce_residue_row(*a.count) : 0;

@@ -92,7 +92,33 @@ def test_negative_scale_few_rows(handle):
         check(masked(7, 1300, 48, dt, np.arange(3, 301), "lowest", alpha=-0.5), handle)
 
 
+# Packed rows: parts of 64 and 128 words a wave.
+@pytest.mark.parametrize("value", ["inf", "lowest"])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("words", ["4", "64", "128", "ragged", "half", "end", "but one"])
+@pytest.mark.parametrize("T,D", [(40, 64), (300, 128)])
+def test_masked_words_packed_rows(handle, T, D, words, dt, value):
+    check(masked(T, 1300, D, dt, runs(1300)[words], value), handle)
+
+
+@pytest.mark.parametrize("words", ["4", "64", "128", "end", "but one"])
+def test_masked_words_big_tiles(handle, words):
+    check(masked(300, 20000, 64, "bf16", runs(20000)[words], "inf"), handle)
+
+
+@pytest.mark.parametrize("words", ["64", "128", "ragged", "but one"])
+def test_lowest_words_in_planes(handle, words):
+    check(masked(600, 13200, 264, "f32", runs(13200)[words], "lowest"), handle)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_negative_scale_packed_rows(handle, dt):
+    for value in ("inf", "lowest"):
+        check(masked(40, 1300, 64, dt, np.arange(3, 301), value, alpha=-0.5), handle)
+
+
 PATHS = [(5, 900, 40, "bf16"), (5, 900, 40, "f16"), (5, 900, 40, "f32"), (90, 900, 40, "f32")]
+PACKED = [(40, 900, 64, "bf16"), (40, 900, 64, "f16"), (300, 20000, 64, "bf16")]
 
 
 @pytest.mark.parametrize("T,V,D,dt", PATHS)
@@ -126,7 +152,7 @@ def test_no_word_left(handle, T, V, D, dt):
     assert (p.loss.cpu().numpy()[~keep] == 0).all() and (p.lse.cpu().numpy()[~keep] == 0).all()
 
 
-@pytest.mark.parametrize("T,V,D,dt", PATHS)
+@pytest.mark.parametrize("T,V,D,dt", PATHS + PACKED)
 def test_infinite_and_nan_logits(handle, T, V, D, dt):
     """One word at +inf: lse is +inf, and the loss but for rows labelled with
     that word (inf - inf).  A label at -inf costs +inf.  One word at NaN:

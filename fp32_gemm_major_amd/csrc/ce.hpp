@@ -266,10 +266,10 @@ __global__ void __launch_bounds__(CE_THREADS) ce_zero_kernel(int rows, int D, vo
 
 // ---- packed rows ------------------------------------------------
 
-// What a packed row's product epilogues need: the factors of dz, lse * log2(e)
-// and the label (CE_IGNORED for padding rows, whose factors are 0).
+// What a packed row's product epilogues need: the factors of dz, lse and the
+// label (CE_IGNORED for padding rows, whose factors are 0).
 struct CeRowInfo {
-  float p, q, lse2;
+  float p, q, lse;
   int label;
 };
 
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(CE_PACK_THREADS)
     if (at >= 0) {
       if (UNIT) f.p /= unit, f.q /= unit;
       const int k = SCALED ? exponent(fmaxf(fabsf(f.p), fabsf(f.q))) : 13;
-      info[at] = CeRowInfo{ldexpf(f.p, 13 - k), ldexpf(f.q, 13 - k), lse[t] * CE_LOG2E, y};
+      info[at] = CeRowInfo{ldexpf(f.p, 13 - k), ldexpf(f.q, 13 - k), lse[t], y};
       x_factor[at] = ldexpf(1.0f, k - kmax);
       out_factor[at] = ldexpf(scale, k - 13);
     }

@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
   const WaveCoords<T> w;
   const int col0 = n0 + w.wn * T::WN;
   const int have = a.g.N - col0;
-  const float c = a.scale.sign * a.scale.c;
+  const float alpha = a.g.alpha;
   float* reg = reinterpret_cast<float*>(lds) + w.wave * 32 * LD;
   const int rr = w.lane / LPR, cc = 8 * (w.lane % LPR);
   const int second = residues ? ce_residue_row(*a.count) : 0;
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC)
     for (int j = 0; j < T::FN; ++j)
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const float p = f.p * __builtin_amdgcn_exp2f(fmaf(c, acc[i][j][k], -f.lse2));
+        const float p = f.p * ce_exp(fmaf(alpha, acc[i][j][k], -f.lse));
         acc[i][j][k] = counts ? p : 0.0f;
       }
     const int y = f.label - v0 - col0;

@@ -121,7 +121,7 @@ PATHS = [(5, 900, 40, "bf16"), (5, 900, 40, "f16"), (5, 900, 40, "f32"), (90, 90
 PACKED = [(40, 900, 64, "bf16"), (40, 900, 64, "f16"), (300, 20000, 64, "bf16")]
 
 
-@pytest.mark.parametrize("T,V,D,dt", PATHS)
+@pytest.mark.parametrize("T,V,D,dt", PATHS + PACKED)
 def test_no_word_left(handle, T, V, D, dt):
     """Every word at the type's lowest value: lse is it (as far as 32 bits hold
     it), the loss the logarithm of V where the others' part of the logits is
@@ -151,6 +151,30 @@ def test_no_word_left(handle, T, V, D, dt):
     assert torch.isnan(p.loss).cpu().numpy()[keep].all()
     assert (p.loss.cpu().numpy()[~keep] == 0).all() and (p.lse.cpu().numpy()[~keep] == 0).all()
 
+
+@pytest.mark.parametrize("T,V,D,dt", [a for a in PATHS + PACKED if a[3] != "f16"] + [(4200, 8200, 520, "f32")])
+def test_gradients_where_no_word_is_left(T, V, D, dt):
+    """Logits and lse at the type's lowest value, whose product with log2(e)
+    leaves 32 bits: their difference is 0 and exp(z - lse) is 1, so dz is
+    dloss + dlse less dloss at the label, off by its rounding to 16 bits."""
+    p = masked(T, V, D, dt, np.arange(V - 1), "lowest", alpha=1.0, seed=2)
+    p.W[:, 0] = torch.finfo(DTYPES[dt]).min
+    with sg.Handle(workspace=False) as h:
+        h.set_workspace(max(h.ce_workspace_size(p.X, p.W, backward=b) for b in (False, True)))
+        p.forward(h)
+        p.backward(h)
+    keep = p.labels != ref.IGNORE
+    dz = ref.dlogits(np.zeros((T, V)), p.labels, np.zeros(T), p.dloss, p.dlse)
+    dx, dw = ref.gradients(p.x, p.w, p.labels, dz)
+    half = torch.finfo(DTYPES[dt]).eps / 2
+    ez = (half + 4 * U) * np.abs(dz)
+    ax, aw = np.abs(np.where(keep[:, None], p.x, 0.0)), np.abs(p.w)
+    for got, want, err, mag in ((p.dX, dx, ez @ aw, 4 * V * U * (np.abs(dz) @ aw)),
+                                (p.dW, dw, ez.T @ ax, 4 * T * U * (np.abs(dz).T @ ax))):
+        bound = err + mag
+        bound = bound + half * (np.abs(want) + bound) + 4 * U * np.abs(want)
+        off = np.abs(got.double().cpu().numpy() - want)[:, 1:]
+        assert np.all(off <= bound[:, 1:]), np.nanmax(off - bound[:, 1:])
 
 @pytest.mark.parametrize("T,V,D,dt", PATHS + PACKED)
 def test_infinite_and_nan_logits(handle, T, V, D, dt):

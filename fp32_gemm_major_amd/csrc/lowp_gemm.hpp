@@ -58,10 +58,11 @@
 // * Padded kernels (the output layer's loss; not in the product table) run
 //   the aligned schedule on an A whose rows and k are padded with zeros to
 //   whole tiles and steps, against a B of any sizes: rows and pieces past N
-//   are clamped as in edge kernels, a K-contiguous B's units past K move back
-//   to the row's last one (K a multiple of a unit), and an outer-contiguous
-//   B's last, partial step is read from a copy whose missing rows are zeros.
-//   What is read in place of a missing k meets A's zeros.
+//   are clamped as in edge kernels, a K-contiguous B's units past K are read
+//   from the row's last one (K a multiple of a unit) and zeroed in LDS once
+//   they have landed (an infinity in that unit would meet A's zeros), and an
+//   outer-contiguous B's last, partial step is read from a copy whose missing
+//   rows are zeros.
 // * Global loads of both kinds, direct-to-LDS ones included, take any byte
 //   address on gfx950 (checked with in-bounds probes at 1- and 2-byte
 //   offsets): no kernel needs aligned leading dimensions or base pointers.
@@ -796,6 +797,11 @@ __device__ __forceinline__ void lp_tile_accumulate(const LpArgs& g, char* lds,
       const bool straddle = (!A_KC && (M & (UE - 1)) != 0) || (!B_KC && (N & (UE - 1)) != 0);
       kd = straddle ? (K - 1) / BKE : K / BKE;
     }
+    // Padded kernels load a step in which a K-contiguous B ends like the
+    // others, but compute it after the loop.
+    const bool past_k = PAD && B_KC && K % BKE != 0;
+    const int loads = kd;
+    if (past_k) kd = nk - 1;
     constexpr int H = QG / 2;  // groups the reads run ahead (the barrier precedes group H)
     Frag fr[QG];
     auto group = [&](int kl, bool live, auto st_c, auto q_c) {
@@ -824,8 +830,8 @@ __device__ __forceinline__ void lp_tile_accumulate(const LpArgs& g, char* lds,
     constexpr int AHEAD = (S - 2) * ND;
     constexpr int WAIT_AHEAD = 0x0F70 | (AHEAD & 15) | ((AHEAD >> 4) << 14);
     auto step = [&](int kt, auto st_c) {
-      const bool live = kt + S < kd;
-      const int kl = live ? kt + S : kd - 1;
+      const bool live = kt + S < loads;
+      const int kl = live ? kt + S : loads - 1;
       lp_static_for<H>([&](auto q_c) { group(kl, live, st_c, q_c); });
       wait_lds();
       __builtin_amdgcn_s_waitcnt(WAIT_AHEAD);
@@ -840,7 +846,7 @@ __device__ __forceinline__ void lp_tile_accumulate(const LpArgs& g, char* lds,
       // first barrier.
       lp_static_for<S>([&](auto i) {
         constexpr int st = decltype(i)::value;
-        issue_step(st < kd ? st : kd - 1, st, st < kd);
+        issue_step(st < loads ? st : loads - 1, st, st < loads);
       });
       constexpr int FIRST = (S - 1) * ND;
       __builtin_amdgcn_s_waitcnt(0x0F70 | (FIRST & 15) | ((FIRST >> 4) << 14));
@@ -855,6 +861,28 @@ __device__ __forceinline__ void lp_tile_accumulate(const LpArgs& g, char* lds,
       lp_static_for<S - 1>([&](auto i) {
         if (kt + decltype(i)::value < kd) step(kt + decltype(i)::value, i);
       });
+    }
+    if (PAD && B_KC && past_k) {
+      // Zeros over the lane's own units past K, which have landed long since.
+      // (777 rows, 389 counting, 50001 words, 1000 columns: 2.2 of 78 us;
+      // before the barrier that shows the step, in the loop, 2.8.)
+      const int st = kd % S;
+      wait_all();
+      if (b_back != 0) {
+#pragma unroll
+        for (int v = 0; v < T::B_VEC; ++v)
+          *reinterpret_cast<u32x4*>(lds + b_off(st) + 16 * ((v * T::WAVES + wave) * 64 + lane)) =
+              u32x4{0u, 0u, 0u, 0u};
+      }
+      wait_lds();
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < QG; ++q) {
+        Frag f;
+        read_frag(st, q, f);
+#pragma unroll
+        for (int m = 0; m < SL; ++m) mma_one(f, m);
+      }
     }
     if (EDGE && kd < nk) {
       // The rest of K (at most one step) through registers, zero-filled past

@@ -199,3 +199,18 @@ def test_infinite_and_nan_logits(handle, T, V, D, dt):
     p.W[V // 2, 0] = float("nan")
     p.forward(handle)
     assert np.isnan(p.lse.cpu().numpy()[keep]).all() and np.isnan(p.loss.cpu().numpy()[keep]).all()
+
+
+# An infinity where D ends inside a K step of the products.
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [8, 40, 72, 120, 200, 264, 1000])
+@pytest.mark.parametrize("T", [20, 300])
+def test_masks_in_the_last_columns(handle, T, D, dt):
+    for column in (D - 1, D - 8):
+        check(masked(T, 1300, D, dt, np.arange(60, 400), "inf", column=column, seed=4), handle)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_masks_in_the_last_columns_big_tiles(handle, dt):
+    for D in (40, 328):
+        check(masked(300, 20001, D, dt, np.arange(60, 400), "inf", column=D - 1, seed=4), handle)

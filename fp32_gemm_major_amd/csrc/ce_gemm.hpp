@@ -42,14 +42,24 @@ struct CeGemm {
 };
 
 // x = h + m + l in three bfloat16 planes (bit patterns).  Values that would
-// round past the largest bfloat16 are truncated; infinities and NaNs are all h.
+// round past the largest bfloat16 are truncated.  An infinity stands in l, which
+// meets the other operand's h alone (LP_PLANE_PRODUCTS): its sign, and a NaN
+// only from 0; in h it would also meet m and l, zeros or of the other sign.  h
+// and m are 2^-64 with its sign, so that another infinity's l makes no NaN
+// there.  A NaN is all h.
 __device__ __forceinline__ void ce_split3(float x, uint16_t (&p)[3]) {
-  p[0] = elem_bits<SGEMM_DTYPE_BF16>(x);
-  const bool finite = (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u;
-  if ((p[0] & 0x7f80u) == 0x7f80u && finite) p[0] = (uint16_t)(__float_as_uint(x) >> 16);
-  const float r = x - elem_value<SGEMM_DTYPE_BF16>(p[0]);
-  p[1] = finite ? elem_bits<SGEMM_DTYPE_BF16>(r) : (uint16_t)0;
-  p[2] = finite ? elem_bits<SGEMM_DTYPE_BF16>(r - elem_value<SGEMM_DTYPE_BF16>(p[1])) : (uint16_t)0;
+  const unsigned bits = __float_as_uint(x);
+  uint16_t h = elem_bits<SGEMM_DTYPE_BF16>(x);
+  const bool finite = (bits & 0x7f800000u) != 0x7f800000u;
+  const bool infinite = (bits & 0x7fffffffu) == 0x7f800000u;
+  if ((h & 0x7f80u) == 0x7f80u && finite) h = (uint16_t)(bits >> 16);
+  const float r = x - elem_value<SGEMM_DTYPE_BF16>(h);
+  const uint16_t m = elem_bits<SGEMM_DTYPE_BF16>(r);
+  const uint16_t l = elem_bits<SGEMM_DTYPE_BF16>(r - elem_value<SGEMM_DTYPE_BF16>(m));
+  const uint16_t small = (uint16_t)((h & 0x8000u) | 0x1f80u);
+  p[0] = infinite ? small : h;
+  p[1] = infinite ? small : finite ? m : (uint16_t)0;
+  p[2] = infinite ? h : finite ? l : (uint16_t)0;
 }
 
 // Rows of tiles that hold rows that count, one at least.

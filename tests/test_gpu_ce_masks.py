@@ -22,7 +22,8 @@ from tests.test_gpu_ce import DTYPES, U, Problem  # noqa: E402
 def handle():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
-    h = sg.Handle()
+    h = sg.Handle(workspace=False)
+    h.set_workspace(1 << 30)
     yield h
     h.close()
 
@@ -119,9 +120,10 @@ def test_negative_scale_packed_rows(handle, dt):
 
 PATHS = [(5, 900, 40, "bf16"), (5, 900, 40, "f16"), (5, 900, 40, "f32"), (90, 900, 40, "f32")]
 PACKED = [(40, 900, 64, "bf16"), (40, 900, 64, "f16"), (300, 20000, 64, "bf16")]
+PLANES = [(600, 13200, 64, "f32"), (4200, 8200, 520, "f32")]  # (forward; both)
 
 
-@pytest.mark.parametrize("T,V,D,dt", PATHS + PACKED)
+@pytest.mark.parametrize("T,V,D,dt", PATHS + PACKED + PLANES)
 def test_no_word_left(handle, T, V, D, dt):
     """Every word at the type's lowest value: lse is it (as far as 32 bits hold
     it), the loss the logarithm of V where the others' part of the logits is
@@ -152,7 +154,7 @@ def test_no_word_left(handle, T, V, D, dt):
     assert (p.loss.cpu().numpy()[~keep] == 0).all() and (p.lse.cpu().numpy()[~keep] == 0).all()
 
 
-@pytest.mark.parametrize("T,V,D,dt", [a for a in PATHS + PACKED if a[3] != "f16"] + [(4200, 8200, 520, "f32")])
+@pytest.mark.parametrize("T,V,D,dt", [a for a in PATHS + PACKED if a[3] != "f16"] + PLANES)
 def test_gradients_where_no_word_is_left(T, V, D, dt):
     """Logits and lse at the type's lowest value, whose product with log2(e)
     leaves 32 bits: their difference is 0 and exp(z - lse) is 1, so dz is
@@ -176,7 +178,7 @@ def test_gradients_where_no_word_is_left(T, V, D, dt):
         off = np.abs(got.double().cpu().numpy() - want)[:, 1:]
         assert np.all(off <= bound[:, 1:]), np.nanmax(off - bound[:, 1:])
 
-@pytest.mark.parametrize("T,V,D,dt", PATHS + PACKED)
+@pytest.mark.parametrize("T,V,D,dt", PATHS + PACKED + PLANES)
 def test_infinite_and_nan_logits(handle, T, V, D, dt):
     """One word at +inf: lse is +inf, and the loss but for rows labelled with
     that word (inf - inf).  A label at -inf costs +inf.  One word at NaN:
@@ -214,3 +216,39 @@ def test_masks_in_the_last_columns(handle, T, D, dt):
 def test_masks_in_the_last_columns_big_tiles(handle, dt):
     for D in (40, 328):
         check(masked(300, 20001, D, dt, np.arange(60, 400), "inf", column=D - 1, seed=4), handle)
+
+
+# Infinite operands in three planes.
+@pytest.mark.parametrize("words", ["64", "128", "ragged", "but one"])
+@pytest.mark.parametrize("column", [0, 263])
+def test_infinite_words_in_planes(handle, words, column):
+    check(masked(600, 13200, 264, "f32", runs(13200)[words], "inf", column=column), handle)
+
+
+@pytest.mark.parametrize("T", [90, 600])
+def test_infinite_operands_with_all_bits_set(handle, T):
+    """X's element that meets the infinity has all 24 bits set, of either sign;
+    an infinite element of X meets finite ones and an infinity of W."""
+    V, D = 13200, 72
+    rng = np.random.default_rng(T)
+    b = 1 + (rng.integers(0, 1 << 11, T) * 4096 + 2047) * 2.0 ** -23
+    sign = np.where(np.arange(T) % 2 == 0, 1.0, -1.0)
+    p = Problem(T, V, D, "f32", seed=5, ignored=0.0, alpha=0.5)
+    p.labels[:] = 7
+    p.Y.copy_(torch.from_numpy(p.labels))
+    p.X[:, 0] = torch.from_numpy(b * sign).float()
+    p.W[:, 0] = 0.0
+    p.W[100:300, 0] = float("-inf")
+    p.forward(handle)
+    lse, loss = p.lse.cpu().numpy(), p.loss.cpu().numpy()
+    assert np.isfinite(lse[sign > 0]).all() and np.isfinite(loss[sign > 0]).all()
+    assert (lse[sign < 0] == np.inf).all() and (loss[sign < 0] == np.inf).all()
+    # the same column of X at infinity: z is -inf for words whose element is
+    # below 0, and for the label
+    p.X[:, 0] = float("inf")
+    p.W[:, 0] = torch.from_numpy(-(1 + (rng.integers(0, 1 << 11, V) * 4096 + 2047) * 2.0 ** -23)).float()
+    p.forward(handle)
+    assert (p.lse == float("-inf")).all() and torch.isnan(p.loss).all()
+    p.W[5, 0] = float("inf")
+    p.forward(handle)
+    assert (p.lse == float("inf")).all() and (p.loss == float("inf")).all()

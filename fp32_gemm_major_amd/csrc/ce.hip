@@ -812,7 +812,12 @@ int backward32(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labe
       if (st != SGEMM_OK) return st;
     }
   }
-  return SGEMM_OK;
+  if (dX == nullptr) return SGEMM_OK;
+  const unsigned g = grid_of(T * (unsigned long long)up_div(a.D, 8));
+  if (g == 0) return SGEMM_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL(ce_clear_rows_kernel, dim3(g), dim3(CE_THREADS), 0, s, a.T, a.D, labels, dloss,
+                     dlse, dX, lddx);
+  return launched();
 }
 
 template <int DT>

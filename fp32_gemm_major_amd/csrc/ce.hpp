@@ -251,6 +251,20 @@ static __global__ void __launch_bounds__(CE_THREADS)
   store8<SGEMM_DTYPE_F32>(row, n - c, v);
 }
 
+// dX's rows that count for nothing: zeros, whatever W made of dz's (0 * inf).
+static __global__ void __launch_bounds__(CE_THREADS)
+    ce_clear_rows_kernel(int T, int D, CeLabels labels, const float* __restrict__ dloss,
+                         const float* __restrict__ dlse, float* __restrict__ dX, int lddx) {
+  const unsigned units = ((unsigned)D + 7u) / 8u;
+  const unsigned long long at = (unsigned long long)blockIdx.x * CE_THREADS + threadIdx.x;
+  const unsigned long long t = at / units;
+  const unsigned c = 8u * (unsigned)(at % units);
+  if (t >= (unsigned long long)T) return;
+  if (ce_counts(ce_row_factors((int)t, ce_label(labels, (int)t), dloss, dlse))) return;
+  const float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  store8<SGEMM_DTYPE_F32>(reinterpret_cast<uint32_t*>(dX) + (size_t)t * lddx + c, D - (int)c, v);
+}
+
 // Zeros (rows x D) in any type: a gradient with no rows to come from.
 template <int DT>
 __global__ void __launch_bounds__(CE_THREADS) ce_zero_kernel(int rows, int D, void* out, int ldo) {

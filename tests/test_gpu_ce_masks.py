@@ -81,7 +81,7 @@ def test_masked_words_few_rows(handle, T, words, dt, value):
     check(masked(T, V, 48, dt, runs(V)[words], value), handle)
 
 
-@pytest.mark.parametrize("value", ["lowest"])
+@pytest.mark.parametrize("value", ["inf", "lowest"])
 @pytest.mark.parametrize("words", ["4", "ragged", "but one"])
 def test_masked_words_32_bit_library_products(handle, words, value):
     check(masked(90, 1300, 48, "f32", runs(1300)[words], value), handle)
@@ -252,3 +252,18 @@ def test_infinite_operands_with_all_bits_set(handle, T):
     p.W[5, 0] = float("inf")
     p.forward(handle)
     assert (p.lse == float("inf")).all() and (p.loss == float("inf")).all()
+
+
+# Left-out rows beside infinities and NaNs of W.
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("T,V,D,dt", PATHS + PACKED + PLANES + [(2000, 220, 100, "f32")])
+def test_left_out_rows_of_dx_are_zero(handle, T, V, D, dt, value):
+    p = Problem(T, V, D, dt, seed=6, ignored=0.4)
+    p.labels[0], p.labels[1] = ref.IGNORE, 3
+    p.Y.copy_(torch.from_numpy(p.labels))
+    p.forward(handle)
+    p.W[V // 2] = value
+    p.backward(handle)
+    out = p.Y == ref.IGNORE
+    assert (p.dX[out] == 0).all()
+    assert not torch.isfinite(p.dX[~out]).any()

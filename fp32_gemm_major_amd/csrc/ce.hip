@@ -797,7 +797,7 @@ int backward32(const sgemm_handle_s* h, const CeProblem& a, const CeLabels& labe
     st = product(&ph, DT, SGEMM_OP_N, SGEMM_OP_T, a.T, n, a.D, a.alpha, a.X, a.ldx, w, a.ldw, 0.0f,
                  z, ldz, s);
     if (st != SGEMM_OK) return st;
-    hipLaunchKernelGGL(ce_dz_kernel, dim3((unsigned)up_div(n, 8 * CE_THREADS), a.T),
+    hipLaunchKernelGGL(ce_dz_kernel, dim3(a.T, (unsigned)up_div(n, 8 * CE_THREADS)),
                        dim3(CE_THREADS), 0, s, z, ldz, n, v0, labels, lse, dloss, dlse);
     st = launched();
     if (st != SGEMM_OK) return st;

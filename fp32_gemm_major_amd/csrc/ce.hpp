@@ -228,13 +228,14 @@ static __global__ void __launch_bounds__(CE_THREADS)
   store8<SGEMM_DTYPE_F32>(reinterpret_cast<uint32_t*>(copy) + (size_t)t * ldcopy + c, 8, v);
 }
 
-// z of a piece, columns [v0, v0 + n), turned into dz in place.
+// z of a piece, columns [v0, v0 + n), turned into dz in place.  Rows are the
+// grid's first extent (the others end at 65536).
 static __global__ void __launch_bounds__(CE_THREADS)
     ce_dz_kernel(float* __restrict__ z, int ldz, int n, int v0, CeLabels labels,
                  const float* __restrict__ lse, const float* __restrict__ dloss,
                  const float* __restrict__ dlse) {
-  const int t = blockIdx.y;
-  const int c = 8 * (blockIdx.x * CE_THREADS + threadIdx.x);
+  const int t = blockIdx.x;
+  const int c = 8 * (blockIdx.y * CE_THREADS + threadIdx.x);
   if (c >= n) return;
   const int label = ce_label(labels, t);
   const CeFactors f = ce_row_factors(t, label, dloss, dlse);

@@ -201,6 +201,16 @@ def test_many_rows_few_words(handle, T, V, D, dt):
     p.check_backward()
 
 
+def test_more_rows_than_a_grid_extent_holds():
+    p = Problem(70000, 130, 24, "f32", seed=7)
+    with sg.Handle(workspace=False) as h:
+        h.set_workspace(max(h.ce_workspace_size(p.X, p.W, backward=b) for b in (False, True)))
+        p.forward(h)
+        p.check_forward()
+        p.backward(h)
+        p.check_backward()
+
+
 @pytest.mark.parametrize("dt", list(DTYPES))
 @pytest.mark.parametrize("T,V,D", [(5, 2050, 64), (16, 9000, 70), (8, 3000, 2), (130, 3000, 96), (300, 1111, 40),
                                    (550, 14000, 300)])

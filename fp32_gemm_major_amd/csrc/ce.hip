@@ -126,7 +126,8 @@ CeLayout packed_layout(const CeProblem& a, int backward) {
     l.fixed += 4 * T + 20 * Tp + 2 * planes * Tp * Dp;
     l.per_col = Tp / 8;  // eight bytes a row for 64 columns or more
   } else {
-    l.fixed += 4 * T + 24 * Tp + (a.dtype == SGEMM_DTYPE_F16 ? 4 : 2) * planes * Rp * Dp +
+    const bool scaled = a.dtype == SGEMM_DTYPE_F16;
+    l.fixed += (scaled ? 8 : 4) * T + 24 * Tp + (scaled ? 4 : 2) * planes * Rp * Dp +
                2 * kStep * 2 * (size_t)a.D + 4 * (size_t)product_rows(a) * (size_t)sum_cols(a);
     l.per_col = 2 * planes * Rp;
   }
@@ -574,6 +575,7 @@ int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels&
   CeRowInfo* info = c.take<CeRowInfo>(sizeof(CeRowInfo) * (size_t)Tp);
   float* x_factor = c.take<float>(4 * (size_t)Tp);
   float* out_factor = c.take<float>(4 * (size_t)Tp);
+  float* x_top = SCALED ? c.take<float>(4 * (size_t)a.T) : nullptr;
   void* xp = c.take<char>(2 * (size_t)planes * Rp * dp);
   // (only binary16 rows are scaled: else one copy serves both products)
   void* xs = SCALED ? c.take<char>(2 * Rp * dp) : xp;
@@ -583,10 +585,17 @@ int packed_backward(const sgemm_handle_s* h, const CeProblem& a, const CeLabels&
   void* wp = c.take<char>(copies_w(a) ? 2 * (size_t)planes * cols * dp : 0);
   const CeDz d = {c.take<uint16_t>(0), (int)cols};
 
+  int st;
+  if constexpr (SCALED) {
+    hipLaunchKernelGGL(ce_row_top_kernel<DT>, dim3((unsigned)up_div(a.T, CE_TOP_ROWS)),
+                       dim3(CE_THREADS), 0, s, a.T, a.D, a.X, a.ldx, labels, dloss, dlse, x_top);
+    st = launched();
+    if (st != SGEMM_OK) return st;
+  }
   hipLaunchKernelGGL((ce_pack_factors_kernel<UNIT, SCALED>), dim3(1), dim3(CE_PACK_THREADS), 0, s,
-                     a.T, Tp, a.alpha, labels, lse, dloss, dlse, (int)residues(a), pos, info,
+                     a.T, Tp, a.alpha, labels, lse, dloss, dlse, (int)residues(a), x_top, pos, info,
                      x_factor, out_factor, dw_factor, count);
-  int st = launched();
+  st = launched();
   if (st != SGEMM_OK) return st;
   CeOperands o = {xp, 0, nullptr, 0, 0, count};
   st = pack_rows<DT>(a, pos, count, residues(a), x_factor, xp, SCALED ? xs : nullptr, dp, &o.ldx, s);

@@ -345,6 +345,32 @@ __host__ __device__ inline int ce_residue_row(int count) {
   return ((count > 1 ? count : 1) + 63) & ~63;
 }
 
+// The largest finite |x| of the rows that count, a wave a row.
+constexpr int CE_TOP_ROWS = CE_THREADS / 64;
+template <int DT>
+__global__ void __launch_bounds__(CE_THREADS)
+    ce_row_top_kernel(int T, int D, const void* X, int ldx, CeLabels labels,
+                      const float* __restrict__ dloss, const float* __restrict__ dlse,
+                      float* __restrict__ x_top) {
+  typedef typename TensorElem<DT>::type E;
+  const int t = blockIdx.x * CE_TOP_ROWS + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (t >= T || !ce_counts(ce_row_factors(t, ce_label(labels, t), dloss, dlse))) return;
+  const E* x = static_cast<const E*>(X) + (size_t)t * ldx;
+  float top = 0.0f;
+  for (int c = 8 * lane; c < D; c += 8 * 64) {
+    float v[8];
+    load8<DT>(x + c, D - c, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = fabsf(v[i]);
+      if (a < INFINITY) top = fmaxf(top, a);
+    }
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  if (lane == 0) x_top[t] = top;
+}
+
 // Backward: the packed rows' factors as info, the factors of X's rows in dW's
 // product (x), of dX's rows (out) and of dW.
 //
@@ -359,8 +385,12 @@ __host__ __device__ inline int ce_residue_row(int count) {
 // binary16 (SCALED) also holds dz between its limits by a power of two a row:
 // with 2^k <= max(|p|, |q|) / u < 2^(k+1), the row is scaled by 2^(13-k) (so
 // |dz| < 2^15, and a probability keeps all its bits down to 2^-27), its row of
-// dX by 2^(k-13) in 32 bits, and its row of X in dW's product by 2^(k-kmax),
-// exactly but for values that the largest row's outweigh by 2^24.
+// dX by 2^(k-13) in 32 bits, and its row of X in dW's product by 2^(k+14-K).
+// K is the largest k + e over the rows, 2^e <= max|x| < 2^(e+1) (x_top), so
+// the row that reaches it comes to 2^14 .. 2^15, and an element of X loses
+// bits only where the largest |dz x| outweighs it by 2^28: half a step of
+// binary16's subnormal numbers there is 2^-40 of that product, and beside a dW
+// that is in range 2^-25, its own half step.
 //
 // count[0]: the rows that count; count[1]: the rows of dX's and dW's products,
 // with the residues' (see ce_dz_gemm_kernel) if any.
@@ -368,7 +398,8 @@ template <bool UNIT, bool SCALED>
 __global__ void __launch_bounds__(CE_PACK_THREADS)
     ce_pack_factors_kernel(int T, int padded, float alpha, CeLabels labels,
                            const float* __restrict__ lse, const float* __restrict__ dloss,
-                           const float* __restrict__ dlse, int residues, int* __restrict__ pos,
+                           const float* __restrict__ dlse, int residues,
+                           const float* __restrict__ x_top, int* __restrict__ pos,
                            CeRowInfo* __restrict__ info, float* __restrict__ x_factor,
                            float* __restrict__ out_factor, float* __restrict__ dw_factor,
                            int* __restrict__ count) {
@@ -401,7 +432,21 @@ __global__ void __launch_bounds__(CE_PACK_THREADS)
   // (a q far below the p's would take them out of range)
   const float unit = !UNIT ? 1.0f : q_max > 0x1p-16f * r_max ? q_max : r_max > 0.0f ? r_max : 1.0f;
   auto exponent = [](float r) { return r > 0.0f && r < INFINITY ? ilogbf(r) : 13; };
-  const int kmax = SCALED ? exponent(r_max / unit) : 13;
+  constexpr int NO_ROWS = -1000;
+  int top = NO_ROWS;  // K
+  if (SCALED) {
+    for (int t = threadIdx.x; t < T; t += CE_PACK_THREADS) {
+      const CeFactors f = ce_row_factors(t, ce_label(labels, t), dloss, dlse);
+      const float r = fmaxf(fabsf(f.p / unit), fabsf(f.q / unit));
+      if (ce_counts(f) && r < INFINITY && x_top[t] > 0.0f) top = max(top, exponent(r) + ilogbf(x_top[t]));
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) top = max(top, __shfl_xor(top, d));
+    if ((threadIdx.x & 63) == 0) wave_sum[threadIdx.x >> 6] = top;
+    __syncthreads();
+    for (int w = 0; w < CE_PACK_WAVES; ++w) top = max(top, wave_sum[w]);
+    if (top == NO_ROWS) top = 14;
+  }
   const float scale = alpha * unit;
   int base = 0;
   for (int t0 = 0; t0 < T; t0 += CE_PACK_THREADS) {
@@ -416,7 +461,8 @@ __global__ void __launch_bounds__(CE_PACK_THREADS)
       if (UNIT) f.p /= unit, f.q /= unit;
       const int k = SCALED ? exponent(fmaxf(fabsf(f.p), fabsf(f.q))) : 13;
       info[at] = CeRowInfo{ldexpf(f.p, 13 - k), ldexpf(f.q, 13 - k), lse[t], y};
-      x_factor[at] = ldexpf(1.0f, k - kmax);
+      // (an exponent past 40: a row of zeros, or one whose gradients are no numbers)
+      x_factor[at] = SCALED ? ldexpf(1.0f, min(k + 14 - top, 40)) : 1.0f;
       out_factor[at] = ldexpf(scale, k - 13);
     }
   }
@@ -425,7 +471,7 @@ __global__ void __launch_bounds__(CE_PACK_THREADS)
   if (threadIdx.x == 0) {
     count[0] = base;
     count[1] = residues ? ce_residue_row(base) + base : base;
-    *dw_factor = ldexpf(scale, kmax - 13);
+    *dw_factor = SCALED ? ldexpf(scale, top - 27) : scale;
   }
 }
 

@@ -556,9 +556,11 @@ int sgemm_ce_forward(sgemm_handle_t h, int dtype, int T, int V, int D,
  *     dX = alpha * dz * W,   dW = alpha * dz^T * X
  *
  * are overwritten (either may be NULL), of type dtype.  lse is a forward
- * call's.  dz is rounded to dtype between the two products (binary16: after a
- * power-of-two scale a row; with up to 128 rows what the rounding leaves is
- * kept too), their sums are FP32 and the results are rounded once. */
+ * call's.  16-bit dz is rounded to dtype between the two products (binary16:
+ * each row, and X's in dW's product, after a power-of-two scale; with up to 128
+ * rows what the rounding leaves is kept too), their sums are FP32 and the
+ * results are rounded once.  A row whose dloss and dlse are both 0 adds
+ * nothing, as if it were left out, whatever X holds there. */
 int sgemm_ce_backward(sgemm_handle_t h, int dtype, int T, int V, int D,
                       float alpha, const void* X, int ldx, const void* W,
                       int ldw, const long long* labels, long long ignore,

@@ -284,6 +284,47 @@ def test_half_gradients_keep_their_range(handle, scale):
                   1.01 * (2.0 ** -25 * (1 + scale) + 2.0 ** -10 * np.abs(one * scale)))
 
 
+@pytest.mark.parametrize("size", [2.0 ** -20, 2.0 ** -13, 1.0, 2.0 ** 10])
+@pytest.mark.parametrize("T", [60, 300])
+def test_half_gradients_of_w_for_small_x_and_uneven_rows(handle, T, size):
+    """binary16 dW keeps the terms of rows whose dloss is far below the largest,
+    whatever X's size.  Beside dz's rounding and the result's, a row's X may
+    lose, scaled for the product, half a step of the subnormal numbers, 2^-25,
+    where the largest |dz x| of all rows is scaled to 2^28 or more: with r the
+    row's largest |dz| and M the largest r max|x|, 2^-36 M |dz| / r at the
+    most."""
+    V, D, alpha = 700, 48, 0.5
+    p = Problem(T, V, D, "f16", seed=8, ignored=0.1)
+    rng = np.random.default_rng(T)
+    weight = np.exp2(-rng.integers(0, 13, T).astype(float))
+    p.dloss = (np.sign(p.dloss) * (1 + rng.random(T)) * weight).astype(np.float32).astype(float)
+    # (results of about 2^-4 times the rows' weights)
+    p.dloss *= 2.0 ** -4 / size
+    p.x *= size
+    p.alpha = alpha / size if size >= 1 else alpha
+    p.w *= 1.0 if size >= 1 else 2.0 ** -6
+    p.X, p.W = p.strided(p.x, torch.float16, 0), p.strided(p.w, torch.float16, 0)
+    p.dl.copy_(torch.from_numpy(p.dloss))
+    p.forward(handle)
+    p.backward(handle, dlse=False)
+    z, _, lse = ref.forward(p.x, p.w, p.labels, p.alpha)
+    dz = ref.dlogits(z, p.labels, lse, p.dloss)
+    _, want = ref.gradients(p.x, p.w, p.labels, dz, p.alpha)
+    keep = p.labels != ref.IGNORE
+    r = np.where(keep, np.abs(p.dloss), 0.0)
+    ax = np.abs(np.where(keep[:, None], p.x, 0.0))
+    half = 2.0 ** -11
+    prob = r[:, None] * np.exp(np.where(keep[:, None], z - lse[:, None], -np.inf))
+    e = (2 * p.sum_error() + 2.0 ** -18) * prob + 4 * U * np.abs(dz)
+    e += (half if T > 128 else half * half) * (np.abs(dz) + e) + 2.0 ** -37 * r[:, None]
+    big = (r * ax.max(1)).max()
+    share = (np.abs(dz) / np.where(r > 0, r, 1.0)[:, None]).sum(0)
+    bound = p.alpha * (e.T @ ax + 4 * T * U * (np.abs(dz).T @ ax) + 2.0 ** -36 * big * share[:, None])
+    bound = bound + half * (np.abs(want) + bound) + 2.0 ** -25
+    off = np.abs(p.dW.double().cpu().numpy() - want)
+    assert np.all(off <= bound), (np.nanmax(off / bound), np.argwhere(~(off <= bound))[:3])
+
+
 @pytest.mark.parametrize("dt", list(DTYPES))
 @pytest.mark.parametrize("T", [3, 70])
 def test_left_out_rows_may_hold_anything(handle, T, dt):

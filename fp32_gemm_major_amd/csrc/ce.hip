@@ -243,7 +243,19 @@ bool any_meet(const ByteRange* r, int outs, int all) {
 // ceil(units / threads) workgroups, or 0 past a launch's limit.
 unsigned grid_of(unsigned long long units) {
   const unsigned long long g = (units + CE_THREADS - 1) / CE_THREADS;
-  return g <= INT_MAX ? (unsigned)g : 0u;
+  return grid_holds(g, CE_THREADS) ? (unsigned)g : 0u;
+}
+
+// Whether every launch of a call holds its rows: checked before the first one.
+// (A piece of W is at most some GB.)
+bool launches_hold(const CeProblem& a, int backward) {
+  const unsigned long long T = a.T, units = up_div(a.D, 8);
+  if (a.T == 0) return grid_of(a.V * units) != 0;
+  if (backward && few(a)) return true;
+  if (!packed(a, backward)) return grid_holds(T, CE_STATS_THREADS) && grid_of(T * units) != 0;
+  const unsigned long long rows = T + (residues(a) ? padded_product_rows(a) : CE_ROW_PAD);
+  return grid_of(rows * (unsigned)(padded_cols(a) / 8)) != 0 &&
+         grid_holds(up_div(T, CE_TOP_ROWS), CE_THREADS);
 }
 
 template <int DT>
@@ -310,7 +322,7 @@ CePiece piece_of(const CeProblem& a, int M, int N, int K, const void* A, int lda
 }
 
 bool grid_fits(const CePiece& p) {
-  return (long long)p.tiles_m * p.tiles_n <= INT_MAX;
+  return grid_holds((unsigned long long)p.tiles_m * p.tiles_n, 256);
 }
 
 template <class T, int DT, int MODE>
@@ -878,9 +890,10 @@ int sgemm_ce_forward(sgemm_handle_t h, int dtype, int T, int V, int D, float alp
   if (h == nullptr) return SGEMM_ERR_HANDLE;
   int st = sgemm_validate_ce(dtype, T, V, D, X, ldx, W, ldw, labels, loss, lse);
   if (st != SGEMM_OK || T == 0) return st;
+  const CeProblem a = {dtype, T, V, D, alpha, X, ldx, W, ldw};
+  if (!launches_hold(a, 0)) return SGEMM_ERR_UNSUPPORTED;
   st = check_device(h);
   if (st != SGEMM_OK) return st;
-  const CeProblem a = {dtype, T, V, D, alpha, X, ldx, W, ldw};
   const CeLabels y = {labels, ignore, V};
   if (h->workspace_bytes < sizes_of(a, 0, h->cus).least) return SGEMM_ERR_SCRATCH;
   return forward(h, a, y, loss, lse, stream);
@@ -914,9 +927,10 @@ int sgemm_ce_backward(sgemm_handle_t h, int dtype, int T, int V, int D, float al
   if (st != SGEMM_OK) return st;
   if (dX == nullptr && dW == nullptr) return SGEMM_OK;
   if (T == 0 && dW == nullptr) return SGEMM_OK;
+  const CeProblem a = {dtype, T, V, D, alpha, X, ldx, W, ldw};
+  if (!launches_hold(a, 1)) return SGEMM_ERR_UNSUPPORTED;
   st = check_device(h);
   if (st != SGEMM_OK) return st;
-  const CeProblem a = {dtype, T, V, D, alpha, X, ldx, W, ldw};
   const CeLabels y = {labels, ignore, V};
   switch (dtype) {
     case SGEMM_DTYPE_F32:

@@ -58,6 +58,12 @@ inline int check_device(const sgemm_handle_s* h) {
   return hipGetDevice(&dev) == hipSuccess && dev == h->device ? SGEMM_OK : SGEMM_ERR_DEVICE;
 }
 
+// Whether one launch holds that many workgroups: their threads are counted in
+// 32 bits.
+inline bool grid_holds(unsigned long long workgroups, unsigned threads) {
+  return workgroups <= 0xffffffffu / threads;
+}
+
 inline int launched() { return hipGetLastError() == hipSuccess ? SGEMM_OK : SGEMM_ERR_HIP; }
 
 }  // namespace sgemm

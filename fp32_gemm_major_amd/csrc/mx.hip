@@ -4,7 +4,6 @@
 #include "sgemm.h"
 
 #include <hip/hip_runtime.h>
-#include <limits.h>
 
 #include "handle.hpp"
 #include "mx_gemm.hpp"
@@ -62,19 +61,23 @@ const small_fn kSmall[7][2] = {MX_SMALL(-1, false),
                                MX_SMALL(SGEMM_DTYPE_F16, true)};
 #undef MX_SMALL
 
+// Workgroups of a quantisation and of its reverse.
+long long quantize_wgs(int trans, int R, int K) {
+  const long long nb = blocks_of(K);
+  return trans ? up_div(R, MXT_ROWS) * up_div(nb, MXT_BLOCKS)
+               : up_div(4 * nb * R, MX_THREADS * MX_UNROLL);
+}
+long long dequantize_wgs(int R, int K) {
+  return up_div(up_div(K, 8) * R, MX_THREADS * MX_UNROLL);
+}
+
 int launch_quantize(int dtype, int trans, const MxQuantArgs& g, hipStream_t stream) {
-  const long long nb = blocks_of(g.K);
-  if (trans) {
-    const long long kgroups = up_div(nb, MXT_BLOCKS);
-    const long long wgs = up_div(g.R, MXT_ROWS) * kgroups;
-    if (wgs > INT_MAX) return SGEMM_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL(kQuantT[dtype], dim3((unsigned)wgs), dim3(MX_THREADS), 0, stream, g,
-                       (int)kgroups);
-  } else {
-    const long long wgs = up_div(4 * nb * g.R, MX_THREADS * MX_UNROLL);
-    if (wgs > INT_MAX) return SGEMM_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL(kQuant[dtype], dim3((unsigned)wgs), dim3(MX_THREADS), 0, stream, g);
-  }
+  const dim3 wgs((unsigned)quantize_wgs(trans, g.R, g.K));
+  if (trans)
+    hipLaunchKernelGGL(kQuantT[dtype], wgs, dim3(MX_THREADS), 0, stream, g,
+                       (int)up_div(blocks_of(g.K), MXT_BLOCKS));
+  else
+    hipLaunchKernelGGL(kQuant[dtype], wgs, dim3(MX_THREADS), 0, stream, g);
   return launched();
 }
 
@@ -82,23 +85,29 @@ int launch_quantize(int dtype, int trans, const MxQuantArgs& g, hipStream_t stre
 // one or four tiles of 16 columns a workgroup.
 int launch_small(int xdt, int tiles, const MxArgs& g, hipStream_t stream) {
   constexpr int kRows = 65535 * MXS_TILE;  // a grid's second extent
+  // (the first one's threads are counted in 32 bits: 2^23 workgroups less one)
+  constexpr int kCols = (int)(0xffffffffu / MXS_THREADS) * MXS_TILE;
   const int kind = xdt < 0 ? 0 : g.M <= MXS_FEW ? 4 + xdt : 1 + xdt;
-  const unsigned tn = (unsigned)up_div(g.N, MXS_TILE * tiles);
-  for (long long m0 = 0; m0 < g.M; m0 += kRows) {
-    MxArgs p = g;
-    p.M = (int)(g.M - m0 < kRows ? g.M - m0 : kRows);
-    if (m0 > 0) {  // (activations come with 16 rows at most)
-      if (g.K > 0) {
+  for (long long m0 = 0; m0 < g.M; m0 += kRows)
+    for (long long n0 = 0; n0 < g.N; n0 += kCols) {
+      MxArgs p = g;
+      p.M = (int)(g.M - m0 < kRows ? g.M - m0 : kRows);
+      p.N = (int)(g.N - n0 < kCols ? g.N - n0 : kCols);
+      if (g.K > 0 && m0 > 0) {  // (activations come with 16 rows at most)
         p.A = static_cast<const uint8_t*>(g.A) + (size_t)m0 * g.lda;
         p.SA = g.SA + (size_t)m0 * g.ldsa;
       }
-      p.C = static_cast<char*>(g.C) + (size_t)m0 * g.ldc * tensor_elem_bytes(g.cdt);
+      if (g.K > 0 && n0 > 0) {
+        p.B = g.B + (size_t)n0 * g.ldb;
+        p.SB = g.SB + (size_t)n0 * g.ldsb;
+      }
+      p.C = static_cast<char*>(g.C) + ((size_t)m0 * g.ldc + (size_t)n0) * tensor_elem_bytes(g.cdt);
+      hipLaunchKernelGGL(kSmall[kind][tiles == 4],
+                         dim3((unsigned)up_div(p.N, MXS_TILE * tiles), (unsigned)up_div(p.M, MXS_TILE)),
+                         dim3(MXS_THREADS), 0, stream, p);
+      const int st = launched();
+      if (st != SGEMM_OK) return st;
     }
-    hipLaunchKernelGGL(kSmall[kind][tiles == 4], dim3(tn, (unsigned)up_div(p.M, MXS_TILE)),
-                       dim3(MXS_THREADS), 0, stream, p);
-    const int st = launched();
-    if (st != SGEMM_OK) return st;
-  }
   return SGEMM_OK;
 }
 
@@ -129,7 +138,7 @@ const MxTileDesc kTiles[3] = {tile_desc<X256x256>(), tile_desc<X128x128>(), tile
 bool tile_fits(const MxTileDesc& t, const MxArgs& g) {
   const long long far = 1LL << 32, r = t.b - 1;
   return r * g.lda + 128 < far && r * g.ldb + 128 < far && r * g.ldsa + 8 < far &&
-         r * g.ldsb + 8 < far && up_div(g.M, t.b) * up_div(g.N, t.b) <= INT_MAX;
+         r * g.ldsb + 8 < far && grid_holds(up_div(g.M, t.b) * up_div(g.N, t.b), t.threads);
 }
 
 int launch_tile(const MxTileDesc& t, const MxArgs& g, hipStream_t stream) {
@@ -199,6 +208,7 @@ int sgemm_mx_quantize(sgemm_handle_t h, int dtype, int trans, int R, int K, cons
   const ByteRange x = byte_range(X, trans ? K : R, trans ? R : K, ldx, esz);
   const ByteRange c = code_range(codes, R, K, ldc), s = scale_range(scales, R, K, lds);
   if (ranges_meet(x, c) || ranges_meet(x, s) || ranges_meet(c, s)) return SGEMM_ERR_ALIAS;
+  if (!grid_holds(quantize_wgs(trans, R, K), MX_THREADS)) return SGEMM_ERR_UNSUPPORTED;
   const int st = check_device(h);
   if (st != SGEMM_OK) return st;
   const MxQuantArgs g = {R, K, X, ldx, static_cast<uint8_t*>(codes), ldc,
@@ -219,13 +229,13 @@ int sgemm_mx_dequantize(sgemm_handle_t h, int dtype, int R, int K, const void* c
   const ByteRange y = byte_range(Y, R, K, ldy, esz);
   if (ranges_meet(y, code_range(codes, R, K, ldc)) || ranges_meet(y, scale_range(scales, R, K, lds)))
     return SGEMM_ERR_ALIAS;
+  if (!grid_holds(dequantize_wgs(R, K), MX_THREADS)) return SGEMM_ERR_UNSUPPORTED;
   const int st = check_device(h);
   if (st != SGEMM_OK) return st;
   const MxDequantArgs g = {R, K, static_cast<const uint8_t*>(codes), ldc,
                            static_cast<const uint8_t*>(scales), lds, Y, ldy};
-  const long long wgs = up_div(up_div(K, 8) * R, MX_THREADS * MX_UNROLL);
-  if (wgs > INT_MAX) return SGEMM_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL(kDequant[dtype], dim3((unsigned)wgs), dim3(MX_THREADS), 0, stream, g);
+  hipLaunchKernelGGL(kDequant[dtype], dim3((unsigned)dequantize_wgs(R, K)), dim3(MX_THREADS), 0,
+                     stream, g);
   return launched();
 }
 
@@ -272,6 +282,7 @@ int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K, float a
   if (K > 0 && !elem_aligned(X, xsz)) return SGEMM_ERR_VALUE;
   if (ranges_meet(byte_range(C, M, N, ldc, tensor_elem_bytes(dtype)), byte_range(X, M, K, ldx, xsz)))
     return SGEMM_ERR_ALIAS;
+  if (!grid_holds(quantize_wgs(SGEMM_OP_N, M, K), MX_THREADS)) return SGEMM_ERR_UNSUPPORTED;
   st = check_device(h);
   if (st != SGEMM_OK) return st;
   MxArgs g = {M, N, K, alpha, beta, X, ldx, nullptr, 0, static_cast<const uint8_t*>(B), ldb,

@@ -460,7 +460,8 @@ int sgemm_set_lowp_kernel(sgemm_handle_t h, int kernel_id);
  *
  * Ownership, streams, errors and threading as for sgemm_run (with a workspace:
  * sgemm_run_mx_quant).  K is at most SGEMM_MX_MAX_K, rows and columns at most
- * SGEMM_MX_MAX_ROWS (SGEMM_ERR_SIZE).  Tensors of activations and results have
+ * SGEMM_MX_MAX_ROWS (SGEMM_ERR_SIZE); a call quantises or reads back 2^36
+ * values at most (SGEMM_ERR_UNSUPPORTED).  Tensors of activations and results have
  * dtype SGEMM_DTYPE_F32, _BF16 or _F16 (SGEMM_ERR_VALUE for another, and for
  * a tensor not aligned to its element). */
 #define SGEMM_MX_MAX_K (1 << 27)
@@ -532,6 +533,8 @@ int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K,
  * with a workspace.  T == 0: nothing is read (backward: dW is set to 0).
  * SGEMM_ERR_SIZE for T < 0, V < 1, D < 1 or D over SGEMM_CE_MAX_D;
  * SGEMM_ERR_LD for a stride below D;
+ * SGEMM_ERR_UNSUPPORTED from 2^26 rows or 2^35 elements of X (T == 0: of dW) on,
+ * which a launch may not hold;
  * SGEMM_ERR_VALUE for another dtype or a tensor not aligned to its element;
  * SGEMM_ERR_ALIAS where an output overlaps another argument. */
 

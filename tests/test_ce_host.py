@@ -94,6 +94,29 @@ def test_validate():
         assert bwd(dW=a) == sg.SGEMM_ERR_ALIAS, hex(a)
 
 
+def test_sizes_that_a_launch_does_not_hold():
+    """Rows or elements whose threads a launch does not count in 32 bits are
+    refused before anything is queued."""
+    h = HostHandle()
+    lib, at = sg.library(), ctypes.addressof(h)
+    x, w, y, a, b = (1 << k for k in (60, 56, 54, 52, 53))  # never touched
+
+    def forward(dtype, T, V, D):
+        return lib.sgemm_ce_forward(at, dtype, T, V, D, 1.0, x, D, w, D, y, -100, a, b, None)
+
+    def backward(dtype, T, V, D):
+        return lib.sgemm_ce_backward(at, dtype, T, V, D, 1.0, x, D, w, D, y, -100, a, b, None, None, 0,
+                                     1 << 58, D, None)
+
+    for dtype in (F32, BF16, F16):
+        for call in (forward, backward):
+            assert call(dtype, 1 << 28, 100, 8) == sg.SGEMM_ERR_UNSUPPORTED
+            assert call(dtype, 1 << 20, 100, 1 << 16) == sg.SGEMM_ERR_UNSUPPORTED
+            for T in (1, 100, 1 << 20):
+                assert call(dtype, T, 100, 8) == sg.SGEMM_ERR_DEVICE
+        assert backward(dtype, 0, 1 << 27, 256) == sg.SGEMM_ERR_UNSUPPORTED
+
+
 def test_null_handle():
     lib = sg.library()
     assert lib.sgemm_ce_workspace_size(None, F32, 1, 1, 1, 0, None, None) == sg.SGEMM_ERR_HANDLE
@@ -120,17 +143,21 @@ def test_binding_checks():
 
 
 class HostHandle(ctypes.Structure):
-    """A handle as the library lays it out, for entries that launch nothing."""
+    """A handle as the library lays it out, for entries that launch nothing: of
+    no device, so that any other entry ends at its check of the device."""
     _fields_ = [("device", ctypes.c_int), ("cus", ctypes.c_int), ("variant", ctypes.c_int),
                 ("forced_kernel", ctypes.c_int), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_size_t), ("forced_lowp", ctypes.c_int)]
+
+    def __init__(self):
+        super().__init__(device=-1, cus=256, forced_kernel=-1, forced_lowp=-1)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("backward", [0, 1])
 def test_workspace_size(dtype, backward):
     """An empty batch needs no workspace; other sizes grow with the rows."""
-    h = HostHandle(cus=256, forced_kernel=-1, forced_lowp=-1)
+    h = HostHandle()
     at = ctypes.addressof(h)
     for V, D in ((1, 1), (32000, 4096), (300, 7)):
         assert sg.sgemm_ce_workspace_size(at, dtype, 0, V, D, backward) == (0, 0)

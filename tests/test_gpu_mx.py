@@ -298,6 +298,22 @@ def test_more_rows_than_a_grid_extent_holds(handle, K):
     assert np.all(np.abs(C.double().cpu().numpy() - want) <= 4 * max(K, 1) * 2.0 ** -24 * mag)
 
 
+@pytest.mark.parametrize("M", [1, 20])
+def test_more_columns_than_a_grid_extent_holds(handle, M):
+    """2^27 and more rows of B: a launch of 16 columns a workgroup holds 2^27 - 16."""
+    N, K = (1 << 27) + 100, 32
+    A, B = operand(M, K, 3), sg.Mx4.empty(N, K)
+    B.codes.random_(0, 256)
+    B.scales.fill_(127)
+    C = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    handle.gemm_mx4(A, B, C)
+    at = torch.tensor([0, 1, (1 << 27) - 18, (1 << 27) - 17, (1 << 27) - 16, (1 << 27) - 15, (1 << 27) - 1,
+                       1 << 27, N - 2, N - 1])
+    b = ref.dequantize(B.codes[at.cuda()].cpu().numpy(), B.scales[at.cuda()].cpu().numpy())
+    check(C[:, at.cuda()].float().cpu().numpy(), ref.dequantize(*as_numpy(A)), b, K, 1.0, 0.0, None,
+          "bf16")
+
+
 def test_refusals(handle):
     A, B = operand(20, 64, 1), operand(5, 64, 2)
     C = torch.empty(20, 5, device="cuda")

@@ -1,10 +1,13 @@
 """Microscaled 4-bit operators without a GPU: the plain implementation against
 hand-worked values, and every refusal of the C entries and the binding."""
+import ctypes
+
 import numpy as np
 import pytest
 
 import fp32_gemm_major_amd as sg
 from tests import mx_reference as ref
+from tests.test_ce_host import HostHandle
 
 A, SA, B, SB, C = 0x1000000, 0x2000000, 0x3000000, 0x4000000, 0x8000000  # never touched
 F32, BF16, F16 = sg.SGEMM_DTYPE_F32, sg.SGEMM_DTYPE_BF16, sg.SGEMM_DTYPE_F16
@@ -66,6 +69,35 @@ def test_null_handle():
                             None) == sg.SGEMM_ERR_HANDLE
     assert lib.sgemm_run_mx_quant(None, F32, 1, 1, 32, 1.0, A, 32, B, 16, SB, 1, 0.0, F32, C, 1,
                                   None) == sg.SGEMM_ERR_HANDLE
+
+
+def test_sizes_that_a_launch_does_not_hold():
+    """A launch's threads are counted in 32 bits: 2^24 workgroups of 256, each
+    with 512 units of eight values (or 64 rows of 256 where X is stored across
+    K).  Refused before anything touches the device; one less gets as far as
+    that (and no further without one)."""
+    h = HostHandle()
+    lib, at = sg.library(), ctypes.addressof(h)
+    X, codes, scales = 1 << 60, 1 << 52, 1 << 56  # never touched
+    K = 1 << 20
+    fits = ((1 << 24) - 1) * 512 * 8 // K  # rows of whole blocks
+
+    def quantize(R, trans=0, k=K):
+        return lib.sgemm_mx_quantize(at, BF16, trans, R, k, X, R if trans else k, codes, k // 2, scales,
+                                     k // 32, None)
+
+    def dequantize(R):
+        return lib.sgemm_mx_dequantize(at, BF16, R, K, codes, K // 2, scales, K // 32, X, K, None)
+
+    def product(R):
+        return lib.sgemm_run_mx_quant(at, BF16, R, 1, K, 1.0, X, K, codes, K // 2, scales, K // 32, 0.0,
+                                      F32, 1 << 48, 1, None)
+
+    for call in (quantize, dequantize, product):
+        assert call(fits + 1) == sg.SGEMM_ERR_UNSUPPORTED
+        assert call(fits) == sg.SGEMM_ERR_DEVICE
+    assert quantize(1 << 22, 1, 1 << 16) == sg.SGEMM_ERR_UNSUPPORTED
+    assert quantize((1 << 22) - 64, 1, 1 << 16) == sg.SGEMM_ERR_DEVICE
 
 
 def test_mx4_container():

@@ -365,8 +365,9 @@ bool kernel_fits(const KernelDesc& k, const RunArgs& a, const LaunchCtx& c) {
     if (a.K <= 0 || a.M > k.bm) return false;
     // (the one-pass kernels index columns and k in 32 bits, a piece past K)
     if (k.variant == SGEMM_VARIANT_VALU)
-      return (k.bn != SKINNY_KN_COLS && !a.tb) ||
-             (a.N <= INT_MAX - k.bn && a.K <= INT_MAX - k.bk);
+      return grid_holds(((long long)a.N + k.bn - 1) / k.bn, k.threads) &&
+             ((k.bn != SKINNY_KN_COLS && !a.tb) ||
+              (a.N <= INT_MAX - k.bn && a.K <= INT_MAX - k.bk));
     // MFMA split-K: the edge instance's conditions, and a workspace for at
     // least one set of partial sums
     const size_t part = (size_t)a.M * skinny_ws_stride(a.N) * sizeof(float);
@@ -717,7 +718,7 @@ int handle_plan(const sgemm_handle_s* h, const RunArgs& a, const LaunchCtx& ctx,
   }
   for (int p = 0; p < plan->count; ++p) {
     const KernelDesc& k = kKernels[plan->part[p].kernel];
-    if (ceil_div(a.M, k.bm) * ceil_div(plan->part[p].n, k.bn) > INT_MAX)
+    if (!grid_holds(ceil_div(a.M, k.bm) * ceil_div(plan->part[p].n, k.bn), k.threads))
       return SGEMM_ERR_UNSUPPORTED;
   }
   return SGEMM_OK;
@@ -961,8 +962,9 @@ bool lp_fits(const LpKernelDesc& k, const LpRun& a) {
   // of ceil(N / bn) workgroups (columns and k indexed in 32 bits, a few
   // blocks past N and K)
   if (k.schedule == SGEMM_SCHEDULE_SMALL_M && !k.split)
-    return a.N <= INT_MAX - k.bn && a.K <= INT_MAX - 1024;
-  if (ceil_div(a.M, k.bm) * ceil_div(a.N, k.bn) > INT_MAX) return false;
+    return a.N <= INT_MAX - k.bn && a.K <= INT_MAX - 1024 &&
+           grid_holds(ceil_div(a.N, k.bn), k.threads);
+  if (!grid_holds(ceil_div(a.M, k.bm) * ceil_div(a.N, k.bn), k.threads)) return false;
   switch (k.mode) {
     case SGEMM_MODE_GUARDED:
       return true;

@@ -765,3 +765,17 @@ def test_errors_launch_nothing(handle):
     assert e.value.status == sg.SGEMM_ERR_UNSUPPORTED
     torch.cuda.synchronize()
     assert torch.all(C == 1.0)
+
+
+@pytest.mark.parametrize("M", [1, 3])
+def test_more_columns_than_one_pass_launches_hold(handle, M):
+    """2^28 columns of B stored N x K: a launch of four or eight a workgroup
+    would have more than 2^32 threads, of which the runtime starts too few
+    without an error.  (Integers: exact.)"""
+    N, K = (1 << 28) + 100, 1
+    A = torch.arange(1, M + 1, device="cuda", dtype=torch.float32).view(M, K)
+    B = torch.randint(-4, 5, (N, K), device="cuda").float()
+    C = torch.full((M, N), 77.0, device="cuda")
+    handle.gemm(A, B, C, transb=True)
+    for m in range(M):
+        assert torch.equal(C[m], (m + 1) * B[:, 0])

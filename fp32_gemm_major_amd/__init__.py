@@ -47,6 +47,7 @@ SGEMM_DTYPE_F16 = 2
 SGEMM_DTYPE_FP8_E4M3 = 3
 SGEMM_DTYPE_FP8_E5M2 = 4
 
+INT_MAX = 2 ** 31 - 1  # of the C ABI's sizes and strides
 SGEMM_MX_BLOCK = 32  # values of a microscaled row that share a scale
 SGEMM_MX_MAX_K = 1 << 27
 SGEMM_MX_MAX_ROWS = 0x7fffff00
@@ -551,6 +552,8 @@ class Mx4:
     @staticmethod
     def empty(rows: int, K: int, device="cuda") -> "Mx4":
         nb = -(-K // SGEMM_MX_BLOCK)
+        if rows > INT_MAX or 16 * nb > INT_MAX:
+            raise ValueError(f"{rows} rows of {K} values: past 32 bits")
         q = object.__new__(Mx4)
         q.codes = torch.empty((rows, 16 * nb), dtype=torch.uint8, device=device)
         q.scales = torch.empty((rows, nb), dtype=torch.uint8, device=device)
@@ -562,6 +565,10 @@ def _row_stride(name, t) -> int:
     """Leading dimension of a 2-D row-major tensor (its rows may be strided,
     but must not overlap)."""
     (rows, cols), (ld, step) = t.shape, t.stride()
+    if rows == 1 and ld > INT_MAX:
+        ld = cols
+    if rows > INT_MAX or cols > INT_MAX or ld > INT_MAX:
+        raise ValueError(f"{name}: {rows} x {cols}, stride {ld}: past 32 bits")
     if rows == 0 or cols == 0:
         return max(ld, cols, 1)
     if step != 1 and cols > 1:
@@ -883,6 +890,12 @@ def _elements_from_pointer(t):
     return t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
 
 
+def _leading(t) -> int:
+    """A 2-D tensor's leading dimension (one row's may be any that fits)."""
+    ld = max(t.stride(0), 1)
+    return max(t.shape[1], 1) if t.shape[0] == 1 and ld > INT_MAX else ld
+
+
 def _shapes(A, B, C, M, N, K, lda, ldb, ldc, transa, transb):
     """Sizes and leading dimensions from 2-D tensors where not given, checked
     against the tensors: a 2-D operand must hold its stored window (A: M x K,
@@ -895,21 +908,23 @@ def _shapes(A, B, C, M, N, K, lda, ldb, ldc, transa, transb):
         ra, ca = A.shape
         M = (ca if transa else ra) if M is None else M
         k_from["A"] = ra if transa else ca
-        lda = max(A.stride(0), 1) if lda is None else lda
+        lda = _leading(A) if lda is None else lda
     if B.dim() == 2:
         rb, cb = B.shape
         k_from["B"] = cb if transb else rb
         N = (rb if transb else cb) if N is None else N
-        ldb = max(B.stride(0), 1) if ldb is None else ldb
+        ldb = _leading(B) if ldb is None else ldb
     if K is None:
         if len(set(k_from.values())) > 1:
             raise ValueError(f"A and B disagree on K: {k_from['A']} (A) and "
                              f"{k_from['B']} (B)")
         K = next(iter(k_from.values()), None)
     if C.dim() == 2:
-        ldc = max(C.stride(0), 1) if ldc is None else ldc
+        ldc = _leading(C) if ldc is None else ldc
     if None in (M, N, K, lda, ldb, ldc):
         raise ValueError("sizes and leading dimensions are needed for 1-D buffers")
+    if max(M, N, K, lda, ldb, ldc) > INT_MAX:
+        raise ValueError(f"{M} x {N} x {K}, leading dimensions {lda}, {ldb}, {ldc}: past 32 bits")
     check_extents(A, B, C, M, N, K, lda, ldb, ldc, transa, transb)
     return M, N, K, lda, ldb, ldc
 

@@ -126,3 +126,42 @@ def test_matrix_checks():
     for t in (torch.zeros(3, 5).t(), torch.zeros(1, 5).expand(3, 5)):
         with pytest.raises(ValueError):
             sg._matrix("X", t)
+
+
+def test_sizes_and_strides_past_32_bits():
+    """The C ABI's ints: what does not fit them is refused, not cut to its low
+    32 bits (a stride of 2^32 + 64 would read as 64)."""
+    torch = pytest.importorskip("torch")
+    far = 2 ** 32 + 64
+    strided = torch.empty_strided((2, 64), (far, 1), dtype=torch.bfloat16, device="meta")
+    for t in (strided, torch.empty((2 ** 32 + 5, 1), device="meta"),
+              torch.empty((1, 2 ** 32 + 5), device="meta"),
+              torch.empty_strided((2, 4), (2 ** 31, 1), device="meta")):
+        with pytest.raises(ValueError):
+            sg._matrix("X", t)
+    assert sg._matrix("X", torch.empty_strided((2, 4), (2 ** 31 - 1, 1), device="meta")) == (F32, 2 ** 31 - 1)
+    # (one row has no stride to speak of)
+    assert sg._matrix("X", torch.empty_strided((1, 64), (far, 1), device="meta")) == (F32, 64)
+    u8 = dict(dtype=torch.uint8, device="meta")
+    sg.Mx4(torch.empty((2, 32), **u8), torch.empty((2, 2), **u8))
+    with pytest.raises(ValueError):
+        sg.Mx4(torch.empty_strided((2, 32), (far, 1), **u8), torch.empty((2, 2), **u8))
+    with pytest.raises(ValueError):
+        sg.Mx4(torch.empty((2, 32), **u8), torch.empty_strided((2, 2), (far, 1), **u8))
+    with pytest.raises(ValueError):
+        sg.Mx4.empty(2 ** 32 + 5, 32, "meta")
+    with pytest.raises(ValueError):
+        sg._ce_shapes(strided, torch.empty((5, 64), dtype=torch.bfloat16, device="meta"))
+    # the products of 32- and 16-bit operands, sizes given or taken from tensors
+    A, B, C = (torch.empty((2, 2), device="meta") for _ in range(3))
+    assert sg._shapes(A, B, C, None, None, None, None, None, None, False, False) == (2,) * 6
+    one = torch.empty_strided((1, 2), (far, 1), device="meta")
+    assert sg._shapes(one, B, one, None, None, None, None, None, None, False, False) == (1, 2, 2, 2, 2, 2)
+    for name in ("M", "N", "K", "lda", "ldb", "ldc"):
+        a = dict(M=None, N=None, K=None, lda=None, ldb=None, ldc=None) | {name: 2 ** 32 + 2}
+        flat = (torch.empty(2 ** 35, device="meta") for _ in range(3))
+        b = dict(M=2, N=2, K=2, lda=2, ldb=2, ldc=2) | {name: 2 ** 32 + 2}
+        with pytest.raises(ValueError):
+            sg._shapes(A, B, C, *a.values(), False, False)
+        with pytest.raises(ValueError):
+            sg._shapes(*flat, *b.values(), False, False)

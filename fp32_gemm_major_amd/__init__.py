@@ -611,12 +611,13 @@ class Handle:
             self.set_workspace(sgemm_workspace_size(self.h))
 
     def set_workspace(self, nbytes: int):
-        """Give the handle a fresh workspace of ``nbytes`` (0: none)."""
+        """Give the handle a fresh workspace of ``nbytes`` (0: none) on its
+        device."""
         sgemm_set_workspace(self.h, 0, 0)
         self.workspace = None
         if nbytes:
             self.workspace = torch.empty((nbytes + 3) // 4, dtype=torch.float32,
-                                         device="cuda")
+                                         device=self.device)
             sgemm_set_workspace(self.h, self.workspace.data_ptr(), nbytes)
 
     def plan(self, M, N, K, A, lda, B, ldb, C, ldc, transa=False, transb=False):
@@ -700,7 +701,7 @@ class Handle:
         (shader clock in GHz, the launch's span in microseconds) of that call,
         from the product kernel's own clock stamps."""
         if self._stamps is None:
-            self._stamps = torch.zeros(4 * 65536, dtype=torch.int64, device="cuda")
+            self._stamps = torch.zeros(4 * 65536, dtype=torch.int64, device=self.device)
         n = self.gemm_stamped(A, B, C, self._stamps, alpha, beta, **kw)
         return clock_from_stamps(self._stamps[: 4 * n].cpu(), n, sgemm_diag_wall_clock_khz())
 

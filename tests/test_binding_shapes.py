@@ -5,6 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import fp32_gemm_major_amd as sg  # noqa: E402
 from fp32_gemm_major_amd import _shapes, check_extents  # noqa: E402
 
 
@@ -78,3 +79,16 @@ def test_16_and_8_bit_element_sizes():
     with pytest.raises(ValueError, match="B"):
         check_extents(torch.zeros(35, dtype=torch.float8_e4m3fn), B.reshape(-1)[1:], t(15),
                       5, 3, 7, 7, 7, 3, False, True)
+
+
+def test_workspace_lies_on_the_handles_device(monkeypatch):
+    """A handle's workspace is its device's, whatever device is current."""
+    h = object.__new__(sg.Handle)
+    h.h, h.device, h.workspace, h._stamps = 0x1000, torch.device("meta"), None, None
+    monkeypatch.setattr(sg, "sgemm_set_workspace", lambda handle, ptr, n: seen.append((handle, n)))
+    monkeypatch.setattr(sg, "sgemm_destroy", lambda handle: None)
+    seen = []
+    h.set_workspace(4096)
+    assert h.workspace.device.type == "meta" and h.workspace.numel() == 1024
+    assert seen == [(0x1000, 0), (0x1000, 4096)]
+    h.h = None

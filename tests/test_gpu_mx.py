@@ -298,6 +298,34 @@ def test_more_rows_than_a_grid_extent_holds(handle, K):
     assert np.all(np.abs(C.double().cpu().numpy() - want) <= 4 * max(K, 1) * 2.0 ** -24 * mag)
 
 
+@pytest.mark.parametrize("M,N,K", [(64, 4096, 8192), (33, 3000, 8224), (17, 8190, 8704)])
+def test_rows_of_a_long_k(handle, M, N, K):
+    """17 to 64 rows straight from memory, four tiles of columns a workgroup."""
+    A, B = operand(M, K, 4), operand(N, K, 5)
+    C, buf = strided(torch.zeros(M, N), 3, fill=7.0)
+    handle.gemm_mx4(A, B, C)
+    check(C.cpu().numpy(), ref.dequantize(*as_numpy(A)), ref.dequantize(*as_numpy(B)), K, 1.0, 0.0, None,
+          "f32")
+    assert (buf[:, N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("M,N,K,far", [(70, 2100, 96, "A"), (2100, 70, 544, "B")])
+def test_rows_past_a_tiles_offsets(handle, M, N, K, far):
+    """Rows so far apart that a tile's lie more than 4 GiB from its first: the
+    kernel that loads straight from memory takes them."""
+    A, B = operand(M, K, 6), operand(N, K, 7)
+    q = A if far == "A" else B
+    ld = (1 << 32) // 63 + 5  # (a 64-row tile's last row)
+    rows = torch.empty((q.rows - 1) * ld + K // 2, dtype=torch.uint8, device="cuda")
+    codes = rows.as_strided((q.rows, K // 2), (ld, 1))
+    codes.copy_(q.codes)
+    wide = sg.Mx4(codes, q.scales)
+    C = torch.full((M, N), 7.0, device="cuda")
+    handle.gemm_mx4(wide if far == "A" else A, wide if far == "B" else B, C)
+    check(C.cpu().numpy(), ref.dequantize(*as_numpy(A)), ref.dequantize(*as_numpy(B)), K, 1.0, 0.0, None,
+          "f32")
+
+
 @pytest.mark.parametrize("M", [1, 20])
 def test_more_columns_than_a_grid_extent_holds(handle, M):
     """2^27 and more rows of B: a launch of 16 columns a workgroup holds 2^27 - 16."""

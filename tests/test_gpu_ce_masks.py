@@ -218,6 +218,13 @@ def test_masks_in_the_last_columns_big_tiles(handle, dt):
         check(masked(300, 20001, D, dt, np.arange(60, 400), "inf", column=D - 1, seed=4), handle)
 
 
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("D", [5, 33, 50, 72, 130, 1030])
+@pytest.mark.parametrize("T", [1, 3, 7, 16, 20, 90, 300])
+def test_masks_in_the_last_column_of_any_width(handle, T, D, dt):
+    check(masked(T, 1300, D, dt, np.arange(60, 400), "inf", column=D - 1, seed=4, pad=T % 4), handle)
+
+
 # Infinite operands in three planes.
 @pytest.mark.parametrize("words", ["64", "128", "ragged", "but one"])
 @pytest.mark.parametrize("column", [0, 263])

@@ -148,14 +148,19 @@ int launch_tile(const MxTileDesc& t, const MxArgs& g, hipStream_t stream) {
   return launched();
 }
 
-// The kernel for a product of codes (measured on 256 CUs):
+// The kernel for a product of codes (measured on 256 CUs, with B read from
+// memory; where it stands in the last-level cache from the call before, 64-square
+// tiles are the faster from some 500 tiles of 16 x 16 on: 64 x 4096 x 11008 11.5
+// us against 16.7):
 //
 // * up to 16 rows: straight from memory, which reads B once;
-// * more, while its 16 x 16 tiles are at most two a CU: the same (17 x 4096 x
-//   11008 in 13.0 us against 17.2 in 64-square tiles, 128 x 1500 x 800 in 3.7
-//   against 4.5); also up to 64 rows of a long K where 64-square tiles reach
-//   a quarter of the CUs, four column tiles a workgroup (64 x 4096 x 11008:
-//   17.1 against 26.0);
+// * more, while its 16 x 16 tiles are at most two a CU: the same (17 x 2048 x
+//   11008 in 8.5 us against 16.8 in 64-square tiles, 32 x 4096 x 4096 7.9
+//   against 9.3, 128 x 600 x 256 3.0 against 3.2); also up to 64 rows of a long
+//   K where 64-square tiles reach a quarter of the CUs, four column tiles a
+//   workgroup (33 x 4096 x 8192: 14.4 against 15.9, 48 x 3584 x 8192 14.4
+//   against 18.3, 64 x 2560 x 16384 25.3 against 36.8, 64 x 4096 x 28672 42.1
+//   against 65.4);
 // * 256-square tiles where they give every CU one, or 128-square ones would
 //   start a second round (512 x 11008 x 4096: 33.7 against 36.7 us);
 // * 128-square ones where they give three CUs in five one (256 x 11008 x 4096:

@@ -229,7 +229,8 @@ int validate(const CeProblem& a, const long long* labels) {
   if (a.ldx < a.D || a.ldw < a.D) return SGEMM_ERR_LD;
   if (a.T == 0) return SGEMM_OK;
   if (a.X == nullptr || a.W == nullptr || labels == nullptr) return SGEMM_ERR_NULL;
-  if (!elem_aligned(a.X, esz) || !elem_aligned(a.W, esz)) return SGEMM_ERR_VALUE;
+  if (!elem_aligned(a.X, esz) || !elem_aligned(a.W, esz) || !elem_aligned(labels, 8))
+    return SGEMM_ERR_VALUE;
   return SGEMM_OK;
 }
 
@@ -878,6 +879,7 @@ int sgemm_validate_ce(int dtype, int T, int V, int D, const void* X, int ldx, co
   const int st = validate(a, labels);
   if (st != SGEMM_OK || T == 0) return st;
   if (loss == nullptr || lse == nullptr) return SGEMM_ERR_NULL;
+  if (!elem_aligned(loss, 4) || !elem_aligned(lse, 4)) return SGEMM_ERR_VALUE;
   const unsigned esz = tensor_elem_bytes(dtype);
   const ByteRange r[] = {byte_range(loss, 1, T, T, 4), byte_range(lse, 1, T, T, 4),
                          byte_range(X, T, D, ldx, esz), byte_range(W, V, D, ldw, esz),
@@ -911,6 +913,8 @@ int sgemm_validate_ce_backward(int dtype, int T, int V, int D, const void* X, in
   const unsigned esz = tensor_elem_bytes(dtype);
   if (!elem_aligned(dX, esz) || !elem_aligned(dW, esz)) return SGEMM_ERR_VALUE;
   if (T > 0 && (lse == nullptr || dloss == nullptr)) return SGEMM_ERR_NULL;
+  if (!elem_aligned(lse, 4) || !elem_aligned(dloss, 4) || !elem_aligned(dlse, 4))
+    return SGEMM_ERR_VALUE;
   const ByteRange r[] = {byte_range(dX, T, D, lddx, esz), byte_range(dW, V, D, lddw, esz),
                          byte_range(X, T, D, ldx, esz),   byte_range(W, V, D, ldw, esz),
                          byte_range(labels, 1, T, T, 8),  byte_range(lse, 1, T, T, 4),

@@ -79,6 +79,10 @@ def test_validate():
         assert v(T=0, X=None, labels=None) == sg.SGEMM_OK
         assert v(X=X + 2) == sg.SGEMM_ERR_VALUE and v(W=W + 1, dtype=BF16) == sg.SGEMM_ERR_VALUE
         assert v(X=X + 2, dtype=BF16) == sg.SGEMM_OK
+        assert v(labels=Y + 4) == sg.SGEMM_ERR_VALUE and v(labels=Y + 8) == sg.SGEMM_OK
+        assert v(lse=LSE + 2) == sg.SGEMM_ERR_VALUE and v(lse=LSE + 64) == sg.SGEMM_OK
+    assert fwd(loss=LOSS + 1) == sg.SGEMM_ERR_VALUE
+    assert bwd(dloss=DL + 2) == sg.SGEMM_ERR_VALUE and bwd(dlse=DE + 1) == sg.SGEMM_ERR_VALUE
     assert fwd(loss=None) == sg.SGEMM_ERR_NULL
     assert fwd(loss=LSE + 12) == sg.SGEMM_ERR_ALIAS and fwd(loss=LSE + 16) == sg.SGEMM_OK
     for a in (X, W, Y):

@@ -524,7 +524,10 @@ int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K,
  * their row of dX is 0, and nothing of them (X, dloss, dlse may be NaN) meets
  * dW.  A label outside [0, V) other than `ignore` makes its row's loss and
  * gradients NaN (and so dW).  Infinities and NaNs in X and W spread as the
- * formulas make them.
+ * formulas make them: a word whose logit is -inf, or so low that its
+ * exponential is 0 (a mask by the type's lowest value), adds nothing to lse and
+ * has a dW of 0, though dX meets 0 * -inf; a row with no other words has lse
+ * -inf, or about that lowest logit.  x w itself must stay within 32 bits.
  *
  * Both calls divide the handle's workspace (sgemm_set_workspace) among the
  * pieces; with less than the size's `least` bytes they return

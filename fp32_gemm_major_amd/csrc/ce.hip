@@ -72,8 +72,8 @@ long long sum_cols(const CeProblem& a) { return round_up(a.D, 8); }
 // Microseconds here and on the other path: bfloat16, 4 rows, 80000 x 801 126 and
 // 211, 131072 x 1023 297 and 403, 50000 x 4095 575 and 536 (one row 527 and 540,
 // eight 587 and 539), one row of 118231 x 2303 825 and 708; 16 rows, 50000 x 128
-// 44 and 57, 16000 x 512 39 and 42, 20000 x 800 77 and 68; 32-bit, 16 rows, 131072 x 64 74 and 83, 20000 x 800 80
-// and 65.
+// 44 and 57, 16000 x 512 39 and 42, 131072 x 64 69 and 60, 20000 x 800 77 and 68;
+// 32-bit, 16 rows, 131072 x 64 74 and 83, 20000 x 800 80 and 65.
 constexpr long long kFewElements8 = 1 << 27, kFewElements16 = 1 << 23;
 bool few(const CeProblem& a) {
   const long long elements = (long long)a.V * a.D;

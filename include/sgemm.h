@@ -72,7 +72,8 @@ enum sgemm_status {
   SGEMM_ERR_DEVICE = -6, /* no device, not gfx950, or not the handle's device */
   SGEMM_ERR_VALUE = -7,  /* unknown variant or kernel id */
   SGEMM_ERR_ALIAS = -8,  /* the C window overlaps the A or B window */
-  SGEMM_ERR_UNSUPPORTED = -9, /* forced kernel cannot run these arguments */
+  SGEMM_ERR_UNSUPPORTED = -9, /* forced kernel cannot run these arguments, or
+                                 no launch holds a call of this size */
   SGEMM_ERR_SCRATCH = -10  /* sgemm_run_ex_noalloc: forced kernel needs more
                               than SGEMM_SCRATCH_BYTES of scratch; 4-bit and
                               loss entries: the handle's workspace is smaller

@@ -3,7 +3,8 @@
 C = alpha * A * B + beta * C for row-major FP32 operands ("GEMM 优化之路",
 problem statement), and the same product with bfloat16 or float16 A and B and
 FP32 C (the gsyq.cn guide, section 5.1).  Beside the products stand microscaled
-4-bit operands (quantisation, and products of them) and the softmax cross
+4-bit operands (quantisation, and products of them), microscaled 8-bit rows (from
+tensors and from a root-mean-square norm) and the softmax cross
 entropy of an output layer with its gradients.  Every step runs in the
 HIP library ``libsgemm.so``; this module only marshals arguments.  PyTorch provides device memory and streams.
 There is no fallback: if the library is missing, loading fails loudly.
@@ -71,6 +72,9 @@ EXPORTED = [
     "sgemm_lowp_kernel_schedule", "sgemm_lowp_plan_handle",
     "sgemm_mx_quantize", "sgemm_mx_dequantize", "sgemm_run_mx", "sgemm_validate_mx",
     "sgemm_run_mx_quant",
+    "sgemm_mx_byte_quantize", "sgemm_mx_byte_dequantize",
+    "sgemm_rmsnorm", "sgemm_validate_rmsnorm", "sgemm_rmsnorm_backward",
+    "sgemm_validate_rmsnorm_backward", "sgemm_rmsnorm_workspace_size",
     "sgemm_ce_workspace_size", "sgemm_ce_forward", "sgemm_ce_backward", "sgemm_validate_ce",
     "sgemm_validate_ce_backward",
 ]
@@ -132,6 +136,13 @@ def _bind(lib):
     lib.sgemm_validate_mx.argtypes = [i, i, i, p, i, p, i, p, i, p, i, i, p, i]
     lib.sgemm_run_mx_quant.argtypes = [p, i, i, i, i, f, p, i, p, i, p, i, f, i, p, i, p]
     q, sp = ctypes.c_longlong, ctypes.POINTER(ctypes.c_size_t)
+    lib.sgemm_mx_byte_quantize.argtypes = lib.sgemm_mx_quantize.argtypes
+    lib.sgemm_mx_byte_dequantize.argtypes = lib.sgemm_mx_dequantize.argtypes
+    lib.sgemm_rmsnorm.argtypes = [p, i, i, i, i, p, i, p, i, p, f, p, i, p, i, p, i, p, p]
+    lib.sgemm_validate_rmsnorm.argtypes = [i, i, i, i, p, i, p, i, p, p, i, p, i, p, i, p]
+    lib.sgemm_rmsnorm_backward.argtypes = [p, i, i, i, i, p, i, p, i, p, p, p, i, p, i, p, p]
+    lib.sgemm_validate_rmsnorm_backward.argtypes = [i, i, i, i, p, i, p, i, p, p, p, i, p, i, p]
+    lib.sgemm_rmsnorm_workspace_size.argtypes = [p, i, i, sp, sp]
     lib.sgemm_ce_workspace_size.argtypes = [p, i, i, i, i, i, sp, sp]
     lib.sgemm_ce_forward.argtypes = [p, i, i, i, i, f, p, i, p, i, p, q, p, p, p]
     lib.sgemm_ce_backward.argtypes = [p, i, i, i, i, f, p, i, p, i, p, q, p, p, p, p, i, p, i, p]
@@ -139,7 +150,10 @@ def _bind(lib):
     lib.sgemm_validate_ce_backward.argtypes = [i, i, i, i, p, i, p, i, p, p, p, p, p, i, p, i]
     for name in ("sgemm_ce_workspace_size", "sgemm_ce_forward", "sgemm_ce_backward",
                  "sgemm_validate_ce", "sgemm_validate_ce_backward", "sgemm_mx_quantize", "sgemm_mx_dequantize", "sgemm_run_mx",
-                 "sgemm_validate_mx", "sgemm_run_mx_quant"):
+                 "sgemm_validate_mx", "sgemm_run_mx_quant", "sgemm_mx_byte_quantize",
+                 "sgemm_mx_byte_dequantize", "sgemm_rmsnorm", "sgemm_validate_rmsnorm",
+                 "sgemm_rmsnorm_backward", "sgemm_validate_rmsnorm_backward",
+                 "sgemm_rmsnorm_workspace_size"):
         getattr(lib, name).restype = i
     for name in ("sgemm_lowp_kernel_schedule", "sgemm_lowp_plan_handle",
                  "sgemm_diag_run_clocked", "sgemm_diag_wall_clock_khz", "sgemm_run_ex_noalloc",
@@ -300,6 +314,57 @@ def sgemm_run_mx_quant(h, xtype, M, N, K, alpha, X, ldx, B, ldb, SB, ldsb, beta,
     return _check(library().sgemm_run_mx_quant(h, xtype, M, N, K, alpha, X, ldx, B, ldb, SB,
                                                ldsb, beta, dtype, C, ldc, stream),
                   "sgemm_run_mx_quant")
+
+
+def sgemm_mx_byte_quantize(h, dtype, trans, R, K, X, ldx, codes, ldc, scales, lds,
+                       stream=0) -> int:
+    """Microscaled 8-bit rows of X; X, codes and scales are device addresses."""
+    return _check(library().sgemm_mx_byte_quantize(h, dtype, trans, R, K, X, ldx, codes, ldc,
+                                               scales, lds, stream), "sgemm_mx_byte_quantize")
+
+
+def sgemm_mx_byte_dequantize(h, dtype, R, K, codes, ldc, scales, lds, Y, ldy, stream=0) -> int:
+    """The values of microscaled 8-bit rows as a tensor of type ``dtype``."""
+    return _check(library().sgemm_mx_byte_dequantize(h, dtype, R, K, codes, ldc, scales, lds, Y,
+                                                 ldy, stream), "sgemm_mx_byte_dequantize")
+
+
+def sgemm_rmsnorm(h, dtype, gtype, T, D, X, ldx, R, ldr, G, eps, H, ldh, codes, ldc, scales,
+                      lds, rstd, stream=0) -> int:
+    """Root-mean-square norm of X + R into microscaled 8-bit rows; R, H and
+    rstd may be None."""
+    return _check(library().sgemm_rmsnorm(h, dtype, gtype, T, D, X, ldx, R, ldr, G, eps, H,
+                                              ldh, codes, ldc, scales, lds, rstd, stream),
+                  "sgemm_rmsnorm")
+
+
+def sgemm_validate_rmsnorm(dtype, gtype, T, D, X, ldx, R, ldr, G, H, ldh, codes, ldc, scales,
+                               lds, rstd) -> int:
+    return library().sgemm_validate_rmsnorm(dtype, gtype, T, D, X, ldx, R, ldr, G, H, ldh,
+                                                codes, ldc, scales, lds, rstd)
+
+
+def sgemm_rmsnorm_backward(h, dtype, gtype, T, D, dY, lddy, H, ldh, G, rstd, dH, lddh, dX, lddx,
+                           dG, stream=0) -> int:
+    """Its gradients; dH and dG may be None."""
+    return _check(library().sgemm_rmsnorm_backward(h, dtype, gtype, T, D, dY, lddy, H, ldh, G,
+                                                   rstd, dH, lddh, dX, lddx, dG, stream),
+                  "sgemm_rmsnorm_backward")
+
+
+def sgemm_validate_rmsnorm_backward(dtype, gtype, T, D, dY, lddy, H, ldh, G, rstd, dH, lddh, dX,
+                                    lddx, dG) -> int:
+    return library().sgemm_validate_rmsnorm_backward(dtype, gtype, T, D, dY, lddy, H, ldh, G,
+                                                     rstd, dH, lddh, dX, lddx, dG)
+
+
+def sgemm_rmsnorm_workspace_size(h, T, D):
+    """(least, full) bytes of workspace of the norm's gradients with dG."""
+    least, full = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(library().sgemm_rmsnorm_workspace_size(h, T, D, ctypes.byref(least),
+                                                  ctypes.byref(full)),
+           "sgemm_rmsnorm_workspace_size")
+    return least.value, full.value
 
 
 def sgemm_ce_workspace_size(h, dtype, T, V, D, backward):
@@ -530,35 +595,54 @@ TENSOR_DTYPES = {torch.float32: SGEMM_DTYPE_F32, torch.bfloat16: SGEMM_DTYPE_BF1
                  torch.float16: SGEMM_DTYPE_F16}
 
 
-class Mx4:
-    """Microscaled 4-bit rows: ``codes``, a uint8 matrix of 16 bytes a block of
-    32 values, and ``scales``, a uint8 matrix of one byte a block (the
+class _MxRows:
+    """Microscaled rows: ``codes``, a uint8 matrix of ``CODE_BYTES`` bytes a
+    block of 32 values, and ``scales``, a uint8 matrix of one byte a block (the
     exponent plus 127).  Rows may be strided, bytes of a row not.  ``rows``
     and ``K`` (values a row holds, whole blocks) are its sizes."""
 
     __slots__ = ("codes", "scales", "rows", "K", "_ldc", "_lds")
+    CODE_BYTES = 0
 
     def __init__(self, codes, scales):
         for name, t in (("codes", codes), ("scales", scales)):
             if t.dtype != torch.uint8 or t.dim() != 2:
                 raise TypeError(f"{name} must be a 2-D uint8 tensor")
         (rows, width), (rows_s, nb) = codes.shape, scales.shape
-        if rows != rows_s or width != 16 * nb:
+        if rows != rows_s or width != self.CODE_BYTES * nb:
             raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} "
-                             "disagree: 16 code bytes and a scale byte a block")
+                             f"disagree: {self.CODE_BYTES} code bytes and a scale byte a block")
         self.codes, self.scales, self.rows, self.K = codes, scales, rows, SGEMM_MX_BLOCK * nb
         self._ldc, self._lds = _row_stride("codes", codes), _row_stride("scales", scales)
 
-    @staticmethod
-    def empty(rows: int, K: int, device="cuda") -> "Mx4":
+    @classmethod
+    def empty(cls, rows: int, K: int, device="cuda"):
         nb = -(-K // SGEMM_MX_BLOCK)
-        if rows > INT_MAX or 16 * nb > INT_MAX:
+        width = cls.CODE_BYTES * nb
+        if rows > INT_MAX or width > INT_MAX:
             raise ValueError(f"{rows} rows of {K} values: past 32 bits")
-        q = object.__new__(Mx4)
-        q.codes = torch.empty((rows, 16 * nb), dtype=torch.uint8, device=device)
+        q = object.__new__(cls)
+        q.codes = torch.empty((rows, width), dtype=torch.uint8, device=device)
         q.scales = torch.empty((rows, nb), dtype=torch.uint8, device=device)
-        q.rows, q.K, q._ldc, q._lds = rows, SGEMM_MX_BLOCK * nb, max(16 * nb, 1), max(nb, 1)
+        q.rows, q.K, q._ldc, q._lds = rows, SGEMM_MX_BLOCK * nb, max(width, 1), max(nb, 1)
         return q
+
+    @classmethod
+    def nbytes(cls, rows: int, K: int) -> int:
+        """Bytes of ``rows`` rows of K values."""
+        return (cls.CODE_BYTES + 1) * -(-K // SGEMM_MX_BLOCK) * rows
+
+
+class Mx4(_MxRows):
+    __doc__ = _MxRows.__doc__.replace("Microscaled rows", "Microscaled 4-bit rows")
+    __slots__ = ()
+    CODE_BYTES = 16
+
+
+class Mx8(_MxRows):
+    __doc__ = _MxRows.__doc__.replace("Microscaled rows", "Microscaled 8-bit (E4M3) rows")
+    __slots__ = ()
+    CODE_BYTES = 32
 
 
 def _row_stride(name, t) -> int:
@@ -752,41 +836,56 @@ class Handle:
             return _current_stream(index)
         return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
-    def mx4_quantize(self, X, trans=False, out=None, stream=None):
-        """Microscaled 4-bit rows of X (R x K, or stored K x R when ``trans``;
-        float32, bfloat16 or float16): an ``Mx4`` of R rows, ``out`` if given
-        (else allocated on ``stream``).  K need not be whole blocks; the last
-        one is filled with zeros."""
+    def _mx_quantize(self, kind, call, X, trans, out, stream):
         dtype, ldx = _matrix("X", X)
         R, K = X.shape
         if trans:
             R, K = K, R
-        if out is None:
-            if stream is None:
-                out = Mx4.empty(R, K, self.device)
-            else:
-                s = stream if isinstance(stream, torch.cuda.Stream) else \
-                    torch.cuda.ExternalStream(stream, self.device)
-                with torch.cuda.stream(s):
-                    out = Mx4.empty(R, K, self.device)
-        elif out.rows != R or out.K != SGEMM_MX_BLOCK * -(-K // SGEMM_MX_BLOCK):
-            raise ValueError(f"out holds {out.rows} rows of {out.K} values, X gives {R} of {K}")
+        out = self._mx_out(kind, R, K, out, stream, "X gives")
         s = self._on(stream, X=X, codes=out.codes, scales=out.scales)
-        sgemm_mx_quantize(self.h, dtype, 1 if trans else 0, R, K, X.data_ptr(), ldx,
-                          out.codes.data_ptr(), out._ldc, out.scales.data_ptr(), out._lds, s)
+        call(self.h, dtype, 1 if trans else 0, R, K, X.data_ptr(), ldx,
+             out.codes.data_ptr(), out._ldc, out.scales.data_ptr(), out._lds, s)
         return out
 
-    def mx4_dequantize(self, Q, out, stream=None):
-        """The values of ``Q`` into ``out`` (float32, bfloat16 or float16; its
-        columns are at most Q.K, the rest is left out).  Returns ``out``."""
+    def _mx_out(self, kind, R, K, out, stream, what):
+        """``out``, checked to be R rows of K values, or such rows allocated on
+        ``stream``."""
+        if out is None:
+            if stream is None:
+                return kind.empty(R, K, self.device)
+            s = stream if isinstance(stream, torch.cuda.Stream) else \
+                torch.cuda.ExternalStream(stream, self.device)
+            with torch.cuda.stream(s):
+                return kind.empty(R, K, self.device)
+        if not isinstance(out, kind):
+            raise TypeError(f"out must be an {kind.__name__}")
+        if out.rows != R or out.K != SGEMM_MX_BLOCK * -(-K // SGEMM_MX_BLOCK):
+            raise ValueError(f"out holds {out.rows} rows of {out.K} values, {what} {R} of {K}")
+        return out
+
+    def _mx_dequantize(self, kind, call, Q, out, stream):
+        if not isinstance(Q, kind):
+            raise TypeError(f"Q must be an {kind.__name__}")
         dtype, ldy = _matrix("out", out)
         R, K = out.shape
         if R != Q.rows or K > Q.K:
             raise ValueError(f"out is {tuple(out.shape)}, Q holds {Q.rows} rows of {Q.K} values")
         s = self._on(stream, codes=Q.codes, scales=Q.scales, out=out)
-        sgemm_mx_dequantize(self.h, dtype, R, K, Q.codes.data_ptr(), Q._ldc,
-                            Q.scales.data_ptr(), Q._lds, out.data_ptr(), ldy, s)
+        call(self.h, dtype, R, K, Q.codes.data_ptr(), Q._ldc,
+             Q.scales.data_ptr(), Q._lds, out.data_ptr(), ldy, s)
         return out
+
+    def mx4_quantize(self, X, trans=False, out=None, stream=None):
+        """Microscaled 4-bit rows of X (R x K, or stored K x R when ``trans``;
+        float32, bfloat16 or float16): an ``Mx4`` of R rows, ``out`` if given
+        (else allocated on ``stream``).  K need not be whole blocks; the last
+        one is filled with zeros."""
+        return self._mx_quantize(Mx4, sgemm_mx_quantize, X, trans, out, stream)
+
+    def mx4_dequantize(self, Q, out, stream=None):
+        """The values of ``Q`` into ``out`` (float32, bfloat16 or float16; its
+        columns are at most Q.K, the rest is left out).  Returns ``out``."""
+        return self._mx_dequantize(Mx4, sgemm_mx_dequantize, Q, out, stream)
 
     def gemm_mx4(self, A, B, C, alpha=1.0, beta=0.0, stream=None):
         """C = alpha * A @ B^T + beta * C with B an ``Mx4`` of N rows and A an
@@ -810,6 +909,82 @@ class Handle:
         return sgemm_run_mx_quant(self.h, xtype, M, N, K, alpha, A.data_ptr(), lda,
                                   B.codes.data_ptr(), B._ldc, B.scales.data_ptr(), B._lds, beta,
                                   dtype, C.data_ptr(), ldc, s)
+
+    # -- microscaled 8-bit rows --
+
+    def mx8_quantize(self, X, trans=False, out=None, stream=None):
+        """``mx4_quantize`` in 8 bits (an ``Mx8``): activations kept for a
+        backward pass at 33/64 of their 16-bit size, or operands of
+        ``gemm_mx8``."""
+        return self._mx_quantize(Mx8, sgemm_mx_byte_quantize, X, trans, out, stream)
+
+    def mx8_dequantize(self, Q, out, stream=None):
+        """The values of an ``Mx8``, as ``mx4_dequantize``."""
+        return self._mx_dequantize(Mx8, sgemm_mx_byte_dequantize, Q, out, stream)
+
+    # -- root-mean-square norm --
+
+    def rmsnorm_mx8(self, X, G, residual=None, H=None, rstd=None, eps=1e-6, out=None, stream=None):
+        """The rows of ``h = X + residual`` (X alone if None) over their
+        root mean square, times the gain ``G``, as an ``Mx8`` (``out`` if given,
+        else allocated on ``stream``).
+
+        X, ``residual`` and ``H`` are T x D, float32, bfloat16 or float16; G is
+        D values of that type or float32.  ``H`` receives h and may be X or
+        ``residual`` itself; ``rstd`` (T float32) the rows' factors, for
+        ``rmsnorm_backward``."""
+        dtype, ldx = _matrix("X", X)
+        T, D = X.shape
+        gtype = _gain(G, X)
+        more, args = {}, []
+        for name, t in (("residual", residual), ("H", H)):
+            if t is None:
+                args.append((None, 0))
+                continue
+            kind, ld = _matrix(name, t)
+            if kind != dtype or t.shape != X.shape:
+                raise ValueError(f"{name} must be {T} x {D} of X's type")
+            more[name] = t
+            args.append((t.data_ptr(), ld))
+        if rstd is not None:
+            _vectors(T, torch.float32, rstd=rstd)
+            more["rstd"] = rstd
+        out = self._mx_out(Mx8, T, D, out, stream, "X gives")
+        s = self._on(stream, X=X, G=G, codes=out.codes, scales=out.scales, **more)
+        sgemm_rmsnorm(self.h, dtype, gtype, T, D, X.data_ptr(), ldx, *args[0], G.data_ptr(),
+                          eps, *args[1], out.codes.data_ptr(), out._ldc, out.scales.data_ptr(),
+                          out._lds, None if rstd is None else rstd.data_ptr(), s)
+        return out
+
+    def rmsnorm_workspace_size(self, T, D, least=False) -> int:
+        """Bytes of workspace (``set_workspace``) that ``rmsnorm_backward`` with
+        dG makes use of; ``least``: the fewest it runs with."""
+        return sgemm_rmsnorm_workspace_size(self.h, T, D)[0 if least else 1]
+
+    def rmsnorm_backward(self, dY, H, G, rstd, dX, dG=None, dH=None, stream=None):
+        """The gradients of ``rmsnorm_mx8``'s X (and ``residual``) into dX and
+        of its G into dG, from that of its result (``dY``) and, if given, of H
+        from elsewhere (``dH``).  H and ``rstd`` are the forward call's (X where
+        it had no H).  dX may be dY or dH itself; dG is of G's type."""
+        dtype, ldh = _matrix("H", H)
+        T, D = H.shape
+        gtype = _gain(G, H)
+        _vectors(T, torch.float32, rstd=rstd)
+        tensors, lds = {"dY": dY, "dX": dX}, {}
+        if dH is not None:
+            tensors["dH"] = dH
+        for name, t in tensors.items():
+            kind, lds[name] = _matrix(name, t)
+            if kind != dtype or t.shape != H.shape:
+                raise ValueError(f"{name} must be {T} x {D} of H's type")
+        if dG is not None:
+            _vectors(D, G.dtype, dG=dG)
+            tensors["dG"] = dG
+        s = self._on(stream, H=H, G=G, rstd=rstd, **tensors)
+        return sgemm_rmsnorm_backward(
+            self.h, dtype, gtype, T, D, dY.data_ptr(), lds["dY"], H.data_ptr(), ldh, G.data_ptr(),
+            rstd.data_ptr(), None if dH is None else dH.data_ptr(), lds.get("dH", 0),
+            dX.data_ptr(), lds["dX"], None if dG is None else dG.data_ptr(), s)
 
     # -- softmax cross entropy of an output layer --
 
@@ -860,6 +1035,14 @@ class Handle:
                                  ldw, labels.data_ptr(), ignore_index, lse.data_ptr(),
                                  dloss.data_ptr(), None if dlse is None else dlse.data_ptr(),
                                  *args, s)
+
+
+def _gain(G, X) -> int:
+    """The library type of a norm's gain for rows X."""
+    if G.dtype not in (X.dtype, torch.float32):
+        raise TypeError(f"G must be of X's type ({X.dtype}) or float32")
+    _vectors(X.shape[1], G.dtype, G=G)
+    return TENSOR_DTYPES[G.dtype]
 
 
 def _ce_shapes(X, W):

@@ -20,7 +20,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libsgemm.so")
-SOURCES = [os.path.join(CSRC, name) for name in ("sgemm.hip", "mx.hip", "ce.hip")]
+SOURCES = [os.path.join(CSRC, name) for name in ("sgemm.hip", "mx.hip", "mx8.hip", "norm.hip",
+                                                    "ce.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

@@ -7,6 +7,7 @@
 
 #include "handle.hpp"
 #include "mx_gemm.hpp"
+#include "mx_host.hpp"
 #include "mx_quant.hpp"
 #include "mx_small.hpp"
 
@@ -14,40 +15,6 @@ using namespace sgemm;
 
 namespace {
 
-int blocks_of(int K) { return K / MX_BLOCK + (K % MX_BLOCK != 0); }
-int at_least_one(int n) { return n > 1 ? n : 1; }
-long long up_div(long long a, long long b) { return (a + b - 1) / b; }
-
-ByteRange code_range(const void* p, int rows, int K, int ld) {
-  return byte_range(p, rows, 16LL * blocks_of(K), ld, 1);
-}
-ByteRange scale_range(const void* p, int rows, int K, int ld) {
-  return byte_range(p, rows, blocks_of(K), ld, 1);
-}
-
-// Strides of a quantised operand of K values a row.
-bool mx_strides_ok(int K, int ldc, int lds) {
-  const int nb = blocks_of(K);
-  return ldc >= at_least_one(16 * nb) && lds >= at_least_one(nb);
-}
-
-// Column and row counts that the kernels' 32-bit indexes hold (a tile past the
-// last row or column included).
-bool mx_sizes_ok(int R, int K) {
-  return R >= 0 && R <= SGEMM_MX_MAX_ROWS && K >= 0 && K <= SGEMM_MX_MAX_K;
-}
-
-typedef void (*quant_fn)(MxQuantArgs);
-typedef void (*quant_t_fn)(MxQuantArgs, int);
-typedef void (*dequant_fn)(MxDequantArgs);
-const quant_fn kQuant[3] = {mx_quantize_kernel<SGEMM_DTYPE_F32>, mx_quantize_kernel<SGEMM_DTYPE_BF16>,
-                            mx_quantize_kernel<SGEMM_DTYPE_F16>};
-const quant_t_fn kQuantT[3] = {mx_quantize_t_kernel<SGEMM_DTYPE_F32>,
-                               mx_quantize_t_kernel<SGEMM_DTYPE_BF16>,
-                               mx_quantize_t_kernel<SGEMM_DTYPE_F16>};
-const dequant_fn kDequant[3] = {mx_dequantize_kernel<SGEMM_DTYPE_F32>,
-                                mx_dequantize_kernel<SGEMM_DTYPE_BF16>,
-                                mx_dequantize_kernel<SGEMM_DTYPE_F16>};
 typedef void (*small_fn)(MxArgs);
 // [A's kind: codes, activations by type, activations of few rows by type]
 // [one or four tiles of columns a workgroup]
@@ -60,26 +27,6 @@ const small_fn kSmall[7][2] = {MX_SMALL(-1, false),
                                MX_SMALL(SGEMM_DTYPE_BF16, true),
                                MX_SMALL(SGEMM_DTYPE_F16, true)};
 #undef MX_SMALL
-
-// Workgroups of a quantisation and of its reverse.
-long long quantize_wgs(int trans, int R, int K) {
-  const long long nb = blocks_of(K);
-  return trans ? up_div(R, MXT_ROWS) * up_div(nb, MXT_BLOCKS)
-               : up_div(4 * nb * R, MX_THREADS * MX_UNROLL);
-}
-long long dequantize_wgs(int R, int K) {
-  return up_div(up_div(K, 8) * R, MX_THREADS * MX_UNROLL);
-}
-
-int launch_quantize(int dtype, int trans, const MxQuantArgs& g, hipStream_t stream) {
-  const dim3 wgs((unsigned)quantize_wgs(trans, g.R, g.K));
-  if (trans)
-    hipLaunchKernelGGL(kQuantT[dtype], wgs, dim3(MX_THREADS), 0, stream, g,
-                       (int)up_div(blocks_of(g.K), MXT_BLOCKS));
-  else
-    hipLaunchKernelGGL(kQuant[dtype], wgs, dim3(MX_THREADS), 0, stream, g);
-  return launched();
-}
 
 // The product straight from memory, A in codes (xdt < 0) or in activations,
 // one or four tiles of 16 columns a workgroup.
@@ -184,13 +131,13 @@ int validate_product(int M, int N, int K, const void* A, const void* B, int ldb,
   const unsigned esz = tensor_elem_bytes(dtype);
   if (esz == 0) return SGEMM_ERR_VALUE;
   if (!mx_sizes_ok(M, K) || !mx_sizes_ok(N, K)) return SGEMM_ERR_SIZE;
-  if (!mx_strides_ok(K, ldb, ldsb) || ldc < at_least_one(N)) return SGEMM_ERR_LD;
+  if (!mx_strides_ok<Mx4Format>(K, ldb, ldsb) || ldc < at_least_one(N)) return SGEMM_ERR_LD;
   if (M == 0 || N == 0) return SGEMM_OK;
   if (C == nullptr || (K > 0 && (A == nullptr || B == nullptr || SB == nullptr)))
     return SGEMM_ERR_NULL;
   if (!elem_aligned(C, esz)) return SGEMM_ERR_VALUE;
   const ByteRange c = byte_range(C, M, N, ldc, esz);
-  if (K > 0 && (ranges_meet(c, code_range(B, N, K, ldb)) || ranges_meet(c, scale_range(SB, N, K, ldsb))))
+  if (K > 0 && (ranges_meet(c, code_range<Mx4Format>(B, N, K, ldb)) || ranges_meet(c, scale_range(SB, N, K, ldsb))))
     return SGEMM_ERR_ALIAS;
   return SGEMM_OK;
 }
@@ -202,46 +149,12 @@ extern "C" {
 int sgemm_mx_quantize(sgemm_handle_t h, int dtype, int trans, int R, int K, const void* X,
                       int ldx, void* codes, int ldc, void* scales, int lds,
                       hipStream_t stream) {
-  if (h == nullptr) return SGEMM_ERR_HANDLE;
-  const unsigned esz = tensor_elem_bytes(dtype);
-  if (esz == 0 || (trans != SGEMM_OP_N && trans != SGEMM_OP_T)) return SGEMM_ERR_VALUE;
-  if (!mx_sizes_ok(R, K)) return SGEMM_ERR_SIZE;
-  if (ldx < at_least_one(trans ? R : K) || !mx_strides_ok(K, ldc, lds)) return SGEMM_ERR_LD;
-  if (R == 0 || K == 0) return SGEMM_OK;
-  if (X == nullptr || codes == nullptr || scales == nullptr) return SGEMM_ERR_NULL;
-  if (!elem_aligned(X, esz)) return SGEMM_ERR_VALUE;
-  const ByteRange x = byte_range(X, trans ? K : R, trans ? R : K, ldx, esz);
-  const ByteRange c = code_range(codes, R, K, ldc), s = scale_range(scales, R, K, lds);
-  if (ranges_meet(x, c) || ranges_meet(x, s) || ranges_meet(c, s)) return SGEMM_ERR_ALIAS;
-  if (!grid_holds(quantize_wgs(trans, R, K), MX_THREADS)) return SGEMM_ERR_UNSUPPORTED;
-  const int st = check_device(h);
-  if (st != SGEMM_OK) return st;
-  const MxQuantArgs g = {R, K, X, ldx, static_cast<uint8_t*>(codes), ldc,
-                         static_cast<uint8_t*>(scales), lds};
-  return launch_quantize(dtype, trans, g, stream);
+  return quantize_entry<Mx4Format>(h, dtype, trans, R, K, X, ldx, codes, ldc, scales, lds, stream);
 }
 
 int sgemm_mx_dequantize(sgemm_handle_t h, int dtype, int R, int K, const void* codes, int ldc,
                         const void* scales, int lds, void* Y, int ldy, hipStream_t stream) {
-  if (h == nullptr) return SGEMM_ERR_HANDLE;
-  const unsigned esz = tensor_elem_bytes(dtype);
-  if (esz == 0) return SGEMM_ERR_VALUE;
-  if (!mx_sizes_ok(R, K)) return SGEMM_ERR_SIZE;
-  if (ldy < at_least_one(K) || !mx_strides_ok(K, ldc, lds)) return SGEMM_ERR_LD;
-  if (R == 0 || K == 0) return SGEMM_OK;
-  if (codes == nullptr || scales == nullptr || Y == nullptr) return SGEMM_ERR_NULL;
-  if (!elem_aligned(Y, esz)) return SGEMM_ERR_VALUE;
-  const ByteRange y = byte_range(Y, R, K, ldy, esz);
-  if (ranges_meet(y, code_range(codes, R, K, ldc)) || ranges_meet(y, scale_range(scales, R, K, lds)))
-    return SGEMM_ERR_ALIAS;
-  if (!grid_holds(dequantize_wgs(R, K), MX_THREADS)) return SGEMM_ERR_UNSUPPORTED;
-  const int st = check_device(h);
-  if (st != SGEMM_OK) return st;
-  const MxDequantArgs g = {R, K, static_cast<const uint8_t*>(codes), ldc,
-                           static_cast<const uint8_t*>(scales), lds, Y, ldy};
-  hipLaunchKernelGGL(kDequant[dtype], dim3((unsigned)dequantize_wgs(R, K)), dim3(MX_THREADS), 0,
-                     stream, g);
-  return launched();
+  return dequantize_entry<Mx4Format>(h, dtype, R, K, codes, ldc, scales, lds, Y, ldy, stream);
 }
 
 int sgemm_validate_mx(int M, int N, int K, const void* A, int lda, const void* SA, int ldsa,
@@ -250,11 +163,11 @@ int sgemm_validate_mx(int M, int N, int K, const void* A, int lda, const void* S
   const int st = validate_product(M, N, K, A, B, ldb, SB, ldsb, dtype, C, ldc);
   if (st != SGEMM_OK) return st;
   if (K % MX_BLOCK != 0) return SGEMM_ERR_SIZE;
-  if (!mx_strides_ok(K, lda, ldsa)) return SGEMM_ERR_LD;
+  if (!mx_strides_ok<Mx4Format>(K, lda, ldsa)) return SGEMM_ERR_LD;
   if (M == 0 || N == 0 || K == 0) return SGEMM_OK;
   if (SA == nullptr) return SGEMM_ERR_NULL;
   const ByteRange c = byte_range(C, M, N, ldc, tensor_elem_bytes(dtype));
-  if (ranges_meet(c, code_range(A, M, K, lda)) || ranges_meet(c, scale_range(SA, M, K, ldsa)))
+  if (ranges_meet(c, code_range<Mx4Format>(A, M, K, lda)) || ranges_meet(c, scale_range(SA, M, K, ldsa)))
     return SGEMM_ERR_ALIAS;
   return SGEMM_OK;
 }
@@ -306,7 +219,7 @@ int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K, float a
   uint8_t* scales = codes + 16 * nb * rows;
   const MxQuantArgs q = {M, K, X, ldx, codes, (int)(16 * nb), scales, (int)nb};
   if (K > 0) {
-    st = launch_quantize(xtype, SGEMM_OP_N, q, stream);
+    st = launch_quantize<Mx4Format>(xtype, SGEMM_OP_N, q, stream);
     if (st != SGEMM_OK) return st;
   }
   g.K = (int)(MX_BLOCK * nb);

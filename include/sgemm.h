@@ -512,6 +512,80 @@ int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K,
                        int ldb, const void* SB, int ldsb, float beta,
                        int dtype, void* C, int ldc, hipStream_t stream);
 
+/* ---- microscaled 8-bit rows ---------------------------------------------------
+ *
+ * As the 4-bit rows above, with 32 code bytes a block: OCP E4M3 (a sign, four
+ * exponent bits, three more of the significand, magnitudes up to 448), value i
+ * of a block in its byte i.  Code strides are at least 32*ceil(K/32) bytes.
+ * Codes of NaN (0x7f, 0xff) stand for NaN.
+ *
+ * Quantising: a block with largest magnitude a gets the least s - 127, of at
+ * least -127, with a <= 448 * 2^(s-127), so that nothing is clipped, and the
+ * elements x / 2^(s-127) rounded to the nearest code, ties to even.  The rest is
+ * as sgemm_mx_quantize and sgemm_mx_dequantize have it, but that a magnitude of
+ * at least 31/32 of the power of two past its type's largest value (binary16:
+ * 63488) rounds to that power, which the type reads back as an infinity. */
+int sgemm_mx_byte_quantize(sgemm_handle_t h, int dtype, int trans, int R, int K,
+                       const void* X, int ldx, void* codes, int ldc,
+                       void* scales, int lds, hipStream_t stream);
+int sgemm_mx_byte_dequantize(sgemm_handle_t h, int dtype, int R, int K,
+                         const void* codes, int ldc, const void* scales,
+                         int lds, void* Y, int ldy, hipStream_t stream);
+
+/* ---- root-mean-square norm of a residual stream ----------------------------------
+ *
+ *     h = x + r,  rstd = (mean_j h_j^2 + eps)^(-1/2),  y_j = (h_j * rstd) * g_j
+ *
+ * for T rows of D values.  X, R (NULL: nothing is added) and H are of type dtype
+ * (SGEMM_DTYPE_F32, _BF16 or _F16) with row strides in elements, the gain G (D
+ * values) of type gtype, dtype or SGEMM_DTYPE_F32.  h is rounded to dtype, and
+ * what is normed is that; it goes to H unless that is NULL.  y leaves as
+ * microscaled 8-bit rows, quantised from 32 bits, and rstd (unless NULL) as T
+ * floats for the gradients.  Arithmetic is 32-bit.  H may be X or R itself
+ * (address and stride); else outputs must not overlap anything
+ * (SGEMM_ERR_ALIAS).  A row with an infinity has rstd 0, one with a NaN NaN.
+ *
+ * Ownership, streams, errors and threading as for sgemm_run (with a workspace:
+ * the gradients).  T == 0: nothing is read.  SGEMM_ERR_SIZE for T < 0 or over
+ * SGEMM_MX_MAX_ROWS and D < 1 or over SGEMM_MX_MAX_K; SGEMM_ERR_VALUE for another
+ * type or a tensor not aligned to its element. */
+int sgemm_rmsnorm(sgemm_handle_t h, int dtype, int gtype, int T, int D,
+                      const void* X, int ldx, const void* R, int ldr,
+                      const void* G, float eps, void* H, int ldh, void* codes,
+                      int ldc, void* scales, int lds, float* rstd,
+                      hipStream_t stream);
+
+/* Gradients: from that of y (dY, the rounding to 8 bits counting as none) and,
+ * unless NULL, of H from elsewhere (dH), with n = h * rstd,
+ *
+ *     dX = rstd * (dY * g - n * mean_j(dY_j g_j n_j)) + dH,  dG = sum_t dY * n
+ *
+ * in 32 bits, rounded once to dtype and gtype.  dX is the gradient of x and of r.
+ * H and rstd are the forward call's (X where it had no R and no H).  dX may be dY
+ * or dH itself.  dG may be NULL; its sums over rows use the handle's workspace:
+ * at least `least` bytes (SGEMM_ERR_SCRATCH), up to `full`; less than that means
+ * fewer workgroups.  The same workspace gives the same bits.  T == 0: dG is set
+ * to 0. */
+int sgemm_rmsnorm_backward(sgemm_handle_t h, int dtype, int gtype, int T, int D,
+                           const void* dY, int lddy, const void* H, int ldh,
+                           const void* G, const float* rstd, const void* dH,
+                           int lddh, void* dX, int lddx, void* dG,
+                           hipStream_t stream);
+int sgemm_rmsnorm_workspace_size(sgemm_handle_t h, int T, int D, size_t* least,
+                                 size_t* full);
+
+/* The argument checks of the two, without a device. */
+int sgemm_validate_rmsnorm(int dtype, int gtype, int T, int D, const void* X,
+                               int ldx, const void* R, int ldr, const void* G,
+                               const void* H, int ldh, const void* codes,
+                               int ldc, const void* scales, int lds,
+                               const float* rstd);
+int sgemm_validate_rmsnorm_backward(int dtype, int gtype, int T, int D,
+                                    const void* dY, int lddy, const void* H,
+                                    int ldh, const void* G, const float* rstd,
+                                    const void* dH, int lddh, const void* dX,
+                                    int lddx, const void* dG);
+
 /* ---- softmax cross entropy of an output layer --------------------------------
  *
  *     z = alpha * X * W^T,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,label(t)

@@ -1,0 +1,199 @@
+"""Microscaled 8-bit rows and the norm without a GPU: the plain implementation
+against hand-worked values and differences, and every refusal of the C entries
+and the binding."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import fp32_gemm_major_amd as sg
+from tests import mx8_reference as ref
+from tests.test_ce_host import HostHandle
+
+F32, BF16, F16 = sg.SGEMM_DTYPE_F32, sg.SGEMM_DTYPE_BF16, sg.SGEMM_DTYPE_F16
+X, R, G, H = 0x10000000, 0x20000000, 0x30000000, 0x40000000  # never touched
+CODES, SCALES, RSTD = 0x50000000, 0x60000000, 0x70000000
+DY, DH, DX, DG = 0x80000000, 0x90000000, 0xA0000000, 0xB0000000
+
+
+def test_reference_by_hand():
+    x = np.zeros((1, 32))
+    # largest 448: scale 2^0, the elements are the values themselves, rounded
+    x[0, :12] = [448, 432, 416, -17, 15.5, 1.0625, 1.1875, 2 ** -9, 2 ** -10, 3 * 2 ** -10, -0.0, 240]
+    codes, scales = ref.quantize(x)
+    assert scales.tolist() == [[127]]
+    got = ref.dequantize(codes, scales)[0, :12]
+    assert got.tolist() == [448, 448, 416, -16, 16, 1, 1.25, 2 ** -9, 0, 2 ** -8, 0, 240]
+    assert codes[0, 0] == 0x7e and codes[0, 10] == 0x80
+    # scales: the least power of two with a <= 448 of them, at least 2^-127
+    for a, s in ((448.0, 127), (448.0001, 128), (1.75, 119), (1.76, 120), (1.0, 119), (0.875, 118),
+                 (2.0 ** -119, 0), (2.0 ** -118, 1), (2.0 ** -149, 0), (2.0 ** 127, 246),
+                 (3.4e38, 247), (0.0, 0)):
+        assert ref.quantize(np.full((1, 3), a))[1].tolist() == [[s]], a
+    assert ref.quantize(np.array([[np.nan, 1.0]]))[1].tolist() == [[255]]
+    # every code but NaN's comes back as itself
+    c = np.array([[k for k in range(256) if k & 127 != 127] + [0x7e, 0]], np.uint8)
+    v = ref.dequantize(c, np.full((1, 8), 127, np.uint8))
+    v[0, ::32] = 448  # (every block's largest)
+    q, s = ref.quantize(v)
+    c[0, ::32] = 0x7e
+    assert (s == 127).all() and np.array_equal(q, c)
+
+
+def test_reference_gradients_by_differences():
+    rng = np.random.default_rng(0)
+    T, D, eps = 4, 7, 0.3
+    x, g = rng.standard_normal((T, D)), rng.standard_normal(D)
+    dy, dh = rng.standard_normal((T, D)), rng.standard_normal((T, D))
+
+    def total():
+        return (dy * ref.norm(x, g, eps)[0]).sum() + (dh * x).sum()
+
+    dx, dg, _, _ = ref.norm_gradients(dy, x, g, ref.norm(x, g, eps)[1], dh)
+    for grad, t in ((dx, x), (dg, g)):
+        for i in np.ndindex(t.shape):
+            keep = t[i]
+            t[i] = keep + 1e-6
+            up = total()
+            t[i] = keep - 1e-6
+            down = total()
+            t[i] = keep
+            assert abs((up - down) / 2e-6 - grad[i]) < 1e-7
+
+
+def norm(**kw):
+    a = dict(dtype=BF16, gtype=BF16, T=4, D=70, X=X, ldx=70, R=R, ldr=70, G=G, H=H, ldh=70,
+             codes=CODES, ldc=96, scales=SCALES, lds=3, rstd=RSTD)
+    a.update(kw)
+    return sg.sgemm_validate_rmsnorm(*a.values())
+
+
+def back(**kw):
+    a = dict(dtype=BF16, gtype=BF16, T=4, D=70, dY=DY, lddy=70, H=H, ldh=70, G=G, rstd=RSTD, dH=DH,
+             lddh=70, dX=DX, lddx=70, dG=DG)
+    a.update(kw)
+    return sg.sgemm_validate_rmsnorm_backward(*a.values())
+
+
+def test_validate_norm():
+    assert norm() == sg.SGEMM_OK and norm(dtype=F32, gtype=F32) == sg.SGEMM_OK
+    assert norm(gtype=F32) == sg.SGEMM_OK and norm(dtype=F16, gtype=F16) == sg.SGEMM_OK
+    assert norm(R=None, ldr=0) == sg.SGEMM_OK and norm(H=None, ldh=0, rstd=None) == sg.SGEMM_OK
+    for bad in (-1, 3, 4):
+        assert norm(dtype=bad) == sg.SGEMM_ERR_VALUE and norm(gtype=bad) == sg.SGEMM_ERR_VALUE
+    assert norm(gtype=F16) == sg.SGEMM_ERR_VALUE and norm(dtype=F32) == sg.SGEMM_ERR_VALUE
+    assert norm(T=-1) == sg.SGEMM_ERR_SIZE and norm(D=0) == sg.SGEMM_ERR_SIZE
+    assert norm(T=sg.SGEMM_MX_MAX_ROWS + 1) == sg.SGEMM_ERR_SIZE
+    assert norm(D=sg.SGEMM_MX_MAX_K + 1, ldx=2 ** 30, ldr=2 ** 30, ldh=2 ** 30, ldc=2 ** 30,
+                lds=2 ** 30) == sg.SGEMM_ERR_SIZE
+    for name, short in (("ldx", 69), ("ldr", 69), ("ldh", 69), ("ldc", 95), ("lds", 2)):
+        assert norm(**{name: short}) == sg.SGEMM_ERR_LD, name
+    for name in ("X", "G", "codes", "scales"):
+        assert norm(**{name: None}) == sg.SGEMM_ERR_NULL, name
+    assert norm(T=0, X=None, G=None, codes=None, scales=None) == sg.SGEMM_OK
+    for name, off in (("X", 1), ("R", 1), ("G", 1), ("H", 1), ("rstd", 2)):
+        assert norm(**{name: globals()[name.upper()] + off}) == sg.SGEMM_ERR_VALUE, name
+    assert norm(gtype=F32, G=G + 2) == sg.SGEMM_ERR_VALUE
+    assert norm(codes=CODES + 1, scales=SCALES + 3) == sg.SGEMM_OK  # any byte address
+    # in place: the same window of X or R, not another one that meets it
+    assert norm(H=X) == sg.SGEMM_OK and norm(H=R) == sg.SGEMM_OK
+    assert norm(H=X, ldh=72) == sg.SGEMM_ERR_ALIAS and norm(H=R + 140) == sg.SGEMM_ERR_ALIAS
+    assert norm(H=X, R=X) == sg.SGEMM_OK
+    last = (3 * 70 + 69) * 2
+    for out in ("codes", "scales", "rstd"):
+        for p in (X + last, R + last, G + 138, H + last):
+            if out != "rstd" or p % 4 == 0:
+                assert norm(**{out: p}) == sg.SGEMM_ERR_ALIAS, (out, p)
+    assert norm(rstd=X) == sg.SGEMM_ERR_ALIAS and norm(rstd=G) == sg.SGEMM_ERR_ALIAS
+    assert norm(H=G) == sg.SGEMM_ERR_ALIAS
+    assert norm(scales=CODES + 3 * 96 + 95) == sg.SGEMM_ERR_ALIAS
+    assert norm(rstd=CODES + 4) == sg.SGEMM_ERR_ALIAS and norm(rstd=SCALES + 8) == sg.SGEMM_ERR_ALIAS
+
+
+def test_validate_backward():
+    assert back() == sg.SGEMM_OK and back(dH=None, lddh=0, dG=None) == sg.SGEMM_OK
+    assert back(dtype=F32, gtype=F32) == sg.SGEMM_OK and back(gtype=F32) == sg.SGEMM_OK
+    assert back(dtype=3) == sg.SGEMM_ERR_VALUE and back(gtype=F16) == sg.SGEMM_ERR_VALUE
+    assert back(T=-1) == sg.SGEMM_ERR_SIZE and back(D=0) == sg.SGEMM_ERR_SIZE
+    for name in ("lddy", "ldh", "lddh", "lddx"):
+        assert back(**{name: 69}) == sg.SGEMM_ERR_LD, name
+    for name in ("dY", "H", "G", "rstd", "dX"):
+        assert back(**{name: None}) == sg.SGEMM_ERR_NULL, name
+    assert back(T=0, dY=None, H=None, G=None, rstd=None, dX=None) == sg.SGEMM_OK
+    for name, off in (("dY", 1), ("H", 1), ("G", 1), ("dH", 1), ("dX", 1), ("dG", 1), ("rstd", 2)):
+        assert back(**{name: globals()[name.upper()] + off}) == sg.SGEMM_ERR_VALUE, name
+    # dX may stand in dY's or dH's place
+    assert back(dX=DY) == sg.SGEMM_OK and back(dX=DH) == sg.SGEMM_OK
+    assert back(dX=DY, lddx=72) == sg.SGEMM_ERR_ALIAS and back(dX=DH + 2) == sg.SGEMM_ERR_ALIAS
+    for p in (H, G, RSTD, DG):
+        assert back(dX=p) == sg.SGEMM_ERR_ALIAS
+    for p in (DY, H, DH, G, RSTD, DX):
+        assert back(dG=p) == sg.SGEMM_ERR_ALIAS
+
+
+def test_entries_without_a_device():
+    lib = sg.library()
+    assert lib.sgemm_mx_byte_quantize(None, F32, 0, 1, 32, X, 32, CODES, 32, SCALES, 1,
+                                      None) == sg.SGEMM_ERR_HANDLE
+    assert lib.sgemm_mx_byte_dequantize(None, F32, 1, 32, CODES, 32, SCALES, 1, X, 32,
+                                        None) == sg.SGEMM_ERR_HANDLE
+    assert lib.sgemm_rmsnorm(None, F32, F32, 1, 32, X, 32, None, 0, G, 1e-6, None, 0, CODES, 32,
+                             SCALES, 1, None, None) == sg.SGEMM_ERR_HANDLE
+    assert lib.sgemm_rmsnorm_backward(None, F32, F32, 1, 32, DY, 32, H, 32, G, RSTD, None, 0, DX, 32,
+                                      None, None) == sg.SGEMM_ERR_HANDLE
+    assert lib.sgemm_rmsnorm_workspace_size(None, 1, 1, None, None) == sg.SGEMM_ERR_HANDLE
+    h = HostHandle()
+    at = ctypes.addressof(h)
+
+    def quantize(dtype=BF16, trans=0, R=3, K=40, ldx=40, ldc=64, lds=2, x=X, c=CODES, s=SCALES):
+        return lib.sgemm_mx_byte_quantize(at, dtype, trans, R, K, x, ldx, c, ldc, s, lds, None)
+
+    assert quantize() == sg.SGEMM_ERR_DEVICE  # (as far as it gets without one)
+    assert quantize(ldc=63) == sg.SGEMM_ERR_LD and quantize(lds=1) == sg.SGEMM_ERR_LD
+    assert quantize(dtype=3) == sg.SGEMM_ERR_VALUE and quantize(trans=2) == sg.SGEMM_ERR_VALUE
+    assert quantize(x=X + 1) == sg.SGEMM_ERR_VALUE and quantize(c=None) == sg.SGEMM_ERR_NULL
+    assert quantize(c=X + 4) == sg.SGEMM_ERR_ALIAS and quantize(s=CODES + 2 * 64 + 63) == sg.SGEMM_ERR_ALIAS
+    assert quantize(R=0, x=None) == sg.SGEMM_OK
+    # 2^24 workgroups of 512 units of eight values are one too many
+    K = 1 << 20
+    fits = ((1 << 24) - 1) * 512 * 8 // K
+    far = dict(K=K, ldx=K, ldc=K, lds=K // 32, x=1 << 60, c=1 << 52, s=1 << 56)
+    assert quantize(R=fits + 1, **far) == sg.SGEMM_ERR_UNSUPPORTED
+    assert quantize(R=fits, **far) == sg.SGEMM_ERR_DEVICE
+    # the norm's rows are taken in turns: any number
+    assert lib.sgemm_rmsnorm(at, F32, F32, sg.SGEMM_MX_MAX_ROWS, 8, 1 << 50, 8, None, 0, G, 1e-6, None,
+                             0, 1 << 54, 32, 1 << 56, 1, None, None) == sg.SGEMM_ERR_DEVICE
+    least, full = sg.sgemm_rmsnorm_workspace_size(at, 1000, 100)
+    assert least == 4 * 4 * 100 and full == min(250, 2 * h.cus) * least
+    assert sg.sgemm_rmsnorm_workspace_size(at, 0, 5000) == (0, 0)
+    assert sg.sgemm_rmsnorm_workspace_size(at, 3, 5000) == (20000, 60000)
+
+
+def test_container():
+    torch = pytest.importorskip("torch")
+    u8 = dict(dtype=torch.uint8)
+    q = sg.Mx8.empty(3, 65, "cpu")
+    assert (q.rows, q.K, tuple(q.codes.shape), tuple(q.scales.shape)) == (3, 96, (3, 96), (3, 3))
+    assert sg.Mx8.nbytes(3, 65) == q.codes.numel() + q.scales.numel()
+    assert sg.Mx4.nbytes(3, 65) == 3 * 17 * 3
+    sg.Mx8(torch.zeros(3, 70, **u8)[:, :64], torch.zeros(3, 2, **u8))
+    for codes, scales in (((3, 32), (3, 2)), ((3, 64), (4, 2))):
+        with pytest.raises(ValueError):
+            sg.Mx8(torch.zeros(codes, **u8), torch.zeros(scales, **u8))
+    with pytest.raises(TypeError):
+        sg.Mx8(torch.zeros(3, 64), torch.zeros(3, 2, **u8))
+    with pytest.raises(ValueError):
+        sg.Mx8.empty(3, 2 ** 31, "meta")
+
+
+def test_binding_checks():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(3, 40, dtype=torch.bfloat16)
+    assert sg._gain(torch.ones(40), x) == F32
+    assert sg._gain(torch.ones(40, dtype=torch.bfloat16), x) == BF16
+    with pytest.raises(TypeError):
+        sg._gain(torch.ones(40, dtype=torch.float16), x)
+    with pytest.raises(ValueError):
+        sg._gain(torch.ones(41), x)
+    with pytest.raises(ValueError):
+        sg._gain(torch.ones(80)[::2], x)

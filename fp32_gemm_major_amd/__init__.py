@@ -72,7 +72,8 @@ EXPORTED = [
     "sgemm_lowp_kernel_schedule", "sgemm_lowp_plan_handle",
     "sgemm_mx_quantize", "sgemm_mx_dequantize", "sgemm_run_mx", "sgemm_validate_mx",
     "sgemm_run_mx_quant",
-    "sgemm_mx_byte_quantize", "sgemm_mx_byte_dequantize",
+    "sgemm_mx_byte_quantize", "sgemm_mx_byte_dequantize", "sgemm_run_mx_byte",
+    "sgemm_validate_mx_byte", "sgemm_run_mx_byte_quant",
     "sgemm_rmsnorm", "sgemm_validate_rmsnorm", "sgemm_rmsnorm_backward",
     "sgemm_validate_rmsnorm_backward", "sgemm_rmsnorm_workspace_size",
     "sgemm_ce_workspace_size", "sgemm_ce_forward", "sgemm_ce_backward", "sgemm_validate_ce",
@@ -138,6 +139,9 @@ def _bind(lib):
     q, sp = ctypes.c_longlong, ctypes.POINTER(ctypes.c_size_t)
     lib.sgemm_mx_byte_quantize.argtypes = lib.sgemm_mx_quantize.argtypes
     lib.sgemm_mx_byte_dequantize.argtypes = lib.sgemm_mx_dequantize.argtypes
+    lib.sgemm_run_mx_byte.argtypes = [p, i, i, i, i, f, p, i, p, i, p, i, p, i, f, i, p, i, p]
+    lib.sgemm_validate_mx_byte.argtypes = [i, i, i, i, p, i, p, i, p, i, p, i, i, p, i]
+    lib.sgemm_run_mx_byte_quant.argtypes = [p, i, i, i, i, i, f, p, i, p, i, p, i, f, i, p, i, p]
     lib.sgemm_rmsnorm.argtypes = [p, i, i, i, i, p, i, p, i, p, f, p, i, p, i, p, i, p, p]
     lib.sgemm_validate_rmsnorm.argtypes = [i, i, i, i, p, i, p, i, p, p, i, p, i, p, i, p]
     lib.sgemm_rmsnorm_backward.argtypes = [p, i, i, i, i, p, i, p, i, p, p, p, i, p, i, p, p]
@@ -151,7 +155,8 @@ def _bind(lib):
     for name in ("sgemm_ce_workspace_size", "sgemm_ce_forward", "sgemm_ce_backward",
                  "sgemm_validate_ce", "sgemm_validate_ce_backward", "sgemm_mx_quantize", "sgemm_mx_dequantize", "sgemm_run_mx",
                  "sgemm_validate_mx", "sgemm_run_mx_quant", "sgemm_mx_byte_quantize",
-                 "sgemm_mx_byte_dequantize", "sgemm_rmsnorm", "sgemm_validate_rmsnorm",
+                 "sgemm_mx_byte_dequantize", "sgemm_run_mx_byte", "sgemm_validate_mx_byte",
+                 "sgemm_run_mx_byte_quant", "sgemm_rmsnorm", "sgemm_validate_rmsnorm",
                  "sgemm_rmsnorm_backward", "sgemm_validate_rmsnorm_backward",
                  "sgemm_rmsnorm_workspace_size"):
         getattr(lib, name).restype = i
@@ -327,6 +332,27 @@ def sgemm_mx_byte_dequantize(h, dtype, R, K, codes, ldc, scales, lds, Y, ldy, st
     """The values of microscaled 8-bit rows as a tensor of type ``dtype``."""
     return _check(library().sgemm_mx_byte_dequantize(h, dtype, R, K, codes, ldc, scales, lds, Y,
                                                  ldy, stream), "sgemm_mx_byte_dequantize")
+
+
+def sgemm_run_mx_byte(h, bits, M, N, K, alpha, A, lda, SA, ldsa, B, ldb, SB, ldsb, beta, dtype, C,
+                      ldc, stream=0) -> int:
+    """The product of microscaled 8-bit rows A and 8- or 4-bit (``bits``) rows B."""
+    return _check(library().sgemm_run_mx_byte(h, bits, M, N, K, alpha, A, lda, SA, ldsa, B, ldb,
+                                              SB, ldsb, beta, dtype, C, ldc, stream),
+                  "sgemm_run_mx_byte")
+
+
+def sgemm_validate_mx_byte(bits, M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, dtype, C, ldc) -> int:
+    return library().sgemm_validate_mx_byte(bits, M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb,
+                                            dtype, C, ldc)
+
+
+def sgemm_run_mx_byte_quant(h, xtype, bits, M, N, K, alpha, X, ldx, B, ldb, SB, ldsb, beta, dtype,
+                            C, ldc, stream=0) -> int:
+    """sgemm_run_mx_byte with A quantised in the call from the M x K tensor X."""
+    return _check(library().sgemm_run_mx_byte_quant(h, xtype, bits, M, N, K, alpha, X, ldx, B, ldb,
+                                                    SB, ldsb, beta, dtype, C, ldc, stream),
+                  "sgemm_run_mx_byte_quant")
 
 
 def sgemm_rmsnorm(h, dtype, gtype, T, D, X, ldx, R, ldr, G, eps, H, ldh, codes, ldc, scales,
@@ -892,23 +918,31 @@ class Handle:
         ``Mx4`` of M rows, or an M x K float32, bfloat16 or float16 tensor
         that the call quantises (``mx4_quantize``; over 16 rows through the
         handle's workspace).  C is M x N, float32, bfloat16 or float16."""
+        if isinstance(A, Mx8):
+            raise TypeError("A must be an Mx4 or a tensor (8-bit rows: gemm_mx8)")
+        if not isinstance(B, Mx4):
+            raise TypeError("B must be an Mx4")
+        return self._mx_product(Mx4, sgemm_run_mx, sgemm_run_mx_quant, (), A, B, C, alpha, beta,
+                                stream)
+
+    def _mx_product(self, kind, call, call_quant, bits, A, B, C, alpha, beta, stream):
         dtype, ldc = _matrix("C", C)
         M, N = C.shape
-        quantised = isinstance(A, Mx4)
+        quantised = isinstance(A, kind)
         rows, K = (A.rows, A.K) if quantised else A.shape
         if rows != M or B.rows != N or SGEMM_MX_BLOCK * -(-K // SGEMM_MX_BLOCK) != B.K:
             raise ValueError(f"A {rows} x {K} and B {B.rows} x {B.K} do not give "
                              f"{M} x {N}")
         if quantised:
             s = self._on(stream, A=A.codes, A_scales=A.scales, B=B.codes, B_scales=B.scales, C=C)
-            return sgemm_run_mx(self.h, M, N, K, alpha, A.codes.data_ptr(), A._ldc,
-                                A.scales.data_ptr(), A._lds, B.codes.data_ptr(), B._ldc,
-                                B.scales.data_ptr(), B._lds, beta, dtype, C.data_ptr(), ldc, s)
+            return call(self.h, *bits, M, N, K, alpha, A.codes.data_ptr(), A._ldc,
+                        A.scales.data_ptr(), A._lds, B.codes.data_ptr(), B._ldc,
+                        B.scales.data_ptr(), B._lds, beta, dtype, C.data_ptr(), ldc, s)
         xtype, lda = _matrix("A", A)
         s = self._on(stream, A=A, B=B.codes, B_scales=B.scales, C=C)
-        return sgemm_run_mx_quant(self.h, xtype, M, N, K, alpha, A.data_ptr(), lda,
-                                  B.codes.data_ptr(), B._ldc, B.scales.data_ptr(), B._lds, beta,
-                                  dtype, C.data_ptr(), ldc, s)
+        return call_quant(self.h, xtype, *bits, M, N, K, alpha, A.data_ptr(), lda,
+                          B.codes.data_ptr(), B._ldc, B.scales.data_ptr(), B._lds, beta,
+                          dtype, C.data_ptr(), ldc, s)
 
     # -- microscaled 8-bit rows --
 
@@ -921,6 +955,20 @@ class Handle:
     def mx8_dequantize(self, Q, out, stream=None):
         """The values of an ``Mx8``, as ``mx4_dequantize``."""
         return self._mx_dequantize(Mx8, sgemm_mx_byte_dequantize, Q, out, stream)
+
+    def gemm_mx8(self, A, B, C, alpha=1.0, beta=0.0, stream=None):
+        """C = alpha * A @ B^T + beta * C with B an ``Mx8`` or ``Mx4`` of N rows
+        and A an ``Mx8`` of M rows, or an M x K float32, bfloat16 or float16
+        tensor that the call quantises (``mx8_quantize``; over four rows
+        through the handle's workspace, ``Mx8.nbytes(M, K)`` bytes of it).  C
+        is M x N, float32, bfloat16 or float16; the products' sums carry about
+        2^-15 of the result as error, more than 32-bit sums would."""
+        if isinstance(A, Mx4):
+            raise TypeError("A must be an Mx8 or a tensor (4-bit rows: gemm_mx4)")
+        if not isinstance(B, _MxRows):
+            raise TypeError("B must be an Mx8 or an Mx4")
+        return self._mx_product(Mx8, sgemm_run_mx_byte, sgemm_run_mx_byte_quant,
+                                (8 if isinstance(B, Mx8) else 4,), A, B, C, alpha, beta, stream)
 
     # -- root-mean-square norm --
 

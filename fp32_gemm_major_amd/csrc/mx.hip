@@ -31,31 +31,8 @@ const small_fn kSmall[7][2] = {MX_SMALL(-1, false),
 // The product straight from memory, A in codes (xdt < 0) or in activations,
 // one or four tiles of 16 columns a workgroup.
 int launch_small(int xdt, int tiles, const MxArgs& g, hipStream_t stream) {
-  constexpr int kRows = 65535 * MXS_TILE;  // a grid's second extent
-  // (the first one's threads are counted in 32 bits: 2^23 workgroups less one)
-  constexpr int kCols = (int)(0xffffffffu / MXS_THREADS) * MXS_TILE;
   const int kind = xdt < 0 ? 0 : g.M <= MXS_FEW ? 4 + xdt : 1 + xdt;
-  for (long long m0 = 0; m0 < g.M; m0 += kRows)
-    for (long long n0 = 0; n0 < g.N; n0 += kCols) {
-      MxArgs p = g;
-      p.M = (int)(g.M - m0 < kRows ? g.M - m0 : kRows);
-      p.N = (int)(g.N - n0 < kCols ? g.N - n0 : kCols);
-      if (g.K > 0 && m0 > 0) {  // (activations come with 16 rows at most)
-        p.A = static_cast<const uint8_t*>(g.A) + (size_t)m0 * g.lda;
-        p.SA = g.SA + (size_t)m0 * g.ldsa;
-      }
-      if (g.K > 0 && n0 > 0) {
-        p.B = g.B + (size_t)n0 * g.ldb;
-        p.SB = g.SB + (size_t)n0 * g.ldsb;
-      }
-      p.C = static_cast<char*>(g.C) + ((size_t)m0 * g.ldc + (size_t)n0) * tensor_elem_bytes(g.cdt);
-      hipLaunchKernelGGL(kSmall[kind][tiles == 4],
-                         dim3((unsigned)up_div(p.N, MXS_TILE * tiles), (unsigned)up_div(p.M, MXS_TILE)),
-                         dim3(MXS_THREADS), 0, stream, p);
-      const int st = launched();
-      if (st != SGEMM_OK) return st;
-    }
-  return SGEMM_OK;
+  return launch_small_grid(kSmall[kind][tiles == 4], tiles, g, stream);
 }
 
 // Tiles of columns a workgroup of up to 16 rows takes.  Four, once that still
@@ -67,12 +44,6 @@ int row_tiles(int xdt, const MxArgs& g, int cus) {
   return 2 * up_div(g.N, 4 * MXS_TILE) >= cus && (xdt >= 0 || g.K >= 2048) ? 4 : 1;
 }
 
-typedef void (*tile_fn)(MxArgs, int, int, int);
-struct MxTileDesc {
-  int b;  // rows and columns of the tile
-  int threads;
-  tile_fn kernel[3];  // by type of C
-};
 template <class T>
 constexpr MxTileDesc tile_desc() {
   return MxTileDesc{T::BM, T::THREADS,
@@ -80,20 +51,6 @@ constexpr MxTileDesc tile_desc() {
                      mx_gemm_kernel<T, SGEMM_DTYPE_F16>}};
 }
 const MxTileDesc kTiles[3] = {tile_desc<X256x256>(), tile_desc<X128x128>(), tile_desc<X64x64>()};
-
-// The tile kernels' direct loads address a tile's rows by 32-bit offsets.
-bool tile_fits(const MxTileDesc& t, const MxArgs& g) {
-  const long long far = 1LL << 32, r = t.b - 1;
-  return r * g.lda + 128 < far && r * g.ldb + 128 < far && r * g.ldsa + 8 < far &&
-         r * g.ldsb + 8 < far && grid_holds(up_div(g.M, t.b) * up_div(g.N, t.b), t.threads);
-}
-
-int launch_tile(const MxTileDesc& t, const MxArgs& g, hipStream_t stream) {
-  const int tm = (int)up_div(g.M, t.b), tn = (int)up_div(g.N, t.b);
-  hipLaunchKernelGGL(t.kernel[g.cdt], dim3((unsigned)(tm * tn)), dim3(t.threads), 0, stream, g, tm,
-                     tn, band_rows(tm, tm * tn));
-  return launched();
-}
 
 // The kernel for a product of codes (measured on 256 CUs, with B read from
 // memory; where it stands in the last-level cache from the call before, 64-square
@@ -125,23 +82,6 @@ int launch_product(const sgemm_handle_s* h, const MxArgs& g, hipStream_t stream)
   return launch_small(-1, 1, g, stream);  // (strides past the tiles' offsets)
 }
 
-// Checks shared by both product entries but for A's own.
-int validate_product(int M, int N, int K, const void* A, const void* B, int ldb, const void* SB,
-                     int ldsb, int dtype, const void* C, int ldc) {
-  const unsigned esz = tensor_elem_bytes(dtype);
-  if (esz == 0) return SGEMM_ERR_VALUE;
-  if (!mx_sizes_ok(M, K) || !mx_sizes_ok(N, K)) return SGEMM_ERR_SIZE;
-  if (!mx_strides_ok<Mx4Format>(K, ldb, ldsb) || ldc < at_least_one(N)) return SGEMM_ERR_LD;
-  if (M == 0 || N == 0) return SGEMM_OK;
-  if (C == nullptr || (K > 0 && (A == nullptr || B == nullptr || SB == nullptr)))
-    return SGEMM_ERR_NULL;
-  if (!elem_aligned(C, esz)) return SGEMM_ERR_VALUE;
-  const ByteRange c = byte_range(C, M, N, ldc, esz);
-  if (K > 0 && (ranges_meet(c, code_range<Mx4Format>(B, N, K, ldb)) || ranges_meet(c, scale_range(SB, N, K, ldsb))))
-    return SGEMM_ERR_ALIAS;
-  return SGEMM_OK;
-}
-
 }  // namespace
 
 extern "C" {
@@ -160,16 +100,8 @@ int sgemm_mx_dequantize(sgemm_handle_t h, int dtype, int R, int K, const void* c
 int sgemm_validate_mx(int M, int N, int K, const void* A, int lda, const void* SA, int ldsa,
                       const void* B, int ldb, const void* SB, int ldsb, int dtype,
                       const void* C, int ldc) {
-  const int st = validate_product(M, N, K, A, B, ldb, SB, ldsb, dtype, C, ldc);
-  if (st != SGEMM_OK) return st;
-  if (K % MX_BLOCK != 0) return SGEMM_ERR_SIZE;
-  if (!mx_strides_ok<Mx4Format>(K, lda, ldsa)) return SGEMM_ERR_LD;
-  if (M == 0 || N == 0 || K == 0) return SGEMM_OK;
-  if (SA == nullptr) return SGEMM_ERR_NULL;
-  const ByteRange c = byte_range(C, M, N, ldc, tensor_elem_bytes(dtype));
-  if (ranges_meet(c, code_range<Mx4Format>(A, M, K, lda)) || ranges_meet(c, scale_range(SA, M, K, ldsa)))
-    return SGEMM_ERR_ALIAS;
-  return SGEMM_OK;
+  return validate_codes<Mx4Format, Mx4Format>(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, dtype,
+                                              C, ldc);
 }
 
 int sgemm_run_mx(sgemm_handle_t h, int M, int N, int K, float alpha, const void* A, int lda,
@@ -191,16 +123,9 @@ int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K, float a
                        const void* X, int ldx, const void* B, int ldb, const void* SB, int ldsb,
                        float beta, int dtype, void* C, int ldc, hipStream_t stream) {
   if (h == nullptr) return SGEMM_ERR_HANDLE;
-  const unsigned xsz = tensor_elem_bytes(xtype);
-  if (xsz == 0) return SGEMM_ERR_VALUE;
-  int st = validate_product(M, N, K, X, B, ldb, SB, ldsb, dtype, C, ldc);
+  int st = validate_activations<Mx4Format>(xtype, M, N, K, X, ldx, B, ldb, SB, ldsb, dtype, C, ldc);
   if (st != SGEMM_OK) return st;
-  if (ldx < at_least_one(K)) return SGEMM_ERR_LD;
   if (M == 0 || N == 0) return SGEMM_OK;
-  if (K > 0 && !elem_aligned(X, xsz)) return SGEMM_ERR_VALUE;
-  if (ranges_meet(byte_range(C, M, N, ldc, tensor_elem_bytes(dtype)), byte_range(X, M, K, ldx, xsz)))
-    return SGEMM_ERR_ALIAS;
-  if (!grid_holds(quantize_wgs(SGEMM_OP_N, M, K), MX_THREADS)) return SGEMM_ERR_UNSUPPORTED;
   st = check_device(h);
   if (st != SGEMM_OK) return st;
   MxArgs g = {M, N, K, alpha, beta, X, ldx, nullptr, 0, static_cast<const uint8_t*>(B), ldb,

@@ -1,0 +1,368 @@
+// Tiled products of microscaled 8-bit rows with microscaled 8- or 4-bit rows on
+// the CDNA4 matrix cores (v_mfma_scale_f32_32x32x64_f8f6f4):
+//
+//     C(m, n) = alpha * sum_k A(m, k) * B(n, k) + beta * C(m, n)
+//
+// The schedule is that of the 4-bit operands (mx_gemm.hpp): block tile in LDS,
+// direct global-to-LDS loads S-1 K steps ahead, fragments half a step ahead, one
+// barrier a step, every MFMA with its share of reads and loads.  What differs:
+//
+// * A K step is 128 values, four blocks: 128 bytes of 8-bit codes a row (units
+//   as there, c ^ ((row / 2) & 7)) or 64 of 4-bit ones (four units, at c ^ ((row /
+//   2) & 3): eight rows at one unit fill all banks).  A step has two groups of
+//   MFMAs over 64 k.
+// * Lane half h of an MFMA takes (measured on the device) k = 16 h .. 16 h + 15 and
+//   32 + 16 h .. of the group's 64 from an 8-bit row, the units h and 2 + h, and k =
+//   32 h .. 32 h + 31 from a 4-bit one, unit h; and the scale byte of block h from
+//   either.  A row's four scale bytes of a step are one dword, shifted by 8 h as it
+//   is read; the instruction's byte select then picks byte 2 q for group q.
+// * Scale bytes come by direct loads, a dword a lane and row, 64 rows a wave
+//   instruction.
+// * A step in which K ends, and K of less than a step, as there.  A's units past
+//   the end are zeroed as they come out of LDS; B's repeat the row's last unit (a
+//   NaN among its codes is in the row's result anyway).
+#pragma once
+
+#include "mx8_small.hpp"
+#include "mx_gemm.hpp"
+
+namespace sgemm {
+
+template <int BM_, int BN_, int WM_, int WN_, int OCC_, int S_, int WB_>
+struct Mx8Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, OCC = OCC_, S = S_, WB = WB_;
+  static constexpr int KG = 1;
+  static constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN;
+  static constexpr int WAVES_MN = WAVES_M * WAVES_N, WAVES = WAVES_MN;
+  static constexpr int THREADS = 64 * WAVES;
+  static constexpr int FM = WM / 32, FN = WN / 32;
+  static constexpr int B_ROW = 16 * WB, B_UNITS = WB, B_FU = WB / 4;  // bytes, units, units a lane
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * B_ROW, SC_BYTES = (BM + BN) * 4;
+  static constexpr int STAGE = A_BYTES + B_BYTES + SC_BYTES;
+  static constexpr int A_VEC = BM * 8 / THREADS, B_VEC = BN * B_UNITS / THREADS;
+  // scale loads a wave and step, 64 rows each (some waves' may be idle)
+  static constexpr int S_VEC = ((BM + BN) / 64 + WAVES - 1) / WAVES;
+  static constexpr int LDS_BYTES = S * STAGE;
+  static constexpr int LDS = LDS_BYTES + 1024;  // and where look-ahead loads past the end land
+  static_assert(WB == 8 || WB == 4, "bits of B");
+  static_assert(A_VEC * THREADS == BM * 8 && B_VEC * THREADS == BN * B_UNITS, "code loads");
+  static_assert(BM % 64 == 0 && BN % 64 == 0 && WAVES == 4, "scale loads; a lane's unit");
+  static_assert(LDS <= 160 * 1024 && S % 2 == 0, "gfx950 LDS; scale sets alternate by stage");
+  static_assert((S - 1) * (A_VEC + B_VEC + S_VEC) <= 63, "vmcnt range");
+};
+
+template <class T>
+__device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, int m0, int n0,
+                                                    f32x16 (&acc)[T::FM][T::FN]) {
+  constexpr int QG = 2, H = 1, S = T::S, BF = T::B_FU;
+  constexpr int B_FMT = T::WB == 8 ? 0 : 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wave_u = __builtin_amdgcn_readfirstlane(wave);
+  const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+  const int li = lane & 31, lh = lane >> 5;
+  const int nb = g.K / MX_BLOCK, kd = nb / 4;  // blocks, whole steps
+  const uint8_t* A = static_cast<const uint8_t*>(g.A) + (size_t)m0 * g.lda;
+  const uint8_t* B = g.B + (size_t)n0 * g.ldb;
+  const uint8_t* SA = g.SA + (size_t)m0 * g.ldsa;
+  const uint8_t* SB = g.SB + (size_t)n0 * g.ldsb;
+  const int a_last = g.M - 1 - m0, b_last = g.N - 1 - n0;  // the tile's last valid rows
+
+  auto a_at = [&](int st) { return st * T::STAGE; };
+  auto b_at = [&](int st) { return st * T::STAGE + T::A_BYTES; };
+  auto s_at = [&](int st) { return st * T::STAGE + T::A_BYTES + T::B_BYTES; };
+  auto b_off = [](int r, int c) {
+    return T::WB == 8 ? lp_unit_off(r, c) : r * 64 + 16 * (c ^ ((r >> 1) & 3));
+  };
+
+  // Slot u of a code tile holds row u / units, unit (u % units) ^ the row's swizzle.
+  unsigned a_voff[T::A_VEC], b_voff[T::B_VEC], s_voff[T::S_VEC];
+  const uint8_t* s_base[T::S_VEC];
+#pragma unroll
+  for (int v = 0; v < T::A_VEC; ++v) {
+    const int u = (v * T::WAVES + wave) * 64 + lane, r = u >> 3;
+    a_voff[v] = (unsigned)min(r, a_last) * (unsigned)g.lda + 16u * ((u & 7) ^ ((r >> 1) & 7));
+  }
+#pragma unroll
+  for (int v = 0; v < T::B_VEC; ++v) {
+    constexpr int UN = T::B_UNITS;
+    const int u = (v * T::WAVES + wave) * 64 + lane, r = u / UN;
+    b_voff[v] = (unsigned)min(r, b_last) * (unsigned)g.ldb +
+                16u * ((u & (UN - 1)) ^ ((r >> 1) & (UN - 1)));
+  }
+  // Scale dwords: A's rows and then B's, one a row.
+  bool s_live[T::S_VEC];
+#pragma unroll
+  for (int v = 0; v < T::S_VEC; ++v) {
+    const int first = 64 * (v * T::WAVES + wave_u);  // wave-uniform
+    const bool of_a = first < T::BM;
+    s_live[v] = first < T::BM + T::BN;
+    const int r = s_live[v] ? (of_a ? first : first - T::BM) + lane : 0;
+    s_base[v] = of_a ? SA : SB;
+    s_voff[v] = (unsigned)min(r, of_a ? a_last : b_last) * (unsigned)(of_a ? g.ldsa : g.ldsb);
+  }
+
+  // With no whole step the loop still runs once, on stages of zeros (see the 4-bit
+  // operands' kernel): its loads all read the same bytes of A, which nothing uses.
+  if (kd == 0) {
+#pragma unroll
+    for (int v = 0; v < T::A_VEC; ++v) a_voff[v] = 0u;
+#pragma unroll
+    for (int v = 0; v < T::B_VEC; ++v) b_voff[v] = 0u;
+#pragma unroll
+    for (int v = 0; v < T::S_VEC; ++v) s_voff[v] = 0u, s_base[v] = A;
+  }
+  const uint8_t* B_loads = kd == 0 ? A : B;
+  const int steps = max(kd, 1);
+  // The partial step, loaded as step `steps` when there is one: its blocks, and
+  // how far a lane's unit lies past the row's last one (the same in all the
+  // lane's loads of an operand).
+  const int rest = kd > 0 ? nb - 4 * kd : 0;
+  const int loads = rest > 0 ? steps + 1 : steps;
+  auto past = [&](int units, int have) {
+    const int c = (lane & (units - 1)) ^ ((((wave * 64 + lane) / units) >> 1) & (units - 1));
+    return rest > 0 ? 16u * (unsigned)max(c - (have - 1), 0) : 0u;
+  };
+  const unsigned a_back = past(8, 2 * rest);
+  const unsigned b_back = past(T::B_UNITS, T::B_FU * rest);
+
+  constexpr int ND = T::A_VEC + T::B_VEC + T::S_VEC;
+  const unsigned lds_u = (unsigned)(uintptr_t)(lds_void_t*)lds;
+  const unsigned dummy = lds_u + (unsigned)T::LDS_BYTES;
+  auto load_one = [&](int kt, int st, int d, bool live) {
+    const bool part = kt == steps;
+    if (d < T::S_VEC) {
+      dma4(s_base[d] + (part ? (size_t)(nb - 4) : (size_t)kt * 4), s_voff[d],
+           live && s_live[d] ? lds_u + (unsigned)s_at(st) + 256u * (unsigned)(d * T::WAVES + wave_u)
+                             : dummy);
+    } else if (d < T::S_VEC + T::A_VEC) {
+      const int v = d - T::S_VEC;
+      dma16(reinterpret_cast<const float*>(A + (size_t)kt * 128), a_voff[v] - (part ? a_back : 0u),
+            live ? lds_u + (unsigned)a_at(st) + 1024u * (unsigned)(v * T::WAVES + wave_u) : dummy);
+    } else {
+      const int v = d - T::S_VEC - T::A_VEC;
+      dma16(reinterpret_cast<const float*>(B_loads + (size_t)kt * T::B_ROW),
+            b_voff[v] - (part ? b_back : 0u),
+            live ? lds_u + (unsigned)b_at(st) + 1024u * (unsigned)(v * T::WAVES + wave_u) : dummy);
+    }
+  };
+
+  struct Frag {
+    u32x4 a[T::FM][2], b[T::FN][BF];
+  };
+  struct Scales {
+    unsigned a[T::FM], b[T::FN];
+  };
+  constexpr int NF = T::FM + T::FN, SL = T::FM * T::FN;
+  // Read r of a group, in the order the MFMAs (i-major) need them.
+  auto read_one = [&](int st, int q, int r, Frag& f) {
+    if (r >= 1 && r <= T::FN) {
+      const int row = wn * T::WN + 32 * (r - 1) + li;
+#pragma unroll
+      for (int u = 0; u < BF; ++u)
+        f.b[r - 1][u] = *reinterpret_cast<const u32x4*>(lds + b_at(st) +
+                                                        b_off(row, 2 * BF * q + 2 * u + lh));
+    } else {
+      const int i = r == 0 ? 0 : r - T::FN;
+      const int row = wm * T::WM + 32 * i + li;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        f.a[i][u] = *reinterpret_cast<const u32x4*>(lds + a_at(st) +
+                                                    lp_unit_off(row, 4 * q + 2 * u + lh));
+    }
+  };
+  auto read_scale = [&](int st, int r, Scales& s) {
+    const char* tile = lds + s_at(st);
+    const int row = r < T::FM ? wm * T::WM + 32 * r + li : T::BM + wn * T::WN + 32 * (r - T::FM) + li;
+    const unsigned v = *reinterpret_cast<const unsigned*>(tile + 4 * row) >> (8 * lh);
+    if (r < T::FM)
+      s.a[r] = v;
+    else
+      s.b[r - T::FM] = v;
+  };
+  auto mma = [&](auto q_c, const Frag& f, const Scales& s, int m) {
+    constexpr int q = decltype(q_c)::value;
+    const int i = m / T::FN, j = m % T::FN;
+    i32x8 x;
+    if constexpr (T::WB == 8)
+      x = mx8_operand(f.b[j]);
+    else
+      x = mx4_operand(f.b[j][0]);
+    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+        x, mx8_operand(f.a[i]), acc[i][j], B_FMT, 0, 2 * q, (int)s.b[j], 2 * q, (int)s.a[i]);
+  };
+
+  Frag fr[QG];
+  Scales sc[2];
+  // Group q of step kt (stage st): its MFMAs with the reads of the next group, the
+  // next step's scales and, in the second half, step kt+S's loads.
+  auto group = [&](int kl, bool live, auto st_c, auto q_c) {
+    constexpr int st = decltype(st_c)::value, q = decltype(q_c)::value;
+    constexpr int st1 = st + 1 == S ? 0 : st + 1;
+    constexpr int rq = (q + H) % QG, rst = q + H < QG ? st : st1;
+#pragma unroll
+    for (int m = 0; m < SL; ++m) {
+      mma(q_c, fr[q], sc[st & 1], m);
+#pragma unroll
+      for (int r = 0; r < NF; ++r)
+        if (r * SL / NF == m) {
+          read_one(rst, rq, r, fr[rq]);
+          if (q == H) read_scale(st1, r, sc[st1 & 1]);
+        }
+      if (q >= H) {
+        constexpr int SLOTS = (QG - H) * SL;
+#pragma unroll
+        for (int o = 0; o < ND; ++o)
+          if (o * SLOTS / ND == (q - H) * SL + m) load_one(kl, st, o, live);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto wait_lds = [] { __builtin_amdgcn_s_waitcnt(0xC07F); };  // lgkmcnt(0)
+  constexpr int AHEAD = (S - 2) * ND;
+  constexpr int WAIT_AHEAD = 0x0F70 | (AHEAD & 15) | ((AHEAD >> 4) << 14);
+  auto step = [&](int kt, auto st_c) {
+    const bool live = kt + S < loads;
+    const int kl = live ? kt + S : loads - 1;
+    lp_static_for<H>([&](auto q_c) { group(kl, live, st_c, q_c); });
+    wait_lds();
+    __builtin_amdgcn_s_waitcnt(WAIT_AHEAD);
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+    lp_static_for<QG - H>([&](auto i) {
+      group(kl, live, st_c, std::integral_constant<int, H + decltype(i)::value>{});
+    });
+  };
+  // (no scalar load may be in flight in the K loop; see lp_tile_accumulate)
+  asm volatile("" ::"s"(g.C), "s"(g.ldc), "s"(g.alpha), "s"(g.beta), "s"(g.M), "s"(g.N));
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  lp_static_for<S>([&](auto i) {
+    constexpr int st = decltype(i)::value;
+#pragma unroll
+    for (int o = 0; o < ND; ++o)
+      load_one(st < loads ? st : loads - 1, st, o, kd > 0 && st < loads);
+  });
+  if (kd == 0) {
+#pragma unroll 1
+    for (int i = tid; i < T::STAGE / 16; i += T::THREADS)
+      *reinterpret_cast<u32x4*>(lds + 16 * i) = u32x4{0u, 0u, 0u, 0u};
+  }
+  constexpr int FIRST = (S - 1) * ND;
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (FIRST & 15) | ((FIRST >> 4) << 14));
+  wait_lds();
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < NF; ++r) read_scale(0, r, sc[0]);
+  lp_static_for<H>([&](auto q_c) {
+#pragma unroll
+    for (int r = 0; r < NF; ++r)
+      read_one(0, decltype(q_c)::value, r, fr[decltype(q_c)::value]);
+  });
+  int kt = 0;
+  for (; kt + S <= steps; kt += S)
+    lp_static_for<S>([&](auto i) { step(kt + decltype(i)::value, i); });
+  lp_static_for<S - 1>([&](auto i) {
+    if (kt + decltype(i)::value < steps) step(kt + decltype(i)::value, i);
+  });
+  if (rest > 0) {
+    // the partial step's loads have had whole steps to land
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    wait_lds();
+    __syncthreads();
+    const int st = steps % S;
+    // (the dword holds the row's last four blocks)
+    const int shift = 8 * (4 - rest + lh);
+    auto scale = [&](int row) {
+      const unsigned long long d = *reinterpret_cast<const unsigned*>(lds + s_at(st) + 4 * row);
+      return (unsigned)(d >> shift);
+    };
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) sc[0].a[i] = scale(wm * T::WM + 32 * i + li);
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) sc[0].b[j] = scale(T::BM + wn * T::WN + 32 * j + li);
+    lp_static_for<QG>([&](auto q_c) {
+      constexpr int q = decltype(q_c)::value;
+#pragma unroll
+      for (int r = 0; r < NF; ++r) read_one(st, q, r, fr[0]);
+#pragma unroll
+      for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (4 * q + 2 * u + lh >= 2 * rest) fr[0].a[i][u] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int m = 0; m < SL; ++m) mma(q_c, fr[0], sc[0], m);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
+  if (kd == 0) {
+    // K of less than a step, into stage 0 once every wave is done with it and
+    // the loop's loads have landed.  (The lane's index is hidden from the
+    // compiler, which would otherwise keep this part's addresses in registers
+    // through the loop.)
+    int t = tid;
+    asm volatile("" : "+v"(t));
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    wait_lds();
+    __syncthreads();
+    auto fill = [&](const uint8_t* rows, int ld, int last, int count, int units, int have, int at,
+                    auto off) {
+#pragma unroll 1
+      for (int u = t; u < count * units; u += T::THREADS) {
+        const int r = u / units, c = u % units;
+        u32x4 x = {0u, 0u, 0u, 0u};
+        if (c < have) {
+          const v4u w = *reinterpret_cast<const v4u_any*>(rows + (size_t)min(r, last) * ld + 16 * c);
+          x = u32x4{w[0], w[1], w[2], w[3]};
+        }
+        *reinterpret_cast<u32x4*>(lds + at + off(r, c)) = x;
+      }
+    };
+    fill(A, g.lda, a_last, T::BM, 8, 2 * nb, a_at(0), [](int r, int c) { return lp_unit_off(r, c); });
+    fill(B, g.ldb, b_last, T::BN, T::B_UNITS, T::B_FU * nb, b_at(0), b_off);
+#pragma unroll 1
+    for (int i = t; i < (T::BM + T::BN) * 4; i += T::THREADS) {
+      const int c = i & 3, r = i >> 2;
+      uint8_t b = 0;
+      if (c < nb)
+        b = r < T::BM ? SA[(size_t)min(r, a_last) * g.ldsa + c]
+                      : SB[(size_t)min(r - T::BM, b_last) * g.ldsb + c];
+      lds[s_at(0) + i] = (char)b;
+    }
+    wait_lds();
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < NF; ++r) read_scale(0, r, sc[0]);
+    lp_static_for<QG>([&](auto q_c) {
+      constexpr int q = decltype(q_c)::value;
+#pragma unroll
+      for (int r = 0; r < NF; ++r) read_one(0, q, r, fr[0]);
+#pragma unroll
+      for (int m = 0; m < SL; ++m) mma(q_c, fr[0], sc[0], m);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
+}
+
+template <class T, int CDT>
+__global__ void __launch_bounds__(T::THREADS, T::OCC)
+    mx8_gemm_kernel(MxArgs g, int tiles_m, int tiles_n, int band) {
+  __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
+  int tm, tn;
+  tile_coords(blockIdx.x, gridDim.x, tiles_m, tiles_n, band, tm, tn);
+  f32x16 acc[T::FM][T::FN];
+  zero_acc<T>(acc);
+  const int m0 = tm * T::BM, n0 = tn * T::BN;
+  mx8_tile_accumulate<T>(g, lds, m0, n0, acc);
+  mx_store_tile<T, CDT>(g, m0, n0, acc, lds);
+  // look-ahead loads into LDS that nothing waits for must land before the
+  // workgroup's LDS is released
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+}
+
+template <int WB>
+using Y256x256 = Mx8Tile<256, 256, 128, 128, 1, 2, WB>;
+template <int WB>
+using Y128x128 = Mx8Tile<128, 128, 64, 64, 1, 4, WB>;
+template <int WB>
+using Y64x64 = Mx8Tile<64, 64, 32, 32, 2, 4, WB>;
+
+}  // namespace sgemm

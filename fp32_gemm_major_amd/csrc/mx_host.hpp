@@ -6,6 +6,7 @@
 
 #include "handle.hpp"
 #include "mx_quant.hpp"
+#include "mx_small.hpp"
 #include "sgemm.h"
 
 namespace sgemm {
@@ -112,6 +113,110 @@ int dequantize_entry(sgemm_handle_t h, int dtype, int R, int K, const void* code
                            static_cast<const uint8_t*>(scales), lds, Y, ldy};
   hipLaunchKernelGGL(kDequant[dtype], dim3((unsigned)dequantize_wgs(R, K)), dim3(MX_THREADS), 0,
                      stream, g);
+  return launched();
+}
+
+// Checks of a product but for A's own, B of format F.
+template <class F>
+int validate_product(int M, int N, int K, const void* A, const void* B, int ldb, const void* SB,
+                     int ldsb, int dtype, const void* C, int ldc) {
+  const unsigned esz = tensor_elem_bytes(dtype);
+  if (esz == 0) return SGEMM_ERR_VALUE;
+  if (!mx_sizes_ok(M, K) || !mx_sizes_ok(N, K)) return SGEMM_ERR_SIZE;
+  if (!mx_strides_ok<F>(K, ldb, ldsb) || ldc < at_least_one(N)) return SGEMM_ERR_LD;
+  if (M == 0 || N == 0) return SGEMM_OK;
+  if (C == nullptr || (K > 0 && (A == nullptr || B == nullptr || SB == nullptr)))
+    return SGEMM_ERR_NULL;
+  if (!elem_aligned(C, esz)) return SGEMM_ERR_VALUE;
+  const ByteRange c = byte_range(C, M, N, ldc, esz);
+  if (K > 0 &&
+      (ranges_meet(c, code_range<F>(B, N, K, ldb)) || ranges_meet(c, scale_range(SB, N, K, ldsb))))
+    return SGEMM_ERR_ALIAS;
+  return SGEMM_OK;
+}
+
+// A in codes of format FA.
+template <class FA, class FB>
+int validate_codes(int M, int N, int K, const void* A, int lda, const void* SA, int ldsa,
+                   const void* B, int ldb, const void* SB, int ldsb, int dtype, const void* C,
+                   int ldc) {
+  const int st = validate_product<FB>(M, N, K, A, B, ldb, SB, ldsb, dtype, C, ldc);
+  if (st != SGEMM_OK) return st;
+  if (K % MX_BLOCK != 0) return SGEMM_ERR_SIZE;
+  if (!mx_strides_ok<FA>(K, lda, ldsa)) return SGEMM_ERR_LD;
+  if (M == 0 || N == 0 || K == 0) return SGEMM_OK;
+  if (SA == nullptr) return SGEMM_ERR_NULL;
+  const ByteRange c = byte_range(C, M, N, ldc, tensor_elem_bytes(dtype));
+  if (ranges_meet(c, code_range<FA>(A, M, K, lda)) || ranges_meet(c, scale_range(SA, M, K, ldsa)))
+    return SGEMM_ERR_ALIAS;
+  return SGEMM_OK;
+}
+
+// A a tensor X that the call quantises.
+template <class FB>
+int validate_activations(int xtype, int M, int N, int K, const void* X, int ldx, const void* B,
+                         int ldb, const void* SB, int ldsb, int dtype, const void* C, int ldc) {
+  const unsigned xsz = tensor_elem_bytes(xtype);
+  if (xsz == 0) return SGEMM_ERR_VALUE;
+  const int st = validate_product<FB>(M, N, K, X, B, ldb, SB, ldsb, dtype, C, ldc);
+  if (st != SGEMM_OK) return st;
+  if (ldx < at_least_one(K)) return SGEMM_ERR_LD;
+  if (M == 0 || N == 0) return SGEMM_OK;
+  if (K > 0 && !elem_aligned(X, xsz)) return SGEMM_ERR_VALUE;
+  if (ranges_meet(byte_range(C, M, N, ldc, tensor_elem_bytes(dtype)), byte_range(X, M, K, ldx, xsz)))
+    return SGEMM_ERR_ALIAS;
+  return grid_holds(quantize_wgs(SGEMM_OP_N, M, K), MX_THREADS) ? SGEMM_OK : SGEMM_ERR_UNSUPPORTED;
+}
+
+// A kernel for few rows, `tiles` tiles of 16 columns a workgroup, over a grid that
+// holds its launches.
+inline int launch_small_grid(void (*kernel)(MxArgs), int tiles, const MxArgs& g,
+                             hipStream_t stream) {
+  constexpr int kRows = 65535 * MXS_TILE;  // a grid's second extent
+  // (the first one's threads are counted in 32 bits: 2^23 workgroups less one)
+  constexpr int kCols = (int)(0xffffffffu / MXS_THREADS) * MXS_TILE;
+  for (long long m0 = 0; m0 < g.M; m0 += kRows)
+    for (long long n0 = 0; n0 < g.N; n0 += kCols) {
+      MxArgs p = g;
+      p.M = (int)(g.M - m0 < kRows ? g.M - m0 : kRows);
+      p.N = (int)(g.N - n0 < kCols ? g.N - n0 : kCols);
+      if (g.K > 0 && m0 > 0) {  // (activations come with 16 rows at most)
+        p.A = static_cast<const uint8_t*>(g.A) + (size_t)m0 * g.lda;
+        p.SA = g.SA + (size_t)m0 * g.ldsa;
+      }
+      if (g.K > 0 && n0 > 0) {
+        p.B = g.B + (size_t)n0 * g.ldb;
+        p.SB = g.SB + (size_t)n0 * g.ldsb;
+      }
+      p.C = static_cast<char*>(g.C) + ((size_t)m0 * g.ldc + (size_t)n0) * tensor_elem_bytes(g.cdt);
+      hipLaunchKernelGGL(kernel,
+                         dim3((unsigned)up_div(p.N, MXS_TILE * tiles), (unsigned)up_div(p.M, MXS_TILE)),
+                         dim3(MXS_THREADS), 0, stream, p);
+      const int st = launched();
+      if (st != SGEMM_OK) return st;
+    }
+  return SGEMM_OK;
+}
+
+// A tile kernel, by type of C.
+typedef void (*tile_fn)(MxArgs, int, int, int);
+struct MxTileDesc {
+  int b;  // rows and columns of the tile
+  int threads;
+  tile_fn kernel[3];
+};
+
+// The tile kernels' direct loads address a tile's rows by 32-bit offsets.
+inline bool tile_fits(const MxTileDesc& t, const MxArgs& g) {
+  const long long far = 1LL << 32, r = t.b - 1;
+  return r * g.lda + 128 < far && r * g.ldb + 128 < far && r * g.ldsa + 8 < far &&
+         r * g.ldsb + 8 < far && grid_holds(up_div(g.M, t.b) * up_div(g.N, t.b), t.threads);
+}
+
+inline int launch_tile(const MxTileDesc& t, const MxArgs& g, hipStream_t stream) {
+  const int tm = (int)up_div(g.M, t.b), tn = (int)up_div(g.N, t.b);
+  hipLaunchKernelGGL(t.kernel[g.cdt], dim3((unsigned)(tm * tn)), dim3(t.threads), 0, stream, g, tm,
+                     tn, band_rows(tm, tm * tn));
   return launched();
 }
 

@@ -157,6 +157,37 @@ __device__ __forceinline__ void mx_quant_few(const typename TensorElem<XDT>::typ
   }
 }
 
+// The waves' partial results of the workgroup's NT tiles from column n0 on,
+// added through LDS in wave order, to C.
+template <int NT>
+__device__ __forceinline__ void mx_small_finish(const MxArgs& g, f32x4* red,
+                                                const f32x4 (&acc)[NT], int n0) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int q = lane >> 4, m = blockIdx.y * MXS_TILE + (lane & 15);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) red[(wave * NT + t) * 64 + lane] = acc[t];
+  __syncthreads();
+  if (wave >= NT) return;
+  // wave t finishes tile t
+  f32x4 s = red[wave * 64 + lane];
+#pragma unroll
+  for (int w = 1; w < MXS_WAVES; ++w) {
+    const f32x4 v = red[(w * NT + wave) * 64 + lane];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[r] += v[r];
+  }
+  if (m >= g.M) return;
+  const int col = n0 + MXS_TILE * wave + 4 * q;
+  const size_t at = (size_t)m * g.ldc + col;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (col + r < g.N) {
+      float o = g.alpha * s[r];
+      if (g.beta != 0.0f) o = fmaf(g.beta, mx_load_c(g, at + r), o);
+      mx_store_c(g, at + r, o);
+    }
+}
+
 // XDT < 0: A in codes.  FEW: activations of at most MXS_FEW rows.  NT: the
 // workgroup's tiles of 16 columns.
 template <int XDT, bool FEW, int NT>
@@ -209,28 +240,7 @@ __global__ void __launch_bounds__(MXS_THREADS) mx_small_kernel(MxArgs g) {
       }
   }
   if constexpr (FEW) __syncthreads();  // (red held the waves' blocks)
-#pragma unroll
-  for (int t = 0; t < NT; ++t) red[(wave * NT + t) * 64 + lane] = acc[t];
-  __syncthreads();
-  if (wave >= NT) return;
-  // wave t finishes tile t
-  f32x4 s = red[wave * 64 + lane];
-#pragma unroll
-  for (int w = 1; w < MXS_WAVES; ++w) {
-    const f32x4 v = red[(w * NT + wave) * 64 + lane];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) s[r] += v[r];
-  }
-  if (!a_in) return;
-  const int col = n0 + MXS_TILE * wave + 4 * q;
-  const size_t at = (size_t)m * g.ldc + col;
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-    if (col + r < g.N) {
-      float o = g.alpha * s[r];
-      if (g.beta != 0.0f) o = fmaf(g.beta, mx_load_c(g, at + r), o);
-      mx_store_c(g, at + r, o);
-    }
+  mx_small_finish<NT>(g, red, acc, n0);
 }
 
 }  // namespace sgemm

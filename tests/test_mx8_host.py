@@ -197,3 +197,64 @@ def test_binding_checks():
         sg._gain(torch.ones(41), x)
     with pytest.raises(ValueError):
         sg._gain(torch.ones(80)[::2], x)
+
+
+A8, SA, W, SW, C = 0x1000000, 0x2000000, 0x3000000, 0x4000000, 0x8000000  # never touched
+
+
+def product(**kw):
+    a = dict(bits=8, M=4, N=5, K=64, A=A8, lda=64, SA=SA, ldsa=2, B=W, ldb=64, SB=SW, ldsb=2, dtype=BF16,
+             C=C, ldc=5)
+    a.update(kw)
+    return sg.sgemm_validate_mx_byte(*a.values())
+
+
+def test_validate_product():
+    assert product() == sg.SGEMM_OK and product(bits=4, ldb=32) == sg.SGEMM_OK
+    assert product(dtype=F32) == sg.SGEMM_OK and product(dtype=F16) == sg.SGEMM_OK
+    for bits in (0, 6, 16, -8):
+        assert product(bits=bits) == sg.SGEMM_ERR_VALUE
+    for bad in (-1, 3, 4, 5):
+        assert product(dtype=bad) == sg.SGEMM_ERR_VALUE
+    for name in ("M", "N", "K"):
+        assert product(**{name: -32}) == sg.SGEMM_ERR_SIZE
+    assert product(K=63) == sg.SGEMM_ERR_SIZE
+    for name in ("M", "N"):
+        assert product(**{name: sg.SGEMM_MX_MAX_ROWS + 1}, ldc=2 ** 31 - 1) == sg.SGEMM_ERR_SIZE
+    for name, short in (("lda", 63), ("ldsa", 1), ("ldb", 63), ("ldsb", 1), ("ldc", 4)):
+        assert product(**{name: short}) == sg.SGEMM_ERR_LD, name
+    assert product(bits=4, ldb=31) == sg.SGEMM_ERR_LD
+    for name in ("A", "SA", "B", "SB", "C"):
+        assert product(**{name: None}) == sg.SGEMM_ERR_NULL, name
+    assert product(A=None, SA=None, B=None, SB=None, K=0) == sg.SGEMM_OK
+    assert product(M=0, A=None, C=None) == sg.SGEMM_OK
+    assert product(C=C + 1) == sg.SGEMM_ERR_VALUE
+    assert product(A=A8 + 1, SA=SA + 1, B=W + 3, SB=SW + 1) == sg.SGEMM_OK  # any byte address
+    assert product(C=A8 + 64 * 3 + 62) == sg.SGEMM_ERR_ALIAS
+    assert product(C=W + 64 * 4 + 62) == sg.SGEMM_ERR_ALIAS
+    assert product(bits=4, ldb=32, C=W + 32 * 4 + 32) == sg.SGEMM_OK
+    assert product(C=SA + 6) == sg.SGEMM_ERR_ALIAS and product(C=SW + 8) == sg.SGEMM_ERR_ALIAS
+
+
+def test_product_entries_without_a_device():
+    lib = sg.library()
+    assert lib.sgemm_run_mx_byte(None, 8, 1, 1, 32, 1.0, A8, 32, SA, 1, W, 32, SW, 1, 0.0, BF16, C, 1,
+                                 None) == sg.SGEMM_ERR_HANDLE
+    assert lib.sgemm_run_mx_byte_quant(None, BF16, 8, 1, 1, 32, 1.0, A8, 32, W, 32, SW, 1, 0.0, BF16, C,
+                                       1, None) == sg.SGEMM_ERR_HANDLE
+    h = HostHandle()
+    at = ctypes.addressof(h)
+
+    def quant(xtype=BF16, bits=8, M=3, K=40, x=A8, ldx=40, ldb=64, c=C):
+        return lib.sgemm_run_mx_byte_quant(at, xtype, bits, M, 5, K, 1.0, x, ldx, W, ldb, SW, 2, 0.0, BF16,
+                                           c, 5, None)
+
+    assert quant() == sg.SGEMM_ERR_DEVICE and quant(bits=4, ldb=32) == sg.SGEMM_ERR_DEVICE
+    assert quant(bits=5) == sg.SGEMM_ERR_VALUE and quant(xtype=3) == sg.SGEMM_ERR_VALUE
+    assert quant(ldx=39) == sg.SGEMM_ERR_LD and quant(ldb=63) == sg.SGEMM_ERR_LD
+    assert quant(x=A8 + 1) == sg.SGEMM_ERR_VALUE and quant(x=None) == sg.SGEMM_ERR_NULL
+    assert quant(c=A8 + 8) == sg.SGEMM_ERR_ALIAS and quant(M=0, x=None) == sg.SGEMM_OK
+    K = 1 << 20
+    fits = ((1 << 24) - 1) * 512 * 8 // K
+    assert lib.sgemm_run_mx_byte_quant(at, BF16, 8, fits + 1, 1, K, 1.0, 1 << 60, K, 1 << 50, K, 1 << 52,
+                                       K // 32, 0.0, BF16, 1 << 48, 1, None) == sg.SGEMM_ERR_UNSUPPORTED

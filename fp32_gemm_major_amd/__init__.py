@@ -73,7 +73,8 @@ EXPORTED = [
     "sgemm_mx_quantize", "sgemm_mx_dequantize", "sgemm_run_mx", "sgemm_validate_mx",
     "sgemm_run_mx_quant",
     "sgemm_mx_byte_quantize", "sgemm_mx_byte_dequantize", "sgemm_run_mx_byte",
-    "sgemm_validate_mx_byte", "sgemm_run_mx_byte_quant",
+    "sgemm_validate_mx_byte", "sgemm_run_mx_byte_quant", "sgemm_mx_byte_weight_grad",
+    "sgemm_mx_byte_weight_grad_workspace_size", "sgemm_validate_mx_byte_weight_grad",
     "sgemm_rmsnorm", "sgemm_validate_rmsnorm", "sgemm_rmsnorm_backward",
     "sgemm_validate_rmsnorm_backward", "sgemm_rmsnorm_workspace_size",
     "sgemm_ce_workspace_size", "sgemm_ce_forward", "sgemm_ce_backward", "sgemm_validate_ce",
@@ -142,6 +143,9 @@ def _bind(lib):
     lib.sgemm_run_mx_byte.argtypes = [p, i, i, i, i, f, p, i, p, i, p, i, p, i, f, i, p, i, p]
     lib.sgemm_validate_mx_byte.argtypes = [i, i, i, i, p, i, p, i, p, i, p, i, i, p, i]
     lib.sgemm_run_mx_byte_quant.argtypes = [p, i, i, i, i, i, f, p, i, p, i, p, i, f, i, p, i, p]
+    lib.sgemm_mx_byte_weight_grad.argtypes = [p, i, i, i, i, f, p, i, p, i, p, i, f, i, p, i, p]
+    lib.sgemm_validate_mx_byte_weight_grad.argtypes = [i, i, i, i, p, i, p, i, p, i, i, p, i]
+    lib.sgemm_mx_byte_weight_grad_workspace_size.argtypes = [p, i, i, i, sp]
     lib.sgemm_rmsnorm.argtypes = [p, i, i, i, i, p, i, p, i, p, f, p, i, p, i, p, i, p, p]
     lib.sgemm_validate_rmsnorm.argtypes = [i, i, i, i, p, i, p, i, p, p, i, p, i, p, i, p]
     lib.sgemm_rmsnorm_backward.argtypes = [p, i, i, i, i, p, i, p, i, p, p, p, i, p, i, p, p]
@@ -156,7 +160,9 @@ def _bind(lib):
                  "sgemm_validate_ce", "sgemm_validate_ce_backward", "sgemm_mx_quantize", "sgemm_mx_dequantize", "sgemm_run_mx",
                  "sgemm_validate_mx", "sgemm_run_mx_quant", "sgemm_mx_byte_quantize",
                  "sgemm_mx_byte_dequantize", "sgemm_run_mx_byte", "sgemm_validate_mx_byte",
-                 "sgemm_run_mx_byte_quant", "sgemm_rmsnorm", "sgemm_validate_rmsnorm",
+                 "sgemm_run_mx_byte_quant", "sgemm_mx_byte_weight_grad",
+                 "sgemm_mx_byte_weight_grad_workspace_size", "sgemm_validate_mx_byte_weight_grad",
+                 "sgemm_rmsnorm", "sgemm_validate_rmsnorm",
                  "sgemm_rmsnorm_backward", "sgemm_validate_rmsnorm_backward",
                  "sgemm_rmsnorm_workspace_size"):
         getattr(lib, name).restype = i
@@ -353,6 +359,28 @@ def sgemm_run_mx_byte_quant(h, xtype, bits, M, N, K, alpha, X, ldx, B, ldb, SB, 
     return _check(library().sgemm_run_mx_byte_quant(h, xtype, bits, M, N, K, alpha, X, ldx, B, ldb,
                                                     SB, ldsb, beta, dtype, C, ldc, stream),
                   "sgemm_run_mx_byte_quant")
+
+
+def sgemm_mx_byte_weight_grad(h, dtype, T, N, D, alpha, dY, lddy, X, ldx, SX, ldsx, beta, wtype, dW,
+                              lddw, stream=0) -> int:
+    """dW = alpha * dY^T * X + beta * dW with X in microscaled 8-bit rows."""
+    return _check(library().sgemm_mx_byte_weight_grad(h, dtype, T, N, D, alpha, dY, lddy, X, ldx, SX,
+                                                      ldsx, beta, wtype, dW, lddw, stream),
+                  "sgemm_mx_byte_weight_grad")
+
+
+def sgemm_validate_mx_byte_weight_grad(dtype, T, N, D, dY, lddy, X, ldx, SX, ldsx, wtype, dW,
+                                       lddw) -> int:
+    return library().sgemm_validate_mx_byte_weight_grad(dtype, T, N, D, dY, lddy, X, ldx, SX, ldsx,
+                                                        wtype, dW, lddw)
+
+
+def sgemm_mx_byte_weight_grad_workspace_size(h, T, N, D) -> int:
+    """Bytes of workspace that a weight gradient makes use of."""
+    n = ctypes.c_size_t()
+    _check(library().sgemm_mx_byte_weight_grad_workspace_size(h, T, N, D, ctypes.byref(n)),
+           "sgemm_mx_byte_weight_grad_workspace_size")
+    return n.value
 
 
 def sgemm_rmsnorm(h, dtype, gtype, T, D, X, ldx, R, ldr, G, eps, H, ldh, codes, ldc, scales,
@@ -969,6 +997,30 @@ class Handle:
             raise TypeError("B must be an Mx8 or an Mx4")
         return self._mx_product(Mx8, sgemm_run_mx_byte, sgemm_run_mx_byte_quant,
                                 (8 if isinstance(B, Mx8) else 4,), A, B, C, alpha, beta, stream)
+
+    def mx8_weight_grad_workspace_size(self, dY, X) -> int:
+        """Bytes of workspace (``set_workspace``) that ``mx8_weight_grad`` on
+        these makes use of; with less it takes longer."""
+        return sgemm_mx_byte_weight_grad_workspace_size(self.h, X.rows, dY.shape[1], X.K)
+
+    def mx8_weight_grad(self, dY, X, dW, alpha=1.0, beta=0.0, stream=None):
+        """dW = alpha * dY^T @ X + beta * dW, the gradient of a linear layer's
+        weight (N x D, float32, bfloat16 or float16) from that of its result
+        (``dY``, T x N, bfloat16 or float16) and its activations kept as an
+        ``Mx8`` of T rows (D may end inside its last block)."""
+        dtype, lddy = _matrix("dY", dY)
+        wtype, lddw = _matrix("dW", dW)
+        (T, N), (rows, D) = dY.shape, dW.shape
+        if not isinstance(X, Mx8):
+            raise TypeError("X must be an Mx8")
+        if dtype == SGEMM_DTYPE_F32:
+            raise TypeError("dY must be bfloat16 or float16")
+        if X.rows != T or rows != N or SGEMM_MX_BLOCK * -(-D // SGEMM_MX_BLOCK) != X.K:
+            raise ValueError(f"dY {T} x {N} and X {X.rows} x {X.K} do not give {rows} x {D}")
+        s = self._on(stream, dY=dY, X=X.codes, X_scales=X.scales, dW=dW)
+        return sgemm_mx_byte_weight_grad(self.h, dtype, T, N, D, alpha, dY.data_ptr(), lddy,
+                                         X.codes.data_ptr(), X._ldc, X.scales.data_ptr(), X._lds,
+                                         beta, wtype, dW.data_ptr(), lddw, s)
 
     # -- root-mean-square norm --
 

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include "mx8_gemm.hpp"
+#include "mx8_grad.hpp"
 #include "mx8_small.hpp"
 #include "mx_host.hpp"
 
@@ -63,6 +64,77 @@ int validate(int bits, int M, int N, int K, const void* A, int lda, const void* 
                                                           dtype, C, ldc)
                    : validate_codes<Mx8Format, Mx4Format>(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb,
                                                           dtype, C, ldc);
+}
+
+// ---- weight gradients ----
+
+typedef void (*grad_fn)(GradArgs, int, int, int);
+typedef void (*grad_split_fn)(GradArgs, int, int, int, int, float*);
+typedef void (*grad_sum_fn)(GradArgs, int, const float*);
+struct GradTile {
+  int b, threads;
+  grad_fn kernel[2][3];  // [type of dY: bfloat16, binary16][type of dW]
+  grad_split_fn split[2];
+};
+template <class T>
+constexpr GradTile grad_tile() {
+  return GradTile{
+      T::BM,
+      T::THREADS,
+      {{mx8_grad_kernel<T, LP_BF16, SGEMM_DTYPE_F32>, mx8_grad_kernel<T, LP_BF16, SGEMM_DTYPE_BF16>,
+        mx8_grad_kernel<T, LP_BF16, SGEMM_DTYPE_F16>},
+       {mx8_grad_kernel<T, LP_F16, SGEMM_DTYPE_F32>, mx8_grad_kernel<T, LP_F16, SGEMM_DTYPE_BF16>,
+        mx8_grad_kernel<T, LP_F16, SGEMM_DTYPE_F16>}},
+      {mx8_grad_split_kernel<T, LP_BF16>, mx8_grad_split_kernel<T, LP_F16>}};
+}
+const GradTile kGrad[2] = {grad_tile<L256x256>(), grad_tile<G128x128>()};
+const grad_sum_fn kGradSum[3] = {mx8_grad_sum_kernel<SGEMM_DTYPE_F32>,
+                                 mx8_grad_sum_kernel<SGEMM_DTYPE_BF16>,
+                                 mx8_grad_sum_kernel<SGEMM_DTYPE_F16>};
+
+size_t grad_part_bytes(int N, int D) { return 4 * (size_t)N * (size_t)((D + 3LL) / 4 * 4); }
+
+// The launch of a weight gradient: which tile, and over how many ranges of `per`
+// tokens the sum is split.
+struct GradPlan {
+  int tile, splits, per;
+};
+GradPlan grad_plan(int cus, int T, int N, int D, size_t workspace) {
+  auto tiles = [&](int b) { return up_div(N, b) * up_div(D, b); };
+  if (4 * tiles(256) >= 3LL * cus) return {0, 1, T};
+  const long long have = tiles(128);
+  // two workgroups a CU, ranges of at least four steps
+  long long splits = have >= cus ? 1 : 2LL * cus / have;
+  const long long most = T / (4 * GRAD_STEP);
+  if (splits > most) splits = most;
+  const long long room = (long long)(workspace / grad_part_bytes(N, D));
+  if (splits > room) splits = room;
+  if (splits < 2) return {1, 1, T};
+  const int per = (int)(up_div(up_div(T, splits), GRAD_STEP) * GRAD_STEP);
+  return {1, (int)up_div(T, per), per};
+}
+
+int validate_grad(int dtype, int T, int N, int D, const void* dY, int lddy, const void* X, int ldx,
+                  const void* SX, int ldsx, int wtype, const void* dW, int lddw) {
+  if (dtype != SGEMM_DTYPE_BF16 && dtype != SGEMM_DTYPE_F16) return SGEMM_ERR_VALUE;
+  const unsigned wsz = tensor_elem_bytes(wtype);
+  if (wsz == 0) return SGEMM_ERR_VALUE;
+  if (!mx_sizes_ok(T, D) || !mx_sizes_ok(N, D)) return SGEMM_ERR_SIZE;
+  if (lddy < at_least_one(N) || lddw < at_least_one(D) || !mx_strides_ok<Mx8Format>(D, ldx, ldsx))
+    return SGEMM_ERR_LD;
+  if (N == 0 || D == 0) return SGEMM_OK;
+  if (dW == nullptr || (T > 0 && (dY == nullptr || X == nullptr || SX == nullptr)))
+    return SGEMM_ERR_NULL;
+  if (!elem_aligned(dW, wsz) || (T > 0 && !elem_aligned(dY, 2))) return SGEMM_ERR_VALUE;
+  const ByteRange w = byte_range(dW, N, D, lddw, wsz);
+  if (ranges_meet(w, byte_range(dY, T, N, lddy, 2)) || ranges_meet(w, code_range<Mx8Format>(X, T, D, ldx)) ||
+      ranges_meet(w, scale_range(SX, T, D, ldsx)))
+    return SGEMM_ERR_ALIAS;
+  // a step's tokens are addressed by 32-bit offsets
+  const long long far = 1LL << 32, r = GRAD_STEP - 1;
+  if (T > 1 && (2 * r * lddy + 1024 >= far || r * ldx + 1024 >= far || r * ldsx + 1024 >= far))
+    return SGEMM_ERR_UNSUPPORTED;
+  return grid_holds(up_div(N, 128) * up_div(D, 128), 256) ? SGEMM_OK : SGEMM_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -134,6 +206,56 @@ int sgemm_run_mx_byte_quant(sgemm_handle_t h, int xtype, int bits, int M, int N,
   g.SA = scales;
   g.ldsa = q.lds;
   return launch_product(h, bits, g, stream);
+}
+
+int sgemm_validate_mx_byte_weight_grad(int dtype, int T, int N, int D, const void* dY, int lddy,
+                                       const void* X, int ldx, const void* SX, int ldsx, int wtype,
+                                       const void* dW, int lddw) {
+  return validate_grad(dtype, T, N, D, dY, lddy, X, ldx, SX, ldsx, wtype, dW, lddw);
+}
+
+int sgemm_mx_byte_weight_grad_workspace_size(sgemm_handle_t h, int T, int N, int D,
+                                             size_t* bytes) {
+  if (h == nullptr) return SGEMM_ERR_HANDLE;
+  if (bytes == nullptr) return SGEMM_ERR_NULL;
+  if (!mx_sizes_ok(T, D) || !mx_sizes_ok(N, D)) return SGEMM_ERR_SIZE;
+  *bytes = 0;
+  if (N == 0 || D == 0) return SGEMM_OK;
+  const GradPlan p = grad_plan(h->cus, T, N, D, ~(size_t)0 >> 1);
+  if (p.splits > 1) *bytes = (size_t)p.splits * grad_part_bytes(N, D);
+  return SGEMM_OK;
+}
+
+int sgemm_mx_byte_weight_grad(sgemm_handle_t h, int dtype, int T, int N, int D, float alpha,
+                              const void* dY, int lddy, const void* X, int ldx, const void* SX,
+                              int ldsx, float beta, int wtype, void* dW, int lddw,
+                              hipStream_t stream) {
+  if (h == nullptr) return SGEMM_ERR_HANDLE;
+  int st = validate_grad(dtype, T, N, D, dY, lddy, X, ldx, SX, ldsx, wtype, dW, lddw);
+  if (st != SGEMM_OK) return st;
+  if (N == 0 || D == 0) return SGEMM_OK;
+  st = check_device(h);
+  if (st != SGEMM_OK) return st;
+  const GradArgs g = {T, N, D, alpha, beta, dY, lddy, static_cast<const uint8_t*>(X), ldx,
+                      static_cast<const uint8_t*>(SX), ldsx, wtype, dW, lddw};
+  const GradPlan p = grad_plan(h->cus, T, N, D, h->workspace_bytes);
+  const GradTile& t = kGrad[p.tile];
+  const int tm = (int)up_div(N, t.b), tn = (int)up_div(D, t.b), band = band_rows(tm, tm * tn);
+  const int half = dtype == SGEMM_DTYPE_F16;
+  if (p.splits == 1) {
+    hipLaunchKernelGGL(t.kernel[half][wtype], dim3((unsigned)(tm * tn)), dim3(t.threads), 0, stream,
+                       g, tm, tn, band);
+    return launched();
+  }
+  float* part = static_cast<float*>(h->workspace);
+  hipLaunchKernelGGL(t.split[half], dim3((unsigned)(tm * tn * p.splits)), dim3(t.threads), 0, stream,
+                     g, tm, tn, band, p.per, part);
+  st = launched();
+  if (st != SGEMM_OK) return st;
+  const long long quads = up_div(D, 4) * N;
+  hipLaunchKernelGGL(kGradSum[wtype], dim3((unsigned)up_div(quads, GRAD_SUM_THREADS)),
+                     dim3(GRAD_SUM_THREADS), 0, stream, g, p.splits, part);
+  return launched();
 }
 
 }  // extern "C"

@@ -562,6 +562,34 @@ int sgemm_run_mx_byte_quant(sgemm_handle_t h, int xtype, int bits, int M, int N,
                             float beta, int dtype, void* C, int ldc,
                             hipStream_t stream);
 
+/* Gradient of a linear layer's weight from activations kept in 8-bit rows:
+ *
+ *     dW(n,d) = alpha * sum_t dY(t,n) * X(t,d) + beta * dW(n,d)
+ *
+ * dY is T x N of type dtype (SGEMM_DTYPE_BF16 or _F16), X T microscaled 8-bit
+ * rows of D values (any D; codes and scales in whole blocks), dW N x D of type
+ * wtype; beta == 0: dW is not read.  X's values are taken in dtype, where they are
+ * exact (bfloat16: below 2^-126 they are 0; binary16: inside that type's range), and
+ * products are summed in 32 bits: |dW - exact| <= 4*max(T,1)*2^-24*(|alpha|*
+ * sum_t|dY*X| + |beta*dW|), plus one rounding to wtype.  T == 0: dW = beta * dW.
+ *
+ * Small gradients split the tokens over workgroups, whose partial sums take up to
+ * `bytes` of the handle's workspace; with less the split is smaller.  The same
+ * inputs and workspace give the same bits.  SGEMM_ERR_UNSUPPORTED for row strides
+ * of 64 MiB and more.  Ownership, streams, errors and threading as for sgemm_run
+ * with a workspace. */
+int sgemm_mx_byte_weight_grad(sgemm_handle_t h, int dtype, int T, int N, int D,
+                              float alpha, const void* dY, int lddy,
+                              const void* X, int ldx, const void* SX, int ldsx,
+                              float beta, int wtype, void* dW, int lddw,
+                              hipStream_t stream);
+int sgemm_mx_byte_weight_grad_workspace_size(sgemm_handle_t h, int T, int N,
+                                             int D, size_t* bytes);
+int sgemm_validate_mx_byte_weight_grad(int dtype, int T, int N, int D,
+                                       const void* dY, int lddy, const void* X,
+                                       int ldx, const void* SX, int ldsx,
+                                       int wtype, const void* dW, int lddw);
+
 /* ---- root-mean-square norm of a residual stream ----------------------------------
  *
  *     h = x + r,  rstd = (mean_j h_j^2 + eps)^(-1/2),  y_j = (h_j * rstd) * g_j

@@ -258,3 +258,52 @@ def test_product_entries_without_a_device():
     fits = ((1 << 24) - 1) * 512 * 8 // K
     assert lib.sgemm_run_mx_byte_quant(at, BF16, 8, fits + 1, 1, K, 1.0, 1 << 60, K, 1 << 50, K, 1 << 52,
                                        K // 32, 0.0, BF16, 1 << 48, 1, None) == sg.SGEMM_ERR_UNSUPPORTED
+
+
+def grad(**kw):
+    a = dict(dtype=BF16, T=4, N=5, D=70, dY=DY, lddy=5, X=CODES, ldx=96, SX=SCALES, ldsx=3, wtype=F32,
+             dW=C, lddw=70)
+    a.update(kw)
+    return sg.sgemm_validate_mx_byte_weight_grad(*a.values())
+
+
+def test_validate_weight_grad():
+    assert grad() == sg.SGEMM_OK and grad(dtype=F16, wtype=F16) == sg.SGEMM_OK
+    assert grad(wtype=BF16) == sg.SGEMM_OK
+    for bad in (-1, F32, 3, 4):
+        assert grad(dtype=bad) == sg.SGEMM_ERR_VALUE
+    for bad in (-1, 3, 4):
+        assert grad(wtype=bad) == sg.SGEMM_ERR_VALUE
+    for name in ("T", "N", "D"):
+        assert grad(**{name: -1}) == sg.SGEMM_ERR_SIZE
+    for name, short in (("lddy", 4), ("ldx", 95), ("ldsx", 2), ("lddw", 69)):
+        assert grad(**{name: short}) == sg.SGEMM_ERR_LD, name
+    for name in ("dY", "X", "SX", "dW"):
+        assert grad(**{name: None}) == sg.SGEMM_ERR_NULL, name
+    assert grad(T=0, dY=None, X=None, SX=None) == sg.SGEMM_OK
+    assert grad(N=0, dY=None, dW=None) == sg.SGEMM_OK and grad(D=0, X=None, dW=None) == sg.SGEMM_OK
+    assert grad(dY=DY + 1) == sg.SGEMM_ERR_VALUE and grad(dW=C + 2) == sg.SGEMM_ERR_VALUE
+    assert grad(X=CODES + 1, SX=SCALES + 1) == sg.SGEMM_OK  # any byte address
+    assert grad(dW=DY + 36) == sg.SGEMM_ERR_ALIAS and grad(dW=CODES + 4 * 96 - 4) == sg.SGEMM_ERR_ALIAS
+    assert grad(dW=SCALES + 8) == sg.SGEMM_ERR_ALIAS
+    # a step of 64 tokens within 32-bit offsets
+    far = dict(dY=1 << 50, X=1 << 52, SX=1 << 54, dW=1 << 40)
+    assert grad(lddy=1 << 24, ldx=1 << 25, ldsx=1 << 25, **far) == sg.SGEMM_OK
+    for name in ("lddy", "ldx", "ldsx"):
+        assert grad(**{name: 1 << 27}, **far) == sg.SGEMM_ERR_UNSUPPORTED
+        assert grad(**{name: 1 << 27}, T=1, **far) == sg.SGEMM_OK
+
+
+def test_weight_grad_workspace_size():
+    lib = sg.library()
+    assert lib.sgemm_mx_byte_weight_grad(None, BF16, 1, 1, 32, 1.0, DY, 1, CODES, 32, SCALES, 1, 0.0, F32,
+                                         C, 32, None) == sg.SGEMM_ERR_HANDLE
+    h = HostHandle()
+    at = ctypes.addressof(h)
+    assert lib.sgemm_mx_byte_weight_grad_workspace_size(at, 1, 1, 1, None) == sg.SGEMM_ERR_NULL
+    size = lambda *a: sg.sgemm_mx_byte_weight_grad_workspace_size(at, *a)  # noqa: E731
+    with pytest.raises(sg.SgemmError):
+        size(-1, 1, 1)
+    assert size(0, 5, 5) == size(100, 5, 5) == size(1000, 0, 5) == 0
+    assert size(4096, 11008, 4096) == 0  # tiles enough
+    assert size(16384, 100, 200) >= 2 * 4 * 100 * 200

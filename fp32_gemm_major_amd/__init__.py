@@ -879,6 +879,18 @@ class Handle:
 
     # -- microscaled 4-bit operands --
 
+    def _ready(self, stream, names, *tensors):
+        """``_on`` for the calls whose time is mostly this binding's: ``names``
+        is split only where a tensor lies elsewhere.  None is passed over."""
+        index = self.device.index
+        for t in tensors:
+            if t is not None and t.get_device() != index:
+                self._on(stream, **{n: t for n, t in zip(names.split(), tensors)
+                                    if t is not None})
+        if stream is None:
+            return _current_stream(index)
+        return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
+
     def _on(self, stream, **tensors):
         """The stream's address, after checking that every tensor lies on the
         handle's device."""
@@ -895,13 +907,14 @@ class Handle:
         R, K = X.shape
         if trans:
             R, K = K, R
-        out = self._mx_out(kind, R, K, out, stream, "X gives")
-        s = self._on(stream, X=X, codes=out.codes, scales=out.scales)
+        out = self._mx_out(kind, R, K, out, stream)
+        codes, scales = out.codes, out.scales
+        s = self._ready(stream, "X codes scales", X, codes, scales)
         call(self.h, dtype, 1 if trans else 0, R, K, X.data_ptr(), ldx,
-             out.codes.data_ptr(), out._ldc, out.scales.data_ptr(), out._lds, s)
+             codes.data_ptr(), out._ldc, scales.data_ptr(), out._lds, s)
         return out
 
-    def _mx_out(self, kind, R, K, out, stream, what):
+    def _mx_out(self, kind, R, K, out, stream):
         """``out``, checked to be R rows of K values, or such rows allocated on
         ``stream``."""
         if out is None:
@@ -914,7 +927,7 @@ class Handle:
         if not isinstance(out, kind):
             raise TypeError(f"out must be an {kind.__name__}")
         if out.rows != R or out.K != SGEMM_MX_BLOCK * -(-K // SGEMM_MX_BLOCK):
-            raise ValueError(f"out holds {out.rows} rows of {out.K} values, {what} {R} of {K}")
+            raise ValueError(f"out holds {out.rows} rows of {out.K} values, X gives {R} of {K}")
         return out
 
     def _mx_dequantize(self, kind, call, Q, out, stream):
@@ -924,9 +937,10 @@ class Handle:
         R, K = out.shape
         if R != Q.rows or K > Q.K:
             raise ValueError(f"out is {tuple(out.shape)}, Q holds {Q.rows} rows of {Q.K} values")
-        s = self._on(stream, codes=Q.codes, scales=Q.scales, out=out)
-        call(self.h, dtype, R, K, Q.codes.data_ptr(), Q._ldc,
-             Q.scales.data_ptr(), Q._lds, out.data_ptr(), ldy, s)
+        codes, scales = Q.codes, Q.scales
+        s = self._ready(stream, "codes scales out", codes, scales, out)
+        call(self.h, dtype, R, K, codes.data_ptr(), Q._ldc, scales.data_ptr(), Q._lds,
+             out.data_ptr(), ldy, s)
         return out
 
     def mx4_quantize(self, X, trans=False, out=None, stream=None):
@@ -961,16 +975,18 @@ class Handle:
         if rows != M or B.rows != N or SGEMM_MX_BLOCK * -(-K // SGEMM_MX_BLOCK) != B.K:
             raise ValueError(f"A {rows} x {K} and B {B.rows} x {B.K} do not give "
                              f"{M} x {N}")
+        codes, scales = B.codes, B.scales
         if quantised:
-            s = self._on(stream, A=A.codes, A_scales=A.scales, B=B.codes, B_scales=B.scales, C=C)
-            return call(self.h, *bits, M, N, K, alpha, A.codes.data_ptr(), A._ldc,
-                        A.scales.data_ptr(), A._lds, B.codes.data_ptr(), B._ldc,
-                        B.scales.data_ptr(), B._lds, beta, dtype, C.data_ptr(), ldc, s)
+            a, sa = A.codes, A.scales
+            s = self._ready(stream, "A A_scales B B_scales C", a, sa, codes, scales, C)
+            return call(self.h, *bits, M, N, K, alpha, a.data_ptr(), A._ldc, sa.data_ptr(), A._lds,
+                        codes.data_ptr(), B._ldc, scales.data_ptr(), B._lds, beta, dtype,
+                        C.data_ptr(), ldc, s)
         xtype, lda = _matrix("A", A)
-        s = self._on(stream, A=A, B=B.codes, B_scales=B.scales, C=C)
+        s = self._ready(stream, "A B B_scales C", A, codes, scales, C)
         return call_quant(self.h, xtype, *bits, M, N, K, alpha, A.data_ptr(), lda,
-                          B.codes.data_ptr(), B._ldc, B.scales.data_ptr(), B._lds, beta,
-                          dtype, C.data_ptr(), ldc, s)
+                          codes.data_ptr(), B._ldc, scales.data_ptr(), B._lds, beta, dtype,
+                          C.data_ptr(), ldc, s)
 
     # -- microscaled 8-bit rows --
 
@@ -1017,9 +1033,10 @@ class Handle:
             raise TypeError("dY must be bfloat16 or float16")
         if X.rows != T or rows != N or SGEMM_MX_BLOCK * -(-D // SGEMM_MX_BLOCK) != X.K:
             raise ValueError(f"dY {T} x {N} and X {X.rows} x {X.K} do not give {rows} x {D}")
-        s = self._on(stream, dY=dY, X=X.codes, X_scales=X.scales, dW=dW)
+        codes, scales = X.codes, X.scales
+        s = self._ready(stream, "dY X X_scales dW", dY, codes, scales, dW)
         return sgemm_mx_byte_weight_grad(self.h, dtype, T, N, D, alpha, dY.data_ptr(), lddy,
-                                         X.codes.data_ptr(), X._ldc, X.scales.data_ptr(), X._lds,
+                                         codes.data_ptr(), X._ldc, scales.data_ptr(), X._lds,
                                          beta, wtype, dW.data_ptr(), lddw, s)
 
     # -- root-mean-square norm --
@@ -1036,24 +1053,18 @@ class Handle:
         dtype, ldx = _matrix("X", X)
         T, D = X.shape
         gtype = _gain(G, X)
-        more, args = {}, []
-        for name, t in (("residual", residual), ("H", H)):
-            if t is None:
-                args.append((None, 0))
-                continue
-            kind, ld = _matrix(name, t)
-            if kind != dtype or t.shape != X.shape:
-                raise ValueError(f"{name} must be {T} x {D} of X's type")
-            more[name] = t
-            args.append((t.data_ptr(), ld))
+        r, ldr = (None, 0) if residual is None else _same("residual", residual, X)
+        hp, ldh = (None, 0) if H is None else _same("H", H, X)
         if rstd is not None:
-            _vectors(T, torch.float32, rstd=rstd)
-            more["rstd"] = rstd
-        out = self._mx_out(Mx8, T, D, out, stream, "X gives")
-        s = self._on(stream, X=X, G=G, codes=out.codes, scales=out.scales, **more)
-        sgemm_rmsnorm(self.h, dtype, gtype, T, D, X.data_ptr(), ldx, *args[0], G.data_ptr(),
-                          eps, *args[1], out.codes.data_ptr(), out._ldc, out.scales.data_ptr(),
-                          out._lds, None if rstd is None else rstd.data_ptr(), s)
+            _vector("rstd", rstd, T, torch.float32)
+        out = self._mx_out(Mx8, T, D, out, stream)
+        codes, scales = out.codes, out.scales
+        s = self._ready(stream, "X G codes scales residual H rstd", X, G, codes, scales, residual, H,
+                        rstd)
+        _check(library().sgemm_rmsnorm(
+            self.h, dtype, gtype, T, D, X.data_ptr(), ldx, r, ldr, G.data_ptr(), eps, hp, ldh,
+            codes.data_ptr(), out._ldc, scales.data_ptr(), out._lds,
+            None if rstd is None else rstd.data_ptr(), s), "sgemm_rmsnorm")
         return out
 
     def rmsnorm_workspace_size(self, T, D, least=False) -> int:
@@ -1069,22 +1080,16 @@ class Handle:
         dtype, ldh = _matrix("H", H)
         T, D = H.shape
         gtype = _gain(G, H)
-        _vectors(T, torch.float32, rstd=rstd)
-        tensors, lds = {"dY": dY, "dX": dX}, {}
-        if dH is not None:
-            tensors["dH"] = dH
-        for name, t in tensors.items():
-            kind, lds[name] = _matrix(name, t)
-            if kind != dtype or t.shape != H.shape:
-                raise ValueError(f"{name} must be {T} x {D} of H's type")
+        _vector("rstd", rstd, T, torch.float32)
+        y, lddy = _same("dY", dY, H)
+        x, lddx = _same("dX", dX, H)
+        r, lddh = (None, 0) if dH is None else _same("dH", dH, H)
         if dG is not None:
-            _vectors(D, G.dtype, dG=dG)
-            tensors["dG"] = dG
-        s = self._on(stream, H=H, G=G, rstd=rstd, **tensors)
-        return sgemm_rmsnorm_backward(
-            self.h, dtype, gtype, T, D, dY.data_ptr(), lds["dY"], H.data_ptr(), ldh, G.data_ptr(),
-            rstd.data_ptr(), None if dH is None else dH.data_ptr(), lds.get("dH", 0),
-            dX.data_ptr(), lds["dX"], None if dG is None else dG.data_ptr(), s)
+            _vector("dG", dG, D, G.dtype)
+        s = self._ready(stream, "H G rstd dY dX dH dG", H, G, rstd, dY, dX, dH, dG)
+        return _check(library().sgemm_rmsnorm_backward(
+            self.h, dtype, gtype, T, D, y, lddy, H.data_ptr(), ldh, G.data_ptr(), rstd.data_ptr(),
+            r, lddh, x, lddx, None if dG is None else dG.data_ptr(), s), "sgemm_rmsnorm_backward")
 
     # -- softmax cross entropy of an output layer --
 
@@ -1141,8 +1146,15 @@ def _gain(G, X) -> int:
     """The library type of a norm's gain for rows X."""
     if G.dtype not in (X.dtype, torch.float32):
         raise TypeError(f"G must be of X's type ({X.dtype}) or float32")
-    _vectors(X.shape[1], G.dtype, G=G)
+    _vector("G", G, X.shape[1], G.dtype)
     return TENSOR_DTYPES[G.dtype]
+
+
+def _same(name, t, X):
+    """Address and leading dimension of a matrix of X's type and shape."""
+    if t.dtype != X.dtype or t.shape != X.shape:
+        raise ValueError(f"{name} must be {tuple(X.shape)} of type {X.dtype}, as the other rows")
+    return t.data_ptr(), _row_stride(name, t)
 
 
 def _ce_shapes(X, W):
@@ -1156,10 +1168,14 @@ def _ce_shapes(X, W):
 
 def _vectors(n, dtype, **tensors):
     for name, t in tensors.items():
-        if t.dtype != dtype or t.dim() != 1:
-            raise TypeError(f"{name} must be a 1-D {dtype} tensor")
-        if t.shape[0] != n or not t.is_contiguous():
-            raise ValueError(f"{name} must be {n} contiguous elements")
+        _vector(name, t, n, dtype)
+
+
+def _vector(name, t, n, dtype):
+    if t.dtype != dtype or t.dim() != 1:
+        raise TypeError(f"{name} must be a 1-D {dtype} tensor")
+    if t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous elements")
 
 
 def _span(rows, cols, ld):

@@ -14,49 +14,70 @@ using namespace sgemm;
 
 namespace {
 
-// Lanes and rows of a workgroup for rows of D values: the fewest lanes that
-// hold a row in two units of eight values each, or in one where that is still a
-// wave (up to 512 values) or four (up to 2048).
+// Lanes of a row, its units of eight values a lane and the rows of a workgroup, by
+// the largest D.  One unit a lane up to 8192 values: the loads of a row then go out
+// together and the sum's steps are few (bfloat16, 8192 x 4096 forward 42.9 us, with
+// two units in 256 lanes 44.6; 1 x 4096 2.9, 3.4).  Rows of up to 1024 values share
+// a workgroup; larger ones do not gain by it (8192 x 4096, two of 512 lanes: 47.4
+// us).  Past 8192 values a second reading costs less than fuller registers
+// (2000 x 16384: 51.9 us, with four units in 512 lanes 57.4); the gradients, which
+// read three tensors, take the registers up to 16384 (63.7 us, read twice 94.4).  The
+// gradients keep a workgroup on every CU, each over many rows, with 512 lanes
+// at least (16384 x 2048: 51.6 us, with one row of 256 lanes 62.4 and with two such
+// workgroups a CU 54.0) and 1024 of the shortest rows (32768 x 500: 38.7, with 512
+// lanes 56.6); a second workgroup a CU only adds partial sums of dg (8192 x 4096:
+// 52.2 us, 56.4).
+constexpr int NORM_SHAPES = 7;
+const long long kMost[NORM_SHAPES] = {512, 1024, 2048, 4096, 8192, 16384, SGEMM_MX_MAX_K};
 struct NormShape {
   int threads, rows;
-  long long most;  // values of a row
 };
-const NormShape kShapes[7] = {{256, 4, 512},  {256, 4, 1024},  {256, 1, 2048},
-                              {256, 1, 4096}, {512, 1, 8192},  {1024, 1, 16384},
-                              {NORM_LONG, 1, SGEMM_MX_MAX_K}};
+const NormShape kForward[NORM_SHAPES] = {{256, 4},  {256, 2}, {256, 1},      {512, 1},
+                                         {1024, 1}, {NORM_LONG, 1}, {NORM_LONG, 1}};
+const NormShape kBackward[NORM_SHAPES] = {{1024, 16}, {512, 4}, {512, 2},      {512, 1},
+                                          {1024, 1},  {512, 1}, {NORM_LONG, 1}};
 
 int shape_of(int D) {
   int i = 0;
-  while (D > kShapes[i].most) ++i;
+  while (D > kMost[i]) ++i;
   return i;
 }
 
-#define NORM_TABLE(KERNEL, DT)                                                                 \
-  {KERNEL<DT, 64, 1, 4>,  KERNEL<DT, 64, 2, 4>,   KERNEL<DT, 256, 1, 1>, KERNEL<DT, 256, 2, 1>, \
-   KERNEL<DT, 512, 2, 1>, KERNEL<DT, 1024, 2, 1>, KERNEL<DT, NORM_LONG, 0, 1>}
 typedef void (*norm_fn)(NormArgs);
-const norm_fn kNorm[3][7] = {NORM_TABLE(rmsnorm_mx8_kernel, SGEMM_DTYPE_F32),
-                             NORM_TABLE(rmsnorm_mx8_kernel, SGEMM_DTYPE_BF16),
-                             NORM_TABLE(rmsnorm_mx8_kernel, SGEMM_DTYPE_F16)};
+#define NORM_FORWARD(DT, WHOLE)                                                                  \
+  {rmsnorm_mx8_kernel<DT, 64, 1, 4, WHOLE>,   rmsnorm_mx8_kernel<DT, 128, 1, 2, WHOLE>,          \
+   rmsnorm_mx8_kernel<DT, 256, 1, 1, WHOLE>,  rmsnorm_mx8_kernel<DT, 512, 1, 1, WHOLE>,          \
+   rmsnorm_mx8_kernel<DT, 1024, 1, 1, WHOLE>, rmsnorm_mx8_kernel<DT, NORM_LONG, 0, 1, WHOLE>,    \
+   rmsnorm_mx8_kernel<DT, NORM_LONG, 0, 1, WHOLE>}
+// [D in whole units][type]
+const norm_fn kNorm[2][3][NORM_SHAPES] = {
+    {NORM_FORWARD(SGEMM_DTYPE_F32, false), NORM_FORWARD(SGEMM_DTYPE_BF16, false),
+     NORM_FORWARD(SGEMM_DTYPE_F16, false)},
+    {NORM_FORWARD(SGEMM_DTYPE_F32, true), NORM_FORWARD(SGEMM_DTYPE_BF16, true),
+     NORM_FORWARD(SGEMM_DTYPE_F16, true)}};
+#undef NORM_FORWARD
 typedef void (*norm_back_fn)(NormBackArgs);
-const norm_back_fn kNormBack[3][7] = {NORM_TABLE(rmsnorm_backward_kernel, SGEMM_DTYPE_F32),
-                                      NORM_TABLE(rmsnorm_backward_kernel, SGEMM_DTYPE_BF16),
-                                      NORM_TABLE(rmsnorm_backward_kernel, SGEMM_DTYPE_F16)};
-#undef NORM_TABLE
+#define NORM_BACKWARD(DT)                                                            \
+  {rmsnorm_backward_kernel<DT, 64, 1, 16>,  rmsnorm_backward_kernel<DT, 128, 1, 4>,  \
+   rmsnorm_backward_kernel<DT, 256, 1, 2>,  rmsnorm_backward_kernel<DT, 512, 1, 1>,  \
+   rmsnorm_backward_kernel<DT, 1024, 1, 1>, rmsnorm_backward_kernel<DT, 512, 4, 1>,  \
+   rmsnorm_backward_kernel<DT, NORM_LONG, 0, 1>}
+const norm_back_fn kNormBack[3][NORM_SHAPES] = {
+    NORM_BACKWARD(SGEMM_DTYPE_F32), NORM_BACKWARD(SGEMM_DTYPE_BF16), NORM_BACKWARD(SGEMM_DTYPE_F16)};
+#undef NORM_BACKWARD
 typedef void (*gain_fn)(const float*, int, int, void*);
 const gain_fn kGain[3] = {rmsnorm_gain_kernel<SGEMM_DTYPE_F32>,
                           rmsnorm_gain_kernel<SGEMM_DTYPE_BF16>,
                           rmsnorm_gain_kernel<SGEMM_DTYPE_F16>};
 
-// Workgroups of a norm: one a row (or four rows); more rows than 2^21
-// workgroups hold are taken in turns.
+// Workgroups of a norm: one a row (or a few rows); more rows than 2^21 workgroups
+// hold are taken in turns.
 constexpr long long kNormWgs = 1LL << 21;
 
-// Workgroups of the gradients: two a CU, each over several rows, so that the
-// partial sums of dg (D values a row of a workgroup) stay few beside the rows.
+// Workgroups of the gradients, each with its partial sums of dg.
 long long back_wgs(const sgemm_handle_s* h, int T, const NormShape& s) {
-  const long long all = up_div(T, s.rows), most = 2LL * h->cus;
-  return all < most ? all : most;
+  const long long all = up_div(T, s.rows);
+  return all < h->cus ? all : h->cus;
 }
 
 bool gain_type_ok(int dtype, int gtype) { return gtype == SGEMM_DTYPE_F32 || gtype == dtype; }
@@ -157,11 +178,11 @@ int sgemm_rmsnorm(sgemm_handle_t h, int dtype, int gtype, int T, int D, const vo
   st = check_device(h);
   if (st != SGEMM_OK) return st;
   const int at = shape_of(D);
-  const NormShape& s = kShapes[at];
+  const NormShape& s = kForward[at];
   const long long all = up_div(T, s.rows), wgs = all < kNormWgs ? all : kNormWgs;
-  const NormArgs g = {T, D, X, ldx, R, ldr, G, gtype, eps, H, ldh, static_cast<uint8_t*>(codes),
-                      ldc, static_cast<uint8_t*>(scales), lds, rstd};
-  hipLaunchKernelGGL(kNorm[dtype][at], dim3((unsigned)wgs), dim3(s.threads), 0, stream, g);
+  const NormArgs g = {T, D, X, ldx, R, ldr, G, gtype, eps, 1.0 / D, H, ldh,
+                      static_cast<uint8_t*>(codes), ldc, static_cast<uint8_t*>(scales), lds, rstd};
+  hipLaunchKernelGGL(kNorm[D % 8 == 0][dtype][at], dim3((unsigned)wgs), dim3(s.threads), 0, stream, g);
   return launched();
 }
 
@@ -175,8 +196,8 @@ int sgemm_validate_rmsnorm_backward(int dtype, int gtype, int T, int D, const vo
 int sgemm_rmsnorm_workspace_size(sgemm_handle_t h, int T, int D, size_t* least, size_t* full) {
   if (h == nullptr) return SGEMM_ERR_HANDLE;
   if (!mx_sizes_ok(T, D) || D < 1) return SGEMM_ERR_SIZE;
-  const NormShape& s = kShapes[shape_of(D)];
-  const size_t row = 4 * (size_t)D * (size_t)s.rows;
+  const NormShape& s = kBackward[shape_of(D)];
+  const size_t row = 4 * (size_t)D;
   if (least != nullptr) *least = T == 0 ? 0 : row;
   if (full != nullptr) *full = row * (size_t)back_wgs(h, T, s);
   return SGEMM_OK;
@@ -194,11 +215,11 @@ int sgemm_rmsnorm_backward(sgemm_handle_t h, int dtype, int gtype, int T, int D,
   if (st != SGEMM_OK) return st;
   if (T == 0) return launch_gain(nullptr, 0, D, gtype, dG, stream);  // (zeros)
   const int at = shape_of(D);
-  const NormShape& s = kShapes[at];
+  const NormShape& s = kBackward[at];
   long long wgs = back_wgs(h, T, s);
   float* part = nullptr;
   if (dG != nullptr) {
-    const long long room = (long long)(h->workspace_bytes / (4 * (size_t)D * (size_t)s.rows));
+    const long long room = (long long)(h->workspace_bytes / (4 * (size_t)D));
     if (room < 1) return SGEMM_ERR_SCRATCH;
     if (room < wgs) wgs = room;
     part = static_cast<float*>(h->workspace);
@@ -207,7 +228,7 @@ int sgemm_rmsnorm_backward(sgemm_handle_t h, int dtype, int gtype, int T, int D,
   hipLaunchKernelGGL(kNormBack[dtype][at], dim3((unsigned)wgs), dim3(s.threads), 0, stream, g);
   st = launched();
   if (st != SGEMM_OK || dG == nullptr) return st;
-  return launch_gain(part, (int)(wgs * s.rows), D, gtype, dG, stream);
+  return launch_gain(part, (int)wgs, D, gtype, dG, stream);
 }
 
 }  // extern "C"

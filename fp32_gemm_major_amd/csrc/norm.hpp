@@ -10,15 +10,26 @@
 //     c = mean_j dy_j g_j n_j,  dx_j = s (dy_j g_j - n_j c) + dh_j,
 //     dg_j = sum_t dy_tj n_tj.
 //
-// All of it is 32-bit arithmetic; h, the codes, dx and dg are each rounded once.
+// All of it is 32-bit arithmetic, but for what every y of a row hangs on: the lanes'
+// sums of squares are added in 64 bits, s is kept in two parts and y's products
+// carry their rounding errors into y's own, to odd.  (A code next to a border of its
+// rounding tips over with any error in y: with 32 bits throughout, codes were 5e-5 of
+// their norm off the exact norm's, now none was in 33 million; the rounding to odd costs
+// 0.4 of the 43.3 us of 8192 x 4096.)  h, the
+// codes, dx and dg are each rounded once.
 //
 // Bound by memory: in one pass over a row, held in registers between the sum and
-// what needs it.  A row takes 64 to 1024 lanes with one or two units of eight
-// values each, up to 16384 values; longer rows are read a second time, from the
-// cache that the first one left them in.  A lane's units are the quantiser's, so
-// that a block of 32 is four neighbouring lanes and its maximum two exchanges.
-// dg's sums over rows stay in a lane's registers over all rows that its workgroup
-// takes; the workgroups' sums are then added by a second launch, in their order.
+// what needs it.  A row takes 64 to 1024 lanes with one unit of eight values each
+// (gradients past 8192 values: four in 512 lanes), so that everything a row needs is
+// asked for at once; rows over 8192 values (gradients: 16384) are read a second time,
+// from the cache that the first one left them in.  A lane's units are the quantiser's, so that a block of 32
+// is four neighbouring lanes and its maximum two exchanges.  The gradients' next row
+// is asked for before this one's is used; dg's sums stay in a lane's registers over
+// all rows that its workgroup takes, and the workgroups' sums are added by a second
+// launch, in their order.
+//
+// bfloat16, 8192 x 4096: forward (235 MB with the residual) 43.3 us, 5.4 TB/s;
+// gradients with dg (268 MB) 52.2 us, 5.1 TB/s; a copy of 2 GiB runs at 4.96 TB/s.
 #pragma once
 
 #include <type_traits>
@@ -29,50 +40,143 @@ namespace sgemm {
 
 constexpr int NORM_LONG = 1024;  // lanes of a row that is read twice
 
-// The sum over a wave, the same in all lanes: rows of sixteen lanes by
-// exchanges within them, then the four rows' in order.
-__device__ __forceinline__ float wave_total(float v) {
-  auto add = [&](auto c) {
-    v += __uint_as_float((unsigned)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v),
-                                                            decltype(c)::value, 0xf, 0xf, true));
-  };
-  add(std::integral_constant<int, 0xB1>{});   // lane ^ 1
-  add(std::integral_constant<int, 0x4E>{});   // lane ^ 2
-  add(std::integral_constant<int, 0x141>{});  // 7 - lane, in eights
-  add(std::integral_constant<int, 0x140>{});  // 15 - lane, in sixteens
-  float s = 0.0f;
-#pragma unroll
-  for (int r = 0; r < 64; r += 16)
-    s += __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(v), r));
-  return s;
+// A value of another lane of the sixteen, in 32 or 64 bits.
+template <int CTRL>
+__device__ __forceinline__ float lane_moved(float v) {
+  return __uint_as_float(
+      (unsigned)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+template <int CTRL>
+__device__ __forceinline__ double lane_moved(double v) {
+  const uint2 b = __builtin_bit_cast(uint2, v);
+  return __builtin_bit_cast(
+      double, uint2{(unsigned)__builtin_amdgcn_mov_dpp((int)b.x, CTRL, 0xf, 0xf, true),
+                    (unsigned)__builtin_amdgcn_mov_dpp((int)b.y, CTRL, 0xf, 0xf, true)});
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint2 b = __builtin_bit_cast(uint2, v);
+  return __builtin_bit_cast(double,
+                            uint2{(unsigned)__builtin_amdgcn_readlane((int)b.x, lane),
+                                  (unsigned)__builtin_amdgcn_readlane((int)b.y, lane)});
 }
 
-// The sum over the TPR lanes of a row.  `red` holds two sets of the waves'
-// sums; `turn` alternates between calls, so that one barrier a call does.
-template <int TPR>
-__device__ __forceinline__ float row_total(float v, float* red, int turn) {
+// The sum over a wave, the same in all lanes: rows of sixteen lanes by
+// exchanges within them, then the four rows' in order.
+template <class V>
+__device__ __forceinline__ V wave_total(V v) {
+  v += lane_moved<0xB1>(v);   // lane ^ 1
+  v += lane_moved<0x4E>(v);   // lane ^ 2
+  v += lane_moved<0x141>(v);  // 7 - lane, in eights
+  v += lane_moved<0x140>(v);  // 15 - lane, in sixteens
+  return ((lane_value(v, 0) + lane_value(v, 16)) + lane_value(v, 32)) + lane_value(v, 48);
+}
+
+// The sum over the TPR lanes of a row, of ROWS in the workgroup.  `red` holds two
+// sets of the waves' sums; `turn` alternates between calls, so that one barrier a
+// call does.
+template <int TPR, int ROWS, class V>
+__device__ __forceinline__ V row_total(V v, V* red, int turn) {
   v = wave_total(v);
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
-    float* at = red + (turn & 1) * W;
-    if ((threadIdx.x & 63) == 0) at[threadIdx.x >> 6] = v;
+    V* at = red + (turn & 1) * W * ROWS;
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) at[wave] = v;
     __syncthreads();
-    v = 0.0f;
+    const V* own = at + wave / W * W;
+    v = V(0);
 #pragma unroll
-    for (int w = 0; w < W; ++w) v += at[w];
+    for (int w = 0; w < W; ++w) v += own[w];
   }
   return v;
 }
+template <int TPR, int ROWS>
+constexpr int row_total_size() {
+  return TPR > 64 ? 2 * ROWS * (TPR / 64) : 1;
+}
+
+// (mean + eps)^-1/2 of a sum of squares, to 64 bits' accuracy: the instruction's
+// estimate (0 and infinity are final) after two Newton steps; in two parts, of which
+// the first is the root rounded to 32 bits.
+struct RowFactor {
+  float hi, lo;
+};
+__device__ __forceinline__ RowFactor row_factor(double ss, double per_value, float eps) {
+  const double v = fma(ss, per_value, (double)eps);
+  double s = __builtin_amdgcn_rsq(v);
+  if (s > 0.0 && s < __builtin_inf()) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) s = fma(0.5 * s, fma(-v * s, s, 1.0), s);
+  }
+  RowFactor f;
+  f.hi = (float)s;
+  const float lo = (float)(s - (double)f.hi);
+  f.lo = lo - lo == 0.0f ? lo : 0.0f;  // (no difference of infinities)
+  return f;
+}
+
+// Eight elements as they stand in memory, to be asked for before they are used;
+// only the first n are read (n may be <= 0), the others are zero.  WHOLE: n is at
+// least eight or not over 0.
+template <int DT>
+struct Raw8 {
+  v4u b[DT == SGEMM_DTYPE_F32 ? 2 : 1];
+};
+template <int DT, bool WHOLE>
+__device__ __forceinline__ Raw8<DT> load_raw8(const typename TensorElem<DT>::type* p, int n) {
+  Raw8<DT> r;
+  constexpr int W = DT == SGEMM_DTYPE_F32 ? 2 : 1, PER = 8 / W;
+#pragma unroll
+  for (int w = 0; w < W; ++w) r.b[w] = v4u{0u, 0u, 0u, 0u};
+  if (WHOLE ? n > 0 : n >= 8) {
+#pragma unroll
+    for (int w = 0; w < W; ++w) r.b[w] = *reinterpret_cast<const v4u_any*>(p + PER * w);
+    return r;
+  }
+  if (WHOLE || n <= 0) return r;
+  typename TensorElem<DT>::type e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = p[i < n ? i : n - 1];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const unsigned v = i < n ? e[i] : 0u;
+    if constexpr (W == 2)
+      r.b[i / 4][i % 4] = v;
+    else
+      r.b[0][i / 2] |= i % 2 ? v << 16 : v;
+  }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void unpack8(const Raw8<DT>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if constexpr (DT == SGEMM_DTYPE_F32)
+      v[i] = __uint_as_float(r.b[i / 4][i % 4]);
+    else
+      v[i] = elem_value<DT>((uint16_t)(i % 2 ? r.b[0][i / 2] >> 16 : r.b[0][i / 2] & 0xffffu));
+}
 
 // Eight values of the gain, of type gdt, from `at` on.
-template <int DT>
+template <int DT, bool WHOLE>
 __device__ __forceinline__ void load_gain(const void* G, int gdt, size_t at, int n,
                                           float (&v)[8]) {
   typedef typename TensorElem<DT>::type E;
-  if (DT != SGEMM_DTYPE_F32 && gdt != SGEMM_DTYPE_F32)
-    load8<DT>(static_cast<const E*>(G) + at, n, v);
+  constexpr int F32 = SGEMM_DTYPE_F32;
+  if (DT != F32 && gdt != F32)
+    unpack8<DT>(load_raw8<DT, WHOLE>(static_cast<const E*>(G) + at, n), v);
   else
-    load8<SGEMM_DTYPE_F32>(static_cast<const uint32_t*>(G) + at, n, v);
+    unpack8<F32>(load_raw8<F32, WHOLE>(static_cast<const uint32_t*>(G) + at, n), v);
+}
+
+// The first n of eight values to p (n over 0).
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void store_eight(typename TensorElem<DT>::type* p, int n,
+                                            const float (&v)[8]) {
+  store8<DT>(p, WHOLE ? 8 : n, v);
 }
 
 struct NormArgs {
@@ -84,7 +188,8 @@ struct NormArgs {
   const void* G;
   int gdt;  // SGEMM_DTYPE_F32 or the stream's type
   float eps;
-  void* H;  // may be null
+  double per_value;  // 1 / D
+  void* H;           // may be null
   int ldh;
   uint8_t* codes;
   int ldc;
@@ -93,31 +198,38 @@ struct NormArgs {
   float* rstd;  // may be null
 };
 
-// h of a unit: the sum rounded, stored if asked for, and read back as rounded.
+// h of a unit: the sum rounded and read back as rounded.
 template <int DT>
-__device__ __forceinline__ void norm_state(const NormArgs& g, size_t row, int at, int n,
+__device__ __forceinline__ void norm_state(bool add, const Raw8<DT>& x, const Raw8<DT>& r,
                                            float (&v)[8]) {
-  typedef typename TensorElem<DT>::type E;
-  load8<DT>(static_cast<const E*>(g.X) + (n > 0 ? row * g.ldx + at : (size_t)0), n, v);
-  if (g.R != nullptr) {
-    float r[8];
-    load8<DT>(static_cast<const E*>(g.R) + (n > 0 ? row * g.ldr + at : (size_t)0), n, r);
+  unpack8<DT>(x, v);
+  if (!add) return;
+  float a[8];
+  unpack8<DT>(r, a);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = elem_value<DT>(elem_bits<DT>(v[i] + r[i]));
-  }
+  for (int i = 0; i < 8; ++i) v[i] = elem_value<DT>(elem_bits<DT>(v[i] + a[i]));
 }
 
 // y of a unit, quantised; a unit's block lies in its quad of lanes, whose units
-// are all inside or all outside of the row's blocks.
-template <int DT>
-__device__ __forceinline__ void norm_result(const NormArgs& g, size_t row, int u, bool in, int n,
-                                            float s, const float (&h)[8]) {
-  float w[8], y[8];
-  load_gain<DT>(g.G, g.gdt, n > 0 ? (size_t)8 * u : (size_t)0, n, w);
+// are all inside or all outside of the row's blocks.  (Past a row's end h and the
+// gain are 0; a factor that is no number makes the real values of that block none
+// either.)
+__device__ __forceinline__ void norm_result(const NormArgs& g, size_t row, int u, bool in, RowFactor s,
+                                            const float (&h)[8], const float (&w)[8]) {
+  float y[8];
   unsigned m = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    y[i] = i < n ? (h[i] * s) * w[i] : 0.0f;
+    // (where a part is infinite the value or its block is none either way)
+    const float a = h[i] * s.hi;
+    const float e = fmaf(h[i], s.lo, fmaf(h[i], s.hi, -a));  // what a's rounding left
+    const float v = fmaf(a, w[i], e * w[i]);
+    // To odd: an even v that is not exact gives way to its neighbour on the exact
+    // side, so that none comes to lie on a border of the codes' rounding.
+    const float rest = fmaf(e, w[i], fmaf(a, w[i], -v));
+    const int bits = (int)__float_as_uint(v);
+    const int side = ((int)__float_as_uint(rest) ^ bits) >> 31 | 1;
+    y[i] = __uint_as_float((unsigned)(bits + (fabsf(rest) > 0.0f && !(bits & 1) ? side : 0)));
     m = max(m, mx_abs_bits(y[i]));
   }
   m = max(m, quad_swap1(m));
@@ -129,16 +241,21 @@ __device__ __forceinline__ void norm_result(const NormArgs& g, size_t row, int u
   if ((u & 3) == 0) g.scales[row * g.lds + (u >> 2)] = (uint8_t)b;
 }
 
-// TPR lanes a row, NV units of eight values each (TPR a multiple of 64), ROWS
-// rows a workgroup; NV = 0: rows of any length.
-template <int DT, int TPR, int NV, int ROWS>
+// TPR lanes a row (a multiple of 64), NV units of eight values each, ROWS rows a
+// workgroup; NV = 0: rows of any length.  WHOLE: D is a multiple of eight.  (The
+// code for parts of units takes 90 registers in place of 58, so that fewer rows are in
+// flight: 8192 x 4096 52.3 us in place of 42.9, 4096 x 8192 59.7 in place of 45.8.)
+template <int DT, int TPR, int NV, int ROWS, bool WHOLE>
 __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_mx8_kernel(NormArgs g) {
   typedef typename TensorElem<DT>::type E;
-  static_assert(ROWS == 1 || TPR == 64, "a workgroup of several waves takes one row");
-  __shared__ float red[TPR > 64 ? 2 * (TPR / 64) : 1];
+  __shared__ double red[row_total_size<TPR, ROWS>()];
   const int lane = ROWS == 1 ? (int)threadIdx.x : (int)threadIdx.x % TPR;
   const int sub = ROWS == 1 ? 0 : (int)threadIdx.x / TPR;
   const int D = g.D, units = 4 * ((D + MX_BLOCK - 1) / MX_BLOCK);
+  const E* X = static_cast<const E*>(g.X);
+  const E* R = static_cast<const E*>(g.R);
+  E* H = static_cast<E*>(g.H);
+  const bool add = R != nullptr;
   int turn = 0;
   for (size_t base = (size_t)blockIdx.x * ROWS; base < (size_t)g.T;
        base += (size_t)gridDim.x * ROWS, ++turn) {
@@ -146,50 +263,65 @@ __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_mx8_kernel(NormArgs g) {
     const bool here = row < (size_t)g.T;
     float ss = 0.0f;
     if constexpr (NV > 0) {
-      float h[NV][8];
+      // everything that the row needs is asked for first
+      Raw8<DT> x[NV], r[NV];
+      float w[NV][8], h[NV][8];
 #pragma unroll
       for (int t = 0; t < NV; ++t) {
-        const int u = t * TPR + lane;
-        norm_state<DT>(g, row, 8 * u, here ? D - 8 * u : 0, h[t]);
+        const int u = t * TPR + lane, n = here ? D - 8 * u : 0;
+        const size_t at = n > 0 ? (size_t)8 * u : (size_t)0, k = n > 0 ? row : (size_t)0;
+        x[t] = load_raw8<DT, WHOLE>(X + k * g.ldx + at, n);
+        if (add) r[t] = load_raw8<DT, WHOLE>(R + k * g.ldr + at, n);
       }
 #pragma unroll
       for (int t = 0; t < NV; ++t) {
         const int u = t * TPR + lane;
-        if (g.H != nullptr && here && 8 * u < D)
-          store8<DT>(static_cast<E*>(g.H) + row * g.ldh + 8 * u, D - 8 * u, h[t]);
+        load_gain<DT, WHOLE>(g.G, g.gdt, 8 * u < D ? (size_t)8 * u : (size_t)0, D - 8 * u, w[t]);
+      }
+#pragma unroll
+      for (int t = 0; t < NV; ++t) {
+        const int u = t * TPR + lane;
+        norm_state<DT>(add, x[t], r[t], h[t]);
+        if (H != nullptr && here && 8 * u < D)
+          store_eight<DT, WHOLE>(H + row * g.ldh + 8 * u, D - 8 * u, h[t]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(h[t][i], h[t][i], ss);
       }
-      ss = row_total<TPR>(ss, red, turn);
-      const float s = 1.0f / sqrtf(ss / (float)D + g.eps);
-      if (lane == 0 && here && g.rstd != nullptr) g.rstd[row] = s;
+      const RowFactor s = row_factor(row_total<TPR, ROWS>((double)ss, red, turn), g.per_value, g.eps);
+      if (lane == 0 && here && g.rstd != nullptr) g.rstd[row] = s.hi;
 #pragma unroll
       for (int t = 0; t < NV; ++t) {
         const int u = t * TPR + lane;
-        norm_result<DT>(g, row, u, here && u < units, here ? D - 8 * u : 0, s, h[t]);
+        norm_result(g, row, u, here && u < units, s, h[t], w[t]);
       }
     } else {
       // (every lane reads again what it read and wrote itself)
+      auto state = [&](int u, float (&h)[8]) {
+        const int n = D - 8 * u;
+        const size_t at = n > 0 ? (size_t)8 * u : (size_t)0, k = n > 0 ? row : (size_t)0;
+        const Raw8<DT> x = load_raw8<DT, WHOLE>(X + k * g.ldx + at, n);
+        Raw8<DT> r = x;
+        if (add) r = load_raw8<DT, WHOLE>(R + k * g.ldr + at, n);
+        norm_state<DT>(add, x, r, h);
+      };
       for (int u = lane; u < units; u += TPR) {
         float h[8];
-        norm_state<DT>(g, row, 8 * u, D - 8 * u, h);
-        if (g.H != nullptr && 8 * u < D)
-          store8<DT>(static_cast<E*>(g.H) + row * g.ldh + 8 * u, D - 8 * u, h);
+        state(u, h);
+        if (H != nullptr && 8 * u < D) store_eight<DT, WHOLE>(H + row * g.ldh + 8 * u, D - 8 * u, h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(h[i], h[i], ss);
       }
-      ss = row_total<TPR>(ss, red, turn);
-      const float s = 1.0f / sqrtf(ss / (float)D + g.eps);
-      if (lane == 0 && g.rstd != nullptr) g.rstd[row] = s;
+      const RowFactor s = row_factor(row_total<TPR, ROWS>((double)ss, red, turn), g.per_value, g.eps);
+      if (lane == 0 && g.rstd != nullptr) g.rstd[row] = s.hi;
       for (int u0 = 0; u0 < units; u0 += TPR) {  // (whole waves: blocks' exchanges)
-        const int u = u0 + lane;
-        float h[8];
-        if (g.H != nullptr)
-          load8<DT>(static_cast<const E*>(g.H) + (8 * u < D ? row * g.ldh + 8 * u : (size_t)0),
-                    D - 8 * u, h);
+        const int u = u0 + lane, n = D - 8 * u;
+        float h[8], w[8];
+        if (H != nullptr)
+          unpack8<DT>(load_raw8<DT, WHOLE>(H + (n > 0 ? row * g.ldh + 8 * u : (size_t)0), n), h);
         else
-          norm_state<DT>(g, row, 8 * u, D - 8 * u, h);
-        norm_result<DT>(g, row, u, u < units, D - 8 * u, s, h);
+          state(u, h);
+        load_gain<DT, WHOLE>(g.G, g.gdt, n > 0 ? (size_t)8 * u : (size_t)0, n, w);
+        norm_result(g, row, u, u < units, s, h, w);
       }
     }
   }
@@ -216,11 +348,13 @@ __device__ __forceinline__ void norm_store_part(float* p, int n, const float (&v
   store8<SGEMM_DTYPE_F32>(reinterpret_cast<uint32_t*>(p), n, v);
 }
 
+// A workgroup takes every gridDim-th set of ROWS rows; the next one's values are
+// asked for before this one's are used (not of the widest 32-bit rows, which fill
+// the registers).
 template <int DT, int TPR, int NV, int ROWS>
 __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_backward_kernel(NormBackArgs g) {
   typedef typename TensorElem<DT>::type E;
-  static_assert(ROWS == 1 || TPR == 64, "a workgroup of several waves takes one row");
-  __shared__ float red[TPR > 64 ? 2 * (TPR / 64) : 1];
+  __shared__ float red[row_total_size<TPR, ROWS>()];
   const int lane = ROWS == 1 ? (int)threadIdx.x : (int)threadIdx.x % TPR;
   const int sub = ROWS == 1 ? 0 : (int)threadIdx.x / TPR;
   const int D = g.D;
@@ -228,63 +362,104 @@ __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_backward_kernel(NormBackAr
   const E* H = static_cast<const E*>(g.H);
   const E* dH = static_cast<const E*>(g.dH);
   E* dX = static_cast<E*>(g.dX);
-  float* part = g.part == nullptr ? nullptr : g.part + ((size_t)blockIdx.x * ROWS + sub) * D;
+  float* part = g.part == nullptr ? nullptr : g.part + (size_t)blockIdx.x * D;
   int turn = 0;
   if constexpr (NV > 0) {
+    struct Row {
+      Raw8<DT> h[NV], dy[NV], dh[NV];
+      float s;
+    };
+    auto load = [&](size_t row, Row& r) {
+      const bool here = row < (size_t)g.T;
+#pragma unroll
+      for (int t = 0; t < NV; ++t) {
+        const int u = t * TPR + lane, n = here ? D - 8 * u : 0;
+        const size_t at = n > 0 ? (size_t)8 * u : (size_t)0, k = n > 0 ? row : (size_t)0;
+        r.h[t] = load_raw8<DT, false>(H + k * g.ldh + at, n);
+        r.dy[t] = load_raw8<DT, false>(dY + k * g.lddy + at, n);
+        if (dH != nullptr) r.dh[t] = load_raw8<DT, false>(dH + k * g.lddh + at, n);
+      }
+      r.s = here ? g.rstd[row] : 0.0f;
+    };
+    constexpr bool AHEAD = DT != SGEMM_DTYPE_F32 || NV < 4;
+    const size_t first = (size_t)blockIdx.x * ROWS, step = (size_t)gridDim.x * ROWS;
+    Row next;
+    if (AHEAD) load(first + sub, next);
     float w[NV][8], dg[NV][8];
 #pragma unroll
     for (int t = 0; t < NV; ++t) {
       const int u = t * TPR + lane;
-      load_gain<DT>(g.G, g.gdt, 8 * u < D ? (size_t)8 * u : (size_t)0, D - 8 * u, w[t]);
+      load_gain<DT, false>(g.G, g.gdt, 8 * u < D ? (size_t)8 * u : (size_t)0, D - 8 * u, w[t]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) dg[t][i] = 0.0f;
     }
-    for (size_t base = (size_t)blockIdx.x * ROWS; base < (size_t)g.T;
-         base += (size_t)gridDim.x * ROWS, ++turn) {
+    for (size_t base = first; base < (size_t)g.T; base += step, ++turn) {
       const size_t row = base + sub;
       const bool here = row < (size_t)g.T;
-      float n[NV][8], dy[NV][8], dh[NV][8];
-#pragma unroll
-      for (int t = 0; t < NV; ++t) {
-        const int u = t * TPR + lane, left = here ? D - 8 * u : 0;
-        const size_t at = left > 0 ? (size_t)8 * u : (size_t)0, r = left > 0 ? row : (size_t)0;
-        load8<DT>(H + r * g.ldh + at, left, n[t]);
-        load8<DT>(dY + r * g.lddy + at, left, dy[t]);
-        if (dH != nullptr) load8<DT>(dH + r * g.lddh + at, left, dh[t]);
-      }
-      const float s = here ? g.rstd[row] : 0.0f;
+      if (!AHEAD) load(row, next);
+      Row now = next;
+      if (AHEAD && base + step < (size_t)g.T) load(row + step, next);
+      const float s = now.s;
       float c = 0.0f;
 #pragma unroll
-      for (int t = 0; t < NV; ++t)
+      for (int t = 0; t < NV; ++t) {
+        float n[8], dy[8];
+        unpack8<DT>(now.h[t], n);
+        unpack8<DT>(now.dy[t], dy);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          n[t][i] *= s;
-          const float v = dy[t][i] * n[t][i];
+          const float v = dy[i] * (n[i] * s);
           // (past the row's end n may be 0 * inf)
-          const bool in = 8 * (t * TPR + lane) + i < D;
-          if (in && here) dg[t][i] += v;
+          const bool in = here && 8 * (t * TPR + lane) + i < D;
+          if (in) dg[t][i] += v;
           c += in ? v * w[t][i] : 0.0f;
         }
-      c = row_total<TPR>(c, red, turn) / (float)D;
+      }
+      c = row_total<TPR, ROWS>(c, red, turn) / (float)D;
 #pragma unroll
       for (int t = 0; t < NV; ++t) {
         const int u = t * TPR + lane;
         if (!here || 8 * u >= D) continue;
-        float o[8];
+        float n[8], dy[8], o[8];
+        // (unpacked again: kept, they are twice the registers)
+        if constexpr (NV > 1) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[i] = s * (dy[t][i] * w[t][i] - n[t][i] * c);
-          if (dH != nullptr) o[i] += dh[t][i];
+          for (auto& b : now.h[t].b) asm volatile("" : "+v"(b));
+#pragma unroll
+          for (auto& b : now.dy[t].b) asm volatile("" : "+v"(b));
         }
-        store8<DT>(dX + row * g.lddx + 8 * u, D - 8 * u, o);
+        unpack8<DT>(now.h[t], n);
+        unpack8<DT>(now.dy[t], dy);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = s * (dy[i] * w[t][i] - (n[i] * s) * c);
+        if (dH != nullptr) {
+          float a[8];
+          unpack8<DT>(now.dh[t], a);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] += a[i];
+        }
+        store_eight<DT, false>(dX + row * g.lddx + 8 * u, D - 8 * u, o);
       }
     }
-    if (part != nullptr) {
+    if (part == nullptr) return;
+    // the workgroup's rows' sums, added in order
+    if constexpr (ROWS > 1) {
+      static_assert(NV == 1, "a unit a lane");
+      __shared__ float sums[(ROWS - 1) * TPR * 9];  // (nine: the banks)
+      if (sub > 0) {
 #pragma unroll
-      for (int t = 0; t < NV; ++t) {
-        const int u = t * TPR + lane;
-        if (8 * u < D) norm_store_part(part + 8 * u, D - 8 * u, dg[t]);
+        for (int i = 0; i < 8; ++i) sums[((sub - 1) * TPR + lane) * 9 + i] = dg[0][i];
       }
+      __syncthreads();
+      if (sub > 0) return;
+      for (int r = 0; r < ROWS - 1; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dg[0][i] += sums[(r * TPR + lane) * 9 + i];
+    }
+#pragma unroll
+    for (int t = 0; t < NV; ++t) {
+      const int u = t * TPR + lane;
+      if (8 * u < D) norm_store_part(part + 8 * u, D - 8 * u, dg[t]);
     }
   } else {
     // rows of any length: read twice, dg's sums in their place in memory
@@ -294,9 +469,9 @@ __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_backward_kernel(NormBackAr
       float c = 0.0f;
       for (int u = lane; 8 * u < D; u += TPR) {
         float n[8], dy[8], w[8], dg[8];
-        load8<DT>(H + row * g.ldh + 8 * u, D - 8 * u, n);
-        load8<DT>(dY + row * g.lddy + 8 * u, D - 8 * u, dy);
-        load_gain<DT>(g.G, g.gdt, (size_t)8 * u, D - 8 * u, w);
+        unpack8<DT>(load_raw8<DT, false>(H + row * g.ldh + 8 * u, D - 8 * u), n);
+        unpack8<DT>(load_raw8<DT, false>(dY + row * g.lddy + 8 * u, D - 8 * u), dy);
+        load_gain<DT, false>(g.G, g.gdt, (size_t)8 * u, D - 8 * u, w);
         if (part != nullptr && !first)
           load8<SGEMM_DTYPE_F32>(reinterpret_cast<const uint32_t*>(part + 8 * u), D - 8 * u, dg);
 #pragma unroll
@@ -307,21 +482,21 @@ __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_backward_kernel(NormBackAr
         }
         if (part != nullptr) norm_store_part(part + 8 * u, D - 8 * u, dg);
       }
-      c = row_total<TPR>(c, red, turn) / (float)D;
+      c = row_total<TPR, ROWS>(c, red, turn) / (float)D;
       for (int u = lane; 8 * u < D; u += TPR) {
         float n[8], dy[8], w[8], o[8];
-        load8<DT>(H + row * g.ldh + 8 * u, D - 8 * u, n);
-        load8<DT>(dY + row * g.lddy + 8 * u, D - 8 * u, dy);
-        load_gain<DT>(g.G, g.gdt, (size_t)8 * u, D - 8 * u, w);
+        unpack8<DT>(load_raw8<DT, false>(H + row * g.ldh + 8 * u, D - 8 * u), n);
+        unpack8<DT>(load_raw8<DT, false>(dY + row * g.lddy + 8 * u, D - 8 * u), dy);
+        load_gain<DT, false>(g.G, g.gdt, (size_t)8 * u, D - 8 * u, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = s * (dy[i] * w[i] - (n[i] * s) * c);
         if (dH != nullptr) {
           float dh[8];
-          load8<DT>(dH + row * g.lddh + 8 * u, D - 8 * u, dh);
+          unpack8<DT>(load_raw8<DT, false>(dH + row * g.lddh + 8 * u, D - 8 * u), dh);
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] += dh[i];
         }
-        store8<DT>(dX + row * g.lddx + 8 * u, D - 8 * u, o);
+        store_eight<DT, false>(dX + row * g.lddx + 8 * u, D - 8 * u, o);
       }
     }
   }

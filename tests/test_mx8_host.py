@@ -164,7 +164,8 @@ def test_entries_without_a_device():
     assert lib.sgemm_rmsnorm(at, F32, F32, sg.SGEMM_MX_MAX_ROWS, 8, 1 << 50, 8, None, 0, G, 1e-6, None,
                              0, 1 << 54, 32, 1 << 56, 1, None, None) == sg.SGEMM_ERR_DEVICE
     least, full = sg.sgemm_rmsnorm_workspace_size(at, 1000, 100)
-    assert least == 4 * 4 * 100 and full == min(250, 2 * h.cus) * least
+    assert least == 4 * 100 and full == 63 * least  # (sixteen rows a workgroup)
+    assert sg.sgemm_rmsnorm_workspace_size(at, 100000, 4096) == (4 * 4096, h.cus * 4 * 4096)
     assert sg.sgemm_rmsnorm_workspace_size(at, 0, 5000) == (0, 0)
     assert sg.sgemm_rmsnorm_workspace_size(at, 3, 5000) == (20000, 60000)
 

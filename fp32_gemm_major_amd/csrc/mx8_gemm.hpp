@@ -16,8 +16,11 @@
 //   32 h .. 32 h + 31 from a 4-bit one, unit h; and the scale byte of block h from
 //   either.  A row's four scale bytes of a step are one dword, shifted by 8 h as it
 //   is read; the instruction's byte select then picks byte 2 q for group q.
-// * Scale bytes come by direct loads, a dword a lane and row, 64 rows a wave
-//   instruction.
+// * Scale bytes come by direct loads too, sixteen of a row, for four steps, at a time
+//   into two areas in turn: a load of a row's four bytes asks the caches for as many
+//   lines as one of its sixteen (4096 x 11008 x 4096: XXX us, a step's four at a time
+//   186).  The row's last, partial sixteen go through registers into a third area
+//   before the loop, zeros after them.
 // * A step in which K ends, and K of less than a step, as there.  A's units past
 //   the end are zeroed as they come out of LDS; B's repeat the row's last unit (a
 //   NaN among its codes is in the row's result anyway).
@@ -37,18 +40,18 @@ struct Mx8Tile {
   static constexpr int THREADS = 64 * WAVES;
   static constexpr int FM = WM / 32, FN = WN / 32;
   static constexpr int B_ROW = 16 * WB, B_UNITS = WB, B_FU = WB / 4;  // bytes, units, units a lane
-  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * B_ROW, SC_BYTES = (BM + BN) * 4;
-  static constexpr int STAGE = A_BYTES + B_BYTES + SC_BYTES;
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * B_ROW, SC_BYTES = (BM + BN) * 16;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int A_VEC = BM * 8 / THREADS, B_VEC = BN * B_UNITS / THREADS;
   // scale loads a wave and step, 64 rows each (some waves' may be idle)
   static constexpr int S_VEC = ((BM + BN) / 64 + WAVES - 1) / WAVES;
-  static constexpr int LDS_BYTES = S * STAGE;
+  static constexpr int LDS_BYTES = S * STAGE + 3 * SC_BYTES;
   static constexpr int LDS = LDS_BYTES + 1024;  // and where look-ahead loads past the end land
   static_assert(WB == 8 || WB == 4, "bits of B");
   static_assert(A_VEC * THREADS == BM * 8 && B_VEC * THREADS == BN * B_UNITS, "code loads");
   static_assert(BM % 64 == 0 && BN % 64 == 0 && WAVES == 4, "scale loads; a lane's unit");
-  static_assert(LDS <= 160 * 1024 && S % 2 == 0, "gfx950 LDS; scale sets alternate by stage");
-  static_assert((S - 1) * (A_VEC + B_VEC + S_VEC) <= 63, "vmcnt range");
+  static_assert(LDS <= 160 * 1024 && (S == 2 || S == 4), "gfx950 LDS; stages of four steps");
+  static_assert((S - 1) * (A_VEC + B_VEC) + S_VEC <= 63, "vmcnt range");
 };
 
 template <class T>
@@ -69,7 +72,7 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
 
   auto a_at = [&](int st) { return st * T::STAGE; };
   auto b_at = [&](int st) { return st * T::STAGE + T::A_BYTES; };
-  auto s_at = [&](int st) { return st * T::STAGE + T::A_BYTES + T::B_BYTES; };
+  auto s_at = [](int area) { return S * T::STAGE + area * T::SC_BYTES; };
   auto b_off = [](int r, int c) {
     return T::WB == 8 ? lp_unit_off(r, c) : r * 64 + 16 * (c ^ ((r >> 1) & 3));
   };
@@ -89,7 +92,7 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
     b_voff[v] = (unsigned)min(r, b_last) * (unsigned)g.ldb +
                 16u * ((u & (UN - 1)) ^ ((r >> 1) & (UN - 1)));
   }
-  // Scale dwords: A's rows and then B's, one a row.
+  // Scale bytes, sixteen a row: A's rows and then B's.
   bool s_live[T::S_VEC];
 #pragma unroll
   for (int v = 0; v < T::S_VEC; ++v) {
@@ -100,16 +103,16 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
     s_base[v] = of_a ? SA : SB;
     s_voff[v] = (unsigned)min(r, of_a ? a_last : b_last) * (unsigned)(of_a ? g.ldsa : g.ldsb);
   }
+  const int sixteens = nb / 16;  // whole ones of a row
 
-  // With no whole step the loop still runs once, on stages of zeros (see the 4-bit
-  // operands' kernel): its loads all read the same bytes of A, which nothing uses.
+  // With no whole step the loop still runs once, on stages and scales of zeros (see
+  // the 4-bit operands' kernel): its loads all read the same bytes of A, which nothing
+  // uses.
   if (kd == 0) {
 #pragma unroll
     for (int v = 0; v < T::A_VEC; ++v) a_voff[v] = 0u;
 #pragma unroll
     for (int v = 0; v < T::B_VEC; ++v) b_voff[v] = 0u;
-#pragma unroll
-    for (int v = 0; v < T::S_VEC; ++v) s_voff[v] = 0u, s_base[v] = A;
   }
   const uint8_t* B_loads = kd == 0 ? A : B;
   const int steps = max(kd, 1);
@@ -125,24 +128,44 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
   const unsigned a_back = past(8, 2 * rest);
   const unsigned b_back = past(T::B_UNITS, T::B_FU * rest);
 
-  constexpr int ND = T::A_VEC + T::B_VEC + T::S_VEC;
+  constexpr int ND = T::A_VEC + T::B_VEC;
   const unsigned lds_u = (unsigned)(uintptr_t)(lds_void_t*)lds;
   const unsigned dummy = lds_u + (unsigned)T::LDS_BYTES;
-  auto load_one = [&](int kt, int st, int d, bool live) {
-    const bool part = kt == steps;
-    if (d < T::S_VEC) {
-      dma4(s_base[d] + (part ? (size_t)(nb - 4) : (size_t)kt * 4), s_voff[d],
-           live && s_live[d] ? lds_u + (unsigned)s_at(st) + 256u * (unsigned)(d * T::WAVES + wave_u)
-                             : dummy);
-    } else if (d < T::S_VEC + T::A_VEC) {
-      const int v = d - T::S_VEC;
+  // Load d of step kt into stage st.  HOT: a whole step that will be used, without
+  // the choices that the others take.
+  auto load_one = [&](auto hot_c, int kt, int st, int d, bool live) {
+    constexpr bool HOT = decltype(hot_c)::value;
+    const bool part = !HOT && kt == steps;
+    const bool of_a = d < T::A_VEC;
+    const int v = of_a ? d : d - T::A_VEC;
+    const unsigned to = lds_u + (unsigned)(of_a ? a_at(st) : b_at(st)) +
+                        1024u * (unsigned)(v * T::WAVES + wave_u);
+    const unsigned at = HOT || live ? to : dummy;
+    if (of_a)
       dma16(reinterpret_cast<const float*>(A + (size_t)kt * 128), a_voff[v] - (part ? a_back : 0u),
-            live ? lds_u + (unsigned)a_at(st) + 1024u * (unsigned)(v * T::WAVES + wave_u) : dummy);
-    } else {
-      const int v = d - T::S_VEC - T::A_VEC;
-      dma16(reinterpret_cast<const float*>(B_loads + (size_t)kt * T::B_ROW),
-            b_voff[v] - (part ? b_back : 0u),
-            live ? lds_u + (unsigned)b_at(st) + 1024u * (unsigned)(v * T::WAVES + wave_u) : dummy);
+            at);
+    else
+      dma16(reinterpret_cast<const float*>((HOT ? B : B_loads) + (size_t)kt * T::B_ROW),
+            b_voff[v] - (part ? b_back : 0u), at);
+  };
+  // The scales of steps 4 i .. 4 i + 3, whole sixteens, into area i % 2.
+  auto load_scales = [&](int i) {
+#pragma unroll
+    for (int v = 0; v < T::S_VEC; ++v)
+      dma16(reinterpret_cast<const float*>(s_base[v] + (size_t)i * 16), s_voff[v],
+            s_live[v] ? lds_u + (unsigned)s_at(i & 1) + 1024u * (unsigned)(v * T::WAVES + wave_u)
+                      : dummy);
+  };
+  // The others, up to fifteen, into area 2, a row a thread.
+  auto fill_scales = [&](int t) {
+    const int have = nb - 16 * sixteens;
+#pragma unroll 1
+    for (int i = t; i < T::BM + T::BN; i += T::THREADS) {
+      const uint8_t* row = i < T::BM ? SA + (size_t)min(i, a_last) * g.ldsa
+                                     : SB + (size_t)min(i - T::BM, b_last) * g.ldsb;
+      u32x4 x = {0u, 0u, 0u, 0u};
+      if (have > 0) x = lp_load_unit(row + 16 * (size_t)sixteens, have);
+      *reinterpret_cast<u32x4*>(lds + s_at(2) + 16 * i) = x;
     }
   };
 
@@ -170,14 +193,24 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
                                                     lp_unit_off(row, 4 * q + 2 * u + lh));
     }
   };
-  auto read_scale = [&](int st, int r, Scales& s) {
-    const char* tile = lds + s_at(st);
+  // A row's dword of the four steps' sixteen, from its area on.
+  auto read_scale = [&](const char* from, int r, Scales& s) {
     const int row = r < T::FM ? wm * T::WM + 32 * r + li : T::BM + wn * T::WN + 32 * (r - T::FM) + li;
-    const unsigned v = *reinterpret_cast<const unsigned*>(tile + 4 * row) >> (8 * lh);
+    const unsigned v = *reinterpret_cast<const unsigned*>(from + 16 * row);
     if (r < T::FM)
       s.a[r] = v;
     else
       s.b[r - T::FM] = v;
+  };
+  auto scales_of = [&](int kt) {
+    const int i = kt >> 2;
+    return lds + (i < sixteens ? s_at(i & 1) : s_at(2)) + 4 * (kt & 3);
+  };
+  // The lane half's bytes of MFMA m's operands into place, at their first use in a
+  // step.  (Next to the reads the shifts would wait for them.)
+  auto shift_scale = [&](Scales& s, int m) {
+    if (m < T::FN) s.b[m] >>= 8 * lh;
+    if (m % T::FN == 0) s.a[m / T::FN] >>= 8 * lh;
   };
   auto mma = [&](auto q_c, const Frag& f, const Scales& s, int m) {
     constexpr int q = decltype(q_c)::value;
@@ -195,24 +228,24 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
   Scales sc[2];
   // Group q of step kt (stage st): its MFMAs with the reads of the next group, the
   // next step's scales and, in the second half, step kt+S's loads.
-  auto group = [&](int kl, bool live, auto st_c, auto q_c) {
+  auto group = [&](auto hot_c, int kl, bool live, const char* next, auto st_c, auto q_c) {
     constexpr int st = decltype(st_c)::value, q = decltype(q_c)::value;
     constexpr int st1 = st + 1 == S ? 0 : st + 1;
     constexpr int rq = (q + H) % QG, rst = q + H < QG ? st : st1;
 #pragma unroll
     for (int m = 0; m < SL; ++m) {
+      if (q == 0) shift_scale(sc[st & 1], m);
       mma(q_c, fr[q], sc[st & 1], m);
 #pragma unroll
-      for (int r = 0; r < NF; ++r)
-        if (r * SL / NF == m) {
-          read_one(rst, rq, r, fr[rq]);
-          if (q == H) read_scale(st1, r, sc[st1 & 1]);
-        }
+      for (int r = 0; r < NF; ++r) {
+        if (r * SL / NF == m) read_one(rst, rq, r, fr[rq]);
+        if (q == H && r * SL / (2 * NF) == m) read_scale(next, r, sc[st1 & 1]);
+      }
       if (q >= H) {
         constexpr int SLOTS = (QG - H) * SL;
 #pragma unroll
         for (int o = 0; o < ND; ++o)
-          if (o * SLOTS / ND == (q - H) * SL + m) load_one(kl, st, o, live);
+          if (o * SLOTS / ND == (q - H) * SL + m) load_one(hot_c, kl, st, o, live);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -220,48 +253,69 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
   auto wait_lds = [] { __builtin_amdgcn_s_waitcnt(0xC07F); };  // lgkmcnt(0)
   constexpr int AHEAD = (S - 2) * ND;
   constexpr int WAIT_AHEAD = 0x0F70 | (AHEAD & 15) | ((AHEAD >> 4) << 14);
-  auto step = [&](int kt, auto st_c) {
-    const bool live = kt + S < loads;
+  auto step = [&](auto hot_c, int kt, const char* next, auto st_c) {
+    const bool live = decltype(hot_c)::value || kt + S < loads;
     const int kl = live ? kt + S : loads - 1;
-    lp_static_for<H>([&](auto q_c) { group(kl, live, st_c, q_c); });
+    lp_static_for<H>([&](auto q_c) { group(hot_c, kl, live, next, st_c, q_c); });
     wait_lds();
     __builtin_amdgcn_s_waitcnt(WAIT_AHEAD);
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
+    // (area i + 1 has been free since the step before)
+    if ((kt & 3) == 0 && (decltype(hot_c)::value || (kt >> 2) + 1 < sixteens))
+      load_scales((kt >> 2) + 1);
     lp_static_for<QG - H>([&](auto i) {
-      group(kl, live, st_c, std::integral_constant<int, H + decltype(i)::value>{});
+      group(hot_c, kl, live, next, st_c, std::integral_constant<int, H + decltype(i)::value>{});
     });
   };
   // (no scalar load may be in flight in the K loop; see lp_tile_accumulate)
   asm volatile("" ::"s"(g.C), "s"(g.ldc), "s"(g.alpha), "s"(g.beta), "s"(g.M), "s"(g.N));
   __builtin_amdgcn_s_waitcnt(0xC07F);
+  if (sixteens > 0) load_scales(0);
   lp_static_for<S>([&](auto i) {
     constexpr int st = decltype(i)::value;
 #pragma unroll
     for (int o = 0; o < ND; ++o)
-      load_one(st < loads ? st : loads - 1, st, o, kd > 0 && st < loads);
+      load_one(std::false_type{}, st < loads ? st : loads - 1, st, o, kd > 0 && st < loads);
   });
   if (kd == 0) {
 #pragma unroll 1
-    for (int i = tid; i < T::STAGE / 16; i += T::THREADS)
+    for (int i = tid; i < T::LDS_BYTES / 16; i += T::THREADS)
       *reinterpret_cast<u32x4*>(lds + 16 * i) = u32x4{0u, 0u, 0u, 0u};
+  } else {
+    if (nb % 16 != 0) fill_scales(tid);
   }
   constexpr int FIRST = (S - 1) * ND;
   __builtin_amdgcn_s_waitcnt(0x0F70 | (FIRST & 15) | ((FIRST >> 4) << 14));
   wait_lds();
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < NF; ++r) read_scale(0, r, sc[0]);
+  for (int r = 0; r < NF; ++r) read_scale(scales_of(0), r, sc[0]);
   lp_static_for<H>([&](auto q_c) {
 #pragma unroll
     for (int r = 0; r < NF; ++r)
       read_one(0, decltype(q_c)::value, r, fr[decltype(q_c)::value]);
   });
   int kt = 0;
+  // Four steps at a time while the loads are of whole steps and sixteens: the choices
+  // of the others, scalar instructions between two MFMAs, hold these up.
+  for (; kt + 8 <= kd; kt += 4) {
+    const char* own = lds + s_at((kt >> 2) & 1);
+    const char* other = lds + s_at(((kt >> 2) + 1) & 1);
+    lp_static_for<4>([&](auto i) {
+      constexpr int n = decltype(i)::value;
+      step(std::true_type{}, kt + n, n == 3 ? other : own + 4 * (n + 1),
+           std::integral_constant<int, n % S>{});
+    });
+  }
   for (; kt + S <= steps; kt += S)
-    lp_static_for<S>([&](auto i) { step(kt + decltype(i)::value, i); });
+    lp_static_for<S>([&](auto i) {
+      const int k = kt + decltype(i)::value;
+      step(std::false_type{}, k, scales_of(k + 1), i);
+    });
   lp_static_for<S - 1>([&](auto i) {
-    if (kt + decltype(i)::value < steps) step(kt + decltype(i)::value, i);
+    const int k = kt + decltype(i)::value;
+    if (k < steps) step(std::false_type{}, k, scales_of(k + 1), i);
   });
   if (rest > 0) {
     // the partial step's loads have had whole steps to land
@@ -269,16 +323,8 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
     wait_lds();
     __syncthreads();
     const int st = steps % S;
-    // (the dword holds the row's last four blocks)
-    const int shift = 8 * (4 - rest + lh);
-    auto scale = [&](int row) {
-      const unsigned long long d = *reinterpret_cast<const unsigned*>(lds + s_at(st) + 4 * row);
-      return (unsigned)(d >> shift);
-    };
 #pragma unroll
-    for (int i = 0; i < T::FM; ++i) sc[0].a[i] = scale(wm * T::WM + 32 * i + li);
-#pragma unroll
-    for (int j = 0; j < T::FN; ++j) sc[0].b[j] = scale(T::BM + wn * T::WN + 32 * j + li);
+    for (int r = 0; r < NF; ++r) read_scale(scales_of(steps), r, sc[0]);
     lp_static_for<QG>([&](auto q_c) {
       constexpr int q = decltype(q_c)::value;
 #pragma unroll
@@ -289,7 +335,10 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
         for (int u = 0; u < 2; ++u)
           if (4 * q + 2 * u + lh >= 2 * rest) fr[0].a[i][u] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int m = 0; m < SL; ++m) mma(q_c, fr[0], sc[0], m);
+      for (int m = 0; m < SL; ++m) {
+        if (q == 0) shift_scale(sc[0], m);
+        mma(q_c, fr[0], sc[0], m);
+      }
       __builtin_amdgcn_sched_barrier(0);
     });
   }
@@ -318,25 +367,20 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
     };
     fill(A, g.lda, a_last, T::BM, 8, 2 * nb, a_at(0), [](int r, int c) { return lp_unit_off(r, c); });
     fill(B, g.ldb, b_last, T::BN, T::B_UNITS, T::B_FU * nb, b_at(0), b_off);
-#pragma unroll 1
-    for (int i = t; i < (T::BM + T::BN) * 4; i += T::THREADS) {
-      const int c = i & 3, r = i >> 2;
-      uint8_t b = 0;
-      if (c < nb)
-        b = r < T::BM ? SA[(size_t)min(r, a_last) * g.ldsa + c]
-                      : SB[(size_t)min(r - T::BM, b_last) * g.ldsb + c];
-      lds[s_at(0) + i] = (char)b;
-    }
+    fill_scales(t);
     wait_lds();
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < NF; ++r) read_scale(0, r, sc[0]);
+    for (int r = 0; r < NF; ++r) read_scale(scales_of(0), r, sc[0]);
     lp_static_for<QG>([&](auto q_c) {
       constexpr int q = decltype(q_c)::value;
 #pragma unroll
       for (int r = 0; r < NF; ++r) read_one(0, q, r, fr[0]);
 #pragma unroll
-      for (int m = 0; m < SL; ++m) mma(q_c, fr[0], sc[0], m);
+      for (int m = 0; m < SL; ++m) {
+        if (q == 0) shift_scale(sc[0], m);
+        mma(q_c, fr[0], sc[0], m);
+      }
       __builtin_amdgcn_sched_barrier(0);
     });
   }

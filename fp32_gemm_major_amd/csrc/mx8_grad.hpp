@@ -15,8 +15,8 @@
 // transposing reads half a step ahead, dY by direct global-to-LDS loads.  X comes
 // through registers: a lane loads sixteen codes of a row, which share a scale, a
 // step before their stage is free, converts two a v_cvt_scalef32_pk instruction
-// and writes them as two units.  (Lanes 4-7 of every eight write their second unit
-// first, so that eight lanes' 16 bytes fill all banks.)  Tokens past the last
+// and writes them as two units, one between two MFMAs.  (Lanes 4-7 of every eight
+// take their second unit first, so that eight lanes' 16 bytes fill all banks.)  Tokens past the last
 // whole step, and those whose pieces of dY would be read past the buffer's end, go
 // through registers, zero-filled.
 //
@@ -108,9 +108,10 @@ __device__ __forceinline__ void grad_tile_accumulate(const GradArgs& g, char* ld
   const unsigned a_voff = 2u * ((unsigned)ak * (unsigned)g.lddy + (unsigned)ao);
   // X: token u / (BN/16) and sixteen columns; those past the row's whole blocks
   // read its last sixteen (columns of dW that are not stored).
-  const int swap = (lane >> 2) & 1;
+  const int swap = (lane >> 2) & 1;  // (the eight codes that a lane takes first)
   const int col = min(n0 + 16 * bc, 32 * ((g.D + 31) / 32) - 16);
-  const unsigned b_voff = (unsigned)bk * (unsigned)g.ldx + (unsigned)col;
+  const unsigned b_row = (unsigned)bk * (unsigned)g.ldx + (unsigned)col;
+  const unsigned b_voff[2] = {b_row + 8u * swap, b_row + 8u * (1 - swap)};
   const unsigned s_voff = (unsigned)bk * (unsigned)g.ldsx + (unsigned)(col >> 5);
   const int b_lds = bk * 2 * T::BN + 16 * (((2 * bc) ^ lp_oc_swz<T::BN>(bk)) + swap);
 
@@ -126,26 +127,27 @@ __device__ __forceinline__ void grad_tile_accumulate(const GradArgs& g, char* ld
     dma16(reinterpret_cast<const float*>(A + (size_t)(kt * GRAD_STEP + v * A_ROWS) * g.lddy), a_voff,
           live ? lds_u + (unsigned)a_at(st) + 1024u * (unsigned)(v * T::WAVES + wave_u) : dummy);
   };
-  v4u codes[BV];
+  v2u codes[BV][2];
   unsigned scale[BV];
+  auto eight = [&](const uint8_t* p, int h) -> v2u {
+    return *reinterpret_cast<const Mx8Format::eight_any*>(p + b_voff[h]);
+  };
   auto load_b = [&](int kt, int v) {
     const size_t k = (size_t)(kt * GRAD_STEP + v * B_ROWS);
-    codes[v] = *reinterpret_cast<const v4u_any*>(B + k * g.ldx + b_voff);
+    codes[v][0] = eight(B + k * g.ldx, 0);
+    codes[v][1] = eight(B + k * g.ldx, 1);
     scale[v] = (SB + k * g.ldsx)[s_voff];
   };
-  auto store_b = [&](int st, int v) {
-    const float s = mx_scale_value(scale[v]);
-    const v4u c = codes[v];
-    const unsigned w[4] = {swap ? c[2] : c[0], swap ? c[3] : c[1], swap ? c[0] : c[2],
-                           swap ? c[1] : c[3]};
-    char* p = lds + b_at(st) + v * B_ROWS * 2 * T::BN;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      // (the units of a pair differ in their lowest bit)
-      *reinterpret_cast<u32x4*>(p + (b_lds ^ (16 * h))) =
-          u32x4{grad_pair<DT, false>(w[2 * h], s), grad_pair<DT, true>(w[2 * h], s),
-                grad_pair<DT, false>(w[2 * h + 1], s), grad_pair<DT, true>(w[2 * h + 1], s)};
+  // Half h of piece v, converted, to its unit.  (The instructions read the exponent of
+  // their scale alone: 0 stands for 2^-127 and 255 for NaN there too.)
+  auto store_codes = [&](int st, int v, int h, v2u c, unsigned sb) {
+    const float s = __uint_as_float(sb << 23);
+    // (the units of a pair differ in their lowest bit)
+    *reinterpret_cast<u32x4*>(lds + b_at(st) + v * B_ROWS * 2 * T::BN + (b_lds ^ (16 * h))) =
+        u32x4{grad_pair<DT, false>(c[0], s), grad_pair<DT, true>(c[0], s),
+              grad_pair<DT, false>(c[1], s), grad_pair<DT, true>(c[1], s)};
   };
+  auto store_b = [&](int st, int v, int h) { store_codes(st, v, h, codes[v][h], scale[v]); };
 
   struct Frag {
     u32x4 a[T::FM], b[T::FN];
@@ -180,16 +182,16 @@ __device__ __forceinline__ void grad_tile_accumulate(const GradArgs& g, char* ld
       for (int r = 0; r < NF; ++r)
         if (r * SL / NF == m) read_one(rst, rq, r, fr[rq]);
       if (q >= H) {
-        constexpr int SLOTS = (QG - H) * SL, ITEMS = BV + T::A_VEC;
+        constexpr int SLOTS = (QG - H) * SL, ITEMS = 2 * BV + T::A_VEC;
         const bool live = kt + S < kd;
 #pragma unroll
         for (int o = 0; o < ITEMS; ++o)
           if (o * SLOTS / ITEMS == (q - H) * SL + m) {
-            if (o < BV) {
-              store_b(st, o);
-              load_b(min(kt + S + 1, kd - 1), o);
+            if (o < 2 * BV) {
+              store_b(st, o / 2, o % 2);
+              if (o % 2) load_b(min(kt + S + 1, kd - 1), o / 2);
             } else {
-              load_a(live ? kt + S : kd - 1, st, o - BV, live);
+              load_a(live ? kt + S : kd - 1, st, o - 2 * BV, live);
             }
           }
       }
@@ -210,20 +212,31 @@ __device__ __forceinline__ void grad_tile_accumulate(const GradArgs& g, char* ld
   asm volatile("" ::"s"(g.dW), "s"(g.lddw), "s"(g.alpha), "s"(g.beta), "s"(g.D), "s"(N));
   __builtin_amdgcn_s_waitcnt(0xC07F);
   if (kd > 0) {
+    // X of three steps asked for at once, and dY of two
+    v2u early[S][BV][2];
+    unsigned early_scale[S][BV];
+#pragma unroll
+    for (int st = 0; st < S; ++st)
+#pragma unroll
+      for (int v = 0; v < BV; ++v) {
+        load_b(min(st, kd - 1), v);
+        early[st][v][0] = codes[v][0];
+        early[st][v][1] = codes[v][1];
+        early_scale[st][v] = scale[v];
+      }
+#pragma unroll
+    for (int v = 0; v < BV; ++v) load_b(min(S, kd - 1), v);
     lp_static_for<S>([&](auto i) {
       constexpr int st = decltype(i)::value;
 #pragma unroll
       for (int v = 0; v < T::A_VEC; ++v) load_a(min(st, kd - 1), st, v, st < kd);
     });
-    lp_static_for<S>([&](auto i) {
-      constexpr int st = decltype(i)::value;
 #pragma unroll
-      for (int v = 0; v < BV; ++v) load_b(min(st, kd - 1), v);
+    for (int st = 0; st < S; ++st)
 #pragma unroll
-      for (int v = 0; v < BV; ++v) store_b(st, v);
-    });
+      for (int v = 0; v < BV; ++v)
 #pragma unroll
-    for (int v = 0; v < BV; ++v) load_b(min(S, kd - 1), v);
+        for (int h = 0; h < 2; ++h) store_codes(st, v, h, early[st][v][h], early_scale[st][v]);
     wait_all();
     wait_lds();
     __syncthreads();
@@ -255,14 +268,16 @@ __device__ __forceinline__ void grad_tile_accumulate(const GradArgs& g, char* ld
     }
 #pragma unroll
     for (int v = 0; v < BV; ++v) {
-      codes[v] = v4u{0u, 0u, 0u, 0u};
+      codes[v][0] = codes[v][1] = v2u{0u, 0u};
       scale[v] = 0u;
       const size_t row = (size_t)(k + v * B_ROWS);
       if (k + v * B_ROWS + bk < kn) {
-        codes[v] = *reinterpret_cast<const v4u_any*>(B + row * g.ldx + b_voff);
+        codes[v][0] = eight(B + row * g.ldx, 0);
+        codes[v][1] = eight(B + row * g.ldx, 1);
         scale[v] = (SB + row * g.ldsx)[s_voff];
       }
-      store_b(0, v);
+      store_b(0, v, 0);
+      store_b(0, v, 1);
     }
     wait_lds();
     __syncthreads();

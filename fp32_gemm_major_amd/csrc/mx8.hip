@@ -16,13 +16,15 @@ namespace {
 typedef void (*small_fn)(MxArgs);
 // [bits of B: 8, 4][A's kind: codes, activations by type][one or four tiles of
 // columns a workgroup]
-#define MX8_SMALL(XDT, WB) {mx8_small_kernel<XDT, WB, 1>, mx8_small_kernel<XDT, WB, 4>}
+#define MX8_SMALL(XDT, WB) {mx8_small_kernel<XDT, WB, 1, 1>, mx8_small_kernel<XDT, WB, 1, 4>}
 #define MX8_SMALLS(WB)                                                     \
   {MX8_SMALL(-1, WB), MX8_SMALL(SGEMM_DTYPE_F32, WB), MX8_SMALL(SGEMM_DTYPE_BF16, WB), \
    MX8_SMALL(SGEMM_DTYPE_F16, WB)}
 const small_fn kSmall[2][4][2] = {MX8_SMALLS(8), MX8_SMALLS(4)};
 #undef MX8_SMALLS
 #undef MX8_SMALL
+// Codes of more rows, two tiles of which share B's loads: [bits].
+const small_fn kRows[2] = {mx8_small_kernel<-1, 8, 2, 1>, mx8_small_kernel<-1, 4, 2, 1>};
 
 template <class T>
 constexpr MxTileDesc tile_desc() {
@@ -39,22 +41,40 @@ int launch_small(int bits, int xdt, int tiles, const MxArgs& g, hipStream_t stre
 }
 
 // Tiles of columns a workgroup of up to 16 rows takes: four, once that still
-// leaves half the CUs one.
+// leaves half the CUs one (16 x 11008 x 4096: 13.3 us in 8 bits and 10.0 in 4, with
+// one tile 17.0 and 13.0; 16 x 4096 x 4096 8.5 and 6.4 with one, 13.2 and 9.2 with
+// four).
 int row_tiles(const MxArgs& g, int cus) {
   return 2 * up_div(g.N, 4 * MXS_TILE) >= cus ? 4 : 1;
 }
 
-// The kernel for a product of codes.
+// The kernel for a product of codes (bfloat16 C, B read from memory, 256 CUs; times of
+// a weight in 8 bits, in 4):
+//
+// * up to 16 rows: straight from memory, which reads B once;
+// * more, while its 16 x 16 tiles are at most two a CU: the same with two tiles of
+//   rows a workgroup (24 x 4096 x 4096: 9.9 us, 7.5; in 64-square tiles 11.8, 7.6; 64
+//   x 2048 x 11008 18.7, 16.1; in 64-square ones 32.7, 27.8);
+// * 64-square tiles while they are at most two a CU, which run side by side (384 x
+//   4096 x 4096: 20.9, 14.0; in 128-square ones 23.3, 14.7; 1000 x 1500 x 800 8.0, 7.6;
+//   11.2, 10.7);
+// * 128-square ones in the same way (1500 x 4096 x 4096: 39.0, 31.6; in 256-square
+//   ones 51.6, 41.9; 2048 x 4096 x 4096 44.8, 34.6; 49.6, 41.0);
+// * else 256-square ones (700 x 11008 x 4096: 50.9, 45.2; in 128-square ones 55.5,
+//   47.1; 3000 x 4096 x 4096 52.7, 45.5; 59.5, 49.6).
 int launch_product(const sgemm_handle_s* h, int bits, const MxArgs& g, hipStream_t stream) {
-  const long long cus = h->cus;
+  const long long most = 2LL * h->cus;
+  const int w = bits == 4;
   if (g.M <= MXS_TILE || g.K == 0)
     return launch_small(bits, -1, row_tiles(g, h->cus), g, stream);
   auto tiles = [&](int b) { return up_div(g.M, b) * up_div(g.N, b); };
-  if (tiles(MXS_TILE) <= 2 * cus) return launch_small(bits, -1, 1, g, stream);
-  const int at = tiles(256) >= cus || 4 * tiles(128) > 5 * cus ? 0 : 5 * tiles(128) >= 3 * cus ? 1 : 2;
-  for (int i = at; i < 3; ++i)
-    if (tile_fits(kTiles[bits == 4][i], g)) return launch_tile(kTiles[bits == 4][i], g, stream);
-  return launch_small(bits, -1, 1, g, stream);  // (strides past the tiles' offsets)
+  if (tiles(MXS_TILE) > most) {
+    const int at = tiles(64) <= most ? 2 : tiles(128) <= most ? 1 : 0;
+    for (int i = at; i < 3; ++i)
+      if (tile_fits(kTiles[w][i], g)) return launch_tile(kTiles[w][i], g, stream);
+  }
+  // (strides past the tiles' offsets come here too)
+  return launch_small_grid(kRows[w], 1, g, stream, 2);
 }
 
 int validate(int bits, int M, int N, int K, const void* A, int lda, const void* SA, int ldsa,
@@ -74,7 +94,6 @@ typedef void (*grad_sum_fn)(GradArgs, int, const float*);
 struct GradTile {
   int b, threads;
   grad_fn kernel[2][3];  // [type of dY: bfloat16, binary16][type of dW]
-  grad_split_fn split[2];
 };
 template <class T>
 constexpr GradTile grad_tile() {
@@ -84,10 +103,11 @@ constexpr GradTile grad_tile() {
       {{mx8_grad_kernel<T, LP_BF16, SGEMM_DTYPE_F32>, mx8_grad_kernel<T, LP_BF16, SGEMM_DTYPE_BF16>,
         mx8_grad_kernel<T, LP_BF16, SGEMM_DTYPE_F16>},
        {mx8_grad_kernel<T, LP_F16, SGEMM_DTYPE_F32>, mx8_grad_kernel<T, LP_F16, SGEMM_DTYPE_BF16>,
-        mx8_grad_kernel<T, LP_F16, SGEMM_DTYPE_F16>}},
-      {mx8_grad_split_kernel<T, LP_BF16>, mx8_grad_split_kernel<T, LP_F16>}};
+        mx8_grad_kernel<T, LP_F16, SGEMM_DTYPE_F16>}}};
 }
 const GradTile kGrad[2] = {grad_tile<L256x256>(), grad_tile<G128x128>()};
+const grad_split_fn kGradSplit[2] = {mx8_grad_split_kernel<G128x128, LP_BF16>,
+                                     mx8_grad_split_kernel<G128x128, LP_F16>};
 const grad_sum_fn kGradSum[3] = {mx8_grad_sum_kernel<SGEMM_DTYPE_F32>,
                                  mx8_grad_sum_kernel<SGEMM_DTYPE_BF16>,
                                  mx8_grad_sum_kernel<SGEMM_DTYPE_F16>};
@@ -96,21 +116,32 @@ size_t grad_part_bytes(int N, int D) { return 4 * (size_t)N * (size_t)((D + 3LL)
 
 // The launch of a weight gradient: which tile, and over how many ranges of `per`
 // tokens the sum is split.
+//
+// 128-square tiles while they are at most two a CU, which run side by side, else
+// 256-square ones (8192 x 2560 x 2560: 121 us, in 256-square ones 156; 8192 x 1500 x
+// 6000, 564 tiles of 128: 167 us in 256-square ones, 230; 4096 x 3000 x 3500 93, 119).
+// Few tiles are split where a model of the launch says so, in us: 0.55 a step of 64
+// tokens, up to 1.6 times that with two workgroups a CU, and for a split 6 for the second
+// launch, 0.06 a range and the partial sums once each way at 4 TB/s (16384 x 1000 x 1000: 48 us in 8
+// ranges, 164 in one; 16384 x 100 x 200 15 in 32, 164 in one; 2048 x 1024 x 1024 18 in
+// one, 20 in 4; 777 x 1500 x 1000 13 in one, 21 in 4).
 struct GradPlan {
   int tile, splits, per;
 };
 GradPlan grad_plan(int cus, int T, int N, int D, size_t workspace) {
-  auto tiles = [&](int b) { return up_div(N, b) * up_div(D, b); };
-  if (4 * tiles(256) >= 3LL * cus) return {0, 1, T};
-  const long long have = tiles(128);
-  // two workgroups a CU, ranges of at least four steps
-  long long splits = have >= cus ? 1 : 2LL * cus / have;
-  const long long most = T / (4 * GRAD_STEP);
-  if (splits > most) splits = most;
-  const long long room = (long long)(workspace / grad_part_bytes(N, D));
-  if (splits > room) splits = room;
-  if (splits < 2) return {1, 1, T};
-  const int per = (int)(up_div(up_div(T, splits), GRAD_STEP) * GRAD_STEP);
+  const long long tiles = up_div(N, 128) * up_div(D, 128);
+  if (tiles > 2LL * cus) return {0, 1, T};
+  const long long steps = up_div(T, GRAD_STEP), room = (long long)(workspace / grad_part_bytes(N, D));
+  auto time = [&](long long s) {
+    const double full = (double)tiles * s / cus;
+    return 0.55 * up_div(steps, s) * (full > 1 ? 1 + 0.6 * (full - 1) : 1) +
+           (s > 1 ? 6 + s * (0.06 + grad_part_bytes(N, D) / 2e6) : 0);
+  };
+  long long best = 1;
+  for (long long s = 2; s <= room && 2 * s <= steps && tiles * s <= 2LL * cus; ++s)
+    if (time(s) < time(best)) best = s;
+  if (best < 2) return {1, 1, T};
+  const int per = (int)(up_div(steps, best) * GRAD_STEP);
   return {1, (int)up_div(T, per), per};
 }
 
@@ -248,7 +279,7 @@ int sgemm_mx_byte_weight_grad(sgemm_handle_t h, int dtype, int T, int N, int D, 
     return launched();
   }
   float* part = static_cast<float*>(h->workspace);
-  hipLaunchKernelGGL(t.split[half], dim3((unsigned)(tm * tn * p.splits)), dim3(t.threads), 0, stream,
+  hipLaunchKernelGGL(kGradSplit[half], dim3((unsigned)(tm * tn * p.splits)), dim3(t.threads), 0, stream,
                      g, tm, tn, band, p.per, part);
   st = launched();
   if (st != SGEMM_OK) return st;

@@ -119,28 +119,28 @@ __device__ __forceinline__ i32x8 mx4_operand(const u32x4& c) {
   return i32x8{(int)c[0], (int)c[1], (int)c[2], (int)c[3], 0, 0, 0, 0};
 }
 
-// XDT < 0: A in codes, else activations of at most MXS_FEW rows.  WB: bits of B.
-// NT: the workgroup's tiles of 16 columns.
-template <int XDT, int WB, int NT>
+// XDT < 0: A in codes, else activations of at most MXS_FEW rows.  WB: bits of B.  The
+// workgroup takes MT tiles of 16 rows (which share B's loads) and NT of 16 columns.
+template <int XDT, int WB, int MT, int NT>
 __global__ void __launch_bounds__(MXS_THREADS) mx8_small_kernel(MxArgs g) {
   constexpr bool FEW = XDT >= 0;
-  __shared__ f32x4 red[MXS_WAVES * 64 * NT];
+  static_assert(!FEW || MT == 1, "few rows are one tile");
+  __shared__ f32x4 red[MXS_WAVES * 64 * MT * NT];
   __shared__ u32x4 few_codes[FEW ? MXS_WAVES * 128 : 1];
   __shared__ unsigned few_scales[FEW ? MXS_WAVES * 64 : 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * (MXS_TILE * NT), m = blockIdx.y * MXS_TILE + i;
-  const bool a_in = m < g.M;
+  const int n0 = blockIdx.x * (MXS_TILE * NT), m0 = blockIdx.y * (MXS_TILE * MT);
   const int nb = (g.K + MX_BLOCK - 1) / MX_BLOCK;
   const int steps = (nb + MXS_STEP - 1) / MXS_STEP;
   const int per = (steps + MXS_WAVES - 1) / MXS_WAVES;
   const int s0 = wave * per, s1 = s0 + per < steps ? s0 + per : steps;
-  f32x4 acc[NT];
+  f32x4 acc[MT * NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int t = 0; t < MT * NT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   for (int s = s0; s < s1; ++s) {
     typename std::conditional<WB == 8, Mx8Run, MxRun>::type b[NT];
-    Mx8Run a;
+    Mx8Run a[MT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int n = n0 + MXS_TILE * t + i;
@@ -151,29 +151,35 @@ __global__ void __launch_bounds__(MXS_THREADS) mx8_small_kernel(MxArgs g) {
         mx_load_run(g.B + r * g.ldb, g.SB + r * g.ldsb, n < g.N, s, q, nb, b[t]);
     }
     if constexpr (!FEW) {
-      const size_t r = (size_t)(a_in ? m : 0);
-      mx8_load_run(static_cast<const uint8_t*>(g.A) + r * g.lda, g.SA + r * g.ldsa, a_in, s, q, nb,
-                   a);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const int m = m0 + MXS_TILE * t + i;
+        const size_t r = (size_t)(m < g.M ? m : 0);
+        mx8_load_run(static_cast<const uint8_t*>(g.A) + r * g.lda, g.SA + r * g.ldsa, m < g.M, s, q,
+                     nb, a[t]);
+      }
     } else {
       typedef typename TensorElem<XDT < 0 ? 0 : XDT>::type E;
       mx8_quant_few<XDT < 0 ? 0 : XDT>(static_cast<const E*>(g.A), g.lda, g.M, s, lane, g.K,
-                                       few_codes + wave * 128, few_scales + wave * 64, a);
+                                       few_codes + wave * 128, few_scales + wave * 64, a[0]);
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < MT * NT; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        const auto& bt = b[t % NT];
+        const Mx8Run& at = a[t / NT];
         i32x8 x;
         if constexpr (WB == 8)
-          x = mx8_operand(b[t].codes[j]);
+          x = mx8_operand(bt.codes[j]);
         else
-          x = mx4_operand(b[t].codes[j]);
+          x = mx4_operand(bt.codes[j]);
         acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            x, mx8_operand(a.codes[j]), acc[t], WB == 8 ? 0 : 4, 0, 0, (int)b[t].scale[j], 0,
-            (int)a.scale[j]);
+            x, mx8_operand(at.codes[j]), acc[t], WB == 8 ? 0 : 4, 0, 0, (int)bt.scale[j], 0,
+            (int)at.scale[j]);
       }
   }
-  mx_small_finish<NT>(g, red, acc, n0);
+  mx_small_finish<NT, MT>(g, red, acc, n0);
 }
 
 }  // namespace sgemm

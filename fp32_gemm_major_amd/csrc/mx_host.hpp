@@ -168,10 +168,10 @@ int validate_activations(int xtype, int M, int N, int K, const void* X, int ldx,
   return grid_holds(quantize_wgs(SGEMM_OP_N, M, K), MX_THREADS) ? SGEMM_OK : SGEMM_ERR_UNSUPPORTED;
 }
 
-// A kernel for few rows, `tiles` tiles of 16 columns a workgroup, over a grid that
-// holds its launches.
+// A kernel for few rows, `tiles` tiles of 16 columns and `row_tiles` of 16 rows a
+// workgroup, over a grid that holds its launches.
 inline int launch_small_grid(void (*kernel)(MxArgs), int tiles, const MxArgs& g,
-                             hipStream_t stream) {
+                             hipStream_t stream, int row_tiles = 1) {
   constexpr int kRows = 65535 * MXS_TILE;  // a grid's second extent
   // (the first one's threads are counted in 32 bits: 2^23 workgroups less one)
   constexpr int kCols = (int)(0xffffffffu / MXS_THREADS) * MXS_TILE;
@@ -190,7 +190,8 @@ inline int launch_small_grid(void (*kernel)(MxArgs), int tiles, const MxArgs& g,
       }
       p.C = static_cast<char*>(g.C) + ((size_t)m0 * g.ldc + (size_t)n0) * tensor_elem_bytes(g.cdt);
       hipLaunchKernelGGL(kernel,
-                         dim3((unsigned)up_div(p.N, MXS_TILE * tiles), (unsigned)up_div(p.M, MXS_TILE)),
+                         dim3((unsigned)up_div(p.N, MXS_TILE * tiles),
+                              (unsigned)up_div(p.M, MXS_TILE * row_tiles)),
                          dim3(MXS_THREADS), 0, stream, p);
       const int st = launched();
       if (st != SGEMM_OK) return st;

@@ -157,27 +157,30 @@ __device__ __forceinline__ void mx_quant_few(const typename TensorElem<XDT>::typ
   }
 }
 
-// The waves' partial results of the workgroup's NT tiles from column n0 on,
+// The waves' partial results of the workgroup's MT x NT tiles from column n0 on,
 // added through LDS in wave order, to C.
-template <int NT>
+template <int NT, int MT = 1>
 __device__ __forceinline__ void mx_small_finish(const MxArgs& g, f32x4* red,
-                                                const f32x4 (&acc)[NT], int n0) {
+                                                const f32x4 (&acc)[MT * NT], int n0) {
+  constexpr int TILES = MT * NT;
+  static_assert(TILES <= MXS_WAVES, "a wave a tile");
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int q = lane >> 4, m = blockIdx.y * MXS_TILE + (lane & 15);
+  const int q = lane >> 4;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) red[(wave * NT + t) * 64 + lane] = acc[t];
+  for (int t = 0; t < TILES; ++t) red[(wave * TILES + t) * 64 + lane] = acc[t];
   __syncthreads();
-  if (wave >= NT) return;
+  if (wave >= TILES) return;
   // wave t finishes tile t
   f32x4 s = red[wave * 64 + lane];
 #pragma unroll
   for (int w = 1; w < MXS_WAVES; ++w) {
-    const f32x4 v = red[(w * NT + wave) * 64 + lane];
+    const f32x4 v = red[(w * TILES + wave) * 64 + lane];
 #pragma unroll
     for (int r = 0; r < 4; ++r) s[r] += v[r];
   }
+  const int m = (blockIdx.y * MT + wave / NT) * MXS_TILE + (lane & 15);
   if (m >= g.M) return;
-  const int col = n0 + MXS_TILE * wave + 4 * q;
+  const int col = n0 + MXS_TILE * (wave % NT) + 4 * q;
   const size_t at = (size_t)m * g.ldc + col;
 #pragma unroll
   for (int r = 0; r < 4; ++r)

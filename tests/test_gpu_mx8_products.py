@@ -61,6 +61,7 @@ PRODUCTS = [(1, 1, 32), (1, 16, 64), (1, 4096, 4096), (2, 17, 96), (4, 100, 512)
             (17, 40, 544), (33, 65, 32), (64, 64, 256), (100, 128, 1056), (128, 256, 800),
             (200, 300, 160), (256, 512, 512), (257, 511, 288), (1000, 1500, 800), (300, 5000, 96),
             (700, 900, 64), (700, 900, 32), (700, 900, 128), (700, 900, 352),
+            (700, 900, 1056), (640, 832, 2048), (650, 840, 1632), (300, 70, 2048), (40, 500, 5000 // 32 * 32),
             # enough tiles for the 128-square and the 256-square ones, K of less
             # than a step, of whole steps (odd and even counts) and ragged
             (2050, 2100, 64), (2050, 2100, 128), (2048, 2176, 1024), (2050, 2100, 1312),

@@ -702,7 +702,10 @@ class Mx8(_MxRows):
 def _row_stride(name, t) -> int:
     """Leading dimension of a 2-D row-major tensor (its rows may be strided,
     but must not overlap)."""
-    (rows, cols), (ld, step) = t.shape, t.stride()
+    rows, cols = t.shape
+    if 0 < cols <= INT_MAX and rows <= INT_MAX and t.is_contiguous():
+        return cols
+    ld, step = t.stride()
     if rows == 1 and ld > INT_MAX:
         ld = cols
     if rows > INT_MAX or cols > INT_MAX or ld > INT_MAX:
@@ -738,6 +741,7 @@ class Handle:
     def __init__(self, variant: int = SGEMM_VARIANT_AUTO, kernel: int = -1,
                  workspace: bool = True):
         self.h = sgemm_create()
+        self._lib = library()
         self.device = torch.device("cuda", torch.cuda.current_device())
         self.workspace = None
         self._stamps = None
@@ -879,9 +883,12 @@ class Handle:
 
     # -- microscaled 4-bit operands --
 
+    # (The calls from here on are short beside their own checks, so these take as
+    # few steps as they can.)
+
     def _ready(self, stream, names, *tensors):
-        """``_on`` for the calls whose time is mostly this binding's: ``names``
-        is split only where a tensor lies elsewhere.  None is passed over."""
+        """``_on``; ``names`` is split only where a tensor lies elsewhere.  None
+        is passed over."""
         index = self.device.index
         for t in tensors:
             if t is not None and t.get_device() != index:
@@ -910,8 +917,10 @@ class Handle:
         out = self._mx_out(kind, R, K, out, stream)
         codes, scales = out.codes, out.scales
         s = self._ready(stream, "X codes scales", X, codes, scales)
-        call(self.h, dtype, 1 if trans else 0, R, K, X.data_ptr(), ldx,
-             codes.data_ptr(), out._ldc, scales.data_ptr(), out._lds, s)
+        st = call(self.h, dtype, 1 if trans else 0, R, K, X.data_ptr(), ldx, codes.data_ptr(),
+                  out._ldc, scales.data_ptr(), out._lds, s)
+        if st < 0:
+            raise SgemmError(st, call.__name__)
         return out
 
     def _mx_out(self, kind, R, K, out, stream):
@@ -939,8 +948,10 @@ class Handle:
             raise ValueError(f"out is {tuple(out.shape)}, Q holds {Q.rows} rows of {Q.K} values")
         codes, scales = Q.codes, Q.scales
         s = self._ready(stream, "codes scales out", codes, scales, out)
-        call(self.h, dtype, R, K, codes.data_ptr(), Q._ldc, scales.data_ptr(), Q._lds,
-             out.data_ptr(), ldy, s)
+        st = call(self.h, dtype, R, K, codes.data_ptr(), Q._ldc, scales.data_ptr(), Q._lds,
+                  out.data_ptr(), ldy, s)
+        if st < 0:
+            raise SgemmError(st, call.__name__)
         return out
 
     def mx4_quantize(self, X, trans=False, out=None, stream=None):
@@ -948,12 +959,12 @@ class Handle:
         float32, bfloat16 or float16): an ``Mx4`` of R rows, ``out`` if given
         (else allocated on ``stream``).  K need not be whole blocks; the last
         one is filled with zeros."""
-        return self._mx_quantize(Mx4, sgemm_mx_quantize, X, trans, out, stream)
+        return self._mx_quantize(Mx4, self._lib.sgemm_mx_quantize, X, trans, out, stream)
 
     def mx4_dequantize(self, Q, out, stream=None):
         """The values of ``Q`` into ``out`` (float32, bfloat16 or float16; its
         columns are at most Q.K, the rest is left out).  Returns ``out``."""
-        return self._mx_dequantize(Mx4, sgemm_mx_dequantize, Q, out, stream)
+        return self._mx_dequantize(Mx4, self._lib.sgemm_mx_dequantize, Q, out, stream)
 
     def gemm_mx4(self, A, B, C, alpha=1.0, beta=0.0, stream=None):
         """C = alpha * A @ B^T + beta * C with B an ``Mx4`` of N rows and A an
@@ -964,8 +975,8 @@ class Handle:
             raise TypeError("A must be an Mx4 or a tensor (8-bit rows: gemm_mx8)")
         if not isinstance(B, Mx4):
             raise TypeError("B must be an Mx4")
-        return self._mx_product(Mx4, sgemm_run_mx, sgemm_run_mx_quant, (), A, B, C, alpha, beta,
-                                stream)
+        return self._mx_product(Mx4, self._lib.sgemm_run_mx, self._lib.sgemm_run_mx_quant, (), A, B,
+                                C, alpha, beta, stream)
 
     def _mx_product(self, kind, call, call_quant, bits, A, B, C, alpha, beta, stream):
         dtype, ldc = _matrix("C", C)
@@ -979,14 +990,18 @@ class Handle:
         if quantised:
             a, sa = A.codes, A.scales
             s = self._ready(stream, "A A_scales B B_scales C", a, sa, codes, scales, C)
-            return call(self.h, *bits, M, N, K, alpha, a.data_ptr(), A._ldc, sa.data_ptr(), A._lds,
-                        codes.data_ptr(), B._ldc, scales.data_ptr(), B._lds, beta, dtype,
-                        C.data_ptr(), ldc, s)
-        xtype, lda = _matrix("A", A)
-        s = self._ready(stream, "A B B_scales C", A, codes, scales, C)
-        return call_quant(self.h, xtype, *bits, M, N, K, alpha, A.data_ptr(), lda,
-                          codes.data_ptr(), B._ldc, scales.data_ptr(), B._lds, beta, dtype,
-                          C.data_ptr(), ldc, s)
+            st = call(self.h, *bits, M, N, K, alpha, a.data_ptr(), A._ldc, sa.data_ptr(), A._lds,
+                      codes.data_ptr(), B._ldc, scales.data_ptr(), B._lds, beta, dtype,
+                      C.data_ptr(), ldc, s)
+        else:
+            xtype, lda = _matrix("A", A)
+            call = call_quant
+            s = self._ready(stream, "A B B_scales C", A, codes, scales, C)
+            st = call(self.h, xtype, *bits, M, N, K, alpha, A.data_ptr(), lda, codes.data_ptr(),
+                      B._ldc, scales.data_ptr(), B._lds, beta, dtype, C.data_ptr(), ldc, s)
+        if st < 0:
+            raise SgemmError(st, call.__name__)
+        return st
 
     # -- microscaled 8-bit rows --
 
@@ -994,11 +1009,11 @@ class Handle:
         """``mx4_quantize`` in 8 bits (an ``Mx8``): activations kept for a
         backward pass at 33/64 of their 16-bit size, or operands of
         ``gemm_mx8``."""
-        return self._mx_quantize(Mx8, sgemm_mx_byte_quantize, X, trans, out, stream)
+        return self._mx_quantize(Mx8, self._lib.sgemm_mx_byte_quantize, X, trans, out, stream)
 
     def mx8_dequantize(self, Q, out, stream=None):
         """The values of an ``Mx8``, as ``mx4_dequantize``."""
-        return self._mx_dequantize(Mx8, sgemm_mx_byte_dequantize, Q, out, stream)
+        return self._mx_dequantize(Mx8, self._lib.sgemm_mx_byte_dequantize, Q, out, stream)
 
     def gemm_mx8(self, A, B, C, alpha=1.0, beta=0.0, stream=None):
         """C = alpha * A @ B^T + beta * C with B an ``Mx8`` or ``Mx4`` of N rows
@@ -1011,7 +1026,7 @@ class Handle:
             raise TypeError("A must be an Mx8 or a tensor (4-bit rows: gemm_mx4)")
         if not isinstance(B, _MxRows):
             raise TypeError("B must be an Mx8 or an Mx4")
-        return self._mx_product(Mx8, sgemm_run_mx_byte, sgemm_run_mx_byte_quant,
+        return self._mx_product(Mx8, self._lib.sgemm_run_mx_byte, self._lib.sgemm_run_mx_byte_quant,
                                 (8 if isinstance(B, Mx8) else 4,), A, B, C, alpha, beta, stream)
 
     def mx8_weight_grad_workspace_size(self, dY, X) -> int:
@@ -1035,9 +1050,10 @@ class Handle:
             raise ValueError(f"dY {T} x {N} and X {X.rows} x {X.K} do not give {rows} x {D}")
         codes, scales = X.codes, X.scales
         s = self._ready(stream, "dY X X_scales dW", dY, codes, scales, dW)
-        return sgemm_mx_byte_weight_grad(self.h, dtype, T, N, D, alpha, dY.data_ptr(), lddy,
-                                         codes.data_ptr(), X._ldc, scales.data_ptr(), X._lds,
-                                         beta, wtype, dW.data_ptr(), lddw, s)
+        return _check(self._lib.sgemm_mx_byte_weight_grad(
+            self.h, dtype, T, N, D, alpha, dY.data_ptr(), lddy, codes.data_ptr(), X._ldc,
+            scales.data_ptr(), X._lds, beta, wtype, dW.data_ptr(), lddw, s),
+            "sgemm_mx_byte_weight_grad")
 
     # -- root-mean-square norm --
 
@@ -1051,20 +1067,26 @@ class Handle:
         ``residual`` itself; ``rstd`` (T float32) the rows' factors, for
         ``rmsnorm_backward``."""
         dtype, ldx = _matrix("X", X)
-        T, D = X.shape
-        gtype = _gain(G, X)
-        r, ldr = (None, 0) if residual is None else _same("residual", residual, X)
-        hp, ldh = (None, 0) if H is None else _same("H", H, X)
+        shape, kind = X.shape, X.dtype
+        T, D = shape
+        gtype = _gain(G, kind, D)
+        r = h = p = None
+        ldr = ldh = 0
+        if residual is not None:
+            r, ldr = _same("residual", residual, kind, shape)
+        if H is not None:
+            h, ldh = _same("H", H, kind, shape)
         if rstd is not None:
-            _vector("rstd", rstd, T, torch.float32)
+            p = _vector("rstd", rstd, T, torch.float32)
         out = self._mx_out(Mx8, T, D, out, stream)
         codes, scales = out.codes, out.scales
         s = self._ready(stream, "X G codes scales residual H rstd", X, G, codes, scales, residual, H,
                         rstd)
-        _check(library().sgemm_rmsnorm(
-            self.h, dtype, gtype, T, D, X.data_ptr(), ldx, r, ldr, G.data_ptr(), eps, hp, ldh,
-            codes.data_ptr(), out._ldc, scales.data_ptr(), out._lds,
-            None if rstd is None else rstd.data_ptr(), s), "sgemm_rmsnorm")
+        st = self._lib.sgemm_rmsnorm(self.h, dtype, gtype, T, D, X.data_ptr(), ldx, r, ldr,
+                                     G.data_ptr(), eps, h, ldh, codes.data_ptr(), out._ldc,
+                                     scales.data_ptr(), out._lds, p, s)
+        if st < 0:
+            raise SgemmError(st, "sgemm_rmsnorm")
         return out
 
     def rmsnorm_workspace_size(self, T, D, least=False) -> int:
@@ -1078,18 +1100,20 @@ class Handle:
         from elsewhere (``dH``).  H and ``rstd`` are the forward call's (X where
         it had no H).  dX may be dY or dH itself; dG is of G's type."""
         dtype, ldh = _matrix("H", H)
-        T, D = H.shape
-        gtype = _gain(G, H)
-        _vector("rstd", rstd, T, torch.float32)
-        y, lddy = _same("dY", dY, H)
-        x, lddx = _same("dX", dX, H)
-        r, lddh = (None, 0) if dH is None else _same("dH", dH, H)
-        if dG is not None:
-            _vector("dG", dG, D, G.dtype)
+        shape, kind = H.shape, H.dtype
+        T, D = shape
+        gtype = _gain(G, kind, D)
+        p = _vector("rstd", rstd, T, torch.float32)
+        y, lddy = _same("dY", dY, kind, shape)
+        x, lddx = _same("dX", dX, kind, shape)
+        r, lddh = (None, 0) if dH is None else _same("dH", dH, kind, shape)
+        w = None if dG is None else _vector("dG", dG, D, G.dtype)
         s = self._ready(stream, "H G rstd dY dX dH dG", H, G, rstd, dY, dX, dH, dG)
-        return _check(library().sgemm_rmsnorm_backward(
-            self.h, dtype, gtype, T, D, y, lddy, H.data_ptr(), ldh, G.data_ptr(), rstd.data_ptr(),
-            r, lddh, x, lddx, None if dG is None else dG.data_ptr(), s), "sgemm_rmsnorm_backward")
+        st = self._lib.sgemm_rmsnorm_backward(self.h, dtype, gtype, T, D, y, lddy, H.data_ptr(), ldh,
+                                              G.data_ptr(), p, r, lddh, x, lddx, w, s)
+        if st < 0:
+            raise SgemmError(st, "sgemm_rmsnorm_backward")
+        return st
 
     # -- softmax cross entropy of an output layer --
 
@@ -1142,18 +1166,19 @@ class Handle:
                                  *args, s)
 
 
-def _gain(G, X) -> int:
-    """The library type of a norm's gain for rows X."""
-    if G.dtype not in (X.dtype, torch.float32):
-        raise TypeError(f"G must be of X's type ({X.dtype}) or float32")
-    _vector("G", G, X.shape[1], G.dtype)
-    return TENSOR_DTYPES[G.dtype]
+def _gain(G, dtype, D) -> int:
+    """The library type of a norm's gain for rows of D values of ``dtype``."""
+    kind = G.dtype
+    if kind != dtype and kind != torch.float32:
+        raise TypeError(f"G must be of the rows' type ({dtype}) or float32")
+    _vector("G", G, D, kind)
+    return TENSOR_DTYPES[kind]
 
 
-def _same(name, t, X):
-    """Address and leading dimension of a matrix of X's type and shape."""
-    if t.dtype != X.dtype or t.shape != X.shape:
-        raise ValueError(f"{name} must be {tuple(X.shape)} of type {X.dtype}, as the other rows")
+def _same(name, t, dtype, shape):
+    """Address and leading dimension of a matrix of other rows' type and shape."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} of type {dtype}, as the other rows")
     return t.data_ptr(), _row_stride(name, t)
 
 
@@ -1172,10 +1197,12 @@ def _vectors(n, dtype, **tensors):
 
 
 def _vector(name, t, n, dtype):
+    """Address of a tensor of n contiguous elements."""
     if t.dtype != dtype or t.dim() != 1:
         raise TypeError(f"{name} must be a 1-D {dtype} tensor")
     if t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name} must be {n} contiguous elements")
+    return t.data_ptr()
 
 
 def _span(rows, cols, ld):

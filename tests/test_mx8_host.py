@@ -189,15 +189,20 @@ def test_container():
 
 def test_binding_checks():
     torch = pytest.importorskip("torch")
-    x = torch.zeros(3, 40, dtype=torch.bfloat16)
-    assert sg._gain(torch.ones(40), x) == F32
-    assert sg._gain(torch.ones(40, dtype=torch.bfloat16), x) == BF16
+    bf16 = torch.bfloat16
+    assert sg._gain(torch.ones(40), bf16, 40) == F32
+    assert sg._gain(torch.ones(40, dtype=bf16), bf16, 40) == BF16
     with pytest.raises(TypeError):
-        sg._gain(torch.ones(40, dtype=torch.float16), x)
+        sg._gain(torch.ones(40, dtype=torch.float16), bf16, 40)
     with pytest.raises(ValueError):
-        sg._gain(torch.ones(41), x)
+        sg._gain(torch.ones(41), bf16, 40)
     with pytest.raises(ValueError):
-        sg._gain(torch.ones(80)[::2], x)
+        sg._gain(torch.ones(80)[::2], bf16, 40)
+    rows = torch.zeros(3, 48, dtype=bf16)[:, :40]
+    assert sg._same("H", rows, bf16, (3, 40)) == (rows.data_ptr(), 48)
+    for bad in (rows.float(), rows[:2], rows.t()):
+        with pytest.raises(ValueError):
+            sg._same("H", bad, bf16, (3, 40))
 
 
 A8, SA, W, SW, C = 0x1000000, 0x2000000, 0x3000000, 0x4000000, 0x8000000  # never touched

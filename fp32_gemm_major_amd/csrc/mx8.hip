@@ -14,13 +14,15 @@ using namespace sgemm;
 namespace {
 
 typedef void (*small_fn)(MxArgs);
-// [bits of B: 8, 4][A's kind: codes, activations by type][one or four tiles of
-// columns a workgroup]
-#define MX8_SMALL(XDT, WB) {mx8_small_kernel<XDT, WB, 1, 1>, mx8_small_kernel<XDT, WB, 1, 4>}
-#define MX8_SMALLS(WB)                                                     \
+// [bits of B: 8, 4][A's kind: codes, activations by type][tiles of columns a
+// workgroup, less one]
+#define MX8_SMALL(XDT, WB)                                             \
+  {mx8_small_kernel<XDT, WB, 1, 1>, mx8_small_kernel<XDT, WB, 1, 2>,   \
+   mx8_small_kernel<XDT, WB, 1, 3>, mx8_small_kernel<XDT, WB, 1, 4>}
+#define MX8_SMALLS(WB)                                                 \
   {MX8_SMALL(-1, WB), MX8_SMALL(SGEMM_DTYPE_F32, WB), MX8_SMALL(SGEMM_DTYPE_BF16, WB), \
    MX8_SMALL(SGEMM_DTYPE_F16, WB)}
-const small_fn kSmall[2][4][2] = {MX8_SMALLS(8), MX8_SMALLS(4)};
+const small_fn kSmall[2][4][4] = {MX8_SMALLS(8), MX8_SMALLS(4)};
 #undef MX8_SMALLS
 #undef MX8_SMALL
 // Codes of more rows, two tiles of which share B's loads: [bits].
@@ -36,16 +38,16 @@ const MxTileDesc kTiles[2][3] = {
     {tile_desc<Y256x256<8>>(), tile_desc<Y128x128<8>>(), tile_desc<Y64x64<8>>()},
     {tile_desc<Y256x256<4>>(), tile_desc<Y128x128<4>>(), tile_desc<Y64x64<4>>()}};
 
-int launch_small(int bits, int xdt, int tiles, const MxArgs& g, hipStream_t stream) {
-  return launch_small_grid(kSmall[bits == 4][1 + xdt][tiles == 4], tiles, g, stream);
-}
-
-// Tiles of columns a workgroup of up to 16 rows takes: four, once that still
-// leaves half the CUs one (16 x 11008 x 4096: 13.3 us in 8 bits and 10.0 in 4, with
-// one tile 17.0 and 13.0; 16 x 4096 x 4096 8.5 and 6.4 with one, 13.2 and 9.2 with
-// four).
-int row_tiles(const MxArgs& g, int cus) {
-  return 2 * up_div(g.N, 4 * MXS_TILE) >= cus ? 4 : 1;
+// The product of up to 16 rows.  A workgroup takes the fewest tiles of 16 columns with
+// which there is one on every CU at most, or four: a CU's stream of B is what takes
+// its time, so a second round of workgroups would double it (16 x 11008 x 4096, 8 and 4
+// bits: 12.2 and 9.1 us with three tiles, with two 17.4 and 12.3, with four 13.5 and
+// 10.0; 16 x 4096 x 4096 8.4 and 6.4 with one, 9.1 and 7.0 with two).
+int launch_small(const sgemm_handle_s* h, int bits, int xdt, const MxArgs& g,
+                 hipStream_t stream) {
+  int tiles = 1;
+  while (tiles < 4 && up_div(g.N, MXS_TILE * tiles) > h->cus) ++tiles;
+  return launch_small_grid(kSmall[bits == 4][1 + xdt][tiles - 1], tiles, g, stream);
 }
 
 // The kernel for a product of codes (bfloat16 C, B read from memory, 256 CUs; times of
@@ -65,8 +67,7 @@ int row_tiles(const MxArgs& g, int cus) {
 int launch_product(const sgemm_handle_s* h, int bits, const MxArgs& g, hipStream_t stream) {
   const long long most = 2LL * h->cus;
   const int w = bits == 4;
-  if (g.M <= MXS_TILE || g.K == 0)
-    return launch_small(bits, -1, row_tiles(g, h->cus), g, stream);
+  if (g.M <= MXS_TILE || g.K == 0) return launch_small(h, bits, -1, g, stream);
   auto tiles = [&](int b) { return up_div(g.M, b) * up_div(g.N, b); };
   if (tiles(MXS_TILE) > most) {
     const int at = tiles(64) <= most ? 2 : tiles(128) <= most ? 1 : 0;
@@ -105,9 +106,11 @@ constexpr GradTile grad_tile() {
        {mx8_grad_kernel<T, LP_F16, SGEMM_DTYPE_F32>, mx8_grad_kernel<T, LP_F16, SGEMM_DTYPE_BF16>,
         mx8_grad_kernel<T, LP_F16, SGEMM_DTYPE_F16>}}};
 }
-const GradTile kGrad[2] = {grad_tile<L256x256>(), grad_tile<G128x128>()};
-const grad_split_fn kGradSplit[2] = {mx8_grad_split_kernel<G128x128, LP_BF16>,
-                                     mx8_grad_split_kernel<G128x128, LP_F16>};
+const GradTile kGrad[3] = {grad_tile<L256x256>(), grad_tile<G128x128>(), grad_tile<G64x64>()};
+// [128- and 64-square tiles][type of dY]
+const grad_split_fn kGradSplit[2][2] = {
+    {mx8_grad_split_kernel<G128x128, LP_BF16>, mx8_grad_split_kernel<G128x128, LP_F16>},
+    {mx8_grad_split_kernel<G64x64, LP_BF16>, mx8_grad_split_kernel<G64x64, LP_F16>}};
 const grad_sum_fn kGradSum[3] = {mx8_grad_sum_kernel<SGEMM_DTYPE_F32>,
                                  mx8_grad_sum_kernel<SGEMM_DTYPE_BF16>,
                                  mx8_grad_sum_kernel<SGEMM_DTYPE_F16>};
@@ -117,32 +120,46 @@ size_t grad_part_bytes(int N, int D) { return 4 * (size_t)N * (size_t)((D + 3LL)
 // The launch of a weight gradient: which tile, and over how many ranges of `per`
 // tokens the sum is split.
 //
-// 128-square tiles while they are at most two a CU, which run side by side, else
-// 256-square ones (8192 x 2560 x 2560: 121 us, in 256-square ones 156; 8192 x 1500 x
-// 6000, 564 tiles of 128: 167 us in 256-square ones, 230; 4096 x 3000 x 3500 93, 119).
-// Few tiles are split where a model of the launch says so, in us: 0.55 a step of 64
-// tokens, up to 1.6 times that with two workgroups a CU, and for a split 6 for the second
-// launch, 0.06 a range and the partial sums once each way at 4 TB/s (16384 x 1000 x 1000: 48 us in 8
-// ranges, 164 in one; 16384 x 100 x 200 15 in 32, 164 in one; 2048 x 1024 x 1024 18 in
-// one, 20 in 4; 777 x 1500 x 1000 13 in one, 21 in 4).
+// 256-square tiles where 128-square ones are more than two a CU, which run side by
+// side (4096 x 3000 x 3500, tokens first: 93 us, in 128-square ones 119; 8192 x 1500 x
+// 6000 167, 230; but 8192 x 2560 x 2560, 400 tiles of 128: 156, 121).  Else the
+// smallest by a model of the launch, in us, fitted on 17 shapes (its choices cost 1%
+// over the best measured ones on them):
+//
+//     steps of 64 tokens a range * (0.28 or 0.44 in 64- or 128-square tiles, 0.2 more
+//     with over 8 MB of operands, past the caches)
+//     * (1 + (0.6 or 0.2) (workgroups a CU - 1), if these are over one)
+//     + for a split 4, 0.06 a range and its partial sums at 2 TB/s
+//
+// (777 x 1500 x 1000: 10.4 us in 64-square tiles, 12.9 in 128-square ones, 18.7 split
+// in two; 16384 x 1000 x 1000 49 in 8 ranges, 165 in one; 16384 x 64 x 64 10 in 32, 72
+// in one.)
 struct GradPlan {
   int tile, splits, per;
 };
 GradPlan grad_plan(int cus, int T, int N, int D, size_t workspace) {
-  const long long tiles = up_div(N, 128) * up_div(D, 128);
-  if (tiles > 2LL * cus) return {0, 1, T};
+  const int edge[2] = {128, 64};
+  const double step[2] = {0.44, 0.28}, share[2] = {0.2, 0.6};
+  const double part = (double)grad_part_bytes(N, D);
   const long long steps = up_div(T, GRAD_STEP), room = (long long)(workspace / grad_part_bytes(N, D));
-  auto time = [&](long long s) {
-    const double full = (double)tiles * s / cus;
-    return 0.55 * up_div(steps, s) * (full > 1 ? 1 + 0.6 * (full - 1) : 1) +
-           (s > 1 ? 6 + s * (0.06 + grad_part_bytes(N, D) / 2e6) : 0);
-  };
-  long long best = 1;
-  for (long long s = 2; s <= room && 2 * s <= steps && tiles * s <= 2LL * cus; ++s)
-    if (time(s) < time(best)) best = s;
-  if (best < 2) return {1, 1, T};
-  const int per = (int)(up_div(steps, best) * GRAD_STEP);
-  return {1, (int)up_div(T, per), per};
+  const bool far = (double)T * (2.0 * N + D) > 8e6;
+  GradPlan best = {0, 1, T};
+  double least = 0;
+  for (int i = 0; i < 2; ++i) {
+    const long long tiles = up_div(N, edge[i]) * up_div(D, edge[i]);
+    for (long long s = 1; tiles * s <= 2LL * cus && (s == 1 || (s <= room && 2 * s <= steps));
+         s += 1 + s / 8) {
+      const double a_cu = (double)tiles * s / cus;
+      const double t = (double)up_div(steps, s) * (step[i] + (far ? 0.2 : 0)) *
+                           (a_cu > 1 ? 1 + share[i] * (a_cu - 1) : 1) +
+                       (s > 1 ? 4 + s * (0.06 + part / 2e6) : 0);
+      if (best.tile != 0 && t >= least) continue;
+      least = t;
+      const int per = (int)(up_div(steps, s) * GRAD_STEP);
+      best = {1 + i, s > 1 ? (int)up_div(T, per) : 1, s > 1 ? per : T};
+    }
+  }
+  return best;
 }
 
 int validate_grad(int dtype, int T, int N, int D, const void* dY, int lddy, const void* X, int ldx,
@@ -220,7 +237,7 @@ int sgemm_run_mx_byte_quant(sgemm_handle_t h, int xtype, int bits, int M, int N,
   if (st != SGEMM_OK) return st;
   MxArgs g = {M, N, K, alpha, beta, X, ldx, nullptr, 0, static_cast<const uint8_t*>(B), ldb,
               static_cast<const uint8_t*>(SB), ldsb, dtype, C, ldc};
-  if (M <= MXS_FEW) return launch_small(bits, xtype, row_tiles(g, h->cus), g, stream);
+  if (M <= MXS_FEW) return launch_small(h, bits, xtype, g, stream);
   // more rows: A's codes and then its scales in the handle's workspace
   const size_t nb = (size_t)blocks_of(K), rows = (size_t)M;
   if (h->workspace_bytes < 33 * nb * rows) return SGEMM_ERR_SCRATCH;
@@ -279,7 +296,7 @@ int sgemm_mx_byte_weight_grad(sgemm_handle_t h, int dtype, int T, int N, int D, 
     return launched();
   }
   float* part = static_cast<float*>(h->workspace);
-  hipLaunchKernelGGL(kGradSplit[half], dim3((unsigned)(tm * tn * p.splits)), dim3(t.threads), 0, stream,
+  hipLaunchKernelGGL(kGradSplit[p.tile - 1][half], dim3((unsigned)(tm * tn * p.splits)), dim3(t.threads), 0, stream,
                      g, tm, tn, band, p.per, part);
   st = launched();
   if (st != SGEMM_OK) return st;

@@ -101,7 +101,7 @@ __device__ __forceinline__ void grad_tile_accumulate(const GradArgs& g, char* ld
   // A lane's pieces of a step lie a whole number of swizzle periods of tokens apart.
   constexpr int A_UPR = T::BM / 8, A_ROWS = T::THREADS / A_UPR;
   constexpr int B_UPR = T::BN / 16, B_ROWS = T::THREADS / B_UPR;
-  static_assert(T::BM >= 128 && T::BN >= 128 && A_ROWS % 4 == 0 && B_ROWS % 4 == 0, "swizzles");
+  static_assert(A_ROWS % 4 == 0 && B_ROWS % 4 == 0, "swizzles repeat every four tokens");
   const int ak = tid / A_UPR, bk = tid / B_UPR, bc = tid % B_UPR;
   int ao = 8 * ((tid % A_UPR) ^ lp_oc_swz<T::BM>(ak));
   if (m0 + ao >= N) ao = N - 8 > m0 ? N - 8 - m0 : 0;
@@ -370,5 +370,6 @@ __global__ void __launch_bounds__(GRAD_SUM_THREADS)
 }
 
 typedef LpTile<128, 128, 64, 64, 2, 2> G128x128;
+typedef LpTile<64, 64, 32, 32, 4, 2> G64x64;
 
 }  // namespace sgemm

@@ -4,7 +4,7 @@
 //     C(m, n) = alpha * sum_k A(m, k) * B(n, k) + beta * C(m, n)
 //
 // for few rows of A, as the 4-bit operands' kernel (mx_small.hpp): a workgroup
-// takes 16 (or 64) columns of C and 16 rows over all of K, its waves take runs of
+// takes 16 to 64 columns of C and 16 (or 32) rows over all of K, its waves take runs of
 // K in super-steps of sixteen blocks and add their results through LDS in wave
 // order.  B is read once; its stream and the launch are what such a call costs.
 //

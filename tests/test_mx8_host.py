@@ -313,3 +313,8 @@ def test_weight_grad_workspace_size():
     assert size(0, 5, 5) == size(100, 5, 5) == size(1000, 0, 5) == 0
     assert size(4096, 11008, 4096) == 0  # tiles enough
     assert size(16384, 100, 200) >= 2 * 4 * 100 * 200
+    # tokens of any number, and sizes at the ends of their ranges
+    for T in (1, 63, 64, 127, 128, 129, 1 << 20, sg.SGEMM_MX_MAX_ROWS):
+        for N, D in ((1, 1), (1, sg.SGEMM_MX_MAX_K), (sg.SGEMM_MX_MAX_ROWS, 1), (300, 200)):
+            parts, rest = divmod(size(T, N, D), 4 * N * -(-D // 4) * 4)
+            assert rest == 0 and (parts == 0 or 2 <= parts <= max(T // 128, 1))

@@ -118,7 +118,7 @@ __device__ __forceinline__ void grad_tile_accumulate(const GradArgs& g, char* ld
   // Whole steps by direct loads: tokens whose last piece of dY (up to the next
   // multiple of eight columns) ends inside the buffer.
   const int over = max((N + 7) & ~7, 8) - N;
-  const int safe = g.T - (over + g.lddy - 1) / g.lddy - k0;
+  const int safe = g.T - (over > 0 ? 1 + (over - 1) / g.lddy : 0) - k0;
   const int kd = max(min(kn, safe), 0) / GRAD_STEP;
 
   const unsigned lds_u = (unsigned)(uintptr_t)(lds_void_t*)lds;

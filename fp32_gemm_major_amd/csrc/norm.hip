@@ -82,11 +82,11 @@ long long back_wgs(const sgemm_handle_s* h, int T, const NormShape& s) {
 
 bool gain_type_ok(int dtype, int gtype) { return gtype == SGEMM_DTYPE_F32 || gtype == dtype; }
 
-// Overlap of an output with an input, or the same window read and written
-// element by element.
-bool bad_overlap(ByteRange out, int ldo, ByteRange in, int ldi, bool may_be_same) {
+// Whether an output of T rows meets an input other than by being its very window,
+// which is read and written element by element.
+bool bad_overlap(ByteRange out, int ldo, ByteRange in, int ldi, int T) {
   if (!ranges_meet(out, in)) return false;
-  return !(may_be_same && out.lo == in.lo && out.hi == in.hi && ldo == ldi);
+  return !(out.lo == in.lo && out.hi == in.hi && (ldo == ldi || T == 1));
 }
 
 int validate_norm(int dtype, int gtype, int T, int D, const void* X, int ldx, const void* R,
@@ -109,7 +109,7 @@ int validate_norm(int dtype, int gtype, int T, int D, const void* X, int ldx, co
   const ByteRange s = byte_range(H, T, D, ldh, esz);
   const ByteRange c = code_range<Mx8Format>(codes, T, D, ldc), b = scale_range(scales, T, D, lds);
   const ByteRange d = byte_range(rstd, 1, T, T, 4);
-  if (bad_overlap(s, ldh, x, ldx, true) || bad_overlap(s, ldh, r, ldr, true))
+  if (bad_overlap(s, ldh, x, ldx, T) || bad_overlap(s, ldh, r, ldr, T))
     return SGEMM_ERR_ALIAS;
   const ByteRange in[3] = {x, r, w}, out[4] = {s, c, b, d};
   for (int i = 0; i < 4; ++i) {
@@ -140,7 +140,7 @@ int validate_back(int dtype, int gtype, int T, int D, const void* dY, int lddy, 
   const ByteRange r = byte_range(dH, T, D, lddh, esz), x = byte_range(dX, T, D, lddx, esz);
   const ByteRange w = byte_range(G, 1, D, D, gsz), d = byte_range(rstd, 1, T, T, 4);
   const ByteRange q = byte_range(dG, 1, D, D, gsz);
-  if (bad_overlap(x, lddx, y, lddy, true) || bad_overlap(x, lddx, r, lddh, true))
+  if (bad_overlap(x, lddx, y, lddy, T) || bad_overlap(x, lddx, r, lddh, T))
     return SGEMM_ERR_ALIAS;
   const ByteRange in[5] = {y, r, s, w, d};
   for (int k = 0; k < 5; ++k)

@@ -261,8 +261,8 @@ __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_mx8_kernel(NormArgs g) {
        base += (size_t)gridDim.x * ROWS, ++turn) {
     const size_t row = base + sub;
     const bool here = row < (size_t)g.T;
-    float ss = 0.0f;
     if constexpr (NV > 0) {
+      float ss = 0.0f;
       // everything that the row needs is asked for first
       Raw8<DT> x[NV], r[NV];
       float w[NV][8], h[NV][8];
@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_mx8_kernel(NormArgs g) {
       }
     } else {
       // (every lane reads again what it read and wrote itself)
+      double total = 0.0;  // (a lane's units may be many)
       auto state = [&](int u, float (&h)[8]) {
         const int n = D - 8 * u;
         const size_t at = n > 0 ? (size_t)8 * u : (size_t)0, k = n > 0 ? row : (size_t)0;
@@ -305,13 +306,15 @@ __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_mx8_kernel(NormArgs g) {
         norm_state<DT>(add, x, r, h);
       };
       for (int u = lane; u < units; u += TPR) {
-        float h[8];
+        float h[8], ss = 0.0f;
         state(u, h);
-        if (H != nullptr && 8 * u < D) store_eight<DT, WHOLE>(H + row * g.ldh + 8 * u, D - 8 * u, h);
+        if (H != nullptr && 8 * u < D)
+          store_eight<DT, WHOLE>(H + row * g.ldh + 8 * u, D - 8 * u, h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(h[i], h[i], ss);
+        total += (double)ss;
       }
-      const RowFactor s = row_factor(row_total<TPR, ROWS>((double)ss, red, turn), g.per_value, g.eps);
+      const RowFactor s = row_factor(row_total<TPR, ROWS>(total, red, turn), g.per_value, g.eps);
       if (lane == 0 && g.rstd != nullptr) g.rstd[row] = s.hi;
       for (int u0 = 0; u0 < units; u0 += TPR) {  // (whole waves: blocks' exchanges)
         const int u = u0 + lane, n = D - 8 * u;
@@ -354,7 +357,8 @@ __device__ __forceinline__ void norm_store_part(float* p, int n, const float (&v
 template <int DT, int TPR, int NV, int ROWS>
 __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_backward_kernel(NormBackArgs g) {
   typedef typename TensorElem<DT>::type E;
-  __shared__ float red[row_total_size<TPR, ROWS>()];
+  typedef typename std::conditional<NV == 0, double, float>::type Sum;  // (of a long row)
+  __shared__ Sum red[row_total_size<TPR, ROWS>()];
   const int lane = ROWS == 1 ? (int)threadIdx.x : (int)threadIdx.x % TPR;
   const int sub = ROWS == 1 ? 0 : (int)threadIdx.x / TPR;
   const int D = g.D;
@@ -466,7 +470,7 @@ __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_backward_kernel(NormBackAr
     for (size_t row = blockIdx.x; row < (size_t)g.T; row += gridDim.x, ++turn) {
       const bool first = row == blockIdx.x;
       const float s = g.rstd[row];
-      float c = 0.0f;
+      double total = 0.0;
       for (int u = lane; 8 * u < D; u += TPR) {
         float n[8], dy[8], w[8], dg[8];
         unpack8<DT>(load_raw8<DT, false>(H + row * g.ldh + 8 * u, D - 8 * u), n);
@@ -474,15 +478,17 @@ __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_backward_kernel(NormBackAr
         load_gain<DT, false>(g.G, g.gdt, (size_t)8 * u, D - 8 * u, w);
         if (part != nullptr && !first)
           load8<SGEMM_DTYPE_F32>(reinterpret_cast<const uint32_t*>(part + 8 * u), D - 8 * u, dg);
+        float part_c = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float v = dy[i] * (n[i] * s);
           dg[i] = first ? v : dg[i] + v;
-          c += 8 * u + i < D ? v * w[i] : 0.0f;
+          part_c += 8 * u + i < D ? v * w[i] : 0.0f;
         }
+        total += (double)part_c;
         if (part != nullptr) norm_store_part(part + 8 * u, D - 8 * u, dg);
       }
-      c = row_total<TPR, ROWS>(c, red, turn) / (float)D;
+      const float c = (float)(row_total<TPR, ROWS>(total, red, turn) / D);
       for (int u = lane; 8 * u < D; u += TPR) {
         float n[8], dy[8], w[8], o[8];
         unpack8<DT>(load_raw8<DT, false>(H + row * g.ldh + 8 * u, D - 8 * u), n);

@@ -537,10 +537,10 @@ int sgemm_mx_byte_dequantize(sgemm_handle_t h, int dtype, int R, int K,
  * other bits.  The matrix instruction adds its products of 8-bit operands in a
  * fixed-point window (see sgemm_run_lowp): beside sgemm_run_mx's bound the
  * result is off by up to 2^-9 * |alpha| * the sum over K's runs of 64 of the
- * largest |a*b| in each, an envelope of measurements (2^-11 was the worst), with
- * unit-normal operands about 2^-15 of the result.  Nothing of it shows in 16-bit
- * results; integers whose runs' products all lie within 2^-11 of one another's
- * size are exact.  The same inputs give the same bits. */
+ * largest |a*b| in each, an envelope of measurements (2^-11 was the worst); with
+ * unit-normal operands, channels ten times as large among them, 2^-15 of the
+ * result, which a 16-bit C's rounding hides.  Small integers with scales near one
+ * another are exact.  The same inputs give the same bits. */
 int sgemm_run_mx_byte(sgemm_handle_t h, int bits, int M, int N, int K,
                       float alpha, const void* A, int lda, const void* SA,
                       int ldsa, const void* B, int ldb, const void* SB,
@@ -571,7 +571,9 @@ int sgemm_run_mx_byte_quant(sgemm_handle_t h, int xtype, int bits, int M, int N,
  * wtype; beta == 0: dW is not read.  X's values are taken in dtype, where they are
  * exact (bfloat16: below 2^-126 they are 0; binary16: inside that type's range), and
  * products are summed in 32 bits: |dW - exact| <= 4*max(T,1)*2^-24*(|alpha|*
- * sum_t|dY*X| + |beta*dW|), plus one rounding to wtype.  T == 0: dW = beta * dW.
+ * sum_t|dY*X| + |beta*dW|), plus one rounding to wtype.  Infinities and NaNs spread
+ * as the formula makes them: a token whose dY is 0 still meets a NaN in X.  T == 0:
+ * dW = beta * dW.
  *
  * Small gradients split the tokens over workgroups, whose partial sums take up to
  * `bytes` of the handle's workspace; with less the split is smaller.  The same

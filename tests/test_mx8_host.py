@@ -99,6 +99,7 @@ def test_validate_norm():
     assert norm(H=X) == sg.SGEMM_OK and norm(H=R) == sg.SGEMM_OK
     assert norm(H=X, ldh=72) == sg.SGEMM_ERR_ALIAS and norm(H=R + 140) == sg.SGEMM_ERR_ALIAS
     assert norm(H=X, R=X) == sg.SGEMM_OK
+    assert norm(H=X, ldh=72, T=1) == sg.SGEMM_OK  # (one row has no stride to speak of)
     last = (3 * 70 + 69) * 2
     for out in ("codes", "scales", "rstd"):
         for p in (X + last, R + last, G + 138, H + last):

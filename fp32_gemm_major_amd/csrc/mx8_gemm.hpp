@@ -18,7 +18,7 @@
 //   is read; the instruction's byte select then picks byte 2 q for group q.
 // * Scale bytes come by direct loads too, sixteen of a row, for four steps, at a time
 //   into two areas in turn: a load of a row's four bytes asks the caches for as many
-//   lines as one of its sixteen (4096 x 11008 x 4096: XXX us, a step's four at a time
+//   lines as one of its sixteen (4096 x 11008 x 4096: 165 us, a step's four at a time
 //   186).  The row's last, partial sixteen go through registers into a third area
 //   before the loop, zeros after them.
 // * A step in which K ends, and K of less than a step, as there.  A's units past

@@ -328,16 +328,16 @@ def sgemm_run_mx_quant(h, xtype, M, N, K, alpha, X, ldx, B, ldb, SB, ldsb, beta,
 
 
 def sgemm_mx_byte_quantize(h, dtype, trans, R, K, X, ldx, codes, ldc, scales, lds,
-                       stream=0) -> int:
+                           stream=0) -> int:
     """Microscaled 8-bit rows of X; X, codes and scales are device addresses."""
     return _check(library().sgemm_mx_byte_quantize(h, dtype, trans, R, K, X, ldx, codes, ldc,
-                                               scales, lds, stream), "sgemm_mx_byte_quantize")
+                                                   scales, lds, stream), "sgemm_mx_byte_quantize")
 
 
 def sgemm_mx_byte_dequantize(h, dtype, R, K, codes, ldc, scales, lds, Y, ldy, stream=0) -> int:
     """The values of microscaled 8-bit rows as a tensor of type ``dtype``."""
     return _check(library().sgemm_mx_byte_dequantize(h, dtype, R, K, codes, ldc, scales, lds, Y,
-                                                 ldy, stream), "sgemm_mx_byte_dequantize")
+                                                     ldy, stream), "sgemm_mx_byte_dequantize")
 
 
 def sgemm_run_mx_byte(h, bits, M, N, K, alpha, A, lda, SA, ldsa, B, ldb, SB, ldsb, beta, dtype, C,
@@ -384,18 +384,18 @@ def sgemm_mx_byte_weight_grad_workspace_size(h, T, N, D) -> int:
 
 
 def sgemm_rmsnorm(h, dtype, gtype, T, D, X, ldx, R, ldr, G, eps, H, ldh, codes, ldc, scales,
-                      lds, rstd, stream=0) -> int:
+                  lds, rstd, stream=0) -> int:
     """Root-mean-square norm of X + R into microscaled 8-bit rows; R, H and
     rstd may be None."""
     return _check(library().sgemm_rmsnorm(h, dtype, gtype, T, D, X, ldx, R, ldr, G, eps, H,
-                                              ldh, codes, ldc, scales, lds, rstd, stream),
+                                          ldh, codes, ldc, scales, lds, rstd, stream),
                   "sgemm_rmsnorm")
 
 
 def sgemm_validate_rmsnorm(dtype, gtype, T, D, X, ldx, R, ldr, G, H, ldh, codes, ldc, scales,
-                               lds, rstd) -> int:
+                           lds, rstd) -> int:
     return library().sgemm_validate_rmsnorm(dtype, gtype, T, D, X, ldx, R, ldr, G, H, ldh,
-                                                codes, ldc, scales, lds, rstd)
+                                            codes, ldc, scales, lds, rstd)
 
 
 def sgemm_rmsnorm_backward(h, dtype, gtype, T, D, dY, lddy, H, ldh, G, rstd, dH, lddh, dX, lddx,

@@ -175,7 +175,8 @@ int validate_grad(int dtype, int T, int N, int D, const void* dY, int lddy, cons
     return SGEMM_ERR_NULL;
   if (!elem_aligned(dW, wsz) || (T > 0 && !elem_aligned(dY, 2))) return SGEMM_ERR_VALUE;
   const ByteRange w = byte_range(dW, N, D, lddw, wsz);
-  if (ranges_meet(w, byte_range(dY, T, N, lddy, 2)) || ranges_meet(w, code_range<Mx8Format>(X, T, D, ldx)) ||
+  if (ranges_meet(w, byte_range(dY, T, N, lddy, 2)) ||
+      ranges_meet(w, code_range<Mx8Format>(X, T, D, ldx)) ||
       ranges_meet(w, scale_range(SX, T, D, ldsx)))
     return SGEMM_ERR_ALIAS;
   // a step's tokens are addressed by 32-bit offsets
@@ -190,13 +191,13 @@ int validate_grad(int dtype, int T, int N, int D, const void* dY, int lddy, cons
 extern "C" {
 
 int sgemm_mx_byte_quantize(sgemm_handle_t h, int dtype, int trans, int R, int K, const void* X,
-                       int ldx, void* codes, int ldc, void* scales, int lds,
-                       hipStream_t stream) {
+                           int ldx, void* codes, int ldc, void* scales, int lds,
+                           hipStream_t stream) {
   return quantize_entry<Mx8Format>(h, dtype, trans, R, K, X, ldx, codes, ldc, scales, lds, stream);
 }
 
 int sgemm_mx_byte_dequantize(sgemm_handle_t h, int dtype, int R, int K, const void* codes, int ldc,
-                         const void* scales, int lds, void* Y, int ldy, hipStream_t stream) {
+                             const void* scales, int lds, void* Y, int ldy, hipStream_t stream) {
   return dequantize_entry<Mx8Format>(h, dtype, R, K, codes, ldc, scales, lds, Y, ldy, stream);
 }
 
@@ -296,8 +297,8 @@ int sgemm_mx_byte_weight_grad(sgemm_handle_t h, int dtype, int T, int N, int D, 
     return launched();
   }
   float* part = static_cast<float*>(h->workspace);
-  hipLaunchKernelGGL(kGradSplit[p.tile - 1][half], dim3((unsigned)(tm * tn * p.splits)), dim3(t.threads), 0, stream,
-                     g, tm, tn, band, p.per, part);
+  hipLaunchKernelGGL(kGradSplit[p.tile - 1][half], dim3((unsigned)(tm * tn * p.splits)),
+                     dim3(t.threads), 0, stream, g, tm, tn, band, p.per, part);
   st = launched();
   if (st != SGEMM_OK) return st;
   const long long quads = up_div(D, 4) * N;

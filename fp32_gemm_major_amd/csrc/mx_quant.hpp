@@ -2,8 +2,8 @@
 //
 // A row of K values is cut into blocks of 32 along K.
 //
-// 4 bits: a block with largest magnitude a holds the byte s = max(floor(log2 a) - 2, -127) + 127 (a = 0:
-// s = 0) and 32 E2M1 codes, code(x) the nearest of 0, 1/2, 1, 3/2, 2, 3, 4, 6
+// 4 bits: a block with largest magnitude a holds the byte s = max(floor(log2 a) - 2,
+// -127) + 127 (a = 0: s = 0) and 32 E2M1 codes, code(x) the nearest of 0, 1/2, 1, 3/2, 2, 3, 4, 6
 // to |x| / 2^(s - 127) (a tie goes to the even code, 6 is the largest) with
 // x's sign.  The "- 2" puts a into [4, 8): the largest element keeps the top
 // binade of E2M1.  A block that holds an infinity or a NaN gets s = 255, which

@@ -159,17 +159,17 @@ int launch_gain(const float* part, int rows, int D, int gtype, void* dG, hipStre
 extern "C" {
 
 int sgemm_validate_rmsnorm(int dtype, int gtype, int T, int D, const void* X, int ldx,
-                               const void* R, int ldr, const void* G, const void* H, int ldh,
-                               const void* codes, int ldc, const void* scales, int lds,
-                               const float* rstd) {
+                           const void* R, int ldr, const void* G, const void* H, int ldh,
+                           const void* codes, int ldc, const void* scales, int lds,
+                           const float* rstd) {
   return validate_norm(dtype, gtype, T, D, X, ldx, R, ldr, G, H, ldh, codes, ldc, scales, lds,
                        rstd);
 }
 
 int sgemm_rmsnorm(sgemm_handle_t h, int dtype, int gtype, int T, int D, const void* X,
-                      int ldx, const void* R, int ldr, const void* G, float eps, void* H,
-                      int ldh, void* codes, int ldc, void* scales, int lds, float* rstd,
-                      hipStream_t stream) {
+                  int ldx, const void* R, int ldr, const void* G, float eps, void* H,
+                  int ldh, void* codes, int ldc, void* scales, int lds, float* rstd,
+                  hipStream_t stream) {
   if (h == nullptr) return SGEMM_ERR_HANDLE;
   int st = validate_norm(dtype, gtype, T, D, X, ldx, R, ldr, G, H, ldh, codes, ldc, scales, lds,
                          rstd);
@@ -182,7 +182,8 @@ int sgemm_rmsnorm(sgemm_handle_t h, int dtype, int gtype, int T, int D, const vo
   const long long all = up_div(T, s.rows), wgs = all < kNormWgs ? all : kNormWgs;
   const NormArgs g = {T, D, X, ldx, R, ldr, G, gtype, eps, 1.0 / D, H, ldh,
                       static_cast<uint8_t*>(codes), ldc, static_cast<uint8_t*>(scales), lds, rstd};
-  hipLaunchKernelGGL(kNorm[D % 8 == 0][dtype][at], dim3((unsigned)wgs), dim3(s.threads), 0, stream, g);
+  hipLaunchKernelGGL(kNorm[D % 8 == 0][dtype][at], dim3((unsigned)wgs), dim3(s.threads), 0, stream,
+                     g);
   return launched();
 }
 

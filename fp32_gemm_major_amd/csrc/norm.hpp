@@ -15,18 +15,17 @@
 // carry their rounding errors into y's own, to odd.  (A code next to a border of its
 // rounding tips over with any error in y: with 32 bits throughout, codes were 5e-5 of
 // their norm off the exact norm's, now none was in 33 million; the rounding to odd costs
-// 0.4 of the 43.3 us of 8192 x 4096.)  h, the
-// codes, dx and dg are each rounded once.
+// 0.4 of the 43.3 us of 8192 x 4096.)  h, the codes, dx and dg are each rounded once.
 //
 // Bound by memory: in one pass over a row, held in registers between the sum and
 // what needs it.  A row takes 64 to 1024 lanes with one unit of eight values each
 // (gradients past 8192 values: four in 512 lanes), so that everything a row needs is
 // asked for at once; rows over 8192 values (gradients: 16384) are read a second time,
-// from the cache that the first one left them in.  A lane's units are the quantiser's, so that a block of 32
-// is four neighbouring lanes and its maximum two exchanges.  The gradients' next row
-// is asked for before this one's is used; dg's sums stay in a lane's registers over
-// all rows that its workgroup takes, and the workgroups' sums are added by a second
-// launch, in their order.
+// from the cache that the first one left them in.  A lane's units are the quantiser's,
+// so that a block of 32 is four neighbouring lanes and its maximum two exchanges.  The
+// gradients' next row is asked for before this one's is used; dg's sums stay in a
+// lane's registers over all rows that its workgroup takes, and the workgroups' sums
+// are added by a second launch, in their order.
 //
 // bfloat16, 8192 x 4096: forward (235 MB with the residual) 43.3 us, 5.4 TB/s;
 // gradients with dg (268 MB) 52.2 us, 5.1 TB/s; a copy of 2 GiB runs at 4.96 TB/s.
@@ -210,12 +209,31 @@ __device__ __forceinline__ void norm_state(bool add, const Raw8<DT>& x, const Ra
   for (int i = 0; i < 8; ++i) v[i] = elem_value<DT>(elem_bits<DT>(v[i] + a[i]));
 }
 
+// The squares of a unit into a sum of 64 bits.  A bfloat16 value's square has sixteen
+// bits, so that eight of them add up in 32 bits with hardly a rounding (all eight in
+// 64 bits: no other code in 33 million, 42.3 us of 8192 x 4096 in place of 40.4);
+// others' would be 2^-28 of the row's factor off, which tips one code in 10^7 (32-bit
+// rows of 16384 x 2048 take 78.7 us either way).
+template <int DT>
+__device__ __forceinline__ void add_squares(const float (&h)[8], double& ss) {
+  if constexpr (DT == SGEMM_DTYPE_BF16) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(h[i], h[i], s);
+    ss += (double)s;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fma((double)h[i], (double)h[i], ss);
+  }
+}
+
 // y of a unit, quantised; a unit's block lies in its quad of lanes, whose units
 // are all inside or all outside of the row's blocks.  (Past a row's end h and the
 // gain are 0; a factor that is no number makes the real values of that block none
 // either.)
-__device__ __forceinline__ void norm_result(const NormArgs& g, size_t row, int u, bool in, RowFactor s,
-                                            const float (&h)[8], const float (&w)[8]) {
+__device__ __forceinline__ void norm_result(const NormArgs& g, size_t row, int u, bool in,
+                                            RowFactor s, const float (&h)[8],
+                                            const float (&w)[8]) {
   float y[8];
   unsigned m = 0u;
 #pragma unroll
@@ -262,7 +280,7 @@ __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_mx8_kernel(NormArgs g) {
     const size_t row = base + sub;
     const bool here = row < (size_t)g.T;
     if constexpr (NV > 0) {
-      float ss = 0.0f;
+      double ss = 0.0;
       // everything that the row needs is asked for first
       Raw8<DT> x[NV], r[NV];
       float w[NV][8], h[NV][8];
@@ -284,10 +302,9 @@ __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_mx8_kernel(NormArgs g) {
         norm_state<DT>(add, x[t], r[t], h[t]);
         if (H != nullptr && here && 8 * u < D)
           store_eight<DT, WHOLE>(H + row * g.ldh + 8 * u, D - 8 * u, h[t]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(h[t][i], h[t][i], ss);
+        add_squares<DT>(h[t], ss);
       }
-      const RowFactor s = row_factor(row_total<TPR, ROWS>((double)ss, red, turn), g.per_value, g.eps);
+      const RowFactor s = row_factor(row_total<TPR, ROWS>(ss, red, turn), g.per_value, g.eps);
       if (lane == 0 && here && g.rstd != nullptr) g.rstd[row] = s.hi;
 #pragma unroll
       for (int t = 0; t < NV; ++t) {
@@ -296,7 +313,7 @@ __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_mx8_kernel(NormArgs g) {
       }
     } else {
       // (every lane reads again what it read and wrote itself)
-      double total = 0.0;  // (a lane's units may be many)
+      double ss = 0.0;
       auto state = [&](int u, float (&h)[8]) {
         const int n = D - 8 * u;
         const size_t at = n > 0 ? (size_t)8 * u : (size_t)0, k = n > 0 ? row : (size_t)0;
@@ -306,15 +323,13 @@ __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_mx8_kernel(NormArgs g) {
         norm_state<DT>(add, x, r, h);
       };
       for (int u = lane; u < units; u += TPR) {
-        float h[8], ss = 0.0f;
+        float h[8];
         state(u, h);
         if (H != nullptr && 8 * u < D)
           store_eight<DT, WHOLE>(H + row * g.ldh + 8 * u, D - 8 * u, h);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(h[i], h[i], ss);
-        total += (double)ss;
+        add_squares<DT>(h, ss);
       }
-      const RowFactor s = row_factor(row_total<TPR, ROWS>(total, red, turn), g.per_value, g.eps);
+      const RowFactor s = row_factor(row_total<TPR, ROWS>(ss, red, turn), g.per_value, g.eps);
       if (lane == 0 && g.rstd != nullptr) g.rstd[row] = s.hi;
       for (int u0 = 0; u0 < units; u0 += TPR) {  // (whole waves: blocks' exchanges)
         const int u = u0 + lane, n = D - 8 * u;

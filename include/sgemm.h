@@ -526,11 +526,11 @@ int sgemm_run_mx_quant(sgemm_handle_t h, int xtype, int M, int N, int K,
  * at least 31/32 of the power of two past its type's largest value (binary16:
  * 63488) rounds to that power, which the type reads back as an infinity. */
 int sgemm_mx_byte_quantize(sgemm_handle_t h, int dtype, int trans, int R, int K,
-                       const void* X, int ldx, void* codes, int ldc,
-                       void* scales, int lds, hipStream_t stream);
+                           const void* X, int ldx, void* codes, int ldc,
+                           void* scales, int lds, hipStream_t stream);
 int sgemm_mx_byte_dequantize(sgemm_handle_t h, int dtype, int R, int K,
-                         const void* codes, int ldc, const void* scales,
-                         int lds, void* Y, int ldy, hipStream_t stream);
+                             const void* codes, int ldc, const void* scales,
+                             int lds, void* Y, int ldy, hipStream_t stream);
 
 /* C(m,n) = alpha * sum_k A(m,k)*B(n,k) + beta*C(m,n) as sgemm_run_mx, with A in
  * 8-bit rows and B in 8-bit (bits 8) or 4-bit (bits 4) ones; SGEMM_ERR_VALUE for
@@ -603,17 +603,19 @@ int sgemm_validate_mx_byte_weight_grad(int dtype, int T, int N, int D,
  * microscaled 8-bit rows, quantised from 32 bits, and rstd (unless NULL) as T
  * floats for the gradients.  Arithmetic is 32-bit.  H may be X or R itself
  * (address and stride); else outputs must not overlap anything
- * (SGEMM_ERR_ALIAS).  A row with an infinity has rstd 0, one with a NaN NaN.
+ * (SGEMM_ERR_ALIAS).  A row with an infinity has rstd 0 and so has a bfloat16 one
+ * in which the squares of eight neighbours add up past 32 bits' range (values over
+ * 6e18); one with a NaN, NaN.
  *
  * Ownership, streams, errors and threading as for sgemm_run (with a workspace:
  * the gradients).  T == 0: nothing is read.  SGEMM_ERR_SIZE for T < 0 or over
  * SGEMM_MX_MAX_ROWS and D < 1 or over SGEMM_MX_MAX_K; SGEMM_ERR_VALUE for another
  * type or a tensor not aligned to its element. */
 int sgemm_rmsnorm(sgemm_handle_t h, int dtype, int gtype, int T, int D,
-                      const void* X, int ldx, const void* R, int ldr,
-                      const void* G, float eps, void* H, int ldh, void* codes,
-                      int ldc, void* scales, int lds, float* rstd,
-                      hipStream_t stream);
+                  const void* X, int ldx, const void* R, int ldr,
+                  const void* G, float eps, void* H, int ldh, void* codes,
+                  int ldc, void* scales, int lds, float* rstd,
+                  hipStream_t stream);
 
 /* Gradients: from that of y (dY, the rounding to 8 bits counting as none) and,
  * unless NULL, of H from elsewhere (dH), with n = h * rstd,
@@ -636,10 +638,10 @@ int sgemm_rmsnorm_workspace_size(sgemm_handle_t h, int T, int D, size_t* least,
 
 /* The argument checks of the two, without a device. */
 int sgemm_validate_rmsnorm(int dtype, int gtype, int T, int D, const void* X,
-                               int ldx, const void* R, int ldr, const void* G,
-                               const void* H, int ldh, const void* codes,
-                               int ldc, const void* scales, int lds,
-                               const float* rstd);
+                           int ldx, const void* R, int ldr, const void* G,
+                           const void* H, int ldh, const void* codes,
+                           int ldc, const void* scales, int lds,
+                           const float* rstd);
 int sgemm_validate_rmsnorm_backward(int dtype, int gtype, int T, int D,
                                     const void* dY, int lddy, const void* H,
                                     int ldh, const void* G, const float* rstd,

@@ -127,23 +127,43 @@ def test_norm_special_rows(handle, D):
     x[2, D // 2] = float("inf")
     x[3, D - 1] = float("nan")
     x[4] = 2.0 ** -140
-    x[5] = 3e38  # (its square leaves 32 bits: rstd 0)
+    x[5] = 3e38  # (its square leaves 32 bits; its rstd is a subnormal of 2^-149's steps)
     X, G = x.cuda(), torch.full((D,), 0.5, device="cuda")
     rstd = torch.empty(8, device="cuda")
     q = handle.rmsnorm_mx8(X, G, rstd=rstd, eps=EPS)
     s = rstd.cpu()
     assert abs(float(s[1]) * EPS ** 0.5 - 1) < 1e-6 and float(s[2]) == 0 and torch.isnan(s[3])
-    assert float(s[5]) == 0
+    assert abs(float(s[5]) * 3e38 - 1) < 2.0 ** -21
     y = handle.mx8_dequantize(q, torch.empty(8, D, device="cuda")).cpu()
     block = slice(D // 2 // 32 * 32, min(D, D // 2 // 32 * 32 + 32))
-    assert (y[1] == 0).all() and (y[5] == 0).all() and torch.isnan(y[3]).all()
+    assert (y[1] == 0).all() and torch.isnan(y[3]).all()
     assert torch.isnan(y[2, block]).all() and torch.nan_to_num(y[2]).abs().sum() == 0
     keep = [0, 4, 6, 7]
     want, _ = ref.norm(x[keep].double().numpy(), np.full(D, 0.5), EPS)
     check_rows(sg.Mx8(q.codes[keep], q.scales[keep]), want, delta(D))
+    check_rows(sg.Mx8(q.codes[5:6], q.scales[5:6]), np.full((1, D), 0.5), 2.0 ** -21)
+    # bfloat16's squares are added in 32 bits, eight at a time
+    q = handle.rmsnorm_mx8(torch.full((1, D), 1e19, device="cuda").bfloat16(), G, rstd=rstd[:1])
+    assert float(rstd[0]) == 0 and not q.codes.any()
     # eps 0: a row of zeros is 0 * inf
     q = handle.rmsnorm_mx8(X[:2], G, eps=0.0)
     assert (q.scales[1] == 255).all() and not (q.scales[0] == 255).any()
+
+
+@pytest.mark.parametrize("T,D,dt", [(600, 1501, "f32"), (400, 2000, "f16"), (300, 4096, "f32"),
+                                    (30, 20000, "f32")])
+def test_codes_of_the_exact_norm(handle, T, D, dt):
+    """Of 32-bit and binary16 rows every code is that of the norm in 64 bits: the
+    factor and what the rounding of y leaves are kept to 2^-40 at least, and of a
+    million values 1e6 * 8 / log(2) * 2 * 2^-40 = 2e-5 lie that near to a border of the
+    codes' rounding, eight of which there are in a binade."""
+    x, r, G = rows(T, D, 11, dt).cuda(), rows(T, D, 12, dt).cuda(), rows(1, D, 13, dt)[0].cuda()
+    eps = float(np.float32(EPS))
+    q = handle.rmsnorm_mx8(x, G, residual=r, eps=eps)
+    f = lambda t: t.double().cpu().numpy()  # noqa: E731
+    want, _ = ref.norm(f((x.float() + r.float()).to(x.dtype)), f(G), eps)
+    for got, exact in zip(as_numpy(q), ref.quantize(want)):
+        assert np.array_equal(got, exact)
 
 
 def check_gradients(dx, dg, dy, h, g, rstd, dh, dt, gt, T, D):

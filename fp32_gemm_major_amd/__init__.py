@@ -659,15 +659,16 @@ class _MxRows:
     CODE_BYTES = 0
 
     def __init__(self, codes, scales):
-        for name, t in (("codes", codes), ("scales", scales)):
-            if t.dtype != torch.uint8 or t.dim() != 2:
+        shape, shape_s = codes.shape, scales.shape
+        for name, t, n in (("codes", codes, shape), ("scales", scales, shape_s)):
+            if t.dtype != torch.uint8 or len(n) != 2:
                 raise TypeError(f"{name} must be a 2-D uint8 tensor")
-        (rows, width), (rows_s, nb) = codes.shape, scales.shape
+        (rows, width), (rows_s, nb) = shape, shape_s
         if rows != rows_s or width != self.CODE_BYTES * nb:
-            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} "
+            raise ValueError(f"codes {tuple(shape)} and scales {tuple(shape_s)} "
                              f"disagree: {self.CODE_BYTES} code bytes and a scale byte a block")
         self.codes, self.scales, self.rows, self.K = codes, scales, rows, SGEMM_MX_BLOCK * nb
-        self._ldc, self._lds = _row_stride("codes", codes), _row_stride("scales", scales)
+        self._ldc, self._lds = _row_stride("codes", codes, shape), _row_stride("scales", scales, shape_s)
 
     @classmethod
     def empty(cls, rows: int, K: int, device="cuda"):
@@ -699,10 +700,10 @@ class Mx8(_MxRows):
     CODE_BYTES = 32
 
 
-def _row_stride(name, t) -> int:
+def _row_stride(name, t, shape=None) -> int:
     """Leading dimension of a 2-D row-major tensor (its rows may be strided,
-    but must not overlap)."""
-    rows, cols = t.shape
+    but must not overlap); ``shape``: its shape, where that is known."""
+    rows, cols = t.shape if shape is None else shape
     if 0 < cols <= INT_MAX and rows <= INT_MAX and t.is_contiguous():
         return cols
     ld, step = t.stride()
@@ -724,10 +725,15 @@ def _row_stride(name, t) -> int:
 def _matrix(name, t):
     """A 2-D row-major float32, bfloat16 or float16 tensor: its library type
     and leading dimension."""
-    dtype = TENSOR_DTYPES.get(t.dtype)
-    if dtype is None or t.dim() != 2:
+    return _rows(name, t)[:2]
+
+
+def _rows(name, t):
+    """``_matrix`` and the shape."""
+    dtype, shape = TENSOR_DTYPES.get(t.dtype), t.shape
+    if dtype is None or len(shape) != 2:
         raise TypeError(f"{name} must be a 2-D float32, bfloat16 or float16 tensor")
-    return dtype, _row_stride(name, t)
+    return dtype, _row_stride(name, t, shape), shape
 
 
 class Handle:
@@ -910,8 +916,7 @@ class Handle:
         return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
     def _mx_quantize(self, kind, call, X, trans, out, stream):
-        dtype, ldx = _matrix("X", X)
-        R, K = X.shape
+        dtype, ldx, (R, K) = _rows("X", X)
         if trans:
             R, K = K, R
         out = self._mx_out(kind, R, K, out, stream)
@@ -942,8 +947,7 @@ class Handle:
     def _mx_dequantize(self, kind, call, Q, out, stream):
         if not isinstance(Q, kind):
             raise TypeError(f"Q must be an {kind.__name__}")
-        dtype, ldy = _matrix("out", out)
-        R, K = out.shape
+        dtype, ldy, (R, K) = _rows("out", out)
         if R != Q.rows or K > Q.K:
             raise ValueError(f"out is {tuple(out.shape)}, Q holds {Q.rows} rows of {Q.K} values")
         codes, scales = Q.codes, Q.scales
@@ -979,10 +983,12 @@ class Handle:
                                 C, alpha, beta, stream)
 
     def _mx_product(self, kind, call, call_quant, bits, A, B, C, alpha, beta, stream):
-        dtype, ldc = _matrix("C", C)
-        M, N = C.shape
+        dtype, ldc, (M, N) = _rows("C", C)
         quantised = isinstance(A, kind)
-        rows, K = (A.rows, A.K) if quantised else A.shape
+        if quantised:
+            rows, K = A.rows, A.K
+        else:
+            xtype, lda, (rows, K) = _rows("A", A)
         if rows != M or B.rows != N or SGEMM_MX_BLOCK * -(-K // SGEMM_MX_BLOCK) != B.K:
             raise ValueError(f"A {rows} x {K} and B {B.rows} x {B.K} do not give "
                              f"{M} x {N}")
@@ -994,7 +1000,6 @@ class Handle:
                       codes.data_ptr(), B._ldc, scales.data_ptr(), B._lds, beta, dtype,
                       C.data_ptr(), ldc, s)
         else:
-            xtype, lda = _matrix("A", A)
             call = call_quant
             s = self._ready(stream, "A B B_scales C", A, codes, scales, C)
             st = call(self.h, xtype, *bits, M, N, K, alpha, A.data_ptr(), lda, codes.data_ptr(),
@@ -1039,9 +1044,8 @@ class Handle:
         weight (N x D, float32, bfloat16 or float16) from that of its result
         (``dY``, T x N, bfloat16 or float16) and its activations kept as an
         ``Mx8`` of T rows (D may end inside its last block)."""
-        dtype, lddy = _matrix("dY", dY)
-        wtype, lddw = _matrix("dW", dW)
-        (T, N), (rows, D) = dY.shape, dW.shape
+        dtype, lddy, (T, N) = _rows("dY", dY)
+        wtype, lddw, (rows, D) = _rows("dW", dW)
         if not isinstance(X, Mx8):
             raise TypeError("X must be an Mx8")
         if dtype == SGEMM_DTYPE_F32:
@@ -1050,10 +1054,12 @@ class Handle:
             raise ValueError(f"dY {T} x {N} and X {X.rows} x {X.K} do not give {rows} x {D}")
         codes, scales = X.codes, X.scales
         s = self._ready(stream, "dY X X_scales dW", dY, codes, scales, dW)
-        return _check(self._lib.sgemm_mx_byte_weight_grad(
+        st = self._lib.sgemm_mx_byte_weight_grad(
             self.h, dtype, T, N, D, alpha, dY.data_ptr(), lddy, codes.data_ptr(), X._ldc,
-            scales.data_ptr(), X._lds, beta, wtype, dW.data_ptr(), lddw, s),
-            "sgemm_mx_byte_weight_grad")
+            scales.data_ptr(), X._lds, beta, wtype, dW.data_ptr(), lddw, s)
+        if st < 0:
+            raise SgemmError(st, "sgemm_mx_byte_weight_grad")
+        return st
 
     # -- root-mean-square norm --
 
@@ -1066,9 +1072,8 @@ class Handle:
         D values of that type or float32.  ``H`` receives h and may be X or
         ``residual`` itself; ``rstd`` (T float32) the rows' factors, for
         ``rmsnorm_backward``."""
-        dtype, ldx = _matrix("X", X)
-        shape, kind = X.shape, X.dtype
-        T, D = shape
+        dtype, ldx, shape = _rows("X", X)
+        kind, (T, D) = X.dtype, shape
         gtype = _gain(G, kind, D)
         r = h = p = None
         ldr = ldh = 0
@@ -1099,9 +1104,8 @@ class Handle:
         of its G into dG, from that of its result (``dY``) and, if given, of H
         from elsewhere (``dH``).  H and ``rstd`` are the forward call's (X where
         it had no H).  dX may be dY or dH itself; dG is of G's type."""
-        dtype, ldh = _matrix("H", H)
-        shape, kind = H.shape, H.dtype
-        T, D = shape
+        dtype, ldh, shape = _rows("H", H)
+        kind, (T, D) = H.dtype, shape
         gtype = _gain(G, kind, D)
         p = _vector("rstd", rstd, T, torch.float32)
         y, lddy = _same("dY", dY, kind, shape)
@@ -1179,7 +1183,7 @@ def _same(name, t, dtype, shape):
     """Address and leading dimension of a matrix of other rows' type and shape."""
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)} of type {dtype}, as the other rows")
-    return t.data_ptr(), _row_stride(name, t)
+    return t.data_ptr(), _row_stride(name, t, shape)
 
 
 def _ce_shapes(X, W):
@@ -1198,11 +1202,11 @@ def _vectors(n, dtype, **tensors):
 
 def _vector(name, t, n, dtype):
     """Address of a tensor of n contiguous elements."""
+    if t.dtype == dtype and t.shape == (n,) and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype or t.dim() != 1:
         raise TypeError(f"{name} must be a 1-D {dtype} tensor")
-    if t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be {n} contiguous elements")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be {n} contiguous elements")
 
 
 def _span(rows, cols, ld):

@@ -49,7 +49,8 @@ def check(got, dy, x, alpha, beta, w, dt, what=""):
 SIZES = [(1, 1, 1), (1, 300, 200), (2, 1, 40), (9, 3, 33), (63, 7, 31), (64, 8, 32), (65, 9, 64),
          (128, 128, 128), (200, 129, 1000), (777, 130, 100), (1000, 1, 16), (1000, 5, 300),
          (1100, 250, 130), (4096, 40, 70), (5000, 300, 600), (300, 1500, 1000), (64, 2900, 3050),
-         (130, 3500, 3600), (193, 3600, 3501), (1, 3600, 3600)]
+         (130, 3500, 3600), (193, 3600, 3501), (1, 3600, 3600), (330, 3500, 3600), (384, 3600, 3501),
+         (450, 3500, 3600)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16"])

@@ -42,11 +42,16 @@ const MxTileDesc kTiles[2][3] = {
 // which there is one on every CU at most, or four: a CU's stream of B is what takes
 // its time, so a second round of workgroups would double it (16 x 11008 x 4096, 8 and 4
 // bits: 12.2 and 9.1 us with three tiles, with two 17.4 and 12.3, with four 13.5 and
-// 10.0; 16 x 4096 x 4096 8.4 and 6.4 with one, 9.1 and 7.0 with two).
+// 10.0; 16 x 4096 x 4096 8.4 and 6.4 with one, 9.1 and 7.0 with two).  Where that is
+// four and K keeps half of a workgroup's waves busy at most, two tiles of 4-bit B, which
+// leave a CU the registers for two workgroups (1 x 50000 x 2048: 18.7 us, with four 23.9;
+// 16 x 131072 x 512 28.9, 33.3; but 16 x 32000 x 4096 22.7, 21.1).  8-bit B's would
+// gain where workgroups of four leave the last round half empty and lose elsewhere.
 int launch_small(const sgemm_handle_s* h, int bits, int xdt, const MxArgs& g,
                  hipStream_t stream) {
   int tiles = 1;
   while (tiles < 4 && up_div(g.N, MXS_TILE * tiles) > h->cus) ++tiles;
+  if (tiles == 4 && bits == 4 && g.K <= MXS_WAVES / 2 * MXS_STEP * MX_BLOCK) tiles = 2;
   return launch_small_grid(kSmall[bits == 4][1 + xdt][tiles - 1], tiles, g, stream);
 }
 

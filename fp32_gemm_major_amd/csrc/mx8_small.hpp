@@ -20,7 +20,10 @@
 // channels ten times as large, K = 4096, 3e-5 of the result's norm.
 //
 // A may be 16- or 32-bit activations of at most MXS_FEW rows (XDT), quantised as
-// they are read by every workgroup for itself, a block a lane.
+// they are read by every workgroup for itself, a block a lane.  (For up to 16 rows that
+// is four blocks a lane, which costs as much as a launch of its own or more: 16 x 11008
+// x 4096 16.8 us, with a launch 17.1; 5 x 4096 x 11008 19.3, 17.3; 5 x 32000 x 4096
+// 43.9, 33.8.)
 #pragma once
 
 #include "mx_small.hpp"
@@ -75,41 +78,49 @@ __device__ __forceinline__ void mx8_load_run(const uint8_t* row, const uint8_t* 
 // Up to MXS_FEW rows of activations: lane l quantises block l / 4 of row l % 4 of
 // the super-step and the wave exchanges them through `codes` and `scales`.
 template <int XDT>
-__device__ __forceinline__ void mx8_quant_few(const typename TensorElem<XDT>::type* A, int lda,
-                                              int M, int s, int lane, int K, u32x4* codes,
-                                              unsigned* scales, Mx8Run& r) {
-  const int row = lane % MXS_FEW, k0 = MX_BLOCK * (s * MXS_STEP + lane / MXS_FEW);
-  const bool in = row < M && k0 < K;
-  const typename TensorElem<XDT>::type* p = A + (size_t)(row < M ? row : 0) * lda;
-  float v[4][8];
-  unsigned m = 0u;
+struct Mx8Few {
+  Raw8<XDT> raw[4];
+
+  __device__ __forceinline__ void load(const typename TensorElem<XDT>::type* A, int lda, int M,
+                                       int s, int lane, int K) {
+    const int row = lane % MXS_FEW, k0 = MX_BLOCK * (s * MXS_STEP + lane / MXS_FEW);
+    const bool in = row < M && k0 < K;
+    const typename TensorElem<XDT>::type* p = A + (size_t)(row < M ? row : 0) * lda;
 #pragma unroll
-  for (int h = 0; h < 4; ++h) load8<XDT>(p + (in ? k0 + 8 * h : 0), in ? K - k0 - 8 * h : 0, v[h]);
-#pragma unroll
-  for (int h = 0; h < 4; ++h)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, mx_abs_bits(v[h][i]));
-  const unsigned sc = mx8_scale_of(m);
-  v2u c[4];
-#pragma unroll
-  for (int h = 0; h < 4; ++h) c[h] = mx8_codes8(v[h], sc);
-  __builtin_amdgcn_wave_barrier();  // (the last super-step's have been read)
-  codes[2 * lane] = u32x4{c[0][0], c[0][1], c[1][0], c[1][1]};
-  codes[2 * lane + 1] = u32x4{c[2][0], c[2][1], c[3][0], c[3][1]};
-  scales[lane] = sc;
-  __builtin_amdgcn_wave_barrier();
-  const int i = lane & 15, g = lane >> 4;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int block = 4 * j + 2 * q + (g >> 1);
-      const u32x4 x = codes[2 * (block * MXS_FEW + i % MXS_FEW) + (g & 1)];
-      r.codes[j][q] = i < MXS_FEW ? x : u32x4{0u, 0u, 0u, 0u};
-    }
-    r.scale[j] = i < MXS_FEW ? scales[(4 * j + g) * MXS_FEW + i % MXS_FEW] : 0u;
+    for (int h = 0; h < 4; ++h)
+      raw[h] = load_raw8<XDT, false>(p + (in ? k0 + 8 * h : 0), in ? K - k0 - 8 * h : 0);
   }
-}
+  __device__ __forceinline__ void quantize(int lane, u32x4* codes, unsigned* scales, Mx8Run& r) {
+    float v[4][8];
+    unsigned m = 0u;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      unpack8<XDT>(raw[h], v[h]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, mx_abs_bits(v[h][i]));
+    }
+    const unsigned sc = mx8_scale_of(m);
+    v2u c[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) c[h] = mx8_codes8(v[h], sc);
+    __builtin_amdgcn_wave_barrier();  // (the last super-step's have been read)
+    codes[2 * lane] = u32x4{c[0][0], c[0][1], c[1][0], c[1][1]};
+    codes[2 * lane + 1] = u32x4{c[2][0], c[2][1], c[3][0], c[3][1]};
+    scales[lane] = sc;
+    __builtin_amdgcn_wave_barrier();
+    const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int block = 4 * j + 2 * q + (g >> 1);
+        const u32x4 x = codes[2 * (block * MXS_FEW + i % MXS_FEW) + (g & 1)];
+        r.codes[j][q] = i < MXS_FEW ? x : u32x4{0u, 0u, 0u, 0u};
+      }
+      r.scale[j] = i < MXS_FEW ? scales[(4 * j + g) * MXS_FEW + i % MXS_FEW] : 0u;
+    }
+  }
+};
 
 __device__ __forceinline__ i32x8 mx8_operand(const u32x4 (&c)[2]) {
   return i32x8{(int)c[0][0], (int)c[0][1], (int)c[0][2], (int)c[0][3],
@@ -141,6 +152,13 @@ __global__ void __launch_bounds__(MXS_THREADS) mx8_small_kernel(MxArgs g) {
   for (int s = s0; s < s1; ++s) {
     typename std::conditional<WB == 8, Mx8Run, MxRun>::type b[NT];
     Mx8Run a[MT];
+    // (loads return in order: activations, asked for first, are quantised while B's
+    // stream comes in; 1 x 4096 x 11008 in 13.0 us, asked for after B in 16.2)
+    Mx8Few<FEW ? XDT : 0> few;
+    if constexpr (FEW) {
+      few.load(static_cast<const typename TensorElem<XDT>::type*>(g.A), g.lda, g.M, s, lane, g.K);
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int n = n0 + MXS_TILE * t + i;
@@ -150,7 +168,10 @@ __global__ void __launch_bounds__(MXS_THREADS) mx8_small_kernel(MxArgs g) {
       else
         mx_load_run(g.B + r * g.ldb, g.SB + r * g.ldsb, n < g.N, s, q, nb, b[t]);
     }
-    if constexpr (!FEW) {
+    if constexpr (FEW) {
+      __builtin_amdgcn_sched_barrier(0);
+      few.quantize(lane, few_codes + wave * 128, few_scales + wave * 64, a[0]);
+    } else {
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         const int m = m0 + MXS_TILE * t + i;
@@ -158,10 +179,6 @@ __global__ void __launch_bounds__(MXS_THREADS) mx8_small_kernel(MxArgs g) {
         mx8_load_run(static_cast<const uint8_t*>(g.A) + r * g.lda, g.SA + r * g.ldsa, m < g.M, s, q,
                      nb, a[t]);
       }
-    } else {
-      typedef typename TensorElem<XDT < 0 ? 0 : XDT>::type E;
-      mx8_quant_few<XDT < 0 ? 0 : XDT>(static_cast<const E*>(g.A), g.lda, g.M, s, lane, g.K,
-                                       few_codes + wave * 128, few_scales + wave * 64, a[0]);
     }
 #pragma unroll
     for (int t = 0; t < MT * NT; ++t)

@@ -131,6 +131,48 @@ __device__ __forceinline__ unsigned quad_swap2(unsigned v) {
   return (unsigned)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xf, 0xf, true);
 }
 
+// Eight elements as they stand in memory, to be asked for before they are used;
+// only the first n are read (n may be <= 0), the others are zero.  WHOLE: n is at
+// least eight or not over 0.
+template <int DT>
+struct Raw8 {
+  v4u b[DT == SGEMM_DTYPE_F32 ? 2 : 1];
+};
+template <int DT, bool WHOLE>
+__device__ __forceinline__ Raw8<DT> load_raw8(const typename TensorElem<DT>::type* p, int n) {
+  Raw8<DT> r;
+  constexpr int W = DT == SGEMM_DTYPE_F32 ? 2 : 1, PER = 8 / W;
+#pragma unroll
+  for (int w = 0; w < W; ++w) r.b[w] = v4u{0u, 0u, 0u, 0u};
+  if (WHOLE ? n > 0 : n >= 8) {
+#pragma unroll
+    for (int w = 0; w < W; ++w) r.b[w] = *reinterpret_cast<const v4u_any*>(p + PER * w);
+    return r;
+  }
+  if (WHOLE || n <= 0) return r;
+  typename TensorElem<DT>::type e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = p[i < n ? i : n - 1];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const unsigned v = i < n ? e[i] : 0u;
+    if constexpr (W == 2)
+      r.b[i / 4][i % 4] = v;
+    else
+      r.b[0][i / 2] |= i % 2 ? v << 16 : v;
+  }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void unpack8(const Raw8<DT>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if constexpr (DT == SGEMM_DTYPE_F32)
+      v[i] = __uint_as_float(r.b[i / 4][i % 4]);
+    else
+      v[i] = elem_value<DT>((uint16_t)(i % 2 ? r.b[0][i / 2] >> 16 : r.b[0][i / 2] & 0xffffu));
+}
+
 struct MxQuantArgs {
   int R, K;
   const void* X;

@@ -61,7 +61,7 @@ PRODUCTS = [(1, 1, 32), (1, 16, 64), (1, 4096, 4096), (2, 17, 96), (4, 100, 512)
             (17, 40, 544), (33, 65, 32), (64, 64, 256), (100, 128, 1056), (128, 256, 800),
             (200, 300, 160), (256, 512, 512), (257, 511, 288), (1000, 1500, 800), (300, 5000, 96),
             (700, 900, 64), (700, 900, 32), (700, 900, 128), (700, 900, 352),
-            (700, 900, 1056), (640, 832, 2048), (650, 840, 1632), (300, 70, 2048), (40, 500, 5000 // 32 * 32),
+            (5, 16500, 544), (16, 13000, 2112), (700, 900, 1056), (640, 832, 2048), (650, 840, 1632), (300, 70, 2048), (40, 500, 5000 // 32 * 32),
             # enough tiles for the 128-square and the 256-square ones, K of less
             # than a step, of whole steps (odd and even counts) and ragged
             (2050, 2100, 64), (2050, 2100, 128), (2048, 2176, 1024), (2050, 2100, 1312),
@@ -117,7 +117,7 @@ def test_integer_products_are_exact(handle, M, N, K, bits):
 @pytest.mark.parametrize("dt", list(DTYPES))
 @pytest.mark.parametrize("M,N,K", [(1, 100, 33), (1, 4096, 4096), (2, 40, 1), (3, 70, 5000), (4, 33, 8192),
                                    (4, 9000, 100), (5, 90, 512), (7, 64, 777), (16, 50, 1024), (17, 64, 100),
-                                   (40, 200, 4090), (300, 260, 520)])
+                                   (40, 200, 4090), (300, 260, 520), (2, 17000, 1000), (3, 13000, 2100)])
 def test_product_of_activations(handle, M, N, K, dt, bits):
     x = torch.from_numpy(values(M, K, M + K, spread=2)).to(DTYPES[dt])
     X, _ = strided(x, 7, fill=float("nan"))

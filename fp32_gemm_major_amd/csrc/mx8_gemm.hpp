@@ -20,16 +20,21 @@
 //   into two areas in turn: a load of a row's four bytes asks the caches for as many
 //   lines as one of its sixteen (4096 x 11008 x 4096: 165 us, a step's four at a time
 //   186).  The row's last, partial sixteen go through registers into a third area
-//   before the loop, zeros after them.
-// * A step in which K ends, and K of less than a step, as there.  A's units past
-//   the end are zeroed as they come out of LDS; B's repeat the row's last unit (a
-//   NaN among its codes is in the row's result anyway).
+//   before the loop, zeros after them: dwords, asked for before the tile's own loads
+//   (byte by byte after them, 4096 x 11008 x 1152 took 64 us in place of 57).
+// * The step in which K ends loads the row's last unit in the place of those past the
+//   end; A's are zeroed at their use (a NaN among B's repeated codes is in the row's
+//   result anyway).  It is a step of the pipeline as the others (on its own after them,
+//   4096 x 11008 x 1056 took 71 us in place of 64 and K of less than a step 50 in place
+//   of 30), but a copy of the code: the choice in each step spills registers.
 #pragma once
 
 #include "mx8_small.hpp"
 #include "mx_gemm.hpp"
 
 namespace sgemm {
+
+typedef unsigned __attribute__((aligned(1), may_alias)) dword_any;
 
 template <int BM_, int BN_, int WM_, int WN_, int OCC_, int S_, int WB_>
 struct Mx8Tile {
@@ -105,28 +110,16 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
   }
   const int sixteens = nb / 16;  // whole ones of a row
 
-  // With no whole step the loop still runs once, on stages and scales of zeros (see
-  // the 4-bit operands' kernel): its loads all read the same bytes of A, which nothing
-  // uses.
-  if (kd == 0) {
-#pragma unroll
-    for (int v = 0; v < T::A_VEC; ++v) a_voff[v] = 0u;
-#pragma unroll
-    for (int v = 0; v < T::B_VEC; ++v) b_voff[v] = 0u;
-  }
-  const uint8_t* B_loads = kd == 0 ? A : B;
-  const int steps = max(kd, 1);
-  // The partial step, loaded as step `steps` when there is one: its blocks, and
-  // how far a lane's unit lies past the row's last one (the same in all the
-  // lane's loads of an operand).
-  const int rest = kd > 0 ? nb - 4 * kd : 0;
-  const int loads = rest > 0 ? steps + 1 : steps;
+  // The step in which K ends is step kd, when there is one: its blocks, and how far a
+  // lane's unit lies past the row's last one (the same in all the lane's loads of an
+  // operand).
+  const int rest = nb - 4 * kd, steps = kd + (rest > 0);
   auto past = [&](int units, int have) {
     const int c = (lane & (units - 1)) ^ ((((wave * 64 + lane) / units) >> 1) & (units - 1));
     return rest > 0 ? 16u * (unsigned)max(c - (have - 1), 0) : 0u;
   };
   const unsigned a_back = past(8, 2 * rest);
-  const unsigned b_back = past(T::B_UNITS, T::B_FU * rest);
+  const unsigned b_back = T::WB == 8 ? a_back : past(T::B_UNITS, T::B_FU * rest);
 
   constexpr int ND = T::A_VEC + T::B_VEC;
   const unsigned lds_u = (unsigned)(uintptr_t)(lds_void_t*)lds;
@@ -135,7 +128,7 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
   // the choices that the others take.
   auto load_one = [&](auto hot_c, int kt, int st, int d, bool live) {
     constexpr bool HOT = decltype(hot_c)::value;
-    const bool part = !HOT && kt == steps;
+    const bool part = !HOT && kt == kd;
     const bool of_a = d < T::A_VEC;
     const int v = of_a ? d : d - T::A_VEC;
     const unsigned to = lds_u + (unsigned)(of_a ? a_at(st) : b_at(st)) +
@@ -145,7 +138,7 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
       dma16(reinterpret_cast<const float*>(A + (size_t)kt * 128), a_voff[v] - (part ? a_back : 0u),
             at);
     else
-      dma16(reinterpret_cast<const float*>((HOT ? B : B_loads) + (size_t)kt * T::B_ROW),
+      dma16(reinterpret_cast<const float*>(B + (size_t)kt * T::B_ROW),
             b_voff[v] - (part ? b_back : 0u), at);
   };
   // The scales of steps 4 i .. 4 i + 3, whole sixteens, into area i % 2.
@@ -156,17 +149,28 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
             s_live[v] ? lds_u + (unsigned)s_at(i & 1) + 1024u * (unsigned)(v * T::WAVES + wave_u)
                       : dummy);
   };
-  // The others, up to fifteen, into area 2, a row a thread.
-  auto fill_scales = [&](int t) {
-    const int have = nb - 16 * sixteens;
-#pragma unroll 1
-    for (int i = t; i < T::BM + T::BN; i += T::THREADS) {
-      const uint8_t* row = i < T::BM ? SA + (size_t)min(i, a_last) * g.ldsa
-                                     : SB + (size_t)min(i - T::BM, b_last) * g.ldsb;
-      u32x4 x = {0u, 0u, 0u, 0u};
-      if (have > 0) x = lp_load_unit(row + 16 * (size_t)sixteens, have);
-      *reinterpret_cast<u32x4*>(lds + s_at(2) + 16 * i) = x;
+  // The others, up to fifteen, of a row a thread, for area 2: dwords, the last one's
+  // from the row's last four bytes (a row of fewer: bytes).
+  constexpr int FILL = (T::BM + T::BN + T::THREADS - 1) / T::THREADS;
+  const int have = nb - 16 * sixteens;
+  auto last_scales = [&](int v) {
+    const int i = min(v * T::THREADS + tid, T::BM + T::BN - 1);
+    const uint8_t* row = i < T::BM ? SA + (size_t)min(i, a_last) * g.ldsa
+                                   : SB + (size_t)min(i - T::BM, b_last) * g.ldsb;
+    u32x4 x = {0u, 0u, 0u, 0u};
+    if (nb < 4) {
+#pragma unroll
+      for (int j = 0; j < 3; ++j) x[0] |= j < nb ? (unsigned)row[min(j, nb - 1)] << (8 * j) : 0u;
+      return x;
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (4 * j < have) {
+        const int at = min(4 * j, have - 4);
+        x[j] = *reinterpret_cast<const dword_any*>(row + 16 * (size_t)sixteens + at) >>
+               (8 * (4 * j - at));
+      }
+    return x;
   };
 
   struct Frag {
@@ -228,13 +232,19 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
   Scales sc[2];
   // Group q of step kt (stage st): its MFMAs with the reads of the next group, the
   // next step's scales and, in the second half, step kt+S's loads.
-  auto group = [&](auto hot_c, int kl, bool live, const char* next, auto st_c, auto q_c) {
+  // LAST: the step in which K ends.
+  auto group = [&](auto hot_c, auto last_c, int kl, bool live, const char* next, auto st_c,
+                   auto q_c) {
     constexpr int st = decltype(st_c)::value, q = decltype(q_c)::value;
     constexpr int st1 = st + 1 == S ? 0 : st + 1;
     constexpr int rq = (q + H) % QG, rst = q + H < QG ? st : st1;
 #pragma unroll
     for (int m = 0; m < SL; ++m) {
       if (q == 0) shift_scale(sc[st & 1], m);
+      if (decltype(last_c)::value && m % T::FN == 0)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (4 * q + 2 * u + lh >= 2 * rest) fr[q].a[m / T::FN][u] = u32x4{0u, 0u, 0u, 0u};
       mma(q_c, fr[q], sc[st & 1], m);
 #pragma unroll
       for (int r = 0; r < NF; ++r) {
@@ -253,10 +263,10 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
   auto wait_lds = [] { __builtin_amdgcn_s_waitcnt(0xC07F); };  // lgkmcnt(0)
   constexpr int AHEAD = (S - 2) * ND;
   constexpr int WAIT_AHEAD = 0x0F70 | (AHEAD & 15) | ((AHEAD >> 4) << 14);
-  auto step = [&](auto hot_c, int kt, const char* next, auto st_c) {
-    const bool live = decltype(hot_c)::value || kt + S < loads;
-    const int kl = live ? kt + S : loads - 1;
-    lp_static_for<H>([&](auto q_c) { group(hot_c, kl, live, next, st_c, q_c); });
+  auto step = [&](auto hot_c, auto last_c, int kt, const char* next, auto st_c) {
+    const bool live = decltype(hot_c)::value || kt + S < steps;
+    const int kl = live ? kt + S : steps - 1;
+    lp_static_for<H>([&](auto q_c) { group(hot_c, last_c, kl, live, next, st_c, q_c); });
     wait_lds();
     __builtin_amdgcn_s_waitcnt(WAIT_AHEAD);
     __syncthreads();
@@ -265,25 +275,30 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
     if ((kt & 3) == 0 && (decltype(hot_c)::value || (kt >> 2) + 1 < sixteens))
       load_scales((kt >> 2) + 1);
     lp_static_for<QG - H>([&](auto i) {
-      group(hot_c, kl, live, next, st_c, std::integral_constant<int, H + decltype(i)::value>{});
+      group(hot_c, last_c, kl, live, next, st_c,
+            std::integral_constant<int, H + decltype(i)::value>{});
     });
   };
   // (no scalar load may be in flight in the K loop; see lp_tile_accumulate)
   asm volatile("" ::"s"(g.C), "s"(g.ldc), "s"(g.alpha), "s"(g.beta), "s"(g.M), "s"(g.N));
   __builtin_amdgcn_s_waitcnt(0xC07F);
+  u32x4 tail[FILL];
+  if (have > 0) {
+#pragma unroll
+    for (int v = 0; v < FILL; ++v) tail[v] = last_scales(v);
+  }
   if (sixteens > 0) load_scales(0);
   lp_static_for<S>([&](auto i) {
     constexpr int st = decltype(i)::value;
 #pragma unroll
     for (int o = 0; o < ND; ++o)
-      load_one(std::false_type{}, st < loads ? st : loads - 1, st, o, kd > 0 && st < loads);
+      load_one(std::false_type{}, st < steps ? st : steps - 1, st, o, st < steps);
   });
-  if (kd == 0) {
-#pragma unroll 1
-    for (int i = tid; i < T::LDS_BYTES / 16; i += T::THREADS)
-      *reinterpret_cast<u32x4*>(lds + 16 * i) = u32x4{0u, 0u, 0u, 0u};
-  } else {
-    if (nb % 16 != 0) fill_scales(tid);
+  if (have > 0) {
+#pragma unroll
+    for (int v = 0; v < FILL; ++v)
+      if (v * T::THREADS + tid < T::BM + T::BN)
+        *reinterpret_cast<u32x4*>(lds + s_at(2) + 16 * (v * T::THREADS + tid)) = tail[v];
   }
   constexpr int FIRST = (S - 1) * ND;
   __builtin_amdgcn_s_waitcnt(0x0F70 | (FIRST & 15) | ((FIRST >> 4) << 14));
@@ -296,6 +311,8 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
     for (int r = 0; r < NF; ++r)
       read_one(0, decltype(q_c)::value, r, fr[decltype(q_c)::value]);
   });
+  const std::true_type yes;
+  const std::false_type no;
   int kt = 0;
   // Four steps at a time while the loads are of whole steps and sixteens: the choices
   // of the others, scalar instructions between two MFMAs, hold these up.
@@ -304,86 +321,23 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
     const char* other = lds + s_at(((kt >> 2) + 1) & 1);
     lp_static_for<4>([&](auto i) {
       constexpr int n = decltype(i)::value;
-      step(std::true_type{}, kt + n, n == 3 ? other : own + 4 * (n + 1),
+      step(yes, no, kt + n, n == 3 ? other : own + 4 * (n + 1),
            std::integral_constant<int, n % S>{});
     });
   }
-  for (; kt + S <= steps; kt += S)
+  for (; kt + S <= kd; kt += S)
     lp_static_for<S>([&](auto i) {
       const int k = kt + decltype(i)::value;
-      step(std::false_type{}, k, scales_of(k + 1), i);
+      step(no, no, k, scales_of(k + 1), i);
     });
   lp_static_for<S - 1>([&](auto i) {
     const int k = kt + decltype(i)::value;
-    if (k < steps) step(std::false_type{}, k, scales_of(k + 1), i);
+    if (k < kd) step(no, no, k, scales_of(k + 1), i);
   });
-  if (rest > 0) {
-    // the partial step's loads have had whole steps to land
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-    wait_lds();
-    __syncthreads();
-    const int st = steps % S;
-#pragma unroll
-    for (int r = 0; r < NF; ++r) read_scale(scales_of(steps), r, sc[0]);
-    lp_static_for<QG>([&](auto q_c) {
-      constexpr int q = decltype(q_c)::value;
-#pragma unroll
-      for (int r = 0; r < NF; ++r) read_one(st, q, r, fr[0]);
-#pragma unroll
-      for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          if (4 * q + 2 * u + lh >= 2 * rest) fr[0].a[i][u] = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int m = 0; m < SL; ++m) {
-        if (q == 0) shift_scale(sc[0], m);
-        mma(q_c, fr[0], sc[0], m);
-      }
-      __builtin_amdgcn_sched_barrier(0);
+  if (rest > 0)
+    lp_static_for<S>([&](auto i) {
+      if (kd % S == decltype(i)::value) step(no, yes, kd, scales_of(kd + 1), i);
     });
-  }
-  if (kd == 0) {
-    // K of less than a step, into stage 0 once every wave is done with it and
-    // the loop's loads have landed.  (The lane's index is hidden from the
-    // compiler, which would otherwise keep this part's addresses in registers
-    // through the loop.)
-    int t = tid;
-    asm volatile("" : "+v"(t));
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-    wait_lds();
-    __syncthreads();
-    auto fill = [&](const uint8_t* rows, int ld, int last, int count, int units, int have, int at,
-                    auto off) {
-#pragma unroll 1
-      for (int u = t; u < count * units; u += T::THREADS) {
-        const int r = u / units, c = u % units;
-        u32x4 x = {0u, 0u, 0u, 0u};
-        if (c < have) {
-          const v4u w = *reinterpret_cast<const v4u_any*>(rows + (size_t)min(r, last) * ld + 16 * c);
-          x = u32x4{w[0], w[1], w[2], w[3]};
-        }
-        *reinterpret_cast<u32x4*>(lds + at + off(r, c)) = x;
-      }
-    };
-    fill(A, g.lda, a_last, T::BM, 8, 2 * nb, a_at(0), [](int r, int c) { return lp_unit_off(r, c); });
-    fill(B, g.ldb, b_last, T::BN, T::B_UNITS, T::B_FU * nb, b_at(0), b_off);
-    fill_scales(t);
-    wait_lds();
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < NF; ++r) read_scale(scales_of(0), r, sc[0]);
-    lp_static_for<QG>([&](auto q_c) {
-      constexpr int q = decltype(q_c)::value;
-#pragma unroll
-      for (int r = 0; r < NF; ++r) read_one(0, q, r, fr[0]);
-#pragma unroll
-      for (int m = 0; m < SL; ++m) {
-        if (q == 0) shift_scale(sc[0], m);
-        mma(q_c, fr[0], sc[0], m);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    });
-  }
 }
 
 template <class T, int CDT>

@@ -64,8 +64,8 @@ PRODUCTS = [(1, 1, 32), (1, 16, 64), (1, 4096, 4096), (2, 17, 96), (4, 100, 512)
             (5, 16500, 544), (16, 13000, 2112), (700, 900, 1056), (640, 832, 2048), (650, 840, 1632), (300, 70, 2048), (40, 500, 5000 // 32 * 32),
             # enough tiles for the 128-square and the 256-square ones, K of less
             # than a step, of whole steps (odd and even counts) and ragged
-            (2050, 2100, 64), (2050, 2100, 128), (2048, 2176, 1024), (2050, 2100, 1312),
-            (2900, 3050, 96), (2900, 3050, 256), (2816, 3328, 512), (2900, 3050, 1568), (2900, 3050, 1184)]
+            (2050, 2100, 32), (2050, 2100, 64), (2050, 2100, 160), (2050, 2100, 224), (2050, 2100, 128), (2048, 2176, 1024), (2050, 2100, 1312),
+            (2900, 3050, 32), (2900, 3050, 96), (2900, 3050, 160), (2900, 3050, 544), (2900, 3050, 256), (2816, 3328, 512), (2900, 3050, 1568), (2900, 3050, 1184)]
 
 
 @pytest.mark.parametrize("bits", [8, 4])

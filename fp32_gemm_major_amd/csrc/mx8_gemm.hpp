@@ -231,8 +231,8 @@ __device__ __forceinline__ void mx8_tile_accumulate(const MxArgs& g, char* lds, 
   Frag fr[QG];
   Scales sc[2];
   // Group q of step kt (stage st): its MFMAs with the reads of the next group, the
-  // next step's scales and, in the second half, step kt+S's loads.
-  // LAST: the step in which K ends.
+  // next step's scales and, in the second half, step kt+S's loads.  HOT: whole steps up
+  // to kt+S; LAST: the step in which K ends.
   auto group = [&](auto hot_c, auto last_c, int kl, bool live, const char* next, auto st_c,
                    auto q_c) {
     constexpr int st = decltype(st_c)::value, q = decltype(q_c)::value;

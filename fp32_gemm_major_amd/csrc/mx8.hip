@@ -139,29 +139,36 @@ size_t grad_part_bytes(int N, int D) { return 4 * (size_t)N * (size_t)((D + 3LL)
 // (777 x 1500 x 1000: 10.4 us in 64-square tiles, 12.9 in 128-square ones, 18.7 split
 // in two; 16384 x 1000 x 1000 49 in 8 ranges, 165 in one; 16384 x 64 x 64 10 in 32, 72
 // in one.)
+//
+// The ranges are whole steps, so fewer of them than were asked for may hold all the
+// tokens (21 steps in ten ranges of three are seven): their number counts for the room and
+// the time.  D counts as whole blocks, as the rows hold them.  So the plan for the bytes
+// that the size query reports is the one without a limit.
 struct GradPlan {
   int tile, splits, per;
 };
 GradPlan grad_plan(int cus, int T, int N, int D, size_t workspace) {
   const int edge[2] = {128, 64};
   const double step[2] = {0.44, 0.28}, share[2] = {0.2, 0.6};
-  const double part = (double)grad_part_bytes(N, D);
+  const int width = MX_BLOCK * blocks_of(D);
+  const double part = (double)grad_part_bytes(N, width);
   const long long steps = up_div(T, GRAD_STEP), room = (long long)(workspace / grad_part_bytes(N, D));
-  const bool far = (double)T * (2.0 * N + D) > 8e6;
+  const bool far = (double)T * (2.0 * N + width) > 8e6;
   GradPlan best = {0, 1, T};
   double least = 0;
   for (int i = 0; i < 2; ++i) {
-    const long long tiles = up_div(N, edge[i]) * up_div(D, edge[i]);
-    for (long long s = 1; tiles * s <= 2LL * cus && (s == 1 || (s <= room && 2 * s <= steps));
-         s += 1 + s / 8) {
+    const long long tiles = up_div(N, edge[i]) * up_div(width, edge[i]);
+    for (long long ask = 1; tiles * ask <= 2LL * cus && (ask == 1 || 2 * ask <= steps);
+         ask += 1 + ask / 8) {
+      const long long each = up_div(steps, ask), s = each > 0 ? up_div(steps, each) : 1;
+      if (s > 1 && s > room) break;
       const double a_cu = (double)tiles * s / cus;
-      const double t = (double)up_div(steps, s) * (step[i] + (far ? 0.2 : 0)) *
+      const double t = (double)each * (step[i] + (far ? 0.2 : 0)) *
                            (a_cu > 1 ? 1 + share[i] * (a_cu - 1) : 1) +
                        (s > 1 ? 4 + s * (0.06 + part / 2e6) : 0);
       if (best.tile != 0 && t >= least) continue;
       least = t;
-      const int per = (int)(up_div(steps, s) * GRAD_STEP);
-      best = {1 + i, s > 1 ? (int)up_div(T, per) : 1, s > 1 ? per : T};
+      best = {1 + i, (int)s, s > 1 ? (int)(each * GRAD_STEP) : T};
     }
   }
   return best;

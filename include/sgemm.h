@@ -576,8 +576,9 @@ int sgemm_run_mx_byte_quant(sgemm_handle_t h, int xtype, int bits, int M, int N,
  * dW = beta * dW.
  *
  * Small gradients split the tokens over workgroups, whose partial sums take up to
- * `bytes` of the handle's workspace; with less the split is smaller.  The same
- * inputs and workspace give the same bits.  SGEMM_ERR_UNSUPPORTED for row strides
+ * `bytes` of the handle's workspace; with less the split is smaller, and more
+ * changes nothing.  The bytes reported for D's whole blocks, 32*ceil(D/32), are
+ * enough for D.  The same inputs and workspace give the same bits.  SGEMM_ERR_UNSUPPORTED for row strides
  * of 64 MiB and more.  Ownership, streams, errors and threading as for sgemm_run
  * with a workspace. */
 int sgemm_mx_byte_weight_grad(sgemm_handle_t h, int dtype, int T, int N, int D,

@@ -191,7 +191,8 @@ int validate_grad(int dtype, int T, int N, int D, const void* dY, int lddy, cons
       ranges_meet(w, code_range<Mx8Format>(X, T, D, ldx)) ||
       ranges_meet(w, scale_range(SX, T, D, ldsx)))
     return SGEMM_ERR_ALIAS;
-  // a step's tokens are addressed by 32-bit offsets
+  // a step's tokens are addressed by 32-bit offsets from the tile's first column, with at
+  // most 512 bytes of a row after them
   const long long far = 1LL << 32, r = GRAD_STEP - 1;
   if (T > 1 && (2 * r * lddy + 1024 >= far || r * ldx + 1024 >= far || r * ldsx + 1024 >= far))
     return SGEMM_ERR_UNSUPPORTED;

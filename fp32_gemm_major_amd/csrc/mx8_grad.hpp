@@ -92,8 +92,8 @@ __device__ __forceinline__ void grad_tile_accumulate(const GradArgs& g, char* ld
   const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
   const int N = g.N;
   const E* A = static_cast<const E*>(g.dY) + (size_t)k0 * g.lddy + m0;
-  const uint8_t* B = g.X + (size_t)k0 * g.ldx;
-  const uint8_t* SB = g.SX + (size_t)k0 * g.ldsx;
+  const uint8_t* B = g.X + (size_t)k0 * g.ldx + n0;
+  const uint8_t* SB = g.SX + (size_t)k0 * g.ldsx + n0 / MX_BLOCK;
   const int kn = k1 - k0;
 
   auto a_at = [](int st) { return st * T::A_BYTES; };
@@ -111,10 +111,11 @@ __device__ __forceinline__ void grad_tile_accumulate(const GradArgs& g, char* ld
   int ao = 8 * ((tid % A_UPR) ^ lp_oc_swz<T::BM>(ak));
   if (m0 + ao >= N) ao = N - 8 > m0 ? N - 8 - m0 : 0;
   const unsigned a_voff = 2u * ((unsigned)ak * (unsigned)g.lddy + (unsigned)ao);
-  // X: token u / (BN/16) and sixteen columns; those past the row's whole blocks
-  // read its last sixteen (columns of dW that are not stored).
+  // X: token u / (BN/16) and sixteen of the tile's columns; those past the row's whole
+  // blocks read its last sixteen (columns of dW that are not stored).  (From the row's
+  // start on, the offsets of a wide row's last tiles could pass 32 bits.)
   const int swap = (lane >> 2) & 1;  // (the eight codes that a lane takes first)
-  const int col = min(n0 + 16 * bc, 32 * ((g.D + 31) / 32) - 16);
+  const int col = min(16 * bc, 32 * ((g.D + 31) / 32) - 16 - n0);
   const unsigned b_row = (unsigned)bk * (unsigned)g.ldx + (unsigned)col;
   const unsigned b_voff[2] = {b_row + 8u * swap, b_row + 8u * (1 - swap)};
   const unsigned s_voff = (unsigned)bk * (unsigned)g.ldsx + (unsigned)(col >> 5);

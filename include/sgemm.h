@@ -578,8 +578,9 @@ int sgemm_run_mx_byte_quant(sgemm_handle_t h, int xtype, int bits, int M, int N,
  * Small gradients split the tokens over workgroups, whose partial sums take up to
  * `bytes` of the handle's workspace; with less the split is smaller, and more
  * changes nothing.  The bytes reported for D's whole blocks, 32*ceil(D/32), are
- * enough for D.  The same inputs and workspace give the same bits.  SGEMM_ERR_UNSUPPORTED for row strides
- * of 64 MiB and more.  Ownership, streams, errors and threading as for sgemm_run
+ * enough for D.  The same inputs and workspace give the same bits.  SGEMM_ERR_UNSUPPORTED where 63
+ * row strides and 1 KiB of dY's, X's codes or its scales reach 2^32 bytes
+ * (strides of about 65 MiB) and T > 1.  Ownership, streams, errors and threading as for sgemm_run
  * with a workspace. */
 int sgemm_mx_byte_weight_grad(sgemm_handle_t h, int dtype, int T, int N, int D,
                               float alpha, const void* dY, int lddy,

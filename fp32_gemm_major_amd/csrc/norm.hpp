@@ -196,16 +196,19 @@ __device__ __forceinline__ void norm_result(const NormArgs& g, size_t row, int u
   unsigned m = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    // (where a part is infinite the value or its block is none either way)
+    // (an infinite h or factor leaves no number here either)
     const float a = h[i] * s.hi;
     const float e = fmaf(h[i], s.lo, fmaf(h[i], s.hi, -a));  // what a's rounding left
     const float v = fmaf(a, w[i], e * w[i]);
     // To odd: an even v that is not exact gives way to its neighbour on the exact
-    // side, so that none comes to lie on a border of the codes' rounding.
+    // side, so that none comes to lie on a border of the codes' rounding.  (What an
+    // infinite v leaves is infinite or none: it stays.)
     const float rest = fmaf(e, w[i], fmaf(a, w[i], -v));
+    constexpr int SOME = 0x198;  // normal or subnormal, of either sign
     const int bits = (int)__float_as_uint(v);
     const int side = ((int)__float_as_uint(rest) ^ bits) >> 31 | 1;
-    y[i] = __uint_as_float((unsigned)(bits + (fabsf(rest) > 0.0f && !(bits & 1) ? side : 0)));
+    const bool even = !(bits & 1);
+    y[i] = __uint_as_float((unsigned)(bits + (__builtin_amdgcn_classf(rest, SOME) && even ? side : 0)));
     m = max(m, mx_abs_bits(y[i]));
   }
   m = max(m, quad_swap1(m));

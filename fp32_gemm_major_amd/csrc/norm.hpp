@@ -171,18 +171,22 @@ __device__ __forceinline__ void norm_state(bool add, const Raw8<DT>& x, const Ra
 // bits, so that eight of them add up in 32 bits with hardly a rounding (all eight in
 // 64 bits: no other code in 33 million, 42.3 us of 8192 x 4096 in place of 40.4);
 // others' would be 2^-28 of the row's factor off, which tips one code in 10^7 (32-bit
-// rows of 16384 x 2048 take 78.7 us either way).
+// rows of 16384 x 2048 take 78.7 us either way).  Where eight squares come to less than
+// 2^-100, 32 bits' smallest ones are no longer small beside them, and they are added in 64
+// bits too.
 template <int DT>
 __device__ __forceinline__ void add_squares(const float (&h)[8], double& ss) {
   if constexpr (DT == SGEMM_DTYPE_BF16) {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = fmaf(h[i], h[i], s);
-    ss += (double)s;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fma((double)h[i], (double)h[i], ss);
+    if (!(s < 0x1p-100f)) {
+      ss += (double)s;
+      return;
+    }
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) ss = fma((double)h[i], (double)h[i], ss);
 }
 
 // y of a unit, quantised; a unit's block lies in its quad of lanes, whose units

@@ -1,4 +1,10 @@
-"""The norm's results over its types' whole ranges, against 64 bits."""
+"""The norm's results over its types' whole ranges, against 64 bits.
+
+The forward norm's factor is the 64-bit root of a sum of squares in 64 bits, rounded
+to 32: off by half a step, 2^-24 of itself.  bfloat16 rows add the squares of eight
+neighbours in 32 bits first: the first is exact, the seven additions that follow are
+off by 2^-24 of their sum each, so the row's sum by 7 * 2^-24 and its root by half of
+that.  (A hair more for the products of these errors.)"""
 import numpy as np
 import pytest
 
@@ -12,6 +18,7 @@ from tests.test_gpu_mx import DTYPES, as_numpy  # noqa: E402
 from tests.test_gpu_norm import rows  # noqa: E402
 
 EPS = float(np.float32(1e-5))
+HAIR = 1 + 2.0 ** -18
 
 
 @pytest.fixture(scope="module")
@@ -21,6 +28,14 @@ def handle():
     h = sg.Handle()
     yield h
     h.close()
+
+
+def root_error(dt):
+    return (3.5 if dt == "bf16" else 0) * 2.0 ** -24 * HAIR
+
+
+def f64(t):
+    return t.double().cpu().numpy()
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
@@ -45,3 +60,29 @@ def test_results_past_32_bits_leave_no_codes(handle, D, dt):
         assert np.array_equal(scales == 255, want[1] == 255)
         if dt == "f32":
             assert np.array_equal(codes, want[0]) and np.array_equal(scales, want[1])
+
+
+@pytest.mark.parametrize("dt,power", [(dt, p) for p in (-110, -100, -75, -65, -60, -40, 20, 50)
+                                      for dt in ("f32", "bf16")] + [("f32", 75), ("f32", 110)])
+@pytest.mark.parametrize("D", [40, 1000, 17000])
+def test_scale_of_a_row_does_not_matter(handle, D, power, dt):
+    """Without eps the norm of a row times a power of two is the row's norm, down to
+    rows whose squares are far below 32 bits' smallest (and up to where bfloat16 rows'
+    leave 32 bits, 32-bit ones' far past that)."""
+    T = 5
+    x = rows(T, D, 3, dt)
+    x = torch.where(x.abs() < 2.0 ** -10, torch.ones_like(x), x)  # (no subnormal ones in any power)
+    G = (1 + 0.3 * torch.from_numpy(np.random.default_rng(D).standard_normal(D))).float().cuda()
+    one, far = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    y, s = ref.norm(x.double().numpy(), f64(G), 0.0)
+    scaled = (x.double() * 2.0 ** power).to(x.dtype)
+    assert torch.equal(scaled.double(), x.double() * 2.0 ** power)
+    a = handle.rmsnorm_mx8(x.cuda(), G, rstd=one, eps=0.0)
+    b = handle.rmsnorm_mx8(scaled.cuda(), G, rstd=far, eps=0.0)
+    assert np.all(np.abs(f64(far) * 2.0 ** power - s) <= (root_error(dt) + 2.0 ** -24) * HAIR * s)
+    d = root_error(dt) * HAIR + 2.0 ** -40
+    low, high = (ref.dequantize(*ref.quantize(y * (1 + e))) for e in (-d, d))
+    for q in (a, b):
+        got = ref.dequantize(*as_numpy(q))[:, :D]
+        lo, hi = low[:, :D], high[:, :D]
+        assert np.all((got >= np.minimum(lo, hi)) & (got <= np.maximum(lo, hi)))

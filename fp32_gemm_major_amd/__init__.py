@@ -650,10 +650,7 @@ TENSOR_DTYPES = {torch.float32: SGEMM_DTYPE_F32, torch.bfloat16: SGEMM_DTYPE_BF1
 
 
 class _MxRows:
-    """Microscaled rows: ``codes``, a uint8 matrix of ``CODE_BYTES`` bytes a
-    block of 32 values, and ``scales``, a uint8 matrix of one byte a block (the
-    exponent plus 127).  Rows may be strided, bytes of a row not.  ``rows``
-    and ``K`` (values a row holds, whole blocks) are its sizes."""
+    """What ``Mx4`` and ``Mx8`` share."""
 
     __slots__ = ("codes", "scales", "rows", "K", "_ldc", "_lds")
     CODE_BYTES = 0
@@ -689,13 +686,18 @@ class _MxRows:
 
 
 class Mx4(_MxRows):
-    __doc__ = _MxRows.__doc__.replace("Microscaled rows", "Microscaled 4-bit rows")
+    """Microscaled 4-bit (E2M1) rows: ``codes``, a uint8 matrix of 16 bytes a block
+    of 32 values, and ``scales``, a uint8 matrix of one byte a block (the
+    exponent plus 127).  Rows may be strided, bytes of a row not.  ``rows``
+    and ``K`` (values a row holds, whole blocks) are its sizes."""
+
     __slots__ = ()
     CODE_BYTES = 16
 
 
 class Mx8(_MxRows):
-    __doc__ = _MxRows.__doc__.replace("Microscaled rows", "Microscaled 8-bit (E4M3) rows")
+    """Microscaled 8-bit (E4M3) rows: as ``Mx4`` with 32 code bytes a block."""
+
     __slots__ = ()
     CODE_BYTES = 32
 

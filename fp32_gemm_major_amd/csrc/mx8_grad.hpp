@@ -6,9 +6,10 @@
 // with dY in bfloat16 or binary16 (T x N) and X's codes and scales (T rows of D
 // values).  X's scales change along the sum, row by row, so the scaled matrix
 // instructions, whose scales stand for runs along the sum, do not fit.  X is taken
-// to dY's type instead, where a code times its scale is exact (bfloat16: down to
-// 2^-126, below which it is 0; binary16: inside that type's range), and summed by
-// the 16-bit instructions (v_mfma_f32_32x32x16) in 32 bits.  Bound by these.
+// to dY's type instead, where a code times its scale is exact (of magnitudes from 2^-130
+// in bfloat16; of 2^-21 to 61440 in binary16; smaller ones are rounded to nearest among
+// the type's subnormal numbers, larger ones are infinities), and summed by the 16-bit
+// instructions (v_mfma_f32_32x32x16) in 32 bits.  Bound by these.
 //
 // The schedule is that of the 16-bit products with both operands stored along
 // their outer index (lowp_gemm.hpp): rows of tokens in LDS, fragments by

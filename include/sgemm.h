@@ -568,12 +568,14 @@ int sgemm_run_mx_byte_quant(sgemm_handle_t h, int xtype, int bits, int M, int N,
  *
  * dY is T x N of type dtype (SGEMM_DTYPE_BF16 or _F16), X T microscaled 8-bit
  * rows of D values (any D; codes and scales in whole blocks), dW N x D of type
- * wtype; beta == 0: dW is not read.  X's values are taken in dtype, where they are
- * exact (bfloat16: below 2^-126 they are 0; binary16: inside that type's range), and
- * products are summed in 32 bits: |dW - exact| <= 4*max(T,1)*2^-24*(|alpha|*
- * sum_t|dY*X| + |beta*dW|), plus one rounding to wtype.  Infinities and NaNs spread
- * as the formula makes them: a token whose dY is 0 still meets a NaN in X.  T == 0:
- * dW = beta * dW.
+ * wtype; beta == 0: dW is not read.  X's values are taken in dtype, to nearest:
+ * exact where that is bfloat16 from 2^-130 on and where it is binary16 from 2^-21
+ * to 61440, below that rounded to multiples of 2^-133 or 2^-24; larger ones are
+ * infinities (in binary16 65536, which kept values of 63488 and more read back as;
+ * in bfloat16 from 2^128 on).  Products are summed in 32 bits: |dW - exact| <=
+ * 4*max(T,1)*2^-24*(|alpha|*sum_t|dY*X| + |beta*dW|), plus one rounding to wtype.
+ * Infinities and NaNs spread as the formula makes them: a token whose dY is 0 still
+ * meets a NaN in X.  T == 0: dW = beta * dW.
  *
  * Small gradients split the tokens over workgroups, whose partial sums take up to
  * `bytes` of the handle's workspace; with less the split is smaller, and more

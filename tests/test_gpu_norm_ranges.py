@@ -38,6 +38,10 @@ def f64(t):
     return t.double().cpu().numpy()
 
 
+def power_of_two(n):
+    return ((n.long() + 1023) << 52).view(torch.float64)
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("D", [64, 1000, 17000])
 def test_results_past_32_bits_leave_no_codes(handle, D, dt):
@@ -86,3 +90,47 @@ def test_scale_of_a_row_does_not_matter(handle, D, power, dt):
         got = ref.dequantize(*as_numpy(q))[:, :D]
         lo, hi = low[:, :D], high[:, :D]
         assert np.all((got >= np.minimum(lo, hi)) & (got <= np.maximum(lo, hi)))
+
+
+def test_codes_of_bfloat16_rows(handle):
+    """Of 33 million values hardly a code differs from the 64-bit norm's.  A lane's sum
+    of eight squares is off by sqrt(7) / sqrt(12) * 2^-24 or so, a row's mean of 512 of them
+    by 1/22 of that and the root by half of it: 1e-9.  A value's code then tips over
+    with a chance of 8 / log(2) * 1e-9 (eight borders of the codes' rounding in a binade):
+    0.4 of 33 million, more than four with a chance of 1e-4.  One rounding of y to 32 bits
+    would be 3e-8 off, and ten codes."""
+    T, D, part = 8192, 4096, 1024
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, r = (torch.randn(T, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    G = (1 + 0.2 * torch.randn(D, generator=g, device="cuda")).bfloat16()
+    q = handle.rmsnorm_mx8(x, G, residual=r, eps=EPS)
+    got = handle.mx8_dequantize(q, torch.empty(T, D, device="cuda"))
+    h = (x.float() + r.float()).bfloat16()
+    off = 0
+    for t in range(0, T, part):
+        v = h[t:t + part].double()
+        y = (v / ((v * v).sum(1, keepdim=True) / D + EPS).sqrt() * G.double()).reshape(part, -1, 32)
+        m, e = torch.frexp(y.abs().amax(-1, keepdim=True) / 448.0)
+        scale = power_of_two(torch.where(m > 0.5, e, e - 1))
+        a = y / scale
+        unit = power_of_two(torch.frexp(a)[1].sub(1).clamp(min=-6) - 3)
+        want = (torch.round(a / unit) * unit * scale).reshape(part, D)
+        off += int((want != got[t:t + part].double()).sum())
+    assert off <= 4
+
+
+@pytest.mark.parametrize("D,per", [(8, 4), (520, 2), (1032, 1)])
+def test_more_rows_than_workgroups(handle, D, per):
+    """2^21 workgroups of `per` rows at most: the ones behind them take a second turn
+    of the same workgroups, with the results that they have by themselves."""
+    T = per * 2 ** 21 + 3001
+    g = torch.Generator(device="cuda").manual_seed(D)
+    X = torch.empty(T, D, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    G = torch.ones(D, device="cuda")
+    rstd, own = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    q = handle.rmsnorm_mx8(X, G, rstd=rstd)
+    for t in range(0, T, 2 ** 20):
+        p = handle.rmsnorm_mx8(X[t:t + 2 ** 20], G, rstd=own[t:t + 2 ** 20])
+        assert torch.equal(q.codes[t:t + 2 ** 20], p.codes), t
+        assert torch.equal(q.scales[t:t + 2 ** 20], p.scales), t
+    assert torch.equal(rstd, own)

@@ -109,3 +109,33 @@ def test_weight_grad_takes_x_in_the_type_of_dy(handle, T, N, D, dt):
         with np.errstate(over="ignore"):
             want = (-2 * x[t]).astype(np.float32)
         assert np.array_equal(got[N - 1][others], want[others])
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (16, 2048, 4096), (300, 2048, 4096), (2048, 2176, 4096)])
+def test_sums_of_hidden_states(handle, M, N, K, bits):
+    """Unit-normal activations, a channel in 64 ten times as large: 32-bit results are off
+    the 64-bit product by about 2^-15 of its norm, the matrix instruction's own sums
+    (2^-14 allowed); 16-bit results by that and their rounding, which are independent of one
+    another, so that their squares add up (a tenth is allowed for the sample).  The same
+    call gives the same bits."""
+    g = torch.Generator(device="cuda").manual_seed(K + M)
+    x = torch.randn(M, K, generator=g, device="cuda")
+    x = torch.where(torch.rand(K, generator=g, device="cuda") < 1 / 64, 10 * x, x)
+    A = handle.mx8_quantize(x)
+    w = torch.randn(N, K, generator=g, device="cuda")
+    B = (handle.mx8_quantize if bits == 8 else handle.mx4_quantize)(w)
+    want = torch.from_numpy(products.numbers(A)) @ torch.from_numpy(products.numbers(B)).T
+    size = float(want.norm())
+    C = torch.empty(M, N, device="cuda")
+    handle.gemm_mx8(A, B, C)
+    assert float((C.double().cpu() - want).norm()) <= 2.0 ** -14 * size
+    for dt in (torch.bfloat16, torch.float16):
+        rounding = float((want.to(dt).double() - want).norm())
+        C = torch.empty(M, N, device="cuda", dtype=dt)
+        again = torch.empty_like(C)
+        handle.gemm_mx8(A, B, C)
+        handle.gemm_mx8(A, B, again)
+        off = float((C.double().cpu() - want).norm())
+        assert off ** 2 <= 1.1 * (rounding ** 2 + (2.0 ** -14 * size) ** 2)
+        assert torch.equal(C, again)

@@ -65,8 +65,9 @@ int launch_small(const sgemm_handle_s* h, int bits, int xdt, const MxArgs& g,
 // * 64-square tiles while they are at most two a CU, which run side by side (384 x
 //   4096 x 4096: 20.9, 14.0; in 128-square ones 23.3, 14.7; 1000 x 1500 x 800 8.0, 7.6;
 //   11.2, 10.7);
-// * 128-square ones in the same way (1500 x 4096 x 4096: 39.0, 31.6; in 256-square
-//   ones 51.6, 41.9; 2048 x 4096 x 4096 44.8, 34.6; 49.6, 41.0);
+// * 128-square ones while they are at most two a CU too; one fills a CU's LDS, so the second
+//   follows the first (1500 x 4096 x 4096: 39.0, 31.6; in 256-square ones 51.6, 41.9; 2048 x
+//   4096 x 4096 44.8, 34.6; 49.6, 41.0);
 // * else 256-square ones (700 x 11008 x 4096: 50.9, 45.2; in 128-square ones 55.5,
 //   47.1; 3000 x 4096 x 4096 52.7, 45.5; 59.5, 49.6).
 int launch_product(const sgemm_handle_s* h, int bits, const MxArgs& g, hipStream_t stream) {

@@ -14,7 +14,6 @@
 // The schedule is that of the 16-bit products with both operands stored along
 // their outer index (lowp_gemm.hpp): rows of tokens in LDS, fragments by
 // transposing reads half a step ahead, dY by direct global-to-LDS loads.  X comes
-// transposing reads half a step ahead, dY by direct global-to-LDS loads.  X comes
 // through registers: a lane loads sixteen codes of a row, which share a scale, a
 // step before their stage is free, converts them two an instruction
 // (v_cvt_scalef32_pk) between the MFMAs and writes them as two units.  (Lanes 4-7 of
@@ -22,9 +21,9 @@
 // banks: counted, no bank conflict.)  Tokens past the last whole step, and those whose
 // pieces of dY would be read past the buffer's end, go through registers, zero-filled.
 //
-// 4096 x 11008 x 4096, bfloat16 into 32 bits: 298 us, 1.24 PFLOP/s, where the product
-// of rows already in 16 bits takes 289 and has half as many bytes of LDS writes and no
-// conversions.
+// 4096 x 11008 x 4096, bfloat16 into 32 bits: 298 to 346 us by device and clock, 1.07 to
+// 1.24 PFLOP/s; at 298 the product of rows already in 16 bits, which has half as many bytes
+// of LDS writes and no conversions, takes 289.
 //
 // Where the tiles are fewer than the CUs the tokens are split over several
 // workgroups a tile; their partial sums (the workspace) are added in order by a

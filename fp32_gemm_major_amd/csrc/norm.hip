@@ -16,11 +16,11 @@ namespace {
 
 // Lanes of a row, its units of eight values a lane and the rows of a workgroup, by
 // the largest D.  One unit a lane up to 8192 values: the loads of a row then go out
-// together and the sum's steps are few (bfloat16, 8192 x 4096 forward 42.9 us, with
-// two units in 256 lanes 44.6; 1 x 4096 2.9, 3.4).  Rows of up to 1024 values share
-// a workgroup; larger ones do not gain by it (8192 x 4096, two of 512 lanes: 47.4
-// us).  Past 8192 values a second reading costs less than fuller registers
-// (2000 x 16384: 51.9 us, with four units in 512 lanes 57.4); the gradients, which
+// together and the sum's steps are few (1 x 4096 bfloat16 forward 2.8 us, with two units in
+// 256 lanes 3.3; 8192 x 4096 in 32 bits 78.4, 81.5, in bfloat16 38.5, 37.8).  Rows of up to
+// 1024 values share a workgroup; larger ones do not gain by it (8192 x 4096 bfloat16,
+// two of 512 lanes: 43.0 us).  Past 8192 values a second reading costs less than fuller
+// registers (2000 x 16384: 47.9 us, with four units in 512 lanes 54.7); the gradients, which
 // read three tensors, take the registers up to 16384 (63.7 us, read twice 94.4).  The
 // gradients keep a workgroup on every CU, each over many rows, with 512 lanes
 // at least (16384 x 2048: 51.6 us, with one row of 256 lanes 62.4 and with two such

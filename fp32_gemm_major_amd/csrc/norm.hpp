@@ -15,7 +15,8 @@
 // carry their rounding errors into y's own, to odd.  (A code next to a border of its
 // rounding tips over with any error in y: with 32 bits throughout, codes were 5e-5 of
 // their norm off the exact norm's, now none was in 33 million; the rounding to odd costs
-// 0.4 of the 43.3 us of 8192 x 4096.)  h, the codes, dx and dg are each rounded once.
+// 2.6 of the 38.5 us of 8192 x 4096 bfloat16.)  h, the codes, dx and dg are each rounded
+// once.
 //
 // Bound by memory: in one pass over a row, held in registers between the sum and
 // what needs it.  A row takes 64 to 1024 lanes with one unit of eight values each
@@ -27,7 +28,8 @@
 // lane's registers over all rows that its workgroup takes, and the workgroups' sums
 // are added by a second launch, in their order.
 //
-// bfloat16, 8192 x 4096: forward (235 MB with the residual) 43.3 us, 5.4 TB/s;
+// bfloat16, 8192 x 4096: forward (235 MB with the residual) 43.3 us, 5.4 TB/s, called over
+// and over on the same rows 38.5, as the caches keep part of them (the figures below);
 // gradients with dg (268 MB) 52.2 us, 5.1 TB/s; a copy of 2 GiB runs at 4.96 TB/s.
 #pragma once
 
@@ -169,9 +171,9 @@ __device__ __forceinline__ void norm_state(bool add, const Raw8<DT>& x, const Ra
 
 // The squares of a unit into a sum of 64 bits.  A bfloat16 value's square has sixteen
 // bits, so that eight of them add up in 32 bits with hardly a rounding (all eight in
-// 64 bits: no other code in 33 million, 42.3 us of 8192 x 4096 in place of 40.4);
-// others' would be 2^-28 of the row's factor off, which tips one code in 10^7 (32-bit
-// rows of 16384 x 2048 take 78.7 us either way).  Where eight squares come to less than
+// 64 bits: no other code in 33 million, and 8192 x 4096 takes 38.5 us either way); others'
+// would be 2^-28 of the row's factor off, which tips one code in 10^7 (32-bit rows of
+// 16384 x 2048 take 78.7 us either way).  A sum past 32 bits is an infinity.  Where eight squares come to less than
 // 2^-100, 32 bits' smallest ones are no longer small beside them, and they are added in 64
 // bits too.
 template <int DT>
@@ -227,7 +229,7 @@ __device__ __forceinline__ void norm_result(const NormArgs& g, size_t row, int u
 // TPR lanes a row (a multiple of 64), NV units of eight values each, ROWS rows a
 // workgroup; NV = 0: rows of any length.  WHOLE: D is a multiple of eight.  (The
 // code for parts of units takes 90 registers in place of 58, so that fewer rows are in
-// flight: 8192 x 4096 52.3 us in place of 42.9, 4096 x 8192 59.7 in place of 45.8.)
+// flight: 8192 x 4096 47.1 us in place of 38.5, 4096 x 8192 56.7 in place of 40.7.)
 template <int DT, int TPR, int NV, int ROWS, bool WHOLE>
 __global__ void __launch_bounds__(TPR * ROWS) rmsnorm_mx8_kernel(NormArgs g) {
   typedef typename TensorElem<DT>::type E;

@@ -538,9 +538,10 @@ int sgemm_mx_byte_dequantize(sgemm_handle_t h, int dtype, int R, int K,
  * fixed-point window (see sgemm_run_lowp): beside sgemm_run_mx's bound the
  * result is off by up to 2^-9 * |alpha| * the sum over K's runs of 64 of the
  * largest |a*b| in each, an envelope of measurements (2^-11 was the worst); with
- * unit-normal operands, channels ten times as large among them, 2^-15 of the
- * result, which a 16-bit C's rounding hides.  Small integers with scales near one
- * another are exact.  The same inputs give the same bits. */
+ * unit-normal operands, channels ten times as large among them, about 2^-15 of the
+ * result's norm, which a 16-bit C's rounding hides and a 32-bit C shows.  Small
+ * integers with scales near one another are exact.  The same inputs give the same
+ * bits. */
 int sgemm_run_mx_byte(sgemm_handle_t h, int bits, int M, int N, int K,
                       float alpha, const void* A, int lda, const void* SA,
                       int ldsa, const void* B, int ldb, const void* SB,
@@ -605,7 +606,11 @@ int sgemm_validate_mx_byte_weight_grad(int dtype, int T, int N, int D,
  * values) of type gtype, dtype or SGEMM_DTYPE_F32.  h is rounded to dtype, and
  * what is normed is that; it goes to H unless that is NULL.  y leaves as
  * microscaled 8-bit rows, quantised from 32 bits, and rstd (unless NULL) as T
- * floats for the gradients.  Arithmetic is 32-bit.  H may be X or R itself
+ * floats for the gradients.  The squares are added and rstd is taken in 64 bits
+ * (bfloat16: eight neighbours' squares in 32 bits first) and rstd is rounded once;
+ * where it is a normal number, codes are those of the exact norm, of bfloat16 rows
+ * but for one in more than 10^7.  A y past 32 bits makes its block one of NaNs, and
+ * so does an rstd past them (rows of tiny values without eps).  H may be X or R itself
  * (address and stride); else outputs must not overlap anything
  * (SGEMM_ERR_ALIAS).  A row with an infinity has rstd 0 and so has a bfloat16 one
  * in which the squares of eight neighbours add up past 32 bits' range (values over

@@ -169,26 +169,18 @@ __device__ __forceinline__ void norm_state(bool add, const Raw8<DT>& x, const Ra
   for (int i = 0; i < 8; ++i) v[i] = elem_value<DT>(elem_bits<DT>(v[i] + a[i]));
 }
 
-// The squares of a unit into a sum of 64 bits.  A bfloat16 value's square has sixteen
-// bits, so that eight of them add up in 32 bits with hardly a rounding (all eight in
-// 64 bits: no other code in 33 million, and 8192 x 4096 takes 38.5 us either way); others'
-// would be 2^-28 of the row's factor off, which tips one code in 10^7 (32-bit rows of
-// 16384 x 2048 take 78.7 us either way).  A sum past 32 bits is an infinity.  Where eight squares come to less than
-// 2^-100, 32 bits' smallest ones are no longer small beside them, and they are added in 64
-// bits too.
+// The squares of a unit into a sum of 64 bits.  (In 32 bits they would be 2^-28 of the
+// row's factor off, which tips one code in 10^7, of bfloat16 rows with wide channels as
+// many although their squares have sixteen bits only; 32-bit rows of 16384 x 2048 take
+// 78.7 us either way, bfloat16 ones of 8192 x 4096 38.5.)  Of bfloat16 rows eight squares
+// past 32 bits' range are an infinity, as the interface has it.
 template <int DT>
 __device__ __forceinline__ void add_squares(const float (&h)[8], double& ss) {
-  if constexpr (DT == SGEMM_DTYPE_BF16) {
-    float s = 0.0f;
+  double s = 0.0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(h[i], h[i], s);
-    if (!(s < 0x1p-100f)) {
-      ss += (double)s;
-      return;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fma((double)h[i], (double)h[i], ss);
+  for (int i = 0; i < 8; ++i) s = fma((double)h[i], (double)h[i], s);
+  if (DT == SGEMM_DTYPE_BF16 && s >= 0x1p128) s = __builtin_inf();
+  ss += s;
 }
 
 // y of a unit, quantised; a unit's block lies in its quad of lanes, whose units

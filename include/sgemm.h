@@ -606,11 +606,10 @@ int sgemm_validate_mx_byte_weight_grad(int dtype, int T, int N, int D,
  * values) of type gtype, dtype or SGEMM_DTYPE_F32.  h is rounded to dtype, and
  * what is normed is that; it goes to H unless that is NULL.  y leaves as
  * microscaled 8-bit rows, quantised from 32 bits, and rstd (unless NULL) as T
- * floats for the gradients.  The squares are added and rstd is taken in 64 bits
- * (bfloat16: eight neighbours' squares in 32 bits first) and rstd is rounded once;
- * where it is a normal number, codes are those of the exact norm, of bfloat16 rows
- * but for one in more than 10^7.  A y past 32 bits makes its block one of NaNs, and
- * so does an rstd past them (rows of tiny values without eps).  H may be X or R itself
+ * floats for the gradients.  The squares are added and rstd is taken in 64 bits and
+ * rounded once; where it is a normal number, codes are those of the exact norm.  A y
+ * past 32 bits makes its block one of NaNs, and so does an rstd past them (rows of
+ * tiny values without eps).  H may be X or R itself
  * (address and stride); else outputs must not overlap anything
  * (SGEMM_ERR_ALIAS).  A row with an infinity has rstd 0 and so has a bfloat16 one
  * in which the squares of eight neighbours add up past 32 bits' range (values over

@@ -1,10 +1,7 @@
 """The norm's results over its types' whole ranges, against 64 bits.
 
 The forward norm's factor is the 64-bit root of a sum of squares in 64 bits, rounded
-to 32: off by half a step, 2^-24 of itself.  bfloat16 rows add the squares of eight
-neighbours in 32 bits first: the first is exact, the seven additions that follow are
-off by 2^-24 of their sum each, so the row's sum by 7 * 2^-24 and its root by half of
-that.  (A hair more for the products of these errors.)"""
+to 32: off by half a step, 2^-24 of itself (and a hair for the 64-bit steps)."""
 import numpy as np
 import pytest
 
@@ -30,16 +27,24 @@ def handle():
     h.close()
 
 
-def root_error(dt):
-    return (3.5 if dt == "bf16" else 0) * 2.0 ** -24 * HAIR
-
-
 def f64(t):
     return t.double().cpu().numpy()
 
 
 def power_of_two(n):
     return ((n.long() + 1023) << 52).view(torch.float64)
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("D", [1, 33, 500, 1000, 2048, 4100, 8192, 16390])
+def test_rstd_is_rounded_once(handle, D, dt):
+    T = 40
+    x, r = rows(T, D, D, dt), rows(T, D, D + 1, dt)
+    rstd = torch.empty(T, device="cuda")
+    handle.rmsnorm_mx8(x.cuda(), torch.ones(D, device="cuda"), residual=r.cuda(), rstd=rstd, eps=EPS)
+    h = (x.float() + r.float()).to(x.dtype).double().numpy()
+    s = ref.norm(h, np.ones(D), EPS)[1]
+    assert np.all(np.abs(f64(rstd) - s) <= 2.0 ** -24 * HAIR * s)
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
@@ -83,32 +88,32 @@ def test_scale_of_a_row_does_not_matter(handle, D, power, dt):
     assert torch.equal(scaled.double(), x.double() * 2.0 ** power)
     a = handle.rmsnorm_mx8(x.cuda(), G, rstd=one, eps=0.0)
     b = handle.rmsnorm_mx8(scaled.cuda(), G, rstd=far, eps=0.0)
-    assert np.all(np.abs(f64(far) * 2.0 ** power - s) <= (root_error(dt) + 2.0 ** -24) * HAIR * s)
-    d = root_error(dt) * HAIR + 2.0 ** -40
-    low, high = (ref.dequantize(*ref.quantize(y * (1 + e))) for e in (-d, d))
+    assert np.all(np.abs(f64(far) * 2.0 ** power - s) <= 2.0 ** -24 * HAIR * s)
+    low, high = (ref.dequantize(*ref.quantize(y * (1 + e))) for e in (-2.0 ** -40, 2.0 ** -40))
     for q in (a, b):
         got = ref.dequantize(*as_numpy(q))[:, :D]
         lo, hi = low[:, :D], high[:, :D]
         assert np.all((got >= np.minimum(lo, hi)) & (got <= np.maximum(lo, hi)))
 
 
-def test_codes_of_bfloat16_rows(handle):
-    """Of 33 million values hardly a code differs from the 64-bit norm's.  A lane's sum
-    of eight squares is off by sqrt(7) / sqrt(12) * 2^-24 or so, a row's mean of 512 of them
-    by 1/22 of that and the root by half of it: 1e-9.  A value's code then tips over
-    with a chance of 8 / log(2) * 1e-9 (eight borders of the codes' rounding in a binade):
-    0.4 of 33 million, more than four with a chance of 1e-4.  One rounding of y to 32 bits
-    would be 3e-8 off, and ten codes."""
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("seed,channels", [(1, 0.0), (2, 1 / 64), (3, 1 / 64)])
+def test_every_code_is_the_exact_norms(handle, seed, channels, dt):
+    """Of 33 million values, with a channel in 64 ten times as large or none: y is kept to
+    2^-40 of itself, and 33e6 * 8 / log(2) * 2 * 2^-40 = 7e-4 values lie that near to a
+    border of the codes' rounding, eight of which there are in a binade."""
     T, D, part = 8192, 4096, 1024
-    g = torch.Generator(device="cuda").manual_seed(5)
-    x, r = (torch.randn(T, D, generator=g, device="cuda").bfloat16() for _ in range(2))
-    G = (1 + 0.2 * torch.randn(D, generator=g, device="cuda")).bfloat16()
-    q = handle.rmsnorm_mx8(x, G, residual=r, eps=EPS)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x, r = (torch.randn(T, D, generator=g, device="cuda") for _ in range(2))
+    r = torch.where(torch.rand(D, generator=g, device="cuda") < channels, 10 * r, r)
+    x, r = (0.5 * x).to(DTYPES[dt]), r.to(DTYPES[dt])
+    G = (1 + 0.2 * torch.randn(D, generator=g, device="cuda")).to(DTYPES[dt])
+    H = torch.empty_like(x)
+    q = handle.rmsnorm_mx8(x, G, residual=r, H=H, eps=EPS)
     got = handle.mx8_dequantize(q, torch.empty(T, D, device="cuda"))
-    h = (x.float() + r.float()).bfloat16()
     off = 0
     for t in range(0, T, part):
-        v = h[t:t + part].double()
+        v = H[t:t + part].double()
         y = (v / ((v * v).sum(1, keepdim=True) / D + EPS).sqrt() * G.double()).reshape(part, -1, 32)
         m, e = torch.frexp(y.abs().amax(-1, keepdim=True) / 448.0)
         scale = power_of_two(torch.where(m > 0.5, e, e - 1))
@@ -116,7 +121,7 @@ def test_codes_of_bfloat16_rows(handle):
         unit = power_of_two(torch.frexp(a)[1].sub(1).clamp(min=-6) - 3)
         want = (torch.round(a / unit) * unit * scale).reshape(part, D)
         off += int((want != got[t:t + part].double()).sum())
-    assert off <= 4
+    assert off == 0
 
 
 @pytest.mark.parametrize("D,per", [(8, 4), (520, 2), (1032, 1)])
